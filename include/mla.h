@@ -102,6 +102,7 @@ typedef enum {
 #define MLA_DEVERR_PAGE    2  /* decode: block_table entry not in [0, num_pages)   */
 #define MLA_DEVERR_SEQLEN  4  /* decode: seq_len < 0 or > max_pages*64            */
 #define MLA_DEVERR_TIMEOUT 8  /* a bounded wait inside a kernel gave up           */
+#define MLA_DEVERR_NO_PAGES 16 /* plan: the free list has too few pages           */
 
 #define MLA_KV_LORA_RANK 512
 #define MLA_ROPE_DIM 64
@@ -467,6 +468,145 @@ mla_status mla_out_unabsorb(const float* o_lat, const uint16_t* w_uv, float* o,
  */
 mla_status mla_lse_merge(const float* o_parts, const float* lse_parts, int32_t parts, int32_t batch,
                          int32_t heads, float* o_lat, float* lse, mla_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * A serving step over a ragged batch: mla_plan_chunks, mla_rope,
+ * mla_cache_append, mla_chunk_attention, in this order.
+ *
+ * The sequences of a step have any numbers of new tokens - 1 for a decode, a
+ * few for a speculative draft, thousands for a prefill chunk - stored one
+ * sequence behind the other: sequence b's are rows q_start[b] ..
+ * q_start[b + 1] - 1 of every per-token array.  Lengths live on the device,
+ * so that a captured step can be replayed with other lengths.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * mla_plan_chunks - block tables, slot map, positions and lengths of a step,
+ * built on the GPU from the requests' lengths.
+ *   Inputs, all device int32:
+ *   ctx_lens    [B]: tokens of the request already in the cache
+ *   new_lens    [B]: its new tokens in this step (0 is allowed)
+ *   req         [B]: its row of page_table
+ *   page_table  [rows][max_pages]: the requests' page ids, kept from step to
+ *               step.  The step's new pages are written into it; every other
+ *               entry stays as it was.
+ *   free_pages  [free_len]: ids of unused pages; free_range {head, tail}:
+ *               entries head .. tail - 1 are available.  New pages are taken
+ *               from free_pages[head] on, in the order of the batch.
+ *   num_pages   pages in the pool (ids are checked against it)
+ *   n_tokens    length of the per-token outputs
+ *   Outputs, all device int32, no two of them (nor an input) overlapping:
+ *   block_table [B][max_pages]: the row of each request, -1 behind its last
+ *               page: what the attention calls take
+ *   q_start     [B + 1]: first token row of each request, then the total
+ *   seq_lens    [B]: ctx + new
+ *   positions, token_req, slot [n_tokens]: each token's position, batch index
+ *               and cache slot (mla_cache_append's); 0, -1 and -1 behind the
+ *               last token, which the append skips
+ *   free_head   [1]: the next step's head (not free_range itself)
+ *   A request is refused, and the others go on, when its lengths are
+ *   negative or exceed max_pages * 64, or its tokens do not fit n_tokens
+ *   (MLA_DEVERR_SEQLEN); its req is out of range or named twice in the call
+ *   (MLA_DEVERR_PAGE); or the free list has too few pages
+ *   (MLA_DEVERR_NO_PAGES: nobody behind it gets pages either).  A refused
+ *   request takes no page; its seq_lens entry is 0, its block_table row -1,
+ *   its tokens' slots -1 and their positions 0.  A page id outside the pool
+ *   sets MLA_DEVERR_PAGE and is written as -1; a bad free_range counts as
+ *   empty and sets MLA_DEVERR_PAGE.
+ *   rows <= 65536; batch <= 4096; batch == 0 is a no-op.  The same inputs
+ *   give the same outputs, also when the call is repeated: it does not move
+ *   free_range.
+ *   seq_lens feeds mla_chunk_attention directly; mla_decode_absorbed reads
+ *   its lengths during the launch overlap and needs an ordering point in
+ *   between (see Execution above).
+ */
+mla_status mla_plan_chunks(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* req, int32_t batch,
+                           int32_t* page_table, int32_t rows, int32_t max_pages, const int32_t* free_pages,
+                           int32_t free_len, const int32_t* free_range, int32_t num_pages, int32_t n_tokens,
+                           int32_t* block_table, int32_t* q_start, int32_t* seq_lens, int32_t* positions,
+                           int32_t* token_req, int32_t* slot, int32_t* free_head, int32_t* dev_err,
+                           mla_stream_t stream);
+
+/*
+ * mla_rope - rotary positions on 64-channel rows of queries and keys, with
+ * one to four position axes (text; time, height and width of images and
+ * video).  Pair i (i = 0..31) of a row turns by
+ *   t = positions[pair_axis[i]][token] * inv_freq[i]:
+ *   y1 = amplitude (x1 cos t - x2 sin t),  y2 = amplitude (x1 sin t + x2 cos t)
+ * Angles are exact to 2e-6 radians at every 32-bit position, the products
+ * are fp32, rounded once to bf16.
+ *   q_pe     bf16 [n][heads][64] at the given strides (elements, multiples of
+ *            8), 16-byte aligned; heads 0..128 (0: keys only)
+ *   k_pe     bf16 [n][64] at k_token_stride, or NULL (then k_out is NULL too)
+ *   positions int32 [axes][n], negative ones allowed; inv_freq fp32 [32],
+ *            finite: the caller's frequency table, with any long-context
+ *            interpolation already in it
+ *   pair_axis HOST uint8 [32], each < axes, read during the call; NULL: axis 0
+ *   interleaved 1: pairs are channels (2i, 2i + 1); 0: (i, i + 32)
+ *   inverse  1: turns by -t (takes a rotation back; also the gradient of the
+ *            forward call)
+ *   q_out, k_out: bf16 at their own strides; a call may write over its
+ *            inputs (same pointer and strides), any other overlap is
+ *            undefined.  Rows of an output must not overlap each other.
+ *   n == 0 is a no-op.
+ */
+mla_status mla_rope(const uint16_t* q_pe, int64_t q_token_stride, int64_t q_head_stride, const uint16_t* k_pe,
+                    int64_t k_token_stride, const int32_t* positions, int32_t axes, const uint8_t* pair_axis,
+                    const float* inv_freq, int32_t n, int32_t heads, int32_t interleaved, int32_t inverse,
+                    float amplitude, uint16_t* q_out, int64_t qo_token_stride, int64_t qo_head_stride,
+                    uint16_t* k_out, int64_t ko_token_stride, mla_stream_t stream);
+
+/*
+ * mla_chunk_attention - causal attention of a ragged batch of new tokens over
+ * the paged cache, from the projected queries to the per-head outputs.  The
+ * new tokens were appended before.  With c = seq_lens[b] - n_b (n_b = q_start
+ * [b + 1] - q_start[b]), new token i of sequence b attends to positions t <=
+ * c + i:
+ *   s[h][t] = (q_nope[h] . (W_UK[h] c_hat[t]) + q_pe[h] . kpe_hat[t]) * scale
+ *   o[h]    = sum_t softmax(s[h])[t] c_hat[t] @ W_UV[h]
+ *   q_nope  bf16 [n_tokens][H][128], q_pe bf16 [n_tokens][H][64], both at the
+ *           given token and head strides (elements, multiples of 8; they may
+ *           be slices of one [n][H][192] array), 16-byte aligned
+ *   w_uk    bf16 [H][128][512], w_uv bf16 [H][512][128]
+ *   block_table int32 [B][max_pages]; q_start int32 [B + 1], increasing;
+ *           seq_lens int32 [B], the new tokens included (0: the sequence's
+ *           rows are 0)
+ *   max_new bound on every n_b (host; at most n_tokens): what the launch and
+ *           the workspace are sized for
+ *   kv_tokens bound on the sum of seq_lens, each rounded up to 128, over the
+ *           sequences with more than MLA_CHUNK_SHORT new tokens (0 when
+ *           there is none)
+ *   workspace: device, >= mla_chunk_workspace_bytes(...) bytes, 256-byte
+ *           aligned; contents are scratch, so calls that may overlap (other
+ *           streams, two graphs replayed at once) need their own
+ *   o       bf16 [n_tokens][H][128], 16-byte aligned.  Rows behind
+ *           q_start[B] are left as they were.
+ *   A page id outside the pool contributes nothing and sets MLA_DEVERR_PAGE.
+ *   A sequence whose figures do not fit (negative or decreasing q_start,
+ *   n_b > max_new, 0 < seq_lens[b] < n_b or > max_pages * 64, kv_tokens
+ *   exceeded) sets MLA_DEVERR_SEQLEN; those of its rows that lie in the
+ *   array are 0.
+ *   Precision: fp16 operands, fp32 accumulation and softmax, one rounding of
+ *   o to bf16.  Cached values, weights and products beyond 65504 in
+ *   magnitude count as non-finite.  A non-finite token makes the rows that
+ *   attend to it NaN and leaves the others alone.
+ *   batch <= 4096, n_tokens * H < 2^31; n_tokens == 0 or batch == 0 is a
+ *   no-op.
+ */
+#define MLA_CHUNK_SHORT 64
+mla_status mla_chunk_attention(const mla_cache_layer* cache, const uint16_t* q_nope, int64_t qn_token_stride,
+                               int64_t qn_head_stride, const uint16_t* q_pe, int64_t qp_token_stride,
+                               int64_t qp_head_stride, const uint16_t* w_uk, const uint16_t* w_uv,
+                               const int32_t* block_table, int32_t max_pages, const int32_t* q_start,
+                               const int32_t* seq_lens, int32_t batch, int32_t n_tokens, int32_t heads,
+                               int32_t max_new, int64_t kv_tokens, float softmax_scale, void* workspace,
+                               size_t workspace_bytes, uint16_t* o, int32_t* dev_err, mla_stream_t stream);
+
+/* Bytes of device workspace mla_chunk_attention needs; 0 for invalid
+ * arguments. */
+size_t mla_chunk_workspace_bytes(int32_t batch, int32_t n_tokens, int32_t heads, int32_t max_new, int64_t kv_tokens);
 
 /* Static string for a status code. */
 const char* mla_status_string(mla_status status);

@@ -27,6 +27,11 @@ of a prefill chunk; ``mla_set_prefill_path`` / ``mla_prefill_path_taken``
 choose and report its implementation: tcgen05 tensor cores or the decode
 kernels) and ``mla_lse_merge`` (merges per-part results of a context-sharded decode;
 the host side of that exchange is in ``sharded``).
+
+A serving step over a ragged batch (decodes, drafts and prefill chunks
+together, lengths on the device) is ``mla_plan_chunks`` (block tables, slots,
+positions), ``mla_rope``, ``mla_cache_append`` and ``mla_chunk_attention``
+(its workspace: ``mla_chunk_workspace_bytes``).
 """
 
 import ctypes
@@ -46,7 +51,8 @@ PREFILL_AUTO = 0            # mla_set_prefill_path: tensor cores for large chunk
 PREFILL_DECODE_KERNELS = 1
 PREFILL_TENSOR_CORES = 2
 OUTLIER_CHANNELS = 25
-DEVERR_SLOT, DEVERR_PAGE, DEVERR_SEQLEN, DEVERR_TIMEOUT = 1, 2, 4, 8
+DEVERR_SLOT, DEVERR_PAGE, DEVERR_SEQLEN, DEVERR_TIMEOUT, DEVERR_NO_PAGES = 1, 2, 4, 8, 16
+CHUNK_SHORT = 64            # mla_chunk_attention: sequences with more new tokens count toward kv_tokens
 KV_LORA_RANK, ROPE_DIM, QK_NOPE_DIM, V_DIM, PAGE_TOKENS = 512, 64, 128, 128, 64
 DEFAULT_SOFTMAX_SCALE = 1.0 / math.sqrt(QK_NOPE_DIM + ROPE_DIM)
 
@@ -80,6 +86,7 @@ def _load():
                           "(or __graft_entry__.build()) on a machine with nvcc")
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, SZ, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
+    I64 = ctypes.c_int64
     CP = ctypes.POINTER(_CacheLayer)
     sig = {
         "mla_abi_version": (I32, []),
@@ -102,6 +109,11 @@ def _load():
         "mla_set_prefill_path": (I32, [I32]),
         "mla_prefill_path_taken": (I32, [I32, I32, I32]),
         "mla_select_outlier_channels": (I32, [P, I32, P, P]),
+        "mla_plan_chunks": (I32, [P, P, P, I32, P, I32, I32, P, I32, P, I32, I32, P, P, P, P, P, P, P, P, P]),
+        "mla_rope": (I32, [P, I64, I64, P, I64, P, I32, P, P, I32, I32, I32, I32, F32, P, I64, I64, P, I64, P]),
+        "mla_chunk_attention": (I32, [CP, P, I64, I64, P, I64, I64, P, P, P, I32, P, P, I32, I32, I32, I32, I64, F32,
+                                      P, SZ, P, P, P]),
+        "mla_chunk_workspace_bytes": (SZ, [I32, I32, I32, I32, I64]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -317,6 +329,93 @@ def mla_lse_merge(o_parts, lse_parts, o_lat, lse=None, stream=None):
         _need(lse, torch.float32, (B, H), "lse")
     _check("mla_lse_merge", lib.mla_lse_merge(_ptr(o_parts), _ptr(lse_parts), R, B, H, _ptr(o_lat), _ptr(lse),
                                               _stream(stream)))
+
+
+def _rows(t, n, heads, width, name):
+    """(token stride, head stride) of a bf16 CUDA tensor [n, heads, width] whose rows are contiguous."""
+    if t.dtype is not torch.bfloat16 or t.shape != (n, heads, width) or not t.is_cuda or t.stride(2) != 1:
+        raise ValueError("%s: expected CUDA bfloat16 %s with contiguous rows, got %s %s" % (
+            name, (n, heads, width), t.dtype, tuple(t.shape)))
+    return t.stride(0), t.stride(1)
+
+
+def _ints(t, shape, name):
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s: expected contiguous CUDA int32 %s, got %s %s" % (name, shape, t.dtype, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def mla_plan_chunks(ctx_lens, new_lens, req, page_table, free_pages, free_range, num_pages, block_table, q_start,
+                    seq_lens, positions, token_req, slot, free_head, dev_err=None, stream=None):
+    """Block tables, slot map, positions and lengths of a serving step from
+    the requests' lengths (int32 CUDA tensors; see include/mla.h).  Takes the
+    new pages from ``free_pages[free_range[0]:free_range[1]]``, writes them
+    into the persistent ``page_table`` and fills the outputs ``block_table``
+    .. ``free_head``."""
+    B, n = ctx_lens.shape[0], slot.shape[0]
+    rows, max_pages = page_table.shape
+    _check("mla_plan_chunks", lib.mla_plan_chunks(
+        _ints(ctx_lens, (B,), "ctx_lens"), _ints(new_lens, (B,), "new_lens"), _ints(req, (B,), "req"), B,
+        _ints(page_table, (rows, max_pages), "page_table"), rows, max_pages,
+        _ints(free_pages, (free_pages.shape[0],), "free_pages"), free_pages.shape[0],
+        _ints(free_range, (2,), "free_range"), int(num_pages), n, _ints(block_table, (B, max_pages), "block_table"),
+        _ints(q_start, (B + 1,), "q_start"), _ints(seq_lens, (B,), "seq_lens"), _ints(positions, (n,), "positions"),
+        _ints(token_req, (n,), "token_req"), _ints(slot, (n,), "slot"), _ints(free_head, (1,), "free_head"),
+        _ptr(dev_err), _stream(stream)))
+
+
+def mla_rope(q_pe, k_pe, positions, inv_freq, q_out, k_out, pair_axis=None, interleaved=True, inverse=False,
+             amplitude=1.0, stream=None):
+    """Rotary positions: q_pe [n, heads, 64] and k_pe [n, 64] (bf16, any token
+    and head strides that are multiples of 8; k_pe and k_out may be None) into
+    q_out and k_out, which may be the inputs.  positions int32 [n] or [axes,
+    n]; inv_freq fp32 [32]; pair_axis: the axis of each of the 32 pairs."""
+    n, H = q_pe.shape[0], q_pe.shape[1]
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    qs, qos = _rows(q_pe, n, H, ROPE_DIM, "q_pe"), _rows(q_out, n, H, ROPE_DIM, "q_out")
+    if (k_pe is None) != (k_out is None):
+        raise ValueError("k_pe and k_out go together")
+    ks = kos = (0, 0)
+    if k_pe is not None:
+        ks = _rows(k_pe[:, None], n, 1, ROPE_DIM, "k_pe")
+        kos = _rows(k_out[:, None], n, 1, ROPE_DIM, "k_out")
+    _ints(positions, (n,) if positions.dim() == 1 else (axes, n), "positions")
+    _need(inv_freq, torch.float32, (ROPE_DIM // 2,), "inv_freq")
+    if pair_axis is not None:
+        pair_axis = bytes(pair_axis)
+        if len(pair_axis) != ROPE_DIM // 2:
+            raise ValueError("pair_axis: expected %d axes" % (ROPE_DIM // 2))
+    _check("mla_rope", lib.mla_rope(
+        _ptr(q_pe), qs[0], qs[1], _ptr(k_pe), ks[0], _ptr(positions), axes, pair_axis, _ptr(inv_freq), n, H,
+        1 if interleaved else 0, 1 if inverse else 0, float(amplitude), _ptr(q_out), qos[0], qos[1], _ptr(k_out),
+        kos[0], _stream(stream)))
+
+
+def mla_chunk_workspace_bytes(batch, n_tokens, heads, max_new, kv_tokens=0):
+    return int(lib.mla_chunk_workspace_bytes(int(batch), int(n_tokens), int(heads), int(max_new), int(kv_tokens)))
+
+
+def mla_chunk_attention(cache, q_nope, q_pe, w_uk, w_uv, block_table, q_start, seq_lens, workspace, o, max_new,
+                        kv_tokens=0, dev_err=None, softmax_scale=None, stream=None):
+    """Causal attention of a ragged batch of just-appended tokens over the
+    paged cache, from q_nope [n, H, 128] and q_pe [n, H, 64] (bf16, strided)
+    to o [n, H, 128] (bf16).  Sequence b's tokens are rows q_start[b] ..
+    q_start[b + 1] - 1 (lengths on the device); max_new bounds their number,
+    kv_tokens the lengths of the sequences with more than CHUNK_SHORT."""
+    n, H = q_nope.shape[0], q_nope.shape[1]
+    B = seq_lens.shape[0]
+    qn, qp = _rows(q_nope, n, H, QK_NOPE_DIM, "q_nope"), _rows(q_pe, n, H, ROPE_DIM, "q_pe")
+    _need(w_uk, torch.bfloat16, (H, QK_NOPE_DIM, KV_LORA_RANK), "w_uk")
+    _need(w_uv, torch.bfloat16, (H, KV_LORA_RANK, V_DIM), "w_uv")
+    _need(o, torch.bfloat16, (n, H, V_DIM), "o")
+    scale = DEFAULT_SOFTMAX_SCALE if softmax_scale is None else float(softmax_scale)
+    cs = cache.c_struct()
+    _check("mla_chunk_attention", lib.mla_chunk_attention(
+        ctypes.byref(cs), _ptr(q_nope), qn[0], qn[1], _ptr(q_pe), qp[0], qp[1], _ptr(w_uk), _ptr(w_uv),
+        _ints(block_table, (B, block_table.shape[1]), "block_table"), block_table.shape[1],
+        _ints(q_start, (B + 1,), "q_start"), _ints(seq_lens, (B,), "seq_lens"), B, n, H, int(max_new),
+        int(kv_tokens), scale, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(o), _ptr(dev_err),
+        _stream(stream)))
 
 
 def mla_set_prefill_path(path):

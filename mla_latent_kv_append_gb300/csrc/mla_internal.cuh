@@ -25,6 +25,7 @@ constexpr int kChunk = 32;                 // decode work unit: 32 tokens
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxSplits = 65535;          // decode grid dimension y
 constexpr int kMaxMergeParts = 4096;         // mla_lse_merge: most parts per call
+constexpr int kPlanMaxRows = 65536;          // mla_plan_chunks: most rows of the persistent page table
 
 // Byte layout of one page; see mla_page_layout in mla.h.  A page is two
 // contiguous blocks of 32 tokens; offsets are within a block.

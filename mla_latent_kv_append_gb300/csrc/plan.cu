@@ -1,0 +1,295 @@
+// mla_plan_chunks: the block tables, slot map, positions and lengths of one
+// serving step, built on the GPU from the requests' lengths.
+//
+// For request b (row req[b] of the persistent page table, ctx cached tokens,
+// new new ones):
+//   need_b  = ceil((ctx + new) / 64) - ceil(ctx / 64)    pages to allocate
+//   first_b = sum of need over earlier requests           (exclusive scan)
+//   page p of the request: table[req][p] if p < ceil(ctx / 64), else
+//                          free[head + first_b + p - ceil(ctx / 64)]
+//   q_start_b = sum of new over earlier requests;  token q_start_b + i sits
+//   at position ctx + i, slot 64 page + position % 64.
+//
+// What bounds it: nothing but latency for a decode step (a few hundred
+// words), and the [B][max_pages] table copy for large batches.  So one
+// launch: every block scans all B requests itself (three words each, at most
+// 4096, from L2) instead of waiting for a scan kernel, and takes its share of
+// the tokens and of the table.  No block reads what another writes: the
+// tokens' old pages come from columns < ceil(ctx / 64) of the persistent
+// table, its new columns are only written, and a table row has one owner
+// (requests that name the same row are all refused).
+#include "mla_internal.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanPer = kMaxBatch / kPlanThreads;      // requests per thread: 8
+static_assert(kPlanThreads * kPlanPer == kMaxBatch, "every request has a thread");
+constexpr int kPlanRowWords = kPlanMaxRows / 32;
+
+struct PlanParams {
+  const int32_t *ctx, *nw, *req;
+  int B;
+  int32_t* table;
+  int rows, max_pages;
+  const int32_t* free_pages;
+  int free_len;
+  const int32_t* free_range;
+  int num_pages;
+  int32_t* block_table;
+  int32_t *q_start, *seq_lens, *positions, *token_req, *slot, *free_head;
+  int n;
+  int32_t* dev_err;
+};
+
+// Exclusive scan over the block of one int64 per thread; *total = the sum.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* red, int64_t* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();                                     // an earlier scan's readers of red are done
+  if (lane == 31) red[warp] = x;
+  __syncthreads();
+  int64_t base = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) base += red[w];
+    sum += red[w];
+  }
+  *total = sum;
+  return base + x - v;
+}
+
+__device__ __forceinline__ int pages_of(int tokens) { return (int)(((int64_t)tokens + kPage - 1) / kPage); }
+
+// Dynamic shared memory: q_start [B + 1], first [B] (pages before the
+// request's own; -1: refused), then two bits per persistent row (seen,
+// seen twice).
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
+  extern __shared__ int32_t plan_smem[];
+  __shared__ int64_t red[kPlanThreads / 32];
+  __shared__ int taken;
+  int32_t* s_start = plan_smem;
+  int32_t* s_first = s_start + p.B + 1;
+  uint32_t* s_seen = reinterpret_cast<uint32_t*>(s_first + p.B);
+  const int row_words = (p.rows + 31) / 32;
+  uint32_t* s_twice = s_seen + row_words;
+  const int tid = threadIdx.x;
+  for (int i = tid; i < 2 * row_words; i += kPlanThreads) s_seen[i] = 0u;
+  if (tid == 0) taken = 0;
+  pdl_launch_dependents();
+  pdl_wait();
+  __syncthreads();
+
+  // this thread's requests b0 .. b0 + per - 1, contiguous so that one scan
+  // of the threads' sums orders them
+  const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
+  const int b0 = tid * per;
+  const int cap = p.max_pages * kPage;                 // fits: the host checks it
+  int ctx[kPlanPer], nw[kPlanPer], row[kPlanPer];
+  int64_t sum = 0;
+  int err = 0;
+#pragma unroll
+  for (int k = 0; k < kPlanPer; ++k) {
+    ctx[k] = nw[k] = 0;
+    row[k] = -1;
+    const int b = b0 + k;
+    if (k < per && b < p.B) {
+      ctx[k] = p.ctx[b];
+      nw[k] = p.nw[b];
+      row[k] = p.req[b];
+      if (row[k] < 0 || row[k] >= p.rows) {
+        err |= MLA_DEVERR_PAGE;
+        row[k] = -1;
+      } else {
+        const uint32_t bit = 1u << (row[k] & 31);
+        if (atomicOr(s_seen + (row[k] >> 5), bit) & bit) atomicOr(s_twice + (row[k] >> 5), bit);
+      }
+      if (ctx[k] < 0 || nw[k] < 0 || (int64_t)ctx[k] + nw[k] > cap) {
+        err |= MLA_DEVERR_SEQLEN;
+        row[k] = -1;
+        ctx[k] = 0;
+        if (nw[k] < 0) nw[k] = 0;
+      }
+      sum += nw[k];
+    }
+  }
+  int64_t total;
+  int64_t at = block_scan(sum, red, &total);           // its barriers also order the seen bits
+  int64_t need_sum = 0;
+#pragma unroll
+  for (int k = 0; k < kPlanPer; ++k) {
+    const int b = b0 + k;
+    if (k < per && b < p.B) {
+      s_start[b] = (int)(at < p.n ? at : p.n);
+      at += nw[k];
+      if (row[k] >= 0 && ((s_twice[row[k] >> 5] >> (row[k] & 31)) & 1u)) {
+        err |= MLA_DEVERR_PAGE;
+        row[k] = -1;
+      }
+      if (at > p.n) {                                  // its tokens do not fit the step's arrays
+        err |= MLA_DEVERR_SEQLEN;
+        row[k] = -1;
+      }
+      if (row[k] >= 0) need_sum += pages_of(ctx[k] + nw[k]) - pages_of(ctx[k]);
+    }
+  }
+  if (tid == 0) s_start[p.B] = (int)(total < p.n ? total : p.n);
+  const int head = p.free_range[0];
+  int avail = p.free_range[1] - head;
+  if (head < 0 || p.free_range[1] > p.free_len || avail < 0) {
+    err |= MLA_DEVERR_PAGE;
+    avail = 0;
+  }
+  int64_t first = block_scan(need_sum, red, &total);
+#pragma unroll
+  for (int k = 0; k < kPlanPer; ++k) {
+    const int b = b0 + k;
+    if (k < per && b < p.B) {
+      int f = -1;
+      if (row[k] >= 0) {
+        const int need = pages_of(ctx[k] + nw[k]) - pages_of(ctx[k]);
+        // with the earlier requests' needs all counted, nobody behind the
+        // first refusal takes a page: the pages taken are one run
+        if (need == 0 || first + need <= avail) {
+          f = need ? (int)first : 0;
+          if (need) atomicMax(&taken, f + need);
+        } else {
+          err |= MLA_DEVERR_NO_PAGES;
+        }
+        first += need;
+      }
+      s_first[b] = f;
+      if (blockIdx.x == 0) {
+        p.q_start[b] = s_start[b];
+        p.seq_lens[b] = f >= 0 ? ctx[k] + nw[k] : 0;
+      }
+    }
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    if (err) set_err(p.dev_err, err);
+    if (tid == 0) {
+      p.q_start[p.B] = s_start[p.B];
+      *p.free_head = head + taken;
+    }
+  }
+
+  const int64_t threads = (int64_t)gridDim.x * kPlanThreads, me = (int64_t)blockIdx.x * kPlanThreads + tid;
+  // ---- tokens
+  const int used = s_start[p.B];
+  for (int64_t i = me; i < p.n; i += threads) {
+    int b = -1, pos = 0, slot = -1;
+    if (i < used) {
+      int lo = 0, hi = p.B;                            // last b with s_start[b] <= i
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_start[mid] <= i) lo = mid;
+        else hi = mid;
+      }
+      b = lo;
+      if (s_first[b] >= 0) {
+        const int c = p.ctx[b];
+        pos = c + (int)(i - s_start[b]);
+        const int pg = pos / kPage, old = pages_of(c);
+        const int id = pg < old ? p.table[(int64_t)p.req[b] * p.max_pages + pg]
+                                : p.free_pages[head + s_first[b] + pg - old];
+        if (id >= 0 && id < p.num_pages) slot = id * kPage + (pos & (kPage - 1));
+        else set_err(p.dev_err, MLA_DEVERR_PAGE);
+      }
+    }
+    p.positions[i] = pos;
+    p.token_req[i] = b;
+    p.slot[i] = slot;
+  }
+  // ---- tables: a warp takes 32 columns of one row at a time
+  const int cols = (p.max_pages + 31) / 32, lane = tid & 31;
+  for (int64_t w = me >> 5; w < (int64_t)p.B * cols; w += threads >> 5) {
+    const int b = (int)(w / cols), pg = 32 * (int)(w % cols) + lane;
+    if (pg >= p.max_pages) continue;
+    int id = -1;
+    if (s_first[b] >= 0) {
+      const int c = p.ctx[b], old = pages_of(c);
+      if (pg < pages_of(c + p.nw[b])) {
+        int32_t* mine = p.table + (int64_t)p.req[b] * p.max_pages + pg;
+        id = pg < old ? *mine : p.free_pages[head + s_first[b] + pg - old];
+        if (id < 0 || id >= p.num_pages) {
+          set_err(p.dev_err, MLA_DEVERR_PAGE);
+          id = -1;
+        }
+        if (pg >= old) *mine = id;
+      }
+    }
+    p.block_table[(int64_t)b * p.max_pages + pg] = id;
+  }
+}
+
+bool ok4(const void* p) { return p && ((uintptr_t)p & 3) == 0; }
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" mla_status mla_plan_chunks(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* req,
+                                      int32_t batch, int32_t* page_table, int32_t rows, int32_t max_pages,
+                                      const int32_t* free_pages, int32_t free_len, const int32_t* free_range,
+                                      int32_t num_pages, int32_t n_tokens, int32_t* block_table, int32_t* q_start,
+                                      int32_t* seq_lens, int32_t* positions, int32_t* token_req, int32_t* slot,
+                                      int32_t* free_head, int32_t* dev_err, mla_stream_t stream) {
+  if (batch < 0 || batch > kMaxBatch || n_tokens < 0) return MLA_ERR_INVALID_ARG;
+  if (rows < 1 || rows > kPlanMaxRows || max_pages < 1 || (int64_t)max_pages * kPage > (int64_t)INT32_MAX)
+    return MLA_ERR_INVALID_ARG;
+  // slots are 32-bit
+  if (num_pages < 1 || (int64_t)num_pages * kPage > (int64_t)INT32_MAX || free_len < 0) return MLA_ERR_INVALID_ARG;
+  if (batch == 0) return MLA_OK;
+  if (!ok4(ctx_lens) || !ok4(new_lens) || !ok4(req) || !ok4(page_table) || !ok4(free_range) || !ok4(block_table) ||
+      !ok4(q_start) || !ok4(seq_lens) || !ok4(free_head) || (free_len > 0 && !ok4(free_pages)) ||
+      (dev_err && !ok4(dev_err)))
+    return MLA_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!ok4(positions) || !ok4(token_req) || !ok4(slot))) return MLA_ERR_INVALID_ARG;
+  if (free_head >= free_range && free_head < free_range + 2) return MLA_ERR_INVALID_ARG;
+  PlanParams p;
+  p.ctx = ctx_lens;
+  p.nw = new_lens;
+  p.req = req;
+  p.B = batch;
+  p.table = page_table;
+  p.rows = rows;
+  p.max_pages = max_pages;
+  p.free_pages = free_pages;
+  p.free_len = free_len;
+  p.free_range = free_range;
+  p.num_pages = num_pages;
+  p.block_table = block_table;
+  p.q_start = q_start;
+  p.seq_lens = seq_lens;
+  p.positions = positions;
+  p.token_req = token_req;
+  p.slot = slot;
+  p.free_head = free_head;
+  p.n = n_tokens;
+  p.dev_err = dev_err;
+  const size_t smem = sizeof(int32_t) * ((size_t)2 * batch + 1 + 2 * ((rows + 31) / 32));
+  static int configured[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (smem > 48 * 1024 && (dev < 0 || dev >= 64 || !configured[dev])) {
+    const int most = (int)sizeof(int32_t) * (2 * kMaxBatch + 1 + 2 * kPlanRowWords);
+    const mla_status st =
+        cuda_status(cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    if (st != MLA_OK) return st;
+    if (dev >= 0 && dev < 64) configured[dev] = 1;
+  }
+  const int sms = device_sm_count();
+  const int64_t work = (int64_t)n_tokens + (int64_t)batch * max_pages;
+  const int64_t want = (work + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  const int64_t most = sms > 0 ? 2 * sms : 1;
+  const int grid = (int)(want < 1 ? 1 : (want < most ? want : most));
+  return cuda_status(launch_pdl(plan_kernel, dim3(grid), dim3(kPlanThreads), smem, (cudaStream_t)stream, p));
+}
