@@ -1,138 +1,326 @@
 // mla_chunk_attention: causal attention of a ragged batch of new tokens over
 // the paged latent cache, from the projected queries to the per-head outputs.
 //
-// The simplest form that is right for every case: one block per (token,
-// head), everything in fp32.  The query is absorbed into the latent space
-// (q_lat = q_nope W_UK), the keys stream through shared memory 32 tokens at
-// a time with an online softmax, and the latent output is projected by W_UV.
+//   s[i,h,t] = (q_nope[i,h] . (W_UK[h] c_hat[t]) + q_pe[i,h] . kpe_hat[t]) scale
+//   o[i,h]   = sum_t softmax(s[i,h])[t] c_hat[t] W_UV[h]
+//
+// Bracketed two ways.  Absorbed, (q_nope W_UK) . c and (sum_t w c) W_UV: 2 x
+// 1088 operations per (query, head, key), and every cached byte serves all
+// heads.  Expanded, with keys c W_UK^T and values c W_UV made once per head:
+// 2 x 320 operations per (query, head, key), plus 2 x 512 x 256 per (key,
+// head).  Sequences with at most MLA_CHUNK_SHORT new tokens take the first
+// (chunk_short.cu).
+//
+// This file: the device plan (which sequences take which path, prefix sums
+// of their work; lengths never visit the host), the query absorption, the
+// output projection and the host side.
+#include <cuda_bf16.h>
 #include <math.h>
 
-#include "dequant.cuh"
-#include "mla_internal.cuh"
+#include "chunk.cuh"
+#include "tc.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int kSimpleThreads = 256;
-constexpr int kSimpleStride = kDc + kDr + 1;
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanPer = kMaxBatch / kPlanThreads;      // sequences per thread: 4
 
-struct ChunkParams {
-  const uint8_t* pool;
-  PageLayout L;
-  OutlierSet outl;
-  int num_pages;
-  const uint16_t *qn, *qp;
-  int64_t qn_tok, qn_head, qp_tok, qp_head;
-  const uint16_t *w_uk, *w_uv;
-  const int32_t* block_table;
-  int max_pages;
-  const int32_t *q_start, *seq_lens;
-  int B, N, H, max_new;
-  float scale_log2;
-  uint16_t* o;
-  int32_t* dev_err;
-};
+// Exclusive block scan of one int64 per thread.
+__device__ __forceinline__ int64_t scan(int64_t v, int64_t* red, int64_t* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) red[warp] = x;
+  __syncthreads();
+  int64_t s = red[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  *total = __shfl_sync(0xffffffffu, s, 31);
+  const int64_t base = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+  return (warp ? base : 0) + x - v;
+}
 
-template <int LF, int KF>
-__global__ void __launch_bounds__(kSimpleThreads) chunk_simple_kernel(const ChunkParams p) {
-  extern __shared__ float cs_smem[];
-  float* s_q = cs_smem;                      // [576]
-  float* s_x = s_q + kDc + kDr;              // [32][577]
-  float* s_p = s_x + 32 * kSimpleStride;     // [32]
-  float* s_o = s_p + 32;                     // [512]
+// chunk_plan_kernel: one block.  Checks every sequence, sorts it to a path,
+// and writes the path's records with the prefix sums of rows and work units.
+// Zeroes the rows of sequences that are empty or refused.
+__global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const ChunkParams p, int R) {
+  __shared__ int64_t red[32];
+  __shared__ uint32_t zero_mask[kMaxBatch / 32];
   pdl_launch_dependents();
   pdl_wait();
-  const int tok = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
-  if (tok >= p.q_start[p.B]) return;
-  int b = 0;
-  while (b < p.B && !(p.q_start[b] <= tok && tok < p.q_start[b + 1])) ++b;
-  if (b == p.B) return;
-  const int q0 = p.q_start[b], n = p.q_start[b + 1] - q0, len = p.seq_lens[b];
-  uint16_t* out = p.o + ((int64_t)tok * p.H + h) * kDv;
-  const bool bad = q0 < 0 || p.q_start[b + 1] > p.N || n > p.max_new || len < 0 || (len > 0 && len < n) ||
-                   (int64_t)len > (int64_t)p.max_pages * kPage;
-  if (bad || len == 0) {
-    if (bad && tid == 0) set_err(p.dev_err, MLA_DEVERR_SEQLEN);
-    if (tid < kDv) out[tid] = 0;
-    return;
+  const int tid = threadIdx.x;
+  for (int i = tid; i < p.grid; i += kPlanThreads) p.splits[i].rows = 0;
+  for (int i = tid; i < kMaxBatch / 32; i += kPlanThreads) zero_mask[i] = 0;
+  const int per = (p.B + kPlanThreads - 1) / kPlanThreads, b0 = tid * per;
+  int q0[kPlanPer], n[kPlanPer], len[kPlanPer];
+  bool order = true;
+#pragma unroll
+  for (int k = 0; k < kPlanPer; ++k) {
+    const int b = b0 + k;
+    q0[k] = n[k] = len[k] = 0;
+    if (k < per && b < p.B) {
+      q0[k] = p.q_start[b];
+      const int q1 = p.q_start[b + 1];
+      len[k] = p.seq_lens[b];
+      order &= q0[k] >= 0 && q1 >= q0[k] && q1 <= p.N;
+      n[k] = q1 - q0[k];
+    }
   }
-  const int pos = len - n + tok - q0;
-  const uint16_t* qn = p.qn + tok * p.qn_tok + h * p.qn_head;
-  const uint16_t* qp = p.qp + tok * p.qp_tok + h * p.qp_head;
-  for (int c = tid; c < kDc; c += kSimpleThreads) {
-    float a = 0.f;
-    for (int d = 0; d < kDn; ++d) a = fmaf(bf16f(qn[d]), bf16f(p.w_uk[((int64_t)h * kDn + d) * kDc + c]), a);
-    s_q[c] = a;
-  }
-  if (tid < kDr) s_q[kDc + tid] = bf16f(qp[tid]);
-  float m = -INFINITY, l = 0.f, acc[2] = {0.f, 0.f};
-  for (int t0 = 0; t0 <= pos; t0 += 32) {
-    const int page = p.block_table[(int64_t)b * p.max_pages + t0 / kPage];
-    if (page < 0 || page >= p.num_pages) {
-      if (tid == 0) set_err(p.dev_err, MLA_DEVERR_PAGE);
+  // rows out of order could overlap: then nobody is served
+  const bool ordered = !__syncthreads_or(!order);
+  int64_t mine = 0, units = 0;
+  bool bad = !ordered, zero = false;
+  int items[kPlanPer], tiles[kPlanPer];
+#pragma unroll
+  for (int k = 0; k < kPlanPer; ++k) {
+    const int b = b0 + k;
+    items[k] = tiles[k] = 0;
+    if (!(k < per && b < p.B) || (ordered && n[k] == 0)) continue;
+    const bool fits = ordered && n[k] <= p.max_new && len[k] >= 0 && (len[k] == 0 || len[k] >= n[k]) &&
+                      (int64_t)len[k] <= (int64_t)p.max_pages * kPage;
+    if (!fits || len[k] == 0) {
+      bad |= !fits;
+      zero = true;
+      atomicOr(zero_mask + (b >> 5), 1u << (b & 31));
       continue;
     }
-    const uint8_t* blk = p.pool + page * p.L.page_bytes + ((t0 >> 5) & 1) * p.L.block_bytes;
-    __syncthreads();
-    for (int i = tid; i < 32 * (kLatentUnits + kKpeUnits); i += kSimpleThreads) {
-      const int u = i & 31, c = i >> 5;
-      if (t0 + u > pos) continue;
-      float x[32];
-      if (c < kLatentUnits) {
-        RawUnit<LF, false> r;
-        load_unit<LF, false>(blk, p.L, u, c, r);
-        convert_unit<LF, false>(r, x);
-        patch_outliers<LF>(blk, p.L, p.outl, u, c, x);
-      } else {
-        RawUnit<KF, true> r;
-        load_unit<KF, true>(blk, p.L, u, c - kLatentUnits, r);
-        convert_unit<KF, true>(r, x);
-      }
-      for (int k = 0; k < 32; ++k) s_x[u * kSimpleStride + 32 * c + k] = x[k];
-    }
-    __syncthreads();
-    for (int u = tid >> 5; u < 32; u += kSimpleThreads / 32) {
-      float a = 0.f;
-      if (t0 + u <= pos)
-        for (int c = tid & 31; c < kDc + kDr; c += 32) a = fmaf(s_q[c], s_x[u * kSimpleStride + c], a);
-      for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-      if ((tid & 31) == 0) s_p[u] = t0 + u <= pos ? a * p.scale_log2 : -INFINITY;
-    }
-    __syncthreads();
-    float mx = m;
-    for (int u = 0; u < 32; ++u) mx = fmaxf(mx, s_p[u]);
-    const float alpha = exp2f(m - mx);
-    l *= alpha;
-    acc[0] *= alpha;
-    acc[1] *= alpha;
-    for (int u = 0; u < 32 && t0 + u <= pos; ++u) {
-      const float w = exp2f(s_p[u] - mx);
-      l += w;
-      acc[0] = fmaf(w, s_x[u * kSimpleStride + tid], acc[0]);
-      acc[1] = fmaf(w, s_x[u * kSimpleStride + tid + 256], acc[1]);
-    }
-    m = mx;
+    items[k] = (n[k] * p.H + R - 1) / R;
+    tiles[k] = (len[k] + kKeyTile - 1) / kKeyTile;
+    // at most 2^12 sequences, 2^18 tokens and 2^22 row tiles: one word
+    mine += ((int64_t)1 << 48) + ((int64_t)items[k] << 20) + n[k];
+    units += (int64_t)items[k] * tiles[k];
   }
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  s_o[tid] = acc[0] * inv;
-  s_o[tid + 256] = acc[1] * inv;
-  __syncthreads();
-  if (tid < kDv) {
-    float a = 0.f;
-    for (int c = 0; c < kDc; ++c) a = fmaf(s_o[c], bf16f(p.w_uv[((int64_t)h * kDc + c) * kDv + tid]), a);
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(0.f), "f"(a));
-    out[tid] = (uint16_t)r;
+  int64_t total, total_units;
+  int64_t at = scan(mine, red, &total), unit = scan(units, red, &total_units);
+#pragma unroll
+  for (int k = 0; k < kPlanPer; ++k) {
+    if (items[k] == 0) continue;
+    ShortSeq s;
+    s.unit0 = unit;
+    s.b = b0 + k;
+    s.q0 = q0[k];
+    s.n = n[k];
+    s.len = len[k];
+    s.item0 = (int)((at >> 20) & 0xFFFFFFF);
+    s.tok0 = (int)(at & 0xFFFFF);
+    s.tiles = tiles[k];
+    s.items = items[k];
+    p.s_seqs[at >> 48] = s;
+    for (int i = 0; i < n[k]; ++i) p.s_toks[s.tok0 + i] = make_int2(q0[k] + i, s.item0 * R + i * p.H);
+    at += ((int64_t)1 << 48) + ((int64_t)items[k] << 20) + n[k];
+    unit += (int64_t)items[k] * tiles[k];
+  }
+  if (tid == 0) {
+    ChunkCounts c;
+    c.s_seqs = (int)(total >> 48);
+    c.s_items = (int)((total >> 20) & 0xFFFFFFF);
+    c.s_toks = (int)(total & 0xFFFFF);
+    c.pad0 = 0;
+    c.s_units = total_units;
+    *p.counts = c;
+  }
+  if (bad) set_err(p.dev_err, MLA_DEVERR_SEQLEN);
+  if (__syncthreads_or(zero)) {
+    for (int b = 0; b < p.B; ++b) {
+      if (!((zero_mask[b >> 5] >> (b & 31)) & 1u)) continue;
+      const int64_t lo = max(p.q_start[b], 0), hi = min(p.q_start[b + 1], p.N);
+      uint4* rows = reinterpret_cast<uint4*>(p.o);
+      for (int64_t i = lo * p.H * (kDv / 8) + tid; i < hi * p.H * (kDv / 8); i += kPlanThreads)
+        rows[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
   }
 }
 
-template <int LF, int KF>
-mla_status launch_simple(const ChunkParams& p, cudaStream_t stream) {
-  const int smem = (int)sizeof(float) * (kDc + kDr + 32 * kSimpleStride + 32 + kDc);
-  const mla_status st =
-      cuda_status(cudaFuncSetAttribute(chunk_simple_kernel<LF, KF>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  if (st != MLA_OK) return st;
-  return cuda_status(launch_pdl(chunk_simple_kernel<LF, KF>, dim3(p.N, p.H), dim3(kSimpleThreads), smem, stream, p));
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void mma_bf16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ---------------------------------------------------------------------------
+// absorb_tiles_kernel: the short path's query tiles.  Row r = (token, head h):
+// q_lat = q_nope W_UK[h] (bf16 products, fp32 sums), times scale log2 e, one
+// rounding to fp16; its last 64 channels are q_pe, likewise.
+// Grid (H, 9, z), block 128: a CTA takes 64 channels of a head (y = 8: the
+// RoPE part, a copy) and every z-th 16-token tile.  The weight slice sits in
+// shared memory; a decode's cost is reading the weights once.
+// ---------------------------------------------------------------------------
+constexpr int kAbWS = 64 + 8;        // W slice row stride: ldmatrix without conflicts
+constexpr int kAbAS = kDn + 8;
+
+// 4 bytes (channels c, c + 1 of block kb) of padded row `row`
+__device__ __forceinline__ uint32_t* tile_word(const ChunkParams& p, int R, int64_t row, int kb, int c) {
+  const int rr = (int)(row % R);
+  return reinterpret_cast<uint32_t*>(p.q_tiles + ((row / R) * kQBlocks + kb) * (int64_t)R * 128 + rr * 128 +
+                                     (((c >> 3) ^ (rr & 7)) << 4) + (c & 7) * 2);
+}
+
+__global__ void __launch_bounds__(128) absorb_tiles_kernel(const ChunkParams p, int R) {
+  pdl_launch_dependents();
+  __shared__ __align__(16) uint16_t ws[kDn * kAbWS];
+  __shared__ __align__(16) uint16_t as[16 * kAbAS];
+  __shared__ int2 toks[16];
+  const int h = blockIdx.x, kb = blockIdx.y;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, j = lane & 3;
+  pdl_wait();
+  const int n = __ldcg(&p.counts->s_toks);
+  if (16 * (int)blockIdx.z >= n) return;
+  if (kb < 8) {
+    const uint16_t* wsrc = p.w_uk + (size_t)h * kDn * kDc + 64 * kb;
+    for (int i = tid; i < kDn * 8; i += 128) {
+      const int k = i >> 3, c = i & 7;
+      *reinterpret_cast<uint4*>(ws + k * kAbWS + 8 * c) = __ldg(reinterpret_cast<const uint4*>(wsrc + (size_t)k * kDc + 8 * c));
+    }
+  }
+  const uint32_t a_base = tc::smem_u32(as) + (((lane & 7) + 8 * ((lane >> 3) & 1)) * kAbAS + 8 * (lane >> 4)) * 2;
+  const uint32_t b_base =
+      tc::smem_u32(ws) + (((lane & 7) + 8 * ((lane >> 3) & 1)) * kAbWS + 16 * warp + 8 * (lane >> 4)) * 2;
+  for (int t0 = 16 * blockIdx.z; t0 < n; t0 += 16 * gridDim.z) {
+    __syncthreads();
+    if (tid < 16) toks[tid] = t0 + tid < n ? __ldcg(p.s_toks + t0 + tid) : make_int2(-1, 0);
+    __syncthreads();
+    if (kb == 8) {
+      for (int i = tid; i < 16 * 8; i += 128) {
+        const int2 tk = toks[i >> 3];
+        const int c = i & 7;
+        if (tk.x < 0) continue;
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.qp + tk.x * p.qp_tok + h * p.qp_head + 8 * c));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = tc::half2_bits(bf16lo(w[q]) * p.scale_log2, bf16hi(w[q]) * p.scale_log2);
+        *reinterpret_cast<uint4*>(tile_word(p, R, tk.y + h, 8, 8 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      continue;
+    }
+    for (int i = tid; i < 16 * 16; i += 128) {
+      const int m = i >> 4, c = i & 15;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (toks[m].x >= 0) v = __ldg(reinterpret_cast<const uint4*>(p.qn + toks[m].x * p.qn_tok + h * p.qn_head + 8 * c));
+      *reinterpret_cast<uint4*>(as + m * kAbAS + 8 * c) = v;
+    }
+    __syncthreads();
+    float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int ks = 0; ks < kDn / 16; ++ks) {
+      uint32_t a[4], bf[4];
+      ldsm_x4(a_base + 32 * ks, a);
+      ldsm_x4_t(b_base + 16 * ks * kAbWS * 2, bf);
+      mma_bf16(acc[0], a, bf[0], bf[1]);
+      mma_bf16(acc[1], a, bf[2], bf[3]);
+    }
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int2 tk = toks[r + 8 * e];
+        if (tk.x >= 0)
+          *tile_word(p, R, tk.y + h, kb, 16 * warp + 8 * nt + 2 * j) =
+              tc::half2_bits(acc[nt][2 * e] * p.scale_log2, acc[nt][2 * e + 1] * p.scale_log2);
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// project_kernel: o = o_lat W_UV[h] for the short path's rows, fp16 operands
+// (W_UV converted as it is staged: exact for weights of normal fp16 range),
+// fp32 sums, one rounding to bf16.  Grid (H, 128 / 32, z), block 128: a CTA
+// takes 32 columns of a head and every z-th 16-token tile; warp w sums the
+// channels 128 w .. 128 w + 127, the four sums are added through shared memory.
+// ---------------------------------------------------------------------------
+constexpr int kPrN = 32;
+constexpr int kPrWS = kPrN + 8;
+
+__global__ void __launch_bounds__(128) project_kernel(const ChunkParams p) {
+  pdl_launch_dependents();
+  __shared__ __align__(16) uint16_t ws[kDc * kPrWS];
+  __shared__ float red[4][16][kPrN + 1];
+  const int h = blockIdx.x, n0 = blockIdx.y * kPrN;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, j = lane & 3;
+  pdl_wait();
+  const int n = __ldcg(&p.counts->s_toks);
+  if (16 * (int)blockIdx.z >= n) return;
+  const uint16_t* wsrc = p.w_uv + (size_t)h * kDc * kDv + n0;
+  for (int i = tid; i < kDc * (kPrN / 8); i += 128) {
+    const int k = i / (kPrN / 8), c = i % (kPrN / 8);
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(wsrc + (size_t)k * kDv + 8 * c));
+    *reinterpret_cast<uint4*>(ws + k * kPrWS + 8 * c) =
+        make_uint4(tc::half2_bits(bf16lo(v.x), bf16hi(v.x)), tc::half2_bits(bf16lo(v.y), bf16hi(v.y)),
+                   tc::half2_bits(bf16lo(v.z), bf16hi(v.z)), tc::half2_bits(bf16lo(v.w), bf16hi(v.w)));
+  }
+  const uint32_t b_base = tc::smem_u32(ws) + ((128 * warp + (lane & 7) + 8 * ((lane >> 3) & 1)) * kPrWS + 8 * (lane >> 4)) * 2;
+  for (int t0 = 16 * blockIdx.z; t0 < n; t0 += 16 * gridDim.z) {
+    __syncthreads();
+    // A: o_lat rows t0 + r and t0 + r + 8 of this head, the warp's 128 channels
+    uint32_t a[8][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int t = t0 + r + 8 * e;
+      const uint32_t* row = reinterpret_cast<const uint32_t*>(p.o_lat + ((int64_t)t * p.H + h) * kDc + 128 * warp);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        a[ks][e] = t < n ? __ldcg(row + 8 * ks + j) : 0u;
+        a[ks][e + 2] = t < n ? __ldcg(row + 8 * ks + 4 + j) : 0u;
+      }
+    }
+    float acc[4][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t bf[4];
+        ldsm_x4_t(b_base + (16 * ks * kPrWS + 16 * q) * 2, bf);
+        mma_f16(acc[2 * q], a[ks], bf[0], bf[1]);
+        mma_f16(acc[2 * q + 1], a[ks], bf[2], bf[3]);
+      }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[warp][r + 8 * (e >> 1)][8 * q + 2 * j + (e & 1)] = acc[q][e];
+    __syncthreads();
+    for (int i = tid; i < 16 * (kPrN / 2); i += 128) {
+      const int m = i / (kPrN / 2), c = 2 * (i % (kPrN / 2));
+      if (t0 + m >= n) continue;
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        s0 += red[w][m][c];
+        s1 += red[w][m][c + 1];
+      }
+      uint32_t bits;
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(bits) : "f"(s1), "f"(s0));
+      const int tok = __ldcg(p.s_toks + t0 + m).x;
+      *reinterpret_cast<uint32_t*>(p.o + ((int64_t)tok * p.H + h) * kDv + n0 + c) = bits;
+    }
+  }
 }
 
 bool al(const void* p, uintptr_t a) { return p && ((uintptr_t)p & (a - 1)) == 0; }
@@ -141,6 +329,41 @@ bool sizes_ok(int batch, int n_tokens, int heads, int max_new, int64_t kv_tokens
   return batch >= 0 && batch <= kMaxBatch && n_tokens >= 0 && heads >= 16 && heads <= 128 && heads % 16 == 0 &&
          (int64_t)n_tokens * heads <= (int64_t)INT32_MAX && max_new >= 0 && max_new <= n_tokens && kv_tokens >= 0 &&
          kv_tokens <= (int64_t)INT32_MAX;
+}
+
+// Workspace of a call; carves it into p where base is not null.
+int64_t carve(ChunkParams* p, char* base, int batch, int n_tokens, int heads, int max_new, int64_t kv_tokens, int grid) {
+  const int R = short_rows_per_tile(max_new, heads);
+  const int64_t per_seq = max_new;
+  const int64_t toks = (int64_t)n_tokens < batch * per_seq ? n_tokens : batch * per_seq;
+  const int64_t seqs = batch < n_tokens ? batch : n_tokens;       // with at least one new token
+  // a sequence's last row tile may be padded
+  const int64_t tiles = (toks * heads + R - 1) / R + seqs;
+  const int64_t sizes[7] = {(int64_t)sizeof(ChunkCounts), seqs * (int64_t)sizeof(ShortSeq), toks * 8,
+                            tiles * kQBlocks * R * 128,   toks * heads * kDc * 2,
+                            2 * grid * partial_floats(R) * 4, grid * (int64_t)sizeof(SplitRec)};
+  int64_t off = 0, at[7];
+  for (int i = 0; i < 7; ++i) {
+    at[i] = off;
+    off += align256(sizes[i]);
+  }
+  if (base) {
+    p->counts = (ChunkCounts*)(base + at[0]);
+    p->s_seqs = (ShortSeq*)(base + at[1]);
+    p->s_toks = (int2*)(base + at[2]);
+    p->q_tiles = (uint8_t*)(base + at[3]);
+    p->o_lat = (uint16_t*)(base + at[4]);
+    p->parts = (float*)(base + at[5]);
+    p->splits = (SplitRec*)(base + at[6]);
+  }
+  return off;
+}
+
+// Blocks of the attention kernels: one per SM.  Without a device (sizes asked
+// for on a machine that has none) the GB300's 152.
+int chunk_grid() {
+  const int sms = device_sm_count();
+  return sms > 0 ? sms : 152;
 }
 
 }  // namespace
@@ -152,7 +375,7 @@ extern "C" {
 
 size_t mla_chunk_workspace_bytes(int32_t batch, int32_t n_tokens, int32_t heads, int32_t max_new, int64_t kv_tokens) {
   if (!sizes_ok(batch, n_tokens, heads, max_new, kv_tokens)) return 0;
-  return 256;
+  return (size_t)carve(nullptr, nullptr, batch, n_tokens, heads, max_new, kv_tokens, chunk_grid());
 }
 
 mla_status mla_chunk_attention(const mla_cache_layer* cache, const uint16_t* q_nope, int64_t qn_token_stride,
@@ -174,7 +397,8 @@ mla_status mla_chunk_attention(const mla_cache_layer* cache, const uint16_t* q_n
   if (!al(q_nope, 16) || !al(q_pe, 16) || !al(w_uk, 16) || !al(w_uv, 16) || !al(block_table, 4) || !al(q_start, 4) ||
       !al(seq_lens, 4) || !al(workspace, 256) || !al(o, 16) || (dev_err && !al(dev_err, 4)))
     return MLA_ERR_INVALID_ARG;
-  if (workspace_bytes_ < mla_chunk_workspace_bytes(batch, n_tokens, heads, max_new, kv_tokens))
+  p.grid = chunk_grid();
+  if ((int64_t)workspace_bytes_ < carve(&p, (char*)workspace, batch, n_tokens, heads, max_new, kv_tokens, p.grid))
     return MLA_ERR_INVALID_ARG;
   p.pool = (const uint8_t*)cache->pool;
   p.num_pages = cache->num_pages;
@@ -194,32 +418,24 @@ mla_status mla_chunk_attention(const mla_cache_layer* cache, const uint16_t* q_n
   p.N = n_tokens;
   p.H = heads;
   p.max_new = max_new;
+  p.kv_tokens = kv_tokens;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.o = o;
   p.dev_err = dev_err;
-  const int lf = cache->latent_fmt, kf = cache->kpe_fmt;
-#define MLA_CHUNK_CASE(A, K) \
-  if (lf == A && kf == K) return launch_simple<A, K>(p, (cudaStream_t)stream);
-  MLA_CHUNK_CASE(MLA_FMT_BF16, MLA_FMT_BF16)
-  MLA_CHUNK_CASE(MLA_FMT_BF16, MLA_FMT_INT8_SYM)
-  MLA_CHUNK_CASE(MLA_FMT_BF16, MLA_FMT_INT4_SYM)
-  MLA_CHUNK_CASE(MLA_FMT_INT8_SYM, MLA_FMT_BF16)
-  MLA_CHUNK_CASE(MLA_FMT_INT8_SYM, MLA_FMT_INT8_SYM)
-  MLA_CHUNK_CASE(MLA_FMT_INT8_SYM, MLA_FMT_INT4_SYM)
-  MLA_CHUNK_CASE(MLA_FMT_INT4_ASYM, MLA_FMT_BF16)
-  MLA_CHUNK_CASE(MLA_FMT_INT4_ASYM, MLA_FMT_INT8_SYM)
-  MLA_CHUNK_CASE(MLA_FMT_INT4_ASYM, MLA_FMT_INT4_SYM)
-  MLA_CHUNK_CASE(MLA_FMT_INT4_SYM, MLA_FMT_BF16)
-  MLA_CHUNK_CASE(MLA_FMT_INT4_SYM, MLA_FMT_INT8_SYM)
-  MLA_CHUNK_CASE(MLA_FMT_INT4_SYM, MLA_FMT_INT4_SYM)
-  MLA_CHUNK_CASE(MLA_FMT_INT8_G8, MLA_FMT_INT8_SYM)
-  MLA_CHUNK_CASE(MLA_FMT_INT8_G32, MLA_FMT_INT8_SYM)
-  MLA_CHUNK_CASE(MLA_FMT_INT8_G64, MLA_FMT_INT8_SYM)
-  MLA_CHUNK_CASE(MLA_FMT_INT8_TOKEN, MLA_FMT_INT8_SYM)
-  MLA_CHUNK_CASE(MLA_FMT_INT8_OUTLIER, MLA_FMT_BF16)
-  MLA_CHUNK_CASE(MLA_FMT_INT8_OUTLIER, MLA_FMT_INT8_SYM)
-#undef MLA_CHUNK_CASE
-  return MLA_ERR_UNSUPPORTED;
+  p.wait_ns = wait_limit_ns();
+  const cudaStream_t st = (cudaStream_t)stream;
+  const int R = short_rows_per_tile(max_new, heads);
+  mla_status s = cuda_status(launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p, R));
+  if (s != MLA_OK) return s;
+  // 16-token tiles of the projections: enough CTAs for four per SM
+  const int64_t most = (int64_t)batch * max_new;
+  const int tok_tiles = (int)((((int64_t)n_tokens < most ? (int64_t)n_tokens : most) + 15) / 16);
+  const int za = 4 * p.grid / (9 * heads) + 1, zp = 4 * p.grid / (4 * heads) + 1;
+  s = cuda_status(launch_pdl(absorb_tiles_kernel, dim3(heads, 9, tok_tiles < za ? tok_tiles : za), dim3(128), 0, st, p, R));
+  if (s != MLA_OK) return s;
+  s = launch_short_attention(p, cache->latent_fmt, cache->kpe_fmt, R, st);
+  if (s != MLA_OK) return s;
+  return cuda_status(launch_pdl(project_kernel, dim3(heads, kDv / kPrN, tok_tiles < zp ? tok_tiles : zp), dim3(128), 0, st, p));
 }
 
 }  // extern "C"

@@ -1,0 +1,102 @@
+// Shared by the translation units of mla_chunk_attention (chunk*.cu).
+#pragma once
+
+#include "mla_internal.cuh"
+
+namespace mla {
+
+constexpr int kChunkShort = MLA_CHUNK_SHORT;
+constexpr int kKeyTile = kPage;              // short path: keys per tile, one page
+constexpr int kQBlocks = (kDc + kDr) / 64;   // 9 blocks of 64 channels
+
+// One sequence of the short path (at most kChunkShort new tokens), in the
+// order of the batch.  Its rows r = i H + h (new token i, head h) are cut
+// into row tiles of R rows; a unit of work is one key tile of one row tile.
+struct __align__(16) ShortSeq {
+  int64_t unit0;          // units before this sequence's
+  int32_t b, q0, n, len;  // batch index, first token row, new tokens, cached tokens (the new ones included)
+  int32_t item0;          // row tiles before this sequence's
+  int32_t tok0;           // short-path tokens before this sequence's
+  int32_t tiles;          // key tiles
+  int32_t items;          // row tiles
+};
+static_assert(sizeof(ShortSeq) == 48, "three 16-byte loads");
+
+// What the device plan writes besides the sequence records.
+struct ChunkCounts {
+  int32_t s_seqs, s_items, s_toks, pad0;
+  int64_t s_units;
+};
+
+// One partial of a row tile whose key tiles two or more blocks share: fp32
+// [R][512] unnormalised output, then [R] maxima and [R] sums.
+__host__ __device__ constexpr int64_t partial_floats(int R) { return (int64_t)R * (kDc + 2); }
+
+// Row tiles that several blocks worked on: block x holds the first part.
+struct SplitRec {
+  int32_t rows;           // 0: none starts in block x
+  int32_t last;           // last block with a part
+  int64_t row0;           // first row in the latent output
+};
+
+struct ChunkParams {
+  const uint8_t* pool;
+  PageLayout L;
+  OutlierSet outl;
+  int num_pages;
+  const uint16_t *qn, *qp;
+  int64_t qn_tok, qn_head, qp_tok, qp_head;
+  const uint16_t *w_uk, *w_uv;
+  const int32_t* block_table;
+  int max_pages;
+  const int32_t *q_start, *seq_lens;
+  int B, N, H, max_new;
+  int64_t kv_tokens;
+  float scale_log2;       // softmax_scale * log2(e)
+  uint16_t* o;
+  int32_t* dev_err;
+  uint64_t wait_ns;
+  int grid;               // blocks of the attention kernels
+  // workspace
+  ChunkCounts* counts;
+  ShortSeq* s_seqs;
+  int2* s_toks;           // per short-path token: its token row, and its first row in the padded row tiles
+  uint8_t* q_tiles;       // [row tile][9][R][64] fp16, swizzled
+  uint16_t* o_lat;        // fp16 [rows][512]
+  float* parts;           // [2 grid] partials
+  SplitRec* splits;       // [grid]
+};
+
+// The row tile's height for calls whose sequences have up to max_new tokens
+// of the short path: the smallest that holds all rows of a sequence, so that
+// a tile is read (and dequantized) once, up to 64, what shared memory holds.
+inline int short_rows_per_tile(int max_new, int heads) {
+  const int n = max_new < kChunkShort ? max_new : kChunkShort;
+  const int64_t rows = (int64_t)n * heads;
+  return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+}
+
+// Every (latent, k_pe) format pair of a cache.
+#define MLA_CHUNK_FORMATS(X)                     \
+  X(MLA_FMT_BF16, MLA_FMT_BF16)                  \
+  X(MLA_FMT_BF16, MLA_FMT_INT8_SYM)              \
+  X(MLA_FMT_BF16, MLA_FMT_INT4_SYM)              \
+  X(MLA_FMT_INT8_SYM, MLA_FMT_BF16)              \
+  X(MLA_FMT_INT8_SYM, MLA_FMT_INT8_SYM)          \
+  X(MLA_FMT_INT8_SYM, MLA_FMT_INT4_SYM)          \
+  X(MLA_FMT_INT4_ASYM, MLA_FMT_BF16)             \
+  X(MLA_FMT_INT4_ASYM, MLA_FMT_INT8_SYM)         \
+  X(MLA_FMT_INT4_ASYM, MLA_FMT_INT4_SYM)         \
+  X(MLA_FMT_INT4_SYM, MLA_FMT_BF16)              \
+  X(MLA_FMT_INT4_SYM, MLA_FMT_INT8_SYM)          \
+  X(MLA_FMT_INT4_SYM, MLA_FMT_INT4_SYM)          \
+  X(MLA_FMT_INT8_G8, MLA_FMT_INT8_SYM)           \
+  X(MLA_FMT_INT8_G32, MLA_FMT_INT8_SYM)          \
+  X(MLA_FMT_INT8_G64, MLA_FMT_INT8_SYM)          \
+  X(MLA_FMT_INT8_TOKEN, MLA_FMT_INT8_SYM)        \
+  X(MLA_FMT_INT8_OUTLIER, MLA_FMT_BF16)          \
+  X(MLA_FMT_INT8_OUTLIER, MLA_FMT_INT8_SYM)
+
+mla_status launch_short_attention(const ChunkParams& p, int latent_fmt, int kpe_fmt, int R, cudaStream_t stream);
+
+}  // namespace mla
