@@ -18,7 +18,8 @@
 // chain per tile - dequantize, S^T, softmax, O^T - is pipelined over two key
 // buffers: warps 0..3 fill buffer 0, warps 4..7 buffer 1 (each thread keeps
 // several 32-channel units in flight, loaded ahead of the buffer's release),
-// warps 8..11 do the softmax, one thread of warp 12 issues the MMAs.
+// warps 8..11 do the softmax, and one thread each of warps 12 and 13 issues
+// the S^T and the O^T MMAs, so that neither waits for the other's operands.
 //
 // Work split: all (row tile, key tile) units of the call, in order, are cut
 // into equal runs, one per SM, so ragged lengths need no care.  A row tile
@@ -39,7 +40,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kSThreads = 13 * 32;
+constexpr int kSThreads = 14 * 32;
 constexpr int kKeyBlk = kKeyTile * 128;              // one 64-key x 64-channel fp16 block: 8 KB
 constexpr int kKeyBuf = kQBlocks * kKeyBlk;          // 72 KB
 constexpr float kSlack = 8.f;                        // the running maximum rises only past this (P <= 2^8 in fp16)
@@ -54,7 +55,7 @@ struct ShortSmem {
 };
 static_assert(ShortSmem<64>::kBytes <= 232448, "a block's shared memory");
 
-enum { bFull0 = 0, bFull1, bFree0, bFree1, bS0, bS1, bP, bQ, bFin, bCount };
+enum { bFull0 = 0, bFull1, bP0, bP1, bFree0, bFree1, bS0, bS1, bQ, bFinS, bFinO, bCount };
 
 // One run's walk over the units: segments (a row tile, key tiles t0 .. t1).
 struct Walk {
@@ -118,36 +119,20 @@ struct Walk {
 template <int LF, int KF>
 struct Producer {
   static constexpr int kAhead = LF == MLA_FMT_BF16 ? 2 : 4;      // latent steps in flight
-  RawUnit<LF, false> ring[kAhead];
-  RawUnit<KF, true> kpe;
-
   static __device__ __forceinline__ int token(int w, int lane, int step) {
     return step < 8 ? 16 * w + 8 * (step >> 2) + (lane & 7) : 16 * w + (lane & 15);
   }
   static __device__ __forceinline__ int unit(int lane, int step) { return step < 8 ? 4 * (step & 3) + (lane >> 3) : lane >> 4; }
 };
 
-// 32 channels as fp16 into their block; non-finite ones become 0 and mark
-// their token.
-__device__ __forceinline__ void put_unit(const float* x, uint8_t* buf, int tok, int unit, uint32_t* bad) {
-  uint32_t h[16];
-  __half2 acc = __float2half2_rn(0.f);
-  const __half2 zero = acc;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    h[i] = half2_bits(x[2 * i], x[2 * i + 1]);
-    acc = __hfma2(*reinterpret_cast<const __half2*>(&h[i]), zero, acc);    // NaN once any is infinite or NaN
-  }
-  if (__hisnan(__low2half(acc)) || __hisnan(__high2half(acc))) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) h[i] = 0u;
-    atomicOr(bad + (tok >> 5), 1u << (tok & 31));
-  }
-  uint8_t* row = buf + (unit >> 1) * kKeyBlk + tok * 128;
-  const int c0 = 4 * (unit & 1);
+// A unit's 32 fp16 channels into their block, swizzled.
+__device__ __forceinline__ void put_unit(const uint32_t* h, uint32_t buf, int tok, int unit) {
+  const uint32_t row = buf + (unit >> 1) * kKeyBlk + tok * 128, flip = (4 * (unit & 1) ^ (tok & 7)) << 4;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<uint4*>(row + (((c0 + i) ^ (tok & 7)) << 4)) = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(row + (flip ^ (i << 4))), "r"(h[4 * i]),
+                 "r"(h[4 * i + 1]), "r"(h[4 * i + 2]), "r"(h[4 * i + 3])
+                 : "memory");
 }
 
 template <int LF, int KF, int R>
@@ -166,7 +151,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
   constexpr int kCols = R == 64 ? 512 : 8 * R;       // 6 R columns used, a power of two allocated
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < bCount; ++i) bar_init(bars + 8 * i, i <= bFull1 || i == bP ? 128 : 1);
+    for (int i = 0; i < bCount; ++i) bar_init(bars + 8 * i, i <= bP1 ? 128 : 1);
     *abort = 0;
     for (int i = 0; i < 4; ++i) bad[i] = 0;
     bar_init_fence();
@@ -192,104 +177,109 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
     // ---- producers
     wk.start(p, lo, hi);
     const int g = warp >> 2, w = warp & 3;
-    uint8_t* buf = sm + g * kKeyBuf;
+    const uint32_t buf = sb + g * kKeyBuf;
     uint32_t* mybad = bad + 2 * g;
-    // this group's tiles: every second of the run
-    int t = 0, seg_t1 = 0, len = 0, n_page = -1;
+    // This group's tiles, every second of the run, are visited one ahead of
+    // the loads: `next` holds the tile whose page id is under way.
+    struct Tile {
+      int page, pos, len;
+    } next = {-1, 0, 0};
+    int t = 0, seg_t1 = 0, skip = g;
     const int32_t* pages = nullptr;
-    int skip = g;
-    // moves (t, pages, len) to the group's next tile; false at the end
-    auto advance = [&]() -> bool {
+    auto advance = [&]() -> bool {           // next = the group's next tile; false at the end
       t += skip;
       while (t >= seg_t1) {
         const int over = t - seg_t1;
         if (!wk.next()) return false;
         seg_t1 = wk.t1;
         t = wk.t0 + over;
-        len = wk.s.len;
+        next.len = wk.s.len;
         pages = p.block_table + (int64_t)wk.s.b * p.max_pages;
       }
       skip = 2;
-      n_page = __ldg(pages + t);
+      next.pos = t * kKeyTile;
+      next.page = __ldg(pages + t);
       return true;
     };
     RawUnit<LF, false> ring[PR::kAhead];
     RawUnit<KF, true> kpe;
-    const uint8_t* page = nullptr;
-    int t_pos = 0, t_len = 0;
-    bool page_ok = false;
-    auto enter = [&]() {                   // the tile of the last advance() becomes the loading one
-      page_ok = n_page >= 0 && n_page < p.num_pages;
-      page = p.pool + (int64_t)(page_ok ? n_page : 0) * p.L.page_bytes;
-      t_pos = t * kKeyTile;
-      t_len = page_ok ? len : 0;
+    const uint8_t* page = nullptr;           // the loading tile; tokens from t_len on read as 0
+    int t_len = 0;
+    bool page_ok = false, more = advance(), after = false;
+    auto enter = [&]() {                     // `next` becomes the loading tile
+      page_ok = next.page >= 0 && next.page < p.num_pages;
+      page = p.pool + (int64_t)(page_ok ? next.page : 0) * p.L.page_bytes;
+      t_len = page_ok ? next.len - next.pos : 0;
       if (!page_ok && (threadIdx.x & 127) == 0) set_err(p.dev_err, MLA_DEVERR_PAGE);
+      after = advance();
     };
     auto load_step = [&](int step, RawUnit<LF, false>& r) {
       const int tok = PR::token(w, lane, step);
-      if (t_pos + tok < t_len)
-        load_unit<LF, false>(page + (tok >> 5) * p.L.block_bytes, p.L, tok & 31, PR::unit(lane, step), r);
+      if (tok < t_len) load_unit<LF, false>(page + (tok >> 5) * p.L.block_bytes, p.L, tok & 31, PR::unit(lane, step), r);
     };
-    bool more = advance();
     if (more) {
       enter();
 #pragma unroll
       for (int i = 0; i < PR::kAhead; ++i) load_step(i, ring[i]);
     }
-    uint32_t n = 0;                        // the group's tiles so far
+    uint32_t n = 0;                          // the group's tiles so far
     while (more) {
-      // the tile being stored, while page / t_pos / t_len move on to the next
+      // the tile being stored, while page / t_len move on to the next
       const uint8_t* s_page = page;
-      const int s_pos = t_pos, s_len = t_len;
+      const int s_len = t_len;
       const bool s_ok = page_ok;
       {
         const int tok = PR::token(w, lane, 8);
-        if (s_pos + tok < s_len)
+        if (tok < s_len)
           load_unit<KF, true>(s_page + (tok >> 5) * p.L.block_bytes, p.L, tok & 31, PR::unit(lane, 8), kpe);
       }
-      bool next_more = false;
       if (n >= 1 && !bar_wait(bars + 8 * (bFree0 + g), (n - 1) & 1, p.wait_ns, abort)) {
         ok = false;
         break;
       }
+      uint32_t bad_lo = 0, bad_hi = 0;
+      const bool go_on = after;
 #pragma unroll
       for (int step = 0; step < 8; ++step) {
         const int tok = PR::token(w, lane, step), unit = PR::unit(lane, step);
-        float v[32];
-        if (s_pos + tok < s_len) {
-          convert_unit<LF, false>(ring[step % PR::kAhead], v);
-          patch_outliers<LF>(s_page + (tok >> 5) * p.L.block_bytes, p.L, p.outl, tok & 31, unit, v);
+        uint32_t h[16];
+        bool fine = true;
+        if (tok < s_len) {
+          fine = convert_unit<LF, false>(ring[step % PR::kAhead], h);
+          fine &= patch_outliers<LF>(s_page + (tok >> 5) * p.L.block_bytes, p.L, p.outl, tok & 31, unit, h);
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          for (int i = 0; i < 16; ++i) h[i] = 0u;
         }
         if (step + PR::kAhead < 8) {
           load_step(step + PR::kAhead, ring[step % PR::kAhead]);
         } else {
-          if (step + PR::kAhead == 8) {
-            next_more = advance();
-            if (next_more) enter();
-          }
-          if (next_more) load_step(step + PR::kAhead - 8, ring[step % PR::kAhead]);
+          if (step + PR::kAhead == 8 && go_on) enter();
+          if (go_on) load_step(step + PR::kAhead - 8, ring[step % PR::kAhead]);
         }
-        put_unit(v, buf, tok, unit, mybad);
+        put_unit(h, buf, tok, unit);
+        if (!fine) (tok < 32 ? bad_lo : bad_hi) |= 1u << (tok & 31);
       }
       {
         const int tok = PR::token(w, lane, 8), unit = PR::unit(lane, 8);
-        float v[32];
-        if (s_pos + tok < s_len) {
-          convert_unit<KF, true>(kpe, v);
+        uint32_t h[16];
+        bool fine = true;
+        if (tok < s_len) {
+          fine = convert_unit<KF, true>(kpe, h);
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          for (int i = 0; i < 16; ++i) h[i] = 0u;
         }
-        put_unit(v, buf, tok, kLatentUnits + unit, mybad);
+        put_unit(h, buf, tok, kLatentUnits + unit);
+        if (!fine) (tok < 32 ? bad_lo : bad_hi) |= 1u << (tok & 31);
       }
+      if (bad_lo) atomicOr(mybad, bad_lo);
+      if (bad_hi) atomicOr(mybad + 1, bad_hi);
       if ((threadIdx.x & 127) == 0) tile_ok[g] = s_ok;
       fence_async_smem();
       bar_arrive(bars + 8 * (bFull0 + g));
       ++n;
-      more = next_more;
+      more = go_on;
     }
   } else if (work && warp < 12) {
     // ---- softmax.  Thread (w, lane) holds keys 16 w + lane / 4 and + 8 of
@@ -425,7 +415,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
         }
         fence_async_smem();
         fence_before();
-        bar_arrive(bars + 8 * bP);
+        bar_arrive(bars + 8 * (bP0 + g));
       }
       if (!ok) break;
       // ---- the segment's end: sums over all keys, then O^T
@@ -513,27 +503,14 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
       set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
       *abort = 1;
     }
-  } else if (work) {
-    // ---- warp 12, lane 0: the query tile's copies and the MMAs
+  } else if (work && warp == 12) {
+    // ---- one thread: the query tiles' copies and the S^T MMAs
     wk.start(p, lo, hi);
     if (lane == 0) {
-      constexpr uint32_t kIdS = f16_idesc(64, R, false, false), kIdO = f16_idesc(128, R, true, false);
+      constexpr uint32_t kId = f16_idesc(64, R, false, false);
       constexpr int kQBytes = kQBlocks * R * 128;
+      const uint64_t d_q = sw128_desc(sb + SM::kQ, 16, 1024), d_k = sw128_desc(sb, 16, 1024);
       uint32_t it = 0, seg = 0;
-      auto qk = [&](uint32_t i) -> bool {              // S^T of tile i into buffer i & 1
-        const uint32_t g = i & 1;
-        if (!bar_wait(bars + 8 * (bFull0 + g), (i >> 1) & 1, p.wait_ns, abort)) return false;
-        fence_after();
-        const uint32_t kb0 = sb + g * kKeyBuf;
-#pragma unroll
-        for (int kb = 0; kb < kQBlocks; ++kb)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma(t_s + g * R, sw128_desc(kb0 + kb * kKeyBlk + 32 * k, 16, 1024),
-                 sw128_desc(sb + SM::kQ + kb * R * 128 + 32 * k, 16, 1024), kIdS, (kb | k) != 0);
-        umma_commit(bars + 8 * (bS0 + g));
-        return true;
-      };
       while (ok && wk.next()) {
         // the query tile: its readers, the S^T MMAs of the segment before, are done
         if (seg > 0 && !bar_wait(bars + 8 * (bS0 + ((it - 1) & 1)), ((it - 1) >> 1) & 1, p.wait_ns, abort)) {
@@ -547,26 +524,22 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
           ok = false;
           break;
         }
-        const int nt = wk.t1 - wk.t0;
-        ok = qk(it);
-        for (int t = 0; t < nt && ok; ++t, ++it) {
-          if (t + 1 < nt && !qk(it + 1)) {
-            ok = false;
-            break;
-          }
-          if (!bar_wait(bars + 8 * bP, it & 1, p.wait_ns, abort)) {
+        for (int t = wk.t0; t < wk.t1; ++t, ++it) {
+          const uint32_t g = it & 1;
+          // the keys are there, and the softmax has read this S^T buffer's last tile
+          if (!bar_wait(bars + 8 * (bFull0 + g), (it >> 1) & 1, p.wait_ns, abort) ||
+              (it >= 2 && !bar_wait(bars + 8 * (bP0 + g), ((it - 2) >> 1) & 1, p.wait_ns, abort))) {
             ok = false;
             break;
           }
           fence_after();
-          const uint32_t kb0 = sb + (it & 1) * kKeyBuf;
+          const uint64_t a = d_k + (uint64_t)(g * (kKeyBuf >> 4));
 #pragma unroll
-          for (int blk = 0; blk < 4; ++blk)
+          for (int kb = 0; kb < kQBlocks; ++kb)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma(tbase + blk * R, sw128_desc(kb0 + 2 * blk * kKeyBlk + 2048 * k, kKeyBlk, 1024),
-                   sw128_desc(sb + SM::kP + 32 * k, 16, 1024), kIdO, (t | k) != 0);
-          umma_commit(bars + 8 * (bFree0 + (it & 1)));
+              umma(t_s + g * R, a + ((kb * kKeyBlk + 32 * k) >> 4), d_q + ((kb * R * 128 + 32 * k) >> 4), kId, (kb | k) != 0);
+          umma_commit(bars + 8 * (bS0 + g));
         }
       }
       if (!ok) {
@@ -574,8 +547,40 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
         *abort = 1;
       }
       if (seg > 0) drain_wait(bars + 8 * bQ, (seg - 1) & 1);     // no copy is in flight when the block ends
-      umma_commit(bars + 8 * bFin);
-      drain_wait(bars + 8 * bFin, 0);
+      umma_commit(bars + 8 * bFinS);
+      drain_wait(bars + 8 * bFinS, 0);
+    }
+    __syncwarp();
+  } else if (work) {
+    // ---- warp 13, one thread: the O^T MMAs
+    wk.start(p, lo, hi);
+    if (lane == 0) {
+      constexpr uint32_t kId = f16_idesc(128, R, true, false);
+      const uint64_t d_p = sw128_desc(sb + SM::kP, 16, 1024), d_v = sw128_desc(sb, kKeyBlk, 1024);
+      uint32_t it = 0;
+      while (ok && wk.next()) {
+        for (int t = wk.t0; t < wk.t1; ++t, ++it) {
+          const uint32_t g = it & 1;
+          if (!bar_wait(bars + 8 * (bP0 + g), (it >> 1) & 1, p.wait_ns, abort)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          const uint64_t a = d_v + (uint64_t)(g * (kKeyBuf >> 4));
+#pragma unroll
+          for (int blk = 0; blk < 4; ++blk)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma(tbase + blk * R, a + ((2 * blk * kKeyBlk + 2048 * k) >> 4), d_p + ((32 * k) >> 4), kId, t > wk.t0 || k != 0);
+          umma_commit(bars + 8 * (bFree0 + g));
+        }
+      }
+      if (!ok) {
+        set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
+        *abort = 1;
+      }
+      umma_commit(bars + 8 * bFinO);
+      drain_wait(bars + 8 * bFinO, 0);
     }
     __syncwarp();
   }

@@ -7,6 +7,8 @@
 // apart from converting, so that a caller can have several units in flight.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "mla_internal.cuh"
 
 namespace mla {
@@ -55,41 +57,72 @@ __device__ __forceinline__ void load_unit(const uint8_t* blk, const PageLayout& 
   }
 }
 
-// A byte as a float: the byte in the low mantissa bits of 2^23, exact.
-__device__ __forceinline__ float byte_float(uint32_t w, int j, float minus) {
-  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 + j)) - minus;
+// Largest magnitude that stays finite in fp16.
+constexpr float kHalfMax = 65504.f;
+
+// A scale rounded to 15 significant bits (2^-15 relative, a sixteenth of the
+// fp16 rounding that follows).  With it the products below are exact: a code
+// q sits in a float's mantissa as f = 1 + q 2^-k, and
+//   fma(f, 2^k s, -(2^k + zero) s) = (q - zero) s
+// is rounded once, since (2^k + zero) s fits 24 bits; one byte select (or
+// shift and mask) and one FMA per value, no conversion instructions.
+__device__ __forceinline__ float short_scale(float s) {
+  return __uint_as_float((__float_as_uint(s) + 0x100u) & 0xFFFFFE00u);
+}
+__device__ __forceinline__ uint32_t half2_word(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// x[0..31] = the unit's dequantized channels in order, x_hat exactly as
-// include/mla.h defines it (fp32, one rounding per product).
+// The unit's 32 channels as fp16 pairs, h[i] = channels (2i, 2i + 1); false
+// (and h = 0) if one of them is not finite in fp16.
 template <int FMT, bool KPE>
-__device__ __forceinline__ void convert_unit(const RawUnit<FMT, KPE>& r, float* x) {
+__device__ __forceinline__ bool convert_unit(const RawUnit<FMT, KPE>& r, uint32_t* h) {
   using S = UnitShape<FMT, KPE>;
+  bool fine = true;
   if constexpr (FMT == MLA_FMT_BF16) {
+    __half2 acc = __float2half2_rn(0.f);
+    const __half2 zero = acc;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        x[8 * i + 2 * j] = bf16lo(w[j]);
-        x[8 * i + 2 * j + 1] = bf16hi(w[j]);
+        h[4 * i + j] = half2_word(bf16lo(w[j]), bf16hi(w[j]));
+        acc = __hfma2(*reinterpret_cast<const __half2*>(&h[4 * i + j]), zero, acc);   // NaN once one is not finite
       }
     }
+    fine = !(__hisnan(__low2half(acc)) || __hisnan(__high2half(acc)));
   } else if constexpr (S::kInt4) {
+    float m[S::kScales], c[S::kScales];
+#pragma unroll
+    for (int g = 0; g < S::kScales; ++g) {
+      const float zero = S::kZeros ? r.z[S::kZeros ? g : 0] : 8.f;
+      fine &= fabsf(r.s[g]) * (S::kZeros ? fabsf(zero - 7.5f) + 7.5f : 7.f) <= kHalfMax;      // false for NaN
+      const float s = short_scale(r.s[g]);
+      m[g] = 128.f * s;
+      c[g] = -(128.f + zero) * s;
+    }
     const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      // even and odd nibbles as bytes: byte m of lo is nibble 2m, of hi 2m + 1
-      const uint32_t lo = w[j] & 0x0F0F0F0Fu, hi = (w[j] >> 4) & 0x0F0F0F0Fu;
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < 4; ++k) {
+        // nibbles k and k + 4 of a word are adjacent channels
         const int ch = int4_nibble_channel(j, k), g = ch / S::kGroup;
-        const float zero = S::kZeros ? r.z[S::kZeros ? g : 0] : 8.f;
-        const float q = byte_float((k & 1) ? hi : lo, k >> 1, 8388608.f);
-        x[ch] = __fmul_rn(__fsub_rn(q, zero), r.s[g]);
+        const uint32_t lo = ((w[j] << (16 - 4 * k)) & 0x000F0000u) | 0x3F800000u;
+        const uint32_t hi = ((w[j] >> (4 * k)) & 0x000F0000u) | 0x3F800000u;
+        h[ch / 2] = half2_word(fmaf(__uint_as_float(lo), m[g], c[g]), fmaf(__uint_as_float(hi), m[g], c[g]));
       }
-    }
   } else {
+    float m[S::kScales], c[S::kScales];
+#pragma unroll
+    for (int g = 0; g < S::kScales; ++g) {
+      fine &= fabsf(r.s[g]) * 127.f <= kHalfMax;
+      const float s = short_scale(r.s[g]);
+      m[g] = 32768.f * s;
+      c[g] = -32896.f * s;               // codes are biased by 128 below
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t w[4] = {r.w[i].x ^ 0x80808080u, r.w[i].y ^ 0x80808080u, r.w[i].z ^ 0x80808080u,
@@ -97,32 +130,48 @@ __device__ __forceinline__ void convert_unit(const RawUnit<FMT, KPE>& r, float* 
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 4; k += 2) {
           // 8-channel latent groups store channels 2j, 2j+1, 8+2j, 8+2j+1 in word j
-          const int ch = 16 * i + (!KPE && S::kGroup == 8 ? 2 * j + (k & 1) + 8 * (k >> 1) : 4 * j + k);
-          x[ch] = __fmul_rn(byte_float(w[j], k, 8388736.f), r.s[S::kScales > 1 ? ch / S::kGroup : 0]);
+          const int ch = 16 * i + (!KPE && S::kGroup == 8 ? 2 * j + 4 * k : 4 * j + k);
+          const int g = S::kScales > 1 ? ch / S::kGroup : 0;
+          const float a = __uint_as_float(__byte_perm(w[j], 0x3F800000u, 0x7604 | (k << 4)));
+          const float b = __uint_as_float(__byte_perm(w[j], 0x3F800000u, 0x7604 | ((k + 1) << 4)));
+          h[ch / 2] = half2_word(fmaf(a, m[g], c[g]), fmaf(b, m[g], c[g]));
         }
     }
   }
+  if (!fine) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) h[i] = 0u;
+  }
+  return fine;
 }
 
-// INT8_OUTLIER: puts the protected channels of unit c in their places.
+// INT8_OUTLIER: puts the protected channels of unit c in their places; false
+// if one is not finite in fp16 (it then reads as 0).
 template <int FMT>
-__device__ __forceinline__ void patch_outliers(const uint8_t* blk, const PageLayout& L, const OutlierSet& outl, int u,
-                                               int c, float* x) {
+__device__ __forceinline__ bool patch_outliers(const uint8_t* blk, const PageLayout& L, const OutlierSet& outl, int u,
+                                               int c, uint32_t* h) {
+  bool fine = true;
   if constexpr (FMT == MLA_FMT_INT8_OUTLIER) {
     const uint32_t mask = outl.mask[c];
-    if (!mask) return;
+    if (!mask) return true;
     const uint16_t* ov = reinterpret_cast<const uint16_t*>(blk + L.outlier_off);
     for (int k = 0; k < kNOut; ++k) {
       const int ch = outl.ch[k];
       if ((ch >> 5) != c) continue;
-      const float v = bf16f(__ldg(ov + k * kBlockTokens + u));
+      float v = bf16f(__ldg(ov + k * kBlockTokens + u));
+      if (!(fabsf(v) <= kHalfMax)) {
+        fine = false;
+        v = 0.f;
+      }
+      const uint32_t bits = half2_word(v, v);
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i == (ch & 31)) x[i] = v;
+      for (int i = 0; i < 16; ++i)
+        if (i == ((ch & 31) >> 1)) h[i] = (ch & 1) ? ((h[i] & 0xFFFFu) | (bits & 0xFFFF0000u)) : ((h[i] & 0xFFFF0000u) | (bits & 0xFFFFu));
     }
   }
+  return fine;
 }
 
 }  // namespace mla
