@@ -68,9 +68,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
     const int b = b0 + k;
     q0[k] = n[k] = len[k] = 0;
     if (k < per && b < p.B) {
-      q0[k] = p.q_start[b];
-      const int q1 = p.q_start[b + 1];
-      len[k] = p.seq_lens[b];
+      q0[k] = __ldcg(p.q_start + b);
+      const int q1 = __ldcg(p.q_start + b + 1);
+      len[k] = __ldcg(p.seq_lens + b);
       order &= q0[k] >= 0 && q1 >= q0[k] && q1 <= p.N;
       n[k] = q1 - q0[k];
     }
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
   if (__syncthreads_or(zero)) {
     for (int b = 0; b < p.B; ++b) {
       if (!((zero_mask[b >> 5] >> (b & 31)) & 1u)) continue;
-      const int64_t lo = max(p.q_start[b], 0), hi = min(p.q_start[b + 1], p.N);
+      const int64_t lo = max(__ldcg(p.q_start + b), 0), hi = min(__ldcg(p.q_start + b + 1), p.N);
       uint4* rows = reinterpret_cast<uint4*>(p.o);
       for (int64_t i = lo * p.H * (kDv / 8) + tid; i < hi * p.H * (kDv / 8); i += kPlanThreads)
         rows[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(128) absorb_tiles_kernel(const ChunkParams p, 
     const uint16_t* wsrc = p.w_uk + (size_t)h * kDn * kDc + 64 * kb;
     for (int i = tid; i < kDn * 8; i += 128) {
       const int k = i >> 3, c = i & 7;
-      *reinterpret_cast<uint4*>(ws + k * kAbWS + 8 * c) = __ldg(reinterpret_cast<const uint4*>(wsrc + (size_t)k * kDc + 8 * c));
+      *reinterpret_cast<uint4*>(ws + k * kAbWS + 8 * c) = __ldcg(reinterpret_cast<const uint4*>(wsrc + (size_t)k * kDc + 8 * c));
     }
   }
   const uint32_t a_base = tc::smem_u32(as) + (((lane & 7) + 8 * ((lane >> 3) & 1)) * kAbAS + 8 * (lane >> 4)) * 2;
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(128) absorb_tiles_kernel(const ChunkParams p, 
         const int2 tk = toks[i >> 3];
         const int c = i & 7;
         if (tk.x < 0) continue;
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.qp + tk.x * p.qp_tok + h * p.qp_head + 8 * c));
+        const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p.qp + tk.x * p.qp_tok + h * p.qp_head + 8 * c));
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t o[4];
 #pragma unroll
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(128) absorb_tiles_kernel(const ChunkParams p, 
     for (int i = tid; i < 16 * 16; i += 128) {
       const int m = i >> 4, c = i & 15;
       uint4 v = make_uint4(0, 0, 0, 0);
-      if (toks[m].x >= 0) v = __ldg(reinterpret_cast<const uint4*>(p.qn + toks[m].x * p.qn_tok + h * p.qn_head + 8 * c));
+      if (toks[m].x >= 0) v = __ldcg(reinterpret_cast<const uint4*>(p.qn + toks[m].x * p.qn_tok + h * p.qn_head + 8 * c));
       *reinterpret_cast<uint4*>(as + m * kAbAS + 8 * c) = v;
     }
     __syncthreads();
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(128) project_kernel(const ChunkParams p) {
   const uint16_t* wsrc = p.w_uv + (size_t)h * kDc * kDv + n0;
   for (int i = tid; i < kDc * (kPrN / 8); i += 128) {
     const int k = i / (kPrN / 8), c = i % (kPrN / 8);
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(wsrc + (size_t)k * kDv + 8 * c));
+    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(wsrc + (size_t)k * kDv + 8 * c));
     *reinterpret_cast<uint4*>(ws + k * kPrWS + 8 * c) =
         make_uint4(tc::half2_bits(bf16lo(v.x), bf16hi(v.x)), tc::half2_bits(bf16lo(v.y), bf16hi(v.y)),
                    tc::half2_bits(bf16lo(v.z), bf16hi(v.z)), tc::half2_bits(bf16lo(v.w), bf16hi(v.w)));

@@ -14,12 +14,20 @@
 // need 4 x 64 TMEM columns for O^T and 2 x 64 for a double-buffered S^T.  C
 // is both operands, as it lies: K-major for S^T, MN-major for O^T.
 //
-// What bounds it: reading the cache (740 bytes per token for INT8).  The
-// chain per tile - dequantize, S^T, softmax, O^T - is pipelined over two key
-// buffers: warps 0..3 fill buffer 0, warps 4..7 buffer 1 (each thread keeps
-// several 32-channel units in flight, loaded ahead of the buffer's release),
-// warps 8..11 do the softmax, and one thread each of warps 12 and 13 issues
-// the S^T and the O^T MMAs, so that neither waits for the other's operands.
+// What bounds it: reading the cache (740 bytes per token for INT8), and for
+// 64-row tiles the shared-memory traffic of the MMAs' operands.  Cached bytes
+// come as bulk copies of whole 32-token blocks into a ring of shared-memory
+// slots (loads through L1 could not keep enough lines in flight next to 200
+// KB of shared memory: 4.7 bytes per cycle and SM); eight warps dequantize
+// them, lane = token, into the fp16 key tile.  A key tile is handed on in four
+// 128-channel pieces (and the RoPE block): the S^T MMAs of a piece start when
+// it is written, and the O^T MMAs release it piece by piece, so that a single
+// key buffer overlaps the conversion with both products; 16-row tiles of
+// quantized formats have room for two buffers.
+//
+// Warps: 0..7 dequantize, 8..11 softmax, 12 and 13 issue the S^T and the O^T
+// MMAs (apart, so that neither waits for the other's operands), 14 issues the
+// copies.
 //
 // Work split: all (row tile, key tile) units of the call, in order, are cut
 // into equal runs, one per SM, so ragged lengths need no care.  A row tile
@@ -40,22 +48,37 @@ namespace {
 
 using namespace tc;
 
-constexpr int kSThreads = 14 * 32;
+constexpr int kSThreads = 15 * 32;
 constexpr int kKeyBlk = kKeyTile * 128;              // one 64-key x 64-channel fp16 block: 8 KB
 constexpr int kKeyBuf = kQBlocks * kKeyBlk;          // 72 KB
 constexpr float kSlack = 8.f;                        // the running maximum rises only past this (P <= 2^8 in fp16)
+constexpr int kMaxSmem = 232448 - 1024;              // a block's shared memory, less the alignment slack
+constexpr int kMaxSlots = 4;
 
-template <int R>
-struct ShortSmem {
-  static constexpr int kQ = 2 * kKeyBuf;
+template <int LF, int KF, int R>
+struct Shape {
+  // two key buffers only where two raw blocks still fit beside them
+  static constexpr int kBlock = block_bytes<LF, KF>();
+  static constexpr int kFixed = kQBlocks * R * 128 + R * 128 + 4 * R * 4 + 512;        // Q, P, reduction, barriers
+  static constexpr int kNB = kMaxSmem - 2 * kKeyBuf - kFixed >= 2 * kBlock ? 2 : 1;
+  static constexpr int kRoom = (kMaxSmem - kNB * kKeyBuf - kFixed) / kBlock;
+  // even: a slot always holds the same half of a tile, so that the warps that
+  // wait for it see every phase of its barrier (a parity wait cannot skip one)
+  static constexpr int kSlots = kRoom < kMaxSlots ? kRoom / 2 * 2 : kMaxSlots;
+  static_assert(kSlots >= 2 && kSlots % 2 == 0, "one block under way while the other is read");
+  static constexpr int kQ = kNB * kKeyBuf;
   static constexpr int kP = kQ + kQBlocks * R * 128;
   static constexpr int kRed = kP + R * 128;          // [4 warps][R] maxima, then sums
-  static constexpr int kBars = kRed + 4 * R * 4;
-  static constexpr int kBytes = kBars + 192 + 1024;  // barriers and words; alignment slack
+  static constexpr int kRaw = kRed + 4 * R * 4;      // 256-byte aligned for R >= 16
+  static constexpr int kBars = kRaw + kSlots * kBlock;
+  static constexpr int kBytes = kBars + 512 + 1024;  // barriers and words; alignment slack
 };
-static_assert(ShortSmem<64>::kBytes <= 232448, "a block's shared memory");
 
-enum { bFull0 = 0, bFull1, bP0, bP1, bFree0, bFree1, bS0, bS1, bQ, bFinS, bFinO, bCount };
+// Barriers: per key buffer and piece (4 x 128 channels, 4: the RoPE block)
+// "written" and "free"; S^T and P per score buffer; raw slots.
+enum { bWritten = 0, bFree = bWritten + 10, bS = bFree + 10, bP = bS + 2, bRaw = bP + 2, bRawFree = bRaw + kMaxSlots,
+       bQ = bRawFree + kMaxSlots, bFinS, bFinO, bCount };
+static_assert(8 * bCount + 16 + 16 + 4 * 2 * kMaxSlots <= 512, "barriers and words");
 
 // One run's walk over the units: segments (a row tile, key tiles t0 .. t1).
 struct Walk {
@@ -110,21 +133,6 @@ struct Walk {
   }
 };
 
-// ---- producers: dequantize a key tile into fp16 blocks
-// Warp w of a group takes the tile's tokens 16 w .. 16 w + 15.  Latent steps
-// 0..7: eight tokens x four units, lane = token + 8 unit, so that a quarter
-// warp's 16-byte stores hit eight different swizzled positions, and a scale
-// load covers whole 32-byte sectors.  The last step: k_pe, sixteen tokens x
-// two units.
-template <int LF, int KF>
-struct Producer {
-  static constexpr int kAhead = LF == MLA_FMT_BF16 ? 2 : 4;      // latent steps in flight
-  static __device__ __forceinline__ int token(int w, int lane, int step) {
-    return step < 8 ? 16 * w + 8 * (step >> 2) + (lane & 7) : 16 * w + (lane & 15);
-  }
-  static __device__ __forceinline__ int unit(int lane, int step) { return step < 8 ? 4 * (step & 3) + (lane >> 3) : lane >> 4; }
-};
-
 // A unit's 32 fp16 channels into their block, swizzled.
 __device__ __forceinline__ void put_unit(const uint32_t* h, uint32_t buf, int tok, int unit) {
   const uint32_t row = buf + (unit >> 1) * kKeyBlk + tok * 128, flip = (4 * (unit & 1) ^ (tok & 7)) << 4;
@@ -137,21 +145,36 @@ __device__ __forceinline__ void put_unit(const uint32_t* h, uint32_t buf, int to
 
 template <int LF, int KF, int R>
 __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const ChunkParams p) {
-  using SM = ShortSmem<R>;
-  using PR = Producer<LF, KF>;
+  using SH = Shape<LF, KF, R>;
+  constexpr int NB = SH::kNB, NS = SH::kSlots;
   extern __shared__ uint8_t short_smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(short_smem_raw) + 1023) & ~(uintptr_t)1023);
-  const uint32_t sb = smem_u32(sm), bars = sb + SM::kBars;
-  uint8_t* words = sm + SM::kBars + 8 * bCount;
+  const uint32_t sb = smem_u32(sm), bars = sb + SH::kBars;
+  uint8_t* words = sm + SH::kBars + 8 * bCount;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words);
   volatile int* abort = reinterpret_cast<volatile int*>(words + 4);
-  volatile int* tile_ok = reinterpret_cast<volatile int*>(words + 8);        // [2 buffers]
-  uint32_t* bad = reinterpret_cast<uint32_t*>(words + 16);                   // [2 buffers][2]: a bit per token
+  volatile int* tile_ok = reinterpret_cast<volatile int*>(words + 8);        // [2], by tile parity
+  uint32_t* bad = reinterpret_cast<uint32_t*>(words + 16);                   // [2][2]: a bit per token
+  volatile int* slot_len = reinterpret_cast<volatile int*>(words + 32);      // [slots] tokens of the block, -1: no page
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kCols = R == 64 ? 512 : 8 * R;       // 6 R columns used, a power of two allocated
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < bCount; ++i) bar_init(bars + 8 * i, i <= bP1 ? 128 : 1);
+    for (int i = 0; i < 10; ++i) {
+      bar_init(bars + 8 * (bWritten + i), i % 5 == 4 ? 128 : 256);
+      bar_init(bars + 8 * (bFree + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(bars + 8 * (bS + i), 1);
+      bar_init(bars + 8 * (bP + i), 128);
+    }
+    for (int i = 0; i < kMaxSlots; ++i) {
+      bar_init(bars + 8 * (bRaw + i), 1);
+      bar_init(bars + 8 * (bRawFree + i), 128);
+    }
+    bar_init(bars + 8 * bQ, 1);
+    bar_init(bars + 8 * bFinS, 1);
+    bar_init(bars + 8 * bFinO, 1);
     *abort = 0;
     for (int i = 0; i < 4; ++i) bad[i] = 0;
     bar_init_fence();
@@ -170,125 +193,86 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
   const int x = blockIdx.x;
   const bool work = x < G;
   const int64_t lo = work ? U * x / G : 0, hi = work ? U * (x + 1) / G : 0;
-  Walk wk;
-  wk.n_seqs = __ldcg(&p.counts->s_seqs);
   bool ok = true;
   if (work && warp < 8) {
-    // ---- producers
-    wk.start(p, lo, hi);
-    const int g = warp >> 2, w = warp & 3;
-    const uint32_t buf = sb + g * kKeyBuf;
-    uint32_t* mybad = bad + 2 * g;
-    // This group's tiles, every second of the run, are visited one ahead of
-    // the loads: `next` holds the tile whose page id is under way.
-    struct Tile {
-      int page, pos, len;
-    } next = {-1, 0, 0};
-    int t = 0, seg_t1 = 0, skip = g;
-    const int32_t* pages = nullptr;
-    auto advance = [&]() -> bool {           // next = the group's next tile; false at the end
-      t += skip;
-      while (t >= seg_t1) {
-        const int over = t - seg_t1;
-        if (!wk.next()) return false;
-        seg_t1 = wk.t1;
-        t = wk.t0 + over;
-        next.len = wk.s.len;
-        pages = p.block_table + (int64_t)wk.s.b * p.max_pages;
-      }
-      skip = 2;
-      next.pos = t * kKeyTile;
-      next.page = __ldg(pages + t);
-      return true;
-    };
-    RawUnit<LF, false> ring[PR::kAhead];
-    RawUnit<KF, true> kpe;
-    const uint8_t* page = nullptr;           // the loading tile; tokens from t_len on read as 0
-    int t_len = 0;
-    bool page_ok = false, more = advance(), after = false;
-    auto enter = [&]() {                     // `next` becomes the loading tile
-      page_ok = next.page >= 0 && next.page < p.num_pages;
-      page = p.pool + (int64_t)(page_ok ? next.page : 0) * p.L.page_bytes;
-      t_len = page_ok ? next.len - next.pos : 0;
-      if (!page_ok && (threadIdx.x & 127) == 0) set_err(p.dev_err, MLA_DEVERR_PAGE);
-      after = advance();
-    };
-    auto load_step = [&](int step, RawUnit<LF, false>& r) {
-      const int tok = PR::token(w, lane, step);
-      if (tok < t_len) load_unit<LF, false>(page + (tok >> 5) * p.L.block_bytes, p.L, tok & 31, PR::unit(lane, step), r);
-    };
-    if (more) {
-      enter();
-#pragma unroll
-      for (int i = 0; i < PR::kAhead; ++i) load_step(i, ring[i]);
-    }
-    uint32_t n = 0;                          // the group's tiles so far
-    while (more) {
-      // the tile being stored, while page / t_len move on to the next
-      const uint8_t* s_page = page;
-      const int s_len = t_len;
-      const bool s_ok = page_ok;
-      {
-        const int tok = PR::token(w, lane, 8);
-        if (tok < s_len)
-          load_unit<KF, true>(s_page + (tok >> 5) * p.L.block_bytes, p.L, tok & 31, PR::unit(lane, 8), kpe);
-      }
-      if (n >= 1 && !bar_wait(bars + 8 * (bFree0 + g), (n - 1) & 1, p.wait_ns, abort)) {
+    // ---- dequantize.  Warps 0..3: the tile's first block, 4..7: the second;
+    // warp w % 4 takes unit w % 4 of every 128-channel piece, warps 0 and 1 of
+    // each four the RoPE units too; lane = token.
+    const int half = warp >> 2, q = warp & 3, tok = 32 * half + lane;
+    const uint32_t n_tiles = (uint32_t)(hi - lo);
+    for (uint32_t it = 0; it < n_tiles; ++it) {
+      const uint32_t blk = 2 * it + half, slot = blk % NS, g = it & 1, kb = it % NB, ph = it / NB;
+      if (!warp_wait(bars + 8 * (bRaw + slot), (blk / NS) & 1, p.wait_ns, abort)) {
         ok = false;
         break;
       }
-      uint32_t bad_lo = 0, bad_hi = 0;
-      const bool go_on = after;
+      const uint8_t* raw = sm + SH::kRaw + slot * SH::kBlock;
+      const int n_tok = slot_len[slot];
+      const bool live = lane < n_tok;
+      RawUnit<LF, false> r[4];
+      RawUnit<KF, true> rk;
+      uint32_t outl_words[LF == MLA_FMT_INT8_OUTLIER ? 4 : 1][16];
+      if (live) {
 #pragma unroll
-      for (int step = 0; step < 8; ++step) {
-        const int tok = PR::token(w, lane, step), unit = PR::unit(lane, step);
+        for (int s = 0; s < 4; ++s) load_unit<LF, false>(raw, p.L, lane, 4 * s + q, r[s]);
+        if (q < 2) load_unit<KF, true>(raw, p.L, lane, q, rk);
+      }
+      bool fine = true;
+      if constexpr (LF == MLA_FMT_INT8_OUTLIER) {      // needs the block's other fields: converted before the slot goes
+        if (live) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            fine &= convert_unit<LF, false>(r[s], outl_words[s]);
+            fine &= patch_outliers<LF>(raw, p.L, p.outl, lane, 4 * s + q, outl_words[s]);
+          }
+        }
+      }
+      bar_arrive(bars + 8 * (bRawFree + slot));
+#pragma unroll
+      for (int s = 0; s < 5; ++s) {
+        if (s == 4 && q >= 2) break;
         uint32_t h[16];
-        bool fine = true;
-        if (tok < s_len) {
-          fine = convert_unit<LF, false>(ring[step % PR::kAhead], h);
-          fine &= patch_outliers<LF>(s_page + (tok >> 5) * p.L.block_bytes, p.L, p.outl, tok & 31, unit, h);
-        } else {
+        if (!live) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) h[i] = 0u;
-        }
-        if (step + PR::kAhead < 8) {
-          load_step(step + PR::kAhead, ring[step % PR::kAhead]);
-        } else {
-          if (step + PR::kAhead == 8 && go_on) enter();
-          if (go_on) load_step(step + PR::kAhead - 8, ring[step % PR::kAhead]);
-        }
-        put_unit(h, buf, tok, unit);
-        if (!fine) (tok < 32 ? bad_lo : bad_hi) |= 1u << (tok & 31);
-      }
-      {
-        const int tok = PR::token(w, lane, 8), unit = PR::unit(lane, 8);
-        uint32_t h[16];
-        bool fine = true;
-        if (tok < s_len) {
-          fine = convert_unit<KF, true>(kpe, h);
-        } else {
+        } else if (s == 4) {
+          fine &= convert_unit<KF, true>(rk, h);
+        } else if constexpr (LF == MLA_FMT_INT8_OUTLIER) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) h[i] = 0u;
+          for (int i = 0; i < 16; ++i) h[i] = outl_words[s & 3][i];
+        } else {
+          fine &= convert_unit<LF, false>(r[s & 3], h);
         }
-        put_unit(h, buf, tok, kLatentUnits + unit);
-        if (!fine) (tok < 32 ? bad_lo : bad_hi) |= 1u << (tok & 31);
+        // the piece of the tile NB before is free
+        if (it >= NB && !warp_wait(bars + 8 * (bFree + 5 * kb + s), (ph - 1) & 1, p.wait_ns, abort)) {
+          ok = false;
+          break;
+        }
+        put_unit(h, sb + kb * kKeyBuf, tok, s < 4 ? 4 * s + q : kLatentUnits + q);
+        if (s == 4 || (s == 3 && q >= 2)) {
+          // the last piece this warp writes: its tokens' flags go with it
+          if (half == 0 && q == 0 && lane == 0) tile_ok[g] = n_tok >= 0;
+          if (!fine) atomicOr(bad + 2 * g + half, 1u << lane);
+        }
+        fence_async_smem();
+        bar_arrive(bars + 8 * (bWritten + 5 * kb + s));
       }
-      if (bad_lo) atomicOr(mybad, bad_lo);
-      if (bad_hi) atomicOr(mybad + 1, bad_hi);
-      if ((threadIdx.x & 127) == 0) tile_ok[g] = s_ok;
-      fence_async_smem();
-      bar_arrive(bars + 8 * (bFull0 + g));
-      ++n;
-      more = go_on;
+      if (!ok) break;
+    }
+    if (!ok) {
+      set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
+      *abort = 1;
     }
   } else if (work && warp < 12) {
+    Walk wk;
+    wk.n_seqs = __ldcg(&p.counts->s_seqs);
     // ---- softmax.  Thread (w, lane) holds keys 16 w + lane / 4 and + 8 of
     // the tile, rows 8 j + 2 (lane % 4) and the next (j < R / 8).
     wk.start(p, lo, hi);
     const int w = warp & 3;
     const uint32_t tl = (uint32_t)(32 * w) << 16;
     constexpr int J = R / 8;
-    float* red = reinterpret_cast<float*>(sm + SM::kRed);
+    float* red = reinterpret_cast<float*>(sm + SH::kRed);
     uint32_t it = 0;
     while (ok && wk.next()) {
       const int row0 = wk.item * R, rows = min(R, wk.s.n * p.H - row0);
@@ -302,7 +286,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
       }
       for (int t = wk.t0; t < wk.t1; ++t, ++it) {
         const uint32_t g = it & 1;
-        if (!warp_wait(bars + 8 * (bS0 + g), (it >> 1) & 1, p.wait_ns, abort)) {
+        if (!warp_wait(bars + 8 * (bS + g), (it >> 1) & 1, p.wait_ns, abort)) {
           ok = false;
           break;
         }
@@ -368,7 +352,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
         }
         any = __any_sync(0xffffffffu, any);
         // the O^T of the tile before is complete: P is free, and O^T may be rescaled
-        if (it >= 1 && !warp_wait(bars + 8 * (bFree0 + (g ^ 1)), ((it - 1) >> 1) & 1, p.wait_ns, abort)) {
+        if (it >= 1 && !warp_wait(bars + 8 * (bFree + 5 * ((it - 1) % NB) + 3), ((it - 1) / NB) & 1, p.wait_ns, abort)) {
           ok = false;
           break;
         }
@@ -410,12 +394,12 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
 #pragma unroll
         for (int j = 0; j < J; j += 2) {
           const int mat = lane >> 3, rr = 8 * (j + (mat >> 1)) + (lane & 7), oct = 2 * w + (mat & 1);
-          stmatrix_x4_trans(sb + SM::kP + rr * 128 + ((oct ^ (rr & 7)) << 4), h[2 * j], h[2 * j + 1], h[2 * j + 2],
+          stmatrix_x4_trans(sb + SH::kP + rr * 128 + ((oct ^ (rr & 7)) << 4), h[2 * j], h[2 * j + 1], h[2 * j + 2],
                             h[2 * j + 3]);
         }
         fence_async_smem();
         fence_before();
-        bar_arrive(bars + 8 * (bP0 + g));
+        bar_arrive(bars + 8 * (bP + g));
       }
       if (!ok) break;
       // ---- the segment's end: sums over all keys, then O^T
@@ -444,7 +428,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
         l[2 * j] = a.x;
         l[2 * j + 1] = a.y;
       }
-      if (!warp_wait(bars + 8 * (bFree0 + ((it - 1) & 1)), ((it - 1) >> 1) & 1, p.wait_ns, abort)) {
+      if (!warp_wait(bars + 8 * (bFree + 5 * ((it - 1) % NB) + 3), ((it - 1) / NB) & 1, p.wait_ns, abort)) {
         ok = false;
         break;
       }
@@ -505,41 +489,49 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
     }
   } else if (work && warp == 12) {
     // ---- one thread: the query tiles' copies and the S^T MMAs
+    Walk wk;
+    wk.n_seqs = __ldcg(&p.counts->s_seqs);
     wk.start(p, lo, hi);
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t kId = f16_idesc(64, R, false, false);
       constexpr int kQBytes = kQBlocks * R * 128;
-      const uint64_t d_q = sw128_desc(sb + SM::kQ, 16, 1024), d_k = sw128_desc(sb, 16, 1024);
+      const uint64_t d_q = sw128_desc(sb + SH::kQ, 16, 1024), d_k = sw128_desc(sb, 16, 1024);
       uint32_t it = 0, seg = 0;
       while (ok && wk.next()) {
         // the query tile: its readers, the S^T MMAs of the segment before, are done
-        if (seg > 0 && !bar_wait(bars + 8 * (bS0 + ((it - 1) & 1)), ((it - 1) >> 1) & 1, p.wait_ns, abort)) {
+        if (seg > 0 && !bar_wait(bars + 8 * (bS + ((it - 1) & 1)), ((it - 1) >> 1) & 1, p.wait_ns, abort)) {
           ok = false;
           break;
         }
         bar_expect(bars + 8 * bQ, kQBytes);
-        bulk_copy(sb + SM::kQ, p.q_tiles + (int64_t)(wk.s.item0 + wk.item) * kQBytes, kQBytes, bars + 8 * bQ);
+        bulk_copy(sb + SH::kQ, p.q_tiles + (int64_t)(wk.s.item0 + wk.item) * kQBytes, kQBytes, bars + 8 * bQ);
         ++seg;
         if (!bar_wait(bars + 8 * bQ, (seg - 1) & 1, p.wait_ns, abort)) {
           ok = false;
           break;
         }
-        for (int t = wk.t0; t < wk.t1; ++t, ++it) {
-          const uint32_t g = it & 1;
-          // the keys are there, and the softmax has read this S^T buffer's last tile
-          if (!bar_wait(bars + 8 * (bFull0 + g), (it >> 1) & 1, p.wait_ns, abort) ||
-              (it >= 2 && !bar_wait(bars + 8 * (bP0 + g), ((it - 2) >> 1) & 1, p.wait_ns, abort))) {
+        for (int t = wk.t0; t < wk.t1 && ok; ++t, ++it) {
+          const uint32_t g = it & 1, kb = it % NB, ph = (it / NB) & 1;
+          // the softmax has read this S^T buffer's last tile
+          if (it >= 2 && !bar_wait(bars + 8 * (bP + g), ((it - 2) >> 1) & 1, p.wait_ns, abort)) {
             ok = false;
             break;
           }
-          fence_after();
-          const uint64_t a = d_k + (uint64_t)(g * (kKeyBuf >> 4));
+          const uint64_t a = d_k + (uint64_t)(kb * (kKeyBuf >> 4));
+          const uint32_t d = t_s + g * R;
 #pragma unroll
-          for (int kb = 0; kb < kQBlocks; ++kb)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma(t_s + g * R, a + ((kb * kKeyBlk + 32 * k) >> 4), d_q + ((kb * R * 128 + 32 * k) >> 4), kId, (kb | k) != 0);
-          umma_commit(bars + 8 * (bS0 + g));
+          for (int s = 0; s < 5; ++s) {
+            if (!bar_wait(bars + 8 * (bWritten + 5 * kb + s), ph, p.wait_ns, abort)) {
+              ok = false;
+              break;
+            }
+            fence_after();
+            umma4<2, 2>(d, a + (2 * s * kKeyBlk >> 4), d_q + (2 * s * R * 128 >> 4), kId, s != 0);
+            if (s < 4) umma4<2, 2>(d, a + ((2 * s + 1) * kKeyBlk >> 4), d_q + ((2 * s + 1) * R * 128 >> 4), kId, 1u);
+          }
+          if (!ok) break;
+          umma_commit(bars + 8 * (bFree + 5 * kb + 4));     // the RoPE block is read here only
+          umma_commit(bars + 8 * (bS + g));
         }
       }
       if (!ok) {
@@ -551,28 +543,29 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
       drain_wait(bars + 8 * bFinS, 0);
     }
     __syncwarp();
-  } else if (work) {
-    // ---- warp 13, one thread: the O^T MMAs
+  } else if (work && warp == 13) {
+    // ---- one thread: the O^T MMAs
+    Walk wk;
+    wk.n_seqs = __ldcg(&p.counts->s_seqs);
     wk.start(p, lo, hi);
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t kId = f16_idesc(128, R, true, false);
-      const uint64_t d_p = sw128_desc(sb + SM::kP, 16, 1024), d_v = sw128_desc(sb, kKeyBlk, 1024);
+      const uint64_t d_p = sw128_desc(sb + SH::kP, 16, 1024), d_v = sw128_desc(sb, kKeyBlk, 1024);
       uint32_t it = 0;
       while (ok && wk.next()) {
         for (int t = wk.t0; t < wk.t1; ++t, ++it) {
-          const uint32_t g = it & 1;
-          if (!bar_wait(bars + 8 * (bP0 + g), (it >> 1) & 1, p.wait_ns, abort)) {
+          const uint32_t g = it & 1, kb = it % NB;
+          if (!bar_wait(bars + 8 * (bP + g), (it >> 1) & 1, p.wait_ns, abort)) {
             ok = false;
             break;
           }
           fence_after();
-          const uint64_t a = d_v + (uint64_t)(g * (kKeyBuf >> 4));
+          const uint64_t a = d_v + (uint64_t)(kb * (kKeyBuf >> 4));
 #pragma unroll
-          for (int blk = 0; blk < 4; ++blk)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma(tbase + blk * R, a + ((2 * blk * kKeyBlk + 2048 * k) >> 4), d_p + ((32 * k) >> 4), kId, t > wk.t0 || k != 0);
-          umma_commit(bars + 8 * (bFree0 + g));
+          for (int s = 0; s < 4; ++s) {
+            umma4<(2048 >> 4), 2>(tbase + s * R, a + (2 * s * kKeyBlk >> 4), d_p, kId, t > wk.t0);
+            umma_commit(bars + 8 * (bFree + 5 * kb + s));
+          }
         }
       }
       if (!ok) {
@@ -583,10 +576,51 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
       drain_wait(bars + 8 * bFinO, 0);
     }
     __syncwarp();
-  }
-  if (warp < 8 && !ok) {
-    set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
-    *abort = 1;
+  } else if (work) {
+    // ---- warp 14: the cache's blocks into the raw slots.  The lanes fetch 32
+    // page ids of the segment at a time, lane 0 issues.
+    Walk wk;
+    wk.n_seqs = __ldcg(&p.counts->s_seqs);
+    wk.start(p, lo, hi);
+    uint32_t blk = 0;
+    while (ok && wk.next()) {
+      const int32_t* pages = p.block_table + (int64_t)wk.s.b * p.max_pages;
+      for (int t0 = wk.t0; t0 < wk.t1 && ok; t0 += 32) {
+        const int mine = t0 + lane < wk.t1 ? __ldcg(pages + t0 + lane) : 0;
+        for (int t = t0; t < min(wk.t1, t0 + 32) && ok; ++t) {
+          const int page = __shfl_sync(0xffffffffu, mine, t - t0);
+          const bool page_ok = page >= 0 && page < p.num_pages;
+          if (!page_ok && lane == 0) set_err(p.dev_err, MLA_DEVERR_PAGE);
+#pragma unroll
+          for (int half = 0; half < 2; ++half, ++blk) {
+            const uint32_t slot = blk % NS;
+            if (blk >= NS && !warp_wait(bars + 8 * (bRawFree + slot), ((blk / NS) - 1) & 1, p.wait_ns, abort)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              const int n_tok = min(32, max(0, wk.s.len - t * kKeyTile - 32 * half));
+              slot_len[slot] = page_ok ? n_tok : -1;
+              if (page_ok && n_tok > 0) {
+                bar_expect(bars + 8 * (bRaw + slot), SH::kBlock);
+                bulk_copy(sb + SH::kRaw + slot * SH::kBlock, p.pool + (int64_t)page * p.L.page_bytes + half * p.L.block_bytes,
+                          SH::kBlock, bars + 8 * (bRaw + slot));
+              } else {
+                bar_arrive(bars + 8 * (bRaw + slot));
+              }
+            }
+            __syncwarp();
+          }
+        }
+      }
+    }
+    if (!ok) {
+      if (lane == 0) set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
+      *abort = 1;
+    }
+    // the copies in flight land before the block ends
+    for (uint32_t s = 0; s < NS; ++s)
+      if (blk > s) drain_wait(bars + 8 * (bRaw + s), ((blk - 1 - s) / NS) & 1);
   }
   fence_before();
   __syncthreads();
@@ -603,31 +637,34 @@ __global__ void __launch_bounds__(128) short_combine_kernel(const ChunkParams p,
   pdl_launch_dependents();
   pdl_wait();
   const int x = blockIdx.x, c = blockIdx.y, tid = threadIdx.x;
-  const SplitRec rec = p.splits[x];
-  if (c >= rec.rows) return;
+  const SplitRec* sr = p.splits + x;
+  const int rows = __ldcg(&sr->rows);
+  if (c >= rows) return;
+  const int last = __ldcg(&sr->last);
+  const int64_t row0 = __ldcg(&sr->row0);
   const int64_t stride = 2 * partial_floats(R);
   const float* part = p.parts + (int64_t)(2 * x + 1) * partial_floats(R);
-  const int n = rec.last - x + 1;
+  const int n = last - x + 1;
   // part 0 is slot 2x + 1, part i > 0 slot 2 (x + i): one slot before the regular stride
   auto at = [&](int i) { return part + i * stride - (i ? partial_floats(R) : 0); };
   float mx = -INFINITY;
-  for (int i = 0; i < n; ++i) mx = fmaxf(mx, at(i)[R * kDc + c]);
+  for (int i = 0; i < n; ++i) mx = fmaxf(mx, __ldcg(at(i) + R * kDc + c));
   if (mx == -INFINITY) mx = 0.f;
   float l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int i = 0; i < n; ++i) {
     const float* s = at(i);
-    const float wt = tc::ex2(s[R * kDc + c] - mx);
-    const float4 v = reinterpret_cast<const float4*>(s + (int64_t)c * kDc)[tid];
-    l = fmaf(wt, s[R * kDc + R + c], l);
+    const float wt = tc::ex2(__ldcg(s + R * kDc + c) - mx);
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(s + (int64_t)c * kDc) + tid);
+    l = fmaf(wt, __ldcg(s + R * kDc + R + c), l);
     acc.x = fmaf(wt, v.x, acc.x);
     acc.y = fmaf(wt, v.y, acc.y);
     acc.z = fmaf(wt, v.z, acc.z);
     acc.w = fmaf(wt, v.w, acc.w);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  reinterpret_cast<uint2*>(p.o_lat + (rec.row0 + c) * kDc)[tid] =
+  reinterpret_cast<uint2*>(p.o_lat + (row0 + c) * kDc)[tid] =
       make_uint2(tc::half2_bits(acc.x * inv, acc.y * inv), tc::half2_bits(acc.z * inv, acc.w * inv));
 }
 
@@ -638,12 +675,12 @@ mla_status launch_r(const ChunkParams& p, cudaStream_t stream) {
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !configured[dev]) {
     const mla_status st = cuda_status(cudaFuncSetAttribute(
-        short_attention_kernel<LF, KF, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, ShortSmem<R>::kBytes));
+        short_attention_kernel<LF, KF, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<LF, KF, R>::kBytes));
     if (st != MLA_OK) return st;
     if (dev >= 0 && dev < 64) configured[dev] = 1;
   }
   const mla_status st = cuda_status(launch_pdl(short_attention_kernel<LF, KF, R>, dim3(p.grid), dim3(kSThreads),
-                                               ShortSmem<R>::kBytes, stream, p));
+                                               Shape<LF, KF, R>::kBytes, stream, p));
   if (st != MLA_OK) return st;
   return cuda_status(launch_pdl(short_combine_kernel, dim3(p.grid, R), dim3(128), 0, stream, p, R));
 }

@@ -34,7 +34,20 @@ struct RawUnit {
   float z[S::kZeros ? S::kScales : 1];
 };
 
-// Unit c of block token u; blk is the token's 32-token block.
+// Bytes of a 32-token block of a format pair (compute_layout's block_bytes).
+template <int LF, int KF>
+constexpr int block_bytes() {
+  const int codes = 32 * UnitShape<LF, false>::kWords * 16 * kLatentUnits, kpe = 32 * UnitShape<KF, true>::kWords * 16 * kKpeUnits;
+  const int quant = LF == MLA_FMT_BF16 ? 0 : 128 * (kDc / latent_group_size(LF)) * (LF == MLA_FMT_INT4_ASYM ? 2 : 1) + 128;
+  return codes + kpe + quant + (KF == MLA_FMT_BF16 ? 0 : 128 * kNKG) + (LF == MLA_FMT_INT8_OUTLIER ? kOutFieldBytes : 0);
+}
+static_assert(block_bytes<MLA_FMT_INT8_SYM, MLA_FMT_INT8_SYM>() == 32 * 740 && block_bytes<MLA_FMT_BF16, MLA_FMT_BF16>() == 32 * 1152 &&
+                  block_bytes<MLA_FMT_INT4_ASYM, MLA_FMT_INT4_SYM>() == 32 * 580,
+              "the documented page sizes");
+
+// Unit c of block token u; blk is the token's 32-token block, in shared memory
+// (staged by a bulk copy).  A warp with one token per lane reads without bank
+// conflicts: scales lie side by side, chunks are swizzled by token.
 template <int FMT, bool KPE>
 __device__ __forceinline__ void load_unit(const uint8_t* blk, const PageLayout& L, int u, int c, RawUnit<FMT, KPE>& r) {
   using S = UnitShape<FMT, KPE>;
@@ -42,17 +55,17 @@ __device__ __forceinline__ void load_unit(const uint8_t* blk, const PageLayout& 
 #pragma unroll
   for (int i = 0; i < S::kWords; ++i) {
     const int chunk = c * S::kWords + i;
-    r.w[i] = __ldg(row + (KPE ? kpe_chunk_pos(chunk, u, FMT) : latent_chunk_pos(chunk, u)));
+    r.w[i] = *(row + (KPE ? kpe_chunk_pos(chunk, u, FMT) : latent_chunk_pos(chunk, u)));
   }
   if constexpr (S::kScales > 0) {
     const float* sc = reinterpret_cast<const float*>(blk + (KPE ? L.kpe_scale_off : L.scale_off));
     const int g0 = c * kUnitChannels / S::kGroup;
 #pragma unroll
-    for (int i = 0; i < S::kScales; ++i) r.s[i] = __ldg(sc + (g0 + i) * kBlockTokens + u);
+    for (int i = 0; i < S::kScales; ++i) r.s[i] = sc[(g0 + i) * kBlockTokens + u];
     if constexpr (S::kZeros) {
       const float* zp = reinterpret_cast<const float*>(blk + L.zero_off);
 #pragma unroll
-      for (int i = 0; i < S::kScales; ++i) r.z[i] = __ldg(zp + (g0 + i) * kBlockTokens + u);
+      for (int i = 0; i < S::kScales; ++i) r.z[i] = zp[(g0 + i) * kBlockTokens + u];
     }
   }
 }
@@ -160,7 +173,7 @@ __device__ __forceinline__ bool patch_outliers(const uint8_t* blk, const PageLay
     for (int k = 0; k < kNOut; ++k) {
       const int ch = outl.ch[k];
       if ((ch >> 5) != c) continue;
-      float v = bf16f(__ldg(ov + k * kBlockTokens + u));
+      float v = bf16f(ov[k * kBlockTokens + u]);
       if (!(fabsf(v) <= kHalfMax)) {
         fine = false;
         v = 0.f;

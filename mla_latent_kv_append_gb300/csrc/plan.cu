@@ -100,9 +100,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     row[k] = -1;
     const int b = b0 + k;
     if (k < per && b < p.B) {
-      ctx[k] = p.ctx[b];
-      nw[k] = p.nw[b];
-      row[k] = p.req[b];
+      ctx[k] = __ldcg(p.ctx + b);
+      nw[k] = __ldcg(p.nw + b);
+      row[k] = __ldcg(p.req + b);
       if (row[k] < 0 || row[k] >= p.rows) {
         err |= MLA_DEVERR_PAGE;
         row[k] = -1;
@@ -140,9 +140,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     }
   }
   if (tid == 0) s_start[p.B] = (int)(total < p.n ? total : p.n);
-  const int head = p.free_range[0];
-  int avail = p.free_range[1] - head;
-  if (head < 0 || p.free_range[1] > p.free_len || avail < 0) {
+  const int head = __ldcg(p.free_range), tail = __ldcg(p.free_range + 1);
+  int avail = tail - head;
+  if (head < 0 || tail > p.free_len || avail < 0) {
     err |= MLA_DEVERR_PAGE;
     avail = 0;
   }
@@ -194,11 +194,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       }
       b = lo;
       if (s_first[b] >= 0) {
-        const int c = p.ctx[b];
+        const int c = __ldcg(p.ctx + b);
         pos = c + (int)(i - s_start[b]);
         const int pg = pos / kPage, old = pages_of(c);
-        const int id = pg < old ? p.table[(int64_t)p.req[b] * p.max_pages + pg]
-                                : p.free_pages[head + s_first[b] + pg - old];
+        const int id = pg < old ? __ldcg(p.table + (int64_t)__ldcg(p.req + b) * p.max_pages + pg)
+                                : __ldcg(p.free_pages + head + s_first[b] + pg - old);
         if (id >= 0 && id < p.num_pages) slot = id * kPage + (pos & (kPage - 1));
         else set_err(p.dev_err, MLA_DEVERR_PAGE);
       }
@@ -214,10 +214,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     if (pg >= p.max_pages) continue;
     int id = -1;
     if (s_first[b] >= 0) {
-      const int c = p.ctx[b], old = pages_of(c);
-      if (pg < pages_of(c + p.nw[b])) {
-        int32_t* mine = p.table + (int64_t)p.req[b] * p.max_pages + pg;
-        id = pg < old ? *mine : p.free_pages[head + s_first[b] + pg - old];
+      const int c = __ldcg(p.ctx + b), old = pages_of(c);
+      if (pg < pages_of(c + __ldcg(p.nw + b))) {
+        int32_t* mine = p.table + (int64_t)__ldcg(p.req + b) * p.max_pages + pg;
+        id = pg < old ? __ldcg(mine) : __ldcg(p.free_pages + head + s_first[b] + pg - old);
         if (id < 0 || id >= p.num_pages) {
           set_err(p.dev_err, MLA_DEVERR_PAGE);
           id = -1;

@@ -96,6 +96,26 @@ __device__ __forceinline__ void umma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar)
                : "memory");
 }
+// One lane of a converged warp.  MMAs issued under this predicate keep their
+// descriptors in uniform registers: an issue costs the operands' shared-memory
+// time (24 cycles for M = 64, N = 16, K = 16), under a plain lane == 0 test 45.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+// Four MMAs along the contraction (64 elements), the operands' descriptors
+// stepping by A and B (in 16-byte units); accumulate: the first one's.
+template <int A, int B>
+__device__ __forceinline__ void umma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      " add.s64 x, %1, %5;\n add.s64 y, %2, %6;\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, 1;\n"
+      " add.s64 x, %1, %7;\n add.s64 y, %2, %8;\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, 1;\n"
+      " add.s64 x, %1, %9;\n add.s64 y, %2, %10;\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, 1;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(A), "n"(B), "n"(2 * A), "n"(2 * B), "n"(3 * A), "n"(3 * B));
+}
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
