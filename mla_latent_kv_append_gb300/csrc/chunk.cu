@@ -433,7 +433,11 @@ mla_status mla_chunk_attention(const mla_cache_layer* cache, const uint16_t* q_n
   const int za = 4 * p.grid / (9 * heads) + 1, zp = 4 * p.grid / (4 * heads) + 1;
   s = cuda_status(launch_pdl(absorb_tiles_kernel, dim3(heads, 9, tok_tiles < za ? tok_tiles : za), dim3(128), 0, st, p, R));
   if (s != MLA_OK) return s;
-  s = launch_short_attention(p, cache->latent_fmt, cache->kpe_fmt, R, st);
+  const int lf = cache->latent_fmt, kf = cache->kpe_fmt;
+  s = lf == MLA_FMT_BF16       ? launch_short_bf16(p, lf, kf, R, st)
+      : lf == MLA_FMT_INT8_SYM ? launch_short_int8(p, lf, kf, R, st)
+      : is_int8_latent(lf)     ? launch_short_int8_blocks(p, lf, kf, R, st)
+                               : launch_short_int4(p, lf, kf, R, st);
   if (s != MLA_OK) return s;
   return cuda_status(launch_pdl(project_kernel, dim3(heads, kDv / kPrN, tok_tiles < zp ? tok_tiles : zp), dim3(128), 0, st, p));
 }

@@ -76,27 +76,11 @@ inline int short_rows_per_tile(int max_new, int heads) {
   return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
 }
 
-// Every (latent, k_pe) format pair of a cache.
-#define MLA_CHUNK_FORMATS(X)                     \
-  X(MLA_FMT_BF16, MLA_FMT_BF16)                  \
-  X(MLA_FMT_BF16, MLA_FMT_INT8_SYM)              \
-  X(MLA_FMT_BF16, MLA_FMT_INT4_SYM)              \
-  X(MLA_FMT_INT8_SYM, MLA_FMT_BF16)              \
-  X(MLA_FMT_INT8_SYM, MLA_FMT_INT8_SYM)          \
-  X(MLA_FMT_INT8_SYM, MLA_FMT_INT4_SYM)          \
-  X(MLA_FMT_INT4_ASYM, MLA_FMT_BF16)             \
-  X(MLA_FMT_INT4_ASYM, MLA_FMT_INT8_SYM)         \
-  X(MLA_FMT_INT4_ASYM, MLA_FMT_INT4_SYM)         \
-  X(MLA_FMT_INT4_SYM, MLA_FMT_BF16)              \
-  X(MLA_FMT_INT4_SYM, MLA_FMT_INT8_SYM)          \
-  X(MLA_FMT_INT4_SYM, MLA_FMT_INT4_SYM)          \
-  X(MLA_FMT_INT8_G8, MLA_FMT_INT8_SYM)           \
-  X(MLA_FMT_INT8_G32, MLA_FMT_INT8_SYM)          \
-  X(MLA_FMT_INT8_G64, MLA_FMT_INT8_SYM)          \
-  X(MLA_FMT_INT8_TOKEN, MLA_FMT_INT8_SYM)        \
-  X(MLA_FMT_INT8_OUTLIER, MLA_FMT_BF16)          \
-  X(MLA_FMT_INT8_OUTLIER, MLA_FMT_INT8_SYM)
-
-mla_status launch_short_attention(const ChunkParams& p, int latent_fmt, int kpe_fmt, int R, cudaStream_t stream);
+// The attention over the short path's sequences, by latent format (one
+// translation unit each); MLA_ERR_UNSUPPORTED for another unit's formats.
+mla_status launch_short_bf16(const ChunkParams& p, int lf, int kf, int R, cudaStream_t stream);
+mla_status launch_short_int8(const ChunkParams& p, int lf, int kf, int R, cudaStream_t stream);
+mla_status launch_short_int8_blocks(const ChunkParams& p, int lf, int kf, int R, cudaStream_t stream);
+mla_status launch_short_int4(const ChunkParams& p, int lf, int kf, int R, cudaStream_t stream);
 
 }  // namespace mla

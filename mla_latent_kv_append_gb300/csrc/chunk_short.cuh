@@ -25,8 +25,8 @@
 // key buffer overlaps the conversion with both products; 16-row tiles of
 // quantized formats have room for two buffers.
 //
-// Warps: 0..7 dequantize, 8..11 softmax, 12 and 13 issue the S^T and the O^T
-// MMAs (apart, so that neither waits for the other's operands), 14 issues the
+// Warps: 0..15 dequantize, 16..19 softmax, 20 and 21 issue the S^T and the O^T
+// MMAs (apart, so that neither waits for the other's operands), 22 issues the
 // copies.
 //
 // Work split: all (row tile, key tile) units of the call, in order, are cut
@@ -37,6 +37,8 @@
 //
 // Rounding: keys, queries and P enter the MMAs as fp16 (2^-11 relative);
 // scores, sums, maxima and O stay fp32 until o_lat is written as fp16.
+#pragma once
+
 #include <math.h>
 
 #include "chunk.cuh"
@@ -48,7 +50,17 @@ namespace {
 
 using namespace tc;
 
-constexpr int kSThreads = 15 * 32;
+constexpr int kSThreads = 24 * 32;
+// Registers: 768 threads launch with 80 each (61,440); then the warps' roles
+// take their shares of that.
+constexpr int kRegsLaunch = 80;
+template <int R>
+struct Regs {
+  static constexpr int kConvert = R == 64 ? 64 : 72, kSoftmax = R == 64 ? 160 : 104, kIssue = R == 64 ? 64 : 88;
+  static_assert(512 * kConvert + 128 * kSoftmax + 128 * kIssue <= kSThreads * kRegsLaunch &&
+                    kSThreads * kRegsLaunch <= 65536 && kSThreads * (kRegsLaunch + 8) > 65536,
+                "the warpgroups' shares come out of the launch's registers");
+};
 constexpr int kKeyBlk = kKeyTile * 128;              // one 64-key x 64-channel fp16 block: 8 KB
 constexpr int kKeyBuf = kQBlocks * kKeyBlk;          // 72 KB
 constexpr float kSlack = 8.f;                        // the running maximum rises only past this (P <= 2^8 in fp16)
@@ -170,7 +182,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
     }
     for (int i = 0; i < kMaxSlots; ++i) {
       bar_init(bars + 8 * (bRaw + i), 1);
-      bar_init(bars + 8 * (bRawFree + i), 128);
+      bar_init(bars + 8 * (bRawFree + i), 256);
     }
     bar_init(bars + 8 * bQ, 1);
     bar_init(bars + 8 * bFinS, 1);
@@ -179,7 +191,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
     for (int i = 0; i < 4; ++i) bad[i] = 0;
     bar_init_fence();
   }
-  if (warp == 12) tmem_alloc(smem_u32(tmem_slot), kCols);
+  if (warp == 20) tmem_alloc(smem_u32(tmem_slot), kCols);
   fence_before();
   __syncthreads();
   fence_after();
@@ -194,12 +206,14 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
   const bool work = x < G;
   const int64_t lo = work ? U * x / G : 0, hi = work ? U * (x + 1) / G : 0;
   bool ok = true;
-  if (work && warp < 8) {
-    // ---- dequantize.  Warps 0..3: the tile's first block, 4..7: the second;
-    // warp w % 4 takes unit w % 4 of every 128-channel piece, warps 0 and 1 of
-    // each four the RoPE units too; lane = token.
-    const int half = warp >> 2, q = warp & 3, tok = 32 * half + lane;
-    const uint32_t n_tiles = (uint32_t)(hi - lo);
+  if (warp < 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(Regs<R>::kConvert));
+    // ---- dequantize.  Warps 0..7: the tile's first block, 8..15: the second.
+    // Of each eight, warp w takes unit w % 4 of pieces w / 4 and w / 4 + 2;
+    // warps 6 and 7 the RoPE units too; lane = token.
+    const int half = warp >> 3, q = warp & 3, s0 = (warp >> 2) & 1, tok = 32 * half + lane;
+    const bool rope = s0 == 1 && q >= 2;
+    const uint32_t n_tiles = (uint32_t)(hi - lo);      // none in a block without work
     for (uint32_t it = 0; it < n_tiles; ++it) {
       const uint32_t blk = 2 * it + half, slot = blk % NS, g = it & 1, kb = it % NB, ph = it / NB;
       if (!warp_wait(bars + 8 * (bRaw + slot), (blk / NS) & 1, p.wait_ns, abort)) {
@@ -208,50 +222,50 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
       }
       const uint8_t* raw = sm + SH::kRaw + slot * SH::kBlock;
       const int n_tok = slot_len[slot];
-      const bool live = lane < n_tok;
-      RawUnit<LF, false> r[4];
+      RawUnit<LF, false> r[2];
       RawUnit<KF, true> rk;
-      uint32_t outl_words[LF == MLA_FMT_INT8_OUTLIER ? 4 : 1][16];
-      if (live) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) load_unit<LF, false>(raw, p.L, lane, 4 * s + q, r[s]);
-        if (q < 2) load_unit<KF, true>(raw, p.L, lane, q, rk);
+      if (lane < n_tok) {
+        load_unit<LF, false>(raw, p.L, lane, 4 * s0 + q, r[0]);
+        load_unit<LF, false>(raw, p.L, lane, 4 * s0 + 8 + q, r[1]);
+        if (rope) load_unit<KF, true>(raw, p.L, lane, q - 2, rk);
+      } else {
+        zero_unit(r[0]);
+        zero_unit(r[1]);
+        zero_unit(rk);
       }
       bool fine = true;
-      if constexpr (LF == MLA_FMT_INT8_OUTLIER) {      // needs the block's other fields: converted before the slot goes
-        if (live) {
+      // the protected channels lie in the block: put in place before the slot goes
+      uint32_t hp[LF == MLA_FMT_INT8_OUTLIER ? 2 : 1][16];
+      if constexpr (LF == MLA_FMT_INT8_OUTLIER) {
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            fine &= convert_unit<LF, false>(r[s], outl_words[s]);
-            fine &= patch_outliers<LF>(raw, p.L, p.outl, lane, 4 * s + q, outl_words[s]);
-          }
+        for (int i = 0; i < 2; ++i) {
+          fine &= convert_unit<LF, false>(r[i], hp[i]);
+          if (lane < n_tok) fine &= patch_outliers<LF>(raw, p.L, p.outl, lane, 4 * s0 + 8 * i + q, hp[i]);
         }
       }
       bar_arrive(bars + 8 * (bRawFree + slot));
 #pragma unroll
-      for (int s = 0; s < 5; ++s) {
-        if (s == 4 && q >= 2) break;
+      for (int i = 0; i < 3; ++i) {
+        if (i == 2 && !rope) break;
+        const int s = i == 2 ? 4 : s0 + 2 * i;           // the piece
         uint32_t h[16];
-        if (!live) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) h[i] = 0u;
-        } else if (s == 4) {
+        if (i == 2) {
           fine &= convert_unit<KF, true>(rk, h);
         } else if constexpr (LF == MLA_FMT_INT8_OUTLIER) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) h[i] = outl_words[s & 3][i];
+          for (int j = 0; j < 16; ++j) h[j] = hp[i & 1][j];
         } else {
-          fine &= convert_unit<LF, false>(r[s & 3], h);
+          fine &= convert_unit<LF, false>(r[i & 1], h);
         }
         // the piece of the tile NB before is free
         if (it >= NB && !warp_wait(bars + 8 * (bFree + 5 * kb + s), (ph - 1) & 1, p.wait_ns, abort)) {
           ok = false;
           break;
         }
-        put_unit(h, sb + kb * kKeyBuf, tok, s < 4 ? 4 * s + q : kLatentUnits + q);
-        if (s == 4 || (s == 3 && q >= 2)) {
+        put_unit(h, sb + kb * kKeyBuf, tok, i < 2 ? 4 * s + q : kLatentUnits + q - 2);
+        if (i == (rope ? 2 : 1)) {
           // the last piece this warp writes: its tokens' flags go with it
-          if (half == 0 && q == 0 && lane == 0) tile_ok[g] = n_tok >= 0;
+          if (warp == 0 && lane == 0) tile_ok[g] = n_tok >= 0;
           if (!fine) atomicOr(bad + 2 * g + half, 1u << lane);
         }
         fence_async_smem();
@@ -263,18 +277,19 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
       set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
       *abort = 1;
     }
-  } else if (work && warp < 12) {
+  } else if (warp < 20) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(Regs<R>::kSoftmax));
     Walk wk;
     wk.n_seqs = __ldcg(&p.counts->s_seqs);
     // ---- softmax.  Thread (w, lane) holds keys 16 w + lane / 4 and + 8 of
     // the tile, rows 8 j + 2 (lane % 4) and the next (j < R / 8).
-    wk.start(p, lo, hi);
+    if (work) wk.start(p, lo, hi);
     const int w = warp & 3;
     const uint32_t tl = (uint32_t)(32 * w) << 16;
     constexpr int J = R / 8;
     float* red = reinterpret_cast<float*>(sm + SH::kRed);
     uint32_t it = 0;
-    while (ok && wk.next()) {
+    while (work && ok && wk.next()) {
       const int row0 = wk.item * R, rows = min(R, wk.s.n * p.H - row0);
       const int ctx = wk.s.len - wk.s.n;
       const int pos_min = ctx + row0 / p.H;          // the earliest row's position
@@ -314,21 +329,23 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
             }
           }
         }
-        float mx[2 * J];
-#pragma unroll
-        for (int i = 0; i < 2 * J; ++i) {
-          float a = fmaxf(v[4 * (i >> 1) + (i & 1)], v[4 * (i >> 1) + 2 + (i & 1)]);
-          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
-          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
-          mx[i] = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16));
+        // every warp has handed over P of the tile before, so its maxima have been read
+        if (it >= 1 && !warp_wait(bars + 8 * (bP + (g ^ 1)), ((it - 1) >> 1) & 1, p.wait_ns, abort)) {
+          ok = false;
+          break;
         }
-        if (lane < 4) {
 #pragma unroll
-          for (int j = 0; j < J; ++j)
-            *reinterpret_cast<float2*>(red + w * R + 8 * j + 2 * lane) = make_float2(mx[2 * j], mx[2 * j + 1]);
+        for (int j = 0; j < J; ++j) {
+          float a = fmaxf(v[4 * j], v[4 * j + 2]), b = fmaxf(v[4 * j + 1], v[4 * j + 3]);
+#pragma unroll
+          for (int o = 4; o <= 16; o <<= 1) {
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+          }
+          if (lane < 4) *reinterpret_cast<float2*>(red + w * R + 8 * j + 2 * lane) = make_float2(a, b);
         }
         asm volatile("bar.sync 1, 128;\n" ::: "memory");
-        if ((bad_lo | bad_hi) && threadIdx.x == 8 * 32) bad[2 * g] = bad[2 * g + 1] = 0;    // all four warps have read them
+        if ((bad_lo | bad_hi) && threadIdx.x == 16 * 32) bad[2 * g] = bad[2 * g + 1] = 0;    // all four warps have read them
         bool any = false;
         float alpha[2 * J];
 #pragma unroll
@@ -344,7 +361,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
           for (int e = 0; e < 2; ++e) {
             const int i = 2 * j + e;
             const float top = e ? a.y : a.x;
-            const bool raise = top > m[i] + kSlack || (m[i] == -INFINITY && top > -INFINITY);
+            const bool raise = top > m[i] + kSlack;      // from -inf: the first key seen
             alpha[i] = raise ? ex2(m[i] - top) : 1.f;
             if (raise) m[i] = top;
             any |= raise;
@@ -378,24 +395,24 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
             }
           }
         }
-        uint32_t h[2 * J];
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          // a row that has seen nothing yet keeps m = -inf: its weights are 0
-          const float m0 = m[2 * j] == -INFINITY ? 0.f : m[2 * j], m1 = m[2 * j + 1] == -INFINITY ? 0.f : m[2 * j + 1];
-          const float p0 = ex2(v[4 * j] - m0), p1 = ex2(v[4 * j + 1] - m1);
-          const float p2 = ex2(v[4 * j + 2] - m0), p3 = ex2(v[4 * j + 3] - m1);
-          l[2 * j] += p0 + p2;
-          l[2 * j + 1] += p1 + p3;
-          h[2 * j] = half2_bits(p0, p1);
-          h[2 * j + 1] = half2_bits(p2, p3);
-        }
         // P^T as rows of 64 keys: the fragment transposed
 #pragma unroll
         for (int j = 0; j < J; j += 2) {
+          uint32_t h[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int i = j + e;
+            // a row that has seen nothing yet keeps m = -inf: its weights are 0
+            const float m0 = m[2 * i] == -INFINITY ? 0.f : m[2 * i], m1 = m[2 * i + 1] == -INFINITY ? 0.f : m[2 * i + 1];
+            const float p0 = ex2(v[4 * i] - m0), p1 = ex2(v[4 * i + 1] - m1);
+            const float p2 = ex2(v[4 * i + 2] - m0), p3 = ex2(v[4 * i + 3] - m1);
+            l[2 * i] += p0 + p2;
+            l[2 * i + 1] += p1 + p3;
+            h[2 * e] = half2_bits(p0, p1);
+            h[2 * e + 1] = half2_bits(p2, p3);
+          }
           const int mat = lane >> 3, rr = 8 * (j + (mat >> 1)) + (lane & 7), oct = 2 * w + (mat & 1);
-          stmatrix_x4_trans(sb + SH::kP + rr * 128 + ((oct ^ (rr & 7)) << 4), h[2 * j], h[2 * j + 1], h[2 * j + 2],
-                            h[2 * j + 3]);
+          stmatrix_x4_trans(sb + SH::kP + rr * 128 + ((oct ^ (rr & 7)) << 4), h[0], h[1], h[2], h[3]);
         }
         fence_async_smem();
         fence_before();
@@ -487,144 +504,151 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
       set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
       *abort = 1;
     }
-  } else if (work && warp == 12) {
-    // ---- one thread: the query tiles' copies and the S^T MMAs
-    Walk wk;
-    wk.n_seqs = __ldcg(&p.counts->s_seqs);
-    wk.start(p, lo, hi);
-    if (elect_one()) {
-      constexpr uint32_t kId = f16_idesc(64, R, false, false);
-      constexpr int kQBytes = kQBlocks * R * 128;
-      const uint64_t d_q = sw128_desc(sb + SH::kQ, 16, 1024), d_k = sw128_desc(sb, 16, 1024);
-      uint32_t it = 0, seg = 0;
-      while (ok && wk.next()) {
-        // the query tile: its readers, the S^T MMAs of the segment before, are done
-        if (seg > 0 && !bar_wait(bars + 8 * (bS + ((it - 1) & 1)), ((it - 1) >> 1) & 1, p.wait_ns, abort)) {
-          ok = false;
-          break;
-        }
-        bar_expect(bars + 8 * bQ, kQBytes);
-        bulk_copy(sb + SH::kQ, p.q_tiles + (int64_t)(wk.s.item0 + wk.item) * kQBytes, kQBytes, bars + 8 * bQ);
-        ++seg;
-        if (!bar_wait(bars + 8 * bQ, (seg - 1) & 1, p.wait_ns, abort)) {
-          ok = false;
-          break;
-        }
-        for (int t = wk.t0; t < wk.t1 && ok; ++t, ++it) {
-          const uint32_t g = it & 1, kb = it % NB, ph = (it / NB) & 1;
-          // the softmax has read this S^T buffer's last tile
-          if (it >= 2 && !bar_wait(bars + 8 * (bP + g), ((it - 2) >> 1) & 1, p.wait_ns, abort)) {
+  } else {
+    if constexpr (Regs<R>::kIssue > kRegsLaunch) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(Regs<R>::kIssue));
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(Regs<R>::kIssue));
+    }
+    if (work && warp == 20) {
+      // ---- one thread: the query tiles' copies and the S^T MMAs
+      Walk wk;
+      wk.n_seqs = __ldcg(&p.counts->s_seqs);
+      wk.start(p, lo, hi);
+      if (elect_one()) {
+        constexpr uint32_t kId = f16_idesc(64, R, false, false);
+        constexpr int kQBytes = kQBlocks * R * 128;
+        const uint64_t d_q = sw128_desc(sb + SH::kQ, 16, 1024), d_k = sw128_desc(sb, 16, 1024);
+        uint32_t it = 0, seg = 0;
+        while (ok && wk.next()) {
+          // the query tile: its readers, the S^T MMAs of the segment before, are done
+          if (seg > 0 && !bar_wait(bars + 8 * (bS + ((it - 1) & 1)), ((it - 1) >> 1) & 1, p.wait_ns, abort)) {
             ok = false;
             break;
           }
-          const uint64_t a = d_k + (uint64_t)(kb * (kKeyBuf >> 4));
-          const uint32_t d = t_s + g * R;
-#pragma unroll
-          for (int s = 0; s < 5; ++s) {
-            if (!bar_wait(bars + 8 * (bWritten + 5 * kb + s), ph, p.wait_ns, abort)) {
+          bar_expect(bars + 8 * bQ, kQBytes);
+          bulk_copy(sb + SH::kQ, p.q_tiles + (int64_t)(wk.s.item0 + wk.item) * kQBytes, kQBytes, bars + 8 * bQ);
+          ++seg;
+          if (!bar_wait(bars + 8 * bQ, (seg - 1) & 1, p.wait_ns, abort)) {
+            ok = false;
+            break;
+          }
+          for (int t = wk.t0; t < wk.t1 && ok; ++t, ++it) {
+            const uint32_t g = it & 1, kb = it % NB, ph = (it / NB) & 1;
+            // the softmax has read this S^T buffer's last tile
+            if (it >= 2 && !bar_wait(bars + 8 * (bP + g), ((it - 2) >> 1) & 1, p.wait_ns, abort)) {
+              ok = false;
+              break;
+            }
+            const uint64_t a = d_k + (uint64_t)(kb * (kKeyBuf >> 4));
+            const uint32_t d = t_s + g * R;
+  #pragma unroll
+            for (int s = 0; s < 5; ++s) {
+              if (!bar_wait(bars + 8 * (bWritten + 5 * kb + s), ph, p.wait_ns, abort)) {
+                ok = false;
+                break;
+              }
+              fence_after();
+              umma4<2, 2>(d, a + (2 * s * kKeyBlk >> 4), d_q + (2 * s * R * 128 >> 4), kId, s != 0);
+              if (s < 4) umma4<2, 2>(d, a + ((2 * s + 1) * kKeyBlk >> 4), d_q + ((2 * s + 1) * R * 128 >> 4), kId, 1u);
+            }
+            if (!ok) break;
+            umma_commit(bars + 8 * (bFree + 5 * kb + 4));     // the RoPE block is read here only
+            umma_commit(bars + 8 * (bS + g));
+          }
+        }
+        if (!ok) {
+          set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
+          *abort = 1;
+        }
+        if (seg > 0) drain_wait(bars + 8 * bQ, (seg - 1) & 1);     // no copy is in flight when the block ends
+        umma_commit(bars + 8 * bFinS);
+        drain_wait(bars + 8 * bFinS, 0);
+      }
+      __syncwarp();
+    } else if (work && warp == 21) {
+      // ---- one thread: the O^T MMAs
+      Walk wk;
+      wk.n_seqs = __ldcg(&p.counts->s_seqs);
+      wk.start(p, lo, hi);
+      if (elect_one()) {
+        constexpr uint32_t kId = f16_idesc(128, R, true, false);
+        const uint64_t d_p = sw128_desc(sb + SH::kP, 16, 1024), d_v = sw128_desc(sb, kKeyBlk, 1024);
+        uint32_t it = 0;
+        while (ok && wk.next()) {
+          for (int t = wk.t0; t < wk.t1; ++t, ++it) {
+            const uint32_t g = it & 1, kb = it % NB;
+            if (!bar_wait(bars + 8 * (bP + g), (it >> 1) & 1, p.wait_ns, abort)) {
               ok = false;
               break;
             }
             fence_after();
-            umma4<2, 2>(d, a + (2 * s * kKeyBlk >> 4), d_q + (2 * s * R * 128 >> 4), kId, s != 0);
-            if (s < 4) umma4<2, 2>(d, a + ((2 * s + 1) * kKeyBlk >> 4), d_q + ((2 * s + 1) * R * 128 >> 4), kId, 1u);
+            const uint64_t a = d_v + (uint64_t)(kb * (kKeyBuf >> 4));
+  #pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              umma4<(2048 >> 4), 2>(tbase + s * R, a + (2 * s * kKeyBlk >> 4), d_p, kId, t > wk.t0);
+              umma_commit(bars + 8 * (bFree + 5 * kb + s));
+            }
           }
-          if (!ok) break;
-          umma_commit(bars + 8 * (bFree + 5 * kb + 4));     // the RoPE block is read here only
-          umma_commit(bars + 8 * (bS + g));
         }
+        if (!ok) {
+          set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
+          *abort = 1;
+        }
+        umma_commit(bars + 8 * bFinO);
+        drain_wait(bars + 8 * bFinO, 0);
       }
-      if (!ok) {
-        set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
-        *abort = 1;
-      }
-      if (seg > 0) drain_wait(bars + 8 * bQ, (seg - 1) & 1);     // no copy is in flight when the block ends
-      umma_commit(bars + 8 * bFinS);
-      drain_wait(bars + 8 * bFinS, 0);
-    }
-    __syncwarp();
-  } else if (work && warp == 13) {
-    // ---- one thread: the O^T MMAs
-    Walk wk;
-    wk.n_seqs = __ldcg(&p.counts->s_seqs);
-    wk.start(p, lo, hi);
-    if (elect_one()) {
-      constexpr uint32_t kId = f16_idesc(128, R, true, false);
-      const uint64_t d_p = sw128_desc(sb + SH::kP, 16, 1024), d_v = sw128_desc(sb, kKeyBlk, 1024);
-      uint32_t it = 0;
+      __syncwarp();
+    } else if (work && warp == 22) {
+      // ---- the cache's blocks into the raw slots.  The lanes fetch 32
+      // page ids of the segment at a time, lane 0 issues.
+      Walk wk;
+      wk.n_seqs = __ldcg(&p.counts->s_seqs);
+      wk.start(p, lo, hi);
+      uint32_t blk = 0;
       while (ok && wk.next()) {
-        for (int t = wk.t0; t < wk.t1; ++t, ++it) {
-          const uint32_t g = it & 1, kb = it % NB;
-          if (!bar_wait(bars + 8 * (bP + g), (it >> 1) & 1, p.wait_ns, abort)) {
-            ok = false;
-            break;
-          }
-          fence_after();
-          const uint64_t a = d_v + (uint64_t)(kb * (kKeyBuf >> 4));
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            umma4<(2048 >> 4), 2>(tbase + s * R, a + (2 * s * kKeyBlk >> 4), d_p, kId, t > wk.t0);
-            umma_commit(bars + 8 * (bFree + 5 * kb + s));
+        const int32_t* pages = p.block_table + (int64_t)wk.s.b * p.max_pages;
+        for (int t0 = wk.t0; t0 < wk.t1 && ok; t0 += 32) {
+          const int mine = t0 + lane < wk.t1 ? __ldcg(pages + t0 + lane) : 0;
+          for (int t = t0; t < min(wk.t1, t0 + 32) && ok; ++t) {
+            const int page = __shfl_sync(0xffffffffu, mine, t - t0);
+            const bool page_ok = page >= 0 && page < p.num_pages;
+            if (!page_ok && lane == 0) set_err(p.dev_err, MLA_DEVERR_PAGE);
+  #pragma unroll
+            for (int half = 0; half < 2; ++half, ++blk) {
+              const uint32_t slot = blk % NS;
+              if (blk >= NS && !warp_wait(bars + 8 * (bRawFree + slot), ((blk / NS) - 1) & 1, p.wait_ns, abort)) {
+                ok = false;
+                break;
+              }
+              if (lane == 0) {
+                const int n_tok = min(32, max(0, wk.s.len - t * kKeyTile - 32 * half));
+                slot_len[slot] = page_ok ? n_tok : -1;
+                if (page_ok && n_tok > 0) {
+                  bar_expect(bars + 8 * (bRaw + slot), SH::kBlock);
+                  bulk_copy(sb + SH::kRaw + slot * SH::kBlock, p.pool + (int64_t)page * p.L.page_bytes + half * p.L.block_bytes,
+                            SH::kBlock, bars + 8 * (bRaw + slot));
+                } else {
+                  bar_arrive(bars + 8 * (bRaw + slot));
+                }
+              }
+              __syncwarp();
+            }
           }
         }
       }
       if (!ok) {
-        set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
+        if (lane == 0) set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
         *abort = 1;
       }
-      umma_commit(bars + 8 * bFinO);
-      drain_wait(bars + 8 * bFinO, 0);
+      // the copies in flight land before the block ends
+      for (uint32_t s = 0; s < NS; ++s)
+        if (blk > s) drain_wait(bars + 8 * (bRaw + s), ((blk - 1 - s) / NS) & 1);
     }
-    __syncwarp();
-  } else if (work) {
-    // ---- warp 14: the cache's blocks into the raw slots.  The lanes fetch 32
-    // page ids of the segment at a time, lane 0 issues.
-    Walk wk;
-    wk.n_seqs = __ldcg(&p.counts->s_seqs);
-    wk.start(p, lo, hi);
-    uint32_t blk = 0;
-    while (ok && wk.next()) {
-      const int32_t* pages = p.block_table + (int64_t)wk.s.b * p.max_pages;
-      for (int t0 = wk.t0; t0 < wk.t1 && ok; t0 += 32) {
-        const int mine = t0 + lane < wk.t1 ? __ldcg(pages + t0 + lane) : 0;
-        for (int t = t0; t < min(wk.t1, t0 + 32) && ok; ++t) {
-          const int page = __shfl_sync(0xffffffffu, mine, t - t0);
-          const bool page_ok = page >= 0 && page < p.num_pages;
-          if (!page_ok && lane == 0) set_err(p.dev_err, MLA_DEVERR_PAGE);
-#pragma unroll
-          for (int half = 0; half < 2; ++half, ++blk) {
-            const uint32_t slot = blk % NS;
-            if (blk >= NS && !warp_wait(bars + 8 * (bRawFree + slot), ((blk / NS) - 1) & 1, p.wait_ns, abort)) {
-              ok = false;
-              break;
-            }
-            if (lane == 0) {
-              const int n_tok = min(32, max(0, wk.s.len - t * kKeyTile - 32 * half));
-              slot_len[slot] = page_ok ? n_tok : -1;
-              if (page_ok && n_tok > 0) {
-                bar_expect(bars + 8 * (bRaw + slot), SH::kBlock);
-                bulk_copy(sb + SH::kRaw + slot * SH::kBlock, p.pool + (int64_t)page * p.L.page_bytes + half * p.L.block_bytes,
-                          SH::kBlock, bars + 8 * (bRaw + slot));
-              } else {
-                bar_arrive(bars + 8 * (bRaw + slot));
-              }
-            }
-            __syncwarp();
-          }
-        }
-      }
-    }
-    if (!ok) {
-      if (lane == 0) set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
-      *abort = 1;
-    }
-    // the copies in flight land before the block ends
-    for (uint32_t s = 0; s < NS; ++s)
-      if (blk > s) drain_wait(bars + 8 * (bRaw + s), ((blk - 1 - s) / NS) & 1);
   }
   fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 20) {
     fence_after();
     tmem_free(tbase, kCols);
   }
@@ -691,13 +715,5 @@ mla_status launch_fmt(const ChunkParams& p, int R, cudaStream_t stream) {
 }
 
 }  // namespace
-
-mla_status launch_short_attention(const ChunkParams& p, int lf, int kf, int R, cudaStream_t stream) {
-#define MLA_CHUNK_CASE(A, K) \
-  if (lf == A && kf == K) return launch_fmt<A, K>(p, R, stream);
-  MLA_CHUNK_FORMATS(MLA_CHUNK_CASE)
-#undef MLA_CHUNK_CASE
-  return MLA_ERR_UNSUPPORTED;
-}
 
 }  // namespace mla

@@ -1,0 +1,13 @@
+// The short path of mla_chunk_attention for bf16 latents (see chunk_short.cuh).
+#include "chunk_short.cuh"
+
+namespace mla {
+
+mla_status launch_short_bf16(const ChunkParams& p, int lf, int kf, int R, cudaStream_t stream) {
+  if (lf == MLA_FMT_BF16 && kf == MLA_FMT_BF16) return launch_fmt<MLA_FMT_BF16, MLA_FMT_BF16>(p, R, stream);
+  if (lf == MLA_FMT_BF16 && kf == MLA_FMT_INT8_SYM) return launch_fmt<MLA_FMT_BF16, MLA_FMT_INT8_SYM>(p, R, stream);
+  if (lf == MLA_FMT_BF16 && kf == MLA_FMT_INT4_SYM) return launch_fmt<MLA_FMT_BF16, MLA_FMT_INT4_SYM>(p, R, stream);
+  return MLA_ERR_UNSUPPORTED;
+}
+
+}  // namespace mla

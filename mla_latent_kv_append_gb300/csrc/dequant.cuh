@@ -74,11 +74,12 @@ __device__ __forceinline__ void load_unit(const uint8_t* blk, const PageLayout& 
 constexpr float kHalfMax = 65504.f;
 
 // A scale rounded to 15 significant bits (2^-15 relative, a sixteenth of the
-// fp16 rounding that follows).  With it the products below are exact: a code
-// q sits in a float's mantissa as f = 1 + q 2^-k, and
+// fp16 rounding that follows).  A code q sits in a float's mantissa as f = 1 +
+// q 2^-k, and
 //   fma(f, 2^k s, -(2^k + zero) s) = (q - zero) s
-// is rounded once, since (2^k + zero) s fits 24 bits; one byte select (or
-// shift and mask) and one FMA per value, no conversion instructions.
+// is then rounded once: (2^k + zero) s fits 24 bits (for 4-bit codes with k =
+// 11 it is off by up to 2^-13 s, a 2^-13th of the codes' step).  One byte
+// select or mask and one FMA per value, no conversion instructions.
 __device__ __forceinline__ float short_scale(float s) {
   return __uint_as_float((__float_as_uint(s) + 0x100u) & 0xFFFFFE00u);
 }
@@ -87,8 +88,20 @@ __device__ __forceinline__ uint32_t half2_word(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The unit's 32 channels as fp16 pairs, h[i] = channels (2i, 2i + 1); false
-// (and h = 0) if one of them is not finite in fp16.
+// A unit that reads as 0.
+template <int FMT, bool KPE>
+__device__ __forceinline__ void zero_unit(RawUnit<FMT, KPE>& r) {
+  using S = UnitShape<FMT, KPE>;
+#pragma unroll
+  for (int i = 0; i < S::kWords; ++i) r.w[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int i = 0; i < (S::kScales > 0 ? S::kScales : 1); ++i) r.s[i] = 0.f;
+#pragma unroll
+  for (int i = 0; i < (S::kZeros ? S::kScales : 1); ++i) r.z[i] = 0.f;
+}
+
+// The unit's 32 channels as fp16 pairs, h[i] = channels (2i, 2i + 1); false if
+// one of them is not finite in fp16 (its group, or the unit, then reads as 0).
 template <int FMT, bool KPE>
 __device__ __forceinline__ bool convert_unit(const RawUnit<FMT, KPE>& r, uint32_t* h) {
   using S = UnitShape<FMT, KPE>;
@@ -106,33 +119,46 @@ __device__ __forceinline__ bool convert_unit(const RawUnit<FMT, KPE>& r, uint32_
       }
     }
     fine = !(__hisnan(__low2half(acc)) || __hisnan(__high2half(acc)));
+    if (!fine) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) h[i] = 0u;
+    }
   } else if constexpr (S::kInt4) {
-    float m[S::kScales], c[S::kScales];
+    // k = 11 and k = 7: a nibble at bits 12..15 or 16..19, so one shift serves two
+    float m[2][S::kScales], c[2][S::kScales];
 #pragma unroll
     for (int g = 0; g < S::kScales; ++g) {
       const float zero = S::kZeros ? r.z[S::kZeros ? g : 0] : 8.f;
-      fine &= fabsf(r.s[g]) * (S::kZeros ? fabsf(zero - 7.5f) + 7.5f : 7.f) <= kHalfMax;      // false for NaN
-      const float s = short_scale(r.s[g]);
-      m[g] = 128.f * s;
-      c[g] = -(128.f + zero) * s;
+      const bool ok = fabsf(r.s[g]) * (S::kZeros ? fabsf(zero - 7.5f) + 7.5f : 7.f) <= kHalfMax;      // false for NaN
+      fine &= ok;
+      const float s = ok ? short_scale(r.s[g]) : 0.f, z = ok ? zero : 0.f;
+      m[0][g] = 2048.f * s;
+      c[0][g] = -(2048.f + z) * s;
+      m[1][g] = 128.f * s;
+      c[1][g] = -(128.f + z) * s;
     }
     const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 4; ++j) {
+      float v[8];                        // nibble k's value
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        // nibbles k and k + 4 of a word are adjacent channels
-        const int ch = int4_nibble_channel(j, k), g = ch / S::kGroup;
-        const uint32_t lo = ((w[j] << (16 - 4 * k)) & 0x000F0000u) | 0x3F800000u;
-        const uint32_t hi = ((w[j] >> (4 * k)) & 0x000F0000u) | 0x3F800000u;
-        h[ch / 2] = half2_word(fmaf(__uint_as_float(lo), m[g], c[g]), fmaf(__uint_as_float(hi), m[g], c[g]));
+      for (int k = 0; k < 8; k += 2) {
+        const uint32_t t = k == 0 ? w[j] << 12 : (k == 2 ? w[j] << 4 : (k == 4 ? w[j] >> 4 : w[j] >> 12));
+        const int g = int4_nibble_channel(j, k) / S::kGroup;       // nibble k + 1 is in the same group
+        v[k] = fmaf(__uint_as_float((t & 0x0000F000u) | 0x3F800000u), m[0][g], c[0][g]);
+        v[k + 1] = fmaf(__uint_as_float((t & 0x000F0000u) | 0x3F800000u), m[1][g], c[1][g]);
       }
+      // nibbles k and k + 4 are adjacent channels
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[int4_nibble_channel(j, k) / 2] = half2_word(v[k], v[k + 4]);
+    }
   } else {
     float m[S::kScales], c[S::kScales];
 #pragma unroll
     for (int g = 0; g < S::kScales; ++g) {
-      fine &= fabsf(r.s[g]) * 127.f <= kHalfMax;
-      const float s = short_scale(r.s[g]);
+      const bool ok = fabsf(r.s[g]) * 127.f <= kHalfMax;
+      fine &= ok;
+      const float s = ok ? short_scale(r.s[g]) : 0.f;
       m[g] = 32768.f * s;
       c[g] = -32896.f * s;               // codes are biased by 128 below
     }
@@ -152,10 +178,6 @@ __device__ __forceinline__ bool convert_unit(const RawUnit<FMT, KPE>& r, uint32_
           h[ch / 2] = half2_word(fmaf(a, m[g], c[g]), fmaf(b, m[g], c[g]));
         }
     }
-  }
-  if (!fine) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) h[i] = 0u;
   }
   return fine;
 }

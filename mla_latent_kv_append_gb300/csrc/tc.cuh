@@ -37,7 +37,7 @@ __device__ __forceinline__ uint64_t now_ns() {
 }
 // Waits for the phase of `bar` with this parity.  Gives up (false) once
 // limit_ns have passed or another role of the block has given up (*abort).
-static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* abort) {
+__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* abort) {
   const uint64_t t0 = now_ns();
   for (;;) {
     if (bar_test(bar, parity)) return true;
@@ -53,7 +53,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
 }
 // The final waits for the block's own copies and MMAs: bounded, but not ended
 // by *abort.
-static __device__ __noinline__ bool drain_wait(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = now_ns();
   while (!bar_test(bar, parity))
     if (now_ns() - t0 >= 2000000000ull) return false;
