@@ -222,47 +222,34 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
       }
       const uint8_t* raw = sm + SH::kRaw + slot * SH::kBlock;
       const int n_tok = slot_len[slot];
-      RawUnit<LF, false> r[2];
+      // both units are converted before the wait for room in the key buffer
+      uint32_t h[2][16];
       RawUnit<KF, true> rk;
-      if (lane < n_tok) {
-        load_unit<LF, false>(raw, p.L, lane, 4 * s0 + q, r[0]);
-        load_unit<LF, false>(raw, p.L, lane, 4 * s0 + 8 + q, r[1]);
-        if (rope) load_unit<KF, true>(raw, p.L, lane, q - 2, rk);
-      } else {
-        zero_unit(r[0]);
-        zero_unit(r[1]);
-        zero_unit(rk);
-      }
       bool fine = true;
-      // the protected channels lie in the block: put in place before the slot goes
-      uint32_t hp[LF == MLA_FMT_INT8_OUTLIER ? 2 : 1][16];
-      if constexpr (LF == MLA_FMT_INT8_OUTLIER) {
+      if (rope) {
+        if (lane < n_tok) load_unit<KF, true>(raw, p.L, lane, q - 2, rk);
+        else zero_unit(rk);
+      }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          fine &= convert_unit<LF, false>(r[i], hp[i]);
-          if (lane < n_tok) fine &= patch_outliers<LF>(raw, p.L, p.outl, lane, 4 * s0 + 8 * i + q, hp[i]);
-        }
+      for (int i = 0; i < 2; ++i) {
+        RawUnit<LF, false> r;
+        if (lane < n_tok) load_unit<LF, false>(raw, p.L, lane, 4 * s0 + 8 * i + q, r);
+        else zero_unit(r);
+        fine &= convert_unit<LF, false>(r, h[i]);
+        if (lane < n_tok) fine &= patch_outliers<LF>(raw, p.L, p.outl, lane, 4 * s0 + 8 * i + q, h[i]);
       }
       bar_arrive(bars + 8 * (bRawFree + slot));
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
         if (i == 2 && !rope) break;
         const int s = i == 2 ? 4 : s0 + 2 * i;           // the piece
-        uint32_t h[16];
-        if (i == 2) {
-          fine &= convert_unit<KF, true>(rk, h);
-        } else if constexpr (LF == MLA_FMT_INT8_OUTLIER) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) h[j] = hp[i & 1][j];
-        } else {
-          fine &= convert_unit<LF, false>(r[i & 1], h);
-        }
+        if (i == 2) fine &= convert_unit<KF, true>(rk, h[0]);
         // the piece of the tile NB before is free
         if (it >= NB && !warp_wait(bars + 8 * (bFree + 5 * kb + s), (ph - 1) & 1, p.wait_ns, abort)) {
           ok = false;
           break;
         }
-        put_unit(h, sb + kb * kKeyBuf, tok, i < 2 ? 4 * s + q : kLatentUnits + q - 2);
+        put_unit(h[i & 1], sb + kb * kKeyBuf, tok, i < 2 ? 4 * s + q : kLatentUnits + q - 2);
         if (i == (rope ? 2 : 1)) {
           // the last piece this warp writes: its tokens' flags go with it
           if (warp == 0 && lane == 0) tile_ok[g] = n_tok >= 0;
@@ -329,45 +316,58 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
             }
           }
         }
-        // every warp has handed over P of the tile before, so its maxima have been read
-        if (it >= 1 && !warp_wait(bars + 8 * (bP + (g ^ 1)), ((it - 1) >> 1) & 1, p.wait_ns, abort)) {
-          ok = false;
-          break;
-        }
+        if (rows < R) {                    // the padding's query rows hold anything: their scores count as 0
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          float a = fmaxf(v[4 * j], v[4 * j + 2]), b = fmaxf(v[4 * j + 1], v[4 * j + 3]);
-#pragma unroll
-          for (int o = 4; o <= 16; o <<= 1) {
-            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
-          }
-          if (lane < 4) *reinterpret_cast<float2*>(red + w * R + 8 * j + 2 * lane) = make_float2(a, b);
+          for (int i = 0; i < 2 * J; ++i)
+            if (8 * (i >> 1) + 2 * (lane & 3) + (i & 1) >= rows) v[4 * (i >> 1) + (i & 1)] = v[4 * (i >> 1) + 2 + (i & 1)] = 0.f;
         }
-        asm volatile("bar.sync 1, 128;\n" ::: "memory");
+        // Does a score pass its row's running maximum by more than the slack?
+        // One vote of the four warps; the maxima themselves are needed only
+        // then (the first tile of a segment, and seldom after it).
+        float over = -INFINITY;            // NaN from a NaN score or a row that has seen nothing yet
+#pragma unroll
+        for (int i = 0; i < 2 * J; ++i)
+          over = max_nan(over, max_nan(v[4 * (i >> 1) + (i & 1)] - m[i], v[4 * (i >> 1) + 2 + (i & 1)] - m[i]));
+        uint32_t any;
+        asm volatile(
+            "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n"
+            " selp.u32 %0, 1, 0, q;\n}\n"
+            : "=r"(any)
+            : "r"((uint32_t)!(over <= kSlack))
+            : "memory");
         if ((bad_lo | bad_hi) && threadIdx.x == 16 * 32) bad[2 * g] = bad[2 * g + 1] = 0;    // all four warps have read them
-        bool any = false;
         float alpha[2 * J];
+        if (any) {
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          float2 a = make_float2(-INFINITY, -INFINITY);
+          for (int j = 0; j < J; ++j) {
+            float a = fmaxf(v[4 * j], v[4 * j + 2]), b = fmaxf(v[4 * j + 1], v[4 * j + 3]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float2 b = *reinterpret_cast<const float2*>(red + q * R + 8 * j + 2 * (lane & 3));
-            a.x = fmaxf(a.x, b.x);
-            a.y = fmaxf(a.y, b.y);
+            for (int o = 4; o <= 16; o <<= 1) {
+              a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+              b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+            }
+            if (lane < 4) *reinterpret_cast<float2*>(red + w * R + 8 * j + 2 * lane) = make_float2(a, b);
           }
+          asm volatile("bar.sync 1, 128;\n" ::: "memory");
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int i = 2 * j + e;
-            const float top = e ? a.y : a.x;
-            const bool raise = top > m[i] + kSlack;      // from -inf: the first key seen
-            alpha[i] = raise ? ex2(m[i] - top) : 1.f;
-            if (raise) m[i] = top;
-            any |= raise;
+          for (int j = 0; j < J; ++j) {
+            float2 a = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float2 b = *reinterpret_cast<const float2*>(red + q * R + 8 * j + 2 * (lane & 3));
+              a.x = fmaxf(a.x, b.x);
+              a.y = fmaxf(a.y, b.y);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int i = 2 * j + e;
+              const float top = e ? a.y : a.x;
+              const bool raise = top > m[i] + kSlack;      // from -inf: the first key seen
+              alpha[i] = raise ? ex2(m[i] - top) : 1.f;
+              if (raise) m[i] = top;
+            }
           }
         }
-        any = __any_sync(0xffffffffu, any);
         // the O^T of the tile before is complete: P is free, and O^T may be rescaled
         if (it >= 1 && !warp_wait(bars + 8 * (bFree + 5 * ((it - 1) % NB) + 3), ((it - 1) / NB) & 1, p.wait_ns, abort)) {
           ok = false;
