@@ -58,7 +58,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x;
-  for (int i = tid; i < p.grid; i += kPlanThreads) p.splits[i].rows = 0;
+  const bool long_path = p.l_seqs != nullptr;
+  for (int i = tid; i < p.grid; i += kPlanThreads) {
+    p.splits[i].rows = 0;
+    if (long_path) p.l_splits[i].rows = 0;
+  }
   for (int i = tid; i < kMaxBatch / 32; i += kPlanThreads) zero_mask[i] = 0;
   const int per = (p.B + kPlanThreads - 1) / kPlanThreads, b0 = tid * per;
   int q0[kPlanPer], n[kPlanPer], len[kPlanPer];
@@ -77,20 +81,28 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
   }
   // rows out of order could overlap: then nobody is served
   const bool ordered = !__syncthreads_or(!order);
-  int64_t mine = 0, units = 0;
+  int64_t mine = 0, units = 0, l_mine = 0;
   bool bad = !ordered, zero = false;
   int items[kPlanPer], tiles[kPlanPer];
+  bool is_long[kPlanPer];
 #pragma unroll
   for (int k = 0; k < kPlanPer; ++k) {
     const int b = b0 + k;
     items[k] = tiles[k] = 0;
+    is_long[k] = false;
     if (!(k < per && b < p.B) || (ordered && n[k] == 0)) continue;
     const bool fits = ordered && n[k] <= p.max_new && len[k] >= 0 && (len[k] == 0 || len[k] >= n[k]) &&
-                      (int64_t)len[k] <= (int64_t)p.max_pages * kPage;
+                      (int64_t)len[k] <= (int64_t)p.max_pages * kPage && (n[k] <= kChunkShort || len[k] == 0 || long_path);
     if (!fits || len[k] == 0) {
       bad |= !fits;
       zero = true;
       atomicOr(zero_mask + (b >> 5), 1u << (b & 31));
+      continue;
+    }
+    if (n[k] > kChunkShort) {
+      is_long[k] = true;
+      tiles[k] = (len[k] + kLongKeys - 1) / kLongKeys;
+      l_mine += ((int64_t)1 << 48) + tiles[k];
       continue;
     }
     items[k] = (n[k] * p.H + R - 1) / R;
@@ -119,15 +131,63 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
     at += ((int64_t)1 << 48) + ((int64_t)items[k] << 20) + n[k];
     unit += (int64_t)items[k] * tiles[k];
   }
-  if (tid == 0) {
-    ChunkCounts c;
-    c.s_seqs = (int)(total >> 48);
-    c.s_items = (int)((total >> 20) & 0xFFFFFFF);
-    c.s_toks = (int)(total & 0xFFFFF);
-    c.pad0 = 0;
-    c.s_units = total_units;
-    *p.counts = c;
+  ChunkCounts c = {};
+  c.s_seqs = (int)(total >> 48);
+  c.s_items = (int)((total >> 20) & 0xFFFFFFF);
+  c.s_toks = (int)(total & 0xFFFFF);
+  c.s_units = total_units;
+  if (long_path) {
+    // key tiles in the order of the batch, as far as the caller's bound goes:
+    // with the refused ones' counted, nobody behind the first refusal fits
+    int64_t l_total, l_units = 0;
+    int64_t l_at = scan(l_mine, red, &l_total);
+    const int64_t room = p.kv_tokens / kLongKeys;
+    int64_t kv = l_at & 0xFFFFFFFFFFFF;
+    int per_head[kPlanPer];
+    int served = 0, served_tiles = 0;
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k) {
+      per_head[k] = 0;
+      if (!is_long[k]) continue;
+      if (kv + tiles[k] > room) {
+        is_long[k] = false;
+        bad = zero = true;
+        atomicOr(zero_mask + ((b0 + k) >> 5), 1u << ((b0 + k) & 31));
+      } else {
+        for (int pr = 0; pr * kLongRows < n[k]; ++pr) per_head[k] += pair_tiles(len[k] - n[k], n[k], pr);
+        l_units += (int64_t)per_head[k] * p.H;
+        ++served;
+        served_tiles += tiles[k];
+      }
+      kv += tiles[k];
+    }
+    int64_t l_unit = scan(l_units, red, &c.l_units);
+    int64_t kv_at = l_at & 0xFFFFFFFFFFFF, rec = l_at >> 48;
+    // the served sequences are a prefix of the long ones, so the scans of all of them place them
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k) {
+      if (!is_long[k]) continue;
+      LongSeq s;
+      s.unit0 = l_unit;
+      s.b = b0 + k;
+      s.q0 = q0[k];
+      s.n = n[k];
+      s.len = len[k];
+      s.kv0 = (int)kv_at;
+      s.kvt = tiles[k];
+      s.per_head = per_head[k];
+      s.pad = 0;
+      p.l_seqs[rec] = s;
+      ++rec;
+      kv_at += tiles[k];
+      l_unit += (int64_t)per_head[k] * p.H;
+    }
+    int64_t done;
+    scan(((int64_t)served << 48) + served_tiles, red, &done);
+    c.l_seqs = (int)(done >> 48);
+    c.l_tiles = (int)(done & 0xFFFFFFFFFFFF);
   }
+  if (tid == 0) *p.counts = c;
   if (bad) set_err(p.dev_err, MLA_DEVERR_SEQLEN);
   if (__syncthreads_or(zero)) {
     for (int b = 0; b < p.B; ++b) {
@@ -331,30 +391,59 @@ bool sizes_ok(int batch, int n_tokens, int heads, int max_new, int64_t kv_tokens
          kv_tokens <= (int64_t)INT32_MAX;
 }
 
+// Most new tokens that can belong to sequences of the short path.
+int64_t short_tokens(int batch, int n_tokens, int max_new) {
+  const int64_t most = (int64_t)batch * (max_new < kChunkShort ? max_new : kChunkShort);
+  return n_tokens < most ? n_tokens : most;
+}
+
 // Workspace of a call; carves it into p where base is not null.
 int64_t carve(ChunkParams* p, char* base, int batch, int n_tokens, int heads, int max_new, int64_t kv_tokens, int grid) {
   const int R = short_rows_per_tile(max_new, heads);
-  const int64_t per_seq = max_new;
-  const int64_t toks = (int64_t)n_tokens < batch * per_seq ? n_tokens : batch * per_seq;
+  const int64_t toks = short_tokens(batch, n_tokens, max_new);
   const int64_t seqs = batch < n_tokens ? batch : n_tokens;       // with at least one new token
   // a sequence's last row tile may be padded
   const int64_t tiles = (toks * heads + R - 1) / R + seqs;
-  const int64_t sizes[7] = {(int64_t)sizeof(ChunkCounts), seqs * (int64_t)sizeof(ShortSeq), toks * 8,
-                            tiles * kQBlocks * R * 128,   toks * heads * kDc * 2,
-                            2 * grid * partial_floats(R) * 4, grid * (int64_t)sizeof(SplitRec)};
-  int64_t off = 0, at[7];
-  for (int i = 0; i < 7; ++i) {
-    at[i] = off;
+  const bool lng = has_long(max_new, kv_tokens);
+  const int64_t kvt = lng ? kv_tokens / kLongKeys : 0;
+  const int64_t l_seqs = lng ? (seqs < n_tokens / (kChunkShort + 1) ? seqs : n_tokens / (kChunkShort + 1)) : 0;
+  const int64_t sizes[15] = {(int64_t)sizeof(ChunkCounts),
+                             seqs * (int64_t)sizeof(ShortSeq),
+                             toks * 8,
+                             tiles * kQBlocks * R * 128,
+                             toks * heads * kDc * 2,
+                             2 * grid * partial_floats(R) * 4,
+                             grid * (int64_t)sizeof(SplitRec),
+                             l_seqs * (int64_t)sizeof(LongSeq),
+                             kvt * kCTile,
+                             kvt * kBlkBytes,
+                             kvt * 32,
+                             lng ? (int64_t)heads * kWHead : 0,
+                             kvt * heads * kHeadTile,
+                             lng ? 2 * grid * long_partial_floats() * 4 : 0,
+                             lng ? grid * (int64_t)sizeof(SplitRec) : 0};
+  int64_t off = 0;
+  char* at[15];
+  for (int i = 0; i < 15; ++i) {
+    at[i] = base ? base + off : nullptr;
     off += align256(sizes[i]);
   }
   if (base) {
-    p->counts = (ChunkCounts*)(base + at[0]);
-    p->s_seqs = (ShortSeq*)(base + at[1]);
-    p->s_toks = (int2*)(base + at[2]);
-    p->q_tiles = (uint8_t*)(base + at[3]);
-    p->o_lat = (uint16_t*)(base + at[4]);
-    p->parts = (float*)(base + at[5]);
-    p->splits = (SplitRec*)(base + at[6]);
+    p->counts = (ChunkCounts*)at[0];
+    p->s_seqs = (ShortSeq*)at[1];
+    p->s_toks = (int2*)at[2];
+    p->q_tiles = (uint8_t*)at[3];
+    p->o_lat = (uint16_t*)at[4];
+    p->parts = (float*)at[5];
+    p->splits = (SplitRec*)at[6];
+    p->l_seqs = lng ? (LongSeq*)at[7] : nullptr;
+    p->c_tiles = (uint8_t*)at[8];
+    p->k_rope = (uint8_t*)at[9];
+    p->kflags = (uint32_t*)at[10];
+    p->w_tiles = (uint8_t*)at[11];
+    p->kv_tiles = (uint8_t*)at[12];
+    p->l_parts = (float*)at[13];
+    p->l_splits = (SplitRec*)at[14];
   }
   return off;
 }
@@ -427,9 +516,12 @@ mla_status mla_chunk_attention(const mla_cache_layer* cache, const uint16_t* q_n
   const int R = short_rows_per_tile(max_new, heads);
   mla_status s = cuda_status(launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p, R));
   if (s != MLA_OK) return s;
+  if (p.l_seqs) {
+    s = launch_long(p, cache->latent_fmt, cache->kpe_fmt, st);
+    if (s != MLA_OK) return s;
+  }
   // 16-token tiles of the projections: enough CTAs for four per SM
-  const int64_t most = (int64_t)batch * max_new;
-  const int tok_tiles = (int)((((int64_t)n_tokens < most ? (int64_t)n_tokens : most) + 15) / 16);
+  const int tok_tiles = (int)((short_tokens(batch, n_tokens, max_new) + 15) / 16);
   const int za = 4 * p.grid / (9 * heads) + 1, zp = 4 * p.grid / (4 * heads) + 1;
   s = cuda_status(launch_pdl(absorb_tiles_kernel, dim3(heads, 9, tok_tiles < za ? tok_tiles : za), dim3(128), 0, st, p, R));
   if (s != MLA_OK) return s;

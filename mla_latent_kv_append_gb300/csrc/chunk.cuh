@@ -22,11 +22,39 @@ struct __align__(16) ShortSeq {
 };
 static_assert(sizeof(ShortSeq) == 48, "three 16-byte loads");
 
+// One sequence of the long path.  Its new tokens are cut into pairs of 128-row
+// query tiles; a unit is one 128-key tile of one pair of one head.
+struct __align__(16) LongSeq {
+  int64_t unit0;          // units before this sequence's
+  int32_t b, q0, n, len;  // batch index, first token row, new tokens, cached tokens (the new ones included)
+  int32_t kv0, kvt;       // key tiles before this sequence's, and its own
+  int32_t per_head;       // units of one head
+  int32_t pad;
+};
+static_assert(sizeof(LongSeq) == 48, "three 16-byte loads");
+
 // What the device plan writes besides the sequence records.
 struct ChunkCounts {
-  int32_t s_seqs, s_items, s_toks, pad0;
-  int64_t s_units;
+  int32_t s_seqs, s_items, s_toks, l_seqs;
+  int64_t s_units, l_units;
+  int32_t l_tiles, pad;
 };
+
+constexpr int kLongKeys = 128;               // long path: keys per tile
+constexpr int kLongRows = 256;               // query rows (tokens of one head) per item, two tiles of 128
+constexpr int kBlkBytes = 16384;             // 128 rows x 64 fp16, swizzled
+constexpr int kCTile = 8 * kBlkBytes;        // a key tile's latents
+constexpr int kHeadTile = 4 * kBlkBytes;     // a key tile's keys (2 blocks) and values (2 blocks) of one head
+constexpr int kWStage = 2 * kBlkBytes;       // 64 latent channels of a head's W_UK and W_UV
+constexpr int kWHead = 8 * kWStage;
+__host__ __device__ constexpr int64_t long_partial_floats() { return (int64_t)kLongRows * (kDv + 2); }
+
+// Key tiles up to (not including) which pair `pr` of a sequence's new tokens
+// sees any key.
+__host__ __device__ inline int pair_tiles(int ctx, int n, int pr) {
+  const int last = n < (pr + 1) * kLongRows ? n : (pr + 1) * kLongRows;
+  return (ctx + last + kLongKeys - 1) / kLongKeys;
+}
 
 // One partial of a row tile whose key tiles two or more blocks share: fp32
 // [R][512] unnormalised output, then [R] maxima and [R] sums.
@@ -65,7 +93,18 @@ struct ChunkParams {
   uint16_t* o_lat;        // fp16 [rows][512]
   float* parts;           // [2 grid] partials
   SplitRec* splits;       // [grid]
+  LongSeq* l_seqs;
+  uint8_t* c_tiles;       // [key tile][8][128][64] fp16 latents, swizzled
+  uint8_t* k_rope;        // [key tile][128][64] fp16 RoPE keys
+  uint32_t* kflags;       // [key tile][8]: a bit per token: 0..3 not finite, 4..7 on no page
+  uint8_t* w_tiles;       // [H][8][W_UK 128 x 64, W_UV 64 x 128] fp16
+  uint8_t* kv_tiles;      // [key tile][H][K 2 blocks, V 2 blocks] fp16
+  float* l_parts;         // [2 grid] partials of the long path
+  SplitRec* l_splits;     // [grid]; row0: output row of the first (token row x H + head), rows H apart
 };
+
+// Whether a call has a long path at all.
+inline bool has_long(int max_new, int64_t kv_tokens) { return max_new > kChunkShort && kv_tokens >= kLongKeys; }
 
 // The row tile's height for calls whose sequences have up to max_new tokens
 // of the short path: the smallest that holds all rows of a sequence, so that
@@ -75,6 +114,9 @@ inline int short_rows_per_tile(int max_new, int heads) {
   const int64_t rows = (int64_t)n * heads;
   return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
 }
+
+// The long path's launches, after the plan.
+mla_status launch_long(const ChunkParams& p, int lf, int kf, cudaStream_t stream);
 
 // The attention over the short path's sequences, by latent format (one
 // translation unit each); MLA_ERR_UNSUPPORTED for another unit's formats.

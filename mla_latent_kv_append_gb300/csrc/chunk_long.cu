@@ -1,0 +1,791 @@
+// Chunk attention of sequences with many new tokens (long path): the cached
+// latents are expanded once per head into keys and values,
+//   K[h][t] = [W_UK[h] c_hat[t]; kpe_hat[t]]  (192),   V[h][t] = c_hat[t] W_UV[h]  (128),
+// and attention runs on those: 2 x 320 operations per (query, head, key)
+// against the absorbed form's 2 x 1088, for 2 x 512 x 256 per (key, head).
+//
+// Three kernels over fp16 tiles in the workspace, all tiles stored as 128-row
+// x 64-channel blocks of 16 KB in the swizzled order that the MMAs read, so
+// that a tile moves as plain bulk copies:
+//   long_prep_kernel    dequantizes the latents (and converts the weights)
+//   long_expand_kernel  K and V tiles: a tcgen05 GEMM, one key tile's latents
+//                       resident, the heads' weights streaming
+//   long_attention_kernel  two 128-row query tiles of one head against the
+//                       head's key tiles, online softmax
+// Work is split as on the short path: all units in order, cut into equal
+// runs, one per SM; query tiles that fall into several runs leave fp32
+// partials that long_combine_kernel merges in block order.
+//
+// Rounding: latents, weights, keys, values, queries and P are fp16 (2^-11
+// relative each; bf16 queries and weights convert exactly within fp16's normal
+// range), all sums, scores, maxima and outputs fp32 until o is written.
+#include <math.h>
+
+#include "chunk.cuh"
+#include "dequant.cuh"
+#include "tc.cuh"
+
+namespace mla {
+namespace {
+
+using namespace tc;
+
+constexpr float kSlack = 8.f;
+
+// ---------------------------------------------------------------------------
+// long_prep_kernel: block x < 4 tiles: a 32-token block of a key tile, lane =
+// token, warp w dequantizes units w and w + 8, warps 0 and 1 the RoPE units.
+// The blocks behind convert 64 latent channels of a head's weights each.
+// ---------------------------------------------------------------------------
+constexpr int kPrepThreads = 256;
+
+__device__ __forceinline__ void put_rows(uint8_t* blk, int row, int c16, const uint32_t* h) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint4*>(blk + row * 128 + (((c16 + i) ^ (row & 7)) << 4)) =
+        make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+}
+
+__device__ void convert_weights(const ChunkParams& p, int h, int st) {
+  uint8_t* out = p.w_tiles + ((int64_t)h * 8 + st) * kWStage;
+  for (int i = threadIdx.x; i < 2 * 128 * 8; i += kPrepThreads) {
+    // W_UK: rows d, 64 channels (K-major); W_UV: rows c, 128 values as two blocks of 64 (MN-major)
+    const bool uk = i < 1024;
+    const int row = (i & 1023) >> (uk ? 3 : 4), c = i & (uk ? 7 : 15);
+    const uint16_t* src = uk ? p.w_uk + ((int64_t)h * kDn + row) * kDc + 64 * st + 8 * c
+                             : p.w_uv + ((int64_t)h * kDc + 64 * st + row) * kDv + 8 * c;
+    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(src));
+    uint8_t* blk = uk ? out : out + kBlkBytes + (c >> 3) * 8192;
+    *reinterpret_cast<uint4*>(blk + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+        make_uint4(half2_bits(bf16lo(v.x), bf16hi(v.x)), half2_bits(bf16lo(v.y), bf16hi(v.y)),
+                   half2_bits(bf16lo(v.z), bf16hi(v.z)), half2_bits(bf16lo(v.w), bf16hi(v.w)));
+  }
+}
+
+template <int LF, int KF>
+__global__ void __launch_bounds__(kPrepThreads) long_prep_kernel(const ChunkParams p, int key_blocks) {
+  constexpr int kBlock = block_bytes<LF, KF>();
+  __shared__ __align__(128) uint8_t raw[kBlock];
+  __shared__ uint64_t bar;
+  __shared__ uint32_t s_bad;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if ((int)blockIdx.x >= key_blocks) {
+    const int w = blockIdx.x - key_blocks;
+    if (__ldcg(&p.counts->l_seqs) > 0) convert_weights(p, w >> 3, w & 7);
+    return;
+  }
+  const int tile = blockIdx.x >> 2, sub = blockIdx.x & 3;
+  if (tile >= __ldcg(&p.counts->l_tiles)) return;
+  int k = 0, n = __ldcg(&p.counts->l_seqs);          // the sequence: last with kv0 <= tile
+  while (n - k > 1) {
+    const int mid = (k + n) >> 1;
+    if (__ldcg(&p.l_seqs[mid].kv0) <= tile) k = mid;
+    else n = mid;
+  }
+  const int kv0 = __ldcg(&p.l_seqs[k].kv0), len = __ldcg(&p.l_seqs[k].len), b = __ldcg(&p.l_seqs[k].b);
+  const int t0 = (tile - kv0) * kLongKeys + 32 * sub;
+  const int n_tok = min(32, max(0, len - t0));
+  const int page = n_tok > 0 ? __ldcg(p.block_table + (int64_t)b * p.max_pages + t0 / kPage) : 0;
+  const bool page_ok = page >= 0 && page < p.num_pages;
+  const bool read = page_ok && n_tok > 0;
+  if (tid == 0) {
+    bar_init(smem_u32(&bar), 1);
+    bar_init_fence();
+    s_bad = 0;
+    if (!page_ok) set_err(p.dev_err, MLA_DEVERR_PAGE);
+  }
+  __syncthreads();
+  if (tid == 0 && read) {
+    bar_expect(smem_u32(&bar), kBlock);
+    bulk_copy(smem_u32(raw), p.pool + (int64_t)page * p.L.page_bytes + ((t0 >> 5) & 1) * p.L.block_bytes, kBlock, smem_u32(&bar));
+  }
+  bool arrived = true;
+  if (read) {
+    volatile int never = 0;
+    arrived = bar_wait(smem_u32(&bar), 0, p.wait_ns, &never);
+    if (!arrived) {
+      if (tid == 0) set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
+      drain_wait(smem_u32(&bar), 0);
+    }
+  }
+  const bool live = read && arrived && lane < n_tok;
+  uint8_t* out = p.c_tiles + (int64_t)tile * kCTile;
+  const int row = 32 * sub + lane;
+  bool fine = true;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int unit = warp + 8 * i;
+    RawUnit<LF, false> r;
+    uint32_t h[16];
+    if (live) load_unit<LF, false>(raw, p.L, lane, unit, r);
+    else zero_unit(r);
+    fine &= convert_unit<LF, false>(r, h);
+    if (live) fine &= patch_outliers<LF>(raw, p.L, p.outl, lane, unit, h);
+    put_rows(out + (unit >> 1) * kBlkBytes, row, 4 * (unit & 1), h);
+  }
+  if (warp < 2) {
+    RawUnit<KF, true> r;
+    uint32_t h[16];
+    if (live) load_unit<KF, true>(raw, p.L, lane, warp, r);
+    else zero_unit(r);
+    fine &= convert_unit<KF, true>(r, h);
+    put_rows(p.k_rope + (int64_t)tile * kBlkBytes, row, 4 * warp, h);
+  }
+  if (!fine) atomicOr(&s_bad, 1u << lane);
+  __syncthreads();
+  if (tid == 0) {
+    p.kflags[8 * tile + sub] = s_bad;
+    p.kflags[8 * tile + 4 + sub] = page_ok ? 0u : 0xFFFFFFFFu;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// long_expand_kernel: unit (key tile, head), tile-major.  The tile's latents
+// (128 KB) stay in shared memory while the heads' weights stream through
+// three 32 KB stages (64 latent channels of W_UK and W_UV).  Per stage eight
+// M = 128, N = 128 MMAs; a head's keys and values fill 256 TMEM columns, and
+// the two halves of TMEM alternate between the MMAs and the epilogue.
+// What bounds it: the weights' way from L2, 32 KB per 520 cycles and SM.
+// Warps: 0 copies, 1 MMAs, 4..7 epilogue.
+// ---------------------------------------------------------------------------
+constexpr int kExThreads = 256;
+constexpr int kExStages = 3;
+constexpr int kExW = kCTile;
+constexpr int kExBars = kExW + kExStages * kWStage;
+constexpr int kExSmem = kExBars + 256 + 1024;
+static_assert(kExSmem <= 232448, "a block's shared memory");
+enum { xFull = 0, xEmpty = 3, xA = 6, xAFree, xD, xDFree = xD + 2, xFin = xDFree + 2, xCount };
+
+__global__ void __launch_bounds__(kExThreads, 1) long_expand_kernel(const ChunkParams p) {
+  extern __shared__ uint8_t ex_smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ex_smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t sb = smem_u32(sm), bars = sb + kExBars;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kExBars + 8 * xCount);
+  volatile int* abort = reinterpret_cast<volatile int*>(sm + kExBars + 8 * xCount + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < xCount; ++i) bar_init(bars + 8 * i, i == xDFree || i == xDFree + 1 ? 128 : 1);
+    *abort = 0;
+    bar_init_fence();
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tbase = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t U = (int64_t)__ldcg(&p.counts->l_tiles) * p.H;
+  const int64_t lo = U * blockIdx.x / gridDim.x, hi = U * (blockIdx.x + 1) / gridDim.x;
+  bool ok = true;
+  if (warp == 0) {
+    if (elect_one() && hi > lo) {
+      uint32_t it = 0, na = 0;
+      for (int64_t u = lo; u < hi && ok; ++u) {
+        const int tile = (int)(u / p.H), h = (int)(u % p.H);
+        if (u == lo || h == 0) {
+          if (na > 0 && !bar_wait(bars + 8 * xAFree, (na - 1) & 1, p.wait_ns, abort)) {
+            ok = false;
+            break;
+          }
+          bar_expect(bars + 8 * xA, kCTile);
+          bulk_copy(sb, p.c_tiles + (int64_t)tile * kCTile, kCTile, bars + 8 * xA);
+          ++na;
+        }
+        for (int st = 0; st < 8; ++st, ++it) {
+          const uint32_t s = it % kExStages;
+          if (it >= kExStages && !bar_wait(bars + 8 * (xEmpty + s), (it / kExStages - 1) & 1, p.wait_ns, abort)) {
+            ok = false;
+            break;
+          }
+          bar_expect(bars + 8 * (xFull + s), kWStage);
+          bulk_copy(sb + kExW + s * kWStage, p.w_tiles + ((int64_t)h * 8 + st) * kWStage, kWStage, bars + 8 * (xFull + s));
+        }
+      }
+      if (!ok) {
+        set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
+        *abort = 1;
+      }
+      if (na > 0) drain_wait(bars + 8 * xA, (na - 1) & 1);
+      for (uint32_t s = 0; s < kExStages; ++s)
+        if (it > s) drain_wait(bars + 8 * (xFull + s), ((it - 1 - s) / kExStages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (elect_one() && hi > lo) {
+      constexpr uint32_t kIdK = f16_idesc(128, 128, false, false), kIdV = f16_idesc(128, 128, false, true);
+      const uint64_t d_c = sw128_desc(sb, 16, 1024);
+      const uint64_t d_uk = sw128_desc(sb + kExW, 16, 1024), d_uv = sw128_desc(sb + kExW + kBlkBytes, 8192, 1024);
+      uint32_t it = 0, na = 0, nd = 0;
+      for (int64_t u = lo; u < hi && ok; ++u, ++nd) {
+        const int h = (int)(u % p.H);
+        if (u == lo || h == 0) {
+          if (!bar_wait(bars + 8 * xA, na & 1, p.wait_ns, abort)) {
+            ok = false;
+            break;
+          }
+          ++na;
+        }
+        const uint32_t g = nd & 1, d = tbase + 256 * g;
+        if (nd >= 2 && !bar_wait(bars + 8 * (xDFree + g), (nd / 2 - 1) & 1, p.wait_ns, abort)) {
+          ok = false;
+          break;
+        }
+        for (int st = 0; st < 8; ++st, ++it) {
+          const uint32_t s = it % kExStages;
+          if (!bar_wait(bars + 8 * (xFull + s), (it / kExStages) & 1, p.wait_ns, abort)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          const uint64_t a = d_c + (uint64_t)(st * (kBlkBytes >> 4)), w = (uint64_t)(s * (kWStage >> 4));
+          umma4<2, 2>(d, a, d_uk + w, kIdK, st != 0);
+          umma4<2, (2048 >> 4)>(d + 128, a, d_uv + w, kIdV, st != 0);
+          umma_commit(bars + 8 * (xEmpty + s));
+        }
+        if (!ok) break;
+        umma_commit(bars + 8 * (xD + g));
+        if (h == p.H - 1) umma_commit(bars + 8 * xAFree);
+      }
+      if (!ok) {
+        set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
+        *abort = 1;
+      }
+      umma_commit(bars + 8 * xFin);
+      drain_wait(bars + 8 * xFin, 0);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    const int w = warp & 3, row = 32 * w + lane;
+    const uint32_t tl = (uint32_t)(32 * w) << 16;
+    uint32_t nd = 0;
+    for (int64_t u = lo; u < hi; ++u, ++nd) {
+      const uint32_t g = nd & 1;
+      if (!warp_wait(bars + 8 * (xD + g), (nd / 2) & 1, p.wait_ns, abort)) {
+        ok = false;
+        break;
+      }
+      fence_after();
+      uint8_t* out = p.kv_tiles + u * kHeadTile;
+      bool fine = true;
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {        // 32 columns: half a block
+        uint32_t r[32], hw[16];
+        tmem_load32(tbase + 256 * g + 32 * c + tl, r);
+        __half2 acc = __float2half2_rn(0.f);
+        const __half2 zero = acc;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          hw[i] = half2_bits(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+          acc = __hfma2(*reinterpret_cast<const __half2*>(&hw[i]), zero, acc);
+        }
+        if (__hisnan(__low2half(acc)) || __hisnan(__high2half(acc))) {
+          fine = false;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) hw[i] = 0u;
+        }
+        put_rows(out + (c >> 1) * kBlkBytes, row, 4 * (c & 1), hw);
+      }
+      if (!fine) atomicOr(p.kflags + 8 * (u / p.H) + w, 1u << lane);
+      fence_before();
+      bar_arrive(bars + 8 * (xDFree + g));
+    }
+    if (!ok) {
+      set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
+      *abort = 1;
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    tmem_free(tbase, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// long_attention_kernel.  An item is 256 query tokens of one head: two tiles
+// of 128 rows that share the head's key tiles.  While the softmax warps of
+// one tile work, the MMAs of the other run:
+//   S_0(j+1) = Q_0 K(j+1)^T after O_0 += P_0(j) V(j), then the same for tile 1.
+// P replaces its S in TMEM (fp16, half the columns) and is the A operand from
+// there.  Per key tile 2 x (12 + 8) MMAs of M = N = 128, 65 cycles each: 2600
+// cycles bound it; the softmax's 2 x 128 x 128 exponentials take less.
+// TMEM: S_0, S_1, O_0, O_1, 128 columns each.  Shared memory: the two query
+// tiles (96 KB) and a ring of eight 16 KB blocks that carries, per key tile,
+// two K blocks, the RoPE keys, two V blocks.
+// Warps: 0..3 and 4..7 softmax (thread = row), 8 copies, 9 MMAs.
+// ---------------------------------------------------------------------------
+constexpr int kLaThreads = 384;
+constexpr int kRing = 8;
+constexpr int kLaRing = 6 * kBlkBytes;
+constexpr int kLaBars = kLaRing + kRing * kBlkBytes;
+constexpr int kLaSmem = kLaBars + 256 + 1024;
+static_assert(kLaSmem <= 232448, "a block's shared memory");
+// Registers: 384 threads launch with 168 each (64,512): then 216 for the
+// softmax warps, 72 for the others.
+constexpr int kLaRegsSoftmax = 216, kLaRegsIssue = 72;
+static_assert(256 * kLaRegsSoftmax + 128 * kLaRegsIssue <= kLaThreads * 168 && kLaThreads * 168 <= 65536 &&
+                  kLaThreads * 176 > 65536,
+              "the warpgroups' shares come out of the launch's registers");
+enum { aFull = 0, aEmpty = aFull + kRing, aQ = aEmpty + kRing, aS = aQ + 2, aP = aS + 2, aO = aP + 2, aFin = aO + 2, aCount };
+
+struct LongWalk {
+  const LongSeq* seqs;
+  int k;
+  int64_t u, hi;
+  LongSeq s;
+  int h, pair, t0, t1, tiles0;     // tiles0: key tiles the pair's first query tile sees
+  bool first, last, two;           // two: the pair has a second query tile
+
+  __device__ __forceinline__ void load() {
+    const int4* r = reinterpret_cast<const int4*>(seqs + k);
+    int4* d = reinterpret_cast<int4*>(&s);
+    d[0] = __ldcg(r);
+    d[1] = __ldcg(r + 1);
+    d[2] = __ldcg(r + 2);
+  }
+  __device__ __forceinline__ void start(const ChunkParams& p, int64_t lo, int64_t hi_) {
+    seqs = p.l_seqs;
+    u = lo;
+    hi = hi_;
+    int n = __ldcg(&p.counts->l_seqs);
+    k = 0;
+    while (n - k > 1) {
+      const int mid = (k + n) >> 1;
+      if (__ldcg(&seqs[mid].unit0) <= u) k = mid;
+      else n = mid;
+    }
+    load();
+  }
+  __device__ __forceinline__ bool next(int H) {
+    if (u >= hi) return false;
+    while (u >= s.unit0 + (int64_t)s.per_head * H) {
+      ++k;
+      load();
+    }
+    const int64_t d = u - s.unit0;
+    h = (int)(d / s.per_head);
+    int r = (int)(d % s.per_head), J = 0;
+    const int ctx = s.len - s.n;
+    for (pair = 0;; ++pair) {
+      J = pair_tiles(ctx, s.n, pair);
+      if (r < J) break;
+      r -= J;
+    }
+    t0 = r;
+    t1 = (int)min((int64_t)J, t0 + (hi - u));
+    first = t0 == 0;
+    last = t1 == J;
+    two = s.n > pair * kLongRows + 128;
+    tiles0 = two ? (ctx + pair * kLongRows + 128 + kLongKeys - 1) / kLongKeys : J;
+    u += t1 - t0;
+    return true;
+  }
+};
+
+__global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const ChunkParams p) {
+  extern __shared__ uint8_t la_smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(la_smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t sb = smem_u32(sm), bars = sb + kLaBars;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kLaBars + 8 * aCount);
+  volatile int* abort = reinterpret_cast<volatile int*>(sm + kLaBars + 8 * aCount + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < aCount; ++i) bar_init(bars + 8 * i, (i >= aQ && i < aS) || (i >= aP && i < aO) ? 128 : 1);
+    *abort = 0;
+    bar_init_fence();
+  }
+  if (warp == 9) tmem_alloc(smem_u32(tmem_slot), 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tbase = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t U = __ldcg(&p.counts->l_units);
+  const int G = (int)(U < gridDim.x ? U : gridDim.x), x = blockIdx.x;
+  const bool work = x < G;
+  const int64_t lo = work ? U * x / G : 0, hi = work ? U * (x + 1) / G : 0;
+  bool ok = true;
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kLaRegsSoftmax));
+    // ---- softmax of query tile i, thread = row
+    const int i = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t tl = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t t_s = tbase + 128 * i + tl, t_o = tbase + 256 + 128 * i + tl;
+    const float sc = p.scale_log2;
+    LongWalk wk;
+    if (work) wk.start(p, lo, hi);
+    uint32_t it = 0;                       // this tile's key tiles so far
+    while (work && ok && wk.next(p.H)) {
+      if (i == 1 && !wk.two) continue;
+      const int t1 = i == 0 ? min(wk.t1, wk.tiles0) : wk.t1;
+      if (wk.t0 >= t1) {                   // the run begins behind the first tile's last key: an empty partial
+        float* part = p.l_parts + (int64_t)(2 * x + (wk.first ? 1 : 0)) * long_partial_floats();
+#pragma unroll 4
+        for (int c = 0; c < kDv / 4; ++c) reinterpret_cast<float4*>(part + row * kDv)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        part[kLongRows * kDv + row] = -INFINITY;
+        part[kLongRows * kDv + kLongRows + row] = 0.f;
+        continue;
+      }
+      const int tok0 = wk.pair * kLongRows + 128 * i, ctx = wk.s.len - wk.s.n;
+      const bool live = tok0 + row < wk.s.n;
+      // the query rows: this thread's row as fp16, swizzled (padding rows are 0)
+      {
+        const int64_t tok = wk.s.q0 + (live ? tok0 + row : 0);
+        const uint4* qn = reinterpret_cast<const uint4*>(p.qn + tok * p.qn_tok + wk.h * p.qn_head);
+        const uint4* qp = reinterpret_cast<const uint4*>(p.qp + tok * p.qp_tok + wk.h * p.qp_head);
+        uint8_t* q = sm + i * 3 * kBlkBytes + row * 128;
+#pragma unroll 8
+        for (int c = 0; c < 24; ++c) {
+          uint4 v = __ldcg(c < 16 ? qn + c : qp + (c - 16));
+          if (!live) v = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(q + (c >> 3) * kBlkBytes + (((c & 7) ^ (row & 7)) << 4)) =
+              make_uint4(half2_bits(bf16lo(v.x), bf16hi(v.x)), half2_bits(bf16lo(v.y), bf16hi(v.y)),
+                         half2_bits(bf16lo(v.z), bf16hi(v.z)), half2_bits(bf16lo(v.w), bf16hi(v.w)));
+        }
+        fence_async_smem();
+        bar_arrive(bars + 8 * (aQ + i));
+      }
+      const int qpos = ctx + tok0 + (live ? row : 0);
+      const uint4* flags = reinterpret_cast<const uint4*>(p.kflags) + 2 * (int64_t)wk.s.kv0;
+      float m = -INFINITY, l = 0.f;
+      uint4 f_bad = __ldcg(flags + 2 * wk.t0), f_out = __ldcg(flags + 2 * wk.t0 + 1);
+      for (int t = wk.t0; t < t1; ++t, ++it) {
+        const uint4 bad4 = f_bad, out4 = f_out;
+        if (t + 1 < t1) {                  // fetched a tile ahead
+          f_bad = __ldcg(flags + 2 * t + 2);
+          f_out = __ldcg(flags + 2 * t + 3);
+        }
+        if (!warp_wait(bars + 8 * (aS + i), it & 1, p.wait_ns, abort)) {
+          ok = false;
+          break;
+        }
+        // the O_i of the tile before (complete by now: its MMAs were issued first)
+        if (t > wk.t0 && !warp_wait(bars + 8 * (aO + i), (it - 1) & 1, p.wait_ns, abort)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_load32(t_s + 32 * c, s + 32 * c);
+        const uint32_t any_flag = bad4.x | bad4.y | bad4.z | bad4.w | out4.x | out4.y | out4.z | out4.w;
+        if ((t + 1) * kLongKeys - 1 > ctx + tok0 || any_flag) {
+          const uint32_t fb[4] = {bad4.x, bad4.y, bad4.z, bad4.w}, fo[4] = {out4.x, out4.y, out4.z, out4.w};
+          const int seen = qpos - t * kLongKeys;       // keys 0 .. seen of the tile are visible
+#pragma unroll
+          for (int c = 0; c < 128; ++c) {
+            const bool hid = c > seen || ((fo[c >> 5] >> (c & 31)) & 1u);
+            const bool nan = (fb[c >> 5] >> (c & 31)) & 1u;
+            s[c] = hid ? 0xFF800000u : (nan ? 0x7FC00000u : s[c]);
+          }
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 128; ++c) mx = fmaxf(mx, __uint_as_float(s[c]));
+        const bool raise = (mx - m) * sc > kSlack;     // from -inf: the first key seen
+        if (__any_sync(0xffffffffu, raise)) {
+          const float alpha = raise ? ex2((m - mx) * sc) : 1.f;
+          if (raise) m = mx;
+          l *= alpha;
+          if (t > wk.t0) {
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              tmem_load16(t_o + 16 * c, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_store16(t_o + 16 * c, o);
+            }
+          }
+        }
+        const float ms = m == -INFINITY ? 0.f : -m * sc;
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pw[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float a = ex2(fmaf(__uint_as_float(s[64 * c + 2 * e]), sc, ms));
+            const float b = ex2(fmaf(__uint_as_float(s[64 * c + 2 * e + 1]), sc, ms));
+            l0 += a;
+            l1 += b;
+            pw[e] = half2_bits(a, b);
+          }
+          tmem_store32(t_s + 32 * c, pw);
+        }
+        l += l0 + l1;
+        fence_before();
+        bar_arrive(bars + 8 * (aP + i));
+      }
+      if (!ok) break;
+      if (!warp_wait(bars + 8 * (aO + i), (it - 1) & 1, p.wait_ns, abort)) {
+        ok = false;
+        break;
+      }
+      fence_after();
+      // whole: this block saw every key of the item
+      const bool whole = wk.first && wk.last;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int64_t out_row = (int64_t)(wk.s.q0 + tok0 + row) * p.H + wk.h;
+      float* part = p.l_parts + (int64_t)(2 * x + (wk.first ? 1 : 0)) * long_partial_floats();
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        tmem_load32(t_o + 32 * c, o);
+        if (!live) continue;
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + out_row * kDv + 32 * c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n"
+                  : "=r"(w[q])
+                  : "f"(__uint_as_float(o[8 * e + 2 * q + 1]) * inv), "f"(__uint_as_float(o[8 * e + 2 * q]) * inv));
+            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(part + (128 * i + row) * kDv + 32 * c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+      __syncwarp();
+      if (!whole && live) {
+        part[kLongRows * kDv + 128 * i + row] = m * sc;
+        part[kLongRows * kDv + kLongRows + 128 * i + row] = l;
+      }
+      fence_before();
+      if (wk.first && !wk.last && i == 0 && row == 0) {
+        const int64_t end = wk.u - (wk.t1 - wk.t0) + pair_tiles(ctx, wk.s.n, wk.pair);
+        int y = x + 1;
+        while (U * (y + 1) / G < end) ++y;
+        SplitRec rec;
+        rec.rows = min(kLongRows, wk.s.n - wk.pair * kLongRows);
+        rec.last = y;
+        rec.row0 = (int64_t)(wk.s.q0 + wk.pair * kLongRows) * p.H + wk.h;
+        p.l_splits[x] = rec;
+      }
+    }
+    if (!ok) {
+      set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
+      *abort = 1;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kLaRegsIssue));
+    if (work && warp == 8 && elect_one()) {
+      // ---- copies: K0 K1 RoPE V0 V1 of every key tile
+      LongWalk wk;
+      wk.start(p, lo, hi);
+      uint32_t n = 0;
+      while (ok && wk.next(p.H)) {
+        for (int t = wk.t0; t < wk.t1 && ok; ++t) {
+          const int64_t tile = wk.s.kv0 + t;
+          const uint8_t* kv = p.kv_tiles + (tile * p.H + wk.h) * kHeadTile;
+#pragma unroll 1
+          for (int c = 0; c < 5; ++c, ++n) {
+            const uint32_t s = n % kRing;
+            if (n >= kRing && !bar_wait(bars + 8 * (aEmpty + s), (n / kRing - 1) & 1, p.wait_ns, abort)) {
+              ok = false;
+              break;
+            }
+            const uint8_t* src = c < 2 ? kv + c * kBlkBytes : (c == 2 ? p.k_rope + tile * kBlkBytes : kv + (c - 1) * kBlkBytes);
+            bar_expect(bars + 8 * (aFull + s), kBlkBytes);
+            bulk_copy(sb + kLaRing + s * kBlkBytes, src, kBlkBytes, bars + 8 * (aFull + s));
+          }
+        }
+      }
+      if (!ok) {
+        set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
+        *abort = 1;
+      }
+      for (uint32_t s = 0; s < kRing; ++s)
+        if (n > s) drain_wait(bars + 8 * (aFull + s), ((n - 1 - s) / kRing) & 1);
+    } else if (work && warp == 9 && elect_one()) {
+      // ---- MMAs
+      LongWalk wk;
+      wk.start(p, lo, hi);
+      constexpr uint32_t kIdS = f16_idesc(128, 128, false, false), kIdO = f16_idesc(128, 128, false, true),
+                         kIdO64 = f16_idesc(128, 64, false, true);
+      const uint64_t d_q = sw128_desc(sb, 16, 1024), d_k = sw128_desc(sb + kLaRing, 16, 1024),
+                     d_v = sw128_desc(sb + kLaRing, kBlkBytes, 1024);
+      uint32_t n = 0;                      // ring blocks of the tiles before this one
+      uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+      auto wait_slots = [&](uint32_t first, int count) -> bool {
+        for (int c = 0; c < count; ++c)
+          if (!bar_wait(bars + 8 * (aFull + (first + c) % kRing), ((first + c) / kRing) & 1, p.wait_ns, abort)) return false;
+        return true;
+      };
+      auto scores = [&](int i, uint32_t at) {              // S_i = Q_i K^T, K in blocks at, at + 1, at + 2
+        fence_after();
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+          umma4<2, 2>(tbase + 128 * i, d_q + (uint64_t)((i * 3 + c) * (kBlkBytes >> 4)),
+                      d_k + (uint64_t)(((at + c) % kRing) * (kBlkBytes >> 4)), kIdS, c != 0);
+        umma_commit(bars + 8 * (aS + i));
+      };
+      auto outputs = [&](int i, uint32_t at, uint32_t acc) {   // O_i += P_i V, V in blocks at, at + 1
+        fence_after();
+        const uint32_t s0 = at % kRing, d = tbase + 256 + 128 * i, a = tbase + 128 * i;
+        const uint64_t v0 = d_v + (uint64_t)(s0 * (kBlkBytes >> 4));
+        if (s0 + 1 < kRing) {
+          umma4_ta<(2048 >> 4)>(d, a, v0, kIdO, acc);
+          umma4_ta<(2048 >> 4)>(d, a + 32, v0 + 4 * (2048 >> 4), kIdO, 1u);
+        } else {                           // the second block wrapped around: 64 columns at a time
+          umma4_ta<(2048 >> 4)>(d, a, v0, kIdO64, acc);
+          umma4_ta<(2048 >> 4)>(d, a + 32, v0 + 4 * (2048 >> 4), kIdO64, 1u);
+          umma4_ta<(2048 >> 4)>(d + 64, a, d_v, kIdO64, acc);
+          umma4_ta<(2048 >> 4)>(d + 64, a + 32, d_v + 4 * (2048 >> 4), kIdO64, 1u);
+        }
+        umma_commit(bars + 8 * (aO + i));
+      };
+      auto release = [&](uint32_t first, int count) {
+        for (int c = 0; c < count; ++c) umma_commit(bars + 8 * (aEmpty + (first + c) % kRing));
+      };
+      while (ok && wk.next(p.H)) {
+        const int end0 = min(wk.t1, wk.tiles0), tiles = wk.t1 - wk.t0;
+        const bool zero = wk.t0 < end0;    // the first query tile takes part
+        if (zero) {
+          if (!bar_wait(bars + 8 * aQ, nq[0] & 1, p.wait_ns, abort)) { ok = false; break; }
+          ++nq[0];
+        }
+        if (wk.two) {
+          if (!bar_wait(bars + 8 * (aQ + 1), nq[1] & 1, p.wait_ns, abort)) { ok = false; break; }
+          ++nq[1];
+        }
+        if (!wait_slots(n, 3)) { ok = false; break; }
+        if (zero) scores(0, n);
+        if (wk.two) scores(1, n);
+        release(n, 3);
+        for (int j = 0; j < tiles; ++j, n += 5) {
+          const int t = wk.t0 + j;
+          const bool more = j + 1 < tiles;
+          if (!wait_slots(n + 3, 2)) { ok = false; break; }
+          if (t < end0) {
+            if (!bar_wait(bars + 8 * aP, np[0] & 1, p.wait_ns, abort)) { ok = false; break; }
+            ++np[0];
+            outputs(0, n + 3, j > 0);
+          }
+          if (more && !wait_slots(n + 5, 3)) { ok = false; break; }
+          if (more && t + 1 < end0) scores(0, n + 5);
+          if (wk.two) {
+            if (!bar_wait(bars + 8 * (aP + 1), np[1] & 1, p.wait_ns, abort)) { ok = false; break; }
+            ++np[1];
+            outputs(1, n + 3, j > 0);
+          }
+          release(n + 3, 2);
+          if (more) {
+            if (wk.two) scores(1, n + 5);
+            release(n + 5, 3);
+          }
+        }
+      }
+      if (!ok) {
+        set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
+        *abort = 1;
+      }
+      umma_commit(bars + 8 * aFin);
+      drain_wait(bars + 8 * aFin, 0);
+    }
+    __syncwarp();
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    fence_after();
+    tmem_free(tbase, 512);
+  }
+}
+
+// long_combine_kernel: grid (blocks of the attention, 64), block 128: a warp
+// merges one row of the item whose first part block x holds.
+__global__ void __launch_bounds__(128) long_combine_kernel(const ChunkParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int x = blockIdx.x, r = 4 * blockIdx.y + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const SplitRec* sr = p.l_splits + x;
+  if (r >= __ldcg(&sr->rows)) return;
+  const int n = __ldcg(&sr->last) - x + 1;
+  const int64_t row0 = __ldcg(&sr->row0);
+  const float* part = p.l_parts + (int64_t)(2 * x + 1) * long_partial_floats();
+  // part 0 is slot 2x + 1, part i > 0 slot 2 (x + i)
+  auto at = [&](int i) { return part + i * 2 * long_partial_floats() - (i ? long_partial_floats() : 0); };
+  float mx = -INFINITY;
+  for (int i = 0; i < n; ++i) mx = fmaxf(mx, __ldcg(at(i) + kLongRows * kDv + r));
+  if (mx == -INFINITY) mx = 0.f;
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float* s = at(i);
+    const float mi = __ldcg(s + kLongRows * kDv + r), li = __ldcg(s + kLongRows * kDv + kLongRows + r);
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(s + r * kDv) + lane);
+    const float wt = ex2(mi - mx);
+    l = fmaf(wt, li, l);
+    acc.x = fmaf(wt, v.x, acc.x);
+    acc.y = fmaf(wt, v.y, acc.y);
+    acc.z = fmaf(wt, v.z, acc.z);
+    acc.w = fmaf(wt, v.w, acc.w);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t a, b;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(a) : "f"(acc.y * inv), "f"(acc.x * inv));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(b) : "f"(acc.w * inv), "f"(acc.z * inv));
+  reinterpret_cast<uint2*>(p.o + (row0 + (int64_t)r * p.H) * kDv)[lane] = make_uint2(a, b);
+}
+
+template <int LF, int KF>
+mla_status launch_prep(const ChunkParams& p, cudaStream_t stream) {
+  const int key_blocks = 4 * (int)(p.kv_tokens / kLongKeys);
+  return cuda_status(launch_pdl(long_prep_kernel<LF, KF>, dim3(key_blocks + 8 * p.H), dim3(kPrepThreads), 0, stream, p, key_blocks));
+}
+
+}  // namespace
+
+mla_status launch_long(const ChunkParams& p, int lf, int kf, cudaStream_t stream) {
+  static int configured[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    mla_status st = cuda_status(cudaFuncSetAttribute(long_expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExSmem));
+    if (st == MLA_OK) st = cuda_status(cudaFuncSetAttribute(long_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLaSmem));
+    if (st != MLA_OK) return st;
+    if (dev >= 0 && dev < 64) configured[dev] = 1;
+  }
+  mla_status st = MLA_ERR_UNSUPPORTED;
+#define MLA_CHUNK_CASE(A, K) \
+  if (lf == A && kf == K) st = launch_prep<A, K>(p, stream);
+  MLA_CHUNK_CASE(MLA_FMT_BF16, MLA_FMT_BF16)
+  MLA_CHUNK_CASE(MLA_FMT_BF16, MLA_FMT_INT8_SYM)
+  MLA_CHUNK_CASE(MLA_FMT_BF16, MLA_FMT_INT4_SYM)
+  MLA_CHUNK_CASE(MLA_FMT_INT8_SYM, MLA_FMT_BF16)
+  MLA_CHUNK_CASE(MLA_FMT_INT8_SYM, MLA_FMT_INT8_SYM)
+  MLA_CHUNK_CASE(MLA_FMT_INT8_SYM, MLA_FMT_INT4_SYM)
+  MLA_CHUNK_CASE(MLA_FMT_INT4_ASYM, MLA_FMT_BF16)
+  MLA_CHUNK_CASE(MLA_FMT_INT4_ASYM, MLA_FMT_INT8_SYM)
+  MLA_CHUNK_CASE(MLA_FMT_INT4_ASYM, MLA_FMT_INT4_SYM)
+  MLA_CHUNK_CASE(MLA_FMT_INT4_SYM, MLA_FMT_BF16)
+  MLA_CHUNK_CASE(MLA_FMT_INT4_SYM, MLA_FMT_INT8_SYM)
+  MLA_CHUNK_CASE(MLA_FMT_INT4_SYM, MLA_FMT_INT4_SYM)
+  MLA_CHUNK_CASE(MLA_FMT_INT8_G8, MLA_FMT_INT8_SYM)
+  MLA_CHUNK_CASE(MLA_FMT_INT8_G32, MLA_FMT_INT8_SYM)
+  MLA_CHUNK_CASE(MLA_FMT_INT8_G64, MLA_FMT_INT8_SYM)
+  MLA_CHUNK_CASE(MLA_FMT_INT8_TOKEN, MLA_FMT_INT8_SYM)
+  MLA_CHUNK_CASE(MLA_FMT_INT8_OUTLIER, MLA_FMT_BF16)
+  MLA_CHUNK_CASE(MLA_FMT_INT8_OUTLIER, MLA_FMT_INT8_SYM)
+#undef MLA_CHUNK_CASE
+  if (st != MLA_OK) return st;
+  st = cuda_status(launch_pdl(long_expand_kernel, dim3(p.grid), dim3(kExThreads), kExSmem, stream, p));
+  if (st != MLA_OK) return st;
+  st = cuda_status(launch_pdl(long_attention_kernel, dim3(p.grid), dim3(kLaThreads), kLaSmem, stream, p));
+  if (st != MLA_OK) return st;
+  return cuda_status(launch_pdl(long_combine_kernel, dim3(p.grid, kLongRows / 4), dim3(128), 0, stream, p));
+}
+
+}  // namespace mla

@@ -79,22 +79,20 @@ __host__ __device__ constexpr uint32_t f16_idesc(int m, int n, bool a_mn_major, 
   return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(m >> 4) << 24);
 }
-__device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
-}
-// The same with A in TMEM.
-__device__ __forceinline__ void umma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
-}
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar)
                : "memory");
+}
+// Four MMAs with A in TMEM (8 columns per 16 elements of the contraction).
+template <int B>
+__device__ __forceinline__ void umma4_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 y;\n .reg .b32 x;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " add.u32 x, %1, 8;\n add.s64 y, %2, %5;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, 1;\n"
+      " add.u32 x, %1, 16;\n add.s64 y, %2, %6;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, 1;\n"
+      " add.u32 x, %1, 24;\n add.s64 y, %2, %7;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, 1;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(B), "n"(2 * B), "n"(3 * B));
 }
 // One lane of a converged warp.  MMAs issued under this predicate keep their
 // descriptors in uniform registers: an issue costs the operands' shared-memory
