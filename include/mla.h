@@ -569,7 +569,8 @@ mla_status mla_rope(const uint16_t* q_pe, int64_t q_token_stride, int64_t q_head
  *   q_nope  bf16 [n_tokens][H][128], q_pe bf16 [n_tokens][H][64], both at the
  *           given token and head strides (elements, multiples of 8; they may
  *           be slices of one [n][H][192] array), 16-byte aligned
- *   w_uk    bf16 [H][128][512], w_uv bf16 [H][512][128]
+ *   w_uk    bf16 [H][128][512], w_uv bf16 [H][512][128]; both are read during
+ *           the launch overlap (see Execution above)
  *   block_table int32 [B][max_pages]; q_start int32 [B + 1], increasing;
  *           seq_lens int32 [B], the new tokens included (0: the sequence's
  *           rows are 0)

@@ -331,18 +331,35 @@ def mla_lse_merge(o_parts, lse_parts, o_lat, lse=None, stream=None):
                                               _stream(stream)))
 
 
-def _rows(t, n, heads, width, name):
+# The serving-step calls run a few microseconds on the GPU, so their bindings
+# keep to cheap checks and pass addresses as plain integers.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _rows(t, shape, name):
     """(token stride, head stride) of a bf16 CUDA tensor [n, heads, width] whose rows are contiguous."""
-    if t.dtype is not torch.bfloat16 or t.shape != (n, heads, width) or not t.is_cuda or t.stride(2) != 1:
-        raise ValueError("%s: expected CUDA bfloat16 %s with contiguous rows, got %s %s" % (
-            name, (n, heads, width), t.dtype, tuple(t.shape)))
-    return t.stride(0), t.stride(1)
+    s = t.stride()
+    if t.dtype is not torch.bfloat16 or t.shape != shape or not t.is_cuda or s[2] != 1:
+        raise ValueError("%s: expected CUDA bfloat16 %s with contiguous rows, got %s %s" % (name, shape, t.dtype,
+                                                                                           tuple(t.shape)))
+    return s
 
 
-def _ints(t, shape, name):
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError("%s: expected contiguous CUDA int32 %s, got %s %s" % (name, shape, t.dtype, tuple(t.shape)))
+def _flat(t, dtype, shape, name):
+    """The address of a contiguous CUDA tensor."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s: expected contiguous CUDA %s %s, got %s %s" % (name, dtype, shape, t.dtype, tuple(t.shape)))
     return t.data_ptr()
+
+
+def _step(name, t, stream, *args):
+    """Calls the library on t's device: on ``stream``, or that device's current one."""
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            _check(name, getattr(lib, name)(*args, stream.cuda_stream if stream is not None else _raw_stream(dev)))
+    else:
+        _check(name, getattr(lib, name)(*args, stream.cuda_stream if stream is not None else _raw_stream(dev)))
 
 
 def mla_plan_chunks(ctx_lens, new_lens, req, page_table, free_pages, free_range, num_pages, block_table, q_start,
@@ -354,14 +371,16 @@ def mla_plan_chunks(ctx_lens, new_lens, req, page_table, free_pages, free_range,
     .. ``free_head``."""
     B, n = ctx_lens.shape[0], slot.shape[0]
     rows, max_pages = page_table.shape
-    _check("mla_plan_chunks", lib.mla_plan_chunks(
-        _ints(ctx_lens, (B,), "ctx_lens"), _ints(new_lens, (B,), "new_lens"), _ints(req, (B,), "req"), B,
-        _ints(page_table, (rows, max_pages), "page_table"), rows, max_pages,
-        _ints(free_pages, (free_pages.shape[0],), "free_pages"), free_pages.shape[0],
-        _ints(free_range, (2,), "free_range"), int(num_pages), n, _ints(block_table, (B, max_pages), "block_table"),
-        _ints(q_start, (B + 1,), "q_start"), _ints(seq_lens, (B,), "seq_lens"), _ints(positions, (n,), "positions"),
-        _ints(token_req, (n,), "token_req"), _ints(slot, (n,), "slot"), _ints(free_head, (1,), "free_head"),
-        _ptr(dev_err), _stream(stream)))
+    i32 = torch.int32
+    _step("mla_plan_chunks", ctx_lens, stream,
+          _flat(ctx_lens, i32, (B,), "ctx_lens"), _flat(new_lens, i32, (B,), "new_lens"), _flat(req, i32, (B,), "req"), B,
+          _flat(page_table, i32, (rows, max_pages), "page_table"), rows, max_pages,
+          _flat(free_pages, i32, (free_pages.shape[0],), "free_pages"), free_pages.shape[0],
+          _flat(free_range, i32, (2,), "free_range"), num_pages, n,
+          _flat(block_table, i32, (B, max_pages), "block_table"), _flat(q_start, i32, (B + 1,), "q_start"),
+          _flat(seq_lens, i32, (B,), "seq_lens"), _flat(positions, i32, (n,), "positions"),
+          _flat(token_req, i32, (n,), "token_req"), _flat(slot, i32, (n,), "slot"), _flat(free_head, i32, (1,), "free_head"),
+          None if dev_err is None else dev_err.data_ptr())
 
 
 def mla_rope(q_pe, k_pe, positions, inv_freq, q_out, k_out, pair_axis=None, interleaved=True, inverse=False,
@@ -370,25 +389,24 @@ def mla_rope(q_pe, k_pe, positions, inv_freq, q_out, k_out, pair_axis=None, inte
     and head strides that are multiples of 8; k_pe and k_out may be None) into
     q_out and k_out, which may be the inputs.  positions int32 [n] or [axes,
     n]; inv_freq fp32 [32]; pair_axis: the axis of each of the 32 pairs."""
-    n, H = q_pe.shape[0], q_pe.shape[1]
+    n, H, _ = q_pe.shape
     axes = 1 if positions.dim() == 1 else positions.shape[0]
-    qs, qos = _rows(q_pe, n, H, ROPE_DIM, "q_pe"), _rows(q_out, n, H, ROPE_DIM, "q_out")
+    qs, qos = _rows(q_pe, (n, H, ROPE_DIM), "q_pe"), _rows(q_out, (n, H, ROPE_DIM), "q_out")
     if (k_pe is None) != (k_out is None):
         raise ValueError("k_pe and k_out go together")
-    ks = kos = (0, 0)
+    kp = ko = None
+    ks = kos = (0,)
     if k_pe is not None:
-        ks = _rows(k_pe[:, None], n, 1, ROPE_DIM, "k_pe")
-        kos = _rows(k_out[:, None], n, 1, ROPE_DIM, "k_out")
-    _ints(positions, (n,) if positions.dim() == 1 else (axes, n), "positions")
-    _need(inv_freq, torch.float32, (ROPE_DIM // 2,), "inv_freq")
+        ks, kos = _rows(k_pe[:, None], (n, 1, ROPE_DIM), "k_pe"), _rows(k_out[:, None], (n, 1, ROPE_DIM), "k_out")
+        kp, ko = k_pe.data_ptr(), k_out.data_ptr()
     if pair_axis is not None:
         pair_axis = bytes(pair_axis)
         if len(pair_axis) != ROPE_DIM // 2:
             raise ValueError("pair_axis: expected %d axes" % (ROPE_DIM // 2))
-    _check("mla_rope", lib.mla_rope(
-        _ptr(q_pe), qs[0], qs[1], _ptr(k_pe), ks[0], _ptr(positions), axes, pair_axis, _ptr(inv_freq), n, H,
-        1 if interleaved else 0, 1 if inverse else 0, float(amplitude), _ptr(q_out), qos[0], qos[1], _ptr(k_out),
-        kos[0], _stream(stream)))
+    _step("mla_rope", q_pe, stream, q_pe.data_ptr(), qs[0], qs[1], kp, ks[0],
+          _flat(positions, torch.int32, (n,) if positions.dim() == 1 else (axes, n), "positions"), axes, pair_axis,
+          _flat(inv_freq, torch.float32, (ROPE_DIM // 2,), "inv_freq"), n, H, 1 if interleaved else 0, 1 if inverse else 0,
+          amplitude, q_out.data_ptr(), qos[0], qos[1], ko, kos[0])
 
 
 def mla_chunk_workspace_bytes(batch, n_tokens, heads, max_new, kv_tokens=0):
@@ -402,20 +420,18 @@ def mla_chunk_attention(cache, q_nope, q_pe, w_uk, w_uv, block_table, q_start, s
     to o [n, H, 128] (bf16).  Sequence b's tokens are rows q_start[b] ..
     q_start[b + 1] - 1 (lengths on the device); max_new bounds their number,
     kv_tokens the lengths of the sequences with more than CHUNK_SHORT."""
-    n, H = q_nope.shape[0], q_nope.shape[1]
-    B = seq_lens.shape[0]
-    qn, qp = _rows(q_nope, n, H, QK_NOPE_DIM, "q_nope"), _rows(q_pe, n, H, ROPE_DIM, "q_pe")
-    _need(w_uk, torch.bfloat16, (H, QK_NOPE_DIM, KV_LORA_RANK), "w_uk")
-    _need(w_uv, torch.bfloat16, (H, KV_LORA_RANK, V_DIM), "w_uv")
-    _need(o, torch.bfloat16, (n, H, V_DIM), "o")
-    scale = DEFAULT_SOFTMAX_SCALE if softmax_scale is None else float(softmax_scale)
+    n, H, _ = q_nope.shape
+    B, max_pages = block_table.shape
+    qn, qp = _rows(q_nope, (n, H, QK_NOPE_DIM), "q_nope"), _rows(q_pe, (n, H, ROPE_DIM), "q_pe")
+    bf16, i32 = torch.bfloat16, torch.int32
     cs = cache.c_struct()
-    _check("mla_chunk_attention", lib.mla_chunk_attention(
-        ctypes.byref(cs), _ptr(q_nope), qn[0], qn[1], _ptr(q_pe), qp[0], qp[1], _ptr(w_uk), _ptr(w_uv),
-        _ints(block_table, (B, block_table.shape[1]), "block_table"), block_table.shape[1],
-        _ints(q_start, (B + 1,), "q_start"), _ints(seq_lens, (B,), "seq_lens"), B, n, H, int(max_new),
-        int(kv_tokens), scale, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(o), _ptr(dev_err),
-        _stream(stream)))
+    _step("mla_chunk_attention", q_nope, stream, ctypes.byref(cs), q_nope.data_ptr(), qn[0], qn[1], q_pe.data_ptr(), qp[0], qp[1],
+          _flat(w_uk, bf16, (H, QK_NOPE_DIM, KV_LORA_RANK), "w_uk"), _flat(w_uv, bf16, (H, KV_LORA_RANK, V_DIM), "w_uv"),
+          _flat(block_table, i32, (B, max_pages), "block_table"), max_pages, _flat(q_start, i32, (B + 1,), "q_start"),
+          _flat(seq_lens, i32, (B,), "seq_lens"), B, n, H, max_new, kv_tokens,
+          DEFAULT_SOFTMAX_SCALE if softmax_scale is None else softmax_scale, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), _flat(o, bf16, (n, H, V_DIM), "o"),
+          None if dev_err is None else dev_err.data_ptr())
 
 
 def mla_set_prefill_path(path):

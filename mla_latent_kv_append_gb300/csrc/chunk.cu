@@ -38,7 +38,7 @@ __device__ __forceinline__ int64_t scan(int64_t v, int64_t* red, int64_t* total)
   __syncthreads();
   if (lane == 31) red[warp] = x;
   __syncthreads();
-  int64_t s = red[lane];
+  int64_t s = lane < (int)(blockDim.x >> 5) ? red[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
@@ -59,12 +59,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
   pdl_wait();
   const int tid = threadIdx.x;
   const bool long_path = p.l_seqs != nullptr;
-  for (int i = tid; i < p.grid; i += kPlanThreads) {
-    p.splits[i].rows = 0;
-    if (long_path) p.l_splits[i].rows = 0;
-  }
-  for (int i = tid; i < kMaxBatch / 32; i += kPlanThreads) zero_mask[i] = 0;
-  const int per = (p.B + kPlanThreads - 1) / kPlanThreads, b0 = tid * per;
+  for (int i = tid; i < kMaxBatch / 32; i += blockDim.x) zero_mask[i] = 0;
+  const int per = (p.B + blockDim.x - 1) / blockDim.x, b0 = tid * per;
   int q0[kPlanPer], n[kPlanPer], len[kPlanPer];
   bool order = true;
 #pragma unroll
@@ -194,7 +190,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
       if (!((zero_mask[b >> 5] >> (b & 31)) & 1u)) continue;
       const int64_t lo = max(__ldcg(p.q_start + b), 0), hi = min(__ldcg(p.q_start + b + 1), p.N);
       uint4* rows = reinterpret_cast<uint4*>(p.o);
-      for (int64_t i = lo * p.H * (kDv / 8) + tid; i < hi * p.H * (kDv / 8); i += kPlanThreads)
+      for (int64_t i = lo * p.H * (kDv / 8) + tid; i < hi * p.H * (kDv / 8); i += blockDim.x)
         rows[i] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
@@ -250,16 +246,24 @@ __global__ void __launch_bounds__(128) absorb_tiles_kernel(const ChunkParams p, 
   __shared__ int2 toks[16];
   const int h = blockIdx.x, kb = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, j = lane & 3;
+  // the weights are no kernel's output: their fetch overlaps the plan
+  if (kb < 8) {
+    const uint16_t* wsrc = p.w_uk + (size_t)h * kDn * kDc + 64 * kb;
+    uint4 v[kDn * 8 / 128];
+#pragma unroll
+    for (int i = 0; i < kDn * 8 / 128; ++i) {
+      const int e = tid + 128 * i;
+      v[i] = __ldcg(reinterpret_cast<const uint4*>(wsrc + (size_t)(e >> 3) * kDc + 8 * (e & 7)));
+    }
+#pragma unroll
+    for (int i = 0; i < kDn * 8 / 128; ++i) {
+      const int e = tid + 128 * i;
+      *reinterpret_cast<uint4*>(ws + (e >> 3) * kAbWS + 8 * (e & 7)) = v[i];
+    }
+  }
   pdl_wait();
   const int n = __ldcg(&p.counts->s_toks);
   if (16 * (int)blockIdx.z >= n) return;
-  if (kb < 8) {
-    const uint16_t* wsrc = p.w_uk + (size_t)h * kDn * kDc + 64 * kb;
-    for (int i = tid; i < kDn * 8; i += 128) {
-      const int k = i >> 3, c = i & 7;
-      *reinterpret_cast<uint4*>(ws + k * kAbWS + 8 * c) = __ldcg(reinterpret_cast<const uint4*>(wsrc + (size_t)k * kDc + 8 * c));
-    }
-  }
   const uint32_t a_base = tc::smem_u32(as) + (((lane & 7) + 8 * ((lane >> 3) & 1)) * kAbAS + 8 * (lane >> 4)) * 2;
   const uint32_t b_base =
       tc::smem_u32(ws) + (((lane & 7) + 8 * ((lane >> 3) & 1)) * kAbWS + 16 * warp + 8 * (lane >> 4)) * 2;
@@ -325,17 +329,27 @@ __global__ void __launch_bounds__(128) project_kernel(const ChunkParams p) {
   __shared__ float red[4][16][kPrN + 1];
   const int h = blockIdx.x, n0 = blockIdx.y * kPrN;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, j = lane & 3;
+  const uint16_t* wsrc = p.w_uv + (size_t)h * kDc * kDv + n0;
+  // the weights are no kernel's output: their fetch overlaps the attention
+#pragma unroll
+  for (int j0 = 0; j0 < kDc * (kPrN / 8) / 128; j0 += 8) {
+    uint4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = tid + 128 * (j0 + i);
+      v[i] = __ldcg(reinterpret_cast<const uint4*>(wsrc + (size_t)(e / (kPrN / 8)) * kDv + 8 * (e % (kPrN / 8))));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = tid + 128 * (j0 + i);
+      *reinterpret_cast<uint4*>(ws + (e / (kPrN / 8)) * kPrWS + 8 * (e % (kPrN / 8))) =
+          make_uint4(tc::half2_bits(bf16lo(v[i].x), bf16hi(v[i].x)), tc::half2_bits(bf16lo(v[i].y), bf16hi(v[i].y)),
+                     tc::half2_bits(bf16lo(v[i].z), bf16hi(v[i].z)), tc::half2_bits(bf16lo(v[i].w), bf16hi(v[i].w)));
+    }
+  }
   pdl_wait();
   const int n = __ldcg(&p.counts->s_toks);
   if (16 * (int)blockIdx.z >= n) return;
-  const uint16_t* wsrc = p.w_uv + (size_t)h * kDc * kDv + n0;
-  for (int i = tid; i < kDc * (kPrN / 8); i += 128) {
-    const int k = i / (kPrN / 8), c = i % (kPrN / 8);
-    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(wsrc + (size_t)k * kDv + 8 * c));
-    *reinterpret_cast<uint4*>(ws + k * kPrWS + 8 * c) =
-        make_uint4(tc::half2_bits(bf16lo(v.x), bf16hi(v.x)), tc::half2_bits(bf16lo(v.y), bf16hi(v.y)),
-                   tc::half2_bits(bf16lo(v.z), bf16hi(v.z)), tc::half2_bits(bf16lo(v.w), bf16hi(v.w)));
-  }
   const uint32_t b_base = tc::smem_u32(ws) + ((128 * warp + (lane & 7) + 8 * ((lane >> 3) & 1)) * kPrWS + 8 * (lane >> 4)) * 2;
   for (int t0 = 16 * blockIdx.z; t0 < n; t0 += 16 * gridDim.z) {
     __syncthreads();
@@ -452,7 +466,7 @@ int64_t carve(ChunkParams* p, char* base, int batch, int n_tokens, int heads, in
 // for on a machine that has none) the GB300's 152.
 int chunk_grid() {
   const int sms = device_sm_count();
-  return sms > 0 ? sms : 152;
+  return sms > 0 ? (sms < 1024 ? sms : 1024) : 152;
 }
 
 }  // namespace
@@ -514,7 +528,9 @@ mla_status mla_chunk_attention(const mla_cache_layer* cache, const uint16_t* q_n
   p.wait_ns = wait_limit_ns();
   const cudaStream_t st = (cudaStream_t)stream;
   const int R = short_rows_per_tile(max_new, heads);
-  mla_status s = cuda_status(launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p, R));
+  // a thread per sequence; small blocks synchronise faster
+  const int plan_threads = batch <= 128 ? 128 : (batch <= 512 ? 512 : kPlanThreads);
+  mla_status s = cuda_status(launch_pdl(chunk_plan_kernel, dim3(1), dim3(plan_threads), 0, st, p, R));
   if (s != MLA_OK) return s;
   if (p.l_seqs) {
     s = launch_long(p, cache->latent_fmt, cache->kpe_fmt, st);

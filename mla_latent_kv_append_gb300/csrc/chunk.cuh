@@ -37,7 +37,8 @@ static_assert(sizeof(LongSeq) == 48, "three 16-byte loads");
 struct ChunkCounts {
   int32_t s_seqs, s_items, s_toks, l_seqs;
   int64_t s_units, l_units;
-  int32_t l_tiles, pad;
+  int32_t l_tiles;
+  int32_t s_splits, l_splits;      // entries of the split lists: counted by the attention kernels
 };
 
 constexpr int kLongKeys = 128;               // long path: keys per tile
@@ -60,12 +61,15 @@ __host__ __device__ inline int pair_tiles(int ctx, int n, int pr) {
 // [R][512] unnormalised output, then [R] maxima and [R] sums.
 __host__ __device__ constexpr int64_t partial_floats(int R) { return (int64_t)R * (kDc + 2); }
 
-// Row tiles that several blocks worked on: block x holds the first part.
-struct SplitRec {
-  int32_t rows;           // 0: none starts in block x
-  int32_t last;           // last block with a part
-  int64_t row0;           // first row in the latent output
+// A row tile that several blocks worked on, listed by the block with its first
+// part (in any order: the tiles are merged independently).
+struct __align__(16) SplitRec {
+  int32_t first, last;    // the blocks with its parts
+  int32_t rows;           // rows to write
+  int32_t pad;
+  int64_t row0;           // first row in the output
 };
+static_assert(sizeof(SplitRec) == 32, "an aligned 16-byte load and an 8-byte one");
 
 struct ChunkParams {
   const uint8_t* pool;

@@ -567,10 +567,12 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
         int y = x + 1;
         while (U * (y + 1) / G < end) ++y;
         SplitRec rec;
-        rec.rows = min(kLongRows, wk.s.n - wk.pair * kLongRows);
+        rec.first = x;
         rec.last = y;
+        rec.rows = min(kLongRows, wk.s.n - wk.pair * kLongRows);
+        rec.pad = 0;
         rec.row0 = (int64_t)(wk.s.q0 + wk.pair * kLongRows) * p.H + wk.h;
-        p.l_splits[x] = rec;
+        p.l_splits[atomicAdd(&p.counts->l_splits, 1)] = rec;
       }
     }
     if (!ok) {
@@ -703,41 +705,47 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
   }
 }
 
-// long_combine_kernel: grid (blocks of the attention, 64), block 128: a warp
-// merges one row of the item whose first part block x holds.
+// long_combine_kernel: block 128, the warps stride over the rows of the split
+// items and merge a row's parts in block order.
 __global__ void __launch_bounds__(128) long_combine_kernel(const ChunkParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int x = blockIdx.x, r = 4 * blockIdx.y + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const SplitRec* sr = p.l_splits + x;
-  if (r >= __ldcg(&sr->rows)) return;
-  const int n = __ldcg(&sr->last) - x + 1;
-  const int64_t row0 = __ldcg(&sr->row0);
-  const float* part = p.l_parts + (int64_t)(2 * x + 1) * long_partial_floats();
-  // part 0 is slot 2x + 1, part i > 0 slot 2 (x + i)
-  auto at = [&](int i) { return part + i * 2 * long_partial_floats() - (i ? long_partial_floats() : 0); };
-  float mx = -INFINITY;
-  for (int i = 0; i < n; ++i) mx = fmaxf(mx, __ldcg(at(i) + kLongRows * kDv + r));
-  if (mx == -INFINITY) mx = 0.f;
-  float l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int lane = threadIdx.x & 31, warps = gridDim.x * 4;
+  const int total = __ldcg(&p.counts->l_splits) * kLongRows;
+  for (int w = blockIdx.x * 4 + (threadIdx.x >> 5); w < total; w += warps) {
+    const SplitRec* sr = p.l_splits + w / kLongRows;
+    const int r = w % kLongRows;
+    const int4 rec = __ldcg(reinterpret_cast<const int4*>(sr));
+    const int64_t row0 = __ldcg(&sr->row0);
+    if (r >= rec.z) continue;
+    const int n = rec.y - rec.x + 1;
+    const float* part = p.l_parts + (int64_t)(2 * rec.x + 1) * long_partial_floats();
+    // part 0 is slot 2 first + 1, part i > 0 slot 2 (first + i)
+    auto at = [&](int i) { return part + i * 2 * long_partial_floats() - (i ? long_partial_floats() : 0); };
+    float mx = -INFINITY;
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* s = at(i);
-    const float mi = __ldcg(s + kLongRows * kDv + r), li = __ldcg(s + kLongRows * kDv + kLongRows + r);
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(s + r * kDv) + lane);
-    const float wt = ex2(mi - mx);
-    l = fmaf(wt, li, l);
-    acc.x = fmaf(wt, v.x, acc.x);
-    acc.y = fmaf(wt, v.y, acc.y);
-    acc.z = fmaf(wt, v.z, acc.z);
-    acc.w = fmaf(wt, v.w, acc.w);
+    for (int i = 0; i < n; ++i) mx = fmaxf(mx, __ldcg(at(i) + kLongRows * kDv + r));
+    if (mx == -INFINITY) mx = 0.f;
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float* s = at(i);
+      const float mi = __ldcg(s + kLongRows * kDv + r), li = __ldcg(s + kLongRows * kDv + kLongRows + r);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(s + r * kDv) + lane);
+      const float wt = ex2(mi - mx);
+      l = fmaf(wt, li, l);
+      acc.x = fmaf(wt, v.x, acc.x);
+      acc.y = fmaf(wt, v.y, acc.y);
+      acc.z = fmaf(wt, v.z, acc.z);
+      acc.w = fmaf(wt, v.w, acc.w);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t a, b;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(a) : "f"(acc.y * inv), "f"(acc.x * inv));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(b) : "f"(acc.w * inv), "f"(acc.z * inv));
+    reinterpret_cast<uint2*>(p.o + (row0 + (int64_t)r * p.H) * kDv)[lane] = make_uint2(a, b);
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t a, b;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(a) : "f"(acc.y * inv), "f"(acc.x * inv));
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(b) : "f"(acc.w * inv), "f"(acc.z * inv));
-  reinterpret_cast<uint2*>(p.o + (row0 + (int64_t)r * p.H) * kDv)[lane] = make_uint2(a, b);
 }
 
 template <int LF, int KF>
@@ -785,7 +793,7 @@ mla_status launch_long(const ChunkParams& p, int lf, int kf, cudaStream_t stream
   if (st != MLA_OK) return st;
   st = cuda_status(launch_pdl(long_attention_kernel, dim3(p.grid), dim3(kLaThreads), kLaSmem, stream, p));
   if (st != MLA_OK) return st;
-  return cuda_status(launch_pdl(long_combine_kernel, dim3(p.grid, kLongRows / 4), dim3(128), 0, stream, p));
+  return cuda_status(launch_pdl(long_combine_kernel, dim3(8 * p.grid), dim3(128), 0, stream, p));
 }
 
 }  // namespace mla

@@ -493,10 +493,12 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
         int y = x + 1;
         while (U * (y + 1) / G < end) ++y;
         SplitRec rec;
-        rec.rows = rows;
+        rec.first = x;
         rec.last = y;
+        rec.rows = rows;
+        rec.pad = 0;
         rec.row0 = out0;
-        p.splits[x] = rec;
+        p.splits[atomicAdd(&p.counts->s_splits, 1)] = rec;
       }
       fence_before();                                  // O^T has been read: ordered before the next P's arrival
     }
@@ -654,42 +656,89 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
   }
 }
 
-// short_combine_kernel: grid (blocks of the attention, R), block 128.  Row y
-// of the row tile whose first part block x holds: parts x (slot 2x + 1) and
-// x + 1 .. last (slots 2 (x + i)), merged with the running maxima's weights.
-__global__ void __launch_bounds__(128) short_combine_kernel(const ChunkParams p, int R) {
+// short_combine_kernel: the blocks stride over the rows of the split row
+// tiles.  A row's parts lie in the slots of its blocks, 2 first + 1 and then 2
+// (first + i).  The parts' maxima and sums are read side by side, then the
+// block's four quarters add up every fourth part (a single long context has a
+// part in every block, so the loads have to overlap) and the quarters are
+// added in order.
+constexpr int kCombineThreads = 512;
+constexpr int kCombineParts = 1024;      // most parts per row: blocks of the attention
+
+__global__ void __launch_bounds__(kCombineThreads) short_combine_kernel(const ChunkParams p, int R) {
+  __shared__ float s_w[kCombineParts];
+  __shared__ float s_red[2][kCombineThreads / 32];
+  __shared__ float4 s_acc[3][128];
   pdl_launch_dependents();
   pdl_wait();
-  const int x = blockIdx.x, c = blockIdx.y, tid = threadIdx.x;
-  const SplitRec* sr = p.splits + x;
-  const int rows = __ldcg(&sr->rows);
-  if (c >= rows) return;
-  const int last = __ldcg(&sr->last);
-  const int64_t row0 = __ldcg(&sr->row0);
-  const int64_t stride = 2 * partial_floats(R);
-  const float* part = p.parts + (int64_t)(2 * x + 1) * partial_floats(R);
-  const int n = last - x + 1;
-  // part 0 is slot 2x + 1, part i > 0 slot 2 (x + i): one slot before the regular stride
-  auto at = [&](int i) { return part + i * stride - (i ? partial_floats(R) : 0); };
-  float mx = -INFINITY;
-  for (int i = 0; i < n; ++i) mx = fmaxf(mx, __ldcg(at(i) + R * kDc + c));
-  if (mx == -INFINITY) mx = 0.f;
-  float l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* s = at(i);
-    const float wt = tc::ex2(__ldcg(s + R * kDc + c) - mx);
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(s + (int64_t)c * kDc) + tid);
-    l = fmaf(wt, __ldcg(s + R * kDc + R + c), l);
-    acc.x = fmaf(wt, v.x, acc.x);
-    acc.y = fmaf(wt, v.y, acc.y);
-    acc.z = fmaf(wt, v.z, acc.z);
-    acc.w = fmaf(wt, v.w, acc.w);
+  const int tid = threadIdx.x, quarter = tid >> 7, col = tid & 127;
+  const int total = __ldcg(&p.counts->s_splits) * R;
+  for (int w = blockIdx.x; w < total; w += gridDim.x) {
+    const SplitRec* sr = p.splits + w / R;
+    const int c = w % R;
+    const int4 rec = __ldcg(reinterpret_cast<const int4*>(sr));
+    const int64_t row0 = __ldcg(&sr->row0);
+    if (c >= rec.z) continue;              // the same for the whole block
+    const int64_t stride = 2 * partial_floats(R);
+    const float* part = p.parts + (int64_t)(2 * rec.x + 1) * partial_floats(R);
+    const int n = rec.y - rec.x + 1;
+    // part i > 0 lies one slot before the regular stride
+    auto at = [&](int i) { return part + i * stride - (i ? partial_floats(R) : 0); };
+    float mi[kCombineParts / kCombineThreads], li[kCombineParts / kCombineThreads], mx = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kCombineParts / kCombineThreads; ++k) {
+      const int i = tid + k * kCombineThreads;
+      mi[k] = i < n ? __ldcg(at(i) + R * kDc + c) : -INFINITY;
+      li[k] = i < n ? __ldcg(at(i) + R * kDc + R + c) : 0.f;
+      mx = fmaxf(mx, mi[k]);
+    }
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if ((tid & 31) == 0) s_red[0][tid >> 5] = mx;
+    __syncthreads();
+    mx = s_red[0][0];
+#pragma unroll
+    for (int k = 1; k < kCombineThreads / 32; ++k) mx = fmaxf(mx, s_red[0][k]);
+    if (mx == -INFINITY) mx = 0.f;
+    float l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kCombineParts / kCombineThreads; ++k) {
+      const float wt = tc::ex2(mi[k] - mx);
+      l = fmaf(wt, li[k], l);
+      s_w[tid + k * kCombineThreads] = wt;
+    }
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if ((tid & 31) == 0) s_red[1][tid >> 5] = l;
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = quarter; i < n; i += 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(at(i) + (int64_t)c * kDc) + col);
+      const float wt = s_w[i];
+      acc.x = fmaf(wt, v.x, acc.x);
+      acc.y = fmaf(wt, v.y, acc.y);
+      acc.z = fmaf(wt, v.z, acc.z);
+      acc.w = fmaf(wt, v.w, acc.w);
+    }
+    if (quarter) s_acc[quarter - 1][col] = acc;
+    __syncthreads();
+    if (!quarter) {
+      l = 0.f;
+#pragma unroll
+      for (int k = 0; k < kCombineThreads / 32; ++k) l += s_red[1][k];
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const float4 a = s_acc[k][col];
+        acc.x += a.x;
+        acc.y += a.y;
+        acc.z += a.z;
+        acc.w += a.w;
+      }
+      reinterpret_cast<uint2*>(p.o_lat + (row0 + c) * kDc)[col] =
+          make_uint2(tc::half2_bits(acc.x * inv, acc.y * inv), tc::half2_bits(acc.z * inv, acc.w * inv));
+    }
+    __syncthreads();                       // s_acc and s_red have been read
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  reinterpret_cast<uint2*>(p.o_lat + (row0 + c) * kDc)[tid] =
-      make_uint2(tc::half2_bits(acc.x * inv, acc.y * inv), tc::half2_bits(acc.z * inv, acc.w * inv));
 }
 
 template <int LF, int KF, int R>
@@ -706,7 +755,7 @@ mla_status launch_r(const ChunkParams& p, cudaStream_t stream) {
   const mla_status st = cuda_status(launch_pdl(short_attention_kernel<LF, KF, R>, dim3(p.grid), dim3(kSThreads),
                                                Shape<LF, KF, R>::kBytes, stream, p));
   if (st != MLA_OK) return st;
-  return cuda_status(launch_pdl(short_combine_kernel, dim3(p.grid, R), dim3(128), 0, stream, p, R));
+  return cuda_status(launch_pdl(short_combine_kernel, dim3(4 * p.grid), dim3(kCombineThreads), 0, stream, p, R));
 }
 
 template <int LF, int KF>
