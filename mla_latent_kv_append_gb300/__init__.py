@@ -397,7 +397,11 @@ def mla_rope(q_pe, k_pe, positions, inv_freq, q_out, k_out, pair_axis=None, inte
     kp = ko = None
     ks = kos = (0,)
     if k_pe is not None:
-        ks, kos = _rows(k_pe[:, None], (n, 1, ROPE_DIM), "k_pe"), _rows(k_out[:, None], (n, 1, ROPE_DIM), "k_out")
+        ks, kos = k_pe.stride(), k_out.stride()
+        for t, s in ((k_pe, ks), (k_out, kos)):
+            if t.dtype is not torch.bfloat16 or t.shape != (n, ROPE_DIM) or not t.is_cuda or s[1] != 1:
+                raise ValueError("k_pe, k_out: expected CUDA bfloat16 %s with contiguous rows, got %s %s" % (
+                    (n, ROPE_DIM), t.dtype, tuple(t.shape)))
         kp, ko = k_pe.data_ptr(), k_out.data_ptr()
     if pair_axis is not None:
         pair_axis = bytes(pair_axis)

@@ -255,7 +255,10 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
           if (warp == 0 && lane == 0) tile_ok[g] = n_tok >= 0;
           if (!fine) atomicOr(bad + 2 * g + half, 1u << lane);
         }
+        // with two buffers a piece's successor is not waiting for it: one fence for both
+        if (NB == 2 && i == 0) continue;
         fence_async_smem();
+        if (NB == 2 && i == 1) bar_arrive(bars + 8 * (bWritten + 5 * kb + s0));
         bar_arrive(bars + 8 * (bWritten + 5 * kb + s));
       }
       if (!ok) break;

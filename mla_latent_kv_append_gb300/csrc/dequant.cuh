@@ -102,8 +102,9 @@ __device__ __forceinline__ void zero_unit(RawUnit<FMT, KPE>& r) {
 
 // The unit's 32 channels as fp16 pairs, h[i] = channels (2i, 2i + 1); false if
 // one of them is not finite in fp16 (its group, or the unit, then reads as 0).
+// Any scale and zero-point.
 template <int FMT, bool KPE>
-__device__ __forceinline__ bool convert_unit(const RawUnit<FMT, KPE>& r, uint32_t* h) {
+__device__ __forceinline__ bool convert_any(const RawUnit<FMT, KPE>& r, uint32_t* h) {
   using S = UnitShape<FMT, KPE>;
   bool fine = true;
   if constexpr (FMT == MLA_FMT_BF16) {
@@ -180,6 +181,80 @@ __device__ __forceinline__ bool convert_unit(const RawUnit<FMT, KPE>& r, uint32_
     }
   }
   return fine;
+}
+
+// The same, two channels at a time in fp16 arithmetic where that loses
+// nothing: codes become exact half integers by placing them in the mantissa of
+// 1024, subtracting the offset and zero-point is exact, and the scale is split
+// into two halves, s = hi + lo, so that q hi + q lo is rounded once (the lo
+// product's own rounding is 2^-22).  11 issue slots for four INT8 codes
+// against 16 of convert_any (byte selects, logic and conversions run at half
+// rate).  Needs scales within fp16's normal range with room for lo, or zero,
+// and small zero-points: other units take convert_any.
+template <int FMT, bool KPE>
+__device__ __forceinline__ bool convert_unit(const RawUnit<FMT, KPE>& r, uint32_t* h) {
+  using S = UnitShape<FMT, KPE>;
+  if constexpr (FMT == MLA_FMT_BF16) {
+    return convert_any<FMT, KPE>(r, h);
+  } else {
+    constexpr uint32_t kLow = 0x39000000u, kHigh = S::kInt4 ? 0x42800000u : 0x44000000u;     // 2^-13 .. 64 or 512
+    bool fast = true;
+#pragma unroll
+    for (int g = 0; g < S::kScales; ++g) {
+      fast &= __float_as_uint(r.s[g]) - kLow <= kHigh - kLow || r.s[g] == 0.f;
+      if constexpr (S::kZeros) fast &= fabsf(r.z[g]) <= 512.f;
+    }
+    if (!fast) return convert_any<FMT, KPE>(r, h);
+    __half2 hi[S::kScales], lo[S::kScales];
+#pragma unroll
+    for (int g = 0; g < S::kScales; ++g) {
+      hi[g] = __float2half2_rn(r.s[g]);
+      lo[g] = __float2half2_rn(r.s[g] - __low2float(hi[g]));
+    }
+    auto put = [&](int ch, __half2 q, int g) {
+      const __half2 x = __hfma2(q, hi[g], __hmul2(q, lo[g]));
+      h[ch / 2] = *reinterpret_cast<const uint32_t*>(&x);
+    };
+    auto half2_of = [](uint32_t w) { return *reinterpret_cast<const __half2*>(&w); };
+    if constexpr (S::kInt4) {
+      __half2 off[S::kScales], off16[S::kScales];          // -(1024 + zero), -(64 + zero): exact
+#pragma unroll
+      for (int g = 0; g < S::kScales; ++g) {
+        const float zero = S::kZeros ? r.z[S::kZeros ? g : 0] : 8.f;
+        off[g] = __float2half2_rn(-1024.f - zero);
+        off16[g] = __float2half2_rn(-64.f - zero);
+      }
+      const __half2 sixteenth = __float2half2_rn(0.0625f);
+      const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // nibbles k and k + 4 are adjacent channels; odd ones stand 16 times as high
+          const uint32_t t = k < 2 ? w[j] : w[j] >> 8;
+          const int ch = int4_nibble_channel(j, k), g = ch / S::kGroup;
+          put(ch, (k & 1) ? __hfma2(half2_of((t & 0x00F000F0u) | 0x64006400u), sixteenth, off16[g])
+                          : __hadd2(half2_of((t & 0x000F000Fu) | 0x64006400u), off[g]),
+              g);
+        }
+    } else {
+      const __half2 off = __float2half2_rn(-1152.f);       // 1024 and the codes' bias of 128
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t w[4] = {r.w[i].x ^ 0x80808080u, r.w[i].y ^ 0x80808080u, r.w[i].z ^ 0x80808080u,
+                               r.w[i].w ^ 0x80808080u};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            const int ch = 16 * i + (!KPE && S::kGroup == 8 ? 2 * j + 4 * k : 4 * j + k);
+            put(ch, __hadd2(half2_of(__byte_perm(w[j], 0x64646464u, k ? 0x4342 : 0x4140)), off),
+                S::kScales > 1 ? ch / S::kGroup : 0);
+          }
+      }
+    }
+    return true;
+  }
 }
 
 // INT8_OUTLIER: puts the protected channels of unit c in their places; false
