@@ -18,12 +18,13 @@
 // 64-row tiles the shared-memory traffic of the MMAs' operands.  Cached bytes
 // come as bulk copies of whole 32-token blocks into a ring of shared-memory
 // slots (loads through L1 could not keep enough lines in flight next to 200
-// KB of shared memory: 4.7 bytes per cycle and SM); eight warps dequantize
-// them, lane = token, into the fp16 key tile.  A key tile is handed on in four
-// 128-channel pieces (and the RoPE block): the S^T MMAs of a piece start when
-// it is written, and the O^T MMAs release it piece by piece, so that a single
-// key buffer overlaps the conversion with both products; 16-row tiles of
-// quantized formats have room for two buffers.
+// KB of shared memory: 4.7 bytes per cycle and SM); sixteen warps dequantize
+// them, lane = token, into fp16.  The key tile is handed on in four pieces of
+// 128 channels, from a ring of 4 to 8 pieces, and the RoPE block: the S^T MMAs
+// of a piece start when it is written, and the O^T MMAs release it.  The
+// shared memory beside the queries is shared out by format: three raw blocks
+// where they fit (the memory's latency wants 40 KB and more under way), the
+// rest pieces, so that the next tile is converted while this one is used.
 //
 // Warps: 0..15 dequantize, 16..19 softmax, 20 and 21 issue the S^T and the O^T
 // MMAs (apart, so that neither waits for the other's operands), 22 issues the
@@ -62,23 +63,25 @@ struct Regs {
                 "the warpgroups' shares come out of the launch's registers");
 };
 constexpr int kKeyBlk = kKeyTile * 128;              // one 64-key x 64-channel fp16 block: 8 KB
-constexpr int kKeyBuf = kQBlocks * kKeyBlk;          // 72 KB
 constexpr float kSlack = 8.f;                        // the running maximum rises only past this (P <= 2^8 in fp16)
 constexpr int kMaxSmem = 232448 - 1024;              // a block's shared memory, less the alignment slack
-constexpr int kMaxSlots = 4;
+constexpr int kMaxSlots = 3;
+
+constexpr int kPiece = 2 * kKeyBlk;                  // 128 channels of a key tile: 16 KB
+constexpr int kMaxPieces = 8;
 
 template <int LF, int KF, int R>
 struct Shape {
-  // two key buffers only where two raw blocks still fit beside them
   static constexpr int kBlock = block_bytes<LF, KF>();
-  static constexpr int kFixed = kQBlocks * R * 128 + R * 128 + 4 * R * 4 + 512;        // Q, P, reduction, barriers
-  static constexpr int kNB = kMaxSmem - 2 * kKeyBuf - kFixed >= 2 * kBlock ? 2 : 1;
-  static constexpr int kRoom = (kMaxSmem - kNB * kKeyBuf - kFixed) / kBlock;
-  // even: a slot always holds the same half of a tile, so that the warps that
-  // wait for it see every phase of its barrier (a parity wait cannot skip one)
-  static constexpr int kSlots = kRoom < kMaxSlots ? kRoom / 2 * 2 : kMaxSlots;
-  static_assert(kSlots >= 2 && kSlots % 2 == 0, "one block under way while the other is read");
-  static constexpr int kQ = kNB * kKeyBuf;
+  static constexpr int kRoom = kMaxSmem - (kQBlocks * R * 128 + R * 128 + 4 * R * 4 + 512);      // beside Q, P, reduction, barriers
+  static constexpr int kRopes = kRoom - 4 * kPiece - 2 * kKeyBlk >= 2 * kBlock ? 2 : 1;
+  static constexpr int kKeys = kRoom - kRopes * kKeyBlk;                                        // for pieces and raw blocks
+  static constexpr int kSlots = kKeys - 4 * kPiece >= 3 * kBlock ? 3 : 2;
+  static constexpr int kFit = (kKeys - kSlots * kBlock) / kPiece;
+  static constexpr int kPieces = kFit < kMaxPieces ? kFit : kMaxPieces;
+  static_assert(kPieces >= 4, "a whole key tile");
+  static constexpr int kRope = kPieces * kPiece;
+  static constexpr int kQ = kRope + kRopes * kKeyBlk;
   static constexpr int kP = kQ + kQBlocks * R * 128;
   static constexpr int kRed = kP + R * 128;          // [4 warps][R] maxima, then sums
   static constexpr int kRaw = kRed + 4 * R * 4;      // 256-byte aligned for R >= 16
@@ -86,11 +89,11 @@ struct Shape {
   static constexpr int kBytes = kBars + 512 + 1024;  // barriers and words; alignment slack
 };
 
-// Barriers: per key buffer and piece (4 x 128 channels, 4: the RoPE block)
-// "written" and "free"; S^T and P per score buffer; raw slots.
-enum { bWritten = 0, bFree = bWritten + 10, bS = bFree + 10, bP = bS + 2, bRaw = bP + 2, bRawFree = bRaw + kMaxSlots,
-       bQ = bRawFree + kMaxSlots, bFinS, bFinO, bCount };
-static_assert(8 * bCount + 16 + 16 + 4 * 2 * kMaxSlots <= 512, "barriers and words");
+// Barriers: per piece of the ring, and per RoPE block, "written" and "free";
+// S^T and P per score buffer; O^T of a tile done; raw slots.
+enum { bWritten = 0, bFree = bWritten + kMaxPieces, bRopeW = bFree + kMaxPieces, bRopeF = bRopeW + 2, bS = bRopeF + 2,
+       bP = bS + 2, bO = bP + 2, bRaw, bRawFree = bRaw + kMaxSlots, bQ = bRawFree + kMaxSlots, bFinS, bFinO, bCount };
+static_assert(8 * bCount + 32 + 4 * kMaxSlots <= 512, "barriers and words");
 
 // One run's walk over the units: segments (a row tile, key tiles t0 .. t1).
 struct Walk {
@@ -145,9 +148,10 @@ struct Walk {
   }
 };
 
-// A unit's 32 fp16 channels into their block, swizzled.
-__device__ __forceinline__ void put_unit(const uint32_t* h, uint32_t buf, int tok, int unit) {
-  const uint32_t row = buf + (unit >> 1) * kKeyBlk + tok * 128, flip = (4 * (unit & 1) ^ (tok & 7)) << 4;
+// A unit's 32 fp16 channels into a 64-channel block (half: its first or second
+// 32 channels), swizzled.
+__device__ __forceinline__ void put_unit(const uint32_t* h, uint32_t blk, int tok, int half) {
+  const uint32_t row = blk + tok * 128, flip = (4 * half ^ (tok & 7)) << 4;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(row + (flip ^ (i << 4))), "r"(h[4 * i]),
@@ -158,7 +162,7 @@ __device__ __forceinline__ void put_unit(const uint32_t* h, uint32_t buf, int to
 template <int LF, int KF, int R>
 __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const ChunkParams p) {
   using SH = Shape<LF, KF, R>;
-  constexpr int NB = SH::kNB, NS = SH::kSlots;
+  constexpr int NP = SH::kPieces, NR = SH::kRopes, NS = SH::kSlots;
   extern __shared__ uint8_t short_smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(short_smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sb = smem_u32(sm), bars = sb + SH::kBars;
@@ -172,17 +176,20 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
   constexpr int kCols = R == 64 ? 512 : 8 * R;       // 6 R columns used, a power of two allocated
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 10; ++i) {
-      bar_init(bars + 8 * (bWritten + i), i % 5 == 4 ? 128 : 256);
+    for (int i = 0; i < kMaxPieces; ++i) {
+      bar_init(bars + 8 * (bWritten + i), 128);        // four warps write a piece
       bar_init(bars + 8 * (bFree + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
+      bar_init(bars + 8 * (bRopeW + i), 128);          // and four the RoPE block
+      bar_init(bars + 8 * (bRopeF + i), 1);
       bar_init(bars + 8 * (bS + i), 1);
       bar_init(bars + 8 * (bP + i), 128);
     }
+    bar_init(bars + 8 * bO, 1);
     for (int i = 0; i < kMaxSlots; ++i) {
       bar_init(bars + 8 * (bRaw + i), 1);
-      bar_init(bars + 8 * (bRawFree + i), 256);
+      bar_init(bars + 8 * (bRawFree + i), 512);
     }
     bar_init(bars + 8 * bQ, 1);
     bar_init(bars + 8 * bFinS, 1);
@@ -208,60 +215,78 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
   bool ok = true;
   if (warp < 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(Regs<R>::kConvert));
-    // ---- dequantize.  Warps 0..7: the tile's first block, 8..15: the second.
-    // Of each eight, warp w takes unit w % 4 of pieces w / 4 and w / 4 + 2;
-    // warps 6 and 7 the RoPE units too; lane = token.
-    const int half = warp >> 3, q = warp & 3, s0 = (warp >> 2) & 1, tok = 32 * half + lane;
-    const bool rope = s0 == 1 && q >= 2;
+    // ---- dequantize.  Warp w takes unit w (32 channels, half a block of piece
+    // w / 4) of both 32-token blocks of a tile; warps 12..15 also the RoPE
+    // block's unit w % 2 of block w / 2 % 2; lane = token.
+    const int s = warp >> 2, rope_half = (warp >> 1) & 1;
+    const bool rope = warp >= 12;
     const uint32_t n_tiles = (uint32_t)(hi - lo);      // none in a block without work
+    uint32_t piece = s, round = 0;                     // the ring's piece for this tile, and how often it went round
     for (uint32_t it = 0; it < n_tiles; ++it) {
-      const uint32_t blk = 2 * it + half, slot = blk % NS, g = it & 1, kb = it % NB, ph = it / NB;
-      if (!warp_wait(bars + 8 * (bRaw + slot), (blk / NS) & 1, p.wait_ns, abort)) {
+      const uint32_t g = it & 1;
+      uint32_t h[2][16];
+      RawUnit<KF, true> rk;
+      uint32_t bad_bits = 0;                           // of this lane's two tokens: bits 0 and 1
+      int n_tok = 0;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t blk = 2 * it + half, slot = blk % NS;
+        if (ok && !warp_wait(bars + 8 * (bRaw + slot), (blk / NS) & 1, p.wait_ns, abort)) ok = false;
+        if (!ok) break;
+        const uint8_t* raw = sm + SH::kRaw + slot * SH::kBlock;
+        n_tok = slot_len[slot];
+        const bool live = lane < n_tok;
+        RawUnit<LF, false> r;
+        if (live) load_unit<LF, false>(raw, p.L, lane, warp, r);
+        else zero_unit(r);
+        if (rope && half == rope_half) {
+          if (live) load_unit<KF, true>(raw, p.L, lane, warp & 1, rk);
+          else zero_unit(rk);
+        }
+        if (LF != MLA_FMT_INT8_OUTLIER) bar_arrive(bars + 8 * (bRawFree + slot));      // read: the next copy may come
+        bool fine = convert_unit<LF, false>(r, h[half]);
+        if constexpr (LF == MLA_FMT_INT8_OUTLIER) {    // the protected channels lie in the slot
+          if (live) fine &= patch_outliers<LF>(raw, p.L, p.outl, lane, warp, h[half]);
+          bar_arrive(bars + 8 * (bRawFree + slot));
+        }
+        if (!fine) bad_bits |= 1u << half;
+      }
+      if (!ok) break;
+      // The piece's last holder has gone.  Releases come in the ring's order,
+      // so the barrier is at most one phase behind: the parity cannot mislead.
+      if (round > 0 && !warp_wait(bars + 8 * (bFree + piece), (round - 1) & 1, p.wait_ns, abort)) {
         ok = false;
         break;
       }
-      const uint8_t* raw = sm + SH::kRaw + slot * SH::kBlock;
-      const int n_tok = slot_len[slot];
-      // both units are converted before the wait for room in the key buffer
-      uint32_t h[2][16];
-      RawUnit<KF, true> rk;
-      bool fine = true;
-      if (rope) {
-        if (lane < n_tok) load_unit<KF, true>(raw, p.L, lane, q - 2, rk);
-        else zero_unit(rk);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        RawUnit<LF, false> r;
-        if (lane < n_tok) load_unit<LF, false>(raw, p.L, lane, 4 * s0 + 8 * i + q, r);
-        else zero_unit(r);
-        fine &= convert_unit<LF, false>(r, h[i]);
-        if (lane < n_tok) fine &= patch_outliers<LF>(raw, p.L, p.outl, lane, 4 * s0 + 8 * i + q, h[i]);
-      }
-      bar_arrive(bars + 8 * (bRawFree + slot));
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        if (i == 2 && !rope) break;
-        const int s = i == 2 ? 4 : s0 + 2 * i;           // the piece
-        if (i == 2) fine &= convert_unit<KF, true>(rk, h[0]);
-        // the piece of the tile NB before is free
-        if (it >= NB && !warp_wait(bars + 8 * (bFree + 5 * kb + s), (ph - 1) & 1, p.wait_ns, abort)) {
+      const uint32_t blk_at = sb + piece * kPiece + ((warp >> 1) & 1) * kKeyBlk;
+      put_unit(h[0], blk_at, lane, warp & 1);
+      put_unit(h[1], blk_at, 32 + lane, warp & 1);
+      if (bad_bits & 1) atomicOr(bad + 2 * g, 1u << lane);
+      if (bad_bits & 2) atomicOr(bad + 2 * g + 1, 1u << lane);
+      if (!rope) {
+        fence_async_smem();
+        bar_arrive(bars + 8 * (bWritten + piece));
+      } else {
+        const bool fine = convert_unit<KF, true>(rk, h[0]);
+        fence_async_smem();
+        bar_arrive(bars + 8 * (bWritten + piece));
+        const uint32_t kb = it % NR;
+        if (it >= NR && !warp_wait(bars + 8 * (bRopeF + kb), (it / NR - 1) & 1, p.wait_ns, abort)) {
           ok = false;
           break;
         }
-        put_unit(h[i & 1], sb + kb * kKeyBuf, tok, i < 2 ? 4 * s + q : kLatentUnits + q - 2);
-        if (i == (rope ? 2 : 1)) {
-          // the last piece this warp writes: its tokens' flags go with it
-          if (warp == 0 && lane == 0) tile_ok[g] = n_tok >= 0;
-          if (!fine) atomicOr(bad + 2 * g + half, 1u << lane);
-        }
-        // with two buffers a piece's successor is not waiting for it: one fence for both
-        if (NB == 2 && i == 0) continue;
+        put_unit(h[0], sb + SH::kRope + kb * kKeyBlk, 32 * rope_half + lane, warp & 1);
+        // with the last barrier before S^T: the tile's flags
+        if (!fine) atomicOr(bad + 2 * g + rope_half, 1u << lane);
+        if (warp == 12 && lane == 0) tile_ok[g] = n_tok >= 0;
         fence_async_smem();
-        if (NB == 2 && i == 1) bar_arrive(bars + 8 * (bWritten + 5 * kb + s0));
-        bar_arrive(bars + 8 * (bWritten + 5 * kb + s));
+        bar_arrive(bars + 8 * (bRopeW + kb));
       }
-      if (!ok) break;
+      piece += 4;
+      if (piece >= NP) {
+        piece -= NP;
+        ++round;
+      }
     }
     if (!ok) {
       set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
@@ -372,7 +397,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
           }
         }
         // the O^T of the tile before is complete: P is free, and O^T may be rescaled
-        if (it >= 1 && !warp_wait(bars + 8 * (bFree + 5 * ((it - 1) % NB) + 3), ((it - 1) / NB) & 1, p.wait_ns, abort)) {
+        if (it >= 1 && !warp_wait(bars + 8 * bO, (it - 1) & 1, p.wait_ns, abort)) {
           ok = false;
           break;
         }
@@ -448,7 +473,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
         l[2 * j] = a.x;
         l[2 * j + 1] = a.y;
       }
-      if (!warp_wait(bars + 8 * (bFree + 5 * ((it - 1) % NB) + 3), ((it - 1) / NB) & 1, p.wait_ns, abort)) {
+      if (!warp_wait(bars + 8 * bO, (it - 1) & 1, p.wait_ns, abort)) {
         ok = false;
         break;
       }
@@ -523,8 +548,9 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
       if (elect_one()) {
         constexpr uint32_t kId = f16_idesc(64, R, false, false);
         constexpr int kQBytes = kQBlocks * R * 128;
-        const uint64_t d_q = sw128_desc(sb + SH::kQ, 16, 1024), d_k = sw128_desc(sb, 16, 1024);
-        uint32_t it = 0, seg = 0;
+        const uint64_t d_q = sw128_desc(sb + SH::kQ, 16, 1024), d_k = sw128_desc(sb, 16, 1024),
+                       d_r = sw128_desc(sb + SH::kRope, 16, 1024);
+        uint32_t it = 0, seg = 0, piece = 0, round = 0;
         while (ok && wk.next()) {
           // the query tile: its readers, the S^T MMAs of the segment before, are done
           if (seg > 0 && !bar_wait(bars + 8 * (bS + ((it - 1) & 1)), ((it - 1) >> 1) & 1, p.wait_ns, abort)) {
@@ -539,27 +565,33 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
             break;
           }
           for (int t = wk.t0; t < wk.t1 && ok; ++t, ++it) {
-            const uint32_t g = it & 1, kb = it % NB, ph = (it / NB) & 1;
-            // the softmax has read this S^T buffer's last tile
-            if (it >= 2 && !bar_wait(bars + 8 * (bP + g), ((it - 2) >> 1) & 1, p.wait_ns, abort)) {
+            const uint32_t g = it & 1, kb = it % NR, d = t_s + g * R;
+          // the softmax has read this S^T buffer's last tile
+          if (it >= 2 && !bar_wait(bars + 8 * (bP + g), ((it - 2) >> 1) & 1, p.wait_ns, abort)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            if (!bar_wait(bars + 8 * (bWritten + piece), round & 1, p.wait_ns, abort)) {
               ok = false;
               break;
             }
-            const uint64_t a = d_k + (uint64_t)(kb * (kKeyBuf >> 4));
-            const uint32_t d = t_s + g * R;
-  #pragma unroll
-            for (int s = 0; s < 5; ++s) {
-              if (!bar_wait(bars + 8 * (bWritten + 5 * kb + s), ph, p.wait_ns, abort)) {
-                ok = false;
-                break;
-              }
-              fence_after();
-              umma4<2, 2>(d, a + (2 * s * kKeyBlk >> 4), d_q + (2 * s * R * 128 >> 4), kId, s != 0);
-              if (s < 4) umma4<2, 2>(d, a + ((2 * s + 1) * kKeyBlk >> 4), d_q + ((2 * s + 1) * R * 128 >> 4), kId, 1u);
+            fence_after();
+            const uint64_t a = d_k + (uint64_t)(piece * (kPiece >> 4));
+            umma4<2, 2>(d, a, d_q + (2 * s * R * 128 >> 4), kId, s != 0);
+            umma4<2, 2>(d, a + (kKeyBlk >> 4), d_q + ((2 * s + 1) * R * 128 >> 4), kId, 1u);
+            if (++piece == NP) {
+              piece = 0;
+              ++round;
             }
-            if (!ok) break;
-            umma_commit(bars + 8 * (bFree + 5 * kb + 4));     // the RoPE block is read here only
-            umma_commit(bars + 8 * (bS + g));
+          }
+          if (ok && !bar_wait(bars + 8 * (bRopeW + kb), (it / NR) & 1, p.wait_ns, abort)) ok = false;
+          if (!ok) break;
+          fence_after();
+          umma4<2, 2>(d, d_r + (uint64_t)(kb * (kKeyBlk >> 4)), d_q + (8 * R * 128 >> 4), kId, 1u);
+          umma_commit(bars + 8 * (bRopeF + kb));           // read here only
+          umma_commit(bars + 8 * (bS + g));
           }
         }
         if (!ok) {
@@ -579,21 +611,22 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
       if (elect_one()) {
         constexpr uint32_t kId = f16_idesc(128, R, true, false);
         const uint64_t d_p = sw128_desc(sb + SH::kP, 16, 1024), d_v = sw128_desc(sb, kKeyBlk, 1024);
-        uint32_t it = 0;
+        uint32_t it = 0, piece = 0;
         while (ok && wk.next()) {
           for (int t = wk.t0; t < wk.t1; ++t, ++it) {
-            const uint32_t g = it & 1, kb = it % NB;
+            const uint32_t g = it & 1;
             if (!bar_wait(bars + 8 * (bP + g), (it >> 1) & 1, p.wait_ns, abort)) {
               ok = false;
               break;
             }
             fence_after();
-            const uint64_t a = d_v + (uint64_t)(kb * (kKeyBuf >> 4));
-  #pragma unroll
+#pragma unroll
             for (int s = 0; s < 4; ++s) {
-              umma4<(2048 >> 4), 2>(tbase + s * R, a + (2 * s * kKeyBlk >> 4), d_p, kId, t > wk.t0);
-              umma_commit(bars + 8 * (bFree + 5 * kb + s));
+              umma4<(2048 >> 4), 2>(tbase + s * R, d_v + (uint64_t)(piece * (kPiece >> 4)), d_p, kId, t > wk.t0);
+              umma_commit(bars + 8 * (bFree + piece));
+              if (++piece == NP) piece = 0;
             }
+            umma_commit(bars + 8 * bO);
           }
         }
         if (!ok) {
