@@ -35,12 +35,25 @@ __device__ __forceinline__ uint64_t now_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
+// The same, suspended for up to `ns` until the phase completes.
+__device__ __forceinline__ bool bar_test_for(uint32_t bar, uint32_t parity, uint32_t ns) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(ns)
+      : "memory");
+  return done != 0;
+}
 // Waits for the phase of `bar` with this parity.  Gives up (false) once
 // limit_ns have passed or another role of the block has given up (*abort).
+// The thread is suspended between polls, 20 us at most: a polling loop would
+// take issue slots from the block's working warps.
 __device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* abort) {
   const uint64_t t0 = now_ns();
+  const uint32_t nap = limit_ns < 20000 ? (uint32_t)limit_ns : 20000u;
   for (;;) {
-    if (bar_test(bar, parity)) return true;
+    if (bar_test_for(bar, parity, nap)) return true;
     if (*abort || now_ns() - t0 >= limit_ns) return false;
   }
 }
