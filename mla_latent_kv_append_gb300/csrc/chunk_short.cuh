@@ -216,14 +216,15 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
   if (warp < 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(Regs<R>::kConvert));
     // ---- dequantize.  Warp w takes unit w (32 channels, half a block of piece
-    // w / 4) of both 32-token blocks of a tile; warps 12..15 also the RoPE
-    // block's unit w % 2 of block w / 2 % 2; lane = token.
+    // w / 4) of both 32-token blocks of a tile; every fourth tile also the RoPE
+    // block's unit w % 2 of block w / 2 % 2 (the four warps of a piece in turn:
+    // always the same ones were a third slower than the rest); lane = token.
     const int s = warp >> 2, rope_half = (warp >> 1) & 1;
-    const bool rope = warp >= 12;
     const uint32_t n_tiles = (uint32_t)(hi - lo);      // none in a block without work
     uint32_t piece = s, round = 0;                     // the ring's piece for this tile, and how often it went round
     for (uint32_t it = 0; it < n_tiles; ++it) {
       const uint32_t g = it & 1;
+      const bool rope = (int)(it & 3) == s;
       uint32_t h[2][16];
       RawUnit<KF, true> rk;
       uint32_t bad_bits = 0;                           // of this lane's two tokens: bits 0 and 1
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
         put_unit(h[0], sb + SH::kRope + kb * kKeyBlk, 32 * rope_half + lane, warp & 1);
         // with the last barrier before S^T: the tile's flags
         if (!fine) atomicOr(bad + 2 * g + rope_half, 1u << lane);
-        if (warp == 12 && lane == 0) tile_ok[g] = n_tok >= 0;
+        if ((warp & 3) == 0 && lane == 0) tile_ok[g] = n_tok >= 0;
         fence_async_smem();
         bar_arrive(bars + 8 * (bRopeW + kb));
       }
