@@ -26,9 +26,9 @@
 // where they fit (the memory's latency wants 40 KB and more under way), the
 // rest pieces, so that the next tile is converted while this one is used.
 //
-// Warps: 0..15 dequantize, 16..19 softmax, 20 and 21 issue the S^T and the O^T
-// MMAs (apart, so that neither waits for the other's operands), 22 issues the
-// copies.
+// Warps: 16 dequantize, 4 or 8 softmax (one group per 32 rows), then one each
+// issues the S^T MMAs, the O^T MMAs (apart, so that neither waits for the
+// other's operands) and the copies.
 //
 // Work split: all (row tile, key tile) units of the call, in order, are cut
 // into equal runs, one per SM, so ragged lengths need no care.  A row tile
@@ -51,15 +51,16 @@ namespace {
 
 using namespace tc;
 
-constexpr int kSThreads = 24 * 32;
-// Registers: 768 threads launch with 80 each (61,440); then the warps' roles
-// take their shares of that.
-constexpr int kRegsLaunch = 80;
+// Warps: 16 convert, 4 per softmax group (32 rows each), 4 issue.  Registers:
+// the block launches with kLaunch a thread, then the roles take their shares.
 template <int R>
-struct Regs {
-  static constexpr int kConvert = R == 64 ? 64 : 72, kSoftmax = R == 64 ? 160 : 104, kIssue = R == 64 ? 64 : 88;
-  static_assert(512 * kConvert + 128 * kSoftmax + 128 * kIssue <= kSThreads * kRegsLaunch &&
-                    kSThreads * kRegsLaunch <= 65536 && kSThreads * (kRegsLaunch + 8) > 65536,
+struct Roles {
+  static constexpr int kGroups = R == 64 ? 2 : 1, kGroupRows = R / kGroups;
+  static constexpr int kSoftmax = 16, kIssue = 16 + 4 * kGroups, kWarps = kIssue + 4, kThreads = 32 * kWarps;
+  static constexpr int kLaunch = R == 64 ? 72 : 80;
+  static constexpr int kRegsConvert = R == 64 ? 64 : 72, kRegsSoftmax = R == 64 ? 96 : 104, kRegsIssue = R == 64 ? 56 : 88;
+  static_assert(512 * kRegsConvert + 128 * kGroups * kRegsSoftmax + 128 * kRegsIssue <= kThreads * kLaunch &&
+                    kThreads * kLaunch <= 65536 && kThreads * (kLaunch + 8) > 65536,
                 "the warpgroups' shares come out of the launch's registers");
 };
 constexpr int kKeyBlk = kKeyTile * 128;              // one 64-key x 64-channel fp16 block: 8 KB
@@ -93,7 +94,7 @@ struct Shape {
 // S^T and P per score buffer; O^T of a tile done; raw slots.
 enum { bWritten = 0, bFree = bWritten + kMaxPieces, bRopeW = bFree + kMaxPieces, bRopeF = bRopeW + 2, bS = bRopeF + 2,
        bP = bS + 2, bO = bP + 2, bRaw, bRawFree = bRaw + kMaxSlots, bQ = bRawFree + kMaxSlots, bFinS, bFinO, bCount };
-static_assert(8 * bCount + 32 + 4 * kMaxSlots <= 512, "barriers and words");
+static_assert(8 * bCount + 72 + 4 * kMaxSlots <= 512, "barriers and words");
 
 // One run's walk over the units: segments (a row tile, key tiles t0 .. t1).
 struct Walk {
@@ -160,8 +161,9 @@ __device__ __forceinline__ void put_unit(const uint32_t* h, uint32_t blk, int to
 }
 
 template <int LF, int KF, int R>
-__global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(const ChunkParams p) {
   using SH = Shape<LF, KF, R>;
+  using RO = Roles<R>;
   constexpr int NP = SH::kPieces, NR = SH::kRopes, NS = SH::kSlots;
   extern __shared__ uint8_t short_smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(short_smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -169,9 +171,10 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
   uint8_t* words = sm + SH::kBars + 8 * bCount;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words);
   volatile int* abort = reinterpret_cast<volatile int*>(words + 4);
-  volatile int* tile_ok = reinterpret_cast<volatile int*>(words + 8);        // [2], by tile parity
-  uint32_t* bad = reinterpret_cast<uint32_t*>(words + 16);                   // [2][2]: a bit per token
-  volatile int* slot_len = reinterpret_cast<volatile int*>(words + 32);      // [slots] tokens of the block, -1: no page
+  volatile int* quit = reinterpret_cast<volatile int*>(words + 8);           // [groups][2, by tile parity]
+  volatile int* tile_ok = reinterpret_cast<volatile int*>(words + 24);       // [4, by tile]
+  uint32_t* bad = reinterpret_cast<uint32_t*>(words + 40);                   // [4, by tile][2]: a bit per token
+  volatile int* slot_len = reinterpret_cast<volatile int*>(words + 72);      // [slots] tokens of the block, -1: no page
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kCols = R == 64 ? 512 : 8 * R;       // 6 R columns used, a power of two allocated
 
@@ -184,7 +187,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
       bar_init(bars + 8 * (bRopeW + i), 128);          // and four the RoPE block
       bar_init(bars + 8 * (bRopeF + i), 1);
       bar_init(bars + 8 * (bS + i), 1);
-      bar_init(bars + 8 * (bP + i), 128);
+      bar_init(bars + 8 * (bP + i), 128 * RO::kGroups);
     }
     bar_init(bars + 8 * bO, 1);
     for (int i = 0; i < kMaxSlots; ++i) {
@@ -195,10 +198,11 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
     bar_init(bars + 8 * bFinS, 1);
     bar_init(bars + 8 * bFinO, 1);
     *abort = 0;
-    for (int i = 0; i < 4; ++i) bad[i] = 0;
+    for (int i = 0; i < 4; ++i) quit[i] = 0;
+    for (int i = 0; i < 8; ++i) bad[i] = 0;
     bar_init_fence();
   }
-  if (warp == 20) tmem_alloc(smem_u32(tmem_slot), kCols);
+  if (warp == RO::kIssue) tmem_alloc(smem_u32(tmem_slot), kCols);
   fence_before();
   __syncthreads();
   fence_after();
@@ -214,7 +218,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
   const int64_t lo = work ? U * x / G : 0, hi = work ? U * (x + 1) / G : 0;
   bool ok = true;
   if (warp < 16) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(Regs<R>::kConvert));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(RO::kRegsConvert));
     // ---- dequantize.  Warp w takes unit w (32 channels, half a block of piece
     // w / 4) of both 32-token blocks of a tile; every fourth tile also the RoPE
     // block's unit w % 2 of block w / 2 % 2 (the four warps of a piece in turn:
@@ -223,7 +227,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
     const uint32_t n_tiles = (uint32_t)(hi - lo);      // none in a block without work
     uint32_t piece = s, round = 0;                     // the ring's piece for this tile, and how often it went round
     for (uint32_t it = 0; it < n_tiles; ++it) {
-      const uint32_t g = it & 1;
+      const uint32_t f = it & 3;                       // the tile's flags
       const bool rope = (int)(it & 3) == s;
       uint32_t h[2][16];
       RawUnit<KF, true> rk;
@@ -262,8 +266,8 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
       const uint32_t blk_at = sb + piece * kPiece + ((warp >> 1) & 1) * kKeyBlk;
       put_unit(h[0], blk_at, lane, warp & 1);
       put_unit(h[1], blk_at, 32 + lane, warp & 1);
-      if (bad_bits & 1) atomicOr(bad + 2 * g, 1u << lane);
-      if (bad_bits & 2) atomicOr(bad + 2 * g + 1, 1u << lane);
+      if (bad_bits & 1) atomicOr(bad + 2 * f, 1u << lane);
+      if (bad_bits & 2) atomicOr(bad + 2 * f + 1, 1u << lane);
       if (!rope) {
         fence_async_smem();
         bar_arrive(bars + 8 * (bWritten + piece));
@@ -278,8 +282,8 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
         }
         put_unit(h[0], sb + SH::kRope + kb * kKeyBlk, 32 * rope_half + lane, warp & 1);
         // with the last barrier before S^T: the tile's flags
-        if (!fine) atomicOr(bad + 2 * g + rope_half, 1u << lane);
-        if ((warp & 3) == 0 && lane == 0) tile_ok[g] = n_tok >= 0;
+        if (!fine) atomicOr(bad + 2 * f + rope_half, 1u << lane);
+        if ((warp & 3) == 0 && lane == 0) tile_ok[f] = n_tok >= 0;
         fence_async_smem();
         bar_arrive(bars + 8 * (bRopeW + kb));
       }
@@ -293,20 +297,23 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
       set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
       *abort = 1;
     }
-  } else if (warp < 20) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(Regs<R>::kSoftmax));
+  } else if (warp < RO::kIssue) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(RO::kRegsSoftmax));
     Walk wk;
     wk.n_seqs = __ldcg(&p.counts->s_seqs);
-    // ---- softmax.  Thread (w, lane) holds keys 16 w + lane / 4 and + 8 of
-    // the tile, rows 8 j + 2 (lane % 4) and the next (j < R / 8).
+    // ---- softmax.  A group of four warps has kGroupRows rows of the tile.
+    // Thread (w, lane) holds keys 16 w + lane / 4 and + 8, rows 8 j + 2 (lane %
+    // 4) and the next (j < J) of the group.  The group votes once per tile, so
+    // its warps leave together: one that gave up a wait says so before a vote.
     if (work) wk.start(p, lo, hi);
-    const int w = warp & 3;
+    constexpr int GR = RO::kGroupRows, J = GR / 8;
+    const int w = warp & 3, gq = (warp - RO::kSoftmax) >> 2, bar_id = 1 + gq;
     const uint32_t tl = (uint32_t)(32 * w) << 16;
-    constexpr int J = R / 8;
-    float* red = reinterpret_cast<float*>(sm + SH::kRed);
+    float* red = reinterpret_cast<float*>(sm + SH::kRed) + gq * 4 * GR;
     uint32_t it = 0;
+    bool late = false;                     // this warp gave up a wait since the last vote
     while (work && ok && wk.next()) {
-      const int row0 = wk.item * R, rows = min(R, wk.s.n * p.H - row0);
+      const int row0 = wk.item * R + gq * GR, rows = min(GR, wk.s.n * p.H - row0);       // rows <= 0: padding alone
       const int ctx = wk.s.len - wk.s.n;
       const int pos_min = ctx + row0 / p.H;          // the earliest row's position
       float m[2 * J], l[2 * J];
@@ -316,57 +323,67 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
         l[i] = 0.f;
       }
       for (int t = wk.t0; t < wk.t1; ++t, ++it) {
-        const uint32_t g = it & 1;
-        if (!warp_wait(bars + 8 * (bS + g), (it >> 1) & 1, p.wait_ns, abort)) {
+        const uint32_t g = it & 1, f = it & 3;
+        if (late || !warp_wait(bars + 8 * (bS + g), (it >> 1) & 1, p.wait_ns, abort)) quit[2 * gq + g] = 1;
+        __syncwarp();
+        fence_after();
+        const bool page_ok = tile_ok[f] != 0;
+        const uint32_t bad_lo = *(volatile uint32_t*)(bad + 2 * f), bad_hi = *(volatile uint32_t*)(bad + 2 * f + 1);
+        const bool masked = !page_ok || t * kKeyTile + kKeyTile - 1 > pos_min || (bad_lo | bad_hi);
+        float v[4 * J];
+        // the tile's scores, masked: hidden keys -inf, non-finite ones NaN, the
+        // padding's rows (whose queries hold anything) 0
+        auto load_scores = [&]() {
+          uint32_t r[4 * J];
+          tmem_load_16x256b<J>(t_s + g * R + gq * GR + tl, r);
+#pragma unroll
+          for (int i = 0; i < 4 * J; ++i) v[i] = __uint_as_float(r[i]);
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = 16 * w + (lane >> 2) + 8 * e, kp = t * kKeyTile + key;
+              const bool is_bad = ((key < 32 ? bad_lo : bad_hi) >> (key & 31)) & 1u;
+#pragma unroll
+              for (int i = 0; i < 2 * J; ++i) {
+                const int c = 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
+                const bool sees = page_ok && kp <= ctx + (row0 + c) / p.H;
+                float& s = v[4 * (i >> 1) + 2 * e + (i & 1)];
+                s = sees ? (is_bad ? NAN : s) : -INFINITY;
+              }
+            }
+          }
+          if (rows < GR) {
+#pragma unroll
+            for (int i = 0; i < 2 * J; ++i)
+              if (8 * (i >> 1) + 2 * (lane & 3) + (i & 1) >= rows) v[4 * (i >> 1) + (i & 1)] = v[4 * (i >> 1) + 2 + (i & 1)] = 0.f;
+          }
+        };
+        load_scores();
+        // Scores relative to their rows' running maxima.  Does one pass the
+        // slack?  The maxima themselves are needed only then (the first tile of
+        // a segment, and seldom after it).
+        float over = -INFINITY;            // NaN from a NaN score or a row that has seen nothing yet
+#pragma unroll
+        for (int i = 0; i < 2 * J; ++i) {
+          float &a = v[4 * (i >> 1) + (i & 1)], &b = v[4 * (i >> 1) + 2 + (i & 1)];
+          a -= m[i];
+          b -= m[i];
+          over = max_nan(over, max_nan(a, b));
+        }
+        uint32_t any;
+        asm volatile(
+            "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n"
+            " selp.u32 %0, 1, 0, q;\n}\n"
+            : "=r"(any)
+            : "r"((uint32_t)!(over <= kSlack)), "r"(bar_id)
+            : "memory");
+        if (quit[2 * gq + g]) {
           ok = false;
           break;
         }
-        fence_after();
-        float v[4 * J];
-        {
-          uint32_t r[4 * J];
-          tmem_load_16x256b<J>(t_s + g * R + tl, r);
-#pragma unroll
-          for (int i = 0; i < 4 * J; ++i) v[i] = __uint_as_float(r[i]);
-        }
-        const bool page_ok = tile_ok[g] != 0;
-        const uint32_t bad_lo = *(volatile uint32_t*)(bad + 2 * g), bad_hi = *(volatile uint32_t*)(bad + 2 * g + 1);
-        if (!page_ok || t * kKeyTile + kKeyTile - 1 > pos_min || (bad_lo | bad_hi)) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int key = 16 * w + (lane >> 2) + 8 * e, kp = t * kKeyTile + key;
-            const bool is_bad = ((key < 32 ? bad_lo : bad_hi) >> (key & 31)) & 1u;
-#pragma unroll
-            for (int i = 0; i < 2 * J; ++i) {
-              const int c = 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
-              const bool sees = page_ok && kp <= ctx + (row0 + c) / p.H;
-              float& s = v[4 * (i >> 1) + 2 * e + (i & 1)];
-              s = sees ? (is_bad ? NAN : s) : -INFINITY;
-            }
-          }
-        }
-        if (rows < R) {                    // the padding's query rows hold anything: their scores count as 0
-#pragma unroll
-          for (int i = 0; i < 2 * J; ++i)
-            if (8 * (i >> 1) + 2 * (lane & 3) + (i & 1) >= rows) v[4 * (i >> 1) + (i & 1)] = v[4 * (i >> 1) + 2 + (i & 1)] = 0.f;
-        }
-        // Does a score pass its row's running maximum by more than the slack?
-        // One vote of the four warps; the maxima themselves are needed only
-        // then (the first tile of a segment, and seldom after it).
-        float over = -INFINITY;            // NaN from a NaN score or a row that has seen nothing yet
-#pragma unroll
-        for (int i = 0; i < 2 * J; ++i)
-          over = max_nan(over, max_nan(v[4 * (i >> 1) + (i & 1)] - m[i], v[4 * (i >> 1) + 2 + (i & 1)] - m[i]));
-        uint32_t any;
-        asm volatile(
-            "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n"
-            " selp.u32 %0, 1, 0, q;\n}\n"
-            : "=r"(any)
-            : "r"((uint32_t)!(over <= kSlack))
-            : "memory");
-        if ((bad_lo | bad_hi) && threadIdx.x == 16 * 32) bad[2 * g] = bad[2 * g + 1] = 0;    // all four warps have read them
         float alpha[2 * J];
         if (any) {
+          load_scores();
 #pragma unroll
           for (int j = 0; j < J; ++j) {
             float a = fmaxf(v[4 * j], v[4 * j + 2]), b = fmaxf(v[4 * j + 1], v[4 * j + 3]);
@@ -375,15 +392,15 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
               a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
               b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
             }
-            if (lane < 4) *reinterpret_cast<float2*>(red + w * R + 8 * j + 2 * lane) = make_float2(a, b);
+            if (lane < 4) *reinterpret_cast<float2*>(red + w * GR + 8 * j + 2 * lane) = make_float2(a, b);
           }
-          asm volatile("bar.sync 1, 128;\n" ::: "memory");
+          asm volatile("bar.sync %0, 128;\n" ::"r"(bar_id) : "memory");
 #pragma unroll
           for (int j = 0; j < J; ++j) {
             float2 a = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const float2 b = *reinterpret_cast<const float2*>(red + q * R + 8 * j + 2 * (lane & 3));
+              const float2 b = *reinterpret_cast<const float2*>(red + q * GR + 8 * j + 2 * (lane & 3));
               a.x = fmaxf(a.x, b.x);
               a.y = fmaxf(a.y, b.y);
             }
@@ -394,13 +411,22 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
               const bool raise = top > m[i] + kSlack;      // from -inf: the first key seen
               alpha[i] = raise ? ex2(m[i] - top) : 1.f;
               if (raise) m[i] = top;
+              // a row that has seen nothing yet keeps m = -inf: its weights are 0
+              const float base = m[i] == -INFINITY ? 0.f : m[i];
+              v[4 * j + e] -= base;
+              v[4 * j + 2 + e] -= base;
             }
           }
         }
-        // the O^T of the tile before is complete: P is free, and O^T may be rescaled
-        if (it >= 1 && !warp_wait(bars + 8 * bO, (it - 1) & 1, p.wait_ns, abort)) {
-          ok = false;
-          break;
+        // the O^T of the tile before is complete: P is free, O^T may be
+        // rescaled, and every group has read that tile's flags
+        if (it >= 1) {
+          if (!warp_wait(bars + 8 * bO, (it - 1) & 1, p.wait_ns, abort)) {
+            late = true;
+            continue;
+          }
+          const uint32_t before = (it - 1) & 3;
+          if (threadIdx.x == 32 * RO::kSoftmax) bad[2 * before] = bad[2 * before + 1] = 0;
         }
         if (any) {
 #pragma unroll
@@ -408,7 +434,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
           if (t > wk.t0) {
             fence_after();
 #pragma unroll
-            for (int c0 = 0; c0 < R; c0 += 16) {
+            for (int c0 = 0; c0 < GR; c0 += 16) {
               float al[16];
 #pragma unroll
               for (int c = 0; c < 16; ++c)
@@ -416,10 +442,10 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
 #pragma unroll 1
               for (int blk = 0; blk < 4; ++blk) {
                 uint32_t r[16];
-                tmem_load16(tbase + blk * R + c0 + tl, r);
+                tmem_load16(tbase + blk * R + gq * GR + c0 + tl, r);
 #pragma unroll
                 for (int c = 0; c < 16; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * al[c]);
-                tmem_store16(tbase + blk * R + c0 + tl, r);
+                tmem_store16(tbase + blk * R + gq * GR + c0 + tl, r);
               }
             }
           }
@@ -431,16 +457,13 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int i = j + e;
-            // a row that has seen nothing yet keeps m = -inf: its weights are 0
-            const float m0 = m[2 * i] == -INFINITY ? 0.f : m[2 * i], m1 = m[2 * i + 1] == -INFINITY ? 0.f : m[2 * i + 1];
-            const float p0 = ex2(v[4 * i] - m0), p1 = ex2(v[4 * i + 1] - m1);
-            const float p2 = ex2(v[4 * i + 2] - m0), p3 = ex2(v[4 * i + 3] - m1);
+            const float p0 = ex2(v[4 * i]), p1 = ex2(v[4 * i + 1]), p2 = ex2(v[4 * i + 2]), p3 = ex2(v[4 * i + 3]);
             l[2 * i] += p0 + p2;
             l[2 * i + 1] += p1 + p3;
             h[2 * e] = half2_bits(p0, p1);
             h[2 * e + 1] = half2_bits(p2, p3);
           }
-          const int mat = lane >> 3, rr = 8 * (j + (mat >> 1)) + (lane & 7), oct = 2 * w + (mat & 1);
+          const int mat = lane >> 3, rr = gq * GR + 8 * (j + (mat >> 1)) + (lane & 7), oct = 2 * w + (mat & 1);
           stmatrix_x4_trans(sb + SH::kP + rr * 128 + ((oct ^ (rr & 7)) << 4), h[0], h[1], h[2], h[3]);
         }
         fence_async_smem();
@@ -455,36 +478,37 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 8);
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 16);
       }
-      asm volatile("bar.sync 1, 128;\n" ::: "memory");         // the last maxima have been read
+      asm volatile("bar.sync %0, 128;\n" ::"r"(bar_id) : "memory");         // the last maxima have been read
       if (lane < 4) {
 #pragma unroll
         for (int j = 0; j < J; ++j)
-          *reinterpret_cast<float2*>(red + w * R + 8 * j + 2 * lane) = make_float2(l[2 * j], l[2 * j + 1]);
+          *reinterpret_cast<float2*>(red + w * GR + 8 * j + 2 * lane) = make_float2(l[2 * j], l[2 * j + 1]);
       }
-      asm volatile("bar.sync 1, 128;\n" ::: "memory");
+      asm volatile("bar.sync %0, 128;\n" ::"r"(bar_id) : "memory");
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         float2 a = make_float2(0.f, 0.f);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float2 b = *reinterpret_cast<const float2*>(red + q * R + 8 * j + 2 * (lane & 3));
+          const float2 b = *reinterpret_cast<const float2*>(red + q * GR + 8 * j + 2 * (lane & 3));
           a.x += b.x;
           a.y += b.y;
         }
         l[2 * j] = a.x;
         l[2 * j + 1] = a.y;
       }
-      if (!warp_wait(bars + 8 * bO, (it - 1) & 1, p.wait_ns, abort)) {
-        ok = false;
-        break;
+      asm volatile("bar.sync %0, 128;\n" ::"r"(bar_id) : "memory");         // the sums have been read: the next maxima may come
+      if (late || !warp_wait(bars + 8 * bO, (it - 1) & 1, p.wait_ns, abort)) {
+        late = true;                       // leaves at the next vote, or with the run
+        continue;
       }
       fence_after();
       const bool whole = wk.first && wk.last;
       const int slot = 2 * x + (wk.first ? 1 : 0);
-      float* part = p.parts + (int64_t)slot * partial_floats(R);
+      float* part = p.parts + (int64_t)slot * partial_floats(R) + (int64_t)gq * GR * kDc;
       const int64_t out0 = (int64_t)wk.s.tok0 * p.H + row0;
 #pragma unroll
-      for (int c0 = 0; c0 < R; c0 += 16) {
+      for (int c0 = 0; c0 < GR; c0 += 16) {
         float inv[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
@@ -494,7 +518,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
 #pragma unroll 1
         for (int blk = 0; blk < 4; ++blk) {
           uint32_t r[16];
-          tmem_load16(tbase + blk * R + c0 + tl, r);
+          tmem_load16(tbase + blk * R + gq * GR + c0 + tl, r);
           const int ch = 128 * blk + 32 * w + lane;
           if (whole) {
 #pragma unroll
@@ -509,14 +533,15 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
         }
       }
       if (!whole && w == 0 && lane < 4) {
+        float* ml = p.parts + (int64_t)slot * partial_floats(R) + R * kDc + gq * GR;
 #pragma unroll
         for (int i = 0; i < 2 * J; ++i) {
           const int c = 8 * (i >> 1) + 2 * lane + (i & 1);
-          part[R * kDc + c] = m[i];
-          part[R * kDc + R + c] = l[i];
+          ml[c] = m[i];
+          ml[R + c] = l[i];
         }
       }
-      if (wk.first && !wk.last && w == 0 && lane == 0) {
+      if (wk.first && !wk.last && warp == RO::kSoftmax && lane == 0) {
         // the row tile goes on in the blocks behind: up to the one that holds its last unit
         const int64_t end = wk.s.unit0 + (int64_t)(wk.item + 1) * wk.s.tiles;
         int y = x + 1;
@@ -524,24 +549,24 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
         SplitRec rec;
         rec.first = x;
         rec.last = y;
-        rec.rows = rows;
+        rec.rows = min(R, wk.s.n * p.H - wk.item * R);
         rec.pad = 0;
         rec.row0 = out0;
         p.splits[atomicAdd(&p.counts->s_splits, 1)] = rec;
       }
       fence_before();                                  // O^T has been read: ordered before the next P's arrival
     }
-    if (!ok) {
+    if (!ok || late) {
       set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
       *abort = 1;
     }
   } else {
-    if constexpr (Regs<R>::kIssue > kRegsLaunch) {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(Regs<R>::kIssue));
+    if constexpr (RO::kRegsIssue > RO::kLaunch) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(RO::kRegsIssue));
     } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(Regs<R>::kIssue));
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(RO::kRegsIssue));
     }
-    if (work && warp == 20) {
+    if (work && warp == RO::kIssue) {
       // ---- one thread: the query tiles' copies and the S^T MMAs
       Walk wk;
       wk.n_seqs = __ldcg(&p.counts->s_seqs);
@@ -604,7 +629,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
         drain_wait(bars + 8 * bFinS, 0);
       }
       __syncwarp();
-    } else if (work && warp == 21) {
+    } else if (work && warp == RO::kIssue + 1) {
       // ---- one thread: the O^T MMAs
       Walk wk;
       wk.n_seqs = __ldcg(&p.counts->s_seqs);
@@ -638,7 +663,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
         drain_wait(bars + 8 * bFinO, 0);
       }
       __syncwarp();
-    } else if (work && warp == 22) {
+    } else if (work && warp == RO::kIssue + 2) {
       // ---- the cache's blocks into the raw slots.  The lanes fetch 32
       // page ids of the segment at a time, lane 0 issues.
       Walk wk;
@@ -687,7 +712,7 @@ __global__ void __launch_bounds__(kSThreads, 1) short_attention_kernel(const Chu
   }
   fence_before();
   __syncthreads();
-  if (warp == 20) {
+  if (warp == RO::kIssue) {
     fence_after();
     tmem_free(tbase, kCols);
   }
@@ -789,7 +814,7 @@ mla_status launch_r(const ChunkParams& p, cudaStream_t stream) {
     if (st != MLA_OK) return st;
     if (dev >= 0 && dev < 64) configured[dev] = 1;
   }
-  const mla_status st = cuda_status(launch_pdl(short_attention_kernel<LF, KF, R>, dim3(p.grid), dim3(kSThreads),
+  const mla_status st = cuda_status(launch_pdl(short_attention_kernel<LF, KF, R>, dim3(p.grid), dim3(Roles<R>::kThreads),
                                                Shape<LF, KF, R>::kBytes, stream, p));
   if (st != MLA_OK) return st;
   return cuda_status(launch_pdl(short_combine_kernel, dim3(4 * p.grid), dim3(kCombineThreads), 0, stream, p, R));

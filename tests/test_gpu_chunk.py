@@ -424,6 +424,25 @@ def test_agrees_with_the_decode_call(mla):
         assert ((o[b].float() - o2[b]).abs().cpu() <= bound[0].float() + lat.cpu()).all()
 
 
+@pytest.mark.parametrize("lens", [[(900, 1)] * 5, [(300, 6), (20, 3)], [(700, 200)]], ids=["decode", "draft", "chunk"])
+def test_waits_that_run_out_end_the_call(mla, lens):
+    """With a wait limit of 0 the kernels give up, flag it and return; the
+    next call, with the limit back, is whole."""
+    t = Batch(mla, lens, 32)
+    prev = mla.mla_set_wait_limit_ns(0)
+    try:
+        t.call()
+        torch.cuda.synchronize()
+    finally:
+        mla.mla_set_wait_limit_ns(prev)
+    assert t.err.item() == mla.DEVERR_TIMEOUT
+    t.err.zero_()
+    o = t.call()
+    torch.cuda.synchronize()
+    assert t.err.item() == 0
+    t.check(o, heads=slice(30, 32))
+
+
 def test_a_serving_step(mla):
     """plan -> rope -> append -> chunk attention over three steps of a small
     server (prefill chunks, then mixed, then decode), against the plain
