@@ -420,52 +420,65 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
     LongWalk wk;
     if (work) wk.start(p, lo, hi);
     uint32_t it = 0;                       // this tile's key tiles so far
-    while (work && ok && wk.next(p.H)) {
-      if (i == 1 && !wk.two) continue;
-      const int t1 = i == 0 ? min(wk.t1, wk.tiles0) : wk.t1;
-      if (wk.t0 >= t1) {                   // the run begins behind the first tile's last key: an empty partial
-        float* part = p.l_parts + (int64_t)(2 * x + (wk.first ? 1 : 0)) * long_partial_floats();
+    // Moves to the next segment that this query tile takes part in and hands
+    // over its query rows as fp16, swizzled (padding rows are 0); false at the
+    // run's end.  A warp loads its own 32 rows, eight lanes to a row.
+    auto enter = [&]() -> bool {
+      for (;;) {
+        if (!wk.next(p.H)) return false;
+        if (i == 1 && !wk.two) continue;
+        if (i == 0 && wk.t0 >= wk.tiles0) {            // the run begins behind the first tile's last key: an empty partial
+          float* part = p.l_parts + (int64_t)(2 * x + (wk.first ? 1 : 0)) * long_partial_floats();
 #pragma unroll 4
-        for (int c = 0; c < kDv / 4; ++c) reinterpret_cast<float4*>(part + row * kDv)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-        part[kLongRows * kDv + row] = -INFINITY;
-        part[kLongRows * kDv + kLongRows + row] = 0.f;
-        continue;
+          for (int c = 0; c < kDv / 4; ++c) reinterpret_cast<float4*>(part + row * kDv)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+          part[kLongRows * kDv + row] = -INFINITY;
+          part[kLongRows * kDv + kLongRows + row] = 0.f;
+          continue;
+        }
+        break;
       }
+      const int tok0 = wk.pair * kLongRows + 128 * i, piece = lane & 7;
+      const uint16_t* qn = p.qn + wk.h * p.qn_head + 8 * piece;
+      const uint16_t* qp = p.qp + wk.h * p.qp_head + 8 * piece;
+      uint8_t* q = sm + i * 3 * kBlkBytes;
+#pragma unroll 4
+      for (int e = 0; e < 8; ++e) {
+        const int r = 32 * (warp & 3) + 4 * e + (lane >> 3);
+        const bool real = tok0 + r < wk.s.n;
+        const int64_t tok = wk.s.q0 + (real ? tok0 + r : 0);
+        uint4 v[3] = {__ldcg(reinterpret_cast<const uint4*>(qn + tok * p.qn_tok)),
+                      __ldcg(reinterpret_cast<const uint4*>(qn + tok * p.qn_tok + 64)),
+                      __ldcg(reinterpret_cast<const uint4*>(qp + tok * p.qp_tok))};
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+          if (!real) v[c] = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(q + c * kBlkBytes + r * 128 + ((piece ^ (r & 7)) << 4)) =
+              make_uint4(half2_bits(bf16lo(v[c].x), bf16hi(v[c].x)), half2_bits(bf16lo(v[c].y), bf16hi(v[c].y)),
+                         half2_bits(bf16lo(v[c].z), bf16hi(v[c].z)), half2_bits(bf16lo(v[c].w), bf16hi(v[c].w)));
+        }
+      }
+      fence_async_smem();
+      bar_arrive(bars + 8 * (aQ + i));
+      return true;
+    };
+    bool more = work && enter();
+    while (more) {
+      const int t0 = wk.t0, t1 = i == 0 ? min(wk.t1, wk.tiles0) : wk.t1;
       const int tok0 = wk.pair * kLongRows + 128 * i, ctx = wk.s.len - wk.s.n;
       const bool live = tok0 + row < wk.s.n;
-      // the query rows: this thread's row as fp16, swizzled (padding rows are 0)
-      {
-        const int64_t tok = wk.s.q0 + (live ? tok0 + row : 0);
-        const uint4* qn = reinterpret_cast<const uint4*>(p.qn + tok * p.qn_tok + wk.h * p.qn_head);
-        const uint4* qp = reinterpret_cast<const uint4*>(p.qp + tok * p.qp_tok + wk.h * p.qp_head);
-        uint8_t* q = sm + i * 3 * kBlkBytes + row * 128;
-#pragma unroll 8
-        for (int c = 0; c < 24; ++c) {
-          uint4 v = __ldcg(c < 16 ? qn + c : qp + (c - 16));
-          if (!live) v = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(q + (c >> 3) * kBlkBytes + (((c & 7) ^ (row & 7)) << 4)) =
-              make_uint4(half2_bits(bf16lo(v.x), bf16hi(v.x)), half2_bits(bf16lo(v.y), bf16hi(v.y)),
-                         half2_bits(bf16lo(v.z), bf16hi(v.z)), half2_bits(bf16lo(v.w), bf16hi(v.w)));
-        }
-        fence_async_smem();
-        bar_arrive(bars + 8 * (aQ + i));
-      }
       const int qpos = ctx + tok0 + (live ? row : 0);
       const uint4* flags = reinterpret_cast<const uint4*>(p.kflags) + 2 * (int64_t)wk.s.kv0;
       float m = -INFINITY, l = 0.f;
-      uint4 f_bad = __ldcg(flags + 2 * wk.t0), f_out = __ldcg(flags + 2 * wk.t0 + 1);
-      for (int t = wk.t0; t < t1; ++t, ++it) {
+      uint4 f_bad = __ldcg(flags + 2 * t0), f_out = __ldcg(flags + 2 * t0 + 1);
+      for (int t = t0; t < t1; ++t, ++it) {
         const uint4 bad4 = f_bad, out4 = f_out;
         if (t + 1 < t1) {                  // fetched a tile ahead
           f_bad = __ldcg(flags + 2 * t + 2);
           f_out = __ldcg(flags + 2 * t + 3);
         }
-        if (!warp_wait(bars + 8 * (aS + i), it & 1, p.wait_ns, abort)) {
-          ok = false;
-          break;
-        }
-        // the O_i of the tile before (complete by now: its MMAs were issued first)
-        if (t > wk.t0 && !warp_wait(bars + 8 * (aO + i), (it - 1) & 1, p.wait_ns, abort)) {
+        // S_i is complete, and the O_i of the tile before (its MMAs were issued first)
+        if (!warp_wait(bars + 8 * (aS + i), it & 1, p.wait_ns, abort) ||
+            (t > t0 && !warp_wait(bars + 8 * (aO + i), (it - 1) & 1, p.wait_ns, abort))) {
           ok = false;
           break;
         }
@@ -474,25 +487,32 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_load32(t_s + 32 * c, s + 32 * c);
         const uint32_t any_flag = bad4.x | bad4.y | bad4.z | bad4.w | out4.x | out4.y | out4.z | out4.w;
-        if ((t + 1) * kLongKeys - 1 > ctx + tok0 || any_flag) {
+        const int seen = qpos - t * kLongKeys;         // keys 0 .. seen of the tile are visible
+        if (any_flag) {
           const uint32_t fb[4] = {bad4.x, bad4.y, bad4.z, bad4.w}, fo[4] = {out4.x, out4.y, out4.z, out4.w};
-          const int seen = qpos - t * kLongKeys;       // keys 0 .. seen of the tile are visible
 #pragma unroll
           for (int c = 0; c < 128; ++c) {
             const bool hid = c > seen || ((fo[c >> 5] >> (c & 31)) & 1u);
             const bool nan = (fb[c >> 5] >> (c & 31)) & 1u;
             s[c] = hid ? 0xFF800000u : (nan ? 0x7FC00000u : s[c]);
           }
-        }
-        float mx = -INFINITY;
+        } else if ((t + 1) * kLongKeys - 1 > ctx + tok0) {
 #pragma unroll
-        for (int c = 0; c < 128; ++c) mx = fmaxf(mx, __uint_as_float(s[c]));
+          for (int c = 0; c < 128; ++c) s[c] = c > seen ? 0xFF800000u : s[c];
+        }
+        float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 128; c += 4) {
+          mx = max3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+          my = max3(my, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+        }
+        mx = fmaxf(mx, my);
         const bool raise = (mx - m) * sc > kSlack;     // from -inf: the first key seen
         if (__any_sync(0xffffffffu, raise)) {
           const float alpha = raise ? ex2((m - mx) * sc) : 1.f;
           if (raise) m = mx;
           l *= alpha;
-          if (t > wk.t0) {
+          if (t > t0) {
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
               uint32_t o[16];
@@ -504,74 +524,83 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
           }
         }
         const float ms = m == -INFINITY ? 0.f : -m * sc;
-        float l0 = 0.f, l1 = 0.f;
+        const uint64_t sc2 = pack2(sc, sc), ms2 = pack2(ms, ms);
+        uint64_t la = pack2(0.f, 0.f), lb = la;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t pw[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float a = ex2(fmaf(__uint_as_float(s[64 * c + 2 * e]), sc, ms));
-            const float b = ex2(fmaf(__uint_as_float(s[64 * c + 2 * e + 1]), sc, ms));
-            l0 += a;
-            l1 += b;
+            float a, b;
+            unpack2(fma2(pack2(__uint_as_float(s[64 * c + 2 * e]), __uint_as_float(s[64 * c + 2 * e + 1])), sc2, ms2), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            uint64_t& acc = (e & 1) ? lb : la;
+            acc = add2(acc, pack2(a, b));
             pw[e] = half2_bits(a, b);
           }
           tmem_store32(t_s + 32 * c, pw);
         }
+        float l0, l1;
+        unpack2(add2(la, lb), l0, l1);
         l += l0 + l1;
         fence_before();
         bar_arrive(bars + 8 * (aP + i));
       }
       if (!ok) break;
+      // this segment's epilogue needs its place; the next one's query rows go
+      // out first (the last S_i has read the old ones), so that its scores are
+      // computed meanwhile
+      const bool whole = wk.first && wk.last, opens = wk.first && !wk.last;       // whole: this block saw every key
+      const int64_t out_row = (int64_t)(wk.s.q0 + tok0 + row) * p.H + wk.h;
+      float* part = p.l_parts + (int64_t)(2 * x + (wk.first ? 1 : 0)) * long_partial_floats();
+      const int64_t end = wk.u - (wk.t1 - wk.t0) + pair_tiles(ctx, wk.s.n, wk.pair);
+      SplitRec rec;
+      rec.rows = min(kLongRows, wk.s.n - wk.pair * kLongRows);
+      rec.row0 = (int64_t)(wk.s.q0 + wk.pair * kLongRows) * p.H + wk.h;
+      more = enter();
       if (!warp_wait(bars + 8 * (aO + i), (it - 1) & 1, p.wait_ns, abort)) {
         ok = false;
         break;
       }
       fence_after();
-      // whole: this block saw every key of the item
-      const bool whole = wk.first && wk.last;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int64_t out_row = (int64_t)(wk.s.q0 + tok0 + row) * p.H + wk.h;
-      float* part = p.l_parts + (int64_t)(2 * x + (wk.first ? 1 : 0)) * long_partial_floats();
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
         tmem_load32(t_o + 32 * c, o);
-        if (!live) continue;
-        if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(p.o + out_row * kDv + 32 * c);
+        if (live) {
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(p.o + out_row * kDv + 32 * c);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n"
-                  : "=r"(w[q])
-                  : "f"(__uint_as_float(o[8 * e + 2 * q + 1]) * inv), "f"(__uint_as_float(o[8 * e + 2 * q]) * inv));
-            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int q = 0; q < 4; ++q)
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n"
+                    : "=r"(w[q])
+                    : "f"(__uint_as_float(o[8 * e + 2 * q + 1]) * inv), "f"(__uint_as_float(o[8 * e + 2 * q]) * inv));
+              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(part + (128 * i + row) * kDv + 32 * c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(part + (128 * i + row) * kDv + 32 * c);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
+        __syncwarp();
       }
-      __syncwarp();
       if (!whole && live) {
         part[kLongRows * kDv + 128 * i + row] = m * sc;
         part[kLongRows * kDv + kLongRows + 128 * i + row] = l;
       }
       fence_before();
-      if (wk.first && !wk.last && i == 0 && row == 0) {
-        const int64_t end = wk.u - (wk.t1 - wk.t0) + pair_tiles(ctx, wk.s.n, wk.pair);
+      if (opens && i == 0 && row == 0) {
         int y = x + 1;
         while (U * (y + 1) / G < end) ++y;
-        SplitRec rec;
         rec.first = x;
         rec.last = y;
-        rec.rows = min(kLongRows, wk.s.n - wk.pair * kLongRows);
         rec.pad = 0;
-        rec.row0 = (int64_t)(wk.s.q0 + wk.pair * kLongRows) * p.H + wk.h;
         p.l_splits[atomicAdd(&p.counts->l_splits, 1)] = rec;
       }
     }
@@ -624,13 +653,16 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
           if (!bar_wait(bars + 8 * (aFull + (first + c) % kRing), ((first + c) / kRing) & 1, p.wait_ns, abort)) return false;
         return true;
       };
-      auto scores = [&](int i, uint32_t at) {              // S_i = Q_i K^T, K in blocks at, at + 1, at + 2
-        fence_after();
+      auto scores = [&](int i, uint32_t at) -> bool {      // S_i = Q_i K^T, K in blocks at, at + 1, at + 2
 #pragma unroll
-        for (int c = 0; c < 3; ++c)
+        for (int c = 0; c < 3; ++c) {
+          if (!wait_slots(at + c, 1)) return false;        // the second tile finds them there
+          fence_after();
           umma4<2, 2>(tbase + 128 * i, d_q + (uint64_t)((i * 3 + c) * (kBlkBytes >> 4)),
                       d_k + (uint64_t)(((at + c) % kRing) * (kBlkBytes >> 4)), kIdS, c != 0);
+        }
         umma_commit(bars + 8 * (aS + i));
+        return true;
       };
       auto outputs = [&](int i, uint32_t at, uint32_t acc) {   // O_i += P_i V, V in blocks at, at + 1
         fence_after();
@@ -661,9 +693,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
           if (!bar_wait(bars + 8 * (aQ + 1), nq[1] & 1, p.wait_ns, abort)) { ok = false; break; }
           ++nq[1];
         }
-        if (!wait_slots(n, 3)) { ok = false; break; }
-        if (zero) scores(0, n);
-        if (wk.two) scores(1, n);
+        if ((zero && !scores(0, n)) || (wk.two && !scores(1, n))) { ok = false; break; }
         release(n, 3);
         for (int j = 0; j < tiles; ++j, n += 5) {
           const int t = wk.t0 + j;
@@ -674,8 +704,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
             ++np[0];
             outputs(0, n + 3, j > 0);
           }
-          if (more && !wait_slots(n + 5, 3)) { ok = false; break; }
-          if (more && t + 1 < end0) scores(0, n + 5);
+          if (more && t + 1 < end0 && !scores(0, n + 5)) { ok = false; break; }
           if (wk.two) {
             if (!bar_wait(bars + 8 * (aP + 1), np[1] & 1, p.wait_ns, abort)) { ok = false; break; }
             ++np[1];
@@ -683,7 +712,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
           }
           release(n + 3, 2);
           if (more) {
-            if (wk.two) scores(1, n + 5);
+            if (wk.two && !scores(1, n + 5)) { ok = false; break; }
             release(n + 5, 3);
           }
         }
