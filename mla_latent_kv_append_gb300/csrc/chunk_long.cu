@@ -142,12 +142,16 @@ __global__ void __launch_bounds__(kPrepThreads) long_prep_kernel(const ChunkPara
 }
 
 // ---------------------------------------------------------------------------
-// long_expand_kernel: unit (key tile, head), tile-major.  The tile's latents
+// long_expand_kernel: clusters of two blocks.  A unit is (pair of key tiles,
+// head), pair-major; each block has one tile of the pair.  The tile's latents
 // (128 KB) stay in shared memory while the heads' weights stream through
 // three 32 KB stages (64 latent channels of W_UK and W_UV).  Per stage eight
 // M = 128, N = 128 MMAs; a head's keys and values fill 256 TMEM columns, and
 // the two halves of TMEM alternate between the MMAs and the epilogue.
-// What bounds it: the weights' way from L2, 32 KB per 520 cycles and SM.
+// What bounds it: the weights' way from L2 - 32 KB per 520 cycles of MMAs is
+// more than L2 gives all SMs (one block by itself took 9000 cycles per unit
+// for 4100 of MMAs) - so each block of the pair fetches half a stage and
+// multicasts it to both.
 // Warps: 0 copies, 1 MMAs, 4..7 epilogue.
 // ---------------------------------------------------------------------------
 constexpr int kExThreads = 256;
@@ -158,7 +162,7 @@ constexpr int kExSmem = kExBars + 256 + 1024;
 static_assert(kExSmem <= 232448, "a block's shared memory");
 enum { xFull = 0, xEmpty = 3, xA = 6, xAFree, xD, xDFree = xD + 2, xFin = xDFree + 2, xCount };
 
-__global__ void __launch_bounds__(kExThreads, 1) long_expand_kernel(const ChunkParams p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_expand_kernel(const ChunkParams p) {
   extern __shared__ uint8_t ex_smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ex_smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sb = smem_u32(sm), bars = sb + kExBars;
@@ -166,25 +170,31 @@ __global__ void __launch_bounds__(kExThreads, 1) long_expand_kernel(const ChunkP
   volatile int* abort = reinterpret_cast<volatile int*>(sm + kExBars + 8 * xCount + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < xCount; ++i) bar_init(bars + 8 * i, i == xDFree || i == xDFree + 1 ? 128 : 1);
+    for (int i = 0; i < xCount; ++i)
+      bar_init(bars + 8 * i, i == xDFree || i == xDFree + 1 ? 128 : (i >= xEmpty && i < xEmpty + kExStages ? 2 : 1));
     *abort = 0;
     bar_init_fence();
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
   fence_before();
   __syncthreads();
+  cluster_sync();                          // the other block's barriers are there
   fence_after();
   const uint32_t tbase = *tmem_slot;
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t U = (int64_t)__ldcg(&p.counts->l_tiles) * p.H;
-  const int64_t lo = U * blockIdx.x / gridDim.x, hi = U * (blockIdx.x + 1) / gridDim.x;
+  const int rank = (int)cluster_rank();
+  const int tiles = __ldcg(&p.counts->l_tiles);
+  const int64_t U = (int64_t)((tiles + 1) / 2) * p.H;
+  const int64_t lo = U * (blockIdx.x >> 1) / (gridDim.x >> 1), hi = U * ((blockIdx.x >> 1) + 1) / (gridDim.x >> 1);
+  // the last pair may have one tile: its second block follows along unheard
+  auto tile_of = [&](int64_t u) { return min((int)(u / p.H) * 2 + rank, tiles - 1); };
   bool ok = true;
   if (warp == 0) {
     if (elect_one() && hi > lo) {
       uint32_t it = 0, na = 0;
       for (int64_t u = lo; u < hi && ok; ++u) {
-        const int tile = (int)(u / p.H), h = (int)(u % p.H);
+        const int tile = tile_of(u), h = (int)(u % p.H);
         if (u == lo || h == 0) {
           if (na > 0 && !bar_wait(bars + 8 * xAFree, (na - 1) & 1, p.wait_ns, abort)) {
             ok = false;
@@ -200,8 +210,10 @@ __global__ void __launch_bounds__(kExThreads, 1) long_expand_kernel(const ChunkP
             ok = false;
             break;
           }
+          // this block's half, to both; the other's half is counted too
           bar_expect(bars + 8 * (xFull + s), kWStage);
-          bulk_copy(sb + kExW + s * kWStage, p.w_tiles + ((int64_t)h * 8 + st) * kWStage, kWStage, bars + 8 * (xFull + s));
+          bulk_copy_both(sb + kExW + s * kWStage + rank * kBlkBytes,
+                         p.w_tiles + ((int64_t)h * 8 + st) * kWStage + rank * kBlkBytes, kBlkBytes, bars + 8 * (xFull + s));
         }
       }
       if (!ok) {
@@ -243,7 +255,7 @@ __global__ void __launch_bounds__(kExThreads, 1) long_expand_kernel(const ChunkP
           const uint64_t a = d_c + (uint64_t)(st * (kBlkBytes >> 4)), w = (uint64_t)(s * (kWStage >> 4));
           umma4<2, 2>(d, a, d_uk + w, kIdK, st != 0);
           umma4<2, (2048 >> 4)>(d + 128, a, d_uv + w, kIdV, st != 0);
-          umma_commit(bars + 8 * (xEmpty + s));
+          umma_commit_both(bars + 8 * (xEmpty + s));       // both blocks' copies write both blocks' stages
         }
         if (!ok) break;
         umma_commit(bars + 8 * (xD + g));
@@ -268,7 +280,9 @@ __global__ void __launch_bounds__(kExThreads, 1) long_expand_kernel(const ChunkP
         break;
       }
       fence_after();
-      uint8_t* out = p.kv_tiles + u * kHeadTile;
+      const int tile = tile_of(u);
+      const bool heard = (int)(u / p.H) * 2 + rank < tiles;
+      uint8_t* out = p.kv_tiles + ((int64_t)tile * p.H + u % p.H) * kHeadTile;
       bool fine = true;
 #pragma unroll 1
       for (int c = 0; c < 8; ++c) {        // 32 columns: half a block
@@ -286,9 +300,10 @@ __global__ void __launch_bounds__(kExThreads, 1) long_expand_kernel(const ChunkP
 #pragma unroll
           for (int i = 0; i < 16; ++i) hw[i] = 0u;
         }
-        put_rows(out + (c >> 1) * kBlkBytes, row, 4 * (c & 1), hw);
+        if (heard) put_rows(out + (c >> 1) * kBlkBytes, row, 4 * (c & 1), hw);
+        __syncwarp();
       }
-      if (!fine) atomicOr(p.kflags + 8 * (u / p.H) + w, 1u << lane);
+      if (heard && !fine) atomicOr(p.kflags + 8 * tile + w, 1u << lane);
       fence_before();
       bar_arrive(bars + 8 * (xDFree + g));
     }
@@ -299,6 +314,7 @@ __global__ void __launch_bounds__(kExThreads, 1) long_expand_kernel(const ChunkP
   }
   fence_before();
   __syncthreads();
+  cluster_sync();                          // no copy or commit of the other block comes after this
   if (warp == 1) {
     fence_after();
     tmem_free(tbase, 512);
@@ -818,11 +834,11 @@ mla_status launch_long(const ChunkParams& p, int lf, int kf, cudaStream_t stream
   MLA_CHUNK_CASE(MLA_FMT_INT8_OUTLIER, MLA_FMT_INT8_SYM)
 #undef MLA_CHUNK_CASE
   if (st != MLA_OK) return st;
-  st = cuda_status(launch_pdl(long_expand_kernel, dim3(p.grid), dim3(kExThreads), kExSmem, stream, p));
+  st = cuda_status(launch_pdl(long_expand_kernel, dim3(p.grid / 2 * 2), dim3(kExThreads), kExSmem, stream, p));
   if (st != MLA_OK) return st;
   st = cuda_status(launch_pdl(long_attention_kernel, dim3(p.grid), dim3(kLaThreads), kLaSmem, stream, p));
   if (st != MLA_OK) return st;
-  return cuda_status(launch_pdl(long_combine_kernel, dim3(8 * p.grid), dim3(128), 0, stream, p));
+  return cuda_status(launch_pdl(long_combine_kernel, dim3(16 * p.grid), dim3(128), 0, stream, p));
 }
 
 }  // namespace mla

@@ -27,6 +27,7 @@ constexpr int kPlanThreads = 512;
 constexpr int kPlanPer = kMaxBatch / kPlanThreads;      // requests per thread: 8
 static_assert(kPlanThreads * kPlanPer == kMaxBatch, "every request has a thread");
 constexpr int kPlanRowWords = kPlanMaxRows / 32;
+constexpr int kPlanAhead = 4;
 
 struct PlanParams {
   const int32_t *ctx, *nw, *req;
@@ -68,15 +69,18 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* red, int64_t* 
 __device__ __forceinline__ int pages_of(int tokens) { return (int)(((int64_t)tokens + kPage - 1) / kPage); }
 
 // Dynamic shared memory: q_start [B + 1], first [B] (pages before the
-// request's own; -1: refused), then two bits per persistent row (seen,
-// seen twice).
+// request's own; -1: refused), ctx [B], pages in use after the step [B], table
+// row [B], then two bits per persistent row (seen, seen twice).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
   extern __shared__ int32_t plan_smem[];
   __shared__ int64_t red[kPlanThreads / 32];
   __shared__ int taken;
   int32_t* s_start = plan_smem;
   int32_t* s_first = s_start + p.B + 1;
-  uint32_t* s_seen = reinterpret_cast<uint32_t*>(s_first + p.B);
+  int32_t* s_ctx = s_first + p.B;
+  int32_t* s_now = s_ctx + p.B;
+  int32_t* s_row = s_now + p.B;
+  uint32_t* s_seen = reinterpret_cast<uint32_t*>(s_row + p.B);
   const int row_words = (p.rows + 31) / 32;
   uint32_t* s_twice = s_seen + row_words;
   const int tid = threadIdx.x;
@@ -165,6 +169,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
         first += need;
       }
       s_first[b] = f;
+      s_ctx[b] = ctx[k];
+      s_now[b] = f >= 0 ? pages_of(ctx[k] + nw[k]) : 0;
+      s_row[b] = row[k];
       if (blockIdx.x == 0) {
         p.q_start[b] = s_start[b];
         p.seq_lens[b] = f >= 0 ? ctx[k] + nw[k] : 0;
@@ -194,10 +201,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       }
       b = lo;
       if (s_first[b] >= 0) {
-        const int c = __ldcg(p.ctx + b);
+        const int c = s_ctx[b];
         pos = c + (int)(i - s_start[b]);
         const int pg = pos / kPage, old = pages_of(c);
-        const int id = pg < old ? __ldcg(p.table + (int64_t)__ldcg(p.req + b) * p.max_pages + pg)
+        const int id = pg < old ? __ldcg(p.table + (int64_t)s_row[b] * p.max_pages + pg)
                                 : __ldcg(p.free_pages + head + s_first[b] + pg - old);
         if (id >= 0 && id < p.num_pages) slot = id * kPage + (pos & (kPage - 1));
         else set_err(p.dev_err, MLA_DEVERR_PAGE);
@@ -207,25 +214,37 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     p.token_req[i] = b;
     p.slot[i] = slot;
   }
-  // ---- tables: a warp takes 32 columns of one row at a time
+  // ---- tables: a warp takes 32 columns of one row at a time, kPlanAhead such
+  // pieces with their loads in flight together
   const int cols = (p.max_pages + 31) / 32, lane = tid & 31;
-  for (int64_t w = me >> 5; w < (int64_t)p.B * cols; w += threads >> 5) {
-    const int b = (int)(w / cols), pg = 32 * (int)(w % cols) + lane;
-    if (pg >= p.max_pages) continue;
-    int id = -1;
-    if (s_first[b] >= 0) {
-      const int c = __ldcg(p.ctx + b), old = pages_of(c);
-      if (pg < pages_of(c + __ldcg(p.nw + b))) {
-        int32_t* mine = p.table + (int64_t)__ldcg(p.req + b) * p.max_pages + pg;
-        id = pg < old ? __ldcg(mine) : __ldcg(p.free_pages + head + s_first[b] + pg - old);
-        if (id < 0 || id >= p.num_pages) {
-          set_err(p.dev_err, MLA_DEVERR_PAGE);
-          id = -1;
-        }
-        if (pg >= old) *mine = id;
-      }
+  const int64_t pieces = (int64_t)p.B * cols, warps = threads >> 5;
+  for (int64_t w0 = me >> 5; w0 < pieces; w0 += warps * kPlanAhead) {
+    int id[kPlanAhead];
+#pragma unroll
+    for (int e = 0; e < kPlanAhead; ++e) {
+      const int64_t w = w0 + e * warps;
+      id[e] = -1;
+      if (w >= pieces) continue;
+      const int b = (int)(w / cols), pg = 32 * (int)(w % cols) + lane, old = pages_of(s_ctx[b]);
+      if (pg < s_now[b])
+        id[e] = pg < old ? __ldcg(p.table + (int64_t)s_row[b] * p.max_pages + pg)
+                         : __ldcg(p.free_pages + head + s_first[b] + pg - old);
     }
-    p.block_table[(int64_t)b * p.max_pages + pg] = id;
+#pragma unroll
+    for (int e = 0; e < kPlanAhead; ++e) {
+      const int64_t w = w0 + e * warps;
+      if (w >= pieces) continue;
+      const int b = (int)(w / cols), pg = 32 * (int)(w % cols) + lane;
+      if (pg >= p.max_pages) continue;
+      if (pg < s_now[b]) {
+        if (id[e] < 0 || id[e] >= p.num_pages) {
+          set_err(p.dev_err, MLA_DEVERR_PAGE);
+          id[e] = -1;
+        }
+        if (pg >= pages_of(s_ctx[b])) p.table[(int64_t)s_row[b] * p.max_pages + pg] = id[e];
+      }
+      p.block_table[(int64_t)b * p.max_pages + pg] = id[e];
+    }
   }
 }
 
@@ -275,12 +294,12 @@ extern "C" mla_status mla_plan_chunks(const int32_t* ctx_lens, const int32_t* ne
   p.free_head = free_head;
   p.n = n_tokens;
   p.dev_err = dev_err;
-  const size_t smem = sizeof(int32_t) * ((size_t)2 * batch + 1 + 2 * ((rows + 31) / 32));
+  const size_t smem = sizeof(int32_t) * ((size_t)5 * batch + 1 + 2 * ((rows + 31) / 32));
   static int configured[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);
   if (smem > 48 * 1024 && (dev < 0 || dev >= 64 || !configured[dev])) {
-    const int most = (int)sizeof(int32_t) * (2 * kMaxBatch + 1 + 2 * kPlanRowWords);
+    const int most = (int)sizeof(int32_t) * (5 * kMaxBatch + 1 + 2 * kPlanRowWords);
     const mla_status st =
         cuda_status(cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
     if (st != MLA_OK) return st;
