@@ -46,8 +46,7 @@ constexpr int kLongRows = 256;               // query rows (tokens of one head) 
 constexpr int kBlkBytes = 16384;             // 128 rows x 64 fp16, swizzled
 constexpr int kCTile = 8 * kBlkBytes;        // a key tile's latents
 constexpr int kHeadTile = 4 * kBlkBytes;     // a key tile's keys (2 blocks) and values (2 blocks) of one head
-constexpr int kWStage = 2 * kBlkBytes;       // 64 latent channels of a head's W_UK and W_UV
-constexpr int kWHead = 8 * kWStage;
+constexpr int kWHead = 16 * kBlkBytes;       // a head's W_UK, then W_UV, 64 latent channels per block
 __host__ __device__ constexpr int64_t long_partial_floats() { return (int64_t)kLongRows * (kDv + 2); }
 
 // Key tiles up to (not including) which pair `pr` of a sequence's new tokens
@@ -101,7 +100,7 @@ struct ChunkParams {
   uint8_t* c_tiles;       // [key tile][8][128][64] fp16 latents, swizzled
   uint8_t* k_rope;        // [key tile][128][64] fp16 RoPE keys
   uint32_t* kflags;       // [key tile][8]: a bit per token: 0..3 not finite, 4..7 on no page
-  uint8_t* w_tiles;       // [H][8][W_UK 128 x 64, W_UV 64 x 128] fp16
+  uint8_t* w_tiles;       // [H][8 W_UK blocks 128 x 64, 8 W_UV blocks 64 x 128] fp16
   uint8_t* kv_tiles;      // [key tile][H][K 2 blocks, V 2 blocks] fp16
   float* l_parts;         // [2 grid] partials of the long path
   SplitRec* l_splits;     // [grid]; row0: output row of the first (token row x H + head), rows H apart

@@ -34,11 +34,15 @@ constexpr float kSlack = 8.f;
 
 // ---------------------------------------------------------------------------
 // long_prep_kernel: block x < 4 tiles: a 32-token block of a key tile, lane =
-// token, warp w dequantizes units w and w + 8, warps 0 and 1 the RoPE units.
+// token, warp w dequantizes units w and w + 8, warps 0 and 1 the RoPE units;
+// the rows leave as 4 KB bulk stores (a lane's own 16-byte stores to its row
+// would touch 32 lines each).
 // The blocks behind convert 64 latent channels of a head's weights each.
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 256;
+constexpr int kPrepRows = 32 * 128;        // a block's 32 rows of one 64-channel block: 4 KB
 
+// 32 channels of a row into a 128-byte row of a swizzled block.
 __device__ __forceinline__ void put_rows(uint8_t* blk, int row, int c16, const uint32_t* h) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -47,7 +51,7 @@ __device__ __forceinline__ void put_rows(uint8_t* blk, int row, int c16, const u
 }
 
 __device__ void convert_weights(const ChunkParams& p, int h, int st) {
-  uint8_t* out = p.w_tiles + ((int64_t)h * 8 + st) * kWStage;
+  uint8_t* out = p.w_tiles + (int64_t)h * kWHead + st * kBlkBytes;
   for (int i = threadIdx.x; i < 2 * 128 * 8; i += kPrepThreads) {
     // W_UK: rows d, 64 channels (K-major); W_UV: rows c, 128 values as two blocks of 64 (MN-major)
     const bool uk = i < 1024;
@@ -55,7 +59,7 @@ __device__ void convert_weights(const ChunkParams& p, int h, int st) {
     const uint16_t* src = uk ? p.w_uk + ((int64_t)h * kDn + row) * kDc + 64 * st + 8 * c
                              : p.w_uv + ((int64_t)h * kDc + 64 * st + row) * kDv + 8 * c;
     const uint4 v = __ldcg(reinterpret_cast<const uint4*>(src));
-    uint8_t* blk = uk ? out : out + kBlkBytes + (c >> 3) * 8192;
+    uint8_t* blk = uk ? out : out + 8 * kBlkBytes + (c >> 3) * 8192;
     *reinterpret_cast<uint4*>(blk + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
         make_uint4(half2_bits(bf16lo(v.x), bf16hi(v.x)), half2_bits(bf16lo(v.y), bf16hi(v.y)),
                    half2_bits(bf16lo(v.z), bf16hi(v.z)), half2_bits(bf16lo(v.w), bf16hi(v.w)));
@@ -65,7 +69,9 @@ __device__ void convert_weights(const ChunkParams& p, int h, int st) {
 template <int LF, int KF>
 __global__ void __launch_bounds__(kPrepThreads) long_prep_kernel(const ChunkParams p, int key_blocks) {
   constexpr int kBlock = block_bytes<LF, KF>();
-  __shared__ __align__(128) uint8_t raw[kBlock];
+  extern __shared__ __align__(1024) uint8_t prep_smem[];
+  uint8_t* out = prep_smem;                // 8 latent blocks' rows and the RoPE keys'
+  uint8_t* raw = prep_smem + kQBlocks * kPrepRows;
   __shared__ uint64_t bar;
   __shared__ uint32_t s_bad;
   pdl_launch_dependents();
@@ -111,8 +117,6 @@ __global__ void __launch_bounds__(kPrepThreads) long_prep_kernel(const ChunkPara
     }
   }
   const bool live = read && arrived && lane < n_tok;
-  uint8_t* out = p.c_tiles + (int64_t)tile * kCTile;
-  const int row = 32 * sub + lane;
   bool fine = true;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -123,7 +127,7 @@ __global__ void __launch_bounds__(kPrepThreads) long_prep_kernel(const ChunkPara
     else zero_unit(r);
     fine &= convert_unit<LF, false>(r, h);
     if (live) fine &= patch_outliers<LF>(raw, p.L, p.outl, lane, unit, h);
-    put_rows(out + (unit >> 1) * kBlkBytes, row, 4 * (unit & 1), h);
+    put_rows(out + (unit >> 1) * kPrepRows, lane, 4 * (unit & 1), h);
   }
   if (warp < 2) {
     RawUnit<KF, true> r;
@@ -131,36 +135,44 @@ __global__ void __launch_bounds__(kPrepThreads) long_prep_kernel(const ChunkPara
     if (live) load_unit<KF, true>(raw, p.L, lane, warp, r);
     else zero_unit(r);
     fine &= convert_unit<KF, true>(r, h);
-    put_rows(p.k_rope + (int64_t)tile * kBlkBytes, row, 4 * warp, h);
+    put_rows(out + 8 * kPrepRows, lane, 4 * warp, h);
   }
   if (!fine) atomicOr(&s_bad, 1u << lane);
+  fence_async_smem();
   __syncthreads();
   if (tid == 0) {
+    for (int c = 0; c < kQBlocks; ++c)
+      bulk_store((c < 8 ? p.c_tiles + (int64_t)tile * kCTile + c * kBlkBytes : p.k_rope + (int64_t)tile * kBlkBytes) + sub * kPrepRows,
+                 smem_u32(out + c * kPrepRows), kPrepRows);
+    bulk_store_commit();
     p.kflags[8 * tile + sub] = s_bad;
     p.kflags[8 * tile + 4 + sub] = page_ok ? 0u : 0xFFFFFFFFu;
+    bulk_store_done();
   }
 }
 
 // ---------------------------------------------------------------------------
 // long_expand_kernel: clusters of two blocks.  A unit is (pair of key tiles,
 // head), pair-major; each block has one tile of the pair.  The tile's latents
-// (128 KB) stay in shared memory while the heads' weights stream through
-// three 32 KB stages (64 latent channels of W_UK and W_UV).  Per stage eight
-// M = 128, N = 128 MMAs; a head's keys and values fill 256 TMEM columns, and
-// the two halves of TMEM alternate between the MMAs and the epilogue.
-// What bounds it: the weights' way from L2 - 32 KB per 520 cycles of MMAs is
-// more than L2 gives all SMs (one block by itself took 9000 cycles per unit
-// for 4100 of MMAs) - so each block of the pair fetches half a stage and
-// multicasts it to both.
-// Warps: 0 copies, 1 MMAs, 4..7 epilogue.
+// stay in TMEM (128 lanes x 256 columns of fp16 pairs) as the A operand while
+// the heads' weights stream through shared memory, 16 KB (64 latent channels
+// of W_UK or of W_UV) per item, four M = 128, N = 128 MMAs each.  A head's keys
+// and values are 128 TMEM columns each; while one half is computed the other
+// leaves, through 32 KB of shared memory as bulk stores.
+// What bounds it: 4100 cycles of MMAs per unit.  The weights' 64 bytes per
+// cycle and SM are more than L2 gives all SMs, so each block of the pair
+// fetches half an item and multicasts it to both; and their latency wants 100
+// KB and more under way, which is why the latents are not in shared memory (64
+// KB under way: 10000 cycles per unit).
+// Warps: 0 copies, 1 MMAs, 4..7 epilogue (and the latents' way into TMEM).
 // ---------------------------------------------------------------------------
 constexpr int kExThreads = 256;
-constexpr int kExStages = 3;
-constexpr int kExW = kCTile;
-constexpr int kExBars = kExW + kExStages * kWStage;
-constexpr int kExSmem = kExBars + 256 + 1024;
+constexpr int kExItems = 11;
+constexpr int kExOut = kExItems * kBlkBytes;
+constexpr int kExBars = kExOut + 2 * kBlkBytes;
+constexpr int kExSmem = kExBars + 512 + 1024;
 static_assert(kExSmem <= 232448, "a block's shared memory");
-enum { xFull = 0, xEmpty = 3, xA = 6, xAFree, xD, xDFree = xD + 2, xFin = xDFree + 2, xCount };
+enum { xFull = 0, xEmpty = xFull + kExItems, xA = xEmpty + kExItems, xD, xDFree = xD + 2, xFin = xDFree + 2, xCount };
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_expand_kernel(const ChunkParams p) {
   extern __shared__ uint8_t ex_smem_raw[];
@@ -168,10 +180,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_
   const uint32_t sb = smem_u32(sm), bars = sb + kExBars;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kExBars + 8 * xCount);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + kExBars + 8 * xCount + 4);
+  volatile int* quit = reinterpret_cast<volatile int*>(sm + kExBars + 8 * xCount + 8);       // [2, by unit parity]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    quit[0] = quit[1] = 0;
     for (int i = 0; i < xCount; ++i)
-      bar_init(bars + 8 * i, i == xDFree || i == xDFree + 1 ? 128 : (i >= xEmpty && i < xEmpty + kExStages ? 2 : 1));
+      bar_init(bars + 8 * i, i == xA || i == xDFree || i == xDFree + 1 ? 128 : (i >= xEmpty && i < xA ? 2 : 1));
     *abort = 0;
     bar_init_fence();
   }
@@ -180,7 +194,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_
   __syncthreads();
   cluster_sync();                          // the other block's barriers are there
   fence_after();
-  const uint32_t tbase = *tmem_slot;
+  const uint32_t tbase = *tmem_slot, t_d = tbase + 256;
   pdl_launch_dependents();
   pdl_wait();
   const int rank = (int)cluster_rank();
@@ -192,74 +206,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_
   bool ok = true;
   if (warp == 0) {
     if (elect_one() && hi > lo) {
-      uint32_t it = 0, na = 0;
+      uint32_t it = 0;
       for (int64_t u = lo; u < hi && ok; ++u) {
-        const int tile = tile_of(u), h = (int)(u % p.H);
-        if (u == lo || h == 0) {
-          if (na > 0 && !bar_wait(bars + 8 * xAFree, (na - 1) & 1, p.wait_ns, abort)) {
-            ok = false;
-            break;
-          }
-          bar_expect(bars + 8 * xA, kCTile);
-          bulk_copy(sb, p.c_tiles + (int64_t)tile * kCTile, kCTile, bars + 8 * xA);
-          ++na;
-        }
-        for (int st = 0; st < 8; ++st, ++it) {
-          const uint32_t s = it % kExStages;
-          if (it >= kExStages && !bar_wait(bars + 8 * (xEmpty + s), (it / kExStages - 1) & 1, p.wait_ns, abort)) {
+        const uint8_t* src = p.w_tiles + (u % p.H) * kWHead + rank * (kBlkBytes / 2);
+        for (int st = 0; st < 16; ++st, ++it) {
+          const uint32_t s = it % kExItems;
+          if (it >= kExItems && !bar_wait(bars + 8 * (xEmpty + s), (it / kExItems - 1) & 1, p.wait_ns, abort)) {
             ok = false;
             break;
           }
           // this block's half, to both; the other's half is counted too
-          bar_expect(bars + 8 * (xFull + s), kWStage);
-          bulk_copy_both(sb + kExW + s * kWStage + rank * kBlkBytes,
-                         p.w_tiles + ((int64_t)h * 8 + st) * kWStage + rank * kBlkBytes, kBlkBytes, bars + 8 * (xFull + s));
+          bar_expect(bars + 8 * (xFull + s), kBlkBytes);
+          bulk_copy_both(sb + s * kBlkBytes + rank * (kBlkBytes / 2), src + st * kBlkBytes, kBlkBytes / 2, bars + 8 * (xFull + s));
         }
       }
       if (!ok) {
         set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
         *abort = 1;
       }
-      if (na > 0) drain_wait(bars + 8 * xA, (na - 1) & 1);
-      for (uint32_t s = 0; s < kExStages; ++s)
-        if (it > s) drain_wait(bars + 8 * (xFull + s), ((it - 1 - s) / kExStages) & 1);
+      for (uint32_t s = 0; s < kExItems; ++s)
+        if (it > s && !drain_wait(bars + 8 * (xFull + s), ((it - 1 - s) / kExItems) & 1)) break;
     }
     __syncwarp();
   } else if (warp == 1) {
     if (elect_one() && hi > lo) {
       constexpr uint32_t kIdK = f16_idesc(128, 128, false, false), kIdV = f16_idesc(128, 128, false, true);
-      const uint64_t d_c = sw128_desc(sb, 16, 1024);
-      const uint64_t d_uk = sw128_desc(sb + kExW, 16, 1024), d_uv = sw128_desc(sb + kExW + kBlkBytes, 8192, 1024);
+      const uint64_t d_uk = sw128_desc(sb, 16, 1024), d_uv = sw128_desc(sb, 8192, 1024);
       uint32_t it = 0, na = 0, nd = 0;
       for (int64_t u = lo; u < hi && ok; ++u, ++nd) {
-        const int h = (int)(u % p.H);
-        if (u == lo || h == 0) {
+        if (u == lo || u % p.H == 0) {
           if (!bar_wait(bars + 8 * xA, na & 1, p.wait_ns, abort)) {
             ok = false;
             break;
           }
           ++na;
         }
-        const uint32_t g = nd & 1, d = tbase + 256 * g;
-        if (nd >= 2 && !bar_wait(bars + 8 * (xDFree + g), (nd / 2 - 1) & 1, p.wait_ns, abort)) {
-          ok = false;
-          break;
-        }
-        for (int st = 0; st < 8; ++st, ++it) {
-          const uint32_t s = it % kExStages;
-          if (!bar_wait(bars + 8 * (xFull + s), (it / kExStages) & 1, p.wait_ns, abort)) {
+        for (int half = 0; half < 2 && ok; ++half) {
+          if (nd >= 1 && !bar_wait(bars + 8 * (xDFree + half), (nd - 1) & 1, p.wait_ns, abort)) {
             ok = false;
             break;
           }
-          fence_after();
-          const uint64_t a = d_c + (uint64_t)(st * (kBlkBytes >> 4)), w = (uint64_t)(s * (kWStage >> 4));
-          umma4<2, 2>(d, a, d_uk + w, kIdK, st != 0);
-          umma4<2, (2048 >> 4)>(d + 128, a, d_uv + w, kIdV, st != 0);
-          umma_commit_both(bars + 8 * (xEmpty + s));       // both blocks' copies write both blocks' stages
+          for (int st = 0; st < 8; ++st, ++it) {
+            const uint32_t s = it % kExItems;
+            if (!bar_wait(bars + 8 * (xFull + s), (it / kExItems) & 1, p.wait_ns, abort)) {
+              ok = false;
+              break;
+            }
+            fence_after();
+            const uint64_t w = (uint64_t)(s * (kBlkBytes >> 4));
+            if (half == 0) umma4_ta<2>(t_d, tbase + 32 * st, d_uk + w, kIdK, st != 0);
+            else umma4_ta<(2048 >> 4)>(t_d + 128, tbase + 32 * st, d_uv + w, kIdV, st != 0);
+            umma_commit_both(bars + 8 * (xEmpty + s));     // both blocks' copies write both blocks' items
+          }
+          if (ok) umma_commit(bars + 8 * (xD + half));
         }
-        if (!ok) break;
-        umma_commit(bars + 8 * (xD + g));
-        if (h == p.H - 1) umma_commit(bars + 8 * xAFree);
       }
       if (!ok) {
         set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
@@ -270,43 +270,96 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_
     }
     __syncwarp();
   } else if (warp >= 4) {
+    // The four warps meet twice per half: when the staging blocks are free, and
+    // when they are filled; one that gave up a wait says so before the meeting.
     const int w = warp & 3, row = 32 * w + lane;
     const uint32_t tl = (uint32_t)(32 * w) << 16;
+    uint8_t* stage = sm + kExOut;
     uint32_t nd = 0;
-    for (int64_t u = lo; u < hi; ++u, ++nd) {
+    for (int64_t u = lo; u < hi && ok; ++u, ++nd) {
       const uint32_t g = nd & 1;
-      if (!warp_wait(bars + 8 * (xD + g), (nd / 2) & 1, p.wait_ns, abort)) {
-        ok = false;
-        break;
-      }
-      fence_after();
       const int tile = tile_of(u);
+      if (u == lo || u % p.H == 0) {
+        // The latents into TMEM, a row per lane (the last tile's MMAs are done,
+        // their results have been read).  A warp reads its 32 rows of four
+        // blocks at a time, side by side, and turns them through its quarter of
+        // the staging blocks.
+        if (threadIdx.x == 128) bulk_store_read_done();
+        asm volatile("bar.sync 1, 128;\n" ::: "memory");
+        const uint8_t* src = p.c_tiles + (int64_t)tile * kCTile + w * 4096 + lane * 16;
+        uint8_t* mine = stage + w * 8192;
+#pragma unroll 1
+        for (int c0 = 0; c0 < 8; c0 += 4) {
+          uint4 v[4][8];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[c][e] = __ldcg(reinterpret_cast<const uint4*>(src + (c0 + c) * kBlkBytes + 512 * e));
+#pragma unroll
+          for (int c2 = 0; c2 < 4; c2 += 2) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(mine + 4096 * c + 512 * e + lane * 16) = v[c2 + c][e];
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t r[32];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<uint4*>(r + 4 * e) =
+                    *reinterpret_cast<const uint4*>(mine + 4096 * c + lane * 128 + ((e ^ (lane & 7)) << 4));
+              tmem_store32(tbase + 32 * (c0 + c2 + c) + tl, r);
+            }
+            __syncwarp();
+          }
+        }
+        fence_before();
+        bar_arrive(bars + 8 * xA);
+      }
       const bool heard = (int)(u / p.H) * 2 + rank < tiles;
       uint8_t* out = p.kv_tiles + ((int64_t)tile * p.H + u % p.H) * kHeadTile;
       bool fine = true;
+      for (int half = 0; half < 2; ++half) {               // keys, values
+        if (!warp_wait(bars + 8 * (xD + half), nd & 1, p.wait_ns, abort)) quit[g] = 1;
+        if (threadIdx.x == 128) bulk_store_read_done();
+        asm volatile("bar.sync 1, 128;\n" ::: "memory");
+        if (quit[g]) {
+          ok = false;
+          break;
+        }
+        fence_after();
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {        // 32 columns: half a block
-        uint32_t r[32], hw[16];
-        tmem_load32(tbase + 256 * g + 32 * c + tl, r);
-        __half2 acc = __float2half2_rn(0.f);
-        const __half2 zero = acc;
+        for (int c = 0; c < 4; ++c) {      // 32 columns: half a block
+          uint32_t r[32], hw[16];
+          tmem_load32(t_d + 128 * half + 32 * c + tl, r);
+          __half2 acc = __float2half2_rn(0.f);
+          const __half2 zero = acc;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          hw[i] = half2_bits(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-          acc = __hfma2(*reinterpret_cast<const __half2*>(&hw[i]), zero, acc);
-        }
-        if (__hisnan(__low2half(acc)) || __hisnan(__high2half(acc))) {
-          fine = false;
+          for (int i = 0; i < 16; ++i) {
+            hw[i] = half2_bits(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+            acc = __hfma2(*reinterpret_cast<const __half2*>(&hw[i]), zero, acc);
+          }
+          if (__hisnan(__low2half(acc)) || __hisnan(__high2half(acc))) {
+            fine = false;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) hw[i] = 0u;
+            for (int i = 0; i < 16; ++i) hw[i] = 0u;
+          }
+          put_rows(stage + (c >> 1) * kBlkBytes, row, 4 * (c & 1), hw);
+          __syncwarp();
         }
-        if (heard) put_rows(out + (c >> 1) * kBlkBytes, row, 4 * (c & 1), hw);
-        __syncwarp();
+        fence_before();
+        bar_arrive(bars + 8 * (xDFree + half));            // TMEM has been read
+        fence_async_smem();
+        asm volatile("bar.sync 1, 128;\n" ::: "memory");
+        if (threadIdx.x == 128 && heard) {
+          bulk_store(out + half * 2 * kBlkBytes, sb + kExOut, 2 * kBlkBytes);
+          bulk_store_commit();
+        }
       }
-      if (heard && !fine) atomicOr(p.kflags + 8 * tile + w, 1u << lane);
-      fence_before();
-      bar_arrive(bars + 8 * (xDFree + g));
+      if (ok && heard && !fine) atomicOr(p.kflags + 8 * tile + w, 1u << lane);
     }
+    if (threadIdx.x == 128) bulk_store_done();
     if (!ok) {
       set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
       *abort = 1;
@@ -795,8 +848,18 @@ __global__ void __launch_bounds__(128) long_combine_kernel(const ChunkParams p) 
 
 template <int LF, int KF>
 mla_status launch_prep(const ChunkParams& p, cudaStream_t stream) {
+  const int smem = kQBlocks * kPrepRows + block_bytes<LF, KF>();
+  static int configured[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    const mla_status st =
+        cuda_status(cudaFuncSetAttribute(long_prep_kernel<LF, KF>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    if (st != MLA_OK) return st;
+    if (dev >= 0 && dev < 64) configured[dev] = 1;
+  }
   const int key_blocks = 4 * (int)(p.kv_tokens / kLongKeys);
-  return cuda_status(launch_pdl(long_prep_kernel<LF, KF>, dim3(key_blocks + 8 * p.H), dim3(kPrepThreads), 0, stream, p, key_blocks));
+  return cuda_status(launch_pdl(long_prep_kernel<LF, KF>, dim3(key_blocks + 8 * p.H), dim3(kPrepThreads), smem, stream, p, key_blocks));
 }
 
 }  // namespace

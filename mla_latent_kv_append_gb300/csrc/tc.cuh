@@ -80,6 +80,14 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// Shared memory to global; the issuing thread's stores form groups.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_store_commit() { asm volatile("cp.async.bulk.commit_group;\n" ::: "memory"); }
+__device__ __forceinline__ void bulk_store_read_done() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+__device__ __forceinline__ void bulk_store_done() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
+
 // Shared-memory matrix descriptor, 128-byte swizzle.  K-major operands: rows
 // of 64 fp16, 8-row groups sbo apart.  MN-major operands: 64-element blocks
 // lbo apart, groups of 8 along the contraction sbo apart.
