@@ -420,6 +420,7 @@ struct LongWalk {
     seqs = p.l_seqs;
     u = lo;
     hi = hi_;
+    pair = -1;
     int n = __ldcg(&p.counts->l_seqs);
     k = 0;
     while (n - k > 1) {
@@ -431,19 +432,26 @@ struct LongWalk {
   }
   __device__ __forceinline__ bool next(int H) {
     if (u >= hi) return false;
-    while (u >= s.unit0 + (int64_t)s.per_head * H) {
-      ++k;
-      load();
-    }
-    const int64_t d = u - s.unit0;
-    h = (int)(d / s.per_head);
-    int r = (int)(d % s.per_head), J = 0;
     const int ctx = s.len - s.n;
-    for (pair = 0;; ++pair) {
-      J = pair_tiles(ctx, s.n, pair);
-      if (r < J) break;
-      r -= J;
+    int r = 0;
+    if (pair < 0) {                  // the run's first segment: wherever unit u lies
+      const int64_t d = u - s.unit0;
+      h = (int)(d / s.per_head);
+      r = (int)(d % s.per_head);
+      for (pair = 0; r >= pair_tiles(ctx, s.n, pair); ++pair) r -= pair_tiles(ctx, s.n, pair);
+    } else if (++pair * kLongRows >= s.n) {            // after it, item by item
+      pair = 0;
+      if (++h == H) {
+        h = 0;
+        ++k;
+        load();
+        return begin(0);
+      }
     }
+    return begin(r);
+  }
+  __device__ __forceinline__ bool begin(int r) {
+    const int ctx = s.len - s.n, J = pair_tiles(ctx, s.n, pair);
     t0 = r;
     t1 = (int)min((int64_t)J, t0 + (hi - u));
     first = t0 == 0;
@@ -688,6 +696,10 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
         for (int t = wk.t0; t < wk.t1 && ok; ++t) {
           const int64_t tile = wk.s.kv0 + t;
           const uint8_t* kv = p.kv_tiles + (tile * p.H + wk.h) * kHeadTile;
+          if (t + 2 < wk.t1) {             // the ring reaches one tile ahead: L2 should have the next
+            bulk_prefetch(kv + 2 * (int64_t)p.H * kHeadTile, kHeadTile);
+            bulk_prefetch(p.k_rope + (tile + 2) * kBlkBytes, kBlkBytes);
+          }
 #pragma unroll 1
           for (int c = 0; c < 5; ++c, ++n) {
             const uint32_t s = n % kRing;
@@ -707,6 +719,33 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
       }
       for (uint32_t s = 0; s < kRing; ++s)
         if (n > s) drain_wait(bars + 8 * (aFull + s), ((n - 1 - s) / kRing) & 1);
+    } else if (work && warp == 10) {
+      // ---- the next segment's query rows to L2 while this one runs
+      LongWalk wk;
+      wk.start(p, lo, hi);
+      uint32_t nq[2] = {0, 0};
+      bool more = wk.next(p.H);
+      while (more && ok) {
+        const bool zero = wk.t0 < min(wk.t1, wk.tiles0);
+        const int i = zero ? 0 : 1;
+        const uint32_t phase = nq[i] & 1;
+        if (zero) ++nq[0];
+        if (wk.two) ++nq[1];
+        more = wk.next(p.H);
+        if (more) {
+          for (int r = lane; r < kLongRows; r += 32) {
+            const int tok = wk.pair * kLongRows + r;
+            if (tok >= wk.s.n) break;
+            const uint16_t* qn = p.qn + (int64_t)(wk.s.q0 + tok) * p.qn_tok + wk.h * p.qn_head;
+            prefetch_line(qn);
+            prefetch_line(qn + 64);
+            prefetch_line(p.qp + (int64_t)(wk.s.q0 + tok) * p.qp_tok + wk.h * p.qp_head);
+          }
+        }
+        // one segment ahead, not more; nothing depends on this warp
+        if (!warp_wait(bars + 8 * (aQ + i), phase, p.wait_ns, abort)) ok = false;
+      }
+      ok = true;
     } else if (work && warp == 9 && elect_one()) {
       // ---- MMAs
       LongWalk wk;
@@ -803,46 +842,57 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
   }
 }
 
-// long_combine_kernel: block 128, the warps stride over the rows of the split
-// items and merge a row's parts in block order.
+// long_combine_kernel: block 128, grid (splits, 16): a warp merges four rows of
+// a split item, their parts in block order with the running maximum's weights
+// (few parts per item, so one pass with all four rows' loads in flight).
 __global__ void __launch_bounds__(128) long_combine_kernel(const ChunkParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31, warps = gridDim.x * 4;
-  const int total = __ldcg(&p.counts->l_splits) * kLongRows;
-  for (int w = blockIdx.x * 4 + (threadIdx.x >> 5); w < total; w += warps) {
-    const SplitRec* sr = p.l_splits + w / kLongRows;
-    const int r = w % kLongRows;
-    const int4 rec = __ldcg(reinterpret_cast<const int4*>(sr));
-    const int64_t row0 = __ldcg(&sr->row0);
-    if (r >= rec.z) continue;
-    const int n = rec.y - rec.x + 1;
-    const float* part = p.l_parts + (int64_t)(2 * rec.x + 1) * long_partial_floats();
-    // part 0 is slot 2 first + 1, part i > 0 slot 2 (first + i)
-    auto at = [&](int i) { return part + i * 2 * long_partial_floats() - (i ? long_partial_floats() : 0); };
-    float mx = -INFINITY;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) mx = fmaxf(mx, __ldcg(at(i) + kLongRows * kDv + r));
-    if (mx == -INFINITY) mx = 0.f;
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float* s = at(i);
-      const float mi = __ldcg(s + kLongRows * kDv + r), li = __ldcg(s + kLongRows * kDv + kLongRows + r);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(s + r * kDv) + lane);
-      const float wt = ex2(mi - mx);
-      l = fmaf(wt, li, l);
-      acc.x = fmaf(wt, v.x, acc.x);
-      acc.y = fmaf(wt, v.y, acc.y);
-      acc.z = fmaf(wt, v.z, acc.z);
-      acc.w = fmaf(wt, v.w, acc.w);
+  const int lane = threadIdx.x & 31, r0 = 16 * blockIdx.y + 4 * (threadIdx.x >> 5);
+  if ((int)blockIdx.x >= __ldcg(&p.counts->l_splits)) return;
+  const SplitRec* sr = p.l_splits + blockIdx.x;
+  const int4 rec = __ldcg(reinterpret_cast<const int4*>(sr));
+  const int64_t row0 = __ldcg(&sr->row0);
+  if (r0 >= rec.z) return;
+  // part 0 is slot 2 first + 1, part i > 0 slot 2 (first + i)
+  const float* part = p.l_parts + (int64_t)(2 * rec.x + 1) * long_partial_floats();
+  float m[4], l[4] = {0.f, 0.f, 0.f, 0.f};
+  float4 acc[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    m[e] = -INFINITY;
+    acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int y = rec.x; y <= rec.y; ++y) {
+    float mi[4], li[4];
+    float4 v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {          // rows of the padding are read (they lie in the slot) and not written
+      mi[e] = __ldcg(part + kLongRows * kDv + r0 + e);
+      li[e] = __ldcg(part + kLongRows * kDv + kLongRows + r0 + e);
+      v[e] = __ldcg(reinterpret_cast<const float4*>(part + (r0 + e) * kDv) + lane);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float top = fmaxf(m[e], mi[e]), base = top == -INFINITY ? 0.f : top;
+      const float a = ex2(m[e] - base), b = ex2(mi[e] - base);
+      m[e] = top;
+      l[e] = l[e] * a + li[e] * b;
+      acc[e].x = acc[e].x * a + v[e].x * b;
+      acc[e].y = acc[e].y * a + v[e].y * b;
+      acc[e].z = acc[e].z * a + v[e].z * b;
+      acc[e].w = acc[e].w * a + v[e].w * b;
+    }
+    part += (y == rec.x ? 1 : 2) * long_partial_floats();
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (r0 + e >= rec.z) break;
+    const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
     uint32_t a, b;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(a) : "f"(acc.y * inv), "f"(acc.x * inv));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(b) : "f"(acc.w * inv), "f"(acc.z * inv));
-    reinterpret_cast<uint2*>(p.o + (row0 + (int64_t)r * p.H) * kDv)[lane] = make_uint2(a, b);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(a) : "f"(acc[e].y * inv), "f"(acc[e].x * inv));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(b) : "f"(acc[e].w * inv), "f"(acc[e].z * inv));
+    reinterpret_cast<uint2*>(p.o + (row0 + (int64_t)(r0 + e) * p.H) * kDv)[lane] = make_uint2(a, b);
   }
 }
 
@@ -901,7 +951,7 @@ mla_status launch_long(const ChunkParams& p, int lf, int kf, cudaStream_t stream
   if (st != MLA_OK) return st;
   st = cuda_status(launch_pdl(long_attention_kernel, dim3(p.grid), dim3(kLaThreads), kLaSmem, stream, p));
   if (st != MLA_OK) return st;
-  return cuda_status(launch_pdl(long_combine_kernel, dim3(16 * p.grid), dim3(128), 0, stream, p));
+  return cuda_status(launch_pdl(long_combine_kernel, dim3(p.grid, kLongRows / 16), dim3(128), 0, stream, p));
 }
 
 }  // namespace mla

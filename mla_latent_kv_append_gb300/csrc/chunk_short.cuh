@@ -117,6 +117,7 @@ struct Walk {
     seqs = p.s_seqs;
     u = lo;
     hi = hi_;
+    item = -1;
     const int lane = threadIdx.x & 31;
     int a = 0, n = n_seqs;                   // the answer is in [a, a + n)
     while (n > 1) {
@@ -134,13 +135,18 @@ struct Walk {
   // The next segment; false behind the run's end.
   __device__ __forceinline__ bool next() {
     if (u >= hi) return false;
-    while (u >= s.unit0 + (int64_t)s.items * s.tiles) {
-      ++k;
-      load();
+    if (item < 0) {                  // the run's first segment: wherever unit u lies
+      const int64_t d = u - s.unit0;
+      item = (int)(d / s.tiles);
+      t0 = (int)(d % s.tiles);
+    } else {                         // after it, row tile by row tile
+      t0 = 0;
+      if (++item == s.items) {
+        item = 0;
+        ++k;
+        load();
+      }
     }
-    const int64_t d = u - s.unit0;
-    item = (int)(d / s.tiles);
-    t0 = (int)(d % s.tiles);
     t1 = (int)min((int64_t)s.tiles, t0 + (hi - u));
     first = t0 == 0;
     last = t1 == s.tiles;
@@ -720,12 +726,13 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
 
 // short_combine_kernel: the blocks stride over the rows of the split row
 // tiles.  A row's parts lie in the slots of its blocks, 2 first + 1 and then 2
-// (first + i).  The parts' maxima and sums are read side by side, then the
-// block's four quarters add up every fourth part (a single long context has a
-// part in every block, so the loads have to overlap) and the quarters are
-// added in order.
+// (first + i), merged in that order.  Few parts: the block's quarters take a
+// row each.  Many (a single long context has a part in every block): the
+// parts' maxima and sums are read side by side, then the quarters add up every
+// fourth part each, so that the loads overlap, and are added in order.
 constexpr int kCombineThreads = 512;
 constexpr int kCombineParts = 1024;      // most parts per row: blocks of the attention
+constexpr int kCombineFew = 8;
 
 __global__ void __launch_bounds__(kCombineThreads) short_combine_kernel(const ChunkParams p, int R) {
   __shared__ float s_w[kCombineParts];
@@ -746,6 +753,30 @@ __global__ void __launch_bounds__(kCombineThreads) short_combine_kernel(const Ch
     const int n = rec.y - rec.x + 1;
     // part i > 0 lies one slot before the regular stride
     auto at = [&](int i) { return part + i * stride - (i ? partial_floats(R) : 0); };
+    if (n <= kCombineFew) {                // rows c .. c + 3, once
+      const int cq = c + quarter;
+      if ((c & 3) || cq >= rec.z) continue;
+      float m = -INFINITY, l = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float* s = at(i);
+        const float mi = __ldcg(s + R * kDc + cq), li = __ldcg(s + R * kDc + R + cq);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(s + (int64_t)cq * kDc) + col);
+        const float top = fmaxf(m, mi), base = top == -INFINITY ? 0.f : top;
+        const float a = tc::ex2(m - base), b = tc::ex2(mi - base);
+        m = top;
+        l = l * a + li * b;
+        acc.x = acc.x * a + v.x * b;
+        acc.y = acc.y * a + v.y * b;
+        acc.z = acc.z * a + v.z * b;
+        acc.w = acc.w * a + v.w * b;
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      reinterpret_cast<uint2*>(p.o_lat + (row0 + cq) * kDc)[col] =
+          make_uint2(tc::half2_bits(acc.x * inv, acc.y * inv), tc::half2_bits(acc.z * inv, acc.w * inv));
+      continue;
+    }
     float mi[kCombineParts / kCombineThreads], li[kCombineParts / kCombineThreads], mx = -INFINITY;
 #pragma unroll
     for (int k = 0; k < kCombineParts / kCombineThreads; ++k) {
@@ -817,7 +848,7 @@ mla_status launch_r(const ChunkParams& p, cudaStream_t stream) {
   const mla_status st = cuda_status(launch_pdl(short_attention_kernel<LF, KF, R>, dim3(p.grid), dim3(Roles<R>::kThreads),
                                                Shape<LF, KF, R>::kBytes, stream, p));
   if (st != MLA_OK) return st;
-  return cuda_status(launch_pdl(short_combine_kernel, dim3(4 * p.grid), dim3(kCombineThreads), 0, stream, p, R));
+  return cuda_status(launch_pdl(short_combine_kernel, dim3(4 * p.grid + 1), dim3(kCombineThreads), 0, stream, p, R));
 }
 
 template <int LF, int KF>

@@ -99,14 +99,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   int64_t sum = 0;
   int err = 0;
 #pragma unroll
+  for (int k = 0; k < kPlanPer; ++k) {                 // all loads first: they are in flight together
+    const int b = b0 + k;
+    const bool mine = k < per && b < p.B;
+    ctx[k] = mine ? __ldcg(p.ctx + b) : 0;
+    nw[k] = mine ? __ldcg(p.nw + b) : 0;
+    row[k] = mine ? __ldcg(p.req + b) : -1;
+  }
+#pragma unroll
   for (int k = 0; k < kPlanPer; ++k) {
-    ctx[k] = nw[k] = 0;
-    row[k] = -1;
     const int b = b0 + k;
     if (k < per && b < p.B) {
-      ctx[k] = __ldcg(p.ctx + b);
-      nw[k] = __ldcg(p.nw + b);
-      row[k] = __ldcg(p.req + b);
       if (row[k] < 0 || row[k] >= p.rows) {
         err |= MLA_DEVERR_PAGE;
         row[k] = -1;

@@ -135,6 +135,12 @@ __device__ __forceinline__ void umma4(uint32_t d, uint64_t a, uint64_t b, uint32
       " add.s64 x, %1, %9;\n add.s64 y, %2, %10;\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, 1;\n}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(A), "n"(B), "n"(2 * A), "n"(2 * B), "n"(3 * A), "n"(3 * B));
 }
+// Fetches bytes to L2 ahead of a bulk copy.
+__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void prefetch_line(const void* src) { asm volatile("prefetch.global.L2 [%0];\n" ::"l"(src)); }
+
 // Over a cluster of two blocks: a copy into the same place of both, counted on
 // both blocks' barriers; a commit that arrives on both.
 __device__ __forceinline__ void bulk_copy_both(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
