@@ -518,20 +518,28 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
       const uint16_t* qn = p.qn + wk.h * p.qn_head + 8 * piece;
       const uint16_t* qp = p.qp + wk.h * p.qp_head + 8 * piece;
       uint8_t* q = sm + i * 3 * kBlkBytes;
-#pragma unroll 4
-      for (int e = 0; e < 8; ++e) {
-        const int r = 32 * (warp & 3) + 4 * e + (lane >> 3);
-        const bool real = tok0 + r < wk.s.n;
-        const int64_t tok = wk.s.q0 + (real ? tok0 + r : 0);
-        uint4 v[3] = {__ldcg(reinterpret_cast<const uint4*>(qn + tok * p.qn_tok)),
-                      __ldcg(reinterpret_cast<const uint4*>(qn + tok * p.qn_tok + 64)),
-                      __ldcg(reinterpret_cast<const uint4*>(qp + tok * p.qp_tok))};
 #pragma unroll
-        for (int c = 0; c < 3; ++c) {
-          if (!real) v[c] = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(q + c * kBlkBytes + r * 128 + ((piece ^ (r & 7)) << 4)) =
-              make_uint4(half2_bits(bf16lo(v[c].x), bf16hi(v[c].x)), half2_bits(bf16lo(v[c].y), bf16hi(v[c].y)),
-                         half2_bits(bf16lo(v[c].z), bf16hi(v[c].z)), half2_bits(bf16lo(v[c].w), bf16hi(v[c].w)));
+      for (int e0 = 0; e0 < 8; e0 += 4) {              // twelve loads in flight, then their stores
+        uint4 v[4][3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 32 * (warp & 3) + 4 * (e0 + e) + (lane >> 3);
+          const int64_t tok = wk.s.q0 + min(tok0 + r, wk.s.n - 1);
+          v[e][0] = __ldcg(reinterpret_cast<const uint4*>(qn + tok * p.qn_tok));
+          v[e][1] = __ldcg(reinterpret_cast<const uint4*>(qn + tok * p.qn_tok + 64));
+          v[e][2] = __ldcg(reinterpret_cast<const uint4*>(qp + tok * p.qp_tok));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 32 * (warp & 3) + 4 * (e0 + e) + (lane >> 3);
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            uint4 x = v[e][c];
+            if (tok0 + r >= wk.s.n) x = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(q + c * kBlkBytes + r * 128 + ((piece ^ (r & 7)) << 4)) =
+                make_uint4(half2_bits(bf16lo(x.x), bf16hi(x.x)), half2_bits(bf16lo(x.y), bf16hi(x.y)),
+                           half2_bits(bf16lo(x.z), bf16hi(x.z)), half2_bits(bf16lo(x.w), bf16hi(x.w)));
+          }
         }
       }
       fence_async_smem();
