@@ -333,7 +333,8 @@ def mla_lse_merge(o_parts, lse_parts, o_lat, lse=None, stream=None):
 
 # The serving-step calls run a few microseconds on the GPU, so their bindings
 # keep to cheap checks and pass addresses as plain integers.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _rows(t, shape, name):
@@ -352,14 +353,16 @@ def _flat(t, dtype, shape, name):
     return t.data_ptr()
 
 
-def _step(name, t, stream, *args):
-    """Calls the library on t's device: on ``stream``, or that device's current one."""
+def _step(fn, t, stream, *args):
+    """Calls a library function on t's device: on ``stream``, or that device's current one."""
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            _check(name, getattr(lib, name)(*args, stream.cuda_stream if stream is not None else _raw_stream(dev)))
+    if dev == _device():
+        status = fn(*args, stream.cuda_stream if stream is not None else _raw_stream(dev))
     else:
-        _check(name, getattr(lib, name)(*args, stream.cuda_stream if stream is not None else _raw_stream(dev)))
+        with torch.cuda.device(dev):
+            status = fn(*args, stream.cuda_stream if stream is not None else _raw_stream(dev))
+    if status:
+        _check(fn.__name__, status)
 
 
 def mla_plan_chunks(ctx_lens, new_lens, req, page_table, free_pages, free_range, num_pages, block_table, q_start,
@@ -372,7 +375,7 @@ def mla_plan_chunks(ctx_lens, new_lens, req, page_table, free_pages, free_range,
     B, n = ctx_lens.shape[0], slot.shape[0]
     rows, max_pages = page_table.shape
     i32 = torch.int32
-    _step("mla_plan_chunks", ctx_lens, stream,
+    _step(lib.mla_plan_chunks, ctx_lens, stream,
           _flat(ctx_lens, i32, (B,), "ctx_lens"), _flat(new_lens, i32, (B,), "new_lens"), _flat(req, i32, (B,), "req"), B,
           _flat(page_table, i32, (rows, max_pages), "page_table"), rows, max_pages,
           _flat(free_pages, i32, (free_pages.shape[0],), "free_pages"), free_pages.shape[0],
@@ -407,7 +410,7 @@ def mla_rope(q_pe, k_pe, positions, inv_freq, q_out, k_out, pair_axis=None, inte
         pair_axis = bytes(pair_axis)
         if len(pair_axis) != ROPE_DIM // 2:
             raise ValueError("pair_axis: expected %d axes" % (ROPE_DIM // 2))
-    _step("mla_rope", q_pe, stream, q_pe.data_ptr(), qs[0], qs[1], kp, ks[0],
+    _step(lib.mla_rope, q_pe, stream, q_pe.data_ptr(), qs[0], qs[1], kp, ks[0],
           _flat(positions, torch.int32, (n,) if positions.dim() == 1 else (axes, n), "positions"), axes, pair_axis,
           _flat(inv_freq, torch.float32, (ROPE_DIM // 2,), "inv_freq"), n, H, 1 if interleaved else 0, 1 if inverse else 0,
           amplitude, q_out.data_ptr(), qos[0], qos[1], ko, kos[0])
@@ -429,7 +432,7 @@ def mla_chunk_attention(cache, q_nope, q_pe, w_uk, w_uv, block_table, q_start, s
     qn, qp = _rows(q_nope, (n, H, QK_NOPE_DIM), "q_nope"), _rows(q_pe, (n, H, ROPE_DIM), "q_pe")
     bf16, i32 = torch.bfloat16, torch.int32
     cs = cache.c_struct()
-    _step("mla_chunk_attention", q_nope, stream, ctypes.byref(cs), q_nope.data_ptr(), qn[0], qn[1], q_pe.data_ptr(), qp[0], qp[1],
+    _step(lib.mla_chunk_attention, q_nope, stream, ctypes.byref(cs), q_nope.data_ptr(), qn[0], qn[1], q_pe.data_ptr(), qp[0], qp[1],
           _flat(w_uk, bf16, (H, QK_NOPE_DIM, KV_LORA_RANK), "w_uk"), _flat(w_uv, bf16, (H, KV_LORA_RANK, V_DIM), "w_uv"),
           _flat(block_table, i32, (B, max_pages), "block_table"), max_pages, _flat(q_start, i32, (B + 1,), "q_start"),
           _flat(seq_lens, i32, (B,), "seq_lens"), B, n, H, max_new, kv_tokens,

@@ -23,11 +23,14 @@
 namespace mla {
 namespace {
 
-constexpr int kPlanThreads = 512;
-constexpr int kPlanPer = kMaxBatch / kPlanThreads;      // requests per thread: 8
-static_assert(kPlanThreads * kPlanPer == kMaxBatch, "every request has a thread");
+// Requests per thread, at most: blocks of 256 threads for up to 1024 requests,
+// of 1024 threads beyond (every block scans all requests: at 4096 of them a
+// 512-thread block with eight each took 20 us, at 8 requests a small block's
+// barriers are the cheaper ones).
+constexpr int kPlanPer = 4;
+constexpr int kPlanSmall = 256, kPlanLarge = kMaxBatch / kPlanPer;
 constexpr int kPlanRowWords = kPlanMaxRows / 32;
-constexpr int kPlanAhead = 4;
+constexpr int kPlanAhead = 8;
 
 struct PlanParams {
   const int32_t *ctx, *nw, *req;
@@ -45,6 +48,7 @@ struct PlanParams {
 };
 
 // Exclusive scan over the block of one int64 per thread; *total = the sum.
+template <int T>
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* red, int64_t* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int64_t x = v;
@@ -56,35 +60,42 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* red, int64_t* 
   __syncthreads();                                     // an earlier scan's readers of red are done
   if (lane == 31) red[warp] = x;
   __syncthreads();
-  int64_t base = 0, sum = 0;
+  int64_t s = lane < T / 32 ? red[lane] : 0;
 #pragma unroll
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w < warp) base += red[w];
-    sum += red[w];
+  for (int o = 1; o < T / 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
   }
-  *total = sum;
-  return base + x - v;
+  *total = __shfl_sync(0xffffffffu, s, T / 32 - 1);
+  const int64_t base = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+  return (warp ? base : 0) + x - v;
 }
 
 __device__ __forceinline__ int pages_of(int tokens) { return (int)(((int64_t)tokens + kPage - 1) / kPage); }
 
-// Dynamic shared memory: q_start [B + 1], first [B] (pages before the
+// Where entry b of a per-request array lies: a thread's requests are contiguous,
+// so 32 threads write every 8th entry; shifted like this those fall in 32 banks.
+__device__ __forceinline__ int spread(int b) { return b + (b >> 5); }
+
+// Dynamic shared memory (entries spread): q_start [B + 1], first [B] (pages before the
 // request's own; -1: refused), ctx [B], pages in use after the step [B], table
 // row [B], then two bits per persistent row (seen, seen twice).
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
+template <int T>
+__global__ void __launch_bounds__(T) plan_kernel(const PlanParams p) {
   extern __shared__ int32_t plan_smem[];
-  __shared__ int64_t red[kPlanThreads / 32];
+  __shared__ int64_t red[T / 32];
   __shared__ int taken;
   int32_t* s_start = plan_smem;
-  int32_t* s_first = s_start + p.B + 1;
-  int32_t* s_ctx = s_first + p.B;
-  int32_t* s_now = s_ctx + p.B;
-  int32_t* s_row = s_now + p.B;
-  uint32_t* s_seen = reinterpret_cast<uint32_t*>(s_row + p.B);
+  const int room = spread(p.B) + 1;
+  int32_t* s_first = s_start + room;
+  int32_t* s_ctx = s_first + room;
+  int32_t* s_now = s_ctx + room;
+  int32_t* s_row = s_now + room;
+  uint32_t* s_seen = reinterpret_cast<uint32_t*>(s_row + room);
   const int row_words = (p.rows + 31) / 32;
   uint32_t* s_twice = s_seen + row_words;
   const int tid = threadIdx.x;
-  for (int i = tid; i < 2 * row_words; i += kPlanThreads) s_seen[i] = 0u;
+  for (int i = tid; i < 2 * row_words; i += T) s_seen[i] = 0u;
   if (tid == 0) taken = 0;
   pdl_launch_dependents();
   pdl_wait();
@@ -92,7 +103,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 
   // this thread's requests b0 .. b0 + per - 1, contiguous so that one scan
   // of the threads' sums orders them
-  const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
+  const int per = (p.B + T - 1) / T;
   const int b0 = tid * per;
   const int cap = p.max_pages * kPage;                 // fits: the host checks it
   int ctx[kPlanPer], nw[kPlanPer], row[kPlanPer];
@@ -127,13 +138,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     }
   }
   int64_t total;
-  int64_t at = block_scan(sum, red, &total);           // its barriers also order the seen bits
+  int64_t at = block_scan<T>(sum, red, &total);           // its barriers also order the seen bits
   int64_t need_sum = 0;
 #pragma unroll
   for (int k = 0; k < kPlanPer; ++k) {
     const int b = b0 + k;
     if (k < per && b < p.B) {
-      s_start[b] = (int)(at < p.n ? at : p.n);
+      s_start[spread(b)] = (int)(at < p.n ? at : p.n);
       at += nw[k];
       if (row[k] >= 0 && ((s_twice[row[k] >> 5] >> (row[k] & 31)) & 1u)) {
         err |= MLA_DEVERR_PAGE;
@@ -146,14 +157,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       if (row[k] >= 0) need_sum += pages_of(ctx[k] + nw[k]) - pages_of(ctx[k]);
     }
   }
-  if (tid == 0) s_start[p.B] = (int)(total < p.n ? total : p.n);
+  if (tid == 0) s_start[spread(p.B)] = (int)(total < p.n ? total : p.n);
   const int head = __ldcg(p.free_range), tail = __ldcg(p.free_range + 1);
   int avail = tail - head;
   if (head < 0 || tail > p.free_len || avail < 0) {
     err |= MLA_DEVERR_PAGE;
     avail = 0;
   }
-  int64_t first = block_scan(need_sum, red, &total);
+  int64_t first = block_scan<T>(need_sum, red, &total);
 #pragma unroll
   for (int k = 0; k < kPlanPer; ++k) {
     const int b = b0 + k;
@@ -171,12 +182,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
         }
         first += need;
       }
-      s_first[b] = f;
-      s_ctx[b] = ctx[k];
-      s_now[b] = f >= 0 ? pages_of(ctx[k] + nw[k]) : 0;
-      s_row[b] = row[k];
+      s_first[spread(b)] = f;
+      s_ctx[spread(b)] = ctx[k];
+      s_now[spread(b)] = f >= 0 ? pages_of(ctx[k] + nw[k]) : 0;
+      s_row[spread(b)] = row[k];
       if (blockIdx.x == 0) {
-        p.q_start[b] = s_start[b];
+        p.q_start[b] = s_start[spread(b)];
         p.seq_lens[b] = f >= 0 ? ctx[k] + nw[k] : 0;
       }
     }
@@ -185,30 +196,30 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   if (blockIdx.x == 0) {
     if (err) set_err(p.dev_err, err);
     if (tid == 0) {
-      p.q_start[p.B] = s_start[p.B];
+      p.q_start[p.B] = s_start[spread(p.B)];
       *p.free_head = head + taken;
     }
   }
 
-  const int64_t threads = (int64_t)gridDim.x * kPlanThreads, me = (int64_t)blockIdx.x * kPlanThreads + tid;
+  const int64_t threads = (int64_t)gridDim.x * T, me = (int64_t)blockIdx.x * T + tid;
   // ---- tokens
-  const int used = s_start[p.B];
+  const int used = s_start[spread(p.B)];
   for (int64_t i = me; i < p.n; i += threads) {
     int b = -1, pos = 0, slot = -1;
     if (i < used) {
-      int lo = 0, hi = p.B;                            // last b with s_start[b] <= i
+      int lo = 0, hi = p.B;                            // last b whose q_start is <= i
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (s_start[mid] <= i) lo = mid;
+        if (s_start[spread(mid)] <= i) lo = mid;
         else hi = mid;
       }
       b = lo;
-      if (s_first[b] >= 0) {
-        const int c = s_ctx[b];
-        pos = c + (int)(i - s_start[b]);
+      if (s_first[spread(b)] >= 0) {
+        const int c = s_ctx[spread(b)];
+        pos = c + (int)(i - s_start[spread(b)]);
         const int pg = pos / kPage, old = pages_of(c);
-        const int id = pg < old ? __ldcg(p.table + (int64_t)s_row[b] * p.max_pages + pg)
-                                : __ldcg(p.free_pages + head + s_first[b] + pg - old);
+        const int id = pg < old ? __ldcg(p.table + (int64_t)s_row[spread(b)] * p.max_pages + pg)
+                                : __ldcg(p.free_pages + head + s_first[spread(b)] + pg - old);
         if (id >= 0 && id < p.num_pages) slot = id * kPage + (pos & (kPage - 1));
         else set_err(p.dev_err, MLA_DEVERR_PAGE);
       }
@@ -217,36 +228,39 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     p.token_req[i] = b;
     p.slot[i] = slot;
   }
-  // ---- tables: a warp takes 32 columns of one row at a time, kPlanAhead such
-  // pieces with their loads in flight together
-  const int cols = (p.max_pages + 31) / 32, lane = tid & 31;
-  const int64_t pieces = (int64_t)p.B * cols, warps = threads >> 5;
-  for (int64_t w0 = me >> 5; w0 < pieces; w0 += warps * kPlanAhead) {
-    int id[kPlanAhead];
+  // ---- tables: a warp per row, or several warps on a row's columns when there
+  // are more warps; kPlanAhead pieces of 32 columns with their loads in flight
+  const int lane = tid & 31;
+  const int64_t warps = threads >> 5, wid = me >> 5;
+  const int split = (int)(warps / p.B > 1 ? warps / p.B : 1);
+  const int64_t lines = warps / split;                 // rows in work at a time
+  if (wid < lines * split) {
+    const int part = (int)(wid % split);
+    for (int64_t b = wid / split; b < p.B; b += lines) {
+      const int first = s_first[spread((int)b)], old = pages_of(s_ctx[spread((int)b)]), now = s_now[spread((int)b)];
+      int32_t* mine = p.table + (int64_t)max(s_row[spread((int)b)], 0) * p.max_pages;
+      int32_t* out = p.block_table + b * p.max_pages;
+      for (int64_t c0 = 32 * part + lane; c0 < p.max_pages; c0 += 32 * split * kPlanAhead) {
+        int id[kPlanAhead];
 #pragma unroll
-    for (int e = 0; e < kPlanAhead; ++e) {
-      const int64_t w = w0 + e * warps;
-      id[e] = -1;
-      if (w >= pieces) continue;
-      const int b = (int)(w / cols), pg = 32 * (int)(w % cols) + lane, old = pages_of(s_ctx[b]);
-      if (pg < s_now[b])
-        id[e] = pg < old ? __ldcg(p.table + (int64_t)s_row[b] * p.max_pages + pg)
-                         : __ldcg(p.free_pages + head + s_first[b] + pg - old);
-    }
-#pragma unroll
-    for (int e = 0; e < kPlanAhead; ++e) {
-      const int64_t w = w0 + e * warps;
-      if (w >= pieces) continue;
-      const int b = (int)(w / cols), pg = 32 * (int)(w % cols) + lane;
-      if (pg >= p.max_pages) continue;
-      if (pg < s_now[b]) {
-        if (id[e] < 0 || id[e] >= p.num_pages) {
-          set_err(p.dev_err, MLA_DEVERR_PAGE);
-          id[e] = -1;
+        for (int e = 0; e < kPlanAhead; ++e) {
+          const int64_t pg = c0 + 32 * split * e;
+          id[e] = pg >= now ? -1 : (pg < old ? __ldcg(mine + pg) : __ldcg(p.free_pages + head + first + pg - old));
         }
-        if (pg >= pages_of(s_ctx[b])) p.table[(int64_t)s_row[b] * p.max_pages + pg] = id[e];
+#pragma unroll
+        for (int e = 0; e < kPlanAhead; ++e) {
+          const int64_t pg = c0 + 32 * split * e;
+          if (pg >= p.max_pages) continue;
+          if (pg < now) {
+            if (id[e] < 0 || id[e] >= p.num_pages) {
+              set_err(p.dev_err, MLA_DEVERR_PAGE);
+              id[e] = -1;
+            }
+            if (pg >= old) mine[pg] = id[e];
+          }
+          out[pg] = id[e];
+        }
       }
-      p.block_table[(int64_t)b * p.max_pages + pg] = id[e];
     }
   }
 }
@@ -297,21 +311,27 @@ extern "C" mla_status mla_plan_chunks(const int32_t* ctx_lens, const int32_t* ne
   p.free_head = free_head;
   p.n = n_tokens;
   p.dev_err = dev_err;
-  const size_t smem = sizeof(int32_t) * ((size_t)5 * batch + 1 + 2 * ((rows + 31) / 32));
-  static int configured[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (smem > 48 * 1024 && (dev < 0 || dev >= 64 || !configured[dev])) {
-    const int most = (int)sizeof(int32_t) * (5 * kMaxBatch + 1 + 2 * kPlanRowWords);
-    const mla_status st =
-        cuda_status(cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
-    if (st != MLA_OK) return st;
-    if (dev >= 0 && dev < 64) configured[dev] = 1;
-  }
+  const size_t smem = sizeof(int32_t) * ((size_t)5 * (batch + batch / 32 + 1) + 2 * ((rows + 31) / 32));
   const int sms = device_sm_count();
+  const bool large = batch > kPlanSmall * kPlanPer;
+  const int block = large ? kPlanLarge : kPlanSmall;
+  if (smem > 48 * 1024) {                  // many rows or requests
+    static int configured[2][64] = {{0}};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !configured[large][dev]) {
+      const int most = (int)sizeof(int32_t) * (5 * (kMaxBatch + kMaxBatch / 32 + 1) + 2 * kPlanRowWords);
+      const mla_status st = cuda_status(
+          cudaFuncSetAttribute(large ? plan_kernel<kPlanLarge> : plan_kernel<kPlanSmall>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+      if (st != MLA_OK) return st;
+      if (dev >= 0 && dev < 64) configured[large][dev] = 1;
+    }
+  }
   const int64_t work = (int64_t)n_tokens + (int64_t)batch * max_pages;
-  const int64_t want = (work + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
-  const int64_t most = sms > 0 ? 2 * sms : 1;
+  const int64_t want = (work + 4 * block - 1) / (4 * block);
+  const int64_t most = sms > 0 ? (large ? sms : 2 * sms) : 1;
   const int grid = (int)(want < 1 ? 1 : (want < most ? want : most));
-  return cuda_status(launch_pdl(plan_kernel, dim3(grid), dim3(kPlanThreads), smem, (cudaStream_t)stream, p));
+  if (large) return cuda_status(launch_pdl(plan_kernel<kPlanLarge>, dim3(grid), dim3(block), smem, (cudaStream_t)stream, p));
+  return cuda_status(launch_pdl(plan_kernel<kPlanSmall>, dim3(grid), dim3(block), smem, (cudaStream_t)stream, p));
 }

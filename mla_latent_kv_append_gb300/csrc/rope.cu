@@ -70,6 +70,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     const int tok = (int)(w / p.groups), g = (int)(w % p.groups);
     const int r_lo = (int)((int64_t)p.rows * g / p.groups), r_hi = (int)((int64_t)p.rows * (g + 1) / p.groups);
     const int64_t at = __ldcg(p.pos + (int64_t)axis * p.n + tok);
+    uint4 a[kRopeUnroll], b[kRopeUnroll];
+    auto fetch = [&](int r0) {
+#pragma unroll
+      for (int u = 0; u < kRopeUnroll; ++u) {
+        const int r = r0 + u * kPer + sub;
+        if (r < r_hi) {
+          const uint16_t* src = r < p.H ? p.q + tok * p.q_tok + r * p.q_head : p.k + tok * p.k_tok;
+          a[u] = __ldcg(reinterpret_cast<const uint4*>(src + 8 * piece));
+          if (!INTERLEAVED) b[u] = __ldcg(reinterpret_cast<const uint4*>(src + kRopePairs + 8 * piece));
+        }
+      }
+    };
+    fetch(r_lo);                           // under way while the angles are computed
     const int32_t half_turns = (int32_t)(uint32_t)(((uint64_t)at * G) >> 32);   // units of 2^-31 half turns
     float sn, cs;
     sincospif((float)half_turns * 0x1p-31f, &sn, &cs);
@@ -82,16 +95,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
       s[i] = __shfl_sync(0xffffffffu, sn, kPer * piece + i);
     }
     for (int r0 = r_lo; r0 < r_hi; r0 += kPer * kRopeUnroll) {
-      uint4 a[kRopeUnroll], b[kRopeUnroll];
-#pragma unroll
-      for (int u = 0; u < kRopeUnroll; ++u) {
-        const int r = r0 + u * kPer + sub;
-        if (r < r_hi) {
-          const uint16_t* src = r < p.H ? p.q + tok * p.q_tok + r * p.q_head : p.k + tok * p.k_tok;
-          a[u] = __ldcg(reinterpret_cast<const uint4*>(src + 8 * piece));
-          if (!INTERLEAVED) b[u] = __ldcg(reinterpret_cast<const uint4*>(src + kRopePairs + 8 * piece));
-        }
-      }
+      if (r0 > r_lo) fetch(r0);
 #pragma unroll
       for (int u = 0; u < kRopeUnroll; ++u) {
         const int r = r0 + u * kPer + sub;
