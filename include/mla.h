@@ -99,8 +99,10 @@ typedef enum {
 
 /* Bits ORed into *dev_err. */
 #define MLA_DEVERR_SLOT    1  /* append: slot not in [0, num_pages*64) and not -1 */
-#define MLA_DEVERR_PAGE    2  /* decode: block_table entry not in [0, num_pages)   */
-#define MLA_DEVERR_SEQLEN  4  /* decode: seq_len < 0 or > max_pages*64            */
+#define MLA_DEVERR_PAGE    2  /* decode, chunks: block_table entry not in [0, num_pages);
+                                 plan: a page id, a table row or the free range */
+#define MLA_DEVERR_SEQLEN  4  /* decode: seq_len < 0 or > max_pages*64; plan, chunks:
+                                 lengths that do not fit the call's arrays */
 #define MLA_DEVERR_TIMEOUT 8  /* a bounded wait inside a kernel gave up           */
 #define MLA_DEVERR_NO_PAGES 16 /* plan: the free list has too few pages           */
 
@@ -578,21 +580,25 @@ mla_status mla_rope(const uint16_t* q_pe, int64_t q_token_stride, int64_t q_head
  *           the workspace are sized for
  *   kv_tokens bound on the sum of seq_lens, each rounded up to 128, over the
  *           sequences with more than MLA_CHUNK_SHORT new tokens (0 when
- *           there is none)
+ *           there is none); at most 2^23.  Those sequences' latents are
+ *           expanded into the workspace, 512 bytes per token and head
  *   workspace: device, >= mla_chunk_workspace_bytes(...) bytes, 256-byte
  *           aligned; contents are scratch, so calls that may overlap (other
  *           streams, two graphs replayed at once) need their own
  *   o       bf16 [n_tokens][H][128], 16-byte aligned.  Rows behind
  *           q_start[B] are left as they were.
  *   A page id outside the pool contributes nothing and sets MLA_DEVERR_PAGE.
- *   A sequence whose figures do not fit (negative or decreasing q_start,
- *   n_b > max_new, 0 < seq_lens[b] < n_b or > max_pages * 64, kv_tokens
- *   exceeded) sets MLA_DEVERR_SEQLEN; those of its rows that lie in the
- *   array are 0.
+ *   A sequence whose figures do not fit (n_b > max_new, 0 < seq_lens[b] <
+ *   n_b, seq_lens[b] < 0 or > max_pages * 64, kv_tokens exceeded: then every
+ *   later one that counts toward kv_tokens too) sets MLA_DEVERR_SEQLEN; its
+ *   rows are 0.  A q_start that decreases or leaves [0, n_tokens] anywhere
+ *   refuses all sequences, since their rows could overlap.
  *   Precision: fp16 operands, fp32 accumulation and softmax, one rounding of
- *   o to bf16.  Cached values, weights and products beyond 65504 in
- *   magnitude count as non-finite.  A non-finite token makes the rows that
- *   attend to it NaN and leaves the others alone.
+ *   o to bf16.  Queries (after the absorption and the scale), cached values,
+ *   weights, keys and values beyond 65504 in magnitude count as non-finite.
+ *   A non-finite token makes the rows that attend to it NaN and leaves the
+ *   others alone.  A wait that runs out (mla_set_wait_limit_ns) sets
+ *   MLA_DEVERR_TIMEOUT and leaves the rows of o undefined.
  *   batch <= 4096, n_tokens * H < 2^31; n_tokens == 0 or batch == 0 is a
  *   no-op.
  */
@@ -619,7 +625,7 @@ const char* mla_last_cuda_error(void);
 /*
  * mla_set_wait_limit_ns - bound, in nanoseconds, on every wait inside the
  * decode kernels (stage arrivals, the hand-offs between the block's warp
- * roles) of the decode and prefill calls this process launches afterwards;
+ * roles) of the decode, prefill and chunk calls this process launches afterwards;
  * returns the previous bound, or -1 (nothing changed) for ns < 0.  The
  * default is 10 s.  A test and diagnostic hook, not part of the pages'
  * method: a wait that runs out sets MLA_DEVERR_TIMEOUT in *dev_err, and its

@@ -8,8 +8,19 @@
 // 1088 operations per (query, head, key), and every cached byte serves all
 // heads.  Expanded, with keys c W_UK^T and values c W_UV made once per head:
 // 2 x 320 operations per (query, head, key), plus 2 x 512 x 256 per (key,
-// head).  Sequences with at most MLA_CHUNK_SHORT new tokens take the first
-// (chunk_short.cu).
+// head).  Sequences with at most MLA_CHUNK_SHORT = 64 new tokens take the
+// first (chunk_short.cuh), the others the second (chunk_long.cu).  The rule
+// looks at the new tokens alone: the absorbed form's time grows with them, the
+// expanded form's is flat up to 256 (one item per head), and where the two
+// meet hardly moves with the heads, the context or the batch.  INT8, absorbed
+// / expanded, microseconds per call:
+//                                  n = 32       48          64          96
+//   16 heads, 16 x  4000 cached   224/378    321/378     406/379     578/382
+//   64 heads,  1 x 30000          286/565    407/566     534/568     776/573
+//   64 heads, 16 x  4000          717/1194  1062/1180   1396/1181   2056/1198
+//  128 heads,  1 x 30000          536/1060   777/1057   1022/1064   1502/1068
+// The expanded form also needs 512 bytes of workspace per token and head,
+// which is why a draw goes to the absorbed one.
 //
 // This file: the device plan (which sequences take which path, prefix sums
 // of their work; lengths never visit the host), the query absorption, the
@@ -51,7 +62,9 @@ __device__ __forceinline__ int64_t scan(int64_t v, int64_t* red, int64_t* total)
 
 // chunk_plan_kernel: one block.  Checks every sequence, sorts it to a path,
 // and writes the path's records with the prefix sums of rows and work units.
-// Zeroes the rows of sequences that are empty or refused.
+// Zeroes the rows of sequences that are empty or refused.  Bound by the
+// latency of two dependent reads and the scans' barriers: about 3 us for up to
+// 128 sequences.
 __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const ChunkParams p, int R) {
   __shared__ int64_t red[32];
   __shared__ uint32_t zero_mask[kMaxBatch / 32];
@@ -227,7 +240,8 @@ __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0
 // rounding to fp16; its last 64 channels are q_pe, likewise.
 // Grid (H, 9, z), block 128: a CTA takes 64 channels of a head (y = 8: the
 // RoPE part, a copy) and every z-th 16-token tile.  The weight slice sits in
-// shared memory; a decode's cost is reading the weights once.
+// shared memory; a decode's cost is reading the weights once, most of it
+// during the plan.
 // ---------------------------------------------------------------------------
 constexpr int kAbWS = 64 + 8;        // W slice row stride: ldmatrix without conflicts
 constexpr int kAbAS = kDn + 8;
@@ -402,7 +416,7 @@ bool al(const void* p, uintptr_t a) { return p && ((uintptr_t)p & (a - 1)) == 0;
 bool sizes_ok(int batch, int n_tokens, int heads, int max_new, int64_t kv_tokens) {
   return batch >= 0 && batch <= kMaxBatch && n_tokens >= 0 && heads >= 16 && heads <= 128 && heads % 16 == 0 &&
          (int64_t)n_tokens * heads <= (int64_t)INT32_MAX && max_new >= 0 && max_new <= n_tokens && kv_tokens >= 0 &&
-         kv_tokens <= (int64_t)INT32_MAX;
+         kv_tokens <= kLongMost;
 }
 
 // Most new tokens that can belong to sequences of the short path.

@@ -42,6 +42,7 @@ struct ChunkCounts {
 };
 
 constexpr int kLongKeys = 128;               // long path: keys per tile
+constexpr int64_t kLongMost = 1 << 23;       // most cached tokens of a call's long path: the units of a head fit 31 bits
 constexpr int kLongRows = 256;               // query rows (tokens of one head) per item, two tiles of 128
 constexpr int kBlkBytes = 16384;             // 128 rows x 64 fp16, swizzled
 constexpr int kCTile = 8 * kBlkBytes;        // a key tile's latents
@@ -112,6 +113,8 @@ inline bool has_long(int max_new, int64_t kv_tokens) { return max_new > kChunkSh
 // The row tile's height for calls whose sequences have up to max_new tokens
 // of the short path: the smallest that holds all rows of a sequence, so that
 // a tile is read (and dequantized) once, up to 64, what shared memory holds.
+// A larger tile than the rows need costs MMA and softmax work for nothing: 32
+// sequences x 32768 tokens INT4 at 16 rows each, 204 us with R = 16.
 inline int short_rows_per_tile(int max_new, int heads) {
   const int n = max_new < kChunkShort ? max_new : kChunkShort;
   const int64_t rows = (int64_t)n * heads;

@@ -16,6 +16,11 @@
 // runs, one per SM; query tiles that fall into several runs leave fp32
 // partials that long_combine_kernel merges in block order.
 //
+// What bounds it: the MMAs.  Measured: 8192 tokens on their own, 64 heads, INT8:
+// 1.25 ms, 1.21 PFLOP/s of the formula's operations (64% of a library matrix
+// product's rate); 2048 tokens after 32768, 16 heads: 0.69 ms (65%); 54.9 and 5.9 ms
+// for the absorbed form's kernel.
+//
 // Rounding: latents, weights, keys, values, queries and P are fp16 (2^-11
 // relative each; bf16 queries and weights convert exactly within fp16's normal
 // range), all sums, scores, maxima and outputs fp32 until o is written.
@@ -36,7 +41,9 @@ constexpr float kSlack = 8.f;
 // long_prep_kernel: block x < 4 tiles: a 32-token block of a key tile, lane =
 // token, warp w dequantizes units w and w + 8, warps 0 and 1 the RoPE units;
 // the rows leave as 4 KB bulk stores (a lane's own 16-byte stores to its row
-// would touch 32 lines each).
+// would touch 32 lines each).  Bound by latency: the cache's block, its
+// conversion and the store follow one another, up to seven blocks per SM overlap;
+// 34816 tokens of INT8 and the weights of 16 heads: 19 us.
 // The blocks behind convert 64 latent channels of a head's weights each.
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 256;
@@ -164,6 +171,9 @@ __global__ void __launch_bounds__(kPrepThreads) long_prep_kernel(const ChunkPara
 // fetches half an item and multicasts it to both; and their latency wants 100
 // KB and more under way, which is why the latents are not in shared memory (64
 // KB under way: 10000 cycles per unit).
+// Measured: 34816 tokens, 16 heads: 106 us, 5100 cycles per unit (81% of the
+// MMAs' rate); with the latents in shared memory and 64 KB of weights under way
+// 136 us, without the multicast the same 136 (latency, not L2's rate, held it).
 // Warps: 0 copies, 1 MMAs, 4..7 epilogue (and the latents' way into TMEM).
 // ---------------------------------------------------------------------------
 constexpr int kExThreads = 256;
@@ -385,7 +395,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_
 // TMEM: S_0, S_1, O_0, O_1, 128 columns each.  Shared memory: the two query
 // tiles (96 KB) and a ring of eight 16 KB blocks that carries, per key tile,
 // two K blocks, the RoPE keys, two V blocks.
-// Warps: 0..3 and 4..7 softmax (thread = row), 8 copies, 9 MMAs.
+// Measured: 3550 cycles per key tile (73% of the MMAs' rate) on long runs; the
+// MMA thread waits 400 for the ring (a block of keys has 1600 cycles from its
+// slot's release to its use, an L2 fetch under load takes most of them) and 300
+// for P.
+// Warps: 0..3 and 4..7 softmax (thread = row), 8 copies, 9 MMAs, 10 fetches the
+// next item's query rows to L2.
 // ---------------------------------------------------------------------------
 constexpr int kLaThreads = 384;
 constexpr int kRing = 8;
@@ -401,13 +416,19 @@ static_assert(256 * kLaRegsSoftmax + 128 * kLaRegsIssue <= kLaThreads * 168 && k
               "the warpgroups' shares come out of the launch's registers");
 enum { aFull = 0, aEmpty = aFull + kRing, aQ = aEmpty + kRing, aS = aQ + 2, aP = aS + 2, aO = aP + 2, aFin = aO + 2, aCount };
 
+// A run's segments (a pair of query tiles of one head, key tiles t0 .. t1), the
+// last one first: the runs that share a head then read its tiles nearly in
+// step.  A run shorter than an item has its end in the middle of one: the
+// beginnings of items, read first, start together, and what is left of the
+// items before follows at the same distance behind in every run, so a tile
+// is still in L2 when its other readers come by.
 struct LongWalk {
   const LongSeq* seqs;
   int k;
-  int64_t u, hi;
+  int64_t lo, u;                   // the run's first unit, and the first one behind what is left
   LongSeq s;
   int h, pair, t0, t1, tiles0;     // tiles0: key tiles the pair's first query tile sees
-  bool first, last, two;           // two: the pair has a second query tile
+  bool started, first, last, two;  // two: the pair has a second query tile
 
   __device__ __forceinline__ void load() {
     const int4* r = reinterpret_cast<const int4*>(seqs + k);
@@ -416,49 +437,49 @@ struct LongWalk {
     d[1] = __ldcg(r + 1);
     d[2] = __ldcg(r + 2);
   }
-  __device__ __forceinline__ void start(const ChunkParams& p, int64_t lo, int64_t hi_) {
+  __device__ __forceinline__ void start(const ChunkParams& p, int64_t lo_, int64_t hi) {
     seqs = p.l_seqs;
-    u = lo;
-    hi = hi_;
-    pair = -1;
+    lo = lo_;
+    u = hi;
+    started = false;
     int n = __ldcg(&p.counts->l_seqs);
     k = 0;
     while (n - k > 1) {
       const int mid = (k + n) >> 1;
-      if (__ldcg(&seqs[mid].unit0) <= u) k = mid;
+      if (__ldcg(&seqs[mid].unit0) < u) k = mid;
       else n = mid;
     }
     load();
   }
   __device__ __forceinline__ bool next(int H) {
-    if (u >= hi) return false;
-    const int ctx = s.len - s.n;
-    int r = 0;
-    if (pair < 0) {                  // the run's first segment: wherever unit u lies
-      const int64_t d = u - s.unit0;
+    if (u <= lo) return false;
+    if (!started) {                  // the run's first segment: the one of unit u - 1
+      started = true;
+      const int64_t d = u - 1 - s.unit0;
       h = (int)(d / s.per_head);
-      r = (int)(d % s.per_head);
-      for (pair = 0; r >= pair_tiles(ctx, s.n, pair); ++pair) r -= pair_tiles(ctx, s.n, pair);
-    } else if (++pair * kLongRows >= s.n) {            // after it, item by item
-      pair = 0;
-      if (++h == H) {
-        h = 0;
-        ++k;
-        load();
-        return begin(0);
-      }
+      int r = (int)(d % s.per_head);
+      for (pair = 0; r >= pair_tiles(s.len - s.n, s.n, pair); ++pair) r -= pair_tiles(s.len - s.n, s.n, pair);
+      return begin(r + 1);
     }
-    return begin(r);
+    if (--pair < 0) {                // after it, item by item
+      if (--h < 0) {
+        --k;
+        load();
+        h = H - 1;
+      }
+      pair = (s.n - 1) / kLongRows;
+    }
+    return begin(pair_tiles(s.len - s.n, s.n, pair));
   }
-  __device__ __forceinline__ bool begin(int r) {
+  __device__ __forceinline__ bool begin(int end) {
     const int ctx = s.len - s.n, J = pair_tiles(ctx, s.n, pair);
-    t0 = r;
-    t1 = (int)min((int64_t)J, t0 + (hi - u));
+    t1 = end;
+    t0 = (int)max((int64_t)0, end - (u - lo));
     first = t0 == 0;
     last = t1 == J;
     two = s.n > pair * kLongRows + 128;
     tiles0 = two ? (ctx + pair * kLongRows + 128 + kLongKeys - 1) / kLongKeys : J;
-    u += t1 - t0;
+    u -= t1 - t0;
     return true;
   }
 };
@@ -639,7 +660,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
       const bool whole = wk.first && wk.last, opens = wk.first && !wk.last;       // whole: this block saw every key
       const int64_t out_row = (int64_t)(wk.s.q0 + tok0 + row) * p.H + wk.h;
       float* part = p.l_parts + (int64_t)(2 * x + (wk.first ? 1 : 0)) * long_partial_floats();
-      const int64_t end = wk.u - (wk.t1 - wk.t0) + pair_tiles(ctx, wk.s.n, wk.pair);
+      const int64_t end = wk.u + pair_tiles(ctx, wk.s.n, wk.pair);       // of the item, if it begins here
       SplitRec rec;
       rec.rows = min(kLongRows, wk.s.n - wk.pair * kLongRows);
       rec.row0 = (int64_t)(wk.s.q0 + wk.pair * kLongRows) * p.H + wk.h;
@@ -852,7 +873,8 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
 
 // long_combine_kernel: block 128, grid (splits, 16): a warp merges four rows of
 // a split item, their parts in block order with the running maximum's weights
-// (few parts per item, so one pass with all four rows' loads in flight).
+// (few parts per item, so one pass with all four rows' loads in flight).  Bound by
+// reading the partials, 132 KB each, from L2: 12 us for 151 split items.
 __global__ void __launch_bounds__(128) long_combine_kernel(const ChunkParams p) {
   pdl_launch_dependents();
   pdl_wait();

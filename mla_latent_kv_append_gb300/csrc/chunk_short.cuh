@@ -26,6 +26,15 @@
 // where they fit (the memory's latency wants 40 KB and more under way), the
 // rest pieces, so that the next tile is converted while this one is used.
 //
+// Measured (whole call, absorption and projection included): 32 sequences x
+// 32768 tokens, 16 heads, one new token each, INT4: 204 us, 3.0 TB/s of cache
+// (44% of a plain copy's rate).  24 ragged drafts at 64 heads, bf16 cache: 177
+// us.  One sequence of 4096 tokens, 16 heads, INT8: 29 us, of which this kernel
+// 9, all latency.  With R = 16 a key tile takes 3100 to 3400 cycles per SM,
+// 2400 of them shared-memory traffic that the split cannot avoid: 72 KB written
+// by the dequantization, 72 + 18 KB read by the S^T MMAs, 64 + 8 KB by the O^T
+// MMAs, the raw bytes in and out.
+//
 // Warps: 16 dequantize, 4 or 8 softmax (one group per 32 rows), then one each
 // issues the S^T MMAs, the O^T MMAs (apart, so that neither waits for the
 // other's operands) and the copies.
@@ -732,6 +741,10 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
 // fourth part each, so that the loads overlap, and are added in order.
 constexpr int kCombineThreads = 512;
 constexpr int kCombineParts = 1024;      // most parts per row: blocks of the attention
+// Up to 8 parts a row's merge is one batch of loads either way, and rows side by
+// side leave fewer idle threads (24 drafts, 2 to 3 parts a row: 28 us a row per
+// block, 12 us four rows per block); a single context of 4096 tokens has 64
+// parts, which one thread after the other would add up in 64 steps.
 constexpr int kCombineFew = 8;
 
 __global__ void __launch_bounds__(kCombineThreads) short_combine_kernel(const ChunkParams p, int R) {

@@ -66,7 +66,7 @@ def chunk(mla, cache=None, **bad):
 
 @pytest.mark.parametrize("bad", [
     {"batch": -1}, {"batch": 4097}, {"n": -1}, {"heads": 8}, {"heads": 24}, {"heads": 144}, {"max_new": -1}, {"max_new": 0},
-    {"max_new": 11}, {"kv": -1}, {"kv": 1 << 31}, {"scale": 0.0}, {"scale": float("nan")}, {"scale": float("inf")},
+    {"max_new": 11}, {"kv": -1}, {"kv": (1 << 23) + 1}, {"kv": 1 << 31}, {"scale": 0.0}, {"scale": float("nan")}, {"scale": float("inf")},
     {"max_pages": 0}, {"max_pages": I32MAX // 64 + 1}, {"qnt": -8}, {"qnh": 4}, {"qpt": 2}, {"qph": 100}, {"qn": None},
     {"qn": A + 8}, {"qp": None}, {"w_uk": None}, {"w_uv": A + 4}, {"table": None}, {"start": None}, {"lens": A + 1},
     {"ws": None}, {"ws": A + 16}, {"ws_bytes": 0}, {"o": None}, {"o": A + 8}, {"err": A + 1},
@@ -90,8 +90,10 @@ def test_chunk_workspace_sizes(mla):
     f = mla.mla_chunk_workspace_bytes
     assert f(4, 10, 16, 1) > 0
     for bad in [(-1, 10, 16, 1, 0), (4097, 10, 16, 1, 0), (4, -1, 16, 1, 0), (4, 10, 15, 1, 0), (4, 10, 16, 11, 0),
-                (4, 10, 16, 1, -1)]:
+                (4, 10, 16, 1, -1), (4, 300, 16, 300, (1 << 23) + 1)]:
         assert f(*bad) == 0
+    # 512 bytes per token and head for the expanded keys and values, at the largest too
+    assert f(4, 300, 16, 300, 1 << 23) >= 512 * 16 << 23
     # larger bounds never need less
     assert f(4, 20, 16, 1) >= f(4, 10, 16, 1)
     assert f(4, 300, 16, 300, 1024) >= f(4, 300, 16, 300, 512) >= f(4, 300, 16, 1, 0)
