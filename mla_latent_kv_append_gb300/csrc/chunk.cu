@@ -276,6 +276,9 @@ __global__ void __launch_bounds__(128) absorb_tiles_kernel(const ChunkParams p, 
     }
   }
   pdl_wait();
+  // the first tokens' records come along with their number (at most 15 places
+  // behind the list, still in the workspace)
+  const int2 first = tid < 16 ? __ldcg(p.s_toks + 16 * blockIdx.z + tid) : make_int2(0, 0);
   const int n = __ldcg(&p.counts->s_toks);
   if (16 * (int)blockIdx.z >= n) return;
   const uint32_t a_base = tc::smem_u32(as) + (((lane & 7) + 8 * ((lane >> 3) & 1)) * kAbAS + 8 * (lane >> 4)) * 2;
@@ -283,7 +286,7 @@ __global__ void __launch_bounds__(128) absorb_tiles_kernel(const ChunkParams p, 
       tc::smem_u32(ws) + (((lane & 7) + 8 * ((lane >> 3) & 1)) * kAbWS + 16 * warp + 8 * (lane >> 4)) * 2;
   for (int t0 = 16 * blockIdx.z; t0 < n; t0 += 16 * gridDim.z) {
     __syncthreads();
-    if (tid < 16) toks[tid] = t0 + tid < n ? __ldcg(p.s_toks + t0 + tid) : make_int2(-1, 0);
+    if (tid < 16) toks[tid] = t0 + tid >= n ? make_int2(-1, 0) : (t0 == 16 * (int)blockIdx.z ? first : __ldcg(p.s_toks + t0 + tid));
     __syncthreads();
     if (kb == 8) {
       for (int i = tid; i < 16 * 8; i += 128) {
@@ -457,6 +460,7 @@ int64_t carve(ChunkParams* p, char* base, int batch, int n_tokens, int heads, in
     off += align256(sizes[i]);
   }
   if (base) {
+    p->row_tiles = tiles;
     p->counts = (ChunkCounts*)at[0];
     p->s_seqs = (ShortSeq*)at[1];
     p->s_toks = (int2*)at[2];

@@ -41,6 +41,15 @@ struct ChunkCounts {
   int32_t s_splits, l_splits;      // entries of the split lists: counted by the attention kernels
 };
 
+// Run x of G equal runs over U units begins here; 32-bit arithmetic where it
+// suffices (a 64-bit division takes a few hundred cycles).
+__device__ __forceinline__ int64_t run_begin(int64_t U, int x, int G) {
+  if (U <= (int64_t)(0xFFFFFFFFu / 1024u)) return (uint32_t)U * (uint32_t)x / (uint32_t)G;
+  return U * x / G;
+}
+// The run that holds unit u: the last one that begins at or before it.
+__device__ __forceinline__ int run_of(int64_t U, int64_t u, int G) { return (int)(((u + 1) * G - 1) / U); }
+
 constexpr int kLongKeys = 128;               // long path: keys per tile
 constexpr int64_t kLongMost = 1 << 23;       // most cached tokens of a call's long path: the units of a head fit 31 bits
 constexpr int kLongRows = 256;               // query rows (tokens of one head) per item, two tiles of 128
@@ -89,6 +98,7 @@ struct ChunkParams {
   int32_t* dev_err;
   uint64_t wait_ns;
   int grid;               // blocks of the attention kernels
+  int64_t row_tiles;      // most row tiles of the short path
   // workspace
   ChunkCounts* counts;
   ShortSeq* s_seqs;

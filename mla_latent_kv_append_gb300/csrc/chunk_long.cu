@@ -17,8 +17,8 @@
 // partials that long_combine_kernel merges in block order.
 //
 // What bounds it: the MMAs.  Measured: 8192 tokens on their own, 64 heads, INT8:
-// 1.25 ms, 1.21 PFLOP/s of the formula's operations (64% of a library matrix
-// product's rate); 2048 tokens after 32768, 16 heads: 0.69 ms (65%); 54.9 and 5.9 ms
+// 1.10 ms, 1.37 PFLOP/s of the formula's operations (73% of a library matrix
+// product's rate); 2048 tokens after 32768, 16 heads: 0.57 ms (79%); 54.9 and 5.9 ms
 // for the absorbed form's kernel.
 //
 // Rounding: latents, weights, keys, values, queries and P are fp16 (2^-11
@@ -395,10 +395,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_
 // TMEM: S_0, S_1, O_0, O_1, 128 columns each.  Shared memory: the two query
 // tiles (96 KB) and a ring of eight 16 KB blocks that carries, per key tile,
 // two K blocks, the RoPE keys, two V blocks.
-// Measured: 3550 cycles per key tile (73% of the MMAs' rate) on long runs; the
-// MMA thread waits 400 for the ring (a block of keys has 1600 cycles from its
-// slot's release to its use, an L2 fetch under load takes most of them) and 300
-// for P.
+// Measured: 2048 tokens after 32768: 360 us; 8192 on their own at 64 heads: 870 us,
+// where the keys and values (268 MB) exceed L2: with all heads on four
+// heads' tiles, so that L2 holds them, 90 us less.  Cutting the runs in two or four, to
+// work on fewer heads at a time, costs more in split items than it saves (2% and 4%
+// slower).
 // Warps: 0..3 and 4..7 softmax (thread = row), 8 copies, 9 MMAs, 10 fetches the
 // next item's query rows to L2.
 // ---------------------------------------------------------------------------
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
   const int64_t U = __ldcg(&p.counts->l_units);
   const int G = (int)(U < gridDim.x ? U : gridDim.x), x = blockIdx.x;
   const bool work = x < G;
-  const int64_t lo = work ? U * x / G : 0, hi = work ? U * (x + 1) / G : 0;
+  const int64_t lo = work ? run_begin(U, x, G) : 0, hi = work ? run_begin(U, x + 1, G) : 0;
   bool ok = true;
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kLaRegsSoftmax));
@@ -702,10 +703,8 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
       }
       fence_before();
       if (opens && i == 0 && row == 0) {
-        int y = x + 1;
-        while (U * (y + 1) / G < end) ++y;
         rec.first = x;
-        rec.last = y;
+        rec.last = run_of(U, end - 1, G);
         rec.pad = 0;
         p.l_splits[atomicAdd(&p.counts->l_splits, 1)] = rec;
       }

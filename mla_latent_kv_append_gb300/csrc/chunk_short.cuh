@@ -29,8 +29,8 @@
 // Measured (whole call, absorption and projection included): 32 sequences x
 // 32768 tokens, 16 heads, one new token each, INT4: 204 us, 3.0 TB/s of cache
 // (44% of a plain copy's rate).  24 ragged drafts at 64 heads, bf16 cache: 177
-// us.  One sequence of 4096 tokens, 16 heads, INT8: 29 us, of which this kernel
-// 9, all latency.  With R = 16 a key tile takes 3100 to 3400 cycles per SM,
+// us.  One sequence of 4096 tokens, 16 heads, INT8: 21 us, of which this kernel
+// 8, all latency.  With R = 16 a key tile takes 3100 to 3400 cycles per SM,
 // 2400 of them shared-memory traffic that the split cannot avoid: 72 KB written
 // by the dequantization, 72 + 18 KB read by the S^T MMAs, 64 + 8 KB by the O^T
 // MMAs, the raw bytes in and out.
@@ -121,9 +121,16 @@ struct Walk {
     d[1] = __ldcg(r + 1);
     d[2] = __ldcg(r + 2);
   }
-  // All lanes of a warp: the sequence of unit u, 32 probes per round.
-  __device__ __forceinline__ void start(const ChunkParams& p, int64_t lo, int64_t hi_) {
+  // The first sequence's record comes along with their number (it lies in the
+  // workspace whether or not there is one).
+  __device__ __forceinline__ void open(const ChunkParams& p) {
     seqs = p.s_seqs;
+    k = 0;
+    load();
+    n_seqs = __ldcg(&p.counts->s_seqs);
+  }
+  // All lanes of a warp: the sequence of unit u, 32 probes per round.
+  __device__ __forceinline__ void start(int64_t lo, int64_t hi_) {
     u = lo;
     hi = hi_;
     item = -1;
@@ -139,7 +146,7 @@ struct Walk {
       a = na;
     }
     k = a;
-    load();
+    if (k > 0) load();
   }
   // The next segment; false behind the run's end.
   __device__ __forceinline__ bool next() {
@@ -230,7 +237,7 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
   const int G = (int)(U < gridDim.x ? U : gridDim.x);
   const int x = blockIdx.x;
   const bool work = x < G;
-  const int64_t lo = work ? U * x / G : 0, hi = work ? U * (x + 1) / G : 0;
+  const int64_t lo = work ? run_begin(U, x, G) : 0, hi = work ? run_begin(U, x + 1, G) : 0;
   bool ok = true;
   if (warp < 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(RO::kRegsConvert));
@@ -314,13 +321,13 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
     }
   } else if (warp < RO::kIssue) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(RO::kRegsSoftmax));
-    Walk wk;
-    wk.n_seqs = __ldcg(&p.counts->s_seqs);
     // ---- softmax.  A group of four warps has kGroupRows rows of the tile.
     // Thread (w, lane) holds keys 16 w + lane / 4 and + 8, rows 8 j + 2 (lane %
     // 4) and the next (j < J) of the group.  The group votes once per tile, so
     // its warps leave together: one that gave up a wait says so before a vote.
-    if (work) wk.start(p, lo, hi);
+    Walk wk;
+    wk.open(p);
+    if (work) wk.start(lo, hi);
     constexpr int GR = RO::kGroupRows, J = GR / 8;
     const int w = warp & 3, gq = (warp - RO::kSoftmax) >> 2, bar_id = 1 + gq;
     const uint32_t tl = (uint32_t)(32 * w) << 16;
@@ -559,11 +566,9 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
       if (wk.first && !wk.last && warp == RO::kSoftmax && lane == 0) {
         // the row tile goes on in the blocks behind: up to the one that holds its last unit
         const int64_t end = wk.s.unit0 + (int64_t)(wk.item + 1) * wk.s.tiles;
-        int y = x + 1;
-        while (U * (y + 1) / G < end) ++y;
         SplitRec rec;
         rec.first = x;
-        rec.last = y;
+        rec.last = run_of(U, end - 1, G);
         rec.rows = min(R, wk.s.n * p.H - wk.item * R);
         rec.pad = 0;
         rec.row0 = out0;
@@ -584,8 +589,8 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
     if (work && warp == RO::kIssue) {
       // ---- one thread: the query tiles' copies and the S^T MMAs
       Walk wk;
-      wk.n_seqs = __ldcg(&p.counts->s_seqs);
-      wk.start(p, lo, hi);
+      wk.open(p);
+      wk.start(lo, hi);
       if (elect_one()) {
         constexpr uint32_t kId = f16_idesc(64, R, false, false);
         constexpr int kQBytes = kQBlocks * R * 128;
@@ -647,8 +652,8 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
     } else if (work && warp == RO::kIssue + 1) {
       // ---- one thread: the O^T MMAs
       Walk wk;
-      wk.n_seqs = __ldcg(&p.counts->s_seqs);
-      wk.start(p, lo, hi);
+      wk.open(p);
+      wk.start(lo, hi);
       if (elect_one()) {
         constexpr uint32_t kId = f16_idesc(128, R, true, false);
         const uint64_t d_p = sw128_desc(sb + SH::kP, 16, 1024), d_v = sw128_desc(sb, kKeyBlk, 1024);
@@ -682,8 +687,8 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
       // ---- the cache's blocks into the raw slots.  The lanes fetch 32
       // page ids of the segment at a time, lane 0 issues.
       Walk wk;
-      wk.n_seqs = __ldcg(&p.counts->s_seqs);
-      wk.start(p, lo, hi);
+      wk.open(p);
+      wk.start(lo, hi);
       uint32_t blk = 0;
       while (ok && wk.next()) {
         const int32_t* pages = p.block_table + (int64_t)wk.s.b * p.max_pages;
@@ -735,39 +740,53 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
 
 // short_combine_kernel: the blocks stride over the rows of the split row
 // tiles.  A row's parts lie in the slots of its blocks, 2 first + 1 and then 2
-// (first + i), merged in that order.  Few parts: the block's quarters take a
-// row each.  Many (a single long context has a part in every block): the
-// parts' maxima and sums are read side by side, then the quarters add up every
-// fourth part each, so that the loads overlap, and are added in order.
+// (first + i), merged in that order.  Few parts: four groups of threads take a
+// row each.  Many (a single long context has a part in every block): the parts'
+// maxima and sums are read side by side, then every group adds up its share of
+// the parts, so that the loads overlap, and the groups are added in order.
+// With many rows a block takes whole rows (COLS = 1); where the call has few row
+// tiles for the SMs, so that rows are few and their parts many, four blocks
+// share a row by columns and have four times the groups (COLS = 4).  One
+// sequence of 4096 tokens: 23.5 us a call with COLS = 1, 20.8 with 4; 24 drafts
+// 175 and 293; 32 sequences of 32768 tokens 201 and 211.  Bound by latency in the
+// first case, by reading the partials from L2 in the others.
 constexpr int kCombineThreads = 512;
 constexpr int kCombineParts = 1024;      // most parts per row: blocks of the attention
 // Up to 8 parts a row's merge is one batch of loads either way, and rows side by
-// side leave fewer idle threads (24 drafts, 2 to 3 parts a row: 28 us a row per
-// block, 12 us four rows per block); a single context of 4096 tokens has 64
-// parts, which one thread after the other would add up in 64 steps.
+// side leave fewer idle threads (24 drafts: 198 us a call without this, 176
+// with it); a single context of 4096 tokens has 64 parts, which one thread after
+// the other would add up in 64 steps (42 us a call).
 constexpr int kCombineFew = 8;
 
-__global__ void __launch_bounds__(kCombineThreads) short_combine_kernel(const ChunkParams p, int R) {
+template <int COLS>
+__global__ void __launch_bounds__(kCombineThreads, 2) short_combine_kernel(const ChunkParams p, int R) {
+  constexpr int kWidth = 128 / COLS, kGroups = kCombineThreads / kWidth;       // 16-byte columns of a block, groups of threads
+  constexpr int kAhead = COLS == 1 ? 4 : 5;      // loads of a thread in flight: 32 and 80 parts a round
   __shared__ float s_w[kCombineParts];
   __shared__ float s_red[2][kCombineThreads / 32];
-  __shared__ float4 s_acc[3][128];
+  __shared__ float4 s_acc[kGroups - 1][kWidth];
   pdl_launch_dependents();
   pdl_wait();
-  const int tid = threadIdx.x, quarter = tid >> 7, col = tid & 127;
-  const int total = __ldcg(&p.counts->s_splits) * R;
+  const int tid = threadIdx.x, group = tid / kWidth, mine = tid % kWidth;
+  // the first record comes along with the count (its place is in the list:
+  // the blocks before it have 16 rows each at least)
+  int4 rec = __ldcg(reinterpret_cast<const int4*>(p.splits + blockIdx.x / (R * COLS)));
+  int64_t row0 = __ldcg(&p.splits[blockIdx.x / (R * COLS)].row0);
+  const int total = __ldcg(&p.counts->s_splits) * R * COLS;
   for (int w = blockIdx.x; w < total; w += gridDim.x) {
-    const SplitRec* sr = p.splits + w / R;
-    const int c = w % R;
-    const int4 rec = __ldcg(reinterpret_cast<const int4*>(sr));
-    const int64_t row0 = __ldcg(&sr->row0);
+    const int c = w / COLS % R, col = w % COLS * kWidth + mine;
+    if (w != (int)blockIdx.x) {
+      rec = __ldcg(reinterpret_cast<const int4*>(p.splits + w / (R * COLS)));
+      row0 = __ldcg(&p.splits[w / (R * COLS)].row0);
+    }
     if (c >= rec.z) continue;              // the same for the whole block
     const int64_t stride = 2 * partial_floats(R);
     const float* part = p.parts + (int64_t)(2 * rec.x + 1) * partial_floats(R);
     const int n = rec.y - rec.x + 1;
     // part i > 0 lies one slot before the regular stride
     auto at = [&](int i) { return part + i * stride - (i ? partial_floats(R) : 0); };
-    if (n <= kCombineFew) {                // rows c .. c + 3, once
-      const int cq = c + quarter;
+    if (COLS == 1 && n <= kCombineFew) {   // rows c .. c + 3, once
+      const int cq = c + group;
       if ((c & 3) || cq >= rec.z) continue;
       float m = -INFINITY, l = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -790,6 +809,14 @@ __global__ void __launch_bounds__(kCombineThreads) short_combine_kernel(const Ch
           make_uint2(tc::half2_bits(acc.x * inv, acc.y * inv), tc::half2_bits(acc.z * inv, acc.w * inv));
       continue;
     }
+    // the first parts are under way while the weights are made
+    float4 v[kAhead];
+    auto fetch = [&](int i0) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (i0 + kGroups * k < n) v[k] = __ldcg(reinterpret_cast<const float4*>(at(i0 + kGroups * k) + (int64_t)c * kDc) + col);
+    };
+    fetch(group);
     float mi[kCombineParts / kCombineThreads], li[kCombineParts / kCombineThreads], mx = -INFINITY;
 #pragma unroll
     for (int k = 0; k < kCombineParts / kCombineThreads; ++k) {
@@ -816,25 +843,28 @@ __global__ void __launch_bounds__(kCombineThreads) short_combine_kernel(const Ch
     if ((tid & 31) == 0) s_red[1][tid >> 5] = l;
     __syncthreads();
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = quarter; i < n; i += 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(at(i) + (int64_t)c * kDc) + col);
-      const float wt = s_w[i];
-      acc.x = fmaf(wt, v.x, acc.x);
-      acc.y = fmaf(wt, v.y, acc.y);
-      acc.z = fmaf(wt, v.z, acc.z);
-      acc.w = fmaf(wt, v.w, acc.w);
+    for (int i0 = group; i0 < n; i0 += kGroups * kAhead) {
+      if (i0 != group) fetch(i0);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (i0 + kGroups * k >= n) break;
+        const float wt = s_w[i0 + kGroups * k];
+        acc.x = fmaf(wt, v[k].x, acc.x);
+        acc.y = fmaf(wt, v[k].y, acc.y);
+        acc.z = fmaf(wt, v[k].z, acc.z);
+        acc.w = fmaf(wt, v[k].w, acc.w);
+      }
     }
-    if (quarter) s_acc[quarter - 1][col] = acc;
+    if (group) s_acc[group - 1][mine] = acc;
     __syncthreads();
-    if (!quarter) {
+    if (!group) {
       l = 0.f;
 #pragma unroll
       for (int k = 0; k < kCombineThreads / 32; ++k) l += s_red[1][k];
       const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const float4 a = s_acc[k][col];
+      for (int k = 0; k < kGroups - 1; ++k) {
+        const float4 a = s_acc[k][mine];
         acc.x += a.x;
         acc.y += a.y;
         acc.z += a.z;
@@ -861,7 +891,9 @@ mla_status launch_r(const ChunkParams& p, cudaStream_t stream) {
   const mla_status st = cuda_status(launch_pdl(short_attention_kernel<LF, KF, R>, dim3(p.grid), dim3(Roles<R>::kThreads),
                                                Shape<LF, KF, R>::kBytes, stream, p));
   if (st != MLA_OK) return st;
-  return cuda_status(launch_pdl(short_combine_kernel, dim3(4 * p.grid + 1), dim3(kCombineThreads), 0, stream, p, R));
+  const dim3 grid(4 * p.grid + 1), block(kCombineThreads);
+  if (p.row_tiles * kCombineFew <= p.grid) return cuda_status(launch_pdl(short_combine_kernel<4>, grid, block, 0, stream, p, R));
+  return cuda_status(launch_pdl(short_combine_kernel<1>, grid, block, 0, stream, p, R));
 }
 
 template <int LF, int KF>

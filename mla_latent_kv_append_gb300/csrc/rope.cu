@@ -21,8 +21,8 @@
 // tokens, so the fp64 constant is paid once per warp.
 //
 // Measured: 8192 tokens x 128 heads (271 MB) 47 us, 5.8 TB/s or 85% of a plain
-// copy's rate; 1 MB-sized calls that L2 holds, 2048 tokens x 63 rows (33 MB),
-// 10.6 us; 8 tokens x 16 heads 2.7 us, latency.
+// copy's rate; 1999 tokens x 64 heads, pairs in halves (33 MB, which L2 holds), 10.6
+// us; 8 tokens x 16 heads 2.7 us, latency.
 #include <math.h>
 
 #include "mla_internal.cuh"
