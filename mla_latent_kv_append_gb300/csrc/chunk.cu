@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
     tiles[k] = (len[k] + kKeyTile - 1) / kKeyTile;
     // at most 2^12 sequences, 2^18 tokens and 2^22 row tiles: one word
     mine += ((int64_t)1 << 48) + ((int64_t)items[k] << 20) + n[k];
-    units += (int64_t)items[k] * tiles[k];
+    units += (int64_t)items[k] * (tiles[k] + kItemCost);
   }
   int64_t total, total_units;
   int64_t at = scan(mine, red, &total), unit = scan(units, red, &total_units);
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
     p.s_seqs[at >> 48] = s;
     for (int i = 0; i < n[k]; ++i) p.s_toks[s.tok0 + i] = make_int2(q0[k] + i, s.item0 * R + i * p.H);
     at += ((int64_t)1 << 48) + ((int64_t)items[k] << 20) + n[k];
-    unit += (int64_t)items[k] * tiles[k];
+    unit += (int64_t)items[k] * (tiles[k] + kItemCost);
   }
   ChunkCounts c = {};
   c.s_seqs = (int)(total >> 48);

@@ -7,11 +7,16 @@ namespace mla {
 
 constexpr int kChunkShort = MLA_CHUNK_SHORT;
 constexpr int kKeyTile = kPage;              // short path: keys per tile, one page
+constexpr int kItemCost = 4;                 // 38 drafts of 2 and 2 chunks of 1023: 145 us a call with 0, 133 with 2, 129 with 4, 130 with 6;
+                                             // 24 drafts of 5 at 64 heads 174, 167, 165, 167; 32 x 32768 201, 200, 202, 203
 constexpr int kQBlocks = (kDc + kDr) / 64;   // 9 blocks of 64 channels
 
 // One sequence of the short path (at most kChunkShort new tokens), in the
 // order of the batch.  Its rows r = i H + h (new token i, head h) are cut
-// into row tiles of R rows; a unit of work is one key tile of one row tile.
+// into row tiles of R rows; a unit of work is one key tile of one row tile, after
+// kItemCost units for what a row tile costs by itself (its queries' way in, its
+// output's way out, a pipeline that runs empty in between): without these a run
+// of short contexts takes twice as long as one out of the middle of a long one.
 struct __align__(16) ShortSeq {
   int64_t unit0;          // units before this sequence's
   int32_t b, q0, n, len;  // batch index, first token row, new tokens, cached tokens (the new ones included)

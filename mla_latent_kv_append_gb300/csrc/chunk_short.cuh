@@ -102,8 +102,8 @@ struct Shape {
 // Barriers: per piece of the ring, and per RoPE block, "written" and "free";
 // S^T and P per score buffer; O^T of a tile done; raw slots.
 enum { bWritten = 0, bFree = bWritten + kMaxPieces, bRopeW = bFree + kMaxPieces, bRopeF = bRopeW + 2, bS = bRopeF + 2,
-       bP = bS + 2, bO = bP + 2, bRaw, bRawFree = bRaw + kMaxSlots, bQ = bRawFree + kMaxSlots, bFinS, bFinO, bCount };
-static_assert(8 * bCount + 72 + 4 * kMaxSlots <= 512, "barriers and words");
+       bP = bS + 2, bO = bP + 2, bRaw, bRawFree = bRaw + kMaxSlots, bQ = bRawFree + kMaxSlots, bFinS, bFinO, bTiles, bCount };
+static_assert(8 * bCount + 76 + 4 * kMaxSlots <= 512, "barriers and words");
 
 // One run's walk over the units: segments (a row tile, key tiles t0 .. t1).
 struct Walk {
@@ -111,7 +111,7 @@ struct Walk {
   int n_seqs, k;
   int64_t u, hi;
   ShortSeq s;
-  int item, t0, t1;
+  int item, t0, t1, skip;   // skip: key tiles of the first segment's row tile before the run
   bool first, last;         // the segment holds the row tile's first / last key tile
 
   __device__ __forceinline__ void load() {
@@ -130,10 +130,7 @@ struct Walk {
     n_seqs = __ldcg(&p.counts->s_seqs);
   }
   // All lanes of a warp: the sequence of unit u, 32 probes per round.
-  __device__ __forceinline__ void start(int64_t lo, int64_t hi_) {
-    u = lo;
-    hi = hi_;
-    item = -1;
+  __device__ __forceinline__ void find(int64_t u) {
     const int lane = threadIdx.x & 31;
     int a = 0, n = n_seqs;                   // the answer is in [a, a + n)
     while (n > 1) {
@@ -145,28 +142,42 @@ struct Walk {
       n = min(step, a + n - na);
       a = na;
     }
-    k = a;
-    if (k > 0) load();
+    if (a != k) {
+      k = a;
+      load();
+    }
   }
-  // The next segment; false behind the run's end.
+  // All lanes of a warp: key tiles before unit v.
+  __device__ __forceinline__ int64_t tiles_before(int64_t v) {
+    find(v);
+    const int cost = s.tiles + kItemCost;
+    const int64_t d = v - s.unit0, at = d / cost;
+    return s.unit0 - (int64_t)kItemCost * s.item0 + at * s.tiles + max((int)(d - at * cost) - kItemCost, 0);
+  }
+  __device__ __forceinline__ void start(int64_t lo, int64_t hi_) {
+    u = lo;
+    hi = hi_;
+    find(u);
+    const int64_t d = u - s.unit0;
+    const int cost = s.tiles + kItemCost, r = (int)(d % cost);
+    item = (int)(d / cost) - 1;
+    skip = max(r - kItemCost, 0);
+    u += max(kItemCost - r, 0);
+  }
+  // The next segment; false behind the run's end.  u: the unit of the next key tile.
   __device__ __forceinline__ bool next() {
     if (u >= hi) return false;
-    if (item < 0) {                  // the run's first segment: wherever unit u lies
-      const int64_t d = u - s.unit0;
-      item = (int)(d / s.tiles);
-      t0 = (int)(d % s.tiles);
-    } else {                         // after it, row tile by row tile
-      t0 = 0;
-      if (++item == s.items) {
-        item = 0;
-        ++k;
-        load();
-      }
+    if (++item == s.items) {
+      item = 0;
+      ++k;
+      load();
     }
+    t0 = skip;
+    skip = 0;
     t1 = (int)min((int64_t)s.tiles, t0 + (hi - u));
     first = t0 == 0;
     last = t1 == s.tiles;
-    u += t1 - t0;
+    u += t1 - t0 + kItemCost;
     return true;
   }
 };
@@ -196,6 +207,7 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
   volatile int* quit = reinterpret_cast<volatile int*>(words + 8);           // [groups][2, by tile parity]
   volatile int* tile_ok = reinterpret_cast<volatile int*>(words + 24);       // [4, by tile]
   uint32_t* bad = reinterpret_cast<uint32_t*>(words + 40);                   // [4, by tile][2]: a bit per token
+  volatile uint32_t* run_tiles = reinterpret_cast<volatile uint32_t*>(words + 72 + 4 * kMaxSlots);
   volatile int* slot_len = reinterpret_cast<volatile int*>(words + 72);      // [slots] tokens of the block, -1: no page
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kCols = R == 64 ? 512 : 8 * R;       // 6 R columns used, a power of two allocated
@@ -219,6 +231,7 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
     bar_init(bars + 8 * bQ, 1);
     bar_init(bars + 8 * bFinS, 1);
     bar_init(bars + 8 * bFinO, 1);
+    bar_init(bars + 8 * bTiles, 1);
     *abort = 0;
     for (int i = 0; i < 4; ++i) quit[i] = 0;
     for (int i = 0; i < 8; ++i) bad[i] = 0;
@@ -246,8 +259,12 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
     // block's unit w % 2 of block w / 2 % 2 (the four warps of a piece in turn:
     // always the same ones were a third slower than the rest); lane = token.
     const int s = warp >> 2, rope_half = (warp >> 1) & 1;
-    const uint32_t n_tiles = (uint32_t)(hi - lo);      // none in a block without work
     uint32_t piece = s, round = 0;                     // the ring's piece for this tile, and how often it went round
+    uint32_t n_tiles = 0;                              // of the run: the last warp counts them
+    if (work) {
+      if (warp_wait(bars + 8 * bTiles, 0, p.wait_ns, abort)) n_tiles = *run_tiles;
+      else ok = false;
+    }
     for (uint32_t it = 0; it < n_tiles; ++it) {
       const uint32_t f = it & 3;                       // the tile's flags
       const bool rope = (int)(it & 3) == s;
@@ -565,7 +582,7 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
       }
       if (wk.first && !wk.last && warp == RO::kSoftmax && lane == 0) {
         // the row tile goes on in the blocks behind: up to the one that holds its last unit
-        const int64_t end = wk.s.unit0 + (int64_t)(wk.item + 1) * wk.s.tiles;
+        const int64_t end = wk.s.unit0 + (int64_t)(wk.item + 1) * (wk.s.tiles + kItemCost);
         SplitRec rec;
         rec.first = x;
         rec.last = run_of(U, end - 1, G);
@@ -728,6 +745,17 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
       // the copies in flight land before the block ends
       for (uint32_t s = 0; s < NS; ++s)
         if (blk > s) drain_wait(bars + 8 * (bRaw + s), ((blk - 1 - s) / NS) & 1);
+    } else if (work && warp == RO::kIssue + 3) {
+      // ---- the run's key tiles, for the converting warps (counted in a
+      // softmax warp they cost its loop registers: 201 -> 208 us for 32 x 32768)
+      Walk wk;
+      wk.open(p);
+      const int64_t all = U - (int64_t)kItemCost * __ldcg(&p.counts->s_items);
+      const int64_t n = (x + 1 == G ? all : wk.tiles_before(hi)) - wk.tiles_before(lo);
+      if (lane == 0) {
+        *run_tiles = (uint32_t)n;
+        bar_arrive(bars + 8 * bTiles);
+      }
     }
   }
   fence_before();

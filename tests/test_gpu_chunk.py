@@ -171,6 +171,18 @@ def test_many_sequences(mla):
     t.check(o, heads=slice(5, 7))
 
 
+@pytest.mark.parametrize("B", [2, 30, 31, 151, 153, 310, 700])
+@pytest.mark.parametrize("most", [64, 200])
+def test_runs_that_end_between_sequences(mla, B, most):
+    """Contexts of one to four pages: an SM's run ends before, at and behind
+    a sequence's first page, and holds several sequences or none."""
+    t = Batch(mla, [((37 * b + 11 * B) % most, 1 + (b % 5 == 3)) for b in range(B)], 16, seed=B)
+    o = t.call()
+    torch.cuda.synchronize()
+    assert t.err.item() == 0
+    t.check(o)
+
+
 def test_many_chunks(mla):
     r = np.random.default_rng(6)
     t = Batch(mla, [(int(r.integers(0, 300)), int(r.integers(60, 200))) for _ in range(12)], 16)
