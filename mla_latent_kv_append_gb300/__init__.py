@@ -353,6 +353,15 @@ def _flat(t, dtype, shape, name):
     return t.data_ptr()
 
 
+def _err(t):
+    """The address of an error word, or None."""
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or not t.is_cuda:
+        raise ValueError("dev_err: expected CUDA int32, got %s on %s" % (t.dtype, t.device))
+    return t.data_ptr()
+
+
 def _step(fn, t, stream, *args):
     """Calls a library function on t's device: on ``stream``, or that device's current one."""
     dev = t.get_device()
@@ -383,7 +392,7 @@ def mla_plan_chunks(ctx_lens, new_lens, req, page_table, free_pages, free_range,
           _flat(block_table, i32, (B, max_pages), "block_table"), _flat(q_start, i32, (B + 1,), "q_start"),
           _flat(seq_lens, i32, (B,), "seq_lens"), _flat(positions, i32, (n,), "positions"),
           _flat(token_req, i32, (n,), "token_req"), _flat(slot, i32, (n,), "slot"), _flat(free_head, i32, (1,), "free_head"),
-          None if dev_err is None else dev_err.data_ptr())
+          _err(dev_err))
 
 
 def mla_rope(q_pe, k_pe, positions, inv_freq, q_out, k_out, pair_axis=None, interleaved=True, inverse=False,
@@ -431,6 +440,8 @@ def mla_chunk_attention(cache, q_nope, q_pe, w_uk, w_uv, block_table, q_start, s
     B, max_pages = block_table.shape
     qn, qp = _rows(q_nope, (n, H, QK_NOPE_DIM), "q_nope"), _rows(q_pe, (n, H, ROPE_DIM), "q_pe")
     bf16, i32 = torch.bfloat16, torch.int32
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous CUDA tensor")
     cs = cache.c_struct()
     _step(lib.mla_chunk_attention, q_nope, stream, ctypes.byref(cs), q_nope.data_ptr(), qn[0], qn[1], q_pe.data_ptr(), qp[0], qp[1],
           _flat(w_uk, bf16, (H, QK_NOPE_DIM, KV_LORA_RANK), "w_uk"), _flat(w_uv, bf16, (H, KV_LORA_RANK, V_DIM), "w_uv"),
@@ -438,7 +449,7 @@ def mla_chunk_attention(cache, q_nope, q_pe, w_uk, w_uv, block_table, q_start, s
           _flat(seq_lens, i32, (B,), "seq_lens"), B, n, H, max_new, kv_tokens,
           DEFAULT_SOFTMAX_SCALE if softmax_scale is None else softmax_scale, workspace.data_ptr(),
           workspace.numel() * workspace.element_size(), _flat(o, bf16, (n, H, V_DIM), "o"),
-          None if dev_err is None else dev_err.data_ptr())
+          _err(dev_err))
 
 
 def mla_set_prefill_path(path):

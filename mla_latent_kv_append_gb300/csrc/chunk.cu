@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
         bad = zero = true;
         atomicOr(zero_mask + ((b0 + k) >> 5), 1u << ((b0 + k) & 31));
       } else {
-        for (int pr = 0; pr * kLongRows < n[k]; ++pr) per_head[k] += pair_tiles(len[k] - n[k], n[k], pr);
+        for (int pr = 0; pr * kLongRows < n[k]; ++pr) per_head[k] += pair_tiles(len[k] - n[k], n[k], pr) + kPairCost;
         l_units += (int64_t)per_head[k] * p.H;
         ++served;
         served_tiles += tiles[k];

@@ -28,7 +28,8 @@ struct __align__(16) ShortSeq {
 static_assert(sizeof(ShortSeq) == 48, "three 16-byte loads");
 
 // One sequence of the long path.  Its new tokens are cut into pairs of 128-row
-// query tiles; a unit is one 128-key tile of one pair of one head.
+// query tiles; a unit is one 128-key tile of one pair of one head, after
+// kPairCost units for what a pair costs by itself.
 struct __align__(16) LongSeq {
   int64_t unit0;          // units before this sequence's
   int32_t b, q0, n, len;  // batch index, first token row, new tokens, cached tokens (the new ones included)
@@ -57,6 +58,8 @@ __device__ __forceinline__ int run_of(int64_t U, int64_t u, int G) { return (int
 
 constexpr int kLongKeys = 128;               // long path: keys per tile
 constexpr int64_t kLongMost = 1 << 23;       // most cached tokens of a call's long path: the units of a head fit 31 bits
+constexpr int kPairCost = 3;                 // 38 drafts of 2 and 2 chunks of 1023: 128 us a call with 0, 126 with 1, 123.5 with 2 and 3; an
+                                             // 8192-token prompt at 64 heads 1138, 1126, 1133, 1091
 constexpr int kLongRows = 256;               // query rows (tokens of one head) per item, two tiles of 128
 constexpr int kBlkBytes = 16384;             // 128 rows x 64 fp16, swizzled
 constexpr int kCTile = 8 * kBlkBytes;        // a key tile's latents

@@ -395,11 +395,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_
 // TMEM: S_0, S_1, O_0, O_1, 128 columns each.  Shared memory: the two query
 // tiles (96 KB) and a ring of eight 16 KB blocks that carries, per key tile,
 // two K blocks, the RoPE keys, two V blocks.
-// Measured: 2048 tokens after 32768: 360 us; 8192 on their own at 64 heads: 870 us,
-// where the keys and values (268 MB) exceed L2: with all heads on four
-// heads' tiles, so that L2 holds them, 90 us less.  Cutting the runs in two or four, to
-// work on fewer heads at a time, costs more in split items than it saves (2% and 4%
-// slower).
+// Measured (profiler): 2048 tokens after 32768, 16 heads: 412 us, tensor pipe 77%
+// active, 0.34 GB from DRAM (460 us and 2.3 GB while runs began with their first
+// item).  8192 tokens on their own, 64 heads: tensor pipe 71% active, 3.8 GB from
+// DRAM, since the keys and values (268 MB) exceed L2: with all heads on four
+// heads' tiles, so that L2 holds them, a call takes 10% less.  Cutting the runs in
+// two or four, to work on fewer heads at a time, costs more in split items than
+// it saves (2% and 4% slower).
 // Warps: 0..3 and 4..7 softmax (thread = row), 8 copies, 9 MMAs, 10 fetches the
 // next item's query rows to L2.
 // ---------------------------------------------------------------------------
@@ -459,8 +461,10 @@ struct LongWalk {
       const int64_t d = u - 1 - s.unit0;
       h = (int)(d / s.per_head);
       int r = (int)(d % s.per_head);
-      for (pair = 0; r >= pair_tiles(s.len - s.n, s.n, pair); ++pair) r -= pair_tiles(s.len - s.n, s.n, pair);
-      return begin(r + 1);
+      for (pair = 0; r >= pair_tiles(s.len - s.n, s.n, pair) + kPairCost; ++pair) r -= pair_tiles(s.len - s.n, s.n, pair) + kPairCost;
+      if (r >= kPairCost) return begin(r + 1 - kPairCost);
+      u -= r + 1;                    // the run ends before the pair's first key tile: its next one has the pair
+      if (u <= lo) return false;
     }
     if (--pair < 0) {                // after it, item by item
       if (--h < 0) {
@@ -480,7 +484,7 @@ struct LongWalk {
     last = t1 == J;
     two = s.n > pair * kLongRows + 128;
     tiles0 = two ? (ctx + pair * kLongRows + 128 + kLongKeys - 1) / kLongKeys : J;
-    u -= t1 - t0;
+    u -= t1 - t0 + (first ? kPairCost : 0);
     return true;
   }
 };
@@ -661,7 +665,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
       const bool whole = wk.first && wk.last, opens = wk.first && !wk.last;       // whole: this block saw every key
       const int64_t out_row = (int64_t)(wk.s.q0 + tok0 + row) * p.H + wk.h;
       float* part = p.l_parts + (int64_t)(2 * x + (wk.first ? 1 : 0)) * long_partial_floats();
-      const int64_t end = wk.u + pair_tiles(ctx, wk.s.n, wk.pair);       // of the item, if it begins here
+      const int64_t end = wk.u + kPairCost + pair_tiles(ctx, wk.s.n, wk.pair);       // of the item, if it begins here
       SplitRec rec;
       rec.rows = min(kLongRows, wk.s.n - wk.pair * kLongRows);
       rec.row0 = (int64_t)(wk.s.q0 + wk.pair * kLongRows) * p.H + wk.h;

@@ -183,6 +183,16 @@ def test_runs_that_end_between_sequences(mla, B, most):
     t.check(o)
 
 
+@pytest.mark.parametrize("B", [3, 9, 10, 38, 77])
+@pytest.mark.parametrize("n", [65, 300])
+def test_runs_that_end_between_chunks(mla, B, n):
+    t = Batch(mla, [((53 * b) % 130, n - b % 2) for b in range(B)], 16, seed=B)
+    o = t.call()
+    torch.cuda.synchronize()
+    assert t.err.item() == 0
+    t.check(o, heads=[0, 7, 15])
+
+
 def test_many_chunks(mla):
     r = np.random.default_rng(6)
     t = Batch(mla, [(int(r.integers(0, 300)), int(r.integers(60, 200))) for _ in range(12)], 16)

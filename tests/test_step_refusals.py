@@ -97,3 +97,18 @@ def test_chunk_workspace_sizes(mla):
     # larger bounds never need less
     assert f(4, 20, 16, 1) >= f(4, 10, 16, 1)
     assert f(4, 300, 16, 300, 1024) >= f(4, 300, 16, 300, 512) >= f(4, 300, 16, 1, 0)
+
+
+def test_bindings_refuse_host_tensors(mla):
+    torch = pytest.importorskip("torch")
+    i = lambda *n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
+    h = lambda *n: torch.zeros(n, dtype=torch.bfloat16)  # noqa: E731
+    with pytest.raises(ValueError):
+        mla.mla_plan_chunks(i(2), i(2), i(2), i(4, 3), i(5), i(2), 9, i(2, 3), i(3), i(2), i(7), i(7), i(7), i(1))
+    with pytest.raises(ValueError):
+        mla.mla_rope(h(5, 16, 64), h(5, 64), i(5), torch.zeros(32), h(5, 16, 64), h(5, 64))
+    with pytest.raises(ValueError):
+        mla.mla_chunk_attention(None, h(5, 16, 128), h(5, 16, 64), h(16, 128, 512), h(16, 512, 128), i(2, 3), i(3), i(2),
+                                torch.zeros(1 << 10, dtype=torch.uint8), h(5, 16, 128), max_new=4)
+    with pytest.raises(ValueError):
+        mla._err(i(1))
