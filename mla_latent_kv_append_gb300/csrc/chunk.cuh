@@ -131,8 +131,10 @@ inline bool has_long(int max_new, int64_t kv_tokens) { return max_new > kChunkSh
 // The row tile's height for calls whose sequences have up to max_new tokens
 // of the short path: the smallest that holds all rows of a sequence, so that
 // a tile is read (and dequantized) once, up to 64, what shared memory holds.
-// A larger tile than the rows need costs MMA and softmax work for nothing: 32
-// sequences x 32768 tokens INT4 at 16 rows each, 204 us with R = 16.
+// A larger tile than the rows need costs MMA and softmax work for nothing (32
+// sequences x 32768 tokens INT4 at 16 rows each: 201, 244 and 308 us with 16, 32
+// and 64), a smaller one converts the keys again (24 drafts of 5 at 64 heads, bf16:
+// 165 us with 64, 233 with 32).
 inline int short_rows_per_tile(int max_new, int heads) {
   const int n = max_new < kChunkShort ? max_new : kChunkShort;
   const int64_t rows = (int64_t)n * heads;

@@ -27,13 +27,15 @@
 // rest pieces, so that the next tile is converted while this one is used.
 //
 // Measured (whole call, absorption and projection included): 32 sequences x
-// 32768 tokens, 16 heads, one new token each, INT4: 204 us, 3.0 TB/s of cache
-// (44% of a plain copy's rate).  24 ragged drafts at 64 heads, bf16 cache: 177
+// 32768 tokens, 16 heads, one new token each, INT4: 201 us, 3.0 TB/s of cache
+// (45% of a plain copy's rate).  24 ragged drafts at 64 heads, bf16 cache: 165
 // us.  One sequence of 4096 tokens, 16 heads, INT8: 21 us, of which this kernel
-// 8, all latency.  With R = 16 a key tile takes 3100 to 3400 cycles per SM,
+// 9, all latency.  With R = 16 a key tile takes 3100 to 3400 cycles per SM,
 // 2400 of them shared-memory traffic that the split cannot avoid: 72 KB written
 // by the dequantization, 72 + 18 KB read by the S^T MMAs, 64 + 8 KB by the O^T
-// MMAs, the raw bytes in and out.
+// MMAs, the raw bytes in and out.  With R = 64 and a bf16 cache (5000 cycles) the
+// queries and the raw blocks leave room for one key tile, so its steps and the
+// next tile's follow one another; 1950 of the cycles are MMAs.
 //
 // Warps: 16 dequantize, 4 or 8 softmax (one group per 32 rows), then one each
 // issues the S^T MMAs, the O^T MMAs (apart, so that neither waits for the
