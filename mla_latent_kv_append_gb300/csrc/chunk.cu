@@ -36,6 +36,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanPer = kMaxBatch / kPlanThreads;      // sequences per thread: 4
+constexpr int kPlanFused = 128;                         // most sequences the absorption plans itself: a thread each
 
 // Exclusive block scan of one int64 per thread.
 __device__ __forceinline__ int64_t scan(int64_t v, int64_t* red, int64_t* total) {
@@ -60,24 +61,25 @@ __device__ __forceinline__ int64_t scan(int64_t v, int64_t* red, int64_t* total)
   return (warp ? base : 0) + x - v;
 }
 
-// chunk_plan_kernel: one block.  Checks every sequence, sorts it to a path,
-// and writes the path's records with the prefix sums of rows and work units.
-// Zeroes the rows of sequences that are empty or refused.  Bound by the
-// latency of two dependent reads and the scans' barriers: about 3 us for up to
-// 128 sequences.
-__global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const ChunkParams p, int R) {
-  __shared__ int64_t red[32];
-  __shared__ uint32_t zero_mask[kMaxBatch / 32];
-  pdl_launch_dependents();
-  pdl_wait();
+// Checks every sequence, sorts it to a path, and makes the path's records with
+// the prefix sums of rows and work units.  Up to PER sequences per thread of the
+// block.  Returns the short path's number of tokens; note(record, first token
+// row, its short-path tokens and row tiles before it) is called for each of its
+// sequences by some thread.  One block of a grid has write set: it also writes
+// the records and counts, reports what does not fit, and zeroes the rows of
+// sequences that are empty or refused.
+template <int PER, class Note>
+__device__ __forceinline__ int plan_sequences(const ChunkParams& p, int R, bool write, int64_t* red, uint32_t* zero_mask,
+                                              Note note) {
   const int tid = threadIdx.x;
-  const bool long_path = p.l_seqs != nullptr;
-  for (int i = tid; i < kMaxBatch / 32; i += blockDim.x) zero_mask[i] = 0;
-  const int per = (p.B + blockDim.x - 1) / blockDim.x, b0 = tid * per;
-  int q0[kPlanPer], n[kPlanPer], len[kPlanPer];
+  const bool long_path = PER > 1 && p.l_seqs != nullptr;
+  if (write)
+    for (int i = tid; i < kMaxBatch / 32; i += blockDim.x) zero_mask[i] = 0;
+  const int per = PER == 1 ? 1 : (p.B + blockDim.x - 1) / blockDim.x, b0 = tid * per;
+  int q0[PER], n[PER], len[PER];
   bool order = true;
 #pragma unroll
-  for (int k = 0; k < kPlanPer; ++k) {
+  for (int k = 0; k < PER; ++k) {
     const int b = b0 + k;
     q0[k] = n[k] = len[k] = 0;
     if (k < per && b < p.B) {
@@ -92,10 +94,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
   const bool ordered = !__syncthreads_or(!order);
   int64_t mine = 0, units = 0, l_mine = 0;
   bool bad = !ordered, zero = false;
-  int items[kPlanPer], tiles[kPlanPer];
-  bool is_long[kPlanPer];
+  int items[PER], tiles[PER];
+  bool is_long[PER];
 #pragma unroll
-  for (int k = 0; k < kPlanPer; ++k) {
+  for (int k = 0; k < PER; ++k) {
     const int b = b0 + k;
     items[k] = tiles[k] = 0;
     is_long[k] = false;
@@ -120,11 +122,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
     mine += ((int64_t)1 << 48) + ((int64_t)items[k] << 20) + n[k];
     units += (int64_t)items[k] * (tiles[k] + kItemCost);
   }
-  int64_t total, total_units;
-  int64_t at = scan(mine, red, &total), unit = scan(units, red, &total_units);
+  int64_t total, total_units = 0, unit = 0;
+  int64_t at = scan(mine, red, &total);
+  if (write) unit = scan(units, red, &total_units);
 #pragma unroll
-  for (int k = 0; k < kPlanPer; ++k) {
+  for (int k = 0; k < PER; ++k) {
     if (items[k] == 0) continue;
+    note((int)(at >> 48), q0[k], (int)(at & 0xFFFFF), (int)((at >> 20) & 0xFFFFFFF));
+    if (!write) continue;
     ShortSeq s;
     s.unit0 = unit;
     s.b = b0 + k;
@@ -140,6 +145,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
     at += ((int64_t)1 << 48) + ((int64_t)items[k] << 20) + n[k];
     unit += (int64_t)items[k] * (tiles[k] + kItemCost);
   }
+  if (!write) return (int)(total & 0xFFFFF);
   ChunkCounts c = {};
   c.s_seqs = (int)(total >> 48);
   c.s_items = (int)((total >> 20) & 0xFFFFFFF);
@@ -152,10 +158,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
     int64_t l_at = scan(l_mine, red, &l_total);
     const int64_t room = p.kv_tokens / kLongKeys;
     int64_t kv = l_at & 0xFFFFFFFFFFFF;
-    int per_head[kPlanPer];
+    int per_head[PER];
     int served = 0, served_tiles = 0;
 #pragma unroll
-    for (int k = 0; k < kPlanPer; ++k) {
+    for (int k = 0; k < PER; ++k) {
       per_head[k] = 0;
       if (!is_long[k]) continue;
       if (kv + tiles[k] > room) {
@@ -174,7 +180,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
     int64_t kv_at = l_at & 0xFFFFFFFFFFFF, rec = l_at >> 48;
     // the served sequences are a prefix of the long ones, so the scans of all of them place them
 #pragma unroll
-    for (int k = 0; k < kPlanPer; ++k) {
+    for (int k = 0; k < PER; ++k) {
       if (!is_long[k]) continue;
       LongSeq s;
       s.unit0 = l_unit;
@@ -207,6 +213,18 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const Chunk
         rows[i] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
+  return c.s_toks;
+}
+
+// chunk_plan_kernel: the plan by one block of its own, for calls with a long path
+// or more than kPlanFused sequences.  Bound by the latency of two dependent
+// reads and the scans' barriers: about 3 us for up to 128 sequences.
+__global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const ChunkParams p, int R) {
+  __shared__ int64_t red[32];
+  __shared__ uint32_t zero_mask[kMaxBatch / 32];
+  pdl_launch_dependents();
+  pdl_wait();
+  plan_sequences<kPlanPer>(p, R, true, red, zero_mask, [](int, int, int, int) {});
 }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t* r) {
@@ -242,6 +260,10 @@ __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0
 // RoPE part, a copy) and every z-th 16-token tile.  The weight slice sits in
 // shared memory; a decode's cost is reading the weights once, most of it
 // during the plan.
+// PLAN: the call has at most kPlanFused sequences and no long path: every block
+// makes the plan for itself (three words per sequence) instead of waiting for a
+// kernel that does, and one of them writes it down.  One sequence of 4096 tokens
+// 20.7 us a call with the plan's own kernel, 19.0 without; 24 drafts 164.8 and 163.3.
 // ---------------------------------------------------------------------------
 constexpr int kAbWS = 64 + 8;        // W slice row stride: ldmatrix without conflicts
 constexpr int kAbAS = kDn + 8;
@@ -253,6 +275,7 @@ __device__ __forceinline__ uint32_t* tile_word(const ChunkParams& p, int R, int6
                                      (((c >> 3) ^ (rr & 7)) << 4) + (c & 7) * 2);
 }
 
+template <bool PLAN>
 __global__ void __launch_bounds__(128) absorb_tiles_kernel(const ChunkParams p, int R) {
   pdl_launch_dependents();
   __shared__ __align__(16) uint16_t ws[kDn * kAbWS];
@@ -276,17 +299,54 @@ __global__ void __launch_bounds__(128) absorb_tiles_kernel(const ChunkParams p, 
     }
   }
   pdl_wait();
-  // the first tokens' records come along with their number (at most 15 places
-  // behind the list, still in the workspace)
-  const int2 first = tid < 16 ? __ldcg(p.s_toks + 16 * blockIdx.z + tid) : make_int2(0, 0);
-  const int n = __ldcg(&p.counts->s_toks);
+  __shared__ int3 seqs[PLAN ? kPlanFused : 1];       // first token row, short-path tokens and row tiles before
+  int n, n_seqs = 0;
+  int2 first = make_int2(0, 0);
+  if constexpr (PLAN) {
+    __shared__ int64_t red[32];
+    __shared__ uint32_t zero_mask[kMaxBatch / 32];
+    __shared__ int used;
+    if (tid == 0) used = 0;
+    // (the scan's barriers lie between)
+    n = plan_sequences<1>(p, R, blockIdx.x == 0 && kb == 8 && blockIdx.z == 0, red, zero_mask,
+                          [&](int rec, int q0, int tok0, int item0) {
+                            seqs[rec] = make_int3(q0, tok0, item0);
+                            atomicMax(&used, rec + 1);
+                          });
+    __syncthreads();
+    n_seqs = used;
+  } else {
+    // the first tokens' records come along with their number (at most 15 places
+    // behind the list, still in the workspace)
+    if (tid < 16) first = __ldcg(p.s_toks + 16 * blockIdx.z + tid);
+    n = __ldcg(&p.counts->s_toks);
+  }
+  // short-path token t: its row, and its first row in the padded row tiles
+  auto token = [&](int t) -> int2 {
+    if constexpr (PLAN) {
+      int lo = 0, m = n_seqs;                            // the last sequence with tok0 <= t
+      while (m > 1) {
+        const int half = m >> 1;
+        if (seqs[lo + half].y <= t) {
+          lo += half;
+          m -= half;
+        } else {
+          m = half;
+        }
+      }
+      const int i = t - seqs[lo].y;
+      return make_int2(seqs[lo].x + i, seqs[lo].z * R + i * p.H);
+    } else {
+      return t < 16 * (int)blockIdx.z + 16 ? first : __ldcg(p.s_toks + t);
+    }
+  };
   if (16 * (int)blockIdx.z >= n) return;
   const uint32_t a_base = tc::smem_u32(as) + (((lane & 7) + 8 * ((lane >> 3) & 1)) * kAbAS + 8 * (lane >> 4)) * 2;
   const uint32_t b_base =
       tc::smem_u32(ws) + (((lane & 7) + 8 * ((lane >> 3) & 1)) * kAbWS + 16 * warp + 8 * (lane >> 4)) * 2;
   for (int t0 = 16 * blockIdx.z; t0 < n; t0 += 16 * gridDim.z) {
     __syncthreads();
-    if (tid < 16) toks[tid] = t0 + tid >= n ? make_int2(-1, 0) : (t0 == 16 * (int)blockIdx.z ? first : __ldcg(p.s_toks + t0 + tid));
+    if (tid < 16) toks[tid] = t0 + tid < n ? token(t0 + tid) : make_int2(-1, 0);
     __syncthreads();
     if (kb == 8) {
       for (int i = tid; i < 16 * 8; i += 128) {
@@ -546,10 +606,14 @@ mla_status mla_chunk_attention(const mla_cache_layer* cache, const uint16_t* q_n
   p.wait_ns = wait_limit_ns();
   const cudaStream_t st = (cudaStream_t)stream;
   const int R = short_rows_per_tile(max_new, heads);
-  // a thread per sequence; small blocks synchronise faster
-  const int plan_threads = batch <= 128 ? 128 : (batch <= 512 ? 512 : kPlanThreads);
-  mla_status s = cuda_status(launch_pdl(chunk_plan_kernel, dim3(1), dim3(plan_threads), 0, st, p, R));
-  if (s != MLA_OK) return s;
+  const bool fused = batch <= kPlanFused && !p.l_seqs;
+  mla_status s = MLA_OK;
+  if (!fused) {
+    // a thread per sequence; small blocks synchronise faster
+    const int plan_threads = batch <= 128 ? 128 : (batch <= 512 ? 512 : kPlanThreads);
+    s = cuda_status(launch_pdl(chunk_plan_kernel, dim3(1), dim3(plan_threads), 0, st, p, R));
+    if (s != MLA_OK) return s;
+  }
   if (p.l_seqs) {
     s = launch_long(p, cache->latent_fmt, cache->kpe_fmt, st);
     if (s != MLA_OK) return s;
@@ -557,7 +621,9 @@ mla_status mla_chunk_attention(const mla_cache_layer* cache, const uint16_t* q_n
   // 16-token tiles of the projections: enough CTAs for four per SM
   const int tok_tiles = (int)((short_tokens(batch, n_tokens, max_new) + 15) / 16);
   const int za = 4 * p.grid / (9 * heads) + 1, zp = 4 * p.grid / (4 * heads) + 1;
-  s = cuda_status(launch_pdl(absorb_tiles_kernel, dim3(heads, 9, tok_tiles < za ? tok_tiles : za), dim3(128), 0, st, p, R));
+  const dim3 ga(heads, 9, tok_tiles < za ? tok_tiles : za);
+  s = fused ? cuda_status(launch_pdl(absorb_tiles_kernel<true>, ga, dim3(128), 0, st, p, R))
+            : cuda_status(launch_pdl(absorb_tiles_kernel<false>, ga, dim3(128), 0, st, p, R));
   if (s != MLA_OK) return s;
   const int lf = cache->latent_fmt, kf = cache->kpe_fmt;
   s = lf == MLA_FMT_BF16       ? launch_short_bf16(p, lf, kf, R, st)

@@ -27,9 +27,9 @@
 // rest pieces, so that the next tile is converted while this one is used.
 //
 // Measured (whole call, absorption and projection included): 32 sequences x
-// 32768 tokens, 16 heads, one new token each, INT4: 201 us, 3.0 TB/s of cache
-// (45% of a plain copy's rate).  24 ragged drafts at 64 heads, bf16 cache: 165
-// us.  One sequence of 4096 tokens, 16 heads, INT8: 21 us, of which this kernel
+// 32768 tokens, 16 heads, one new token each, INT4: 200 us, 3.0 TB/s of cache
+// (45% of a plain copy's rate).  24 ragged drafts at 64 heads, bf16 cache: 163
+// us.  One sequence of 4096 tokens, 16 heads, INT8: 19 us, of which this kernel
 // 9, all latency.  With R = 16 a key tile takes 3100 to 3400 cycles per SM,
 // 2400 of them shared-memory traffic that the split cannot avoid: 72 KB written
 // by the dequantization, 72 + 18 KB read by the S^T MMAs, 64 + 8 KB by the O^T
