@@ -257,6 +257,25 @@ def test_more_keys_than_announced(mla):
     t.check(o, seqs=[0, 1, 3])
 
 
+def test_chunk_without_room_for_any(mla):
+    """kv_tokens 0: chunks are refused, the decodes around them are served."""
+    t = Batch(mla, [(70, 1), (10, 65), (200, 2)], 16)
+    o = t.call(kv_tokens=0)
+    torch.cuda.synchronize()
+    assert t.err.item() == mla.DEVERR_SEQLEN
+    assert not o[1:66].any()
+    t.check(o, seqs=[0, 2])
+
+
+@pytest.mark.parametrize("B", [127, 128, 129])
+def test_batches_around_a_block_of_sequences(mla, B):
+    t = Batch(mla, [((29 * b) % 100, (b + 1) % 3) for b in range(B)], 32, seed=B)
+    o = t.call()
+    torch.cuda.synchronize()
+    assert t.err.item() == 0
+    t.check(o, heads=[3, 31])
+
+
 def test_row_starts_out_of_order(mla):
     t = Batch(mla, [(10, 2), (20, 4), (30, 3)], 16)
     for start in ([0, 6, 2, 9], [-3, 2, 6, 9], [0, 2, 6, 900]):
