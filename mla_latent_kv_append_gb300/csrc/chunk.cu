@@ -15,10 +15,10 @@
 // meet hardly moves with the heads, the context or the batch.  INT8, absorbed
 // / expanded, microseconds per call:
 //                                  n = 32       48          64          96
-//   16 heads, 16 x  4000 cached   224/378    321/378     406/379     578/382
-//   64 heads,  1 x 30000          286/565    407/566     534/568     776/573
-//   64 heads, 16 x  4000          717/1194  1062/1180   1396/1181   2056/1198
-//  128 heads,  1 x 30000          536/1060   777/1057   1022/1064   1502/1068
+//   16 heads, 16 x  4000 cached   223/379    310/379     399/381     571/383
+//   64 heads,  1 x 30000          279/566    402/567     524/569     765/573
+//   64 heads, 16 x  4000          709/1181  1051/1178   1384/1185   2044/1196
+//  128 heads,  1 x 30000          524/1069   768/1068   1004/1075   1490/1077
 // The expanded form also needs 512 bytes of workspace per token and head,
 // which is why a draw goes to the absorbed one.
 //
