@@ -341,9 +341,23 @@ __global__ void __launch_bounds__(128) absorb_tiles_kernel(const ChunkParams p, 
     }
   };
   if (16 * (int)blockIdx.z >= n) return;
+  auto token_row = [&](int t) -> int64_t {
+    if constexpr (PLAN) return token(t).x;
+    else return __ldcg(&p.s_toks[t].x);
+  };
   const uint32_t a_base = tc::smem_u32(as) + (((lane & 7) + 8 * ((lane >> 3) & 1)) * kAbAS + 8 * (lane >> 4)) * 2;
   const uint32_t b_base =
       tc::smem_u32(ws) + (((lane & 7) + 8 * ((lane >> 3) & 1)) * kAbWS + 16 * warp + 8 * (lane >> 4)) * 2;
+  uint4 v[2];
+  auto fetch = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = t0 + 8 * i + (tid >> 4);
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (t < n) v[i] = __ldcg(reinterpret_cast<const uint4*>(p.qn + token_row(t) * p.qn_tok + h * p.qn_head + 8 * (tid & 15)));
+    }
+  };
+  if (kb < 8) fetch(16 * blockIdx.z);
   for (int t0 = 16 * blockIdx.z; t0 < n; t0 += 16 * gridDim.z) {
     __syncthreads();
     if (tid < 16) toks[tid] = t0 + tid < n ? token(t0 + tid) : make_int2(-1, 0);
@@ -362,12 +376,9 @@ __global__ void __launch_bounds__(128) absorb_tiles_kernel(const ChunkParams p, 
       }
       continue;
     }
-    for (int i = tid; i < 16 * 16; i += 128) {
-      const int m = i >> 4, c = i & 15;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (toks[m].x >= 0) v = __ldcg(reinterpret_cast<const uint4*>(p.qn + toks[m].x * p.qn_tok + h * p.qn_head + 8 * c));
-      *reinterpret_cast<uint4*>(as + m * kAbAS + 8 * c) = v;
-    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(as + (8 * i + (tid >> 4)) * kAbAS + 8 * (tid & 15)) = v[i];
+    fetch(t0 + 16 * gridDim.z);            // the next tile's, while this one is multiplied
     __syncthreads();
     float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
@@ -396,6 +407,9 @@ __global__ void __launch_bounds__(128) absorb_tiles_kernel(const ChunkParams p, 
 // fp32 sums, one rounding to bf16.  Grid (H, 128 / 32, z), block 128: a CTA
 // takes 32 columns of a head and every z-th 16-token tile; warp w sums the
 // channels 128 w .. 128 w + 127, the four sums are added through shared memory.
+// Bound by reading o_lat from L2, once per column block: 16 bytes a lane, a tile
+// ahead (50 sequences of 26 tokens at 128 heads: 854 -> 728 us a call, of which
+// this and the absorption had been 400; 24 drafts at 64 heads 163 -> 159).
 // ---------------------------------------------------------------------------
 constexpr int kPrN = 32;
 constexpr int kPrWS = kPrN + 8;
@@ -419,7 +433,10 @@ __global__ void __launch_bounds__(128) project_kernel(const ChunkParams p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int e = tid + 128 * (j0 + i);
-      *reinterpret_cast<uint4*>(ws + (e / (kPrN / 8)) * kPrWS + 8 * (e % (kPrN / 8))) =
+      // a lane's 16 bytes of A are two steps' fragments: the rows of 32 channels
+      // are stored in the order in which the steps then take them
+      const int c = e / (kPrN / 8), at = (c & ~31) | (c & 4) << 2 | (c & 2) << 2 | (c >> 2 & 6) | (c & 1);
+      *reinterpret_cast<uint4*>(ws + at * kPrWS + 8 * (e % (kPrN / 8))) =
           make_uint4(tc::half2_bits(bf16lo(v[i].x), bf16hi(v[i].x)), tc::half2_bits(bf16lo(v[i].y), bf16hi(v[i].y)),
                      tc::half2_bits(bf16lo(v[i].z), bf16hi(v[i].z)), tc::half2_bits(bf16lo(v[i].w), bf16hi(v[i].w)));
     }
@@ -428,20 +445,31 @@ __global__ void __launch_bounds__(128) project_kernel(const ChunkParams p) {
   const int n = __ldcg(&p.counts->s_toks);
   if (16 * (int)blockIdx.z >= n) return;
   const uint32_t b_base = tc::smem_u32(ws) + ((128 * warp + (lane & 7) + 8 * ((lane >> 3) & 1)) * kPrWS + 8 * (lane >> 4)) * 2;
-  for (int t0 = 16 * blockIdx.z; t0 < n; t0 += 16 * gridDim.z) {
-    __syncthreads();
-    // A: o_lat rows t0 + r and t0 + r + 8 of this head, the warp's 128 channels
-    uint32_t a[8][4];
+  // A: o_lat rows t0 + r and t0 + r + 8 of this head, the warp's 128 channels
+  uint4 x[2][4];
+  auto fetch = [&](int t0) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int t = t0 + r + 8 * e;
-      const uint32_t* row = reinterpret_cast<const uint32_t*>(p.o_lat + ((int64_t)t * p.H + h) * kDc + 128 * warp);
+      const uint4* row = reinterpret_cast<const uint4*>(p.o_lat + ((int64_t)t * p.H + h) * kDc + 128 * warp + 8 * j);
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        a[ks][e] = t < n ? __ldcg(row + 8 * ks + j) : 0u;
-        a[ks][e + 2] = t < n ? __ldcg(row + 8 * ks + 4 + j) : 0u;
-      }
+      for (int g = 0; g < 4; ++g) x[e][g] = t < n ? __ldcg(row + 4 * g) : make_uint4(0u, 0u, 0u, 0u);
     }
+  };
+  fetch(16 * blockIdx.z);
+  for (int t0 = 16 * blockIdx.z; t0 < n; t0 += 16 * gridDim.z) {
+    __syncthreads();
+    uint32_t a[8][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        a[2 * g][e] = x[e][g].x;
+        a[2 * g][e + 2] = x[e][g].y;
+        a[2 * g + 1][e] = x[e][g].z;
+        a[2 * g + 1][e + 2] = x[e][g].w;
+      }
+    fetch(t0 + 16 * gridDim.z);            // the next tile's, while this one is multiplied
     float acc[4][4] = {};
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks)

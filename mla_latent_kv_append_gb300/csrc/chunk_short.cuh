@@ -28,7 +28,7 @@
 //
 // Measured (whole call, absorption and projection included): 32 sequences x
 // 32768 tokens, 16 heads, one new token each, INT4: 200 us, 3.0 TB/s of cache
-// (45% of a plain copy's rate).  24 ragged drafts at 64 heads, bf16 cache: 163
+// (45% of a plain copy's rate).  24 ragged drafts at 64 heads, bf16 cache: 159
 // us.  One sequence of 4096 tokens, 16 heads, INT8: 19 us, of which this kernel
 // 9, all latency.  With R = 16 a key tile takes 3100 to 3400 cycles per SM,
 // 2400 of them shared-memory traffic that the split cannot avoid: 72 KB written
