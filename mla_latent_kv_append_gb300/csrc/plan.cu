@@ -163,10 +163,11 @@ __global__ void __launch_bounds__(T) plan_kernel(const PlanParams p) {
   }
   if (tid == 0) s_start[spread(p.B)] = (int)(total < p.n ? total : p.n);
   const int head = __ldcg(p.free_range), tail = __ldcg(p.free_range + 1);
-  int avail = tail - head;
-  if (head < 0 || tail > p.free_len || avail < 0) {
+  int avail = 0;
+  if (head < 0 || tail < head || tail > p.free_len) {
     err |= MLA_DEVERR_PAGE;
-    avail = 0;
+  } else {
+    avail = tail - head;                               // not before: with a tail far below 0 it would wrap around
   }
   int64_t first = block_scan<T>(need_sum, red, &total);
 #pragma unroll
