@@ -159,21 +159,16 @@ __global__ void __launch_bounds__(kPrepThreads) long_prep_kernel(const ChunkPara
 }
 
 // ---------------------------------------------------------------------------
-// long_expand_kernel: clusters of two blocks.  A unit is (pair of key tiles,
-// head), pair-major; each block has one tile of the pair.  The tile's latents
+// long_expand_kernel: a unit is (key tile, head), tile-major.  The tile's latents
 // stay in TMEM (128 lanes x 256 columns of fp16 pairs) as the A operand while
 // the heads' weights stream through shared memory, 16 KB (64 latent channels
 // of W_UK or of W_UV) per item, four M = 128, N = 128 MMAs each.  A head's keys
 // and values are 128 TMEM columns each; while one half is computed the other
 // leaves, through 32 KB of shared memory as bulk stores.
-// What bounds it: 4100 cycles of MMAs per unit.  The weights' 64 bytes per
-// cycle and SM are more than L2 gives all SMs, so each block of the pair
-// fetches half an item and multicasts it to both; and their latency wants 100
-// KB and more under way, which is why the latents are not in shared memory (64
-// KB under way: 10000 cycles per unit).
-// Measured: 34816 tokens, 16 heads: 106 us, 5100 cycles per unit (81% of the
-// MMAs' rate); with the latents in shared memory and 64 KB of weights under way
-// 136 us, without the multicast the same 136 (latency, not L2's rate, held it).
+// What bounds it: 4100 cycles of MMAs per unit, and the weights' 64 bytes per
+// cycle and SM from L2, whose latency wants 100 KB and more under way: that is
+// why the latents are not in shared memory (64 KB under way: 10000 cycles per
+// unit).  Every block fetches its own items with plain copies.
 // Warps: 0 copies, 1 MMAs, 4..7 epilogue (and the latents' way into TMEM).
 // ---------------------------------------------------------------------------
 constexpr int kExThreads = 256;
@@ -184,7 +179,7 @@ constexpr int kExSmem = kExBars + 512 + 1024;
 static_assert(kExSmem <= 232448, "a block's shared memory");
 enum { xFull = 0, xEmpty = xFull + kExItems, xA = xEmpty + kExItems, xD, xDFree = xD + 2, xFin = xDFree + 2, xCount };
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_expand_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(kExThreads, 1) long_expand_kernel(const ChunkParams p) {
   extern __shared__ uint8_t ex_smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ex_smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sb = smem_u32(sm), bars = sb + kExBars;
@@ -195,39 +190,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_
   if (threadIdx.x == 0) {
     quit[0] = quit[1] = 0;
     for (int i = 0; i < xCount; ++i)
-      bar_init(bars + 8 * i, i == xA || i == xDFree || i == xDFree + 1 ? 128 : (i >= xEmpty && i < xA ? 2 : 1));
+      bar_init(bars + 8 * i, i == xA || i == xDFree || i == xDFree + 1 ? 128 : 1);
     *abort = 0;
     bar_init_fence();
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
   fence_before();
   __syncthreads();
-  cluster_sync();                          // the other block's barriers are there
   fence_after();
   const uint32_t tbase = *tmem_slot, t_d = tbase + 256;
   pdl_launch_dependents();
   pdl_wait();
-  const int rank = (int)cluster_rank();
-  const int tiles = __ldcg(&p.counts->l_tiles);
-  const int64_t U = (int64_t)((tiles + 1) / 2) * p.H;
-  const int64_t lo = U * (blockIdx.x >> 1) / (gridDim.x >> 1), hi = U * ((blockIdx.x >> 1) + 1) / (gridDim.x >> 1);
-  // the last pair may have one tile: its second block follows along unheard
-  auto tile_of = [&](int64_t u) { return min((int)(u / p.H) * 2 + rank, tiles - 1); };
+  const int64_t U = (int64_t)__ldcg(&p.counts->l_tiles) * p.H;
+  const int64_t lo = U * blockIdx.x / gridDim.x, hi = U * (blockIdx.x + 1) / gridDim.x;
   bool ok = true;
   if (warp == 0) {
     if (elect_one() && hi > lo) {
       uint32_t it = 0;
       for (int64_t u = lo; u < hi && ok; ++u) {
-        const uint8_t* src = p.w_tiles + (u % p.H) * kWHead + rank * (kBlkBytes / 2);
+        const uint8_t* src = p.w_tiles + (u % p.H) * kWHead;
         for (int st = 0; st < 16; ++st, ++it) {
           const uint32_t s = it % kExItems;
           if (it >= kExItems && !bar_wait(bars + 8 * (xEmpty + s), (it / kExItems - 1) & 1, p.wait_ns, abort)) {
             ok = false;
             break;
           }
-          // this block's half, to both; the other's half is counted too
           bar_expect(bars + 8 * (xFull + s), kBlkBytes);
-          bulk_copy_both(sb + s * kBlkBytes + rank * (kBlkBytes / 2), src + st * kBlkBytes, kBlkBytes / 2, bars + 8 * (xFull + s));
+          bulk_copy(sb + s * kBlkBytes, src + st * kBlkBytes, kBlkBytes, bars + 8 * (xFull + s));
         }
       }
       if (!ok) {
@@ -235,7 +224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_
         *abort = 1;
       }
       for (uint32_t s = 0; s < kExItems; ++s)
-        if (it > s && !drain_wait(bars + 8 * (xFull + s), ((it - 1 - s) / kExItems) & 1)) break;
+        if (it > s) drain_wait(bars + 8 * (xFull + s), ((it - 1 - s) / kExItems) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -266,7 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_
             const uint64_t w = (uint64_t)(s * (kBlkBytes >> 4));
             if (half == 0) umma4_ta<2>(t_d, tbase + 32 * st, d_uk + w, kIdK, st != 0);
             else umma4_ta<(2048 >> 4)>(t_d + 128, tbase + 32 * st, d_uv + w, kIdV, st != 0);
-            umma_commit_both(bars + 8 * (xEmpty + s));     // both blocks' copies write both blocks' items
+            umma_commit(bars + 8 * (xEmpty + s));
           }
           if (ok) umma_commit(bars + 8 * (xD + half));
         }
@@ -288,7 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_
     uint32_t nd = 0;
     for (int64_t u = lo; u < hi && ok; ++u, ++nd) {
       const uint32_t g = nd & 1;
-      const int tile = tile_of(u);
+      const int tile = (int)(u / p.H);
       if (u == lo || u % p.H == 0) {
         // The latents into TMEM, a row per lane (the last tile's MMAs are done,
         // their results have been read).  A warp reads its 32 rows of four
@@ -327,7 +316,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_
         fence_before();
         bar_arrive(bars + 8 * xA);
       }
-      const bool heard = (int)(u / p.H) * 2 + rank < tiles;
       uint8_t* out = p.kv_tiles + ((int64_t)tile * p.H + u % p.H) * kHeadTile;
       bool fine = true;
       for (int half = 0; half < 2; ++half) {               // keys, values
@@ -362,12 +350,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_
         bar_arrive(bars + 8 * (xDFree + half));            // TMEM has been read
         fence_async_smem();
         asm volatile("bar.sync 1, 128;\n" ::: "memory");
-        if (threadIdx.x == 128 && heard) {
+        if (threadIdx.x == 128) {
           bulk_store(out + half * 2 * kBlkBytes, sb + kExOut, 2 * kBlkBytes);
           bulk_store_commit();
         }
       }
-      if (ok && heard && !fine) atomicOr(p.kflags + 8 * tile + w, 1u << lane);
+      if (ok && !fine) atomicOr(p.kflags + 8 * tile + w, 1u << lane);
     }
     if (threadIdx.x == 128) bulk_store_done();
     if (!ok) {
@@ -377,7 +365,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1) long_
   }
   fence_before();
   __syncthreads();
-  cluster_sync();                          // no copy or commit of the other block comes after this
   if (warp == 1) {
     fence_after();
     tmem_free(tbase, 512);
@@ -980,7 +967,7 @@ mla_status launch_long(const ChunkParams& p, int lf, int kf, cudaStream_t stream
   MLA_CHUNK_CASE(MLA_FMT_INT8_OUTLIER, MLA_FMT_INT8_SYM)
 #undef MLA_CHUNK_CASE
   if (st != MLA_OK) return st;
-  st = cuda_status(launch_pdl(long_expand_kernel, dim3(p.grid / 2 * 2), dim3(kExThreads), kExSmem, stream, p));
+  st = cuda_status(launch_pdl(long_expand_kernel, dim3(p.grid), dim3(kExThreads), kExSmem, stream, p));
   if (st != MLA_OK) return st;
   st = cuda_status(launch_pdl(long_attention_kernel, dim3(p.grid), dim3(kLaThreads), kLaSmem, stream, p));
   if (st != MLA_OK) return st;
