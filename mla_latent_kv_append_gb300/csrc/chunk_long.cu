@@ -482,10 +482,12 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
   const uint32_t sb = smem_u32(sm), bars = sb + kLaBars;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kLaBars + 8 * aCount);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + kLaBars + 8 * aCount + 4);
+  volatile uint32_t* begun = reinterpret_cast<volatile uint32_t*>(sm + kLaBars + 8 * aCount + 8);    // segments whose MMAs have begun
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < aCount; ++i) bar_init(bars + 8 * i, (i >= aQ && i < aS) || (i >= aP && i < aO) ? 128 : 1);
     *abort = 0;
+    *begun = 0;
     bar_init_fence();
   }
   if (warp == 9) tmem_alloc(smem_u32(tmem_slot), 512);
@@ -739,32 +741,26 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
       for (uint32_t s = 0; s < kRing; ++s)
         if (n > s) drain_wait(bars + 8 * (aFull + s), ((n - 1 - s) / kRing) & 1);
     } else if (work && warp == 10) {
-      // ---- the next segment's query rows to L2 while this one runs
+      // ---- the next segment's query rows to L2 while this one runs.  No other
+      // warp waits for this one, so it may be any number of segments late: it is
+      // paced by a count that only grows (a barrier's parity could pass it twice
+      // and leave it waiting for a phase that never comes).
       LongWalk wk;
       wk.start(p, lo, hi);
-      uint32_t nq[2] = {0, 0};
-      bool more = wk.next(p.H);
-      while (more && ok) {
-        const bool zero = wk.t0 < min(wk.t1, wk.tiles0);
-        const int i = zero ? 0 : 1;
-        const uint32_t phase = nq[i] & 1;
-        if (zero) ++nq[0];
-        if (wk.two) ++nq[1];
-        more = wk.next(p.H);
-        if (more) {
-          for (int r = lane; r < kLongRows; r += 32) {
-            const int tok = wk.pair * kLongRows + r;
-            if (tok >= wk.s.n) break;
-            const uint16_t* qn = p.qn + (int64_t)(wk.s.q0 + tok) * p.qn_tok + wk.h * p.qn_head;
-            prefetch_line(qn);
-            prefetch_line(qn + 64);
-            prefetch_line(p.qp + (int64_t)(wk.s.q0 + tok) * p.qp_tok + wk.h * p.qp_head);
-          }
+      const bool any = wk.next(p.H);
+      for (uint32_t seg = 1; any && wk.next(p.H); ++seg) {
+        for (int r = lane; r < kLongRows; r += 32) {
+          const int tok = wk.pair * kLongRows + r;
+          if (tok >= wk.s.n) break;
+          const uint16_t* qn = p.qn + (int64_t)(wk.s.q0 + tok) * p.qn_tok + wk.h * p.qn_head;
+          prefetch_line(qn);
+          prefetch_line(qn + 64);
+          prefetch_line(p.qp + (int64_t)(wk.s.q0 + tok) * p.qp_tok + wk.h * p.qp_head);
         }
-        // one segment ahead, not more; nothing depends on this warp
-        if (!warp_wait(bars + 8 * (aQ + i), phase, p.wait_ns, abort)) ok = false;
+        // one segment ahead, not more
+        const uint64_t t0 = now_ns();
+        while (*begun < seg && !*abort && now_ns() - t0 < p.wait_ns) __nanosleep(500);
       }
-      ok = true;
     } else if (work && warp == 9 && elect_one()) {
       // ---- MMAs
       LongWalk wk;
@@ -774,7 +770,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
       const uint64_t d_q = sw128_desc(sb, 16, 1024), d_k = sw128_desc(sb + kLaRing, 16, 1024),
                      d_v = sw128_desc(sb + kLaRing, kBlkBytes, 1024);
       uint32_t n = 0;                      // ring blocks of the tiles before this one
-      uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+      uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, segs = 0;
       auto wait_slots = [&](uint32_t first, int count) -> bool {
         for (int c = 0; c < count; ++c)
           if (!bar_wait(bars + 8 * (aFull + (first + c) % kRing), ((first + c) / kRing) & 1, p.wait_ns, abort)) return false;
@@ -820,6 +816,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
           if (!bar_wait(bars + 8 * (aQ + 1), nq[1] & 1, p.wait_ns, abort)) { ok = false; break; }
           ++nq[1];
         }
+        *begun = ++segs;
         if ((zero && !scores(0, n)) || (wk.two && !scores(1, n))) { ok = false; break; }
         release(n, 3);
         for (int j = 0; j < tiles; ++j, n += 5) {
@@ -848,6 +845,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
         set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
         *abort = 1;
       }
+      *begun = 0xFFFFFFFFu;
       umma_commit(bars + 8 * aFin);
       drain_wait(bars + 8 * aFin, 0);
     }
