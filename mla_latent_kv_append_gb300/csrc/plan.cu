@@ -35,6 +35,7 @@ constexpr int kPlanPer = 4;
 constexpr int kPlanSmall = 256, kPlanLarge = kMaxBatch / kPlanPer;
 constexpr int kPlanRowWords = kPlanMaxRows / 32;
 constexpr int kPlanAhead = 8;
+constexpr int kPlanStatic = 512;             // at least the kernel's static shared memory, which counts toward the same limit
 
 struct PlanParams {
   const int32_t *ctx, *nw, *req;
@@ -89,6 +90,7 @@ __global__ void __launch_bounds__(T) plan_kernel(const PlanParams p) {
   extern __shared__ int32_t plan_smem[];
   __shared__ int64_t red[T / 32];
   __shared__ int taken;
+  static_assert(sizeof(red) + sizeof(taken) + 16 <= kPlanStatic, "the static share");
   int32_t* s_start = plan_smem;
   const int room = spread(p.B) + 1;
   int32_t* s_first = s_start + room;
@@ -320,7 +322,7 @@ extern "C" mla_status mla_plan_chunks(const int32_t* ctx_lens, const int32_t* ne
   const int sms = device_sm_count();
   const bool large = batch > kPlanSmall * kPlanPer;
   const int block = large ? kPlanLarge : kPlanSmall;
-  if (smem > 48 * 1024) {                  // many rows or requests
+  if (smem + kPlanStatic > 48 * 1024) {    // many rows or requests: past what a launch gets unasked
     static int configured[2][64] = {{0}};
     int dev = 0;
     cudaGetDevice(&dev);
