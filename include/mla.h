@@ -594,7 +594,9 @@ mla_status mla_rope(const uint16_t* q_pe, int64_t q_token_stride, int64_t q_head
  *   rows are 0.  A q_start that decreases or leaves [0, n_tokens] anywhere
  *   refuses all sequences, since their rows could overlap.
  *   Precision: fp16 operands, fp32 accumulation and softmax, one rounding of
- *   o to bf16.  Queries (after the absorption and the scale), cached values,
+ *   o to bf16.  A softmax weight keeps 11 bits down to 2^-21 of the row's
+ *   largest one; below it is off by at most 2^-32 of that (so 2^23 keys by
+ *   2^-9 together).  Queries (after the absorption and the scale), cached values,
  *   weights, keys and values beyond 65504 in magnitude count as non-finite.
  *   A non-finite token makes the rows that attend to it NaN and leaves the
  *   others alone.  A wait that runs out (mla_set_wait_limit_ns) sets

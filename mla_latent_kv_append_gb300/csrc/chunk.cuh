@@ -56,6 +56,13 @@ __device__ __forceinline__ int64_t run_begin(int64_t U, int x, int G) {
 // The run that holds unit u: the last one that begins at or before it.
 __device__ __forceinline__ int run_of(int64_t U, int64_t u, int G) { return (int)(((u + 1) * G - 1) / U); }
 
+// The softmax's weights are 2^(s - m + kHead) with the running maximum m, which
+// rises only when a score has passed it by kSlack: at most 2^15 in fp16, and the
+// largest at least 2^7 once m has risen to it, so that a weight keeps 11 bits
+// down to 2^-21 of the largest and steps of 2^-31 of it below (with kHead = 0 a
+// key 25 bits under the largest one was lost, and 65536 such keys with it).  Sums
+// carry the same factor, so it cancels.
+constexpr float kSlack = 8.f, kHead = 7.f;
 constexpr int kLongKeys = 128;               // long path: keys per tile
 constexpr int64_t kLongMost = 1 << 23;       // most cached tokens of a call's long path: the units of a head fit 31 bits
 constexpr int kPairCost = 3;                 // 38 drafts of 2 and 2 chunks of 1023: 128 us a call with 0, 126 with 1, 123.5 with 2 and 3; an

@@ -35,8 +35,6 @@ namespace {
 
 using namespace tc;
 
-constexpr float kSlack = 8.f;
-
 // ---------------------------------------------------------------------------
 // long_prep_kernel: block x < 4 tiles: a 32-token block of a key tile, lane =
 // token, warp w dequantizes units w and w + 8, warps 0 and 1 the RoPE units;
@@ -623,7 +621,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) long_attention_kernel(const Chu
             }
           }
         }
-        const float ms = m == -INFINITY ? 0.f : -m * sc;
+        const float ms = m == -INFINITY ? 0.f : kHead - m * sc;
         const uint64_t sc2 = pack2(sc, sc), ms2 = pack2(ms, ms);
         uint64_t la = pack2(0.f, 0.f), lb = la;
 #pragma unroll

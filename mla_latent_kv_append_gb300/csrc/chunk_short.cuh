@@ -3,7 +3,8 @@
 // dequantized once for all heads and new tokens of a row tile.
 //
 //   S^T = C Q^T          [64 keys] x [R rows], contraction over 576 channels
-//   P^T = exp2(S^T - m)  (the softmax scale and log2 e are folded into Q)
+//   P^T = exp2(S^T - m)  (the softmax scale and log2 e are folded into Q; m is
+//                        the running maximum less kHead)
 //   O^T = C^T P^T        [512 channels] x [R rows], contraction over 64 keys
 //
 // with C the key tile (one 64-token page, dequantized to fp16) and Q a tile
@@ -75,7 +76,6 @@ struct Roles {
                 "the warpgroups' shares come out of the launch's registers");
 };
 constexpr int kKeyBlk = kKeyTile * 128;              // one 64-key x 64-channel fp16 block: 8 KB
-constexpr float kSlack = 8.f;                        // the running maximum rises only past this (P <= 2^8 in fp16)
 constexpr int kMaxSmem = 232448 - 1024;              // a block's shared memory, less the alignment slack
 constexpr int kMaxSlots = 3;
 
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
       const int row0 = wk.item * R + gq * GR, rows = min(GR, wk.s.n * p.H - row0);       // rows <= 0: padding alone
       const int ctx = wk.s.len - wk.s.n;
       const int pos_min = ctx + row0 / p.H;          // the earliest row's position
-      float m[2 * J], l[2 * J];
+      float m[2 * J], l[2 * J];            // the running maxima less kHead, and the sums of the weights
 #pragma unroll
       for (int i = 0; i < 2 * J; ++i) {
         m[i] = -INFINITY;
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
             "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n"
             " selp.u32 %0, 1, 0, q;\n}\n"
             : "=r"(any)
-            : "r"((uint32_t)!(over <= kSlack)), "r"(bar_id)
+            : "r"((uint32_t)!(over <= kSlack + kHead)), "r"(bar_id)
             : "memory");
         if (quit[2 * gq + g]) {
           ok = false;
@@ -449,9 +449,9 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
             for (int e = 0; e < 2; ++e) {
               const int i = 2 * j + e;
               const float top = e ? a.y : a.x;
-              const bool raise = top > m[i] + kSlack;      // from -inf: the first key seen
-              alpha[i] = raise ? ex2(m[i] - top) : 1.f;
-              if (raise) m[i] = top;
+              const bool raise = top > m[i] + (kSlack + kHead);      // from -inf: the first key seen
+              alpha[i] = raise ? ex2(m[i] - (top - kHead)) : 1.f;
+              if (raise) m[i] = top - kHead;
               // a row that has seen nothing yet keeps m = -inf: its weights are 0
               const float base = m[i] == -INFINITY ? 0.f : m[i];
               v[4 * j + e] -= base;
