@@ -183,21 +183,23 @@ __device__ __forceinline__ bool convert_any(const RawUnit<FMT, KPE>& r, uint32_t
   return fine;
 }
 
-// The same, two channels at a time in fp16 arithmetic where that loses
-// nothing: codes become exact half integers by placing them in the mantissa of
+// The same, two channels at a time in fp16 arithmetic where that is as exact:
+// codes become exact half integers by placing them in the mantissa of
 // 1024, subtracting the offset and zero-point is exact, and the scale is split
-// into two halves, s = hi + lo, so that q hi + q lo is rounded once (the lo
-// product's own rounding is 2^-22).  11 issue slots for four INT8 codes
-// against 16 of convert_any (byte selects, logic and conversions run at half
-// rate).  Needs scales within fp16's normal range with room for lo, or zero,
-// and small zero-points: other units take convert_any.
+// into two halves, s = hi + lo, so that q hi + q lo is rounded once.  lo lies on
+// fp16's subnormal grid, off by up to 2^-25: for scales from 2^-10 on that is
+// 2^-15 of s at most, what convert_any's short scale is off by (an eighth of
+// half a step of the fp16 result at most; at 2^-13 it would be a whole half step).
+// 11 issue slots for four INT8 codes against 16 of convert_any (byte selects,
+// logic and conversions run at half rate).  Needs scales in that range, or
+// zero, and small zero-points: other units take convert_any.
 template <int FMT, bool KPE>
 __device__ __forceinline__ bool convert_unit(const RawUnit<FMT, KPE>& r, uint32_t* h) {
   using S = UnitShape<FMT, KPE>;
   if constexpr (FMT == MLA_FMT_BF16) {
     return convert_any<FMT, KPE>(r, h);
   } else {
-    constexpr uint32_t kLow = 0x39000000u, kHigh = S::kInt4 ? 0x42800000u : 0x44000000u;     // 2^-13 .. 64 or 512
+    constexpr uint32_t kLow = 0x3A800000u, kHigh = S::kInt4 ? 0x42800000u : 0x44000000u;     // 2^-10 .. 64 or 512
     bool fast = true;
 #pragma unroll
     for (int g = 0; g < S::kScales; ++g) {

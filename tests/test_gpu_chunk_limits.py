@@ -3,9 +3,11 @@ uneven weights, small scales, waits that run out anywhere."""
 
 import time
 
+import numpy as np
 import pytest
 import torch
 
+from oracle import quant as Q
 from tests._helpers import F_BF16, F_INT8
 from tests.test_gpu_chunk import Batch, mla  # noqa: F401
 
@@ -66,3 +68,52 @@ def test_one_key_outweighs_thousands(mla, B, H, n, x):  # noqa: F811
     for b in {0, B // 2, B - 1}:
         d = (o[t.start[b]:t.start[b + 1], :2] - want).abs()
         assert (d <= bound).all(), "%g times the bound, %g of the output" % ((d / bound).max(), d.norm() / want.norm())
+
+
+def test_small_scales_are_dequantized_with_one_rounding(mla):  # noqa: F811
+    """The value code x scale of INT8 groups with scales from 2^-13 to 2^-7, as
+    the attention holds it in fp16.  A sequence of one token gives its latents
+    back, o = c W_UV.  Group 0 holds the values; groups 1 to 4 hold, in codes
+    of a power-of-two scale u (which fp16 holds exactly), each value to within u
+    2^-8 as two digits, and W_UV takes their difference: what is left is small,
+    so that o's rounding to bf16 (2^-8 of it) does not hide fp16's.
+
+    Bound, in half steps of fp16 at the value: 1 for the rounding, 1/8 for a
+    scale rounded to 15 bits (2^-15 of a value below two steps of 2^11), with
+    fp32 noise 2^-10."""
+    B, H = 2000, 16
+    r = np.random.default_rng(3)
+    c = np.zeros((B, 512), np.float32)
+    s0 = 2.0 ** -13 * 2.0 ** (6 * r.random(B))
+    c[:, :16] = (r.integers(8, 128, (B, 16)) * r.choice([-1, 1], (B, 16))) * s0[:, None]
+    c[:, 0] = 127 * s0
+    c = torch.from_numpy(c).bfloat16().float().numpy()
+    code, scale = Q.quantize_sym_int8(c[:, :16], 16)
+    exact = code.astype(np.float64) * scale.astype(np.float64)
+    u = 2.0 ** np.ceil(np.log2(scale.astype(np.float64)))         # [B, 1]
+    hi = np.rint(exact / u)
+    lo = np.rint((exact - hi * u) / (u / 128))
+    assert np.abs(hi).max() <= 127 and np.abs(lo).max() <= 64
+    w_uv = torch.zeros((H, 512, 128))
+    for j in range(16):
+        chans = [16 * (1 + j // 4) + 2 * (j % 4) + 1, 16 * (1 + j // 4) + 2 * (j % 4) + 2]
+        c[:, chans[0]], c[:, chans[1]] = hi[:, j] * u[:, 0], lo[:, j] * u[:, 0]
+        w_uv[:, j, j], w_uv[:, chans[0], j], w_uv[:, chans[1], j] = 1, -1, -1 / 128
+    for g in range(1, 5):
+        c[:, 16 * g] = 127 * u[:, 0]                              # makes the group's scale u
+    x = torch.from_numpy(c).bfloat16()
+    assert (x.float().numpy() == c).all()
+    cache = mla.CacheLayer(B, F_INT8, F_INT8)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    mla.mla_cache_append(cache, x.cuda(), torch.zeros((B, 64), dtype=torch.bfloat16, device="cuda"), i32(range(0, 64 * B, 64)))
+    q = torch.zeros((B, H, 192), dtype=torch.bfloat16, device="cuda")
+    o = torch.empty((B, H, 128), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(mla.mla_chunk_workspace_bytes(B, B, H, 1), dtype=torch.uint8, device="cuda")
+    mla.mla_chunk_attention(cache, q[..., :128], q[..., 128:], torch.zeros((H, 128, 512), dtype=torch.bfloat16, device="cuda"),
+                            w_uv.bfloat16().cuda(), i32(range(B)).view(B, 1), i32(range(B + 1)), i32([1] * B), ws, o, max_new=1)
+    left = o[:, 0, :16].double().cpu().numpy()
+    got = hi * u + lo * u / 128 + left
+    half = 2.0 ** (np.floor(np.log2(np.abs(exact))) - 11)
+    off = np.abs(got - exact) - 2.0 ** -8 * np.abs(left)
+    worst = (off / half).max()
+    assert worst <= 1 + 1 / 8 + 2.0 ** -10, worst
