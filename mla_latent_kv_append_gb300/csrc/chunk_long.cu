@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(kPrepThreads) long_prep_kernel(const ChunkPara
   if (read) {
     volatile int never = 0;
     arrived = bar_wait(smem_u32(&bar), 0, p.wait_ns, &never);
-    if (!arrived) {
-      if (tid == 0) set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
+    if (!arrived) {                        // any thread's: the limit may end between two of them
+      set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
       drain_wait(smem_u32(&bar), 0);
     }
   }

@@ -117,3 +117,25 @@ def test_small_scales_are_dequantized_with_one_rounding(mla):  # noqa: F811
     off = np.abs(got - exact) - 2.0 ** -8 * np.abs(left)
     worst = (off / half).max()
     assert worst <= 1 + 1 / 8 + 2.0 ** -10, worst
+
+
+@pytest.mark.parametrize("limit", [0, 1000, 5000, 50000])
+@pytest.mark.parametrize("lens", [[(40, 1)] * 3, [(0, 65)], [(300, 70), (20, 3)]], ids=["decode", "chunk", "both"])
+def test_a_wait_that_runs_out_is_never_silent(mla, lens, limit):  # noqa: F811
+    """Limits near the time that the waits take: whichever of them runs out, in
+    whichever thread, a call either sets the flag or gives the whole result."""
+    t = Batch(mla, lens, 16)
+    ws = t.workspace()
+    good = t.call(ws=ws)
+    for _ in range(20):
+        prev = mla.mla_set_wait_limit_ns(limit)
+        try:
+            o = t.call(ws=ws)
+            torch.cuda.synchronize()
+        finally:
+            mla.mla_set_wait_limit_ns(prev)
+        assert t.err.item() in (0, mla.DEVERR_TIMEOUT)
+        assert t.err.item() or torch.equal(o, good)
+        t.err.zero_()
+    assert torch.equal(t.call(ws=ws), good)
+    assert t.err.item() == 0
