@@ -332,39 +332,56 @@ def mla_lse_merge(o_parts, lse_parts, o_lat, lse=None, stream=None):
 
 
 # The serving-step calls run a few microseconds on the GPU, so their bindings
-# keep to cheap checks and pass addresses as plain integers.
+# keep to cheap checks and pass addresses as plain integers.  All tensors of a
+# call lie on one GPU, ``dev`` (a host tensor's get_device() is -1).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _rows(t, shape, name):
-    """(token stride, head stride) of a bf16 CUDA tensor [n, heads, width] whose rows are contiguous."""
+def _gpu(t, name):
+    """The index of a CUDA tensor's device."""
+    if not t.is_cuda:
+        raise ValueError("%s: expected a CUDA tensor, got one on %s" % (name, t.device))
+    return t.get_device()
+
+
+def _elsewhere(t, name, dev):
+    return ValueError("%s: expected a tensor on cuda:%d, as the call's others, got one on %s" % (name, dev, t.device))
+
+
+def _rows(t, shape, name, dev):
+    """(token stride, head stride) of a bf16 tensor [n, heads, width] whose rows are contiguous."""
     s = t.stride()
-    if t.dtype is not torch.bfloat16 or t.shape != shape or not t.is_cuda or s[2] != 1:
+    if t.dtype is not torch.bfloat16 or t.shape != shape or s[2] != 1:
         raise ValueError("%s: expected CUDA bfloat16 %s with contiguous rows, got %s %s" % (name, shape, t.dtype,
                                                                                            tuple(t.shape)))
+    if t.get_device() != dev:
+        raise _elsewhere(t, name, dev)
     return s
 
 
-def _flat(t, dtype, shape, name):
-    """The address of a contiguous CUDA tensor."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+def _flat(t, dtype, shape, name, dev):
+    """The address of a contiguous tensor."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s: expected contiguous CUDA %s %s, got %s %s" % (name, dtype, shape, t.dtype, tuple(t.shape)))
+    if t.get_device() != dev:
+        raise _elsewhere(t, name, dev)
     return t.data_ptr()
 
 
-def _err(t):
+def _err(t, dev=None):
     """The address of an error word, or None."""
     if t is None:
         return None
     if t.dtype is not torch.int32 or not t.is_cuda:
         raise ValueError("dev_err: expected CUDA int32, got %s on %s" % (t.dtype, t.device))
+    if dev is not None and t.get_device() != dev:
+        raise _elsewhere(t, "dev_err", dev)
     return t.data_ptr()
 
 
-def _step(fn, t, stream, *args):
-    """Calls a library function on t's device: on ``stream``, or that device's current one."""
-    dev = t.get_device()
+def _step(fn, dev, stream, *args):
+    """Calls a library function on device ``dev``: on ``stream``, or that device's current one."""
     if dev == _device():
         status = fn(*args, stream.cuda_stream if stream is not None else _raw_stream(dev))
     else:
@@ -383,16 +400,18 @@ def mla_plan_chunks(ctx_lens, new_lens, req, page_table, free_pages, free_range,
     .. ``free_head``."""
     B, n = ctx_lens.shape[0], slot.shape[0]
     rows, max_pages = page_table.shape
-    i32 = torch.int32
-    _step(lib.mla_plan_chunks, ctx_lens, stream,
-          _flat(ctx_lens, i32, (B,), "ctx_lens"), _flat(new_lens, i32, (B,), "new_lens"), _flat(req, i32, (B,), "req"), B,
-          _flat(page_table, i32, (rows, max_pages), "page_table"), rows, max_pages,
-          _flat(free_pages, i32, (free_pages.shape[0],), "free_pages"), free_pages.shape[0],
-          _flat(free_range, i32, (2,), "free_range"), num_pages, n,
-          _flat(block_table, i32, (B, max_pages), "block_table"), _flat(q_start, i32, (B + 1,), "q_start"),
-          _flat(seq_lens, i32, (B,), "seq_lens"), _flat(positions, i32, (n,), "positions"),
-          _flat(token_req, i32, (n,), "token_req"), _flat(slot, i32, (n,), "slot"), _flat(free_head, i32, (1,), "free_head"),
-          _err(dev_err))
+    i32, dev = torch.int32, _gpu(ctx_lens, "ctx_lens")
+    _step(lib.mla_plan_chunks, dev, stream,
+          _flat(ctx_lens, i32, (B,), "ctx_lens", dev), _flat(new_lens, i32, (B,), "new_lens", dev),
+          _flat(req, i32, (B,), "req", dev), B,
+          _flat(page_table, i32, (rows, max_pages), "page_table", dev), rows, max_pages,
+          _flat(free_pages, i32, (free_pages.shape[0],), "free_pages", dev), free_pages.shape[0],
+          _flat(free_range, i32, (2,), "free_range", dev), num_pages, n,
+          _flat(block_table, i32, (B, max_pages), "block_table", dev), _flat(q_start, i32, (B + 1,), "q_start", dev),
+          _flat(seq_lens, i32, (B,), "seq_lens", dev), _flat(positions, i32, (n,), "positions", dev),
+          _flat(token_req, i32, (n,), "token_req", dev), _flat(slot, i32, (n,), "slot", dev),
+          _flat(free_head, i32, (1,), "free_head", dev),
+          _err(dev_err, dev))
 
 
 def mla_rope(q_pe, k_pe, positions, inv_freq, q_out, k_out, pair_axis=None, interleaved=True, inverse=False,
@@ -403,7 +422,8 @@ def mla_rope(q_pe, k_pe, positions, inv_freq, q_out, k_out, pair_axis=None, inte
     n]; inv_freq fp32 [32]; pair_axis: the axis of each of the 32 pairs."""
     n, H, _ = q_pe.shape
     axes = 1 if positions.dim() == 1 else positions.shape[0]
-    qs, qos = _rows(q_pe, (n, H, ROPE_DIM), "q_pe"), _rows(q_out, (n, H, ROPE_DIM), "q_out")
+    dev = _gpu(q_pe, "q_pe")
+    qs, qos = _rows(q_pe, (n, H, ROPE_DIM), "q_pe", dev), _rows(q_out, (n, H, ROPE_DIM), "q_out", dev)
     if (k_pe is None) != (k_out is None):
         raise ValueError("k_pe and k_out go together")
     kp = ko = None
@@ -411,17 +431,19 @@ def mla_rope(q_pe, k_pe, positions, inv_freq, q_out, k_out, pair_axis=None, inte
     if k_pe is not None:
         ks, kos = k_pe.stride(), k_out.stride()
         for t, s in ((k_pe, ks), (k_out, kos)):
-            if t.dtype is not torch.bfloat16 or t.shape != (n, ROPE_DIM) or not t.is_cuda or s[1] != 1:
+            if t.dtype is not torch.bfloat16 or t.shape != (n, ROPE_DIM) or s[1] != 1:
                 raise ValueError("k_pe, k_out: expected CUDA bfloat16 %s with contiguous rows, got %s %s" % (
                     (n, ROPE_DIM), t.dtype, tuple(t.shape)))
+            if t.get_device() != dev:
+                raise _elsewhere(t, "k_pe, k_out", dev)
         kp, ko = k_pe.data_ptr(), k_out.data_ptr()
     if pair_axis is not None:
         pair_axis = bytes(pair_axis)
         if len(pair_axis) != ROPE_DIM // 2:
             raise ValueError("pair_axis: expected %d axes" % (ROPE_DIM // 2))
-    _step(lib.mla_rope, q_pe, stream, q_pe.data_ptr(), qs[0], qs[1], kp, ks[0],
-          _flat(positions, torch.int32, (n,) if positions.dim() == 1 else (axes, n), "positions"), axes, pair_axis,
-          _flat(inv_freq, torch.float32, (ROPE_DIM // 2,), "inv_freq"), n, H, 1 if interleaved else 0, 1 if inverse else 0,
+    _step(lib.mla_rope, dev, stream, q_pe.data_ptr(), qs[0], qs[1], kp, ks[0],
+          _flat(positions, torch.int32, (n,) if positions.dim() == 1 else (axes, n), "positions", dev), axes, pair_axis,
+          _flat(inv_freq, torch.float32, (ROPE_DIM // 2,), "inv_freq", dev), n, H, 1 if interleaved else 0, 1 if inverse else 0,
           amplitude, q_out.data_ptr(), qos[0], qos[1], ko, kos[0])
 
 
@@ -438,18 +460,24 @@ def mla_chunk_attention(cache, q_nope, q_pe, w_uk, w_uv, block_table, q_start, s
     kv_tokens the lengths of the sequences with more than CHUNK_SHORT."""
     n, H, _ = q_nope.shape
     B, max_pages = block_table.shape
-    qn, qp = _rows(q_nope, (n, H, QK_NOPE_DIM), "q_nope"), _rows(q_pe, (n, H, ROPE_DIM), "q_pe")
+    dev = _gpu(q_nope, "q_nope")
+    qn, qp = _rows(q_nope, (n, H, QK_NOPE_DIM), "q_nope", dev), _rows(q_pe, (n, H, ROPE_DIM), "q_pe", dev)
     bf16, i32 = torch.bfloat16, torch.int32
-    if not workspace.is_cuda or not workspace.is_contiguous():
+    if not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous CUDA tensor")
+    if workspace.get_device() != dev:
+        raise _elsewhere(workspace, "workspace", dev)
+    if cache.pool.get_device() != dev:
+        raise _elsewhere(cache.pool, "the cache's pool", dev)
     cs = cache.c_struct()
-    _step(lib.mla_chunk_attention, q_nope, stream, ctypes.byref(cs), q_nope.data_ptr(), qn[0], qn[1], q_pe.data_ptr(), qp[0], qp[1],
-          _flat(w_uk, bf16, (H, QK_NOPE_DIM, KV_LORA_RANK), "w_uk"), _flat(w_uv, bf16, (H, KV_LORA_RANK, V_DIM), "w_uv"),
-          _flat(block_table, i32, (B, max_pages), "block_table"), max_pages, _flat(q_start, i32, (B + 1,), "q_start"),
-          _flat(seq_lens, i32, (B,), "seq_lens"), B, n, H, max_new, kv_tokens,
+    _step(lib.mla_chunk_attention, dev, stream, ctypes.byref(cs), q_nope.data_ptr(), qn[0], qn[1], q_pe.data_ptr(), qp[0], qp[1],
+          _flat(w_uk, bf16, (H, QK_NOPE_DIM, KV_LORA_RANK), "w_uk", dev),
+          _flat(w_uv, bf16, (H, KV_LORA_RANK, V_DIM), "w_uv", dev),
+          _flat(block_table, i32, (B, max_pages), "block_table", dev), max_pages, _flat(q_start, i32, (B + 1,), "q_start", dev),
+          _flat(seq_lens, i32, (B,), "seq_lens", dev), B, n, H, max_new, kv_tokens,
           DEFAULT_SOFTMAX_SCALE if softmax_scale is None else softmax_scale, workspace.data_ptr(),
-          workspace.numel() * workspace.element_size(), _flat(o, bf16, (n, H, V_DIM), "o"),
-          _err(dev_err))
+          workspace.numel() * workspace.element_size(), _flat(o, bf16, (n, H, V_DIM), "o", dev),
+          _err(dev_err, dev))
 
 
 def mla_set_prefill_path(path):
