@@ -112,7 +112,7 @@ __device__ __forceinline__ int plan_sequences(const ChunkParams& p, int R, bool 
     }
     if (n[k] > kChunkShort) {
       is_long[k] = true;
-      tiles[k] = (len[k] + kLongKeys - 1) / kLongKeys;
+      tiles[k] = (len[k] - 1) / kLongKeys + 1;         // len + 127 may pass 31 bits
       l_mine += ((int64_t)1 << 48) + tiles[k];
       continue;
     }

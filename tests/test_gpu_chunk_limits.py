@@ -139,3 +139,18 @@ def test_a_wait_that_runs_out_is_never_silent(mla, lens, limit):  # noqa: F811
         t.err.zero_()
     assert torch.equal(t.call(ws=ws), good)
     assert t.err.item() == 0
+
+
+@pytest.mark.parametrize("length", [2 ** 31 - 64, 2 ** 31 - 127, 2 ** 31 - 128, 2 ** 24])
+def test_a_chunk_of_a_length_near_32_bits_is_refused(mla, length):  # noqa: F811
+    """A table of 2^25 - 1 pages allows lengths up to 2^31 - 64: a chunk that
+    says so goes far past kv_tokens, and its neighbours are served."""
+    t = Batch(mla, [(70, 2), (20, 90), (5, 1)], 16)
+    table = torch.full((3, 2 ** 25 - 1), -1, dtype=torch.int32, device="cuda")
+    table[:, :t.P] = t.dev["table"]
+    lens = t.dev["lens"].clone()
+    lens[1] = length
+    o = t.call(dev={"table": table, "lens": lens})
+    assert t.err.item() == mla.DEVERR_SEQLEN
+    assert (o[t.start[1]:t.start[2]] == 0).all()
+    t.check(o, seqs=[0, 2])
