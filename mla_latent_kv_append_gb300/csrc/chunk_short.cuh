@@ -631,32 +631,32 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
           }
           for (int t = wk.t0; t < wk.t1 && ok; ++t, ++it) {
             const uint32_t g = it & 1, kb = it % NR, d = t_s + g * R;
-          // the softmax has read this S^T buffer's last tile
-          if (it >= 2 && !bar_wait(bars + 8 * (bP + g), ((it - 2) >> 1) & 1, p.wait_ns, abort)) {
-            ok = false;
-            break;
-          }
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            if (!bar_wait(bars + 8 * (bWritten + piece), round & 1, p.wait_ns, abort)) {
+            // the softmax has read this S^T buffer's last tile
+            if (it >= 2 && !bar_wait(bars + 8 * (bP + g), ((it - 2) >> 1) & 1, p.wait_ns, abort)) {
               ok = false;
               break;
             }
-            fence_after();
-            const uint64_t a = d_k + (uint64_t)(piece * (kPiece >> 4));
-            umma4<2, 2>(d, a, d_q + (2 * s * R * 128 >> 4), kId, s != 0);
-            umma4<2, 2>(d, a + (kKeyBlk >> 4), d_q + ((2 * s + 1) * R * 128 >> 4), kId, 1u);
-            if (++piece == NP) {
-              piece = 0;
-              ++round;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              if (!bar_wait(bars + 8 * (bWritten + piece), round & 1, p.wait_ns, abort)) {
+                ok = false;
+                break;
+              }
+              fence_after();
+              const uint64_t a = d_k + (uint64_t)(piece * (kPiece >> 4));
+              umma4<2, 2>(d, a, d_q + (2 * s * R * 128 >> 4), kId, s != 0);
+              umma4<2, 2>(d, a + (kKeyBlk >> 4), d_q + ((2 * s + 1) * R * 128 >> 4), kId, 1u);
+              if (++piece == NP) {
+                piece = 0;
+                ++round;
+              }
             }
-          }
-          if (ok && !bar_wait(bars + 8 * (bRopeW + kb), (it / NR) & 1, p.wait_ns, abort)) ok = false;
-          if (!ok) break;
-          fence_after();
-          umma4<2, 2>(d, d_r + (uint64_t)(kb * (kKeyBlk >> 4)), d_q + (8 * R * 128 >> 4), kId, 1u);
-          umma_commit(bars + 8 * (bRopeF + kb));           // read here only
-          umma_commit(bars + 8 * (bS + g));
+            if (ok && !bar_wait(bars + 8 * (bRopeW + kb), (it / NR) & 1, p.wait_ns, abort)) ok = false;
+            if (!ok) break;
+            fence_after();
+            umma4<2, 2>(d, d_r + (uint64_t)(kb * (kKeyBlk >> 4)), d_q + (8 * R * 128 >> 4), kId, 1u);
+            umma_commit(bars + 8 * (bRopeF + kb));           // read here only
+            umma_commit(bars + 8 * (bS + g));
           }
         }
         if (!ok) {
@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
             const int page = __shfl_sync(0xffffffffu, mine, t - t0);
             const bool page_ok = page >= 0 && page < p.num_pages;
             if (!page_ok && lane == 0) set_err(p.dev_err, MLA_DEVERR_PAGE);
-  #pragma unroll
+#pragma unroll
             for (int half = 0; half < 2; ++half, ++blk) {
               const uint32_t slot = blk % NS;
               if (blk >= NS && !warp_wait(bars + 8 * (bRawFree + slot), ((blk / NS) - 1) & 1, p.wait_ns, abort)) {

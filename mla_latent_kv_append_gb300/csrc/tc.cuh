@@ -195,7 +195,7 @@ __device__ __forceinline__ void tmem_store32(uint32_t t, const uint32_t* v) {
 // 2], r[4j + 3]), columns 8j + 2 (t % 4) and the next.
 template <int COLS8>
 __device__ __forceinline__ void tmem_load_16x256b(uint32_t t, uint32_t* r) {
-  static_assert(COLS8 == 2 || COLS8 == 4 || COLS8 == 8, "16, 32 or 64 columns");
+  static_assert(COLS8 == 2 || COLS8 == 4, "16 or 32 columns");
   if constexpr (COLS8 == 2) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
@@ -203,19 +203,11 @@ __device__ __forceinline__ void tmem_load_16x256b(uint32_t t, uint32_t* r) {
         : MLA_R8(r, 0)
         : "r"(t)
         : "memory");
-  } else if constexpr (COLS8 == 4) {
+  } else {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
         "tcgen05.wait::ld.sync.aligned;\n"
         : MLA_R8(r, 0), MLA_R8(r, 8)
-        : "r"(t)
-        : "memory");
-  } else {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-        "tcgen05.wait::ld.sync.aligned;\n"
-        : MLA_R8(r, 0), MLA_R8(r, 8), MLA_R8(r, 16), MLA_R8(r, 24)
         : "r"(t)
         : "memory");
   }
