@@ -28,8 +28,8 @@
  * heads.
  *
  * Conventions for every call.
- *   - Ownership: the caller allocates and frees all memory (device memory
- *     unless stated).  The library never allocates, frees or synchronizes;
+ *   - Ownership: the caller allocates and frees all memory (memory of the
+ *     current device unless stated).  The library never allocates, frees or synchronizes;
  *     it keeps no state between calls apart from a per-device attribute
  *     cache.  Calls are thread-safe and re-entrant.
  *   - Execution: every call enqueues its kernels on `stream` (NULL = the
@@ -514,7 +514,9 @@ mla_status mla_lse_merge(const float* o_parts, const float* lse_parts, int32_t p
  *   (MLA_DEVERR_PAGE); or the free list has too few pages
  *   (MLA_DEVERR_NO_PAGES: nobody behind it gets pages either).  A refused
  *   request takes no page; its seq_lens entry is 0, its block_table row -1,
- *   its tokens' slots -1 and their positions 0.  A page id outside the pool
+ *   its tokens' slots -1 and their positions 0.  Its new tokens (none where
+ *   new is negative) keep their rows, so that a count far too large leaves the
+ *   requests behind it no room.  A page id outside the pool
  *   sets MLA_DEVERR_PAGE and is written as -1; a bad free_range counts as
  *   empty and sets MLA_DEVERR_PAGE.
  *   rows <= 65536; batch <= 4096; batch == 0 is a no-op.  The same inputs
@@ -537,8 +539,9 @@ mla_status mla_plan_chunks(const int32_t* ctx_lens, const int32_t* new_lens, con
  * video).  Pair i (i = 0..31) of a row turns by
  *   t = positions[pair_axis[i]][token] * inv_freq[i]:
  *   y1 = amplitude (x1 cos t - x2 sin t),  y2 = amplitude (x1 sin t + x2 cos t)
- * Angles are exact to 2e-6 radians at every 32-bit position, the products
- * are fp32, rounded once to bf16.
+ * Angles are off by at most 1e-7 + 2^-52 |position * inv_freq| radians (6e-7
+ * at every 32-bit position for |inv_freq| <= 1), the products are fp32,
+ * rounded once to bf16.
  *   q_pe     bf16 [n][heads][64] at the given strides (elements, multiples of
  *            8), 16-byte aligned; heads 0..128 (0: keys only)
  *   k_pe     bf16 [n][64] at k_token_stride, or NULL (then k_out is NULL too)
@@ -547,8 +550,8 @@ mla_status mla_plan_chunks(const int32_t* ctx_lens, const int32_t* new_lens, con
  *            interpolation already in it
  *   pair_axis HOST uint8 [32], each < axes, read during the call; NULL: axis 0
  *   interleaved 1: pairs are channels (2i, 2i + 1); 0: (i, i + 32)
- *   inverse  1: turns by -t (takes a rotation back; also the gradient of the
- *            forward call)
+ *   inverse  1: turns by -t (the gradient of the forward call; with amplitude
+ *            1 or -1 it also takes a rotation back)
  *   q_out, k_out: bf16 at their own strides; a call may write over its
  *            inputs (same pointer and strides), any other overlap is
  *            undefined.  Rows of an output must not overlap each other.

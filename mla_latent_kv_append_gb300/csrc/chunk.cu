@@ -10,17 +10,23 @@
 // 2 x 320 operations per (query, head, key), plus 2 x 512 x 256 per (key,
 // head).  Sequences with at most MLA_CHUNK_SHORT = 64 new tokens take the
 // first (chunk_short.cuh), the others the second (chunk_long.cu).  The rule
-// looks at the new tokens alone: the absorbed form's time grows with them, the
-// expanded form's is flat up to 256 (one item per head), and where the two
-// meet hardly moves with the heads, the context or the batch.  INT8, absorbed
-// / expanded, microseconds per call:
-//                                  n = 32       48          64          96
-//   16 heads, 16 x  4000 cached   223/379    310/379     399/381     571/383
-//   64 heads,  1 x 30000          279/566    402/567     524/569     765/573
-//   64 heads, 16 x  4000          709/1181  1051/1178   1384/1185   2044/1196
-//  128 heads,  1 x 30000          524/1069   768/1068   1004/1075   1490/1077
-// The expanded form also needs 512 bytes of workspace per token and head,
-// which is why a draw goes to the absorbed one.
+// looks at the new tokens alone, which the host bounds.  The absorbed form's
+// time grows with them, the expanded form's is flat up to 256 (one item per
+// head); where the two meet depends on the context too.  Absorbed / expanded,
+// microseconds of a captured call, INT8 (bf16 and INT4 at 64 heads are within 8 %):
+//                                  n = 16        32         48         64         96
+//   16 heads, 16 x   500 cached    72/99      98/100    128/100    149/101    217/104
+//             16 x  4000          122/381    211/382    296/383    372/383    529/386
+//   64 heads,  1 x   200           58/43      40/43      49/43      58/48      65/48
+//             16 x   500          146/252    249/257    348/259    453/262    697/268
+//             16 x  4000          360/1218   662/1224   980/1227  1288/1230  1901/1236
+//              1 x 30000          176/580    271/582    395/584    515/585    757/592
+//  128 heads, 16 x   500          251/448    452/457    649/461    845/467   1329/480
+//              1 x 30000          274/1093   516/1094   756/1099   993/1099  1470/1122
+// So they meet at about 64 new tokens after thousands of cached ones and at 32
+// after a few hundred, where 33 to 64 new tokens cost up to 1.8 times what the
+// expanded form would.  That form also needs 512 bytes of workspace per token
+// and head, within a bound that the host has to give for such sequences.
 //
 // This file: the device plan (which sequences take which path, prefix sums
 // of their work; lengths never visit the host), the query absorption, the
@@ -263,7 +269,8 @@ __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0
 // PLAN: the call has at most kPlanFused sequences and no long path: every block
 // makes the plan for itself (three words per sequence) instead of waiting for a
 // kernel that does, and one of them writes it down.  One sequence of 4096 tokens
-// 20.7 us a call with the plan's own kernel, 19.0 without; 24 drafts 164.8 and 163.3.
+// 20.7 us a captured call with the plan's own kernel, 19.0 without; 24 drafts 164.8 and
+// 163.3.
 // ---------------------------------------------------------------------------
 constexpr int kAbWS = 64 + 8;        // W slice row stride: ldmatrix without conflicts
 constexpr int kAbAS = kDn + 8;
@@ -408,8 +415,8 @@ __global__ void __launch_bounds__(128) absorb_tiles_kernel(const ChunkParams p, 
 // takes 32 columns of a head and every z-th 16-token tile; warp w sums the
 // channels 128 w .. 128 w + 127, the four sums are added through shared memory.
 // Bound by reading o_lat from L2, once per column block: 16 bytes a lane, a tile
-// ahead (50 sequences of 26 tokens at 128 heads: 854 -> 728 us a call, of which
-// this and the absorption had been 400; 24 drafts at 64 heads 163 -> 159).
+// ahead (50 sequences of 26 tokens at 128 heads: 854 -> 728 us a captured call, of
+// which this and the absorption had been 400; 24 drafts at 64 heads 163 -> 159).
 // ---------------------------------------------------------------------------
 constexpr int kPrN = 32;
 constexpr int kPrWS = kPrN + 8;

@@ -16,10 +16,12 @@
 // runs, one per SM; query tiles that fall into several runs leave fp32
 // partials that long_combine_kernel merges in block order.
 //
-// What bounds it: the MMAs.  Measured: 8192 tokens on their own, 64 heads, INT8:
-// 1.10 ms, 1.37 PFLOP/s of the formula's operations (73% of a library matrix
-// product's rate); 2048 tokens after 32768, 16 heads: 0.57 ms (79%); 54.9 and 5.9 ms
-// for the absorbed form's kernel.
+// What bounds it: the MMAs.  Measured, call after call: 8192 tokens on their own, 64
+// heads, INT8: 1.21 to 1.25 ms, 1.25 to 1.21 PFLOP/s of the formula's operations (64 to
+// 66% of a library matrix product's rate in a short burst, 71 to 74% of its rate
+// under the power limit); 2048 tokens after 32768, 16 heads: 0.63 ms (72 and 80%); in a
+// burst of 20 ms, before the power limit acts, 1.13 and 0.58 ms; 54.9 and 5.9 ms for
+// the absorbed form's kernel.
 //
 // Rounding: latents, weights, keys, values, queries and P are fp16 (2^-11
 // relative each; bf16 queries and weights convert exactly within fp16's normal
@@ -167,6 +169,8 @@ __global__ void __launch_bounds__(kPrepThreads) long_prep_kernel(const ChunkPara
 // cycle and SM from L2, whose latency wants 100 KB and more under way: that is
 // why the latents are not in shared memory (64 KB under way: 10000 cycles per
 // unit).  Every block fetches its own items with plain copies.
+// Measured: 34816 tokens, 16 heads: 106 us, 5100 cycles per unit (81% of the MMAs'
+// rate); with the latents in shared memory and 64 KB of weights under way 136 us.
 // Warps: 0 copies, 1 MMAs, 4..7 epilogue (and the latents' way into TMEM).
 // ---------------------------------------------------------------------------
 constexpr int kExThreads = 256;

@@ -29,9 +29,9 @@
 //
 // Measured (whole call, absorption and projection included): 32 sequences x
 // 32768 tokens, 16 heads, one new token each, INT4: 200 us, 3.0 TB/s of cache
-// (45% of a plain copy's rate).  24 ragged drafts at 64 heads, bf16 cache: 159
-// us.  One sequence of 4096 tokens, 16 heads, INT8: 19 us, of which this kernel
-// 9, all latency.  With R = 16 a key tile takes 3100 to 3400 cycles per SM,
+// (45% of a plain copy's rate).  24 ragged drafts at 64 heads, bf16 cache: 160
+// us.  One sequence of 4096 tokens, 16 heads, INT8: 19 us of a captured graph, of
+// which this kernel 9, all latency (called from Python 25 to 30, the host's part).  With R = 16 a key tile takes 3100 to 3400 cycles per SM,
 // 2400 of them shared-memory traffic that the split cannot avoid: 72 KB written
 // by the dequantization, 72 + 18 KB read by the S^T MMAs, 64 + 8 KB by the O^T
 // MMAs, the raw bytes in and out.  With R = 64 and a bf16 cache (5000 cycles) the
@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(Roles<R>::kThreads, 1) short_attention_kernel(
 // With many rows a block takes whole rows (COLS = 1); where the call has few row
 // tiles for the SMs, so that rows are few and their parts many, four blocks
 // share a row by columns and have four times the groups (COLS = 4).  One
-// sequence of 4096 tokens: 23.5 us a call with COLS = 1, 20.8 with 4; 24 drafts
+// sequence of 4096 tokens: 23.5 us a captured call with COLS = 1, 20.8 with 4; 24 drafts
 // 175 and 293; 32 sequences of 32768 tokens 201 and 211.  Bound by latency in the
 // first case, by reading the partials from L2 in the others.
 constexpr int kCombineThreads = 512;

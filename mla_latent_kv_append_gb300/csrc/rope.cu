@@ -11,8 +11,9 @@
 // as a 64-bit fixed-point fraction instead: G_i = frac(f_i / (2 pi)) 2^64 is
 // computed once per lane in fp64, pos * G_i wraps modulo 2^64 = one turn on
 // its own, and the top 32 bits are the angle to 2^-31 of a half turn.  The
-// fp64 quotient is off by 2^-53 relative, so a position of 2^31 is off by at
-// most 2^-22 turns (1.5e-6 radians): far below bf16.
+// fp64 quotient is off by 2^-52 relative (1 / (2 pi) and the product, rounded), so
+// an angle is off by 2^-52 |pos f| radians, and by 1e-7 through its conversion to
+// fp32: 6e-7 at position 2^31 for f = 1, far below bf16.
 //
 // What bounds it: reading and writing N (H + 1) rows of 128 bytes.  A warp
 // takes a token (or a run of its heads); lane i computes pair i's cosine and
