@@ -572,7 +572,7 @@ def _plain_pages(s):
     if s["case"]["move"]:
         moves = new < old
         take = torch.where(moves, now, torch.zeros_like(now))
-        first = tail - take.sum() + torch.cumsum(take, 0) - take
+        first = head + torch.cumsum(take, 0) - take
         fresh = free[(first[:, None] + col).clamp(0, free.numel() - 1)]
         mine = moves[:, None] & (col < now[:, None])
         back = moves[:, None] & (col < was[:, None])
@@ -583,13 +583,14 @@ def _plain_pages(s):
         back = (col >= now[:, None]) & (col < was[:, None])
         out = torch.where(col < now[:, None], table, torch.full_like(table, -1))
     flat = back.flatten()
-    at = head - flat.sum() + torch.cumsum(flat, 0) - 1
+    to = head + take.sum() - flat.sum()
+    at = to + torch.cumsum(flat, 0) - 1
     at = torch.where(flat, at, torch.full_like(at, free.numel()))
     longer = torch.cat([free, free[:1]])
     longer.scatter_(0, at, table.flatten())
     free.copy_(longer[:-1])
     return {"table": out, "page_table": s["page_table"], "free": free, "lens": s["new"].clone(),
-            "free_range": torch.stack([head - flat.sum(), tail - take.sum()]).int()}
+            "free_range": torch.stack([to, tail]).int()}
 
 
 def _own_pages(s):
