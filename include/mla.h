@@ -98,13 +98,16 @@ typedef enum {
 } mla_fmt;
 
 /* Bits ORed into *dev_err. */
-#define MLA_DEVERR_SLOT    1  /* append: slot not in [0, num_pages*64) and not -1 */
-#define MLA_DEVERR_PAGE    2  /* decode, chunks: block_table entry not in [0, num_pages);
-                                 plan: a page id, a table row or the free range */
-#define MLA_DEVERR_SEQLEN  4  /* decode: seq_len < 0 or > max_pages*64; plan, chunks:
-                                 lengths that do not fit the call's arrays */
+#define MLA_DEVERR_SLOT    1  /* append: slot not in [0, num_pages*64) and not -1;
+                                 move: a kept position outside the sequence */
+#define MLA_DEVERR_PAGE    2  /* decode, chunks, mass, select, move: block_table entry not in
+                                 [0, num_pages); plan, release: a page id, a table row or the free range */
+#define MLA_DEVERR_SEQLEN  4  /* decode: seq_len < 0 or > max_pages*64; plan, chunks and the
+                                 calls behind a step: lengths that do not fit the call's arrays */
 #define MLA_DEVERR_TIMEOUT 8  /* a bounded wait inside a kernel gave up           */
-#define MLA_DEVERR_NO_PAGES 16 /* plan: the free list has too few pages           */
+#define MLA_DEVERR_NO_PAGES 16 /* plan, release: the free list has too few pages, or
+                                 (release) no room for those given back */
+#define MLA_DEVERR_TOKEN   32 /* verify: a draft outside the vocabulary, or a row without weight */
 
 #define MLA_KV_LORA_RANK 512
 #define MLA_ROPE_DIM 64
@@ -619,6 +622,185 @@ mla_status mla_chunk_attention(const mla_cache_layer* cache, const uint16_t* q_n
 /* Bytes of device workspace mla_chunk_attention needs; 0 for invalid
  * arguments. */
 size_t mla_chunk_workspace_bytes(int32_t batch, int32_t n_tokens, int32_t heads, int32_t max_new, int64_t kv_tokens);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Behind a step's attention: which of the cached tokens stay.
+ *
+ * Speculative decoding: mla_verify_drafts says how many drafts of each
+ * sequence were accepted, mla_release_pages (trim) gives back the pages of
+ * the rejected ones.  A cache with a budget: mla_token_mass adds up the
+ * attention weight that every token received, mla_select_tokens picks those
+ * that stay, mla_release_pages (move) gives the sequences fresh pages for
+ * them, mla_move_tokens moves them.  Pages are the same for all layers, so
+ * the release runs once a step, the others once a layer.  Lengths live on the
+ * device, so that a captured step can be replayed with other ones.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * mla_verify_drafts - drafted tokens against the target model's
+ * probabilities, from given random numbers, and the token sampled behind the
+ * accepted ones.  Sequence b has rows row_start[b] .. row_start[b + 1] - 1,
+ * one more than its drafts (one row: it only samples; none: it takes no part).
+ * Row r holds the target's and the draft model's distribution of the same
+ * token.  With c(x) = x where 0 < x < inf and 0 elsewhere:
+ *   drafts pass in order while u_accept[r] * c(q_r(d_r)) < c(p_r(d_r));
+ *   behind the last that passed, at row j, the next token is drawn from
+ *   w(v) = max(c(p_j(v)) - c(q_j(v)), 0), or from w = c(p_j) behind the
+ *   last draft or where nothing else is left: the smallest v for which the
+ *   sum of w up to v is larger than u_sample[b] * sum w
+ *   target_probs [rows][vocab] of type prob_type, rows target_row_stride
+ *           elements apart (>= vocab; any alignment of the type).  Rows need
+ *           not add up to 1
+ *   draft_probs the same (the last row of a sequence is not read), or NULL:
+ *           drafts that were certain, as from a lookup: q_r is 1 at d_r
+ *   drafts  int32 [rows]: d_r; a sequence's last entry is not used
+ *   u_accept fp32 [rows], u_sample fp32 [B], in [0, 1): u_sample is clamped
+ *           to [0, 1] (1: the last v with weight; NaN counts as 0), a NaN in
+ *           u_accept rejects
+ *   seq_lens int32 [B]: cached tokens with all drafts; with kept_lens, or both NULL
+ *   accepted int32 [B]: drafts that passed
+ *   tokens  int32 [B][max_out]: the accepted drafts, the drawn token, -1 behind
+ *   kept_lens int32 [B]: seq_lens less the rejected drafts (may be seq_lens):
+ *           the next step's context
+ *   A draft outside [0, vocab) is rejected, with the draft's row as it is, and
+ *   sets MLA_DEVERR_TOKEN.  A row without weight draws -1 and sets it too.  A
+ *   sequence with more than max_out rows is refused (MLA_DEVERR_SEQLEN): it
+ *   accepts nothing, its tokens are -1, its length stays.  So are all
+ *   sequences when row_start decreases or leaves [0, rows] anywhere.
+ *   Sums are good to 2^-46 of the row's, the comparison is exact.
+ *   vocab <= 2^22, batch <= 4096; batch == 0 is a no-op.
+ */
+#define MLA_PROB_FP32 0
+#define MLA_PROB_BF16 1
+#define MLA_PROB_FP16 2
+mla_status mla_verify_drafts(const void* target_probs, int64_t target_row_stride, const void* draft_probs,
+                             int64_t draft_row_stride, int32_t prob_type, int32_t vocab, const int32_t* drafts,
+                             const int32_t* row_start, int32_t batch, int32_t rows, const float* u_accept,
+                             const float* u_sample, const int32_t* seq_lens, int32_t* accepted, int32_t* tokens,
+                             int32_t max_out, int32_t* kept_lens, int32_t* dev_err, mla_stream_t stream);
+
+/*
+ * mla_token_mass - adds up the attention weight that every cached token
+ * received from a step's queries, all heads together:
+ *   mass[slot(t)] = m + sum_{i, h} exp(s_{i,h}(t) - lse_{i,h})
+ * over the queries i that see t, with the scores s of mla_decode_absorbed and
+ * the lse that it (or mla_prefill_absorbed) returned; m = decay * mass
+ * [slot(t)] for t < counted[b], else 0 (tokens that are new in their slot).
+ * Sequence b's queries are rows q_start[b] .. q_start[b + 1] - 1, the last of
+ * its seq_lens[b] tokens: query i (of n) sees positions t <= seq_lens[b] - n +
+ * i.  They may be fewer than the step's new tokens (an observation window).
+ *   q_lat   fp32 [n_tokens][H][512], q_pe bf16 [n_tokens][H][64], lse fp32
+ *           [n_tokens][H] (natural log; a row whose lse is not finite adds nothing)
+ *   block_table int32 [B][max_pages], q_start int32 [B + 1], seq_lens int32 [B]
+ *   counted int32 [B]: tokens whose mass is up to date; NULL: seq_lens[b] - n
+ *   max_new bound on every n (host; at most n_tokens)
+ *   mass    fp32 [num_pages * 64], by cache slot
+ *   workspace: device, >= mla_mass_workspace_bytes(...) bytes, 256-byte
+ *           aligned; contents are scratch, so calls that may overlap need
+ *           their own
+ *   A page id outside the pool is passed over and sets MLA_DEVERR_PAGE.  A
+ *   sequence whose figures do not fit (n > max_new, 0 < seq_lens[b] < n,
+ *   seq_lens[b] < 0 or > max_pages * 64, counted[b] not in [0, seq_lens[b]])
+ *   is left alone and sets MLA_DEVERR_SEQLEN; so are all when q_start
+ *   decreases or leaves [0, n_tokens].  Sequences without queries are left
+ *   alone.  Sequences of a call must not share pages.
+ *   The same call gives the same bits.  batch <= 4096, n_tokens * H < 2^31;
+ *   n_tokens == 0 or batch == 0 is a no-op.
+ */
+mla_status mla_token_mass(const mla_cache_layer* cache, const float* q_lat, const uint16_t* q_pe, const float* lse,
+                          const int32_t* block_table, int32_t max_pages, const int32_t* q_start,
+                          const int32_t* seq_lens, const int32_t* counted, int32_t batch, int32_t n_tokens,
+                          int32_t heads, int32_t max_new, float softmax_scale, float decay, void* workspace,
+                          size_t workspace_bytes, float* mass, int32_t* dev_err, mla_stream_t stream);
+
+/* Bytes of device workspace mla_token_mass needs; 0 for invalid arguments. */
+size_t mla_mass_workspace_bytes(int32_t batch, int32_t n_tokens, int32_t heads, int32_t max_new);
+
+/*
+ * mla_select_tokens - the tokens of each sequence that stay when it is cut to
+ * keep_lens[b]: the first `sinks`, the last `recent` and, of those in
+ * between, the ones with the largest mass (ties: the lower position; a NaN,
+ * and a token on a page outside the pool, which sets MLA_DEVERR_PAGE, counts
+ * as the smallest).  Where keep_lens is small, sinks come first, then recent.
+ *   mass    fp32 [num_pages * 64], by cache slot
+ *   keep_lens int32 [B], 0 and more; not below seq_lens: nothing is cut
+ *   kept    int32 [B][max_keep]: the positions that stay, increasing, -1
+ *           behind (all positions, as far as they fit, where nothing is cut)
+ *   kept_lens int32 [B]: min(keep_lens, seq_lens); not seq_lens or keep_lens
+ *   A sequence with keep_lens < 0, or with max_keep < keep_lens < seq_lens,
+ *   is not cut and sets MLA_DEVERR_SEQLEN; a seq_lens outside [0, max_pages *
+ *   64] counts as 0 and sets it.
+ *   max_pages <= 2^24, batch <= 4096; batch == 0 is a no-op.
+ */
+mla_status mla_select_tokens(const float* mass, int32_t num_pages, const int32_t* block_table, int32_t max_pages,
+                             const int32_t* seq_lens, const int32_t* keep_lens, int32_t batch, int32_t sinks,
+                             int32_t recent, int32_t* kept, int32_t max_keep, int32_t* kept_lens, int32_t* dev_err,
+                             mla_stream_t stream);
+
+/*
+ * mla_release_pages - page tables and the free list after requests got
+ * shorter, from old_lens[b] to new_lens[b] tokens.
+ *   move 0  the last tokens go (rejected drafts): the pages behind the new
+ *           length are given back
+ *   move 1  a request with new_lens < old_lens gets fresh pages for its new
+ *           length and gives all its old ones back; one with new_lens ==
+ *           old_lens keeps its pages
+ *   block_table int32 [B][max_pages]: the requests' pages (mla_plan_chunks's
+ *           output), read only
+ *   req     int32 [B]: each request's row of page_table (move 1; else may be NULL)
+ *   page_table int32 [rows][max_pages]: move 1: the fresh pages are written
+ *           into it, other entries stay (may be NULL for move 0)
+ *   free_pages int32 [free_len], free_range {head, tail}: as for the plan,
+ *           entries head .. tail - 1 are available.  Fresh pages are taken
+ *           from free_pages[head] on, pages given back are then written in
+ *           front of the first entry left, both in the order of the batch
+ *   new_table int32 [B][max_pages]: the requests' pages, -1 behind the last
+ *   lens_out int32 [B]: new_lens, or old_lens for a refused request
+ *   free_range_out int32 [2]: the next call's free_range (not free_range
+ *           itself): {head + pages taken - pages given back, tail}
+ *   No output may overlap an input or another output (MLA_ERR_INVALID_ARG),
+ *   apart from page_table and free_pages being changed in place.
+ *   A request is refused and stays as it was, while the others go on, when
+ *   its lengths do not fit (MLA_DEVERR_SEQLEN; an old length outside [0,
+ *   max_pages * 64] counts as 0), when its req is out of range or named twice
+ *   (move 1; MLA_DEVERR_PAGE), or when the list has too few pages left or too
+ *   few places in front (MLA_DEVERR_NO_PAGES: nobody behind it gets any
+ *   either).  A page id outside the pool is written as -1 and sets
+ *   MLA_DEVERR_PAGE; a bad free_range counts as empty, without places, and
+ *   sets it too.  A move writes over list entries that it took, so it is made
+ *   once; a trim made again writes the same.
+ *   rows <= 65536; batch <= 4096; batch == 0 is a no-op.
+ */
+mla_status mla_release_pages(const int32_t* old_lens, const int32_t* new_lens, const int32_t* req, int32_t batch,
+                             const int32_t* block_table, int32_t* page_table, int32_t rows, int32_t max_pages,
+                             int32_t* free_pages, int32_t free_len, const int32_t* free_range, int32_t num_pages,
+                             int32_t move, int32_t* new_table, int32_t* lens_out, int32_t* free_range_out,
+                             int32_t* dev_err, mla_stream_t stream);
+
+/*
+ * mla_move_tokens - moves the tokens that stay: token j < lens[b] of sequence
+ * b's pages in dst_table becomes token kept[b][j] of its pages in src_table,
+ * in the stored form, bit for bit; with mass, their mass too.  A sequence with
+ * lens[b] == seq_lens[b] stays where it is.
+ *   src_table, dst_table int32 [B][max_pages]: the old pages and the fresh
+ *           ones (no page of one may be a page of the other that the call
+ *           touches, or be named twice in dst_table)
+ *   seq_lens int32 [B]: tokens in the old pages
+ *   kept    int32 [B][max_keep] of mla_select_tokens; lens int32 [B]:
+ *           mla_release_pages's lens_out
+ *   mass    fp32 [num_pages * 64], by cache slot, or NULL
+ *   Slots behind a sequence's last token are left as they were.  A kept
+ *   position outside the sequence (MLA_DEVERR_SLOT) or a page id outside the
+ *   pool (MLA_DEVERR_PAGE) leaves the new token's slot as it was; a sequence
+ *   whose lens do not fit (negative, above seq_lens or max_keep; seq_lens
+ *   outside [0, max_pages * 64]) is left alone and sets MLA_DEVERR_SEQLEN.
+ *   batch <= 4096; batch == 0 is a no-op.
+ */
+mla_status mla_move_tokens(const mla_cache_layer* cache, const int32_t* src_table, const int32_t* seq_lens,
+                           const int32_t* kept, int32_t max_keep, const int32_t* lens, const int32_t* dst_table,
+                           int32_t max_pages, int32_t batch, float* mass, int32_t* dev_err, mla_stream_t stream);
 
 /* Static string for a status code. */
 const char* mla_status_string(mla_status status);

@@ -31,7 +31,12 @@ the host side of that exchange is in ``sharded``).
 A serving step over a ragged batch (decodes, drafts and prefill chunks
 together, lengths on the device) is ``mla_plan_chunks`` (block tables, slots,
 positions), ``mla_rope``, ``mla_cache_append`` and ``mla_chunk_attention``
-(its workspace: ``mla_chunk_workspace_bytes``).
+(its workspace: ``mla_chunk_workspace_bytes``).  Behind it, which tokens stay:
+``mla_verify_drafts`` (speculative drafts against the target's probabilities),
+``mla_token_mass`` (the attention weight of every cached token; workspace:
+``mla_mass_workspace_bytes``), ``mla_select_tokens`` (those with the most),
+``mla_release_pages`` (page tables and the free list of requests that got
+shorter) and ``mla_move_tokens`` (the kept tokens into their fresh pages).
 """
 
 import ctypes
@@ -51,7 +56,8 @@ PREFILL_AUTO = 0            # mla_set_prefill_path: tensor cores for large chunk
 PREFILL_DECODE_KERNELS = 1
 PREFILL_TENSOR_CORES = 2
 OUTLIER_CHANNELS = 25
-DEVERR_SLOT, DEVERR_PAGE, DEVERR_SEQLEN, DEVERR_TIMEOUT, DEVERR_NO_PAGES = 1, 2, 4, 8, 16
+DEVERR_SLOT, DEVERR_PAGE, DEVERR_SEQLEN, DEVERR_TIMEOUT, DEVERR_NO_PAGES, DEVERR_TOKEN = 1, 2, 4, 8, 16, 32
+PROB_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}     # mla_verify_drafts' probabilities
 CHUNK_SHORT = 64            # mla_chunk_attention: sequences with more new tokens count toward kv_tokens
 KV_LORA_RANK, ROPE_DIM, QK_NOPE_DIM, V_DIM, PAGE_TOKENS = 512, 64, 128, 128, 64
 DEFAULT_SOFTMAX_SCALE = 1.0 / math.sqrt(QK_NOPE_DIM + ROPE_DIM)
@@ -114,6 +120,12 @@ def _load():
         "mla_chunk_attention": (I32, [CP, P, I64, I64, P, I64, I64, P, P, P, I32, P, P, I32, I32, I32, I32, I64, F32,
                                       P, SZ, P, P, P]),
         "mla_chunk_workspace_bytes": (SZ, [I32, I32, I32, I32, I64]),
+        "mla_verify_drafts": (I32, [P, I64, P, I64, I32, I32, P, P, I32, I32, P, P, P, P, P, I32, P, P, P]),
+        "mla_token_mass": (I32, [CP, P, P, P, P, I32, P, P, P, I32, I32, I32, I32, F32, F32, P, SZ, P, P, P]),
+        "mla_mass_workspace_bytes": (SZ, [I32, I32, I32, I32]),
+        "mla_select_tokens": (I32, [P, I32, P, I32, P, P, I32, I32, I32, P, I32, P, P, P]),
+        "mla_release_pages": (I32, [P, P, P, I32, P, P, I32, I32, P, I32, P, I32, I32, P, P, P, P, P]),
+        "mla_move_tokens": (I32, [CP, P, P, P, I32, P, P, I32, I32, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -478,6 +490,126 @@ def mla_chunk_attention(cache, q_nope, q_pe, w_uk, w_uv, block_table, q_start, s
           DEFAULT_SOFTMAX_SCALE if softmax_scale is None else softmax_scale, workspace.data_ptr(),
           workspace.numel() * workspace.element_size(), _flat(o, bf16, (n, H, V_DIM), "o", dev),
           _err(dev_err, dev))
+
+
+def _pool_on(cache, dev):
+    if cache.pool.get_device() != dev:
+        raise _elsewhere(cache.pool, "the cache's pool", dev)
+    return ctypes.byref(cache.c_struct())
+
+
+def _mass_of(mass, num_pages, dev):
+    """The address of a mass array of a pool's slots."""
+    return _flat(mass, torch.float32, (num_pages * PAGE_TOKENS,), "mass", dev)
+
+
+def mla_verify_drafts(target_probs, draft_probs, drafts, row_start, u_accept, u_sample, accepted, tokens, seq_lens=None,
+                      kept_lens=None, dev_err=None, stream=None):
+    """Drafted tokens against the target's probabilities, from given random
+    numbers.  target_probs and draft_probs [rows, vocab] (float32, bfloat16 or
+    float16, contiguous rows; draft_probs None: drafts that were certain);
+    sequence b's rows are row_start[b] .. row_start[b + 1] - 1, one more than
+    its drafts.  Fills accepted [B], tokens [B, max_out] (the accepted drafts,
+    the drawn token, -1 behind) and, with seq_lens, kept_lens [B]."""
+    rows, vocab = target_probs.shape
+    B, width = tokens.shape
+    i32, f32, dev = torch.int32, torch.float32, _gpu(target_probs, "target_probs")
+    kind = PROB_TYPES.get(target_probs.dtype)
+    if kind is None or (rows and target_probs.stride()[1] != 1):
+        raise ValueError("target_probs: expected contiguous rows of float32, bfloat16 or float16, got %s" % target_probs.dtype)
+    dp, ds = None, 0
+    if draft_probs is not None:
+        if draft_probs.dtype is not target_probs.dtype or draft_probs.shape != (rows, vocab) or (rows and draft_probs.stride()[1] != 1):
+            raise ValueError("draft_probs: expected %s %s with contiguous rows, got %s %s" % (
+                target_probs.dtype, (rows, vocab), draft_probs.dtype, tuple(draft_probs.shape)))
+        if draft_probs.get_device() != dev:
+            raise _elsewhere(draft_probs, "draft_probs", dev)
+        dp, ds = draft_probs.data_ptr(), draft_probs.stride()[0]
+    if (seq_lens is None) != (kept_lens is None):
+        raise ValueError("seq_lens and kept_lens go together")
+    _step(lib.mla_verify_drafts, dev, stream, target_probs.data_ptr(), target_probs.stride()[0], dp, ds, kind, vocab,
+          _flat(drafts, i32, (rows,), "drafts", dev), _flat(row_start, i32, (B + 1,), "row_start", dev), B, rows,
+          _flat(u_accept, f32, (rows,), "u_accept", dev), _flat(u_sample, f32, (B,), "u_sample", dev),
+          None if seq_lens is None else _flat(seq_lens, i32, (B,), "seq_lens", dev), _flat(accepted, i32, (B,), "accepted", dev),
+          _flat(tokens, i32, (B, width), "tokens", dev), width,
+          None if kept_lens is None else _flat(kept_lens, i32, (B,), "kept_lens", dev), _err(dev_err, dev))
+
+
+def mla_mass_workspace_bytes(batch, n_tokens, heads, max_new):
+    return int(lib.mla_mass_workspace_bytes(int(batch), int(n_tokens), int(heads), int(max_new)))
+
+
+def mla_token_mass(cache, q_lat, q_pe, lse, block_table, q_start, seq_lens, workspace, mass, max_new, decay=1.0, counted=None,
+                   dev_err=None, softmax_scale=None, stream=None):
+    """Adds the attention weight that every cached token received from a
+    step's queries (all heads) to mass, fp32 [num_pages * 64] by cache slot,
+    which is multiplied by decay before.  q_lat fp32 [n, H, 512], q_pe bf16
+    [n, H, 64] and lse fp32 [n, H] are the attention's; sequence b's queries
+    are rows q_start[b] .. q_start[b + 1] - 1, the last of its seq_lens[b]
+    tokens.  Tokens from position counted[b] on (None: those of the queries)
+    start from 0."""
+    n, H, _ = q_lat.shape
+    B, max_pages = block_table.shape
+    f32, i32, dev = torch.float32, torch.int32, _gpu(q_lat, "q_lat")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous CUDA tensor")
+    if workspace.get_device() != dev:
+        raise _elsewhere(workspace, "workspace", dev)
+    _step(lib.mla_token_mass, dev, stream, _pool_on(cache, dev), _flat(q_lat, f32, (n, H, KV_LORA_RANK), "q_lat", dev),
+          _flat(q_pe, torch.bfloat16, (n, H, ROPE_DIM), "q_pe", dev), _flat(lse, f32, (n, H), "lse", dev),
+          _flat(block_table, i32, (B, max_pages), "block_table", dev), max_pages, _flat(q_start, i32, (B + 1,), "q_start", dev),
+          _flat(seq_lens, i32, (B,), "seq_lens", dev), None if counted is None else _flat(counted, i32, (B,), "counted", dev),
+          B, n, H, max_new, DEFAULT_SOFTMAX_SCALE if softmax_scale is None else softmax_scale, decay, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), _mass_of(mass, cache.num_pages, dev), _err(dev_err, dev))
+
+
+def mla_select_tokens(mass, block_table, seq_lens, keep_lens, kept, kept_lens, sinks=0, recent=0, dev_err=None, stream=None):
+    """The tokens of each sequence that stay when it is cut to keep_lens[b]:
+    the first ``sinks``, the last ``recent``, and those with the largest mass
+    (fp32 [num_pages * 64] by cache slot).  Fills kept [B, max_keep]
+    (positions, increasing, -1 behind) and kept_lens [B]."""
+    B, max_pages = block_table.shape
+    i32, dev = torch.int32, _gpu(mass, "mass")
+    num_pages = mass.shape[0] // PAGE_TOKENS
+    _step(lib.mla_select_tokens, dev, stream, _mass_of(mass, num_pages, dev), num_pages,
+          _flat(block_table, i32, (B, max_pages), "block_table", dev), max_pages, _flat(seq_lens, i32, (B,), "seq_lens", dev),
+          _flat(keep_lens, i32, (B,), "keep_lens", dev), B, sinks, recent, _flat(kept, i32, (B, kept.shape[1]), "kept", dev),
+          kept.shape[1], _flat(kept_lens, i32, (B,), "kept_lens", dev), _err(dev_err, dev))
+
+
+def mla_release_pages(old_lens, new_lens, req, block_table, page_table, free_pages, free_range, num_pages, new_table, lens_out,
+                      free_range_out, move=False, dev_err=None, stream=None):
+    """Page tables and the free list after requests got shorter (int32 CUDA
+    tensors; see include/mla.h).  Gives the pages behind the new lengths back
+    (req and page_table may be None) or, with move, all pages of the requests
+    that got shorter, which get fresh ones.  free_pages and page_table are
+    changed in place; fills new_table, lens_out and free_range_out."""
+    B, max_pages = block_table.shape
+    i32, dev = torch.int32, _gpu(old_lens, "old_lens")
+    if move and (req is None or page_table is None):
+        raise ValueError("req and page_table: needed to move")
+    rows = 0 if page_table is None else page_table.shape[0]
+    _step(lib.mla_release_pages, dev, stream, _flat(old_lens, i32, (B,), "old_lens", dev),
+          _flat(new_lens, i32, (B,), "new_lens", dev), None if req is None else _flat(req, i32, (B,), "req", dev), B,
+          _flat(block_table, i32, (B, max_pages), "block_table", dev),
+          None if page_table is None else _flat(page_table, i32, (rows, max_pages), "page_table", dev), rows, max_pages,
+          _flat(free_pages, i32, (free_pages.shape[0],), "free_pages", dev), free_pages.shape[0],
+          _flat(free_range, i32, (2,), "free_range", dev), num_pages, 1 if move else 0,
+          _flat(new_table, i32, (B, max_pages), "new_table", dev), _flat(lens_out, i32, (B,), "lens_out", dev),
+          _flat(free_range_out, i32, (2,), "free_range_out", dev), _err(dev_err, dev))
+
+
+def mla_move_tokens(cache, src_table, seq_lens, kept, lens, dst_table, mass=None, dev_err=None, stream=None):
+    """Moves the tokens that stay into their fresh pages: token j < lens[b] of
+    sequence b's pages in dst_table becomes token kept[b][j] of its pages in
+    src_table, bit for bit, with its mass.  A sequence with lens[b] ==
+    seq_lens[b] stays where it is."""
+    B, max_pages = src_table.shape
+    i32, dev = torch.int32, _gpu(src_table, "src_table")
+    _step(lib.mla_move_tokens, dev, stream, _pool_on(cache, dev), _flat(src_table, i32, (B, max_pages), "src_table", dev),
+          _flat(seq_lens, i32, (B,), "seq_lens", dev), _flat(kept, i32, (B, kept.shape[1]), "kept", dev), kept.shape[1],
+          _flat(lens, i32, (B,), "lens", dev), _flat(dst_table, i32, (B, max_pages), "dst_table", dev), max_pages, B,
+          None if mass is None else _mass_of(mass, cache.num_pages, dev), _err(dev_err, dev))
 
 
 def mla_set_prefill_path(path):

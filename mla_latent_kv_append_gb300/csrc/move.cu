@@ -1,0 +1,146 @@
+// mla_move_tokens: the kept tokens of a sequence, from its old pages into its
+// new ones: token j of the shorter sequence is token kept[j] of the longer one.
+//
+// A token's codes, scales, zero-points, bound and protected channels keep their
+// bits; its chunks change places (their swizzle goes by the token's place in
+// its 32-token block).
+//
+// What bounds it: reading and writing the kept tokens' bytes.  A block takes a
+// 32-token block of the destination and writes it whole; codes are gathered in
+// 16-byte chunks, the per-token fields (scales lie side by side for 32 tokens) in
+// 4-byte words, a lane per token, of which a read moves a 32-byte sector.
+#include "mla_internal.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kMoveThreads = 256, kMoveWarps = kMoveThreads / 32;
+
+struct MoveParams {
+  uint8_t* pool;
+  PageLayout L;
+  int num_pages, kpe_fmt, groups, out_groups;          // scale groups; protected channels (0: none)
+  const int32_t* src_table;
+  const int32_t* dst_table;
+  int max_pages;
+  const int32_t *seq_lens, *kept, *lens;
+  int max_keep;
+  float* mass;
+  int32_t* dev_err;
+};
+
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) {
+  __shared__ const uint8_t* s_src[kBlockTokens];       // the token's old block; null: nothing to move
+  __shared__ int s_u[kBlockTokens];                    // and its place in it
+  const int b = blockIdx.y, blk = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int len = __ldcg(p.seq_lens + b), n = __ldcg(p.lens + b);
+  if (n == len) return;                                // stays where it is
+  if (len < 0 || len > p.max_pages * kPage || n < 0 || n > len || n > p.max_keep) {
+    if (blk == 0 && tid == 0) set_err(p.dev_err, MLA_DEVERR_SEQLEN);
+    return;
+  }
+  const int j0 = blk * kBlockTokens;
+  if (j0 >= n) return;
+  const int page = __ldcg(p.dst_table + (int64_t)b * p.max_pages + blk / 2);
+  if (page < 0 || page >= p.num_pages) {
+    if (tid == 0) set_err(p.dev_err, MLA_DEVERR_PAGE);
+    return;
+  }
+  uint8_t* dst = p.pool + (int64_t)page * p.L.page_bytes + (blk & 1) * p.L.block_bytes;
+  const int count = min(kBlockTokens, n - j0);
+  if (warp == 0) {
+    const uint8_t* src = nullptr;
+    int u = 0;
+    if (lane < count) {
+      const int t = __ldcg(p.kept + (int64_t)b * p.max_keep + j0 + lane);
+      if (t < 0 || t >= len) {
+        set_err(p.dev_err, MLA_DEVERR_SLOT);
+      } else {
+        const int from = __ldcg(p.src_table + (int64_t)b * p.max_pages + t / kPage);
+        if (from < 0 || from >= p.num_pages) {
+          set_err(p.dev_err, MLA_DEVERR_PAGE);
+        } else {
+          src = p.pool + (int64_t)from * p.L.page_bytes + (t / kBlockTokens % 2) * p.L.block_bytes;
+          u = t % kBlockTokens;
+          if (p.mass)
+            p.mass[(int64_t)page * kPage + (blk & 1) * kBlockTokens + lane] = __ldcg(p.mass + (int64_t)from * kPage + t % kPage);
+        }
+      }
+    }
+    s_src[lane] = src;
+    s_u[lane] = u;
+  }
+  __syncthreads();
+  const int chunks = (int)p.L.codes_row / 16, kchunks = (int)p.L.kpe_row / 16;
+  for (int i = tid; i < count * chunks; i += kMoveThreads) {
+    const int v = i / chunks, c = i - v * chunks;
+    const uint8_t* src = s_src[v];
+    if (!src) continue;
+    const uint4 x = __ldcg(reinterpret_cast<const uint4*>(src + p.L.codes_off + s_u[v] * p.L.codes_row) + latent_chunk_pos(c, s_u[v]));
+    *(reinterpret_cast<uint4*>(dst + p.L.codes_off + v * p.L.codes_row) + latent_chunk_pos(c, v)) = x;
+  }
+  for (int i = tid; i < count * kchunks; i += kMoveThreads) {
+    const int v = i / kchunks, c = i - v * kchunks;
+    const uint8_t* src = s_src[v];
+    if (!src) continue;
+    const uint4 x =
+        __ldcg(reinterpret_cast<const uint4*>(src + p.L.kpe_off + s_u[v] * p.L.kpe_row) + kpe_chunk_pos(c, s_u[v], p.kpe_fmt));
+    *(reinterpret_cast<uint4*>(dst + p.L.kpe_off + v * p.L.kpe_row) + kpe_chunk_pos(c, v, p.kpe_fmt)) = x;
+  }
+  const uint8_t* src = s_src[lane];
+  if (!src) return;
+  const int u = s_u[lane];
+  auto words = [&](int64_t off, int groups) {
+    if (off < 0) return;
+    for (int g = warp; g < groups; g += kMoveWarps)
+      reinterpret_cast<uint32_t*>(dst + off)[g * kBlockTokens + lane] =
+          __ldcg(reinterpret_cast<const uint32_t*>(src + off) + g * kBlockTokens + u);
+  };
+  words(p.L.scale_off, p.groups);
+  words(p.L.zero_off, kNLG);
+  words(p.L.kpe_scale_off, kNKG);
+  words(p.L.bound_off, 1);
+  for (int g = warp; g < p.out_groups; g += kMoveWarps)
+    reinterpret_cast<uint16_t*>(dst + p.L.outlier_off)[g * kBlockTokens + lane] =
+        __ldcg(reinterpret_cast<const uint16_t*>(src + p.L.outlier_off) + g * kBlockTokens + u);
+}
+
+bool ok4(const void* p) { return p && ((uintptr_t)p & 3) == 0; }
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" mla_status mla_move_tokens(const mla_cache_layer* cache, const int32_t* src_table, const int32_t* seq_lens,
+                                      const int32_t* kept, int32_t max_keep, const int32_t* lens,
+                                      const int32_t* dst_table, int32_t max_pages, int32_t batch, float* mass,
+                                      int32_t* dev_err, mla_stream_t stream) {
+  MoveParams p;
+  OutlierSet outl;
+  if (!cache_check(cache, &p.L, &outl) || batch < 0 || batch > kMaxBatch || max_keep < 1) return MLA_ERR_INVALID_ARG;
+  if (max_pages < 1 || (int64_t)max_pages * kPage > (int64_t)INT32_MAX) return MLA_ERR_INVALID_ARG;
+  if (batch == 0) return MLA_OK;
+  if (!ok4(src_table) || !ok4(seq_lens) || !ok4(kept) || !ok4(lens) || !ok4(dst_table) || (mass && !ok4(mass)) ||
+      (dev_err && !ok4(dev_err)))
+    return MLA_ERR_INVALID_ARG;
+  p.pool = (uint8_t*)cache->pool;
+  p.num_pages = cache->num_pages;
+  p.kpe_fmt = cache->kpe_fmt;
+  p.groups = kDc / latent_group_size(cache->latent_fmt);
+  p.out_groups = cache->latent_fmt == MLA_FMT_INT8_OUTLIER ? kNOut : 0;
+  p.src_table = src_table;
+  p.dst_table = dst_table;
+  p.max_pages = max_pages;
+  p.seq_lens = seq_lens;
+  p.kept = kept;
+  p.lens = lens;
+  p.max_keep = max_keep;
+  p.mass = mass;
+  p.dev_err = dev_err;
+  const int64_t cap = (int64_t)max_pages * kPage < max_keep ? (int64_t)max_pages * kPage : max_keep;
+  const dim3 grid((unsigned)((cap + kBlockTokens - 1) / kBlockTokens), batch);
+  return cuda_status(launch_pdl(move_kernel, grid, dim3(kMoveThreads), 0, (cudaStream_t)stream, p));
+}
