@@ -1,121 +1,144 @@
-// mla_token_mass: the attention weight that every cached token received.
-//
-//   mass[slot(t)] = decay mass[slot(t)] + sum_{i, h} exp(s_{i,h}(t) - lse_{i,h})
-// over the step's queries i that see token t and all heads, with the decode's
-// scores s and the log-sum-exp that the attention returned.
-//
-// The simplest form: a block takes 32 tokens, dequantizes them into shared
-// memory, and its warps go through the rows, lane = token.
+// mla_token_mass: argument checks, the device plan and the queries' halves
+// (the kernel itself is in mass.cuh).
+#include <cuda_fp16.h>
 #include <math.h>
 
-#include "mla_internal.cuh"
+#include "mass_params.cuh"
+#include "scan.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int kMassThreads = 256, kMassWarps = kMassThreads / 32;
-constexpr int kMassPitch = kDc + kDr + 1;
+constexpr int kPrepThreads = 512, kPrepPer = kMaxBatch / kPrepThreads;
+constexpr int kPieces = (kDc + kDr) / 8;               // of 8 channels per row
 
-struct MassParams {
-  const uint8_t* pool;
-  PageLayout L;
-  OutlierSet outl;
-  int lf, kf, num_pages;
-  const float* q_lat;
-  const uint16_t* q_pe;
-  const float* lse;
-  const int32_t* table;
-  int max_pages;
-  const int32_t *q_start, *seq_lens, *counted;
-  int B, N, H, max_new;
-  float scale, decay;
-  float* mass;
-  int32_t* dev_err;
-};
-
-// Channel ch of block token u (0..511 latent, then k_pe), dequantized.
-__device__ float value_of(const MassParams& p, const uint8_t* blk, int u, int ch) {
-  const bool kpe = ch >= kDc;
-  const int c = kpe ? ch - kDc : ch, fmt = kpe ? p.kf : p.lf;
-  const uint8_t* row = blk + (kpe ? p.L.kpe_off + u * p.L.kpe_row : p.L.codes_off + u * p.L.codes_row);
-  auto at = [&](int chunk) { return row + 16 * (kpe ? kpe_chunk_pos(chunk, u, fmt) : latent_chunk_pos(chunk, u)); };
-  if (fmt == MLA_FMT_BF16) return bf16f(reinterpret_cast<const uint16_t*>(at(c / 8))[c % 8]);
-  if (!kpe && fmt == MLA_FMT_INT8_OUTLIER && (p.outl.mask[c >> 5] >> (c & 31) & 1u)) {
-    for (int k = 0; k < kNOut; ++k)
-      if (p.outl.ch[k] == c) return bf16f(reinterpret_cast<const uint16_t*>(blk + p.L.outlier_off)[k * kBlockTokens + u]);
-  }
-  const int group = kpe ? kKG : latent_group_size(fmt);
-  const float s = reinterpret_cast<const float*>(blk + (kpe ? p.L.kpe_scale_off : p.L.scale_off))[c / group * kBlockTokens + u];
-  if (fmt == MLA_FMT_INT4_ASYM || fmt == MLA_FMT_INT4_SYM) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(at(c / 32));
-    const int idx = c % 16, j = idx / 4, k = ((idx & 2) >> 1) + 4 * (idx & 1) + 2 * (c / 16 % 2);
-    const float q = (float)((w[j] >> (4 * k)) & 15u);
-    const float z = fmt == MLA_FMT_INT4_SYM ? 8.f : reinterpret_cast<const float*>(blk + p.L.zero_off)[c / group * kBlockTokens + u];
-    return (q - z) * s;
-  }
-  const int8_t* q = reinterpret_cast<const int8_t*>(at(c / 16));
-  const int i = c % 16;
-  return (float)(fmt == MLA_FMT_INT8_G8 && !kpe ? q[i % 8 / 2 * 4 + i / 8 * 2 + i % 2] : q[i]) * s;
-}
-
-__global__ void __launch_bounds__(kMassThreads) mass_kernel(const MassParams p) {
-  extern __shared__ float s_x[];
-  __shared__ float s_sum[kMassWarps][kBlockTokens];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.y;
-  pdl_launch_dependents();
-  pdl_wait();
+// Block 0: which sequences take part, and where their units begin.
+__device__ void plan_mass(const MassParams& p) {
+  __shared__ int64_t red[kPrepThreads / 32];
+  const int tid = threadIdx.x;
+  for (int i = tid; i < p.grid; i += kPrepThreads) p.done[i] = 0;
   bool bad = false;
-  for (int i = tid; i < p.B; i += kMassThreads) {
+  for (int i = tid; i < p.B; i += kPrepThreads) {
     const int lo = __ldcg(p.q_start + i), hi = __ldcg(p.q_start + i + 1);
     bad |= lo < 0 || hi < lo || hi > p.N;
   }
   bad = __syncthreads_or(bad);
-  const int q0 = __ldcg(p.q_start + b), n = bad ? 0 : __ldcg(p.q_start + b + 1) - q0, len = __ldcg(p.seq_lens + b);
-  if (bad || n > p.max_new || len < 0 || len > p.max_pages * kPage || (len > 0 && len < n)) {
-    if (tid == 0) set_err(p.dev_err, MLA_DEVERR_SEQLEN);
+  const int per = (p.B + kPrepThreads - 1) / kPrepThreads, b0 = tid * per;
+  MassSeq s[1];
+  int64_t units = 0, passes = 0;
+  int count = 0, err = bad ? MLA_DEVERR_SEQLEN : 0;
+  // twice: sums first, then the records
+  int64_t unit0 = 0, pass0 = 0, at = 0, total_u = 0, total_p = 0, total_c = 0;
+  for (int round = 0; round < 2; ++round) {
+    for (int k = 0; k < per && b0 + k < p.B && !bad; ++k) {
+      const int b = b0 + k;
+      MassSeq& r = s[0];
+      r.b = b;
+      r.q0 = __ldcg(p.q_start + b);
+      r.n = __ldcg(p.q_start + b + 1) - r.q0;
+      r.len = __ldcg(p.seq_lens + b);
+      if (r.n == 0) continue;
+      r.counted = p.counted ? __ldcg(p.counted + b) : r.len - r.n;
+      if (r.n > p.max_new || r.len < 0 || r.len > p.max_pages * kPage || (r.len > 0 && (r.len < r.n || r.counted < 0 || r.counted > r.len))) {
+        err |= MLA_DEVERR_SEQLEN;
+        continue;
+      }
+      if (r.len == 0) continue;
+      const int rows = r.n * p.H;
+      r.heads = p.H;
+      r.tiles = (int)(((int64_t)r.len + kMassKeys - 1) / kMassKeys);
+      r.blocks = (rows + p.R - 1) / p.R;
+      r.tile_cost = (r.blocks - 1) * mass_cost(p.R) + mass_cost(rows - (r.blocks - 1) * p.R);
+      const int64_t u = (int64_t)r.tiles * r.tile_cost, q = (int64_t)r.tiles * r.blocks;
+      if (round == 0) {
+        units += u;
+        passes += q;
+        ++count;
+      } else {
+        r.unit0 = unit0;
+        r.pass0 = pass0;
+        r.pad[0] = r.pad[1] = r.pad[2] = 0;
+        p.seqs[at++] = r;
+        unit0 += u;
+        pass0 += q;
+      }
+    }
+    if (round == 0) {
+      unit0 = block_scan<kPrepThreads>(units, red, &total_u);
+      pass0 = block_scan<kPrepThreads>(passes, red, &total_p);
+      at = block_scan<kPrepThreads>((int64_t)count, red, &total_c);
+    }
+  }
+  if (err) set_err(p.dev_err, err);
+  if (tid == 0) {
+    p.counts->units = total_u;
+    p.counts->passes = total_p;
+    p.counts->seqs = (int)total_c;
+  }
+}
+
+// The queries times the softmax scale, log2 e and kQueryGain, as two halves:
+// piece kb of 64 channels, all rows of it side by side, in the 128-byte swizzle.
+// A row whose lse is not finite is 0 (it adds nothing).
+__global__ void __launch_bounds__(kPrepThreads) mass_prep_kernel(const MassParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  if (blockIdx.x == 0) {
+    plan_mass(p);
     return;
   }
-  if (n == 0 || len == 0) return;
-  const int ctx = len - n;
-  int counted = p.counted ? __ldcg(p.counted + b) : ctx;
-  if (counted < 0 || counted > len) {
-    if (tid == 0) set_err(p.dev_err, MLA_DEVERR_SEQLEN);
-    return;
-  }
-  for (int blk = blockIdx.x; blk * kBlockTokens < len; blk += gridDim.x) {
-    const int page = __ldcg(p.table + (int64_t)b * p.max_pages + blk / 2);
-    if (page < 0 || page >= p.num_pages) {
-      if (tid == 0) set_err(p.dev_err, MLA_DEVERR_PAGE);
-      continue;
+  const float gain = p.scale_log2 * kQueryGain;
+  for (int64_t i = (int64_t)(blockIdx.x - 1) * kPrepThreads + threadIdx.x; i < p.rows * kPieces;
+       i += (int64_t)(gridDim.x - 1) * kPrepThreads) {
+    const int64_t r = i / kPieces;
+    const int c = (int)(i - r * kPieces);
+    float v[8];
+    if (c < kDc / 8) {
+      const float4* src = reinterpret_cast<const float4*>(p.q_lat + r * kDc) + 2 * c;
+      *reinterpret_cast<float4*>(v) = __ldcg(src);
+      *reinterpret_cast<float4*>(v + 4) = __ldcg(src + 1);
+    } else {
+      const uint4 w = __ldcg(reinterpret_cast<const uint4*>(p.q_pe + r * kDr) + (c - kDc / 8));
+      v[0] = bf16lo(w.x), v[1] = bf16hi(w.x), v[2] = bf16lo(w.y), v[3] = bf16hi(w.y);
+      v[4] = bf16lo(w.z), v[5] = bf16hi(w.z), v[6] = bf16lo(w.w), v[7] = bf16hi(w.w);
     }
-    const uint8_t* src = p.pool + (int64_t)page * p.L.page_bytes + (blk & 1) * p.L.block_bytes;
-    __syncthreads();
-    for (int i = tid; i < kBlockTokens * (kDc + kDr); i += kMassThreads)
-      s_x[i % kBlockTokens * kMassPitch + i / kBlockTokens] = value_of(p, src, i % kBlockTokens, i / kBlockTokens);
-    __syncthreads();
-    const int t = blk * kBlockTokens + lane;
-    float sum = 0.f;
-    for (int r = warp; r < n * p.H; r += kMassWarps) {
-      const float lse = __ldg(p.lse + (int64_t)q0 * p.H + r);
-      const float* q = p.q_lat + ((int64_t)q0 * p.H + r) * kDc;
-      const uint16_t* qp = p.q_pe + ((int64_t)q0 * p.H + r) * kDr;
-      float s = 0.f;
-      for (int c = 0; c < kDc; ++c) s = fmaf(__ldg(q + c), s_x[lane * kMassPitch + c], s);
-      for (int c = 0; c < kDr; ++c) s = fmaf(bf16f(__ldg(qp + c)), s_x[lane * kMassPitch + kDc + c], s);
-      if (t <= ctx + r / p.H && isfinite(lse)) sum += expf(fmaf(s, p.scale, -lse));
+    const bool live = fabsf(__ldcg(p.lse + r)) < INFINITY;
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float a = live ? v[2 * k] * gain : 0.f, b = live ? v[2 * k + 1] * gain : 0.f;
+      const __half2 h = __floats2half2_rn(a, b), l = __floats2half2_rn(a - __low2float(h), b - __high2float(h));
+      hi[k] = *reinterpret_cast<const uint32_t*>(&h);
+      lo[k] = *reinterpret_cast<const uint32_t*>(&l);
     }
-    s_sum[warp][lane] = sum;
-    __syncthreads();
-    if (warp == 0 && t < len) {
-      sum = 0.f;
-      for (int w = 0; w < kMassWarps; ++w) sum += s_sum[w][lane];
-      float* m = p.mass + (int64_t)page * kPage + (blk & 1) * kBlockTokens + lane;
-      *m = t < counted ? fmaf(*m, p.decay, sum) : sum;
-    }
+    uint8_t* at = p.q_tiles + ((int64_t)(c / 8) * p.rows + r) * 128 + (((c & 7) ^ (int)(r & 7)) << 4);
+    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(at + (int64_t)9 * p.rows * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
 
 bool aligned_to(const void* p, uintptr_t a) { return p && ((uintptr_t)p & (a - 1)) == 0; }
+
+bool sizes_ok(int32_t batch, int32_t n_tokens, int32_t heads, int32_t max_new) {
+  return batch >= 0 && batch <= kMaxBatch && n_tokens >= 0 && heads >= 16 && heads <= 128 && heads % 16 == 0 && max_new >= 0 &&
+         max_new <= n_tokens && (int64_t)n_tokens * heads <= (int64_t)INT32_MAX;
+}
+
+// Places the workspace's arrays; its size.
+int64_t carve(void* base, int B, int64_t rows, MassParams* p) {
+  char* c = (char*)base;
+  auto take = [&](int64_t bytes) {
+    char* at = c;
+    c += align256(bytes);
+    return at;
+  };
+  p->counts = (MassCounts*)take(sizeof(MassCounts));
+  p->seqs = (MassSeq*)take((int64_t)(B + 1) * sizeof(MassSeq));
+  p->done = (int32_t*)take(kMassMaxGrid * 4);
+  p->parts = (float*)take((int64_t)2 * kMassMaxGrid * kMassKeys * 4);
+  p->q_tiles = (uint8_t*)take(rows * 9 * 256);
+  return c - (char*)base;
+}
 
 }  // namespace
 }  // namespace mla
@@ -123,10 +146,9 @@ bool aligned_to(const void* p, uintptr_t a) { return p && ((uintptr_t)p & (a - 1
 using namespace mla;
 
 extern "C" size_t mla_mass_workspace_bytes(int32_t batch, int32_t n_tokens, int32_t heads, int32_t max_new) {
-  if (batch < 0 || batch > kMaxBatch || n_tokens < 0 || heads < 16 || heads > 128 || heads % 16 || max_new < 0 ||
-      max_new > n_tokens || (int64_t)n_tokens * heads > (int64_t)INT32_MAX)
-    return 0;
-  return 256;
+  if (!sizes_ok(batch, n_tokens, heads, max_new)) return 0;
+  MassParams p;
+  return (size_t)carve(nullptr, batch, (int64_t)n_tokens * heads, &p);
 }
 
 extern "C" mla_status mla_token_mass(const mla_cache_layer* cache, const float* q_lat, const uint16_t* q_pe,
@@ -136,18 +158,17 @@ extern "C" mla_status mla_token_mass(const mla_cache_layer* cache, const float* 
                                      float softmax_scale, float decay, void* workspace, size_t workspace_bytes,
                                      float* mass, int32_t* dev_err, mla_stream_t stream) {
   MassParams p;
-  if (!cache_check(cache, &p.L, &p.outl)) return MLA_ERR_INVALID_ARG;
-  const size_t need = mla_mass_workspace_bytes(batch, n_tokens, heads, max_new);
-  if (need == 0 || max_pages < 1 || (int64_t)max_pages * kPage > (int64_t)INT32_MAX) return MLA_ERR_INVALID_ARG;
+  if (!cache_check(cache, &p.L, &p.outl) || !sizes_ok(batch, n_tokens, heads, max_new)) return MLA_ERR_INVALID_ARG;
+  if (max_pages < 1 || (int64_t)max_pages * kPage > (int64_t)INT32_MAX) return MLA_ERR_INVALID_ARG;
   if (!(softmax_scale > 0.f) || !isfinite(softmax_scale) || !(decay >= 0.f) || !isfinite(decay)) return MLA_ERR_INVALID_ARG;
   if (batch == 0 || n_tokens == 0) return MLA_OK;
   if (max_new < 1 || !aligned_to(q_lat, 16) || !aligned_to(q_pe, 16) || !aligned_to(lse, 4) || !aligned_to(block_table, 4) ||
       !aligned_to(q_start, 4) || !aligned_to(seq_lens, 4) || (counted && !aligned_to(counted, 4)) || !aligned_to(mass, 4) ||
-      !aligned_to(workspace, 256) || workspace_bytes < need || (dev_err && !aligned_to(dev_err, 4)))
+      !aligned_to(workspace, 256) || (dev_err && !aligned_to(dev_err, 4)))
     return MLA_ERR_INVALID_ARG;
+  p.rows = (int64_t)n_tokens * heads;
+  if ((int64_t)workspace_bytes < carve(workspace, batch, p.rows, &p)) return MLA_ERR_INVALID_ARG;
   p.pool = (const uint8_t*)cache->pool;
-  p.lf = cache->latent_fmt;
-  p.kf = cache->kpe_fmt;
   p.num_pages = cache->num_pages;
   p.q_lat = q_lat;
   p.q_pe = q_pe;
@@ -161,20 +182,24 @@ extern "C" mla_status mla_token_mass(const mla_cache_layer* cache, const float* 
   p.N = n_tokens;
   p.H = heads;
   p.max_new = max_new;
-  p.scale = softmax_scale;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.decay = decay;
   p.mass = mass;
   p.dev_err = dev_err;
-  static int configured[64] = {0};
-  constexpr int kSmem = kBlockTokens * kMassPitch * 4;
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !configured[dev]) {
-    const mla_status st = cuda_status(cudaFuncSetAttribute(mass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
-    if (st != MLA_OK) return st;
-    if (dev >= 0 && dev < 64) configured[dev] = 1;
+  p.wait_ns = wait_limit_ns();
+  const int64_t most = (int64_t)max_new * heads;
+  p.R = most <= 16 ? 16 : (most <= 32 ? 32 : (most <= 64 ? 64 : kMassMaxRows));
+  const int sms = device_sm_count();
+  p.grid = sms < 1 ? 1 : (sms < kMassMaxGrid ? sms : kMassMaxGrid);
+  const int64_t want = 1 + (p.rows * kPieces + kPrepThreads - 1) / kPrepThreads;
+  const mla_status st = cuda_status(launch_pdl(mass_prep_kernel, dim3((unsigned)(want < 4 * p.grid ? want : 4 * p.grid)),
+                                               dim3(kPrepThreads), 0, (cudaStream_t)stream, p));
+  if (st != MLA_OK) return st;
+  switch (cache->latent_fmt) {
+    case MLA_FMT_BF16: return launch_mass_bf16(p, cache->latent_fmt, cache->kpe_fmt, (cudaStream_t)stream);
+    case MLA_FMT_INT8_SYM: return launch_mass_int8(p, cache->latent_fmt, cache->kpe_fmt, (cudaStream_t)stream);
+    case MLA_FMT_INT4_ASYM:
+    case MLA_FMT_INT4_SYM: return launch_mass_int4(p, cache->latent_fmt, cache->kpe_fmt, (cudaStream_t)stream);
+    default: return launch_mass_int8_blocks(p, cache->latent_fmt, cache->kpe_fmt, (cudaStream_t)stream);
   }
-  const int64_t blocks = (int64_t)max_pages * 2;
-  const dim3 grid((unsigned)(blocks < 1024 ? blocks : 1024), batch);
-  return cuda_status(launch_pdl(mass_kernel, grid, dim3(kMassThreads), kSmem, (cudaStream_t)stream, p));
 }

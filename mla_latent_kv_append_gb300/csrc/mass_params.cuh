@@ -1,0 +1,84 @@
+// Shared by the translation units of mla_token_mass (mass*.cu).
+#pragma once
+
+#include "mla_internal.cuh"
+
+namespace mla {
+
+constexpr int kMassKeys = 128;                         // keys per tile
+constexpr int kMassMaxRows = 128;                      // most rows per pass
+constexpr int kMassMaxGrid = 512;                      // most blocks
+// Cached values are multiplied by kKeyGain, queries (with the softmax scale and
+// log2 e) by kQueryGain: halves keep 22 bits of values down to 2^-5 and 2^-8, and stay
+// finite up to 16376 and 2047.
+constexpr float kKeyGain = 4.f, kQueryGain = 32.f, kMassUngain = 1.f / (kKeyGain * kQueryGain);
+
+// One sequence with queries and tokens, in the order of the batch.  Its rows r =
+// i H + h are cut into row blocks of R; a pass is a row block of a key tile, the
+// passes of a tile lie side by side.  A pass costs mass_cost(its rows) units.
+struct __align__(16) MassSeq {
+  int64_t unit0;          // units before this sequence's
+  int64_t pass0;          // passes before this sequence's
+  int32_t b, q0, n, len;  // batch index, first query row (token), queries, cached tokens
+  int32_t counted;        // tokens whose mass is up to date
+  int32_t tiles, blocks;  // key tiles, row blocks
+  int32_t tile_cost;      // units of a key tile
+  int32_t heads, pad[3];
+};
+static_assert(sizeof(MassSeq) == 64, "four 16-byte loads");
+
+struct MassCounts {
+  int64_t units, passes;
+  int32_t seqs, pad;
+};
+
+// Units of a pass with this many rows.
+__host__ __device__ constexpr int mass_cost(int rows) { return rows <= 48 ? 3 : (rows + 15) / 16; }
+
+// Run x of G equal runs over U units begins here; the run that holds unit u.
+__device__ __forceinline__ int64_t mass_run(int64_t U, int x, int G) {
+  if (U <= (int64_t)(0xFFFFFFFFu / 1024u)) return (uint32_t)U * (uint32_t)x / (uint32_t)G;
+  return U * x / G;
+}
+__device__ __forceinline__ int mass_run_of(int64_t U, int64_t u, int G) { return (int)(((u + 1) * G - 1) / U); }
+
+struct MassParams {
+  const uint8_t* pool;
+  PageLayout L;
+  OutlierSet outl;
+  int num_pages;
+  const float* q_lat;
+  const uint16_t* q_pe;
+  const float* lse;
+  const int32_t* table;
+  int max_pages;
+  const int32_t *q_start, *seq_lens, *counted;
+  int B, N, H, max_new;
+  float scale_log2, decay;
+  float* mass;
+  int32_t* dev_err;
+  uint64_t wait_ns;
+  int R, grid;
+  int query_pieces, raw_slots;                         // pieces of the queries and raw blocks in shared memory
+  int64_t rows;                                        // N H
+  // workspace
+  MassCounts* counts;
+  MassSeq* seqs;
+  int32_t* done;          // [kMassMaxGrid] passes finished of the tile that a run ends in
+  float* parts;           // [2 kMassMaxGrid][128]
+  uint8_t* q_tiles;       // [hi, lo][9][rows][64] fp16, swizzled
+};
+
+__device__ __forceinline__ void mass_store(const MassParams& p, int page, int t, int counted, float w) {
+  float* m = p.mass + (int64_t)page * kPage + (t & (kPage - 1));
+  *m = t < counted ? fmaf(*m, p.decay, w) : w;
+}
+
+// The kernel over the key tiles, by latent format (one translation unit each);
+// MLA_ERR_UNSUPPORTED for another unit's formats.
+mla_status launch_mass_bf16(const MassParams& p, int lf, int kf, cudaStream_t stream);
+mla_status launch_mass_int8(const MassParams& p, int lf, int kf, cudaStream_t stream);
+mla_status launch_mass_int8_blocks(const MassParams& p, int lf, int kf, cudaStream_t stream);
+mla_status launch_mass_int4(const MassParams& p, int lf, int kf, cudaStream_t stream);
+
+}  // namespace mla

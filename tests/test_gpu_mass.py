@@ -277,3 +277,19 @@ def test_two_calls_at_once(mla):
                                stream=st)
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("H,lens", [(16, [(3000, 1), (500, 1)]), (64, [(900, 5), (300, 4)])], ids=["resident", "streamed"])
+def test_waits_that_run_out_end_the_call(mla, H, lens):
+    """With no patience the kernel gives up and says so; the context stays usable and the next call is right."""
+    t = Mass(mla, lens, H, seed=21)
+    want = t.go()
+    prev = mla.mla_set_wait_limit_ns(0)
+    try:
+        for _ in range(3):
+            t.go()
+    finally:
+        mla.mla_set_wait_limit_ns(prev)
+    assert t.err.item() in (0, mla.DEVERR_TIMEOUT)
+    t.err.zero_()
+    assert torch.equal(t.go(), want) and t.err.item() == 0
