@@ -30,10 +30,13 @@ namespace {
 
 using namespace tc;
 
-// Warps: 16 convert, 4 read the scores, then one each issues the MMAs, the
+// Warps: 24 convert, 4 read the scores, then one each issues the MMAs, the
 // cache's copies and the queries' copies; one is idle.
-constexpr int kMassConvert = 16, kMassRead = 16, kMassMma = 20, kMassRaw = 21, kMassQ = 22, kMassWarps = 24;
+constexpr int kMassGroups = 6, kMassConvert = 4 * kMassGroups, kMassRead = kMassConvert, kMassMma = kMassRead + 4, kMassRaw = kMassMma + 1,
+              kMassQ = kMassMma + 2, kMassWarps = kMassMma + 4;
 constexpr int kMassThreads = 32 * kMassWarps;
+constexpr int kMassUnits = kLatentUnits + kKpeUnits;   // 18 units of 32 channels, two to a piece
+static_assert(kMassUnits == 3 * kMassGroups && kMassThreads == 1024, "a converting warp has three units of a tile");
 constexpr int kMassSmem = 232448 - 1024;               // a block's shared memory, less the alignment slack
 constexpr int kMassMaxRaw = 8;
 constexpr int kMassAligned = 1024;
@@ -44,30 +47,82 @@ enum { mA = 0, mAFree = mA + 8, mS = mAFree + 8, mE = mS + 2, mRaw = mE + 2, mRa
 constexpr int kMassMisc = 8 * mCount + 64 + kMassMaxRows * 4;      // barriers, words, the rows' lse
 static_assert(8 * mCount + 64 <= 1024, "barriers and words");
 
+// Byte offsets in a 32-token block of a format pair (compute_layout's), known
+// at compile time: with runtime ones a fifth of the conversion's instructions
+// were address arithmetic.
+template <int LF, int KF>
+struct BlockAt {
+  static constexpr int kRow = 16 * UnitShape<LF, false>::kWords * kLatentUnits, kKpeRow = 16 * UnitShape<KF, true>::kWords * kKpeUnits;
+  static constexpr int kScale = kBlockTokens * kRow;
+  static constexpr int kGroups = LF == MLA_FMT_BF16 ? 0 : kDc / latent_group_size(LF);
+  static constexpr int kZero = kScale + 128 * kGroups;
+  static constexpr int kOutlier = kZero + (LF == MLA_FMT_INT4_ASYM ? 128 * kGroups : 0);
+  static constexpr int kKpe = kOutlier + (LF == MLA_FMT_INT8_OUTLIER ? kOutFieldBytes : 0);
+  static constexpr int kKpeScale = kKpe + kBlockTokens * kKpeRow;
+  static constexpr int kBytes = kKpeScale + (KF == MLA_FMT_BF16 ? 0 : 128 * kNKG) + (LF == MLA_FMT_BF16 ? 0 : 128);
+  static_assert(kBytes == block_bytes<LF, KF>(), "the documented block");
+};
+
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds4(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// Unit c of token u: row = the token's code row in shared memory (on a 32-byte
+// boundary or more, so that chunk i of the unit is chunk 0's address with i's bits
+// flipped), scale and zero = the token's entries of group 0.
+template <int FMT, bool KPE>
+__device__ __forceinline__ void load_split(uint32_t row, uint32_t scale, uint32_t zero, int u, int c, RawUnit<FMT, KPE>& r) {
+  using S = UnitShape<FMT, KPE>;
+  const uint32_t at = row + 16 * (KPE ? kpe_chunk_pos(c * S::kWords, u, FMT) : latent_chunk_pos(c * S::kWords, u));
+#pragma unroll
+  for (int i = 0; i < S::kWords; ++i) r.w[i] = lds16(at ^ (16 * i));
+  if constexpr (S::kScales > 0) {
+    const uint32_t g = 128 * (c * kUnitChannels / S::kGroup);
+#pragma unroll
+    for (int i = 0; i < S::kScales; ++i) {
+      r.s[i] = lds4(scale + g + 128 * i);
+      if constexpr (S::kZeros) r.z[i] = lds4(zero + g + 128 * i);
+    }
+  }
+}
+
 template <int LF, int KF>
 struct MassShape {
-  static constexpr int kBlock = block_bytes<LF, KF>();
-  static constexpr bool kSplit = LF != MLA_FMT_BF16;   // a latent piece has a low half
-  static constexpr int kCols = kSplit ? 64 : 32;       // TMEM columns of a piece (64 channels)
-  static constexpr int kSlots = 256 / 64;              // pieces in TMEM
-  // shared memory: queries of R rows in `qs` pieces, then raw blocks
+  static constexpr int kBlock = BlockAt<LF, KF>::kBytes;
+  // A bulk copy costs 85 ns of the copy engine besides its bytes, and a block of
+  // 4-bit codes is 18 KB: whole pages of those (a stream of nothing but copies:
+  // 18.5 KB each 5.6 TB/s, 23.7 KB 7.0, 37 KB 6.9).
+  static constexpr int kBlocks = kBlock < 20000 ? 2 : 1;             // 32-token blocks of a copy
+  static constexpr int kCopy = kBlocks * kBlock;
+  static constexpr int kTileCopies = 4 / kBlocks;
+  // TMEM columns of a piece (64 channels): a bf16 value has no low half
+  static constexpr int kCols = LF == MLA_FMT_BF16 && KF == MLA_FMT_BF16 ? 32 : 64;
+  // shared memory: queries of R rows in `qs` pieces, then the copies
   static constexpr int query_pieces(int R) {
-    const int room = kMassSmem - 2048, piece = R * 256;
-    if (9 * piece + 5 * kBlock <= room) return 9;
-    return (room - 5 * kBlock) / piece >= 2 ? (room - 5 * kBlock) / piece : 2;
+    const int room = kMassSmem - 2048 - (kTileCopies + 1) * kCopy, piece = R * 256;
+    return 9 * piece <= room ? 9 : (room / piece >= 2 ? room / piece : 2);
   }
   static constexpr int raw_slots(int R) {
-    const int n = (kMassSmem - 2048 - query_pieces(R) * R * 256) / kBlock;
+    const int n = (kMassSmem - 2048 - query_pieces(R) * R * 256) / kCopy;
     return n < kMassMaxRaw ? n : kMassMaxRaw;
   }
-  static_assert(raw_slots(kMassMaxRows) >= 4 && raw_slots(64) >= 4 && raw_slots(32) >= 4 && raw_slots(16) >= 4, "a whole key tile");
+  static_assert(raw_slots(kMassMaxRows) >= kTileCopies && raw_slots(64) >= kTileCopies && raw_slots(32) >= kTileCopies &&
+                    raw_slots(16) >= kTileCopies,
+                "a whole key tile");
 };
 
 // A block's walk over its passes (a row block of a key tile).
 struct MassWalk {
   const MassSeq* seqs;
   int n_seqs, k, tile, rb, R, cost;                    // cost: of a full row block
-  int64_t at, hi;
+  int64_t left;                                        // passes, the current one included
   MassSeq s;
 
   __device__ __forceinline__ void load() {
@@ -75,13 +130,6 @@ struct MassWalk {
     int4* d = reinterpret_cast<int4*>(&s);
 #pragma unroll
     for (int i = 0; i < (int)sizeof(MassSeq) / 16; ++i) d[i] = __ldcg(r + i);
-  }
-  __device__ __forceinline__ void open(const MassParams& p) {
-    seqs = p.seqs;
-    n_seqs = __ldcg(&p.counts->seqs);
-    R = p.R;
-    cost = mass_cost(R);
-    k = -1;
   }
   // All lanes of a warp: the sequence of unit u, 32 probes per round.
   __device__ __forceinline__ void find(int64_t u) {
@@ -100,39 +148,37 @@ struct MassWalk {
       load();
     }
   }
-  // All lanes of a warp: passes that start before unit v.
+  // All lanes of a warp: passes that start before unit v, and the first that does not.
   __device__ __forceinline__ int64_t passes_before(int64_t v) {
     find(v);
     const int64_t d = v - s.unit0, t = d / s.tile_cost;
-    const int off = (int)(d - t * s.tile_cost);
-    return s.pass0 + t * s.blocks + min(s.blocks, (off + cost - 1) / cost);
+    tile = (int)t;
+    rb = min(s.blocks, ((int)(d - t * s.tile_cost) + cost - 1) / cost);
+    return s.pass0 + t * s.blocks + rb;
   }
-  __device__ __forceinline__ void start(int64_t lo, int64_t hi_) {
-    hi = hi_;
-    find(lo);
-    const int64_t d = lo - s.unit0;
-    tile = (int)(d / s.tile_cost);
-    rb = ((int)(d - (int64_t)tile * s.tile_cost) + cost - 1) / cost;
-    settle();
+  __device__ __forceinline__ void open(const MassParams& p, int64_t U, int64_t lo, int64_t hi) {
+    seqs = p.seqs;
+    n_seqs = __ldcg(&p.counts->seqs);
+    R = p.R;
+    cost = mass_cost(R);
+    k = -1;
+    left = hi == U ? __ldcg(&p.counts->passes) : passes_before(hi);
+    left -= passes_before(lo);
+    if (left > 0 && rb == s.blocks) step();
   }
-  __device__ __forceinline__ void settle() {
-    if (rb >= s.blocks) {
-      rb = 0;
-      if (++tile >= s.tiles) {
-        tile = 0;
-        if (++k < n_seqs) load();
-        else {
-          at = hi;
-          return;
-        }
-      }
+  __device__ __forceinline__ bool valid() const { return left > 0; }
+  // From behind a tile's last row block.
+  __device__ __forceinline__ void step() {
+    rb = 0;
+    if (++tile >= s.tiles) {
+      tile = 0;
+      ++k;
+      load();
     }
-    at = s.unit0 + (int64_t)tile * s.tile_cost + (int64_t)rb * cost;
   }
-  __device__ __forceinline__ bool valid() const { return at < hi; }
   __device__ __forceinline__ void next() {
-    ++rb;
-    settle();
+    --left;
+    if (++rb >= s.blocks && left > 0) step();
   }
   __device__ __forceinline__ int rows() const { return min(R, s.n * s.heads - rb * R); }
 };
@@ -140,14 +186,15 @@ struct MassWalk {
 __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
 __device__ __forceinline__ uint32_t as_word(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-// (a, b) as halves: hi + lo.
+// (a, b) as halves: lo - hi.
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(a, b);
+  const __half2 h = __floats2half2_rn(-a, -b);
   hi = as_word(h);
-  lo = as_word(__floats2half2_rn(a - __low2float(h), b - __high2float(h)));
+  lo = as_word(__floats2half2_rn(a + __low2float(h), b + __high2float(h)));
 }
 
-// The unit's 32 channels times kKeyGain: hi[i] + lo[i] = channels (2i, 2i + 1).
+// The unit's 32 channels times kKeyGain: lo[i] - hi[i] = channels (2i, 2i + 1).
+// Any scale and zero-point.
 template <int FMT, bool KPE>
 __device__ __forceinline__ void split_any(const RawUnit<FMT, KPE>& r, uint32_t* hi, uint32_t* lo) {
   using S = UnitShape<FMT, KPE>;
@@ -179,15 +226,85 @@ __device__ __forceinline__ void split_any(const RawUnit<FMT, KPE>& r, uint32_t* 
 
 template <int FMT, bool KPE>
 __device__ __forceinline__ void split_unit(const RawUnit<FMT, KPE>& r, uint32_t* hi, uint32_t* lo) {
+  using S = UnitShape<FMT, KPE>;
   if constexpr (FMT == MLA_FMT_BF16) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) hi[4 * i + j] = half2_bits(bf16lo(w[j]) * kKeyGain, bf16hi(w[j]) * kKeyGain);
+      for (int j = 0; j < 4; ++j) hi[4 * i + j] = half2_bits(bf16lo(w[j]) * -kKeyGain, bf16hi(w[j]) * -kKeyGain);
     }
   } else {
-    split_any<FMT, KPE>(r, hi, lo);
+    // Two channels at a time in fp16 arithmetic.  Codes q become exact halves
+    // (placed in the mantissa of 1024, the offset and zero-point taken off), the scale
+    // is two halves, a + b; then with h = fl(q a) the rest q a - h is exact in a half
+    // (q has at most 8 bits), and l = fl(q b + (q a - h)): three instructions a
+    // pair, 2^-22 of x.  (h is made as q (-a), which the last step needs, and stays
+    // negated: the MMA turns it back.)  b lies on fp16's subnormal grid, off by up to 2^-25: for
+    // scales from 2^-9 on 2^-18 of them at most.  Needs scales in that range and
+    // zero-points that keep q a finite; other units go through fp32.
+    constexpr uint32_t kLow = 0x3B000000u, kHigh = 0x42800000u;      // 2^-9 .. 64
+    uint32_t most = 0u;
+    float top = 0.f;
+#pragma unroll
+    for (int g = 0; g < S::kScales; ++g) {
+      most = max(most, __float_as_uint(r.s[g]) - kLow);
+      if constexpr (S::kZeros) top = max_nan(top, fabsf(r.z[g]));
+    }
+    if (most > kHigh - kLow || !(top <= 127.f)) {
+      split_any<FMT, KPE>(r, hi, lo);
+      return;
+    }
+    __half2 a[S::kScales], b[S::kScales], minus_a[S::kScales];
+#pragma unroll
+    for (int g = 0; g < S::kScales; ++g) {
+      const float s = r.s[g] * kKeyGain;
+      a[g] = __float2half2_rn(s);
+      minus_a[g] = as_half2(as_word(a[g]) ^ 0x80008000u);
+      b[g] = __float2half2_rn(s - __low2float(a[g]));
+    }
+    auto put = [&](int ch, __half2 q, int g) {
+      const __half2 h = __hmul2_rn(q, minus_a[g]);
+      hi[ch / 2] = as_word(h);
+      lo[ch / 2] = as_word(__hfma2(q, b[g], __hfma2(q, a[g], h)));
+    };
+    if constexpr (S::kInt4) {
+      __half2 off[S::kScales], off16[S::kScales];      // -(1024 + zero), -(64 + zero): exact
+#pragma unroll
+      for (int g = 0; g < S::kScales; ++g) {
+        const float zero = S::kZeros ? r.z[S::kZeros ? g : 0] : 8.f;
+        off[g] = __float2half2_rn(-1024.f - zero);
+        off16[g] = __float2half2_rn(-64.f - zero);
+      }
+      const __half2 sixteenth = __float2half2_rn(0.0625f);
+      const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // nibbles k and k + 4 are adjacent channels; odd ones stand 16 times as high
+          const uint32_t t = k < 2 ? w[j] : w[j] >> 8;
+          const int ch = int4_nibble_channel(j, k), g = ch / S::kGroup;
+          put(ch, (k & 1) ? __hfma2(as_half2((t & 0x00F000F0u) | 0x64006400u), sixteenth, off16[g])
+                          : __hadd2(as_half2((t & 0x000F000Fu) | 0x64006400u), off[g]),
+              g);
+        }
+    } else {
+      const __half2 off = __float2half2_rn(-1152.f);   // 1024 and the codes' bias of 128
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t w[4] = {r.w[i].x ^ 0x80808080u, r.w[i].y ^ 0x80808080u, r.w[i].z ^ 0x80808080u,
+                               r.w[i].w ^ 0x80808080u};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            const int ch = 16 * i + (!KPE && S::kGroup == 8 ? 2 * j + 4 * k : 4 * j + k);
+            put(ch, __hadd2(as_half2(__byte_perm(w[j], 0x64646464u, k ? 0x4342 : 0x4140)), off),
+                S::kScales > 1 ? ch / S::kGroup : 0);
+          }
+      }
+    }
   }
 }
 
@@ -215,6 +332,7 @@ __device__ __forceinline__ void patch_split(const uint8_t* blk, const PageLayout
   }
 }
 
+constexpr uint32_t kNegateA = 1u << 13;                // instruction descriptor: the products of -A
 __device__ __forceinline__ void tmem_put16(uint32_t t, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(t),
@@ -222,6 +340,13 @@ __device__ __forceinline__ void tmem_put16(uint32_t t, const uint32_t* v) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// One arrival for the warp (32 on one barrier are carried out one after the
+// other: a tile's 3200 of them took 4700 cycles).
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) bar_arrive(bar);
+}
 
 // Whether any thread of the four reading warps says so; also their barrier.
 __device__ __forceinline__ bool vote_128(bool mine) {
@@ -237,13 +362,18 @@ __device__ __forceinline__ bool vote_128(bool mine) {
 template <int LF, int KF>
 __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams p) {
   using SH = MassShape<LF, KF>;
-  constexpr int NA = SH::kSlots, COLS = 64;
+  constexpr int COLS = SH::kCols;
   extern __shared__ uint8_t mass_smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(mass_smem_raw) + kMassAligned - 1) & ~(uintptr_t)(kMassAligned - 1));
   const int R = p.R, QS = p.query_pieces, NS = p.raw_slots;
   const bool resident = QS == 9;
-  const uint32_t sb = smem_u32(sm), s_raw = QS * R * 256, bars = sb + s_raw + NS * SH::kBlock;
-  uint8_t* words = sm + s_raw + NS * SH::kBlock + 8 * mCount;
+  // TMEM: two buffers of scores, then pieces of PU units.  Up to 64 rows the MMAs
+  // of 64 channels take less time (256 cycles) than their thread takes for a
+  // piece besides (370), so a piece has 192 channels.
+  const int d_cols = R <= 64 ? 64 : kMassMaxRows, PU = R <= 64 ? 6 : 2, cols = COLS / 2 * PU, NA = min(8, (512 - 2 * d_cols) / cols);
+  const int pieces = kMassUnits / PU;
+  const uint32_t sb = smem_u32(sm), s_raw = QS * R * 256, bars = sb + s_raw + NS * SH::kCopy;
+  uint8_t* words = sm + s_raw + NS * SH::kCopy + 8 * mCount;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words);
   volatile int* abort = reinterpret_cast<volatile int*>(words + 4);
   volatile int* s_last = reinterpret_cast<volatile int*>(words + 8);
@@ -252,16 +382,16 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {
-      bar_init(bars + 8 * (mA + i), 128);              // four warps write a piece
+      bar_init(bars + 8 * (mA + i), 4 * PU);           // four warps write a unit
       bar_init(bars + 8 * (mAFree + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(bars + 8 * (mS + i), 1);
-      bar_init(bars + 8 * (mE + i), 128);
+      bar_init(bars + 8 * (mE + i), 4);
     }
     for (int i = 0; i < kMassMaxRaw; ++i) {
       bar_init(bars + 8 * (mRaw + i), 1);
-      bar_init(bars + 8 * (mRawFree + i), 128);        // the four warps of the block's lanes
+      bar_init(bars + 8 * (mRawFree + i), kMassGroups * SH::kBlocks);    // the warps of its tokens' lanes
     }
     for (int i = 0; i < 9; ++i) {
       bar_init(bars + 8 * (mQ + i), 1);
@@ -276,7 +406,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tbase = *tmem_slot, t_a = tbase + 256;              // scores: two buffers of 128 columns; then the pieces
+  const uint32_t tbase = *tmem_slot, t_a = tbase + 2 * d_cols;
   pdl_launch_dependents();
   pdl_wait();
 
@@ -286,61 +416,70 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
   const int64_t lo = work ? mass_run(U, x, G) : 0, hi = work ? mass_run(U, x + 1, G) : 0;
   bool ok = true;
   if (work && warp < kMassConvert) {
-    // ---- Warp (s, d): lanes 32 d .. 32 d + 31 (a 32-token block of the tile) of
-    // the pieces s, s + 4, ... of the run; lane = token.
-    const int s = warp >> 2, d = warp & 3;
+    // ---- Warp (e, d): lanes 32 d .. 32 d + 31 (a 32-token block of the tile) of
+    // units e, e + 6 and e + 12; lane = token.
+    using AT = BlockAt<LF, KF>;
+    const int e = warp >> 2, d = warp & 3;
     const uint32_t tl = (uint32_t)(32 * d) << 16;
     int64_t n_pass;
     {
       MassWalk wk;
-      wk.open(p);
-      n_pass = (x + 1 == G ? __ldcg(&p.counts->passes) : wk.passes_before(hi)) - wk.passes_before(lo);
+      wk.open(p, U, lo, hi);
+      n_pass = wk.left;
     }
-    uint32_t kb = s, blk = d, turn = 0;                // piece of the pass, raw block, how many pieces this warp has made
-    for (int64_t it = 0; it < n_pass;) {
-      const uint32_t slot = blk % NS;
-      if (!warp_wait(bars + 8 * (mRaw + slot), (blk / NS) & 1, p.wait_ns, abort)) {
-        ok = false;
-        break;
-      }
-      const uint8_t* raw = sm + s_raw + slot * SH::kBlock;
-      const uint32_t a = t_a + s * COLS + tl;
-      bool split = true;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
+    int rs = d / SH::kBlocks, slot0 = 0;               // raw copy; TMEM place of the pass's first piece
+    uint32_t raw_round = 0, round0 = 0;                // how often they went round
+    for (; n_pass > 0; --n_pass) {
+      if (!(ok = warp_wait(bars + 8 * (mRaw + rs), raw_round & 1, p.wait_ns, abort))) break;
+      const uint32_t raw = s_raw + rs * SH::kCopy + (d % SH::kBlocks) * SH::kBlock, at = sb + raw;
+#pragma unroll 1
+      for (int j = e; j < kMassUnits; j += kMassGroups) {
         uint32_t h[16], l[16];
-        if (kb < 8) {
+        const bool last = j + kMassGroups >= kMassUnits;
+        bool split;
+        if (j < kLatentUnits) {
           RawUnit<LF, false> r;
-          load_unit<LF, false>(raw, p.L, lane, 2 * kb + half, r);
+          load_split<LF, false>(at + lane * AT::kRow, at + AT::kScale + 4 * lane, at + AT::kZero + 4 * lane, lane, j, r);
+          if (last && LF != MLA_FMT_INT8_OUTLIER) warp_arrive(bars + 8 * (mRawFree + rs));
           split_unit<LF, false>(r, h, l);
-          patch_split<LF>(raw, p.L, p.outl, lane, 2 * kb + half, h, l);
+          patch_split<LF>(sm + raw, p.L, p.outl, lane, j, h, l);
+          if (last && LF == MLA_FMT_INT8_OUTLIER) warp_arrive(bars + 8 * (mRawFree + rs));      // its protected channels lie there
           split = LF != MLA_FMT_BF16;
         } else {
           RawUnit<KF, true> r;
-          load_unit<KF, true>(raw, p.L, lane, half, r);
+          load_split<KF, true>(at + AT::kKpe + lane * AT::kKpeRow, at + AT::kKpeScale + 4 * lane, 0u, lane, j - kLatentUnits, r);
+          warp_arrive(bars + 8 * (mRawFree + rs));
           split_unit<KF, true>(r, h, l);
           split = KF != MLA_FMT_BF16;
         }
-        // the piece before, four earlier, has been multiplied
-        if (half == 0 && turn > 0 && !warp_wait(bars + 8 * (mAFree + s), (turn - 1) & 1, p.wait_ns, abort)) {
-          ok = false;
-          break;
+        const int piece = PU == 6 ? j / 6 : j >> 1, unit = j - piece * PU;
+        int slot = slot0 + piece;
+        uint32_t round = round0;
+        while (slot >= NA) {
+          slot -= NA;
+          ++round;
         }
+        // the place's last piece has been multiplied (releases come in the ring's
+        // order, so the barrier is at most one phase behind)
+        if (round > 0 && !(ok = warp_wait(bars + 8 * (mAFree + slot), (round - 1) & 1, p.wait_ns, abort))) break;
         fence_after();
-        tmem_put16(a + 16 * half, h);
-        if (split) tmem_put16(a + 32 + 16 * half, l);
+        const uint32_t a = t_a + slot * cols + tl + 16 * unit;
+        tmem_put16(a, h);
+        if (split) tmem_put16(a + 16 * PU, l);
+        tmem_put_wait();
+        fence_before();
+        warp_arrive(bars + 8 * (mA + slot));
       }
       if (!ok) break;
-      tmem_put_wait();
-      fence_before();
-      bar_arrive(bars + 8 * (mA + s));
-      ++turn;
-      kb += 4;
-      if (kb >= 9) {                                   // this warp's last piece of the pass
-        bar_arrive(bars + 8 * (mRawFree + slot));
-        kb -= 9;
-        blk += 4;
-        ++it;
+      rs += SH::kTileCopies;
+      if (rs >= NS) {
+        rs -= NS;
+        ++raw_round;
+      }
+      slot0 += pieces;
+      while (slot0 >= NA) {
+        slot0 -= NA;
+        ++round0;
       }
     }
     if (!ok) {
@@ -348,31 +487,46 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
       *abort = 1;
     }
   } else if (work && warp >= kMassRead && warp < kMassMma) {
-    // ---- the scores: thread = key
+    // ---- the scores: thread = key.  The walk is a pass ahead, so that a tile's
+    // old masses are there when its scores are; the lanes fetch the page ids of
+    // 32 tiles at a time.
     MassWalk wk;
-    wk.open(p);
-    wk.start(lo, hi);
-    const int key = threadIdx.x - 32 * kMassRead;
+    wk.open(p, U, lo, hi);
+    const int key = threadIdx.x - 32 * kMassRead, half = (warp & 3) >> 1;        // the warp's keys lie in one page of the tile
     const uint32_t tl = (uint32_t)(32 * (warp & 3)) << 16;
+    int ids = -1, ids_k = -1, ids_tile = 0, page = -1, parts = 0;
+    float old = 0.f, total = 0.f;
+    // the walk's tile: its page (-1: none that counts) and old mass
+    auto look = [&](int& pg, float& m) {
+      const int t = wk.tile * kMassKeys + key;
+      if (wk.k != ids_k || wk.tile >= ids_tile + 32) {
+        ids_k = wk.k;
+        ids_tile = wk.tile;
+        const int at = 2 * (wk.tile + lane) + half;
+        ids = (int64_t)at * kPage < wk.s.len ? __ldcg(p.table + (int64_t)wk.s.b * p.max_pages + at) : -1;
+      }
+      pg = __shfl_sync(0xffffffffu, ids, wk.tile - ids_tile);
+      m = 0.f;
+      if (t >= wk.s.len) {
+        pg = -1;
+      } else if (pg < 0 || pg >= p.num_pages) {
+        set_err(p.dev_err, MLA_DEVERR_PAGE);
+        pg = -1;
+      } else if (t < wk.s.counted) {
+        m = p.mass[(int64_t)pg * kPage + (t & (kPage - 1))];
+      }
+    };
+    if (wk.valid()) look(page, old);
     uint32_t it = 0;
     int held_k = -1, held_rb = -1;
-    bool odd = false, fresh = true, late = false;      // odd: a row without a finite lse
-    float total = 0.f;
-    int page = -1, parts = 0;
+    bool odd = false, late = false;                    // odd: a row without a finite lse
     for (; wk.valid(); ++it) {
       const uint32_t g = it & 1;
-      const int rows = wk.rows(), row0 = wk.rb * R, t = wk.tile * kMassKeys + key, len = wk.s.len;
-      if (fresh) {
-        total = 0.f;
-        parts = 0;
-        page = t < len ? __ldcg(p.table + (int64_t)wk.s.b * p.max_pages + t / kPage) : -1;
-        if (t < len && (page < 0 || page >= p.num_pages)) {
-          set_err(p.dev_err, MLA_DEVERR_PAGE);
-          page = -1;
-        }
-      }
-      if (wk.k != held_k || wk.rb != held_rb) {
-        held_k = wk.k;
+      const int rows = wk.rows(), row0 = wk.rb * R, ctx = wk.s.len - wk.s.n, n = wk.s.n, t = wk.tile * kMassKeys + key;
+      const int tile = wk.tile, k = wk.k, blocks = wk.s.blocks;
+      const int64_t u0 = wk.s.unit0 + (int64_t)tile * wk.s.tile_cost;
+      if (k != held_k || wk.rb != held_rb) {
+        held_k = k;
         held_rb = wk.rb;
         const float v = key < rows ? __ldcg(p.lse + (int64_t)wk.s.q0 * p.H + row0 + key) * -1.4426950408889634f : 0.f;
         const bool fin = fabsf(v) < INFINITY;
@@ -380,6 +534,11 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
         s_lse[key] = fin ? v : -INFINITY;
         odd = vote_128(!fin);
       }
+      wk.next();
+      const bool done = !wk.valid() || wk.k != k || wk.tile != tile;             // the tile's last pass of this block
+      int next_page = -1;
+      float next_old = 0.f;
+      if (done && wk.valid()) look(next_page, next_old);
       // the four warps meet at barriers: they leave together
       late = !warp_wait(bars + 8 * (mS + g), (it >> 1) & 1, p.wait_ns, abort);
       if (late) *abort = 1;
@@ -389,12 +548,18 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
       }
       fence_after();
       // rows from `first` on see the key
-      const int pos = t - (len - wk.s.n), first = pos > 0 ? (pos >= wk.s.n ? rows : max(pos * p.H - row0, 0)) : 0;
+      const int pos = t - ctx, first = pos > 0 ? (pos >= n ? rows : max(pos * p.H - row0, 0)) : 0;
       const bool plain = !odd && __all_sync(0xffffffffu, first == 0);
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
       for (int c0 = 0; c0 < rows; c0 += 16) {
         uint32_t r[16];
-        tmem_load16(tbase + g * kMassMaxRows + c0 + tl, r);
+        tmem_load16(tbase + g * d_cols + c0 + tl, r);
+        if (2 * rows <= d_cols) {                      // the queries' low halves have columns of their own
+          uint32_t l[16];
+          tmem_load16(tbase + g * d_cols + rows + c0 + tl, l);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) + __uint_as_float(l[c]));
+        }
         if (plain) {
 #pragma unroll
           for (int c = 0; c < 16; ++c) sum[c & 3] += ex2(fmaf(__uint_as_float(r[c]), kMassUngain, s_lse[c0 + c]));
@@ -408,85 +573,98 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
         }
       }
       fence_before();
-      bar_arrive(bars + 8 * (mE + g));
+      warp_arrive(bars + 8 * (mE + g));
       total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       ++parts;
-      // the tile's last pass of this block?
-      const MassSeq seq = wk.s;
-      const int tile = wk.tile, k = wk.k;
-      wk.next();
-      fresh = !wk.valid() || wk.k != k || wk.tile != tile;
-      if (!fresh) continue;
-      if (parts == seq.blocks) {
-        if (page >= 0) mass_store(p, page, t, seq.counted, total);
-        continue;
-      }
-      // several blocks share the tile: its parts are added up, in the blocks'
-      // order, by whichever is the last to finish
-      const int64_t u0 = seq.unit0 + (int64_t)tile * seq.tile_cost;
-      const int x0 = mass_run_of(U, u0, G), x1 = mass_run_of(U, u0 + (int64_t)(seq.blocks - 1) * wk.cost, G);
-      __stcg(p.parts + (int64_t)(2 * x + (x == x0 ? 1 : 0)) * kMassKeys + key, total);
-      __threadfence();
-      asm volatile("bar.sync 1, 128;\n" ::: "memory");
-      if (key == 0) *s_last = atomicAdd(p.done + x0, parts) + parts == seq.blocks;
-      asm volatile("bar.sync 1, 128;\n" ::: "memory");
-      const bool last = *s_last != 0;
-      asm volatile("bar.sync 1, 128;\n" ::: "memory");
-      if (last) {
+      if (!done) continue;
+      bool mine = true;
+      if (parts < blocks) {
+        // several blocks share the tile: its parts are added up, in the blocks'
+        // order, by whichever is the last to finish
+        const int x0 = mass_run_of(U, u0, G), x1 = mass_run_of(U, u0 + (int64_t)(blocks - 1) * wk.cost, G);
+        __stcg(p.parts + (int64_t)(2 * x + (x == x0 ? 1 : 0)) * kMassKeys + key, total);
         __threadfence();
-        float sum_all = 0.f;
-        for (int y = x0; y <= x1; ++y) {
-          // a block whose run holds no pass of the tile has no part
-          const int64_t from = mass_run(U, y, G) - u0, to = mass_run(U, y + 1, G) - u0;
-          const int64_t r0 = from <= 0 ? 0 : (from + wk.cost - 1) / wk.cost;
-          if (r0 < seq.blocks && r0 * wk.cost < to) sum_all += __ldcg(p.parts + (int64_t)(2 * y + (y == x0 ? 1 : 0)) * kMassKeys + key);
+        asm volatile("bar.sync 1, 128;\n" ::: "memory");
+        if (key == 0) *s_last = atomicAdd(p.done + x0, parts) + parts == blocks;
+        asm volatile("bar.sync 1, 128;\n" ::: "memory");
+        mine = *s_last != 0;
+        asm volatile("bar.sync 1, 128;\n" ::: "memory");
+        if (mine) {
+          __threadfence();
+          total = 0.f;
+          for (int y = x0; y <= x1; ++y) {
+            // a block whose run holds no pass of the tile has no part
+            const int64_t from = mass_run(U, y, G) - u0, to = mass_run(U, y + 1, G) - u0;
+            const int64_t r0 = from <= 0 ? 0 : (from + wk.cost - 1) / wk.cost;
+            if (r0 < blocks && r0 * wk.cost < to) total += __ldcg(p.parts + (int64_t)(2 * y + (y == x0 ? 1 : 0)) * kMassKeys + key);
+          }
         }
-        if (page >= 0) mass_store(p, page, t, seq.counted, sum_all);
       }
+      if (mine && page >= 0) p.mass[(int64_t)page * kPage + (t & (kPage - 1))] = fmaf(old, p.decay, total);
+      page = next_page;
+      old = next_old;
+      total = 0.f;
+      parts = 0;
     }
     if (late) set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
   } else if (work && warp == kMassMma) {
-    // ---- one thread issues the MMAs
+    // ---- the MMAs.  The warp runs converged, one lane issues: loop counters and
+    // descriptors then live in uniform registers.
     MassWalk wk;
-    wk.open(p);
-    wk.start(lo, hi);
-    if (elect_one()) {
-      const uint64_t d_q = sw128_desc(sb, 16, 1024);
-      uint32_t it = 0, piece = 0, q = 0;               // passes, pieces, query pieces
-      int held_k = -1, held_rb = -1;
-      for (; ok && wk.valid(); wk.next(), ++it) {
-        const uint32_t g = it & 1, d = tbase + g * kMassMaxRows, id = f16_idesc(128, wk.rows(), false, false);
-        const bool held = resident && wk.k == held_k && wk.rb == held_rb;
+    wk.open(p, U, lo, hi);
+    const bool leader = elect_one();
+    const uint64_t d_q = sw128_desc(sb, 16, 1024);
+    uint32_t it = 0, q_round = 0, id = 0, id_minus = 0, id_both = 0, lo_step = 0;
+    int qs = 0, slot = 0, round = 0, held_k = -1, held_rb = -1;
+    bool both = false;
+    while (ok && wk.valid()) {
+      const uint32_t g = it & 1, d = tbase + g * d_cols;
+      const bool held = resident && wk.k == held_k && wk.rb == held_rb;
+      if (wk.k != held_k || wk.rb != held_rb) {
         held_k = wk.k;
         held_rb = wk.rb;
-        // the scores of two passes before have been read
-        if (it >= 2 && !bar_wait(bars + 8 * (mE + g), ((it - 2) >> 1) & 1, p.wait_ns, abort)) {
-          ok = false;
-          break;
-        }
-        if (held) q -= 9;
-        else if (resident && it > 0) umma_commit(bars + 8 * mQDone);       // the old queries' last reader
-        for (uint32_t kb = 0; kb < 9; ++kb, ++piece, ++q) {
-          const uint32_t slot = piece % NA, qs = q % QS;
-          if (!held && !bar_wait(bars + 8 * (mQ + qs), (q / QS) & 1, p.wait_ns, abort)) {
-            ok = false;
-            break;
-          }
-          if (!bar_wait(bars + 8 * (mA + slot), (piece / NA) & 1, p.wait_ns, abort)) {
-            ok = false;
-            break;
-          }
-          fence_after();
-          const uint32_t a = t_a + slot * COLS;
-          const uint64_t b_hi = d_q + (uint64_t)(qs * R * 256 >> 4), b_lo = b_hi + (uint64_t)(R * 128 >> 4);
-          umma4_ta<2>(d, a, b_hi, id, kb != 0);
-          umma4_ta<2>(d, a, b_lo, id, 1u);
-          if (kb < 8 ? LF != MLA_FMT_BF16 : KF != MLA_FMT_BF16) umma4_ta<2>(d, a + 32, b_hi, id, 1u);
-          umma_commit(bars + 8 * (mAFree + slot));
-          if (!resident) umma_commit(bars + 8 * (mQFree + qs));
-        }
-        if (ok) umma_commit(bars + 8 * (mS + g));
+        // Where the buffer has the columns, both halves of the queries are one N
+        // of twice the rows: an MMA with A in TMEM costs 32 cycles up to N = 64.
+        const int rows = wk.rows();
+        both = 2 * rows <= d_cols;
+        id = f16_idesc(128, rows, false, false);
+        id_minus = id | kNegateA;
+        id_both = (both ? f16_idesc(128, 2 * rows, false, false) : id) | kNegateA;
+        lo_step = rows * 128 >> 4;
+        if (resident && it > 0 && leader) umma_commit(bars + 8 * mQDone);          // the old queries' last reader
       }
+      wk.next();
+      // the scores of two passes before have been read
+      if (it >= 2 && !(ok = warp_wait(bars + 8 * (mE + g), ((it - 2) >> 1) & 1, p.wait_ns, abort))) break;
+      for (int kb = 0; kb < 9;) {
+        if (!(ok = warp_wait(bars + 8 * (mA + slot), round & 1, p.wait_ns, abort))) break;
+        uint32_t a = t_a + slot * cols;
+        for (const int end = kb + PU / 2; kb < end; ++kb, a += 32) {
+          if (!held && !(ok = warp_wait(bars + 8 * (mQ + qs), q_round & 1, p.wait_ns, abort))) break;
+          fence_after();
+          const uint64_t b_hi = d_q + (uint32_t)(qs * R * 16);
+          if (leader) {
+            umma4_ta<2>(d, a, b_hi, id_both, kb != 0);
+            if (!both) umma4_ta<2>(d, a, b_hi + lo_step, id_minus, 1u);
+            if (kb < 8 ? LF != MLA_FMT_BF16 : KF != MLA_FMT_BF16) umma4_ta<2>(d, a + 16 * PU, b_hi, id, 1u);
+            if (!resident) umma_commit(bars + 8 * (mQFree + qs));
+          }
+          if (++qs == QS) {
+            qs = 0;
+            if (!held) ++q_round;
+          }
+        }
+        if (!ok) break;
+        if (leader) umma_commit(bars + 8 * (mAFree + slot));
+        if (++slot == NA) {
+          slot = 0;
+          ++round;
+        }
+      }
+      if (ok && leader) umma_commit(bars + 8 * (mS + g));
+      ++it;
+    }
+    if (leader) {
       if (!ok) {
         set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
         *abort = 1;
@@ -498,11 +676,11 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
   } else if (work && warp == kMassRaw) {
     // ---- the cache's blocks, a pass ahead with the page ids
     MassWalk wk;
-    wk.open(p);
-    wk.start(lo, hi);
-    auto pages = [&]() {                               // lane i < 4: the page of block i of the walk's tile, -1: nothing to load
-      const int t = wk.tile * kMassKeys + 32 * (lane & 3);
-      return wk.valid() && lane < 4 && t < wk.s.len ? __ldcg(p.table + (int64_t)wk.s.b * p.max_pages + t / kPage) : -1;
+    wk.open(p, U, lo, hi);
+    constexpr int C = SH::kTileCopies;
+    auto pages = [&]() {                               // lane i < C: the page of copy i of the walk's tile, -1: nothing to load
+      const int t = wk.tile * kMassKeys + kMassKeys / C * (lane & (C - 1));
+      return wk.valid() && lane < C && t < wk.s.len ? __ldcg(p.table + (int64_t)wk.s.b * p.max_pages + t / kPage) : -1;
     };
     uint32_t blk = 0;
     int ids = pages();
@@ -510,7 +688,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
       const int mine = ids >= 0 && ids < p.num_pages ? ids : -1;
       wk.next();
       ids = pages();
-      for (int i = 0; i < 4; ++i, ++blk) {
+      for (int i = 0; i < C; ++i, ++blk) {
         const uint32_t slot = blk % NS;
         if (blk >= (uint32_t)NS && !warp_wait(bars + 8 * (mRawFree + slot), ((blk / NS) - 1) & 1, p.wait_ns, abort)) {
           ok = false;
@@ -519,9 +697,9 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
         const int page = __shfl_sync(0xffffffffu, mine, i);
         if (lane == 0) {
           if (page >= 0) {
-            bar_expect(bars + 8 * (mRaw + slot), SH::kBlock);
-            bulk_copy(sb + s_raw + slot * SH::kBlock, p.pool + (int64_t)page * p.L.page_bytes + (i & 1) * p.L.block_bytes,
-                      SH::kBlock, bars + 8 * (mRaw + slot));
+            bar_expect(bars + 8 * (mRaw + slot), SH::kCopy);
+            bulk_copy(sb + s_raw + slot * SH::kCopy, p.pool + (int64_t)page * p.L.page_bytes + (C == 4 ? (i & 1) * SH::kBlock : 0),
+                      SH::kCopy, bars + 8 * (mRaw + slot));
           } else {
             bar_arrive(bars + 8 * (mRaw + slot));      // the lanes' keys are not read: whatever lies there will do
           }
@@ -539,8 +717,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
   } else if (work && warp == kMassQ) {
     // ---- the queries: pieces of 64 channels of the row block, high halves then low ones
     MassWalk wk;
-    wk.open(p);
-    wk.start(lo, hi);
+    wk.open(p, U, lo, hi);
     if (elect_one()) {
       uint32_t q = 0;
       int held_k = -1, held_rb = -1;
@@ -567,7 +744,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
           const uint32_t dst = sb + qs * R * 256;
           bar_expect(bars + 8 * (mQ + qs), rows * 256);
           bulk_copy(dst, src, rows * 128, bars + 8 * (mQ + qs));
-          bulk_copy(dst + R * 128, src + (int64_t)9 * p.rows * 128, rows * 128, bars + 8 * (mQ + qs));
+          bulk_copy(dst + rows * 128, src + (int64_t)9 * p.rows * 128, rows * 128, bars + 8 * (mQ + qs));
         }
       }
       if (!ok) {
@@ -593,7 +770,7 @@ mla_status launch_mass_fmt(const MassParams& p0, cudaStream_t stream) {
   MassParams p = p0;
   p.query_pieces = SH::query_pieces(p.R);
   p.raw_slots = SH::raw_slots(p.R);
-  const int smem = p.query_pieces * p.R * 256 + p.raw_slots * SH::kBlock + kMassMisc + kMassAligned;
+  const int smem = p.query_pieces * p.R * 256 + p.raw_slots * SH::kCopy + kMassMisc + kMassAligned;
   static int configured[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);

@@ -69,11 +69,6 @@ struct MassParams {
   uint8_t* q_tiles;       // [hi, lo][9][rows][64] fp16, swizzled
 };
 
-__device__ __forceinline__ void mass_store(const MassParams& p, int page, int t, int counted, float w) {
-  float* m = p.mass + (int64_t)page * kPage + (t & (kPage - 1));
-  *m = t < counted ? fmaf(*m, p.decay, w) : w;
-}
-
 // The kernel over the key tiles, by latent format (one translation unit each);
 // MLA_ERR_UNSUPPORTED for another unit's formats.
 mla_status launch_mass_bf16(const MassParams& p, int lf, int kf, cudaStream_t stream);
