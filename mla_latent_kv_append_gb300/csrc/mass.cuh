@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
       fence_after();
       // rows from `first` on see the key
       const int pos = t - ctx, first = pos > 0 ? (pos >= n ? rows : max(pos * p.H - row0, 0)) : 0;
-      const bool plain = !odd && __all_sync(0xffffffffu, first == 0);
+      const bool plain = __all_sync(0xffffffffu, first == 0 && !odd);
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
       for (int c0 = 0; c0 < rows; c0 += 16) {
         uint32_t r[16];

@@ -20,6 +20,7 @@ struct MoveParams {
   uint8_t* pool;
   PageLayout L;
   int num_pages, kpe_fmt, groups, out_groups;          // scale groups; protected channels (0: none)
+  int chunk_shift, kchunk_shift;                       // a row's 16-byte chunks: 1 << shift
   const int32_t* src_table;
   const int32_t* dst_table;
   int max_pages;
@@ -27,6 +28,11 @@ struct MoveParams {
   int max_keep;
   float* mass;
   int32_t* dev_err;
+};
+
+template <int N>
+struct Count {
+  static constexpr int value = N;
 };
 
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) {
@@ -73,38 +79,56 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) 
     s_u[lane] = u;
   }
   __syncthreads();
-  const int chunks = (int)p.L.codes_row / 16, kchunks = (int)p.L.kpe_row / 16;
-  for (int i = tid; i < count * chunks; i += kMoveThreads) {
-    const int v = i / chunks, c = i - v * chunks;
-    const uint8_t* src = s_src[v];
-    if (!src) continue;
-    const uint4 x = __ldcg(reinterpret_cast<const uint4*>(src + p.L.codes_off + s_u[v] * p.L.codes_row) + latent_chunk_pos(c, s_u[v]));
-    *(reinterpret_cast<uint4*>(dst + p.L.codes_off + v * p.L.codes_row) + latent_chunk_pos(c, v)) = x;
-  }
-  for (int i = tid; i < count * kchunks; i += kMoveThreads) {
-    const int v = i / kchunks, c = i - v * kchunks;
-    const uint8_t* src = s_src[v];
-    if (!src) continue;
-    const uint4 x =
-        __ldcg(reinterpret_cast<const uint4*>(src + p.L.kpe_off + s_u[v] * p.L.kpe_row) + kpe_chunk_pos(c, s_u[v], p.kpe_fmt));
-    *(reinterpret_cast<uint4*>(dst + p.L.kpe_off + v * p.L.kpe_row) + kpe_chunk_pos(c, v, p.kpe_fmt)) = x;
-  }
-  const uint8_t* src = s_src[lane];
-  if (!src) return;
-  const int u = s_u[lane];
-  auto words = [&](int64_t off, int groups) {
-    if (off < 0) return;
-    for (int g = warp; g < groups; g += kMoveWarps)
-      reinterpret_cast<uint32_t*>(dst + off)[g * kBlockTokens + lane] =
-          __ldcg(reinterpret_cast<const uint32_t*>(src + off) + g * kBlockTokens + u);
+  // Everything of a thread is loaded before anything is stored: one round of
+  // memory latency a block.  Codes: 16-byte chunks of the rows; a row has a power
+  // of two of them.
+  const int shift = p.chunk_shift, kshift = p.kchunk_shift;
+  auto rows = [&](auto batch, int64_t off, int64_t pitch, int sh, auto pos) {
+    constexpr int N = decltype(batch)::value;
+    for (int i0 = tid; i0 < count << sh; i0 += N * kMoveThreads) {
+      uint4 x[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int i = i0 + n * kMoveThreads, v = min(i >> sh, kBlockTokens - 1), c = i & ((1 << sh) - 1);
+        const uint8_t* src = i < count << sh ? s_src[v] : nullptr;
+        if (src) x[n] = __ldcg(reinterpret_cast<const uint4*>(src + off + s_u[v] * pitch) + pos(c, s_u[v]));
+      }
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int i = i0 + n * kMoveThreads, v = min(i >> sh, kBlockTokens - 1), c = i & ((1 << sh) - 1);
+        if (i < count << sh && s_src[v]) *(reinterpret_cast<uint4*>(dst + off + v * pitch) + pos(c, v)) = x[n];
+      }
+    }
   };
-  words(p.L.scale_off, p.groups);
-  words(p.L.zero_off, kNLG);
-  words(p.L.kpe_scale_off, kNKG);
-  words(p.L.bound_off, 1);
-  for (int g = warp; g < p.out_groups; g += kMoveWarps)
-    reinterpret_cast<uint16_t*>(dst + p.L.outlier_off)[g * kBlockTokens + lane] =
-        __ldcg(reinterpret_cast<const uint16_t*>(src + p.L.outlier_off) + g * kBlockTokens + u);
+  const uint8_t* src = s_src[lane];
+  const int u = s_u[lane];
+  // words of a field [groups][32 tokens], lane = token
+  auto words = [&](auto batch, int64_t off, int groups) {
+    constexpr int N = decltype(batch)::value;
+    if (off < 0 || !src) return;
+    for (int g0 = warp; g0 < groups; g0 += N * kMoveWarps) {
+      uint32_t x[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        if (g0 + n * kMoveWarps < groups)
+          x[n] = __ldcg(reinterpret_cast<const uint32_t*>(src + off) + (g0 + n * kMoveWarps) * kBlockTokens + u);
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        if (g0 + n * kMoveWarps < groups)
+          reinterpret_cast<uint32_t*>(dst + off)[(g0 + n * kMoveWarps) * kBlockTokens + lane] = x[n];
+    }
+  };
+  rows(Count<4>(), p.L.codes_off, p.L.codes_row, shift, [](int c, int t) { return latent_chunk_pos(c, t); });
+  words(Count<4>(), p.L.scale_off, p.groups);
+  words(Count<4>(), p.L.zero_off, kNLG);
+  rows(Count<1>(), p.L.kpe_off, p.L.kpe_row, kshift, [&](int c, int t) { return kpe_chunk_pos(c, t, p.kpe_fmt); });
+  words(Count<1>(), p.L.kpe_scale_off, kNKG);
+  words(Count<1>(), p.L.bound_off, 1);
+  if (src) {
+    for (int g = warp; g < p.out_groups; g += kMoveWarps)
+      reinterpret_cast<uint16_t*>(dst + p.L.outlier_off)[g * kBlockTokens + lane] =
+          __ldcg(reinterpret_cast<const uint16_t*>(src + p.L.outlier_off) + g * kBlockTokens + u);
+  }
 }
 
 bool ok4(const void* p) { return p && ((uintptr_t)p & 3) == 0; }
@@ -131,6 +155,13 @@ extern "C" mla_status mla_move_tokens(const mla_cache_layer* cache, const int32_
   p.kpe_fmt = cache->kpe_fmt;
   p.groups = kDc / latent_group_size(cache->latent_fmt);
   p.out_groups = cache->latent_fmt == MLA_FMT_INT8_OUTLIER ? kNOut : 0;
+  auto log2_chunks = [](int64_t row) {
+    int n = 0;
+    while ((16 << n) < row) ++n;
+    return n;
+  };
+  p.chunk_shift = log2_chunks(p.L.codes_row);
+  p.kchunk_shift = log2_chunks(p.L.kpe_row);
   p.src_table = src_table;
   p.dst_table = dst_table;
   p.max_pages = max_pages;

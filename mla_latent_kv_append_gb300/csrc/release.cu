@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(T) release_kernel(const ReleaseParams p, int p
       const int kept = take_b >= 0 ? 0 : now_b;        // columns below keep their pages, those given back begin here
       const int32_t* in = p.table + b * p.max_pages;
       int32_t* out = p.out + b * p.max_pages;
-      for (int64_t c0 = 32 * part + lane; c0 < p.max_pages; c0 += 32 * split * kRelAhead) {
+      const int end = part_of & kTables ? p.max_pages : (back_b >= 0 ? was_b : 0);
+      for (int64_t c0 = 32 * part + lane; c0 < end; c0 += 32 * split * kRelAhead) {
         int id[kRelAhead], fresh[kRelAhead];
 #pragma unroll
         for (int e = 0; e < kRelAhead; ++e) {
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(T) release_kernel(const ReleaseParams p, int p
 #pragma unroll
         for (int e = 0; e < kRelAhead; ++e) {
           const int64_t pg = c0 + 32 * split * e;
-          if (pg >= p.max_pages) continue;
+          if (pg >= end) continue;
           if (pg < was_b && (id[e] < 0 || id[e] >= p.num_pages)) {
             set_err(p.dev_err, MLA_DEVERR_PAGE);
             id[e] = -1;

@@ -7,11 +7,11 @@
 // three counting passes of 11, 11 and 10 bits fix a threshold and how many of its
 // equals stay, and one more lists the tokens in increasing order.
 //
-// What bounds it: latency.  A cluster of up to 8 blocks takes a sequence; each
-// holds its part of the weights in shared memory (read once, through the block
-// table), the blocks' counts meet in distributed shared memory.  Many tokens
-// have equal weights (never looked at: 0), so a warp adds equal digits up
-// before it counts them.
+// What bounds it: latency.  A cluster of up to 8 blocks takes a sequence; up to
+// 262144 tokens a block's threads hold its weights in registers (8, 16 or 32 each,
+// all of a thread's loads in flight at once), beyond that in shared memory.  The
+// blocks' counts meet in distributed shared memory.  Many tokens have equal
+// weights (never looked at: 0), so a warp adds those up before it counts them.
 #include <cooperative_groups.h>
 
 #include "mla_internal.cuh"
@@ -24,9 +24,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
-constexpr int kSelKeys = 49152;                        // weights that a block holds; those behind are read again
+constexpr int kSelKeys = 32768;                        // weights that a block holds in shared memory; those behind are read again
 constexpr int kSelMaxPages = 1 << 24;                  // 2^30 tokens: a block's strides past the end stay in 31 bits
-constexpr int kSelPart = 32768;                        // tokens per block where the cluster can be larger
 
 struct SelectParams {
   const float* mass;
@@ -48,10 +47,19 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 
 struct Exchange {
-  uint32_t bins[kSelBins];
+  uint32_t bins[3][kSelBins];                          // of each pass
   int32_t above, equal;                                // of this block's part, against the threshold
 };
+// The first pass's digits are a float's exponent and two bits: most weights fall
+// into a few dozen bins, and additions to one word come one after the other.  So
+// that pass counts in kSelCopies copies, by lane (32768 weights in one block: 16 us
+// of that pass with one copy).
+constexpr int kSelCopies = 8, kSelPitch = kSelBins + 4;
 
+// One thread's weights: HELD of them in registers, or the block's part in shared
+// memory and behind it in global memory (HELD = 0).  Token t_i of thread (w, lane)
+// is first + 32 i + lane, first = the warp's run.
+template <int HELD>
 __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectParams p, int CL) {
   extern __shared__ uint32_t s_keys[];
   __shared__ Exchange ex;
@@ -61,6 +69,9 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), b = blockIdx.x / CL;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t* copies = s_keys + p.keys;
+  for (int i = tid; i < 3 * kSelBins; i += kSelThreads) (&ex.bins[0][0])[i] = 0u;
+  for (int i = tid; i < kSelCopies * kSelPitch; i += kSelThreads) copies[i] = 0u;
   pdl_launch_dependents();
   pdl_wait();
   int L = __ldcg(p.seq_lens + b);
@@ -75,7 +86,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
   }
   if (err || K >= L || K == 0) {                       // the whole cluster alike
     const int n = !err && K == 0 ? 0 : L;
-    for (int i = rank * kSelThreads + tid; i < p.max_keep; i += CL * kSelThreads) kept[i] = i < n ? i : -1;
+    for (int64_t i = (int64_t)rank * kSelThreads + tid; i < p.max_keep; i += CL * kSelThreads) kept[i] = i < n ? (int)i : -1;
     if (rank == 0 && tid == 0) {
       p.kept_lens[b] = n;
       if (err) set_err(p.dev_err, err);
@@ -83,115 +94,187 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
     return;
   }
   const int sinks = min(p.sinks, K), recent = min(p.recent, K - sinks), want = K - sinks - recent;
-  // this block's tokens: whole pages
+  // this block's tokens: whole pages; a warp's: a run of them, so that order
+  // needs one exchange of counts
   const int pages = (L + kPage - 1) / kPage, per = (pages + CL - 1) / CL * kPage;
   const int t0 = min(rank * per, L), t1 = min(t0 + per, L);
   const int m0 = max(t0, sinks), m1 = min(t1, L - recent);           // those that compete
+  const int run = (t1 - t0 + kSelThreads - 1) / kSelThreads, w0 = min(t0 + warp * run * 32, t1), w1 = min(w0 + run * 32, t1);
   const int32_t* table = p.table + (int64_t)b * p.max_pages;
-  auto fetch = [&](int t) {
-    const int page = __ldcg(table + t / kPage);
+  auto weight = [&](int page, int t) {
     return page >= 0 && page < p.num_pages ? order_key(__ldcg(p.mass + (int64_t)page * kPage + t % kPage)) : 0u;
   };
-  for (int t = t0 + tid; t < t1; t += kSelThreads) {
-    if (t - t0 < p.keys) s_keys[t - t0] = fetch(t);
-    if (t % kPage == 0) {
+  uint32_t held[HELD ? HELD : 1];
+  if constexpr (HELD > 0) {
+    // lane i: the page of the run's i-th 32 tokens
+    const int mine = w0 + 32 * lane < w1 ? __ldcg(table + (w0 + 32 * lane) / kPage) : 0;
+    if (mine < 0 || mine >= p.num_pages) set_err(p.dev_err, MLA_DEVERR_PAGE);
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      const int t = w0 + 32 * i + lane, page = __shfl_sync(0xffffffffu, mine, i);
+      held[i] = t < w1 ? weight(page, t) : 0u;
+    }
+  } else {
+    for (int t = t0 + tid; t < t1; t += kSelThreads) {
       const int page = __ldcg(table + t / kPage);
       if (page < 0 || page >= p.num_pages) set_err(p.dev_err, MLA_DEVERR_PAGE);
+      if (t - t0 < p.keys) s_keys[t - t0] = weight(page, t);
+    }
+    __syncthreads();
+  }
+  // f(token, its key) for all of the run, 32 tokens at a time, every lane
+  auto each = [&](auto f) {
+    if constexpr (HELD > 0) {
+#pragma unroll
+      for (int i = 0; i < HELD; ++i)
+        if (w0 + 32 * i < w1) f(w0 + 32 * i + lane, held[i]);
+    } else {
+      for (int base = w0; base < w1; base += 32) {
+        const int t = base + lane;
+        f(t, t >= w1 ? 0u : (t - t0 < p.keys ? s_keys[t - t0] : weight(__ldcg(table + t / kPage), t)));
+      }
+    }
+  };
+
+  // bit i: the thread's i-th token competes
+  uint32_t competes = 0u;
+  if constexpr (HELD > 0) {
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      const int t = w0 + 32 * i + lane;
+      if (t >= m0 && t < min(m1, w1)) competes |= 1u << i;
     }
   }
-  auto key = [&](int t) { return t - t0 < p.keys ? s_keys[t - t0] : fetch(t); };
-
   uint32_t prefix = 0u, mask = 0u;
   int need = want;                                     // how many stay among the keys that share the prefix
   for (int pass = 0; pass < 3 && want > 0; ++pass) {
-    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-    const uint32_t digits = (1u << bits) - 1u;
-    for (int i = tid; i < kSelBins; i += kSelThreads) ex.bins[i] = 0u;
-    __syncthreads();
-    for (int base = m0 + warp * 32; base < m1; base += kSelThreads) {
-      const int t = base + lane;
-      const uint32_t k = t < m1 ? key(t) : 0u;
-      const bool in = t < m1 && (k & mask) == prefix;
-      const uint32_t d = (k >> shift) & digits;
-      const uint32_t peers = __match_any_sync(0xffffffffu, in ? d : 0xFFFFFFFFu);
-      if (in && lane == __ffs(peers) - 1) atomicAdd(&ex.bins[d], (uint32_t)__popc(peers));
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+    const uint32_t digits = pass == 2 ? 1023u : 2047u;
+    if (pass == 0) __syncthreads();                    // the bins are clear
+    uint32_t* bins = pass == 0 ? copies + (lane % kSelCopies) * kSelPitch : ex.bins[pass];
+    // equal keys count as one: those equal to the warp's first
+    auto count = [&](bool in, uint32_t k) {
+      const uint32_t some = __ballot_sync(0xffffffffu, in);
+      if (!some) return;
+      const int first = __ffs(some) - 1;
+      const uint32_t common = __shfl_sync(0xffffffffu, k, first);    // every lane takes part
+      const uint32_t peers = __ballot_sync(0xffffffffu, in && k == common);
+      if (in && (k != common || lane == first)) atomicAdd(bins + ((k >> shift) & digits), k == common ? (uint32_t)__popc(peers) : 1u);
+    };
+    if constexpr (HELD > 0) {
+#pragma unroll
+      for (int i = 0; i < HELD; ++i)
+        if (w0 + 32 * i < w1) count((competes >> i & 1u) && (held[i] & mask) == prefix, held[i]);
+    } else {
+      each([&](int t, uint32_t k) { count(t >= m0 && t < min(m1, w1) && (k & mask) == prefix, k); });
+    }
+    if (pass == 0) {
+      __syncthreads();
+      for (int i = tid; i < kSelBins; i += kSelThreads) {
+        uint32_t n = 0;
+#pragma unroll
+        for (int c = 0; c < kSelCopies; ++c) n += copies[c * kSelPitch + i];
+        ex.bins[0][i] = n;
+      }
     }
     cluster.sync();
     // thread i has bins 2046 - 2 i and the next: from the largest digit down
     const int top = kSelBins - 2 - 2 * tid;
-    int hi = 0, lo = 0;
+    int high = 0, low = 0;
+#pragma unroll 8
     for (int r = 0; r < CL; ++r) {
-      const uint2 v = *reinterpret_cast<const uint2*>(&cluster.map_shared_rank(&ex, r)->bins[top]);
-      lo += v.x;
-      hi += v.y;
+      const uint2 v = *reinterpret_cast<const uint2*>(&cluster.map_shared_rank(&ex, r)->bins[pass][top]);
+      low += v.x;
+      high += v.y;
     }
     int total;
-    const int above = block_scan<kSelThreads>(hi + lo, red, &total);
-    if (above < need && need <= above + hi) {
+    const int above = block_scan<kSelThreads>(high + low, red, &total);
+    if (above < need && need <= above + high) {
       s_digit = top + 1;
       s_need = need - above;
-    } else if (above + hi < need && need <= above + hi + lo) {
+    } else if (above + high < need && need <= above + high + low) {
       s_digit = top;
-      s_need = need - above - hi;
+      s_need = need - above - high;
     }
     __syncthreads();
     need = s_need;
     prefix |= (uint32_t)s_digit << shift;
     mask |= digits << shift;
-    cluster.sync();                                    // the counts have been read
+    __syncthreads();                                   // both have been read
   }
 
-  // Which tokens stay: a warp takes a run of the part, so that order needs one
-  // exchange of counts
-  const int run = ((t1 - t0 + kSelThreads - 1) / kSelThreads) * 32, w0 = t0 + warp * run, w1 = min(w0 + run, t1);
-  auto classes = [&](int t, bool& more, bool& same) {
+  // Which tokens stay
+  auto classes = [&](int t, uint32_t k, bool& more, bool& same) {
     const bool competes = t >= m0 && t < m1 && want > 0;
-    const uint32_t k = competes ? key(t) : 0u;
     more = t < w1 && (competes ? k > prefix : (t < sinks || t >= L - recent));
     same = competes && t < w1 && k == prefix;
   };
   int n_more = 0, n_same = 0;
-  for (int base = w0; base < w1; base += 32) {
-    bool more, same;
-    classes(base + lane, more, same);
-    n_more += __popc(__ballot_sync(0xffffffffu, more));
-    n_same += __popc(__ballot_sync(0xffffffffu, same));
+  uint32_t mores = 0u, sames = 0u;                     // bit i: the thread's i-th token
+  if constexpr (HELD > 0) {
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      bool more, same;
+      classes(w0 + 32 * i + lane, held[i], more, same);
+      mores |= more ? 1u << i : 0u;
+      sames |= same ? 1u << i : 0u;
+    }
+    n_more = __reduce_add_sync(0xffffffffu, __popc(mores));
+    n_same = __reduce_add_sync(0xffffffffu, __popc(sames));
+  } else {
+    each([&](int t, uint32_t k) {
+      bool more, same;
+      classes(t, k, more, same);
+      n_more += __popc(__ballot_sync(0xffffffffu, more));
+      n_same += __popc(__ballot_sync(0xffffffffu, same));
+    });
   }
   if (lane == 0) {
     s_above[warp] = n_more;
     s_equal[warp] = n_same;
   }
   __syncthreads();
-  if (tid == 0) {
-    int a = 0, e = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      const int x = s_above[w], y = s_equal[w];
-      s_above[w] = a;
-      s_equal[w] = e;
+  // every warp: the sums over the warps before it, and the block's
+  int a = s_above[lane], e = s_equal[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, e, o);
+    if (lane >= o) {
       a += x;
       e += y;
     }
+  }
+  if (tid == kSelWarps - 1) {
     ex.above = a;
     ex.equal = e;
   }
+  int before_more = __shfl_sync(0xffffffffu, a, warp) - n_more, before_same = __shfl_sync(0xffffffffu, e, warp) - n_same;
   cluster.sync();
-  int before_more = s_above[warp], before_same = s_equal[warp];
-  for (int r = 0; r < rank; ++r) {
-    before_more += cluster.map_shared_rank(&ex, r)->above;
-    before_same += cluster.map_shared_rank(&ex, r)->equal;
+  if (CL > 1) {
+    const int va = lane < rank ? cluster.map_shared_rank(&ex, lane)->above : 0, ve = lane < rank ? cluster.map_shared_rank(&ex, lane)->equal : 0;
+    before_more += __reduce_add_sync(0xffffffffu, va);
+    before_same += __reduce_add_sync(0xffffffffu, ve);
   }
-  for (int base = w0; base < w1; base += 32) {
-    bool more, same;
-    const int t = base + lane;
-    classes(t, more, same);
+  auto list = [&](int t, bool more, bool same) {
     const uint32_t bm = __ballot_sync(0xffffffffu, more), bs = __ballot_sync(0xffffffffu, same);
+    if (!(bm | bs)) return;
     const uint32_t below = (1u << lane) - 1u;
     const int ties = before_same + __popc(bs & below);               // equals before this one
     if (more || (same && ties < need)) kept[before_more + __popc(bm & below) + min(ties, need)] = t;
     before_more += __popc(bm);
     before_same += __popc(bs);
+  };
+  if constexpr (HELD > 0) {
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) list(w0 + 32 * i + lane, mores >> i & 1u, sames >> i & 1u);
+  } else {
+    each([&](int t, uint32_t k) {
+      bool more, same;
+      classes(t, k, more, same);
+      list(t, more, same);
+    });
   }
-  for (int i = K + rank * kSelThreads + tid; i < p.max_keep; i += CL * kSelThreads) kept[i] = -1;
+  for (int64_t i = K + (int64_t)rank * kSelThreads + tid; i < p.max_keep; i += CL * kSelThreads) kept[i] = -1;
   if (rank == 0 && tid == 0) p.kept_lens[b] = K;
   cluster.sync();                                      // no block leaves while its counts may be read
 }
@@ -227,21 +310,38 @@ extern "C" mla_status mla_select_tokens(const float* mass, int32_t num_pages, co
   p.kept = kept;
   p.kept_lens = kept_lens;
   p.max_keep = max_keep;
+  p.keys = 0;
   p.dev_err = dev_err;
-  int CL = 1;
+  // The more tokens a thread holds, the fewer blocks a sequence needs: as few
+  // tokens as let all sequences run side by side, one block to an SM.
   const int64_t tokens = (int64_t)max_pages * kPage;
-  while (CL < 8 && tokens > (int64_t)CL * kSelPart) CL *= 2;
-  const int64_t part = ((max_pages + CL - 1) / CL) * (int64_t)kPage;
-  p.keys = (int)(part < kSelKeys ? part : kSelKeys);
-  const int smem = p.keys * 4;
-  static int configured[64] = {0};
+  const int sms = device_sm_count();
+  int CL = 0;
+  void (*kernel)(const SelectParams, int) = nullptr;
+  int smem = 0;
+  for (int held = 8; held <= 32; held *= 2) {
+    CL = 1;
+    while (CL < 8 && tokens > (int64_t)CL * kSelThreads * held) CL *= 2;
+    if (tokens > (int64_t)CL * kSelThreads * held) continue;
+    kernel = held == 8 ? select_kernel<8> : (held == 16 ? select_kernel<16> : select_kernel<32>);
+    if (batch * CL <= sms) break;
+  }
+  if (!kernel) {
+    kernel = select_kernel<0>;
+    const int64_t part = ((max_pages + CL - 1) / CL) * (int64_t)kPage;
+    p.keys = (int)(part < kSelKeys ? part : kSelKeys);
+    smem = p.keys * 4;
+  }
+  smem += kSelCopies * kSelPitch * 4;
+  const int which = kernel == select_kernel<0> ? 0 : (kernel == select_kernel<8> ? 1 : (kernel == select_kernel<16> ? 2 : 3));
+  static int configured[4][64] = {{0}};
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !configured[dev]) {
-    const mla_status st =
-        cuda_status(cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4));
+  if (dev < 0 || dev >= 64 || !configured[which][dev]) {
+    const mla_status st = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                           (which ? 0 : kSelKeys * 4) + kSelCopies * kSelPitch * 4));
     if (st != MLA_OK) return st;
-    if (dev >= 0 && dev < 64) configured[dev] = 1;
+    if (dev >= 0 && dev < 64) configured[which][dev] = 1;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(batch * CL);
@@ -256,5 +356,5 @@ extern "C" mla_status mla_select_tokens(const float* mass, int32_t num_pages, co
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cuda_status(cudaLaunchKernelEx(&cfg, select_kernel, p, CL));
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, p, CL));
 }

@@ -14,9 +14,9 @@
 // What bounds it: reading row j of p and q once (a megabyte for 131072 fp32
 // probabilities); one sequence is latency.  A cluster of blocks shares a
 // sequence, so that a few sequences spread over many SMs.  A warp sums tiles of
-// 1024 values: w and its rounding error by Dekker's difference (c(p) > c(q) >=
-// 0), the sum by a two-sum, 13 fp32 operations a value (an fp64 addition costs
-// 64 times an fp32 one here: 33.5 million of them 55 us).  The tiles' sums
+// 1024 values: w and its rounding error by Dekker's difference (c(p) >= min(c(p),
+// c(q)) >= 0), the sum by a two-sum, 14 fp32 operations a value (an fp64 addition
+// costs 64 times an fp32 one here: 33.5 million of them 55 us).  The tiles' sums
 // meet in distributed shared memory; one warp then reads the tile that holds the
 // border again, in fp64.
 #include <cooperative_groups.h>
@@ -73,6 +73,13 @@ __device__ __forceinline__ void load_row(const T* row, int e, int vocab, float* 
   }
 }
 
+template <typename T, int N>
+__device__ __forceinline__ void widen(const uint4& raw, float* v) {      // NaN and what is below 0: 0
+  const T* x = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = fmaxf(to_f(x[i]), 0.f);
+}
+
 // (h, l) += w exactly up to l's rounding.
 __device__ __forceinline__ void two_sum(float& h, float& l, float w) {
   const float s = __fadd_rn(h, w), b = __fadd_rn(s, -h);
@@ -81,8 +88,8 @@ __device__ __forceinline__ void two_sum(float& h, float& l, float w) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams p, int CL) {
-  constexpr int N = 16 / sizeof(T), kSweeps = kVerTile / (32 * N);
+__global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyParams p, int CL) {
+  constexpr int N = 16 / sizeof(T), kSweeps = kVerTile / (32 * N), kBatch = 4;
   extern __shared__ double s_sums[];                   // this block's tiles' sums; in the last block's turn all of them
   __shared__ int s_fail;
   cg::cluster_group cluster = cg::this_cluster();
@@ -137,30 +144,79 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
   double total = 0.0;
   for (int attempt = 0; attempt < 2; ++attempt) {
     for (int t = rank + CL * warp; t < tiles; t += CL * kVerWarps) {
-      float h = 0.f, l = 0.f;
-      const int e0 = t * kVerTile - mis + lane * N;
+      float h[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};      // two chains of additions side by side
+      const int e0 = t * kVerTile - mis + lane * N, first = t * kVerTile - mis;
+      auto add = [&](const float* a, const float* c, int e) {
 #pragma unroll
-      for (int s = 0; s < kSweeps; ++s) {
-        const int e = e0 + s * 32 * N;
-        float a[N], c[N];
-        load_row<T, N>(pr, e, p.vocab, a);
-        if (qr) {
-          load_row<T, N>(qr, e, p.vocab, c);
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const float w = __fadd_rn(a[i], -c[i]);
-            const bool more = a[i] > c[i];
-            // w + err = a - c exactly
-            const float err = __fadd_rn(__fadd_rn(a[i], -w), -c[i]);
-            two_sum(h, l, more ? w : 0.f);
-            l = __fadd_rn(l, more ? err : 0.f);
+        for (int i = 0; i < N; ++i) {
+          if (c) {
+            // w + err = a - min(a, c) exactly
+            const float q = fminf(a[i], c[i]), w = __fadd_rn(a[i], -q), err = __fadd_rn(__fadd_rn(a[i], -w), -q);
+            two_sum(h[i & 1], l[i & 1], w);
+            l[i & 1] = __fadd_rn(l[i & 1], err);
+          } else {
+            two_sum(h[i & 1], l[i & 1], e + i == skip ? 0.f : a[i]);
           }
-        } else {
+        }
+      };
+      bool careful = qr && (reinterpret_cast<uintptr_t>(qr + first) & 15) != 0;
+      if (!careful) {
+        // aligned: kBatch loads of a lane and row in flight; what the row's ends
+        // leave of a lane's 16 bytes comes one by one
 #pragma unroll
-          for (int i = 0; i < N; ++i) two_sum(h, l, e + i == skip ? 0.f : a[i]);
+        for (int s0 = 0; s0 < kSweeps; s0 += kBatch) {
+          uint4 ra[kBatch], rc[kBatch];
+          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int s = 0; s < kBatch; ++s) {
+            const int e = e0 + (s0 + s) * 32 * N;
+            ra[s] = e >= 0 && e + N <= p.vocab ? __ldg(reinterpret_cast<const uint4*>(pr + e)) : zero;
+          }
+          if (qr) {
+#pragma unroll
+            for (int s = 0; s < kBatch; ++s) {
+              const int e = e0 + (s0 + s) * 32 * N;
+              rc[s] = e >= 0 && e + N <= p.vocab ? __ldg(reinterpret_cast<const uint4*>(qr + e)) : zero;
+            }
+          }
+#pragma unroll
+          for (int s = 0; s < kBatch; ++s) {
+            const int e = e0 + (s0 + s) * 32 * N;
+            float a[N], c[N];
+            widen<T, N>(ra[s], a);
+            if (qr) {
+              widen<T, N>(rc[s], c);
+              add(a, c, e);
+            } else {
+              add(a, nullptr, e);
+            }
+          }
+        }
+#pragma unroll 1
+        for (int end = 0; end < 2; ++end) {
+          // the lane's 16 bytes over the row's beginning, or over its end
+          const int at = end ? (p.vocab + mis) / N * N - mis : -mis, k = at - e0;
+          if (k < 0 || k >= kVerTile || k % (32 * N) || (at >= 0 && at + N <= p.vocab) || (end && at <= 0)) continue;
+          float a[N], c[N];
+          load_row<T, N>(pr, at, p.vocab, a);
+          if (qr) load_row<T, N>(qr, at, p.vocab, c);
+          add(a, qr ? c : nullptr, at);
+        }
+        // an infinite entry (which has no weight) has spoilt a sum
+        careful = __any_sync(0xffffffffu, !(h[0] + h[1] < INFINITY));
+        if (careful) h[0] = h[1] = l[0] = l[1] = 0.f;
+      }
+      if (careful) {
+#pragma unroll 1
+        for (int s = 0; s < kSweeps; ++s) {
+          const int e = e0 + s * 32 * N;
+          float a[N], c[N];
+          load_row<T, N>(pr, e, p.vocab, a);
+          if (qr) load_row<T, N>(qr, e, p.vocab, c);
+          add(a, qr ? c : nullptr, e);
         }
       }
-      double sum = (double)h + (double)l;
+      double sum = ((double)h[0] + (double)l[0]) + ((double)h[1] + (double)l[1]);
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane == 0) s_sums[t / CL] = sum;
@@ -262,7 +318,12 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
 
 template <typename T>
 mla_status launch_verify(const VerifyParams& p, cudaStream_t stream) {
-  const int CL = 8;
+  // Blocks of a sequence: 8 where there are few sequences, so that their rows
+  // spread over the SMs; with many, no more blocks than run side by side (256
+  // sequences of 131072 fp32 values: 108 us with 8, which come in four waves).
+  const int sms = device_sm_count();
+  int CL = 8;
+  while (CL > 1 && (int64_t)p.B * CL > 4 * (int64_t)sms) CL /= 2;
   const int tiles = (p.vocab + kVerTile - 1) / kVerTile + 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.B * CL);
