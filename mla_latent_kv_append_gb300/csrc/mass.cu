@@ -46,7 +46,7 @@ __device__ void plan_mass(const MassParams& p) {
       if (r.len == 0) continue;
       const int rows = r.n * p.H;
       r.heads = p.H;
-      r.tiles = (int)(((int64_t)r.len + kMassKeys - 1) / kMassKeys);
+      r.tiles = (int)(((int64_t)r.len + p.unit_tokens - 1) / p.unit_tokens);
       r.blocks = (rows + p.R - 1) / p.R;
       r.tile_cost = (r.blocks - 1) * mass_cost(p.R) + mass_cost(rows - (r.blocks - 1) * p.R);
       const int64_t u = (int64_t)r.tiles * r.tile_cost, q = (int64_t)r.tiles * r.blocks;
@@ -191,7 +191,12 @@ extern "C" mla_status mla_token_mass(const mla_cache_layer* cache, const float* 
   p.R = most <= 16 ? 16 : (most <= 32 ? 32 : (most <= 64 ? 64 : kMassMaxRows));
   const int sms = device_sm_count();
   p.grid = sms < 1 ? 1 : (sms < kMassMaxGrid ? sms : kMassMaxGrid);
-  const int64_t want = 1 + (p.rows * kPieces + kPrepThreads - 1) / kPrepThreads;
+  p.few = most <= 16 && (cache->latent_fmt == MLA_FMT_BF16 || cache->latent_fmt == MLA_FMT_INT8_SYM ||
+                         cache->latent_fmt == MLA_FMT_INT4_ASYM || cache->latent_fmt == MLA_FMT_INT4_SYM);
+  // the unit that the kernels copy at a time (FewShape::kBlocks), or a tile of theirs
+  p.unit_tokens = p.few ? (p.L.block_bytes < 20000 ? kPage : kBlockTokens) : kMassKeys;
+  // the few rows' kernel makes its queries' fragments itself: the plan alone
+  const int64_t want = p.few ? 1 : 1 + (p.rows * kPieces + kPrepThreads - 1) / kPrepThreads;
   const mla_status st = cuda_status(launch_pdl(mass_prep_kernel, dim3((unsigned)(want < 4 * p.grid ? want : 4 * p.grid)),
                                                dim3(kPrepThreads), 0, (cudaStream_t)stream, p));
   if (st != MLA_OK) return st;

@@ -59,6 +59,7 @@ struct MassParams {
   int32_t* dev_err;
   uint64_t wait_ns;
   int R, grid;
+  int few, unit_tokens;                                // 16 rows (mass_few.cuh); cached tokens of a key tile
   int query_pieces, raw_slots;                         // pieces of the queries and raw blocks in shared memory
   int64_t rows;                                        // N H
   // workspace
