@@ -36,7 +36,7 @@ struct FewShape {
   static constexpr int kUnits = kFewQuads / kBlocks;                 // copies in work at a time
   static constexpr int kLatStep = LF == MLA_FMT_BF16 ? 1536 : 1024, kKpeStep = KF == MLA_FMT_BF16 ? 1536 : 1024;      // fragments
   static constexpr int kQ = 32 * kLatStep + 4 * kKpeStep;
-  static constexpr int kSums = kQ;                                   // fp32 [32 groups][16 rows]: sums of a group's queries
+  static constexpr int kSums = kQ;                                   // fp32 [32 groups][16 rows]: sums of a group's queries, negated
   static constexpr int kParts = kSums + 32 * 16 * 4;                 // [quad][3][4][32] float4
   static constexpr int kLse = kParts + kFewQuads * 3 * 2048;
   static constexpr int kBars = kLse + 64;                            // and words
@@ -124,15 +124,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
   bool ok = true;
   if (warp == kFewCompute) {
     // ---- the cache's blocks, 32 page ids at a time
-    int64_t gi = 0;
+    int slot = 0;
+    uint32_t round = 0;                                // how often the ring went round
     while (ok && wk.left > 0) {
       const int n = (int)min(wk.left, (int64_t)(wk.s.tiles - wk.tile));
       for (int i0 = 0; i0 < n && ok; i0 += 32) {
         const int at = (wk.tile + i0 + lane) * SH::kBlocks / 2;      // the unit's page
         const int mine = i0 + lane < n ? __ldcg(p.table + (int64_t)wk.s.b * p.max_pages + at) : -1;
-        for (int i = i0; i < min(n, i0 + 32); ++i, ++gi) {
-          const int slot = (int)(gi % NS), page = __shfl_sync(0xffffffffu, mine, i - i0);
-          if (gi >= NS && !warp_wait(raw_free + 8 * slot, (uint32_t)(gi / NS - 1) & 1, p.wait_ns, abort)) {
+        for (int i = i0; i < min(n, i0 + 32); ++i) {
+          const int page = __shfl_sync(0xffffffffu, mine, i - i0);
+          if (round > 0 && !warp_wait(raw_free + 8 * slot, (round - 1) & 1, p.wait_ns, abort)) {
             ok = false;
             break;
           }
@@ -147,6 +148,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
             }
           }
           __syncwarp();
+          if (++slot == NS) {
+            slot = 0;
+            ++round;
+          }
         }
       }
       wk.left -= n;
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
     }
     // the copies in flight land before the block ends
     for (int s = 0; s < NS; ++s)
-      if (gi > s) drain_wait(raw_full + 8 * s, (uint32_t)((gi - 1 - s) / NS) & 1);
+      if (round > 0 || s < slot) drain_wait(raw_full + 8 * s, (s < slot ? round : round - 1) & 1);
     return;
   }
   // ---- Warp w of quad q: channels 128 w .. 128 w + 127 and RoPE channels 16 w ..
@@ -172,8 +177,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
   int key[4];
 #pragma unroll
   for (int nt = 0; nt < 4; ++nt) key[nt] = 8 * (n8 >> 1) + 2 * nt + (n8 & 1);
-  int64_t gi0 = 0;                                     // units of the segments before
-  uint32_t turn = 0;
+  int skip = q / SH::kBlocks;                          // units of the segment before this quad's next one
+  int slot = q / SH::kBlocks;                          // that unit's place in the ring
+  uint32_t round = 0, turn = 0;
   bool late = false;
   float4* parts = reinterpret_cast<float4*>(sm + SH::kParts) + q * 3 * 128;
   const float gain = p.scale_log2 * kQueryGain;
@@ -231,8 +237,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
           }
           if (j == 0) {
             float* sums = reinterpret_cast<float*>(sm + SH::kSums) + 16 * st;
-            sums[n8] = sa;
-            sums[n8 + 8] = sc;
+            sums[n8] = -sa;
+            sums[n8 + 8] = -sc;
           }
         }
         uint32_t hi[4], lo[4];
@@ -251,16 +257,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
     const float y0 = s_lse[n8], y1 = s_lse[n8 + 8];
 
     // this quad's units of the segment
-    const int mine = (int)(((q / SH::kBlocks - gi0) % SH::kUnits + SH::kUnits) % SH::kUnits);
-    for (int i = mine; i < n; i += SH::kUnits, ++turn) {
-      const int64_t gi = gi0 + i;
-      const int slot = (int)(gi % NS), t0 = ((tile0 + i) * SH::kBlocks + q % SH::kBlocks) * kBlockTokens;
-      if (!late && !warp_wait(raw_full + 8 * slot, (uint32_t)(gi / NS) & 1, p.wait_ns, abort)) {
+    int i = skip;
+    for (; i < n; i += SH::kUnits, ++turn) {
+      const int at = slot, t0 = ((tile0 + i) * SH::kBlocks + q % SH::kBlocks) * kBlockTokens;
+      const uint32_t phase = round & 1;
+      slot += SH::kUnits;
+      if (slot >= NS) {
+        slot -= NS;
+        ++round;
+      }
+      if (!late && !warp_wait(raw_full + 8 * at, phase, p.wait_ns, abort)) {
         late = true;                                   // leaves with the others, at the next sequence
         *abort = 1;
       }
       if (t0 >= len) {                                 // the page's second half holds nothing
-        warp_arrive(raw_free + 8 * slot);
+        warp_arrive(raw_free + 8 * at);
         continue;
       }
       // the fourth, in turn, has the result: its page and the old masses
@@ -278,7 +289,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
           old = p.mass[(int64_t)page * kPage + (t & (kPage - 1))];
         }
       }
-      const uint32_t blk = sb + SH::kRaw + slot * SH::kCopy + (q % SH::kBlocks) * SH::kBlock;
+      const uint32_t blk = sb + SH::kRaw + at * SH::kCopy + (q % SH::kBlocks) * SH::kBlock;
       float acc[4][4];
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt)
@@ -300,9 +311,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t at = sb + (g + h) * SH::kLatStep + 16 * lane;
+          const uint32_t fr = sb + (g + h) * SH::kLatStep + 16 * lane;
           if constexpr (LF == MLA_FMT_BF16) {
-            const uint4 a0 = lds16(at), a1 = lds16(at + 512), a2 = lds16(at + 1024);
+            const uint4 a0 = lds16(fr), a1 = lds16(fr + 512), a2 = lds16(fr + 1024);
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt) {
               const uint2 v = lds_pair(row[nt] + (((2 * (g + h) + (j >> 1)) << 4) ^ flip[nt]) + 8 * (j & 1));
@@ -311,14 +322,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
               mma_bf16(acc[nt], a2, v.x, v.y);
             }
           } else {
-            const uint4 hi = lds16(at), lo = lds16(at + 512);
+            const uint4 hi = lds16(fr), lo = lds16(fr + 512);
             float s[8];
             lds_floats8(blk + AT::kScale + 128 * (g + h) + 32 * j, s);
-            float z[8], sum0 = 0.f, sum1 = 0.f;
+            float z[8];
+            uint64_t sum0 = 0, sum1 = 0;
             if constexpr (LF == MLA_FMT_INT4_ASYM) {
               lds_floats8(blk + AT::kZero + 128 * (g + h) + 32 * j, z);
-              sum0 = lds4(sb + SH::kSums + 4 * (16 * (g + h) + n8));
-              sum1 = lds4(sb + SH::kSums + 4 * (16 * (g + h) + n8 + 8));
+              const float u = lds4(sb + SH::kSums + 4 * (16 * (g + h) + n8)), v = lds4(sb + SH::kSums + 4 * (16 * (g + h) + n8 + 8));
+              sum0 = pack2(u, u);
+              sum1 = pack2(v, v);
             }
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt) {
@@ -327,20 +340,23 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
               else codes8(lds_word(row[nt] + (((g + h) << 4) ^ flip[nt]) + 4 * j), b0, b1);
               float d[4] = {0.f, 0.f, 0.f, 0.f};
               if constexpr (LF == MLA_FMT_INT4_ASYM) {
-                d[0] = -z[2 * nt] * sum0, d[1] = -z[2 * nt + 1] * sum0, d[2] = -z[2 * nt] * sum1, d[3] = -z[2 * nt + 1] * sum1;
+                const uint64_t zz = pack2(z[2 * nt], z[2 * nt + 1]);
+                unpack2(mul2(zz, sum0), d[0], d[1]);
+                unpack2(mul2(zz, sum1), d[2], d[3]);
               }
               mma_half(d, hi, b0, b1);
               mma_half(d, lo, b0, b1);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[nt][e] = fmaf(s[2 * nt + (e & 1)], d[e], acc[nt][e]);
+              const uint64_t ss = pack2(s[2 * nt], s[2 * nt + 1]);
+              unpack2(fma2(ss, pack2(d[0], d[1]), pack2(acc[nt][0], acc[nt][1])), acc[nt][0], acc[nt][1]);
+              unpack2(fma2(ss, pack2(d[2], d[3]), pack2(acc[nt][2], acc[nt][3])), acc[nt][2], acc[nt][3]);
             }
           }
         }
       }
       {                                                // RoPE channels 16 w .. 16 w + 15: groups of 8
-        const uint32_t at = sb + 32 * SH::kLatStep + w * SH::kKpeStep + 16 * lane, kpe = blk + AT::kKpe;
+        const uint32_t fk = sb + 32 * SH::kLatStep + w * SH::kKpeStep + 16 * lane, kpe = blk + AT::kKpe;
         if constexpr (KF == MLA_FMT_BF16) {
-          const uint4 a0 = lds16(at), a1 = lds16(at + 512), a2 = lds16(at + 1024);
+          const uint4 a0 = lds16(fk), a1 = lds16(fk + 512), a2 = lds16(fk + 1024);
 #pragma unroll
           for (int nt = 0; nt < 4; ++nt) {
             const uint2 v = lds_pair(kpe + key[nt] * AT::kKpeRow + 16 * kpe_chunk_pos(2 * w + (j >> 1), key[nt], KF) + 8 * (j & 1));
@@ -349,7 +365,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
             mma_bf16(acc[nt], a2, v.x, v.y);
           }
         } else {
-          const uint4 hi = lds16(at), lo = lds16(at + 512);
+          const uint4 hi = lds16(fk), lo = lds16(fk + 512);
           float s0[8], s1[8];
           lds_floats8(blk + AT::kKpeScale + 128 * (2 * w) + 32 * j, s0);
           lds_floats8(blk + AT::kKpeScale + 128 * (2 * w + 1) + 32 * j, s1);
@@ -373,7 +389,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
           }
         }
       }
-      warp_arrive(raw_free + 8 * slot);                // read: the next copy may come
+      warp_arrive(raw_free + 8 * at);                  // read: the next copy may come
       if (!final) {
         float4* out = parts + ((w - (int)(turn & 3) + 3) & 3) * 128 + lane;
 #pragma unroll
@@ -417,7 +433,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
       const float sum = keep + __shfl_xor_sync(0xffffffffu, give, 4);
       if (page >= 0 && t < len && !late) p.mass[(int64_t)page * kPage + (t & (kPage - 1))] = fmaf(old, p.decay, sum);
     }
-    gi0 += n;
+    skip = i - n;
     wk.left -= n;
     if (wk.left > 0) {
       wk.tile = 0;
