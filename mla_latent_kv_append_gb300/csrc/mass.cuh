@@ -608,63 +608,61 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
     }
     if (late) set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
   } else if (work && warp == kMassMma) {
-    // ---- the MMAs.  The warp runs converged, one lane issues: loop counters and
-    // descriptors then live in uniform registers.
+    // ---- one thread issues the MMAs (with the whole warp in the loop and one lane
+    // issuing, a 32-query window over 4 x 16000 tokens took 112 us)
     MassWalk wk;
     wk.open(p, U, lo, hi);
-    const bool leader = elect_one();
-    const uint64_t d_q = sw128_desc(sb, 16, 1024);
-    uint32_t it = 0, q_round = 0, id = 0, id_minus = 0, id_both = 0, lo_step = 0;
-    int qs = 0, slot = 0, round = 0, held_k = -1, held_rb = -1;
-    bool both = false;
-    while (ok && wk.valid()) {
-      const uint32_t g = it & 1, d = tbase + g * d_cols;
-      const bool held = resident && wk.k == held_k && wk.rb == held_rb;
-      if (wk.k != held_k || wk.rb != held_rb) {
-        held_k = wk.k;
-        held_rb = wk.rb;
-        // Where the buffer has the columns, both halves of the queries are one N
-        // of twice the rows: an MMA with A in TMEM costs 32 cycles up to N = 64.
-        const int rows = wk.rows();
-        both = 2 * rows <= d_cols;
-        id = f16_idesc(128, rows, false, false);
-        id_minus = id | kNegateA;
-        id_both = (both ? f16_idesc(128, 2 * rows, false, false) : id) | kNegateA;
-        lo_step = rows * 128 >> 4;
-        if (resident && it > 0 && leader) umma_commit(bars + 8 * mQDone);          // the old queries' last reader
-      }
-      wk.next();
-      // the scores of two passes before have been read
-      if (it >= 2 && !(ok = warp_wait(bars + 8 * (mE + g), ((it - 2) >> 1) & 1, p.wait_ns, abort))) break;
-      for (int kb = 0; kb < 9;) {
-        if (!(ok = warp_wait(bars + 8 * (mA + slot), round & 1, p.wait_ns, abort))) break;
-        uint32_t a = t_a + slot * cols;
-        for (const int end = kb + PU / 2; kb < end; ++kb, a += 32) {
-          if (!held && !(ok = warp_wait(bars + 8 * (mQ + qs), q_round & 1, p.wait_ns, abort))) break;
-          fence_after();
-          const uint64_t b_hi = d_q + (uint32_t)(qs * R * 16);
-          if (leader) {
+    if (elect_one()) {
+      const uint64_t d_q = sw128_desc(sb, 16, 1024);
+      uint32_t it = 0, q_round = 0, id = 0, id_minus = 0, id_both = 0, lo_step = 0;
+      int qs = 0, slot = 0, round = 0, held_k = -1, held_rb = -1;
+      bool both = false;
+      while (ok && wk.valid()) {
+        const uint32_t g = it & 1, d = tbase + g * d_cols;
+        const bool held = resident && wk.k == held_k && wk.rb == held_rb;
+        if (wk.k != held_k || wk.rb != held_rb) {
+          held_k = wk.k;
+          held_rb = wk.rb;
+          // Where the buffer has the columns, both halves of the queries are one N
+          // of twice the rows: an MMA with A in TMEM costs about 75 cycles however
+          // small its N is.
+          const int rows = wk.rows();
+          both = 2 * rows <= d_cols;
+          id = f16_idesc(128, rows, false, false);
+          id_minus = id | kNegateA;
+          id_both = (both ? f16_idesc(128, 2 * rows, false, false) : id) | kNegateA;
+          lo_step = rows * 128 >> 4;
+          if (resident && it > 0) umma_commit(bars + 8 * mQDone);      // the old queries' last reader
+        }
+        wk.next();
+        // the scores of two passes before have been read
+        if (it >= 2 && !(ok = bar_wait(bars + 8 * (mE + g), ((it - 2) >> 1) & 1, p.wait_ns, abort))) break;
+        for (int kb = 0; kb < 9;) {
+          if (!(ok = bar_wait(bars + 8 * (mA + slot), round & 1, p.wait_ns, abort))) break;
+          uint32_t a = t_a + slot * cols;
+          for (const int end = kb + PU / 2; kb < end; ++kb, a += 32) {
+            if (!held && !(ok = bar_wait(bars + 8 * (mQ + qs), q_round & 1, p.wait_ns, abort))) break;
+            fence_after();
+            const uint64_t b_hi = d_q + (uint32_t)(qs * R * 16);
             umma4_ta<2>(d, a, b_hi, id_both, kb != 0);
             if (!both) umma4_ta<2>(d, a, b_hi + lo_step, id_minus, 1u);
             if (kb < 8 ? LF != MLA_FMT_BF16 : KF != MLA_FMT_BF16) umma4_ta<2>(d, a + 16 * PU, b_hi, id, 1u);
             if (!resident) umma_commit(bars + 8 * (mQFree + qs));
+            if (++qs == QS) {
+              qs = 0;
+              if (!held) ++q_round;
+            }
           }
-          if (++qs == QS) {
-            qs = 0;
-            if (!held) ++q_round;
+          if (!ok) break;
+          umma_commit(bars + 8 * (mAFree + slot));
+          if (++slot == NA) {
+            slot = 0;
+            ++round;
           }
         }
-        if (!ok) break;
-        if (leader) umma_commit(bars + 8 * (mAFree + slot));
-        if (++slot == NA) {
-          slot = 0;
-          ++round;
-        }
+        if (ok) umma_commit(bars + 8 * (mS + g));
+        ++it;
       }
-      if (ok && leader) umma_commit(bars + 8 * (mS + g));
-      ++it;
-    }
-    if (leader) {
       if (!ok) {
         set_err(p.dev_err, MLA_DEVERR_TIMEOUT);
         *abort = 1;
