@@ -32,8 +32,10 @@ struct MassCounts {
   int32_t seqs, pad;
 };
 
-// Units of a pass with this many rows.
-__host__ __device__ constexpr int mass_cost(int rows) { return rows <= 48 ? 3 : (rows + 15) / 16; }
+// Units of a pass with this many rows: an MMA takes about 75 cycles however few
+// there are, 92 with 128 (24 drafts of up to 5 tokens at 64 heads: 98 us a call when
+// passes were counted by their rows alone, 77 so).
+__host__ __device__ constexpr int mass_cost(int rows) { return 4 + (rows + 31) / 32; }
 
 // Run x of G equal runs over U units begins here; the run that holds unit u.
 __device__ __forceinline__ int64_t mass_run(int64_t U, int x, int G) {
