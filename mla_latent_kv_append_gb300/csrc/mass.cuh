@@ -96,6 +96,14 @@ __device__ __forceinline__ void load_split(uint32_t row, uint32_t scale, uint32_
 template <int LF, int KF>
 struct MassShape {
   static constexpr int kBlock = BlockAt<LF, KF>::kBytes;
+  // An accumulation in TMEM cuts the sum to 24 bits, towards 0: it loses half a last
+  // place on average, 4.3e-8 of a sum whose mantissa is spread as in nature.  A large
+  // score grows to its value on a nearly straight way, so that n accumulations take
+  // n 4.3e-8 0.45 of it; given back here, what is left of the error is a fifth (512
+  // queries over 6000 tokens: 4e-6 of the masses before, 0.6 to 1.3e-6 after; an
+  // emulation of the sums gives the same).  (The small products in columns of their
+  // own would leave 36 accumulations, 2e-7, and take 7 to 12% longer.)
+  static constexpr float kUngain = kMassUngain * (1.f + 4.3e-8f * 0.45f * (LF == MLA_FMT_BF16 ? 72 : 108));
   // A bulk copy costs 85 ns of the copy engine besides its bytes, and a block of
   // 4-bit codes is 18 KB: whole pages of those (a stream of nothing but copies:
   // 18.5 KB each 5.6 TB/s, 23.7 KB 7.0, 37 KB 6.9).
@@ -241,9 +249,9 @@ __device__ __forceinline__ void split_unit(const RawUnit<FMT, KPE>& r, uint32_t*
     // (q has at most 8 bits), and l = fl(q b + (q a - h)): three instructions a
     // pair, 2^-22 of x.  (h is made as q (-a), which the last step needs, and stays
     // negated: the MMA turns it back.)  b lies on fp16's subnormal grid, off by up to 2^-25: for
-    // scales from 2^-9 on 2^-18 of them at most.  Needs scales in that range and
+    // scales from 2^-9 on 2^-20 of them at most.  Needs scales in that range and
     // zero-points that keep q a finite; other units go through fp32.
-    constexpr uint32_t kLow = 0x3B000000u, kHigh = 0x42800000u;      // 2^-9 .. 64
+    constexpr uint32_t kLow = 0x3B000000u, kHigh = 0x41800000u;      // 2^-9 .. 16
     uint32_t most = 0u;
     float top = 0.f;
 #pragma unroll
@@ -562,12 +570,12 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
         }
         if (plain) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) sum[c & 3] += ex2(fmaf(__uint_as_float(r[c]), kMassUngain, s_lse[c0 + c]));
+          for (int c = 0; c < 16; ++c) sum[c & 3] += ex2(fmaf(__uint_as_float(r[c]), SH::kUngain, s_lse[c0 + c]));
         } else {
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             const float y = s_lse[c0 + c];
-            const float w = ex2(fmaf(__uint_as_float(r[c]), kMassUngain, y));
+            const float w = ex2(fmaf(__uint_as_float(r[c]), SH::kUngain, y));
             sum[c & 3] += c0 + c >= first && y > -INFINITY ? w : 0.f;
           }
         }
@@ -623,9 +631,9 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
         if (wk.k != held_k || wk.rb != held_rb) {
           held_k = wk.k;
           held_rb = wk.rb;
-          // Where the buffer has the columns, both halves of the queries are one N
-          // of twice the rows: an MMA with A in TMEM costs about 75 cycles however
-          // small its N is.
+          // Where the buffer has the columns (up to 32 rows), both halves of the
+          // queries are one N of twice the rows: an MMA with A in TMEM costs about
+          // 75 cycles however small its N is.
           const int rows = wk.rows();
           both = 2 * rows <= d_cols;
           id = f16_idesc(128, rows, false, false);

@@ -39,7 +39,7 @@ struct FewShape {
   static constexpr int kSums = kQ;                                   // fp32 [32 groups][16 rows]: sums of a group's queries, negated
   static constexpr int kParts = kSums + 32 * 16 * 4;                 // [quad][3][4][32] float4
   static constexpr int kLse = kParts + kFewQuads * 3 * 2048;
-  static constexpr int kBars = kLse + 64;                            // and words
+  static constexpr int kBars = kLse + 128;                            // and words
   static constexpr int kRaw = (kBars + 256 + 127) / 128 * 128;
   static constexpr int kFit = (232448 - 1024 - kRaw) / kCopy;
   static constexpr int kSlots = kFit < kFewMaxRaw ? kFit : kFewMaxRaw;
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(few_smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sb = smem_u32(sm), raw_full = sb + SH::kBars, raw_free = raw_full + 8 * kFewMaxRaw;
   volatile int* abort = reinterpret_cast<volatile int*>(sm + SH::kBars + 16 * kFewMaxRaw);
-  float* s_lse = reinterpret_cast<float*>(sm + SH::kLse);
+  float2* s_lse = reinterpret_cast<float2*>(sm + SH::kLse);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -197,8 +197,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
     // ---- the sequence's queries as A fragments: rows n8 and n8 + 8, channels 4 j
     // .. 4 j + 3 of a step of 16
     if (warp == 0 && lane < 16) {
-      const float v = __ldcg(p.lse + row0 + lane) * -1.4426950408889634f;
-      s_lse[lane] = fabsf(v) < INFINITY ? v : -INFINITY;
+      // -lse log2 e and what its rounding left
+      const float lse = __ldcg(p.lse + row0 + lane), v = lse * -1.4426950408889634f;
+      const float rest = fmaf(lse, -1.4426950408889634f, -v) - lse * 1.925963033500e-8f;
+      s_lse[lane] = fabsf(v) < INFINITY ? make_float2(v, rest) : make_float2(-INFINITY, 0.f);
     }
     const bool live0 = fabsf(__ldcg(p.lse + row0 + n8)) < INFINITY, live1 = fabsf(__ldcg(p.lse + row0 + n8 + 8)) < INFINITY;
     for (int st = warp; st < 36; st += kFewCompute) {
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
       }
     }
     asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kFewCompute) : "memory");
-    const float y0 = s_lse[n8], y1 = s_lse[n8 + 8];
+    const float2 y0 = s_lse[n8], y1 = s_lse[n8 + 8];
 
     // this quad's units of the segment
     int i = skip;
@@ -411,8 +413,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
       float v[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float w0 = ex2(fmaf(acc[k >> 1][k & 1], 1.f / kQueryGain, y0)), w1 = ex2(fmaf(acc[k >> 1][2 + (k & 1)], 1.f / kQueryGain, y1));
-        v[k] = (y0 > -INFINITY ? w0 : 0.f) + (y1 > -INFINITY ? w1 : 0.f);
+        const float w0 = ex2(fmaf(acc[k >> 1][k & 1], 1.f / kQueryGain, y0.x) + y0.y);
+        const float w1 = ex2(fmaf(acc[k >> 1][2 + (k & 1)], 1.f / kQueryGain, y1.x) + y1.y);
+        v[k] = (y0.x > -INFINITY ? w0 : 0.f) + (y1.x > -INFINITY ? w1 : 0.f);
       }
       // added up over the eight lanes of a j; each keeps one key: bit 2 of n8 says
       // which half of the eight, bit 1 which pair, bit 0 which of the two

@@ -9,9 +9,9 @@ constexpr int kMassKeys = 128;                         // keys per tile
 constexpr int kMassMaxRows = 128;                      // most rows per pass
 constexpr int kMassMaxGrid = 512;                      // most blocks
 // Cached values are multiplied by kKeyGain, queries (with the softmax scale and
-// log2 e) by kQueryGain: halves keep 22 bits of values down to 2^-5 and 2^-8, and stay
-// finite up to 16376 and 2047.
-constexpr float kKeyGain = 4.f, kQueryGain = 32.f, kMassUngain = 1.f / (kKeyGain * kQueryGain);
+// log2 e) by kQueryGain: halves keep 22 bits of values down to 2^-7 and 2^-8, and stay
+// finite up to 4094 and 2047.
+constexpr float kKeyGain = 16.f, kQueryGain = 32.f, kMassUngain = 1.f / (kKeyGain * kQueryGain);
 
 // One sequence with queries and tokens, in the order of the batch.  Its rows r =
 // i H + h are cut into row blocks of R; a pass is a row block of a key tile, the
