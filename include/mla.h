@@ -669,7 +669,7 @@ size_t mla_chunk_workspace_bytes(int32_t batch, int32_t n_tokens, int32_t heads,
  *   sequence with more than max_out rows is refused (MLA_DEVERR_SEQLEN): it
  *   accepts nothing, its tokens are -1, its length stays.  So are all
  *   sequences when row_start decreases or leaves [0, rows] anywhere.
- *   Sums are good to 2^-46 of the row's, the comparison is exact.
+ *   Sums are good to 2^-40 of the row's, the comparison is exact.
  *   vocab <= 2^22, batch <= 4096; batch == 0 is a no-op.
  */
 #define MLA_PROB_FP32 0
@@ -706,6 +706,14 @@ mla_status mla_verify_drafts(const void* target_probs, int64_t target_row_stride
  *   is left alone and sets MLA_DEVERR_SEQLEN; so are all when q_start
  *   decreases or leaves [0, n_tokens].  Sequences without queries are left
  *   alone.  Sequences of a call must not share pages.
+ *   Precision: queries and cached values as two fp16 halves (22 bits), products
+ *   summed in fp32 by the tensor cores, exponentials and masses in fp32: about
+ *   1e-6 of the masses.  A cached value beyond 4094 in magnitude, or a query
+ *   beyond 2047 after the scale and log2 e, may count as non-finite: its token's
+ *   mass, or that of all tokens the query sees, is then not finite.  A cached
+ *   value below 2^-7 is off by up to 2^-29.
+ *   A wait that runs out (mla_set_wait_limit_ns) sets MLA_DEVERR_TIMEOUT and
+ *   leaves the call's masses undefined.
  *   The same call gives the same bits.  batch <= 4096, n_tokens * H < 2^31;
  *   n_tokens == 0 or batch == 0 is a no-op.
  */
@@ -812,7 +820,7 @@ const char* mla_last_cuda_error(void);
 /*
  * mla_set_wait_limit_ns - bound, in nanoseconds, on every wait inside the
  * decode kernels (stage arrivals, the hand-offs between the block's warp
- * roles) of the decode, prefill and chunk calls this process launches afterwards;
+ * roles) of the decode, prefill, chunk and mass calls this process launches afterwards;
  * returns the previous bound, or -1 (nothing changed) for ns < 0.  The
  * default is 10 s.  A test and diagnostic hook, not part of the pages'
  * method: a wait that runs out sets MLA_DEVERR_TIMEOUT in *dev_err, and its

@@ -8,7 +8,7 @@
 //   (all passed: j is the last row and w = c(p_j)), and the next token is the
 //   smallest v with sum of w up to v > u total(w).
 // The product and the subtraction round nothing (below), and the sums are good to
-// 2^-46: a border between two tokens is 1 / vocab wide, and an fp32 sum would
+// 2^-40: a border between two tokens is 1 / vocab wide, and an fp32 sum would
 // pick a neighbour now and then.
 //
 // What bounds it: reading row j of p and q once (a megabyte for 131072 fp32

@@ -262,6 +262,31 @@ def test_in_a_graph_with_other_lengths(mla):
     u.compare(mass[: u.before.numel()])
 
 
+@pytest.mark.parametrize("lf,kf", [(F_INT8, F_INT8), (F_BF16, F_BF16), (F_INT4, F_INT4S), (F_INT4S, F_INT8)], ids=lambda f: FMT_NAME[f])
+def test_many_sequences_of_one_row_tile(mla, lf, kf):
+    """Decodes of 16 heads: more sequences than SMs, lengths around pages and blocks."""
+    lens = [(t, 1) for t in ([0, 1, 30, 31, 32, 33, 62, 63, 64, 65, 94, 95, 96, 127, 128, 129] * 14 + [2000, 700])]
+    t = Mass(mla, lens, 16, lf, kf, seed=22)
+    t.compare(t.go())
+    assert t.err.item() == 0
+
+
+def test_scales_and_zero_points_of_any_size(mla):
+    """Groups whose values differ by little, far from zero (large zero-points), and groups of very different scale."""
+    for lf, kf, gain in ((F_INT4, F_INT8, 1e-3), (F_INT4, F_INT4S, 30.0), (F_INT8, F_INT4S, 1e-4), (F_INT8, F_INT8, 100.0)):
+        for H in (16, 32):
+            t = Mass(mla, [(200, 1), (70, 1)], H, lf, kf, seed=23, gain=gain, scale=SCALE / max(1.0, gain), q_gain=0.3)
+            t.compare(t.go())
+
+
+def test_a_bound_above_the_step_s_figures(mla):
+    """max_new larger than any sequence's: another kernel, the same masses."""
+    t = Mass(mla, [(300, 1), (90, 1), (5, 1)], 16, seed=24)
+    n = mla.mla_mass_workspace_bytes(t.B, t.N, 16, 3)
+    t.compare(t.go(max_new=3, ws=torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")))
+    t.compare(t.go(max_new=1))
+
+
 def test_two_calls_at_once(mla):
     """Two streams, a workspace each."""
     a, b = Mass(mla, [(3000, 2)], 16, seed=19), Mass(mla, [(2500, 5)], 32, F_INT4, F_INT8, seed=20)
@@ -279,7 +304,8 @@ def test_two_calls_at_once(mla):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
-@pytest.mark.parametrize("H,lens", [(16, [(3000, 1), (500, 1)]), (64, [(900, 5), (300, 4)])], ids=["resident", "streamed"])
+@pytest.mark.parametrize("H,lens", [(16, [(3000, 1), (500, 1)]), (32, [(3000, 1), (500, 1)]), (64, [(900, 5), (300, 4)])],
+                         ids=["few rows", "resident", "streamed"])
 def test_waits_that_run_out_end_the_call(mla, H, lens):
     """With no patience the kernel gives up and says so; the context stays usable and the next call is right."""
     t = Mass(mla, lens, H, seed=21)

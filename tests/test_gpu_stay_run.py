@@ -212,3 +212,41 @@ def test_a_cache_within_its_budget(mla, lf, kf):
                 assert np.allclose(have, s.weight[layer][b], rtol=1e-4, atol=1e-6)
             s.attend(layer, table)
     assert cuts == 3
+
+
+def test_a_cut_in_a_graph(mla):
+    """Selection, release and move captured once and replayed with other
+    lengths, against the calls one by one on a copy."""
+    B, P, num_pages, budget = 3, 6, 50, 90
+    s = Server(mla, B, P, num_pages, F_INT8, F_INT8, layers=1, seed=5)
+    s.plan([300, 140, 128])                               # pages for every replay below
+    cache, keep = s.caches[0], dev([budget] * B)
+    kept, kept_lens, out, lens, rng = e(B, budget), e(B), e(B, P), e(B), e(2)
+    state = [cache.pool, s.mass[0], s.table, s.lens, s.page_table, s.free, s.range]
+
+    def cut():
+        mla.mla_select_tokens(s.mass[0], s.table, s.lens, keep, kept, kept_lens, sinks=2, recent=8, dev_err=s.err)
+        mla.mla_release_pages(s.lens, kept_lens, s.req, s.table, s.page_table, s.free, s.range, num_pages, out, lens, rng, move=True,
+                              dev_err=s.err)
+        mla.mla_move_tokens(cache, s.table, s.lens, kept, lens, out, mass=s.mass[0], dev_err=s.err)
+
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    first = [t.clone() for t in state]
+    cut()                                                 # loads the kernels before the capture
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=side):
+        cut()
+    for lengths in ([300, 140, 64], [91, 90, 0], [200, 1, 128]):
+        results = []
+        for call in (g.replay, cut):
+            for t, v in zip(state, first):
+                t.copy_(v)
+            s.mass[0].copy_(torch.rand(num_pages * 64, generator=torch.Generator().manual_seed(6)))
+            s.lens.copy_(dev(lengths))
+            torch.cuda.synchronize()
+            call()
+            torch.cuda.synchronize()
+            results.append([t.clone() for t in state + [kept, kept_lens, out, lens, rng]])
+        assert all(torch.equal(a, b) for a, b in zip(*results))
+        assert results[0][-2].tolist() == [min(budget, n) for n in lengths]
+    assert s.err.item() == 0
