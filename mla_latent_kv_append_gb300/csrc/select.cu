@@ -147,19 +147,20 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
   }
   uint32_t prefix = 0u, mask = 0u;
   int need = want;                                     // how many stay among the keys that share the prefix
+#pragma unroll 1
   for (int pass = 0; pass < 3 && want > 0; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     const uint32_t digits = pass == 2 ? 1023u : 2047u;
     if (pass == 0) __syncthreads();                    // the bins are clear
-    uint32_t* bins = pass == 0 ? copies + (lane % kSelCopies) * kSelPitch : ex.bins[pass];
-    // equal keys count as one: those equal to the warp's first
+    // a shared-memory address: through a generic one an addition takes many times as long
+    const uint32_t bins = (uint32_t)__cvta_generic_to_shared(pass == 0 ? copies + (lane % kSelCopies) * kSelPitch : ex.bins[pass]);
+    // a warp's weights of 0 count at once
+    constexpr uint32_t kZero = 0x80000000u;
+    auto add = [](uint32_t at, uint32_t n) { asm volatile("red.shared.add.u32 [%0], %1;\n" ::"r"(at), "r"(n) : "memory"); };
     auto count = [&](bool in, uint32_t k) {
-      const uint32_t some = __ballot_sync(0xffffffffu, in);
-      if (!some) return;
-      const int first = __ffs(some) - 1;
-      const uint32_t common = __shfl_sync(0xffffffffu, k, first);    // every lane takes part
-      const uint32_t peers = __ballot_sync(0xffffffffu, in && k == common);
-      if (in && (k != common || lane == first)) atomicAdd(bins + ((k >> shift) & digits), k == common ? (uint32_t)__popc(peers) : 1u);
+      const uint32_t zeros = __ballot_sync(0xffffffffu, in && k == kZero);
+      if (in && k != kZero) add(bins + 4 * ((k >> shift) & digits), 1u);
+      if (zeros && lane == 0) add(bins + 4 * ((kZero >> shift) & digits), (uint32_t)__popc(zeros));
     };
     if constexpr (HELD > 0) {
 #pragma unroll
