@@ -17,6 +17,17 @@
 // X lies in TMEM as the MMAs' A: as shared-memory operands, two halves of 128
 // keys do not fit (288 KB), and writing and reading them would cost 5700 cycles
 // of shared-memory time a tile.
+//
+// What bounds it: the MMAs, 75 to 92 cycles each with A in TMEM, and for 128 rows the
+// queries' way from L2 (295 KB for a pass, 40 bytes a cycle and SM).  Measured
+// (a captured call's share of many): 4 x 16000 tokens INT8, a window of 32 queries at 16 heads
+// 93 us, 400 TFLOP/s of scores or 21% of the bf16 rate, of which three products make
+// 62%; 24 drafts of up to 5 tokens at 64 heads, bf16, 77 us; 32 x 32768 tokens INT4
+// at 32 heads 211 us, at 64 heads 247.
+//
+// Work split: all passes (a key tile, up to 128 rows) in a row, cut into runs of equal
+// cost, one to an SM.  A tile that several blocks share is added up by whichever
+// finishes last, in the blocks' order, so that results repeat bit for bit.
 #pragma once
 
 #include <math.h>
@@ -356,6 +367,16 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   if ((threadIdx.x & 31) == 0) bar_arrive(bar);
 }
 
+// A ring's copy in round `round` of its place.  Warps share the copies out among
+// them, and where the places are no multiple of the shares a place goes from warp to
+// warp: the copy before this one is another warp's and may land after this warp's own
+// last one, and a wait by parity for this one would take the round before that for
+// it.  So that one's release first, which is at most one round behind (it was issued
+// before this warp's last copy); from then on `full` is in this round or behind it.
+__device__ __forceinline__ bool ring_wait(uint32_t full, uint32_t free, uint32_t round, uint64_t limit_ns, volatile int* abort) {
+  return (round == 0 || warp_wait(free, (round - 1) & 1, limit_ns, abort)) && warp_wait(full, round & 1, limit_ns, abort);
+}
+
 // Whether any thread of the four reading warps says so; also their barrier.
 __device__ __forceinline__ bool vote_128(bool mine) {
   uint32_t any;
@@ -438,7 +459,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
     int rs = d / SH::kBlocks, slot0 = 0;               // raw copy; TMEM place of the pass's first piece
     uint32_t raw_round = 0, round0 = 0;                // how often they went round
     for (; n_pass > 0; --n_pass) {
-      if (!(ok = warp_wait(bars + 8 * (mRaw + rs), raw_round & 1, p.wait_ns, abort))) break;
+      if (!(ok = ring_wait(bars + 8 * (mRaw + rs), bars + 8 * (mRawFree + rs), raw_round, p.wait_ns, abort))) break;
       const uint32_t raw = s_raw + rs * SH::kCopy + (d % SH::kBlocks) * SH::kBlock, at = sb + raw;
 #pragma unroll 1
       for (int j = e; j < kMassUnits; j += kMassGroups) {
@@ -521,7 +542,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
         set_err(p.dev_err, MLA_DEVERR_PAGE);
         pg = -1;
       } else if (t < wk.s.counted) {
-        m = p.mass[(int64_t)pg * kPage + (t & (kPage - 1))];
+        m = __ldcg(p.mass + (int64_t)pg * kPage + (t & (kPage - 1)));
       }
     };
     if (wk.valid()) look(page, old);

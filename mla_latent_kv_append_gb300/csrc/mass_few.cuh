@@ -10,12 +10,17 @@
 // enter in fp32, behind the product, for any value they may have.  q is two fp16
 // halves (22 bits); bf16 latents take bf16 operands, q in three parts.
 //
-// What bounds it: instruction issue, 580 instructions a warp and 32-token
-// block, then the cache's bytes.  The cache comes in bulk copies into a ring; four
+// What bounds it: the latency of its instructions (890 a warp and 32-token block,
+// half the issue slots, with the 16 warps that the registers allow) and two thirds of
+// the shared-memory pipe, not the cache's bytes.  The cache comes in bulk copies into a ring; four
 // warps share a 32-token block by channels (eight latent groups and 16 RoPE
 // channels each), three hand their partial scores to the fourth, in turn, which
 // takes the exponentials and adds up the rows.  The queries' fragments lie in
 // shared memory, made anew for every sequence.
+//
+// Measured (a captured call's share of many): 32 x 32768 tokens INT4 206 us, 3.0 TB/s
+// or 45% of a plain copy's rate.  Eight warps to a block, with their queries'
+// fragments in registers: 325 us.
 #pragma once
 
 #include <math.h>
@@ -262,18 +267,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
     int i = skip;
     for (; i < n; i += SH::kUnits, ++turn) {
       const int at = slot, t0 = ((tile0 + i) * SH::kBlocks + q % SH::kBlocks) * kBlockTokens;
-      const uint32_t phase = round & 1;
+      const uint32_t its_round = round;
       slot += SH::kUnits;
       if (slot >= NS) {
         slot -= NS;
         ++round;
       }
-      if (!late && !warp_wait(raw_full + 8 * at, phase, p.wait_ns, abort)) {
+      // a place that is always this quad's needs no look at who had it before (32 x
+      // 32768 tokens INT4: 206 us, with it 212)
+      if (!late && !(NS % SH::kUnits ? ring_wait(raw_full + 8 * at, raw_free + 8 * at, its_round, p.wait_ns, abort)
+                                     : warp_wait(raw_full + 8 * at, its_round & 1, p.wait_ns, abort))) {
         late = true;                                   // leaves with the others, at the next sequence
         *abort = 1;
       }
       if (t0 >= len) {                                 // the page's second half holds nothing
-        warp_arrive(raw_free + 8 * at);
+        if (!late) warp_arrive(raw_free + 8 * at);
         continue;
       }
       // the fourth, in turn, has the result: its page and the old masses
@@ -288,7 +296,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
           if (lane == 0) set_err(p.dev_err, MLA_DEVERR_PAGE);
           page = -1;
         } else if (t < min(len, counted)) {
-          old = p.mass[(int64_t)page * kPage + (t & (kPage - 1))];
+          old = __ldcg(p.mass + (int64_t)page * kPage + (t & (kPage - 1)));
         }
       }
       const uint32_t blk = sb + SH::kRaw + at * SH::kCopy + (q % SH::kBlocks) * SH::kBlock;
@@ -391,7 +399,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
           }
         }
       }
-      warp_arrive(raw_free + 8 * at);                  // read: the next copy may come
+      // read: the next copy may come (behind a wait given up the last one may be on its way)
+      if (!late) warp_arrive(raw_free + 8 * at);
       if (!final) {
         float4* out = parts + ((w - (int)(turn & 3) + 3) & 3) * 128 + lane;
 #pragma unroll
@@ -464,8 +473,6 @@ mla_status launch_mass_few(const MassParams& p, cudaStream_t stream) {
   return cuda_status(launch_pdl(mass_few_kernel<LF, KF>, dim3(p.grid), dim3(kFewThreads), FewShape<LF, KF>::kBytes, stream, p));
 }
 
-// Sequences of 16 rows here, others on tcgen05.  Measured, 32 x 32768 tokens INT4
-// at 16 heads: the tcgen05 kernel takes 219 us.
 template <int LF, int KF>
 mla_status launch_mass_pair(const MassParams& p, cudaStream_t stream) {
   if constexpr (LF == MLA_FMT_BF16 || LF == MLA_FMT_INT8_SYM || LF == MLA_FMT_INT4_ASYM || LF == MLA_FMT_INT4_SYM) {

@@ -319,3 +319,41 @@ def test_waits_that_run_out_end_the_call(mla, H, lens):
     assert t.err.item() in (0, mla.DEVERR_TIMEOUT)
     t.err.zero_()
     assert torch.equal(t.go(), want) and t.err.item() == 0
+
+
+@pytest.mark.parametrize("lf,kf,H", [(F_BF16, F_BF16, 16), (F_INT8, F_INT8, 16), (F_INT8, F_BF16, 16), (F_BF16, F_BF16, 32),
+                                     (F_INT4, F_INT8, 32), (F_INT8, F_INT8, 64), (F_INT8, F_BF16, 128)],
+                         ids=lambda f: FMT_NAME.get(f, str(f)))
+def test_hundreds_of_megabytes_of_pages(mla, lf, kf, H):
+    """Long runs of key tiles from memory that no cache holds, ragged ends: copies
+    land late and out of order.  The pages are copies of a few, so that 64 bits are soon
+    done."""
+    one = Batch(mla, [(639, 1)], H, lf, kf, seed=31, spare=0)
+    B, P = 24, 250
+    g = torch.Generator().manual_seed(32)
+    pages = one.cache.pool.view(10, -1)
+    perm, of = torch.randperm(B * P, generator=g).cuda(), torch.randint(0, 10, (B * P,), generator=g).cuda()
+    pool = torch.empty((B * P, pages.shape[1]), dtype=torch.uint8, device="cuda")
+    pool[perm] = pages[one.table[0].long().cuda()[of]]
+    cache = mla.CacheLayer(B * P, lf, kf, pool=pool.view(-1))
+    lens = [P * 64 - 301 * b for b in range(B)]
+    q_lat, q_pe = torch.randn((B, H, 512), generator=g) * 0.5, torch.randn((B, H, 64), generator=g).bfloat16()
+    lse = 6.0 + torch.randn((B, H), generator=g)
+    ws = torch.empty(mla.mla_mass_workspace_bytes(B, B, H, 1), dtype=torch.uint8, device="cuda")
+    args = [x.cuda() for x in (q_lat, q_pe, lse)] + [perm.int().view(B, P), torch.arange(B + 1, dtype=torch.int32, device="cuda"),
+                                                     torch.tensor(lens, dtype=torch.int32, device="cuda"), ws]
+    want = [R.mass(*one.hat[0], q_lat[b:b + 1].double(), q_pe[b:b + 1].double(), lse[b:b + 1].double(), 639, SCALE) for b in range(B)]
+    err, first = torch.zeros(1, dtype=torch.int32, device="cuda"), None
+    for _ in range(12):
+        mass = torch.full((B * P * 64,), 7.0, device="cuda")
+        mla.mla_token_mass(cache, *args, mass, max_new=1, decay=0.0, dev_err=err, softmax_scale=SCALE)
+        first = mass if first is None else first
+        assert torch.equal(mass, first)
+    assert err.item() == 0
+    got = first.view(-1, 64)[perm].view(B, P * 64).double().cpu()
+    src = (64 * of.view(B, P, 1) + torch.arange(64, device="cuda")).flatten(1).cpu()
+    for b in range(B):
+        w, bound = want[b][0][src[b]], want[b][1][src[b]]
+        d = (got[b] - w).abs()[: lens[b]]
+        assert bool((d <= (bound + 2.0 ** -23 * w)[: lens[b]]).all()), (b, float((d / bound[: lens[b]]).max()))
+        assert bool((got[b, lens[b]:] == 7.0).all())
