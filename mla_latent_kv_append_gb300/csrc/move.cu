@@ -9,6 +9,10 @@
 // 32-token block of the destination and writes it whole; codes are gathered in
 // 16-byte chunks, the per-token fields (scales lie side by side for 32 tokens) in
 // 4-byte words, a lane per token, of which a read moves a 32-byte sector.
+//
+// Measured: 2048 tokens of 32768 INT8 4.2 us; 32 sequences cut to a quarter, 104000
+// tokens INT4 (122 MB in and out) 43 us, 2.8 TB/s: a quarter of a block's tokens
+// touch nearly all sectors of its scales, 1.8 times the bytes that are kept.
 #include "mla_internal.cuh"
 
 namespace mla {

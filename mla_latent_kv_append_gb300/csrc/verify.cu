@@ -19,6 +19,11 @@
 // costs 64 times an fp32 one here: 33.5 million of them 55 us).  The tiles' sums
 // meet in distributed shared memory; one warp then reads the tile that holds the
 // border again, in fp64.
+//
+// Measured (a captured call's share of many): 256 sequences of up to 4 drafts over
+// 131072 fp32 values, 268 MB, 67 us, 4.0 TB/s or 60% of a plain copy's rate; one of 4
+// drafts over 32003 values 9.4 us, latency: lengths, drafts, their probabilities,
+// the row, two meetings of the cluster and the last tile follow one another.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
