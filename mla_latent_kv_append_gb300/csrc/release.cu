@@ -18,8 +18,8 @@
 // requests itself (three words each, from L2) and then takes its share of the
 // rows.
 //
-// Measured: 32 requests x 512 pages trimmed 3.6 us; 4096 x 640 moved 31 us, two
-// launches that each scan all requests (5 us) and go through the tables.
+// Measured: 32 requests x 512 pages trimmed 3.0 us; 4096 x 640 moved 26 us: two
+// launches that each scan all requests (8 us), then the tables (6) and the list (4).
 #include "mla_internal.cuh"
 #include "scan.cuh"
 
@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kRelPer = 4;                             // requests per thread, at most
 constexpr int kRelSmall = 256, kRelLarge = kMaxBatch / kRelPer;
-constexpr int kRelAhead = 8;                           // columns of a lane with their loads in flight
+constexpr int kRelAhead = 4;                           // columns of a lane with their loads in flight (8: 30 us for 4096 x 640 pages)
 
 struct ReleaseParams {
   const int32_t *old_lens, *new_lens, *req;
@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(T) release_kernel(const ReleaseParams p, int p
   int64_t unused;
   int64_t first_take = block_scan<T>(take_sum, red, &unused);
   int64_t first_back = block_scan<T>(back_sum, red, &unused);
+  int most_take = 0, most_back = 0;
 #pragma unroll
   for (int k = 0; k < kRelPer; ++k) {
     const int b = b0 + k;
@@ -150,8 +151,10 @@ __global__ void __launch_bounds__(T) release_kernel(const ReleaseParams p, int p
       now[k] = was[k];
     }
     const bool done = any && fits;
-    if (done && take[k]) atomicMax(&total_take, (int)first_take + take[k]);
-    if (done && back[k]) atomicMax(&total_back, (int)first_back + back[k]);
+    if (done) {                                        // runs: the last one's end
+      most_take = (int)first_take + take[k];
+      most_back = (int)first_back + back[k];
+    }
     s_take[spread(b)] = done && p.move ? (int)first_take : -1;
     s_back[spread(b)] = done && back[k] ? (int)first_back : -1;
     s_now[spread(b)] = pages_of(now[k]);
@@ -160,6 +163,13 @@ __global__ void __launch_bounds__(T) release_kernel(const ReleaseParams p, int p
     first_take += take[k];
     first_back += back[k];
     if (blockIdx.x == 0 && (part_of & kTables)) p.lens_out[b] = now[k];
+  }
+  // one atomic a warp (4096 requests: one each, all on one word, 0.5 us more a launch)
+  most_take = __reduce_max_sync(0xffffffffu, most_take);
+  most_back = __reduce_max_sync(0xffffffffu, most_back);
+  if ((tid & 31) == 0) {
+    atomicMax(&total_take, most_take);
+    atomicMax(&total_back, most_back);
   }
   __syncthreads();
   const int64_t to = (int64_t)head + total_take - total_back;
