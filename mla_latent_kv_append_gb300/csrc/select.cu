@@ -128,26 +128,23 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
   }
   // f(token, its key) for all of the run, 32 tokens at a time, every lane
   auto each = [&](auto f) {
-    if constexpr (HELD > 0) {
-#pragma unroll
-      for (int i = 0; i < HELD; ++i)
-        if (w0 + 32 * i < w1) f(w0 + 32 * i + lane, held[i]);
-    } else {
-      for (int base = w0; base < w1; base += 32) {
-        const int t = base + lane;
-        f(t, t >= w1 ? 0u : (t - t0 < p.keys ? s_keys[t - t0] : weight(__ldcg(table + t / kPage), t)));
-      }
+    for (int base = w0; base < w1; base += 32) {
+      const int t = base + lane;
+      f(t, t >= w1 ? 0u : (t - t0 < p.keys ? s_keys[t - t0] : weight(__ldcg(table + t / kPage), t)));
     }
   };
 
-  // bit i: the thread's i-th token competes
-  uint32_t competes = 0u;
+  // With the weights in registers, bit i of a word stands for the thread's i-th
+  // token, w0 + 32 i + lane: those that compete, and the others, which stay.  (Token
+  // by token, bounds and all, 64 ragged sequences took 40 us.)
+  uint32_t competes = 0u, stays = 0u;
   if constexpr (HELD > 0) {
-#pragma unroll
-    for (int i = 0; i < HELD; ++i) {
-      const int t = w0 + 32 * i + lane;
-      if (t >= m0 && t < min(m1, w1)) competes |= 1u << i;
-    }
+    auto before = [&](int t) {                         // the thread's tokens before t
+      const int n = (t - w0 - lane + 31) >> 5;
+      return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u);
+    };
+    competes = before(min(m1, w1)) & ~before(m0);
+    stays = before(w1) & ~competes;
   }
   uint32_t prefix = 0u, mask = 0u;
   int need = want;                                     // how many stay among the keys that share the prefix
@@ -158,18 +155,27 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
     if (pass == 0) __syncthreads();                    // the bins are clear
     // a shared-memory address: through a generic one an addition takes many times as long
     const uint32_t bins = (uint32_t)__cvta_generic_to_shared(pass == 0 ? copies + (lane % kSelCopies) * kSelPitch : ex.bins[pass]);
-    // a warp's weights of 0 count at once
+    // a warp's weights of 0 count at once, where there can be any
     constexpr uint32_t kZero = 0x80000000u;
+    const bool zero_too = (kZero & mask) == prefix;
     auto add = [](uint32_t at, uint32_t n) { asm volatile("red.shared.add.u32 [%0], %1;\n" ::"r"(at), "r"(n) : "memory"); };
     auto count = [&](bool in, uint32_t k) {
-      const uint32_t zeros = __ballot_sync(0xffffffffu, in && k == kZero);
-      if (in && k != kZero) add(bins + 4 * ((k >> shift) & digits), 1u);
-      if (zeros && lane == 0) add(bins + 4 * ((kZero >> shift) & digits), (uint32_t)__popc(zeros));
+      if (zero_too) {
+        const uint32_t zeros = __ballot_sync(0xffffffffu, in && k == kZero);
+        if (zeros && lane == 0) add(bins + 4 * ((kZero >> shift) & digits), (uint32_t)__popc(zeros));
+        in = in && k != kZero;
+      }
+      if (in) add(bins + 4 * ((k >> shift) & digits), 1u);
     };
     if constexpr (HELD > 0) {
+      uint32_t in = 0u;
+#pragma unroll
+      for (int i = 0; i < HELD; ++i) in |= (held[i] & mask) == prefix ? 1u << i : 0u;
+      in &= competes;
+      const uint32_t any = __reduce_or_sync(0xffffffffu, in);
 #pragma unroll
       for (int i = 0; i < HELD; ++i)
-        if (w0 + 32 * i < w1) count((competes >> i & 1u) && (held[i] & mask) == prefix, held[i]);
+        if (any >> i & 1u) count(in >> i & 1u, held[i]);
     } else {
       each([&](int t, uint32_t k) { count(t >= m0 && t < min(m1, w1) && (k & mask) == prefix, k); });
     }
@@ -219,11 +225,12 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
   if constexpr (HELD > 0) {
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-      bool more, same;
-      classes(w0 + 32 * i + lane, held[i], more, same);
-      mores |= more ? 1u << i : 0u;
-      sames |= same ? 1u << i : 0u;
+      mores |= held[i] > prefix ? 1u << i : 0u;
+      sames |= held[i] == prefix ? 1u << i : 0u;
     }
+    if (want == 0) mores = sames = 0u;
+    mores = (mores & competes) | stays;
+    sames &= competes;
     n_more = __reduce_add_sync(0xffffffffu, __popc(mores));
     n_same = __reduce_add_sync(0xffffffffu, __popc(sames));
   } else {
@@ -260,23 +267,35 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
     before_more += __reduce_add_sync(0xffffffffu, va);
     before_same += __reduce_add_sync(0xffffffffu, ve);
   }
-  auto list = [&](int t, bool more, bool same) {
-    const uint32_t bm = __ballot_sync(0xffffffffu, more), bs = __ballot_sync(0xffffffffu, same);
-    if (!(bm | bs)) return;
-    const uint32_t below = (1u << lane) - 1u;
-    const int ties = before_same + __popc(bs & below);               // equals before this one
-    if (more || (same && ties < need)) kept[before_more + __popc(bm & below) + min(ties, need)] = t;
-    before_more += __popc(bm);
-    before_same += __popc(bs);
-  };
+  const uint32_t below = (1u << lane) - 1u;
   if constexpr (HELD > 0) {
+    int at = before_more + min(before_same, need);     // the warp's first place
+    if (n_same > 0 && before_same < need) {            // the first equals stay as well
 #pragma unroll
-    for (int i = 0; i < HELD; ++i) list(w0 + 32 * i + lane, mores >> i & 1u, sames >> i & 1u);
+      for (int i = 0; i < HELD; ++i) {
+        const bool same = sames >> i & 1u;
+        const uint32_t bs = __ballot_sync(0xffffffffu, same);
+        if (same && before_same + __popc(bs & below) < need) mores |= 1u << i;
+        before_same += __popc(bs);
+      }
+    }
+    const uint32_t any = __reduce_or_sync(0xffffffffu, mores);
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      if (!(any >> i & 1u)) continue;
+      const uint32_t b = __ballot_sync(0xffffffffu, mores >> i & 1u);
+      if (mores >> i & 1u) kept[at + __popc(b & below)] = w0 + 32 * i + lane;
+      at += __popc(b);
+    }
   } else {
     each([&](int t, uint32_t k) {
       bool more, same;
       classes(t, k, more, same);
-      list(t, more, same);
+      const uint32_t bm = __ballot_sync(0xffffffffu, more), bs = __ballot_sync(0xffffffffu, same);
+      const int ties = before_same + __popc(bs & below);             // equals before this one
+      if (more || (same && ties < need)) kept[before_more + __popc(bm & below) + min(ties, need)] = t;
+      before_more += __popc(bm);
+      before_same += __popc(bs);
     });
   }
   for (int64_t i = K + (int64_t)rank * kSelThreads + tid; i < p.max_keep; i += CL * kSelThreads) kept[i] = -1;
