@@ -13,9 +13,10 @@
 // blocks' counts meet in distributed shared memory.  Many tokens have equal
 // weights (never looked at: 0), so a warp adds those up before it counts them.
 //
-// Measured: one sequence of 32768 tokens cut to 2048 16 us, of which the three
+// Measured: one sequence of 32768 tokens cut to 2048 15 us, of which the three
 // passes' meetings of the cluster and their reads of the others' counts take 8; 64 of
-// 2000 to 65536 tokens, cut to a quarter, 40 us.
+// 2000 to 65536 tokens, cut to a quarter, 31 us, of which the first pass's additions to
+// shared memory take 10.
 #include <cooperative_groups.h>
 
 #include "mla_internal.cuh"
@@ -110,13 +111,18 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
   };
   uint32_t held[HELD ? HELD : 1];
   if constexpr (HELD > 0) {
-    // lane i: the page of the run's i-th 32 tokens
-    const int mine = w0 + 32 * lane < w1 ? __ldcg(table + (w0 + 32 * lane) / kPage) : 0;
-    if (mine < 0 || mine >= p.num_pages) set_err(p.dev_err, MLA_DEVERR_PAGE);
+    // lane i: where the weights of the run's i-th 32 tokens begin (they lie in one
+    // page), -1: nowhere
+    int mine = -1;
+    if (w0 + 32 * lane < w1) {
+      const int page = __ldcg(table + (w0 + 32 * lane) / kPage);
+      if (page < 0 || page >= p.num_pages) set_err(p.dev_err, MLA_DEVERR_PAGE);
+      else mine = page * kPage + (w0 + 32 * lane) % kPage;
+    }
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-      const int t = w0 + 32 * i + lane, page = __shfl_sync(0xffffffffu, mine, i);
-      held[i] = t < w1 ? weight(page, t) : 0u;
+      const int at = __shfl_sync(0xffffffffu, mine, i);
+      held[i] = at >= 0 && 32 * i + lane < w1 - w0 ? order_key(__ldcg(p.mass + at + lane)) : 0u;
     }
   } else {
     for (int t = t0 + tid; t < t1; t += kSelThreads) {
@@ -136,7 +142,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
 
   // With the weights in registers, bit i of a word stands for the thread's i-th
   // token, w0 + 32 i + lane: those that compete, and the others, which stay.  (Token
-  // by token, bounds and all, 64 ragged sequences took 40 us.)
+  // by token, bounds and all, the 64 ragged sequences took 6 us more.)
   uint32_t competes = 0u, stays = 0u;
   if constexpr (HELD > 0) {
     auto before = [&](int t) {                         // the thread's tokens before t
