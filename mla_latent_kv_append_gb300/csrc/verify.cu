@@ -324,8 +324,9 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
 template <typename T>
 mla_status launch_verify(const VerifyParams& p, cudaStream_t stream) {
   // Blocks of a sequence: 8 where there are few sequences, so that their rows
-  // spread over the SMs; with many, no more blocks than run side by side (256
-  // sequences of 131072 fp32 values: 108 us with 8, which come in four waves).
+  // spread over the SMs; with many, no more blocks than run side by side, four to an
+  // SM (256 sequences of 131072 fp32 values: 94 us with 1, 67 with 2, 82 with 4, 108
+  // with 8, which come in four waves; three blocks to an SM 87, five 84).
   const int sms = device_sm_count();
   int CL = 8;
   while (CL > 1 && (int64_t)p.B * CL > 4 * (int64_t)sms) CL /= 2;
