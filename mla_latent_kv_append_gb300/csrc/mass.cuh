@@ -110,11 +110,12 @@ struct MassShape {
   // An accumulation in TMEM cuts the sum to 24 bits, towards 0: it loses half a last
   // place on average, 4.3e-8 of a sum whose mantissa is spread as in nature.  A large
   // score grows to its value on a nearly straight way, so that n accumulations take
-  // n 4.3e-8 0.45 of it; given back here, what is left of the error is a fifth (512
-  // queries over 6000 tokens: 4e-6 of the masses before, 0.6 to 1.3e-6 after; an
-  // emulation of the sums gives the same).  (The small products in columns of their
-  // own would leave 36 accumulations, 2e-7, and take 7 to 12% longer.)
-  static constexpr float kUngain = kMassUngain * (1.f + 4.3e-8f * 0.45f * (LF == MLA_FMT_BF16 ? 72 : 108));
+  // less than half of n 4.3e-8 of it; 0.39 is given back here, which leaves a sixth of the
+  // error (512 queries over 6000 tokens, eight draws: 4e-6 of the masses before, 0.3
+  // to 1.0e-6 after; with 0.45 0.6 to 1.6e-6, with 0.33 0.45 to 1.3e-6).  (The small
+  // products in columns of their own would leave 36 accumulations, 2e-7, and take 7 to
+  // 12% longer; ahead of the large ones they change little.)
+  static constexpr float kUngain = kMassUngain * (1.f + 4.3e-8f * 0.39f * (LF == MLA_FMT_BF16 ? 72 : 108));
   // A bulk copy costs 85 ns of the copy engine besides its bytes, and a block of
   // 4-bit codes is 18 KB: whole pages of those (a stream of nothing but copies:
   // 18.5 KB each 5.6 TB/s, 23.7 KB 7.0, 37 KB 6.9).
