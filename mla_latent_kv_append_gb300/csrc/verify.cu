@@ -29,6 +29,7 @@
 #include <cuda_fp16.h>
 
 #include "mla_internal.cuh"
+#include "tc.cuh"
 
 namespace mla {
 namespace {
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
   for (int attempt = 0; attempt < 2; ++attempt) {
     for (int t = rank + CL * warp; t < tiles; t += CL * kVerWarps) {
       float h[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};      // two chains of additions side by side
+      float top = 0.f;                                 // the draft's largest entry
       const int e0 = t * kVerTile - mis + lane * N, first = t * kVerTile - mis;
       auto add = [&](const float* a, const float* c, int e) {
 #pragma unroll
@@ -191,6 +193,8 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
             widen<T, N>(ra[s], a);
             if (qr) {
               widen<T, N>(rc[s], c);
+#pragma unroll
+              for (int i = 0; i < N; i += 2) top = tc::max3(top, c[i], c[i + 1]);
               add(a, c, e);
             } else {
               add(a, nullptr, e);
@@ -207,8 +211,9 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
           if (qr) load_row<T, N>(qr, at, p.vocab, c);
           add(a, qr ? c : nullptr, at);
         }
-        // an infinite entry (which has no weight) has spoilt a sum
-        careful = __any_sync(0xffffffffu, !(h[0] + h[1] < INFINITY));
+        // an infinite entry (which has no weight) has spoilt a sum, or, the draft's,
+        // has taken a finite one of the target away
+        careful = __any_sync(0xffffffffu, !(h[0] + h[1] < INFINITY) || top == INFINITY);
         if (careful) h[0] = h[1] = l[0] = l[1] = 0.f;
       }
       if (careful) {
