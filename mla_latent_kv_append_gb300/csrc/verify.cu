@@ -9,7 +9,8 @@
 //   smallest v with sum of w up to v > u total(w).
 // The product and the subtraction round nothing (below), and the sums are good to
 // 2^-40: a border between two tokens is 1 / vocab wide, and an fp32 sum would
-// pick a neighbour now and then.
+// pick a neighbour now and then.  Rows need not be probabilities: where a sum passes
+// fp32's range it is made in fp64.
 //
 // What bounds it: reading row j of p and q once (a megabyte for 131072 fp32
 // probabilities); one sequence is latency.  A cluster of blocks shares a
@@ -91,6 +92,19 @@ __device__ __forceinline__ void two_sum(float& h, float& l, float w) {
   const float s = __fadd_rn(h, w), b = __fadd_rn(s, -h);
   l = __fadd_rn(l, __fadd_rn(__fadd_rn(h, -__fadd_rn(s, -b)), __fadd_rn(w, -b)));
   h = s;
+}
+
+// A lane's sum over a tile in fp64, value by value: what lies beside the loop over
+// the tiles must be short and need few registers.
+template <typename T>
+__device__ __forceinline__ double wide_sum(const T* pr, const T* qr, int first, int vocab, int skip) {
+  double sum = 0.0;
+#pragma unroll 1
+  for (int e = max(first, 0) + (int)(threadIdx.x & 31); e < min(first + kVerTile, vocab); e += 32) {
+    const float a = e == skip ? 0.f : positive(to_f(pr[e]));
+    sum += (double)a - (double)fminf(a, qr ? positive(to_f(qr[e])) : 0.f);
+  }
+  return sum;
 }
 
 template <typename T>
@@ -227,6 +241,8 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
         }
       }
       double sum = ((double)h[0] + (double)l[0]) + ((double)h[1] + (double)l[1]);
+      // finite entries whose sum no fp32 holds
+      if (careful && __any_sync(0xffffffffu, !(h[0] + h[1] < INFINITY))) sum = wide_sum<T>(pr, qr, first, p.vocab, skip);
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane == 0) s_sums[t / CL] = sum;
