@@ -71,7 +71,7 @@ constexpr int kAbN = 64;             // columns per CTA
 constexpr int kAbWS = kAbN + 8;      // W tile row stride (bf16): 144 B
 constexpr int kAbAS = kDn + 8;       // A tile row stride (bf16): 272 B
 
-__global__ void __launch_bounds__(128) q_absorb_kernel(const uint16_t* __restrict__ q_nope,
+__global__ void __launch_bounds__(128) q_absorb_kernel(const uint16_t* q_nope,
                                                        const uint16_t* __restrict__ w_uk,
                                                        float* __restrict__ q_lat, int B, int H) {
   pdl_launch_dependents();
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(128) q_absorb_kernel(const uint16_t* __restric
 constexpr int kUnN = 16;             // columns per CTA
 constexpr int kUnWS = kUnN + 8;      // W tile row stride (bf16): 48 B, conflict-free ldmatrix
 
-__global__ void __launch_bounds__(128) out_unabsorb_kernel(const float* __restrict__ o_lat,
+__global__ void __launch_bounds__(128) out_unabsorb_kernel(const float* o_lat,
                                                            const uint16_t* __restrict__ w_uv,
                                                            float* __restrict__ o, int B, int H) {
   pdl_launch_dependents();
@@ -218,7 +218,7 @@ constexpr int kBigUnSmem = kDc * kBigUnWS * 2;                     // 139,264 B
 
 // q_lat tile: 16 rows x 128 columns (quarter cq of 512) per warp unit; the
 // A fragments (bf16 pairs of q_nope) come straight from global memory.
-__global__ void __launch_bounds__(kBigThreads, 1) q_absorb_big_kernel(const uint16_t* __restrict__ q_nope,
+__global__ void __launch_bounds__(kBigThreads, 1) q_absorb_big_kernel(const uint16_t* q_nope,
                                                                       const uint16_t* __restrict__ w_uk,
                                                                       float* __restrict__ q_lat, int B, int H) {
   extern __shared__ __align__(16) uint16_t big_ws[];
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) q_absorb_big_kernel(const uint
 // o tile: 16 rows x all 128 columns per warp unit, K = 512 in 32 steps; the
 // fp32 A fragments come from global memory one step ahead and are split
 // into three bf16 pieces once.
-__global__ void __launch_bounds__(kBigThreads, 1) out_unabsorb_big_kernel(const float* __restrict__ o_lat,
+__global__ void __launch_bounds__(kBigThreads, 1) out_unabsorb_big_kernel(const float* o_lat,
                                                                           const uint16_t* __restrict__ w_uv,
                                                                           float* __restrict__ o, int B, int H) {
   extern __shared__ __align__(16) uint16_t big_ws[];
@@ -400,7 +400,7 @@ static mla_status allow_big_smem(K kernel, int bytes, int* configured) {
   return st;
 }
 
-mla_status launch_q_absorb(const uint16_t* q_nope, const uint16_t* w_uk, float* q_lat, int B, int H,
+mla_status launch_q_absorb(const uint16_t* q_nope, const uint16_t* w_uk, float* __restrict__ q_lat, int B, int H,
                            cudaStream_t stream) {
   if (B >= kBigB) {
     static int configured[64] = {0};
@@ -414,7 +414,7 @@ mla_status launch_q_absorb(const uint16_t* q_nope, const uint16_t* w_uk, float* 
                                 w_uk, q_lat, B, H));
 }
 
-mla_status launch_out_unabsorb(const float* o_lat, const uint16_t* w_uv, float* o, int B, int H,
+mla_status launch_out_unabsorb(const float* o_lat, const uint16_t* w_uv, float* __restrict__ o, int B, int H,
                                cudaStream_t stream) {
   if (B >= kBigB) {
     static int configured[64] = {0};

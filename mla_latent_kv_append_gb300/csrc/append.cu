@@ -128,9 +128,9 @@ __device__ __forceinline__ void quant_asym4(const float* x, float& s_out, float&
 
 template <int LF, int KF>
 __global__ void __launch_bounds__(256) append_kernel(uint8_t* __restrict__ pool, PageLayout L, OutlierSet outl,
-                                                     int64_t num_slots, const uint16_t* __restrict__ c_new,
-                                                     const uint16_t* __restrict__ kpe_new,
-                                                     const int32_t* __restrict__ slot, int n,
+                                                     int64_t num_slots, const uint16_t* c_new,
+                                                     const uint16_t* kpe_new,
+                                                     const int32_t* slot, int n,
                                                      int32_t* dev_err) {
   pdl_launch_dependents();
   pdl_wait();
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(256) append_kernel(uint8_t* __restrict__ pool,
 // is one coalesced sweep), ranks it against the other 511 (larger maxima
 // first, ties to the lower index) and, when it ranks below 25, writes c at
 // its position among the selected channels in increasing order.
-__global__ void __launch_bounds__(kDc) select_outliers_kernel(const uint16_t* __restrict__ c, int n,
+__global__ void __launch_bounds__(kDc) select_outliers_kernel(const uint16_t* c, int n,
                                                               int32_t* __restrict__ out) {
   pdl_launch_dependents();
   pdl_wait();

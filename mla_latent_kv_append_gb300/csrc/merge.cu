@@ -45,8 +45,8 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 }
 
 // grid (B, H), block 128
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const float* __restrict__ o_parts,
-                                                              const float* __restrict__ lse_parts, int R, int B,
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const float* o_parts,
+                                                              const float* lse_parts, int R, int B,
                                                               int H, float* __restrict__ o_lat,
                                                               float* __restrict__ lse) {
   pdl_launch_dependents();

@@ -462,8 +462,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const TcParam
           rs += pv[k];
         }
         if (p.risk) {
-          const float4 ma = __ldg(reinterpret_cast<const float4*>(p.mt + kpos0 + 8 * c8));
-          const float4 mb = __ldg(reinterpret_cast<const float4*>(p.mt + kpos0 + 8 * c8 + 4));
+          // the expansion's, of the kernel before: no non-coherent load
+          const float4 ma = *reinterpret_cast<const float4*>(p.mt + kpos0 + 8 * c8);
+          const float4 mb = *reinterpret_cast<const float4*>(p.mt + kpos0 + 8 * c8 + 4);
           const float mv[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
 #pragma unroll
           for (int k = 0; k < 8; ++k) {

@@ -66,11 +66,13 @@ __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 __device__ __forceinline__ float positive(float x) { return x > 0.f && x < INFINITY ? x : 0.f; }
 
 // Elements e .. e + N - 1 of a row (N fill 16 bytes), 0 outside [0, vocab):
-// one 16-byte load where they are all inside and aligned.
+// one 16-byte load where they are all inside and aligned.  (The rows may come from a
+// kernel that still runs when this one starts: no non-coherent loads, though they
+// would take 0.5% less.)
 template <typename T, int N>
 __device__ __forceinline__ void load_row(const T* row, int e, int vocab, float* v) {
   if (e >= 0 && e + N <= vocab && (reinterpret_cast<uintptr_t>(row + e) & 15) == 0) {
-    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(row + e));
+    const uint4 raw = __ldcg(reinterpret_cast<const uint4*>(row + e));
     const T* x = reinterpret_cast<const T*>(&raw);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = positive(to_f(x[i]));
@@ -191,13 +193,13 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
 #pragma unroll
           for (int s = 0; s < kBatch; ++s) {
             const int e = e0 + (s0 + s) * 32 * N;
-            ra[s] = e >= 0 && e + N <= p.vocab ? __ldg(reinterpret_cast<const uint4*>(pr + e)) : zero;
+            ra[s] = e >= 0 && e + N <= p.vocab ? __ldcg(reinterpret_cast<const uint4*>(pr + e)) : zero;
           }
           if (qr) {
 #pragma unroll
             for (int s = 0; s < kBatch; ++s) {
               const int e = e0 + (s0 + s) * 32 * N;
-              rc[s] = e >= 0 && e + N <= p.vocab ? __ldg(reinterpret_cast<const uint4*>(qr + e)) : zero;
+              rc[s] = e >= 0 && e + N <= p.vocab ? __ldcg(reinterpret_cast<const uint4*>(qr + e)) : zero;
             }
           }
 #pragma unroll
