@@ -707,8 +707,12 @@ mla_status mla_verify_drafts(const void* target_probs, int64_t target_row_stride
  *   decreases or leaves [0, n_tokens].  Sequences without queries are left
  *   alone.  Sequences of a call must not share pages.
  *   Precision: queries and cached values as two fp16 halves (22 bits), products
- *   summed in fp32 by the tensor cores, exponentials and masses in fp32: about
- *   1e-6 of the masses.  A cached value beyond 4094 in magnitude, or a query
+ *   summed by the tensor cores, which cut a running sum off at 24 bits (what that
+ *   takes on average is given back), exponentials and masses in fp32.  A weight
+ *   is off by its score's error: 1e-6 of it for scores of a nat or so, and in
+ *   proportion to larger ones, on average within 5e-7 of the score (1.2e-6 of it for
+ *   one query of 16 heads over bf16), single weights within 2^-16 of the sum of
+ *   the score's |products|.  A cached value beyond 4094 in magnitude, or a query
  *   beyond 2047 after the scale and log2 e, may count as non-finite: its token's
  *   mass, or that of all tokens the query sees, is then not finite.  A cached
  *   value below 2^-7 is off by up to 2^-29.

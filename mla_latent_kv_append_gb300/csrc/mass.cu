@@ -9,8 +9,9 @@
 namespace mla {
 namespace {
 
-constexpr int kPrepThreads = 512, kPrepPer = kMaxBatch / kPrepThreads;
 constexpr int kPieces = (kDc + kDr) / 8;               // of 8 channels per row
+constexpr int kPrepRows = 4, kPrepThreads = kPrepRows * kPieces;     // a thread per piece
+static_assert(kPrepThreads % 32 == 0 && kPrepRows <= kPrepThreads / 32, "whole warps, a warp for each row's sequence");
 
 // Block 0: which sequences take part, and where their units begin.
 __device__ void plan_mass(const MassParams& p) {
@@ -77,10 +78,38 @@ __device__ void plan_mass(const MassParams& p) {
   }
 }
 
+// All lanes of a warp: the sequence that row r belongs to, and the rows of its row
+// block there.  Any q_start: a batch that does not fit is refused by the plan.
+__device__ __forceinline__ int rows_beside(const MassParams& p, int r) {
+  const int lane = threadIdx.x & 31, token = (int)((uint32_t)r / (uint32_t)p.H);
+  int a = 0, n = p.B;                                  // the answer is in [a, a + n)
+  for (;;) {
+    const int step = (n + 31) / 32, at = a + lane * step;
+    const bool in = at < a + n;
+    const int lo = in ? __ldcg(p.q_start + at) : 0, next = in ? __ldcg(p.q_start + at + 1) : 0;
+    const int c = max(__popc(__ballot_sync(0xffffffffu, in && lo <= token)), 1);
+    if (step == 1) {
+      const int r0 = __shfl_sync(0xffffffffu, lo, c - 1), n_q = __shfl_sync(0xffffffffu, next, c - 1) - r0;
+      return min(p.R, n_q * p.H - ((r - r0 * p.H) & -p.R));           // R is a power of two
+    }
+    const int na = a + (c - 1) * step;
+    n = min(step, a + n - na);
+    a = na;
+  }
+}
+
 // The queries times the softmax scale, log2 e and kQueryGain, as two halves:
 // piece kb of 64 channels, all rows of it side by side, in the 128-byte swizzle.
-// A row whose lse is not finite is 0 (it adds nothing).
+// A row whose lse is not finite is 0 (it adds nothing).  8 rows a block.
+//
+// What the MMAs' accumulations cut off on average (kMassCut) is given back here: a
+// channel's part of a score is cut at every accumulation from its own K-step's on, so
+// it is multiplied by 1 + kMassCut times their number.  That holds for scores that
+// come from any channels: the mean of what is cut off is linear in them.  K-steps where
+// the row's query is 0 are not counted.
 __global__ void __launch_bounds__(kPrepThreads) mass_prep_kernel(const MassParams p) {
+  __shared__ uint32_t s_any[2][kPrepThreads / 32 + 2];               // the pieces that are not 0, bit by bit
+  __shared__ bool s_apart[2][kPrepRows];
   pdl_launch_dependents();
   pdl_wait();
   if (blockIdx.x == 0) {
@@ -88,32 +117,74 @@ __global__ void __launch_bounds__(kPrepThreads) mass_prep_kernel(const MassParam
     return;
   }
   const float gain = p.scale_log2 * kQueryGain;
-  for (int64_t i = (int64_t)(blockIdx.x - 1) * kPrepThreads + threadIdx.x; i < p.rows * kPieces;
-       i += (int64_t)(gridDim.x - 1) * kPrepThreads) {
-    const int64_t r = i / kPieces;
-    const int c = (int)(i - r * kPieces);
-    float v[8];
-    if (c < kDc / 8) {
-      const float4* src = reinterpret_cast<const float4*>(p.q_lat + r * kDc) + 2 * c;
-      *reinterpret_cast<float4*>(v) = __ldcg(src);
-      *reinterpret_cast<float4*>(v + 4) = __ldcg(src + 1);
-    } else {
-      const uint4 w = __ldcg(reinterpret_cast<const uint4*>(p.q_pe + r * kDr) + (c - kDc / 8));
-      v[0] = bf16lo(w.x), v[1] = bf16hi(w.x), v[2] = bf16lo(w.y), v[3] = bf16hi(w.y);
-      v[4] = bf16lo(w.z), v[5] = bf16hi(w.z), v[6] = bf16lo(w.w), v[7] = bf16hi(w.w);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int mine = threadIdx.x / kPieces, c = threadIdx.x - mine * kPieces;
+  int turn = 0;
+  for (int64_t row0 = (int64_t)(blockIdx.x - 1) * kPrepRows; row0 < p.rows; row0 += (int64_t)(gridDim.x - 1) * kPrepRows, turn ^= 1) {
+    const int64_t r = row0 + mine;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    bool live = false;
+    if (r < p.rows) {
+      live = fabsf(__ldcg(p.lse + r)) < INFINITY;
+      if (c < kDc / 8) {
+        const float4* src = reinterpret_cast<const float4*>(p.q_lat + r * kDc) + 2 * c;
+        *reinterpret_cast<float4*>(v) = __ldcg(src);
+        *reinterpret_cast<float4*>(v + 4) = __ldcg(src + 1);
+      } else {
+        const uint4 w = __ldcg(reinterpret_cast<const uint4*>(p.q_pe + r * kDr) + (c - kDc / 8));
+        v[0] = bf16lo(w.x), v[1] = bf16hi(w.x), v[2] = bf16lo(w.y), v[3] = bf16hi(w.y);
+        v[4] = bf16lo(w.z), v[5] = bf16hi(w.z), v[6] = bf16lo(w.w), v[7] = bf16hi(w.w);
+      }
     }
-    const bool live = fabsf(__ldcg(p.lse + r)) < INFINITY;
+    // whether the low halves' products have columns of their own: always up to 32 rows a pass
+    if (warp < kPrepRows && p.R > 32) {
+      const bool apart = 2 * rows_beside(p, (int)min(row0 + warp, p.rows - 1)) <= mass_columns(p.R);
+      if (lane == 0) s_apart[turn][warp] = apart;
+    }
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      v[k] = live ? v[k] * gain : 0.f;
+      any |= v[k] != 0.f;
+    }
+    const uint32_t some = __ballot_sync(0xffffffffu, any);
+    if (lane == 0) s_any[turn][warp] = some;
+    __syncthreads();
+    if (r >= p.rows) continue;                         // the next turn writes the other arrays: one barrier is enough
+    // K-steps of 16 channels that are not 0, 32 of the latent and 4 of the RoPE part; bit
+    // 2 s: step s (a row's bits begin at an even one)
+    const uint32_t* word = s_any[turn] + mine * kPieces / 32;
+    const int shift = mine * kPieces % 32;
+    uint32_t steps[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const uint32_t bits = __funnelshift_r(word[i], word[i + 1], shift);
+      steps[i] = (bits | bits >> 1) & 0x55555555u;
+    }
+    steps[2] &= 0xFFu;
+    const bool apart = p.R <= 32 || s_apart[turn][mine];
+    const int lat = 1 + !apart + p.split_lat, kpe = 1 + !apart + p.split_kpe;      // MMAs of a K-step on the scores' columns
+    // The MMAs of 64 channels (4 K-steps, 8 bits) follow one another by product: high
+    // halves first, from the channel's own step on; then the others, all four steps;
+    // then the 64-channel pieces behind.
+    const int i = c >> 5, at = c & 30, block = c & 24, m = i < 2 ? lat : kpe;
+    const uint32_t own = i == 0 ? steps[0] : (i == 1 ? steps[1] : steps[2]);
+    const uint32_t here = own & (0xFFu << block), behind = block == 24 ? 0u : own & (0xFFFFFFFFu << (block + 8));
+    int cuts = __popc(here & (0xFFFFFFFFu << at)) + (m - 1) * __popc(here) + m * __popc(behind);
+    if (i == 0) cuts += lat * __popc(steps[1]);
+    if (i < 2) cuts += kpe * __popc(steps[2]);
+    const float back = kMassCut * (float)cuts;
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float a = live ? v[2 * k] * gain : 0.f, b = live ? v[2 * k + 1] * gain : 0.f;
+      const float a = fmaf(v[2 * k], back, v[2 * k]), b = fmaf(v[2 * k + 1], back, v[2 * k + 1]);
       const __half2 h = __floats2half2_rn(a, b), l = __floats2half2_rn(a - __low2float(h), b - __high2float(h));
       hi[k] = *reinterpret_cast<const uint32_t*>(&h);
       lo[k] = *reinterpret_cast<const uint32_t*>(&l);
     }
-    uint8_t* at = p.q_tiles + ((int64_t)(c / 8) * p.rows + r) * 128 + (((c & 7) ^ (int)(r & 7)) << 4);
-    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(at + (int64_t)9 * p.rows * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    uint8_t* dst = p.q_tiles + ((int64_t)(c / 8) * p.rows + r) * 128 + (((c & 7) ^ (int)(r & 7)) << 4);
+    *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(dst + (int64_t)9 * p.rows * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
 
@@ -201,8 +272,10 @@ extern "C" mla_status mla_token_mass(const mla_cache_layer* cache, const float* 
                          cache->latent_fmt == MLA_FMT_INT4_ASYM || cache->latent_fmt == MLA_FMT_INT4_SYM);
   // the unit that the kernels copy at a time (FewShape::kBlocks), or a tile of theirs
   p.unit_tokens = p.few ? (p.L.block_bytes < 20000 ? kPage : kBlockTokens) : kMassKeys;
+  p.split_lat = cache->latent_fmt != MLA_FMT_BF16;
+  p.split_kpe = cache->kpe_fmt != MLA_FMT_BF16;
   // the few rows' kernel makes its queries' fragments itself: the plan alone
-  const int64_t want = p.few ? 1 : 1 + (p.rows * kPieces + kPrepThreads - 1) / kPrepThreads;
+  const int64_t want = p.few ? 1 : 1 + (p.rows + kPrepRows - 1) / kPrepRows;
   const mla_status st = cuda_status(launch_pdl(mass_prep_kernel, dim3((unsigned)(want < 4 * p.grid ? want : 4 * p.grid)),
                                                dim3(kPrepThreads), 0, (cudaStream_t)stream, p));
   if (st != MLA_OK) return st;

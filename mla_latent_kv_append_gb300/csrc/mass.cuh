@@ -107,15 +107,6 @@ __device__ __forceinline__ void load_split(uint32_t row, uint32_t scale, uint32_
 template <int LF, int KF>
 struct MassShape {
   static constexpr int kBlock = BlockAt<LF, KF>::kBytes;
-  // An accumulation in TMEM cuts the sum to 24 bits, towards 0: it loses half a last
-  // place on average, 4.3e-8 of a sum whose mantissa is spread as in nature.  A large
-  // score grows to its value on a nearly straight way, so that n accumulations take
-  // less than half of n 4.3e-8 of it; 0.39 is given back here, which leaves a sixth of the
-  // error (512 queries over 6000 tokens, eight draws: 4e-6 of the masses before, 0.3
-  // to 1.0e-6 after; with 0.45 0.6 to 1.6e-6, with 0.33 0.45 to 1.3e-6).  (The small
-  // products in columns of their own would leave 36 accumulations, 2e-7, and take 7 to
-  // 12% longer; ahead of the large ones they change little.)
-  static constexpr float kUngain = kMassUngain * (1.f + 4.3e-8f * 0.39f * (LF == MLA_FMT_BF16 ? 72 : 108));
   // A bulk copy costs 85 ns of the copy engine besides its bytes, and a block of
   // 4-bit codes is 18 KB: whole pages of those (a stream of nothing but copies:
   // 18.5 KB each 5.6 TB/s, 23.7 KB 7.0, 37 KB 6.9).
@@ -400,7 +391,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
   // TMEM: two buffers of scores, then pieces of PU units.  Up to 64 rows the MMAs
   // of 64 channels take less time (256 cycles) than their thread takes for a
   // piece besides (370), so a piece has 192 channels.
-  const int d_cols = R <= 64 ? 64 : kMassMaxRows, PU = R <= 64 ? 6 : 2, cols = COLS / 2 * PU, NA = min(8, (512 - 2 * d_cols) / cols);
+  const int d_cols = mass_columns(R), PU = R <= 64 ? 6 : 2, cols = COLS / 2 * PU, NA = min(8, (512 - 2 * d_cols) / cols);
   const int pieces = kMassUnits / PU;
   const uint32_t sb = smem_u32(sm), s_raw = QS * R * 256, bars = sb + s_raw + NS * SH::kCopy;
   uint8_t* words = sm + s_raw + NS * SH::kCopy + 8 * mCount;
@@ -592,12 +583,12 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const MassParams 
         }
         if (plain) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) sum[c & 3] += ex2(fmaf(__uint_as_float(r[c]), SH::kUngain, s_lse[c0 + c]));
+          for (int c = 0; c < 16; ++c) sum[c & 3] += ex2(fmaf(__uint_as_float(r[c]), kMassUngain, s_lse[c0 + c]));
         } else {
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             const float y = s_lse[c0 + c];
-            const float w = ex2(fmaf(__uint_as_float(r[c]), SH::kUngain, y));
+            const float w = ex2(fmaf(__uint_as_float(r[c]), kMassUngain, y));
             sum[c & 3] += c0 + c >= first && y > -INFINITY ? w : 0.f;
           }
         }

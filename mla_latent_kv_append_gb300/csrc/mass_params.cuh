@@ -13,6 +13,17 @@ constexpr int kMassMaxGrid = 512;                      // most blocks
 // finite up to 4094 and 2047.
 constexpr float kKeyGain = 16.f, kQueryGain = 32.f, kMassUngain = 1.f / (kKeyGain * kQueryGain);
 
+// An accumulation in TMEM cuts the sum off to 24 bits, towards 0: half a last place of
+// it on average, 2^-24 E[1/m] = 4.3e-8 of the sum for its mantissa m spread as in
+// nature.  (Scores of 20 nats were off by 0.75 to 1.0 times that for each accumulation
+// from their channels on, less where products of both signs are added; K-steps of
+// zeros cut nothing off.)  The queries' channels give that mean back, each as often as
+// it is cut off: mass_prep_kernel.
+constexpr float kMassCut = 3.9e-8f;
+
+// TMEM columns of the scores of a pass of R rows.
+__host__ __device__ constexpr int mass_columns(int R) { return R <= 64 ? 64 : kMassMaxRows; }
+
 // One sequence with queries and tokens, in the order of the batch.  Its rows r =
 // i H + h are cut into row blocks of R; a pass is a row block of a key tile, the
 // passes of a tile lie side by side.  A pass costs mass_cost(its rows) units.
@@ -61,6 +72,7 @@ struct MassParams {
   int32_t* dev_err;
   uint64_t wait_ns;
   int R, grid;
+  int split_lat, split_kpe;                            // cached values have low halves (all formats but bf16)
   int few, unit_tokens;                                // 16 rows (mass_few.cuh); cached tokens of a key tile
   int query_pieces, raw_slots;                         // pieces of the queries and raw blocks in shared memory
   int64_t rows;                                        // N H
