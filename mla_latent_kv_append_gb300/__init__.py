@@ -503,6 +503,13 @@ def _mass_of(mass, num_pages, dev):
     return _flat(mass, torch.float32, (num_pages * PAGE_TOKENS,), "mass", dev)
 
 
+def _row_stride(t):
+    """The distance of a matrix's rows in elements, None where a row is not
+    contiguous.  A dimension of one entry may have any stride."""
+    (n, width), (row, one) = t.shape, t.stride()
+    return None if n and width > 1 and one != 1 else row if n > 1 else width
+
+
 def mla_verify_drafts(target_probs, draft_probs, drafts, row_start, u_accept, u_sample, accepted, tokens, seq_lens=None,
                       kept_lens=None, dev_err=None, stream=None):
     """Drafted tokens against the target's probabilities, from given random
@@ -515,19 +522,21 @@ def mla_verify_drafts(target_probs, draft_probs, drafts, row_start, u_accept, u_
     B, width = tokens.shape
     i32, f32, dev = torch.int32, torch.float32, _gpu(target_probs, "target_probs")
     kind = PROB_TYPES.get(target_probs.dtype)
-    if kind is None or (rows and target_probs.stride()[1] != 1):
+    ts = _row_stride(target_probs)
+    if kind is None or ts is None:
         raise ValueError("target_probs: expected contiguous rows of float32, bfloat16 or float16, got %s" % target_probs.dtype)
     dp, ds = None, 0
     if draft_probs is not None:
-        if draft_probs.dtype is not target_probs.dtype or draft_probs.shape != (rows, vocab) or (rows and draft_probs.stride()[1] != 1):
+        ds = _row_stride(draft_probs) if draft_probs.shape == (rows, vocab) else None
+        if draft_probs.dtype is not target_probs.dtype or ds is None:
             raise ValueError("draft_probs: expected %s %s with contiguous rows, got %s %s" % (
                 target_probs.dtype, (rows, vocab), draft_probs.dtype, tuple(draft_probs.shape)))
         if draft_probs.get_device() != dev:
             raise _elsewhere(draft_probs, "draft_probs", dev)
-        dp, ds = draft_probs.data_ptr(), draft_probs.stride()[0]
+        dp = draft_probs.data_ptr()
     if (seq_lens is None) != (kept_lens is None):
         raise ValueError("seq_lens and kept_lens go together")
-    _step(lib.mla_verify_drafts, dev, stream, target_probs.data_ptr(), target_probs.stride()[0], dp, ds, kind, vocab,
+    _step(lib.mla_verify_drafts, dev, stream, target_probs.data_ptr(), ts, dp, ds, kind, vocab,
           _flat(drafts, i32, (rows,), "drafts", dev), _flat(row_start, i32, (B + 1,), "row_start", dev), B, rows,
           _flat(u_accept, f32, (rows,), "u_accept", dev), _flat(u_sample, f32, (B,), "u_sample", dev),
           None if seq_lens is None else _flat(seq_lens, i32, (B,), "seq_lens", dev), _flat(accepted, i32, (B,), "accepted", dev),
