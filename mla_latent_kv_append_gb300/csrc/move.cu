@@ -48,8 +48,9 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const MoveParams 
   const int len = __ldcg(p.seq_lens + b), n = __ldcg(p.lens + b);
   const int page = __ldcg(p.dst_table + (int64_t)b * p.max_pages + blk / 2);
   const int t = warp == 0 && j0 + lane < p.max_keep ? __ldcg(p.kept + (int64_t)b * p.max_keep + j0 + lane) : -1;
-  if (n == len) return;                                // stays where it is
-  if (len < 0 || len > p.max_pages * kPage || n < 0 || n > len || n > p.max_keep) {
+  const bool fits = len >= 0 && len <= p.max_pages * kPage && n >= 0 && n <= len;
+  if (fits && n == len) return;                        // stays where it is
+  if (!fits || n > p.max_keep) {
     if (blk == 0 && tid == 0) set_err(p.dev_err, MLA_DEVERR_SEQLEN);
     return;
   }
