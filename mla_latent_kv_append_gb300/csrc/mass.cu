@@ -3,6 +3,7 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include "checks.cuh"
 #include "mass_params.cuh"
 #include "scan.cuh"
 
@@ -187,8 +188,6 @@ __global__ void __launch_bounds__(kPrepThreads) mass_prep_kernel(const MassParam
     *reinterpret_cast<uint4*>(dst + (int64_t)9 * p.rows * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
-
-bool aligned_to(const void* p, uintptr_t a) { return p && ((uintptr_t)p & (a - 1)) == 0; }
 
 bool sizes_ok(int32_t batch, int32_t n_tokens, int32_t heads, int32_t max_new) {
   return batch >= 0 && batch <= kMaxBatch && n_tokens >= 0 && heads >= 16 && heads <= 128 && heads % 16 == 0 && max_new >= 0 &&

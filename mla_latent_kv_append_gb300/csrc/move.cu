@@ -14,6 +14,7 @@
 // tokens INT4 (122 MB in and out) 43 us: a quarter of a block's tokens touch nine
 // tenths of its scales' sectors, so that 200 MB move, 4.7 TB/s or 70% of a plain
 // copy's rate.  Four blocks an SM with 64 registers; five (48): 47 us.
+#include "checks.cuh"
 #include "mla_internal.cuh"
 
 namespace mla {
@@ -147,8 +148,6 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const MoveParams 
           __ldcg(reinterpret_cast<const uint16_t*>(src + L.outlier_off) + g * kBlockTokens + u);
   }
 }
-
-bool ok4(const void* p) { return p && ((uintptr_t)p & 3) == 0; }
 
 }  // namespace
 }  // namespace mla

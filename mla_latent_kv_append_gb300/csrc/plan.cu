@@ -22,7 +22,9 @@
 // Measured: 1 request 3.5 us, 256 requests x 512 pages 4.8 us, 4096 requests x
 // 640 pages (11.9 MB) 13.4 us, each as a captured call's share of many; the
 // last was 25 us with one element per thread and 64-bit divisions.
+#include "checks.cuh"
 #include "mla_internal.cuh"
+#include "scan.cuh"
 
 namespace mla {
 namespace {
@@ -51,30 +53,6 @@ struct PlanParams {
   int n;
   int32_t* dev_err;
 };
-
-// Exclusive scan over the block of one int64 per thread; *total = the sum.
-template <int T>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* red, int64_t* total) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();                                     // an earlier scan's readers of red are done
-  if (lane == 31) red[warp] = x;
-  __syncthreads();
-  int64_t s = lane < T / 32 ? red[lane] : 0;
-#pragma unroll
-  for (int o = 1; o < T / 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += y;
-  }
-  *total = __shfl_sync(0xffffffffu, s, T / 32 - 1);
-  const int64_t base = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
-  return (warp ? base : 0) + x - v;
-}
 
 __device__ __forceinline__ int pages_of(int tokens) { return (int)(((int64_t)tokens + kPage - 1) / kPage); }
 
@@ -271,8 +249,6 @@ __global__ void __launch_bounds__(T) plan_kernel(const PlanParams p) {
     }
   }
 }
-
-bool ok4(const void* p) { return p && ((uintptr_t)p & 3) == 0; }
 
 }  // namespace
 }  // namespace mla

@@ -20,6 +20,7 @@
 //
 // Measured: 32 requests x 512 pages trimmed 3.0 us; 4096 x 640 moved 26 us: two
 // launches that each scan all requests (8 us), then the tables (6) and the list (4).
+#include "checks.cuh"
 #include "mla_internal.cuh"
 #include "scan.cuh"
 
@@ -226,17 +227,6 @@ __global__ void __launch_bounds__(T) release_kernel(const ReleaseParams p, int p
       }
     }
   }
-}
-
-bool ok4(const void* p) { return p && ((uintptr_t)p & 3) == 0; }
-
-struct Range {
-  const void* at;
-  int64_t bytes;          // 0: not used
-};
-bool overlap(const Range& a, const Range& b) {
-  const char *x = (const char*)a.at, *y = (const char*)b.at;
-  return a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
 }
 
 }  // namespace

@@ -19,6 +19,7 @@
 // shared memory take 10.
 #include <cooperative_groups.h>
 
+#include "checks.cuh"
 #include "mla_internal.cuh"
 #include "scan.cuh"
 
@@ -309,8 +310,6 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
   cluster.sync();                                      // no block leaves while its counts may be read
 }
 
-bool ok4(const void* p) { return p && ((uintptr_t)p & 3) == 0; }
-
 }  // namespace
 }  // namespace mla
 
@@ -358,8 +357,7 @@ extern "C" mla_status mla_select_tokens(const float* mass, int32_t num_pages, co
   }
   if (!kernel) {
     kernel = select_kernel<0>;
-    const int64_t part = ((max_pages + CL - 1) / CL) * (int64_t)kPage;
-    p.keys = (int)(part < kSelKeys ? part : kSelKeys);
+    p.keys = kSelKeys;                                 // a block's part is more
     smem = p.keys * 4;
   }
   smem += kSelCopies * kSelPitch * 4;

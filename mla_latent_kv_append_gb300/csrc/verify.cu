@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "checks.cuh"
 #include "mla_internal.cuh"
 #include "tc.cuh"
 
@@ -40,7 +41,6 @@ namespace cg = cooperative_groups;
 constexpr int kVerThreads = 256, kVerWarps = kVerThreads / 32;
 constexpr int kVerTile = 1024;                         // values per tile
 constexpr int kVerMaxVocab = 1 << 22;
-constexpr int kVerMaxTiles = kVerMaxVocab / kVerTile + 1;   // one more where a row starts off a 16-byte boundary
 
 struct VerifyParams {
   const void *p, *q;
@@ -369,8 +369,6 @@ mla_status launch_verify(const VerifyParams& p, cudaStream_t stream) {
   cfg.numAttrs = 2;
   return cuda_status(cudaLaunchKernelEx(&cfg, verify_kernel<T>, p, CL));
 }
-
-bool aligned_to(const void* p, uintptr_t a) { return p && ((uintptr_t)p & (a - 1)) == 0; }
 
 }  // namespace
 }  // namespace mla
