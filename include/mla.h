@@ -634,7 +634,8 @@ size_t mla_chunk_workspace_bytes(int32_t batch, int32_t n_tokens, int32_t heads,
  * that stay, mla_release_pages (move) gives the sequences fresh pages for
  * them, mla_move_tokens moves them.  Pages are the same for all layers, so
  * the release runs once a step, the others once a layer.  Lengths live on the
- * device, so that a captured step can be replayed with other ones.
+ * device, so that a captured step can be replayed with other ones.  No output
+ * may overlap an input or another output, but where a call says so.
  * ---------------------------------------------------------------------------
  */
 
@@ -662,8 +663,8 @@ size_t mla_chunk_workspace_bytes(int32_t batch, int32_t n_tokens, int32_t heads,
  *   seq_lens int32 [B]: cached tokens with all drafts; with kept_lens, or both NULL
  *   accepted int32 [B]: drafts that passed
  *   tokens  int32 [B][max_out]: the accepted drafts, the drawn token, -1 behind
- *   kept_lens int32 [B]: seq_lens less the rejected drafts (may be seq_lens):
- *           the next step's context
+ *   kept_lens int32 [B]: seq_lens less the rejected drafts (may be seq_lens,
+ *           else must not overlap it): the next step's context
  *   A draft outside [0, vocab) is rejected, with the draft's row as it is, and
  *   sets MLA_DEVERR_TOKEN.  A row without weight draws -1 and sets it too.  A
  *   sequence with more than max_out rows is refused (MLA_DEVERR_SEQLEN): it
@@ -740,7 +741,8 @@ size_t mla_mass_workspace_bytes(int32_t batch, int32_t n_tokens, int32_t heads, 
  *   keep_lens int32 [B], 0 and more; not below seq_lens: nothing is cut
  *   kept    int32 [B][max_keep]: the positions that stay, increasing, -1
  *           behind (all positions, as far as they fit, where nothing is cut)
- *   kept_lens int32 [B]: min(keep_lens, seq_lens); not seq_lens or keep_lens
+ *   kept_lens int32 [B]: min(keep_lens, seq_lens); must not overlap seq_lens or
+ *           keep_lens
  *   A sequence with keep_lens < 0, or with max_keep < keep_lens < seq_lens,
  *   is not cut and sets MLA_DEVERR_SEQLEN; a seq_lens outside [0, max_pages *
  *   64] counts as 0 and sets it.

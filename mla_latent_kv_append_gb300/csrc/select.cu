@@ -326,7 +326,9 @@ extern "C" mla_status mla_select_tokens(const float* mass, int32_t num_pages, co
   if (!ok4(mass) || !ok4(block_table) || !ok4(seq_lens) || !ok4(keep_lens) || !ok4(kept) || !ok4(kept_lens) ||
       (dev_err && !ok4(dev_err)))
     return MLA_ERR_INVALID_ARG;
-  if (kept_lens == seq_lens || kept_lens == keep_lens) return MLA_ERR_INVALID_ARG;      // read by several blocks
+  // the lengths are read by several blocks at any time
+  const int64_t per = (int64_t)batch * 4;
+  if (overlap({kept_lens, per}, {seq_lens, per}) || overlap({kept_lens, per}, {keep_lens, per})) return MLA_ERR_INVALID_ARG;
   SelectParams p;
   p.mass = mass;
   p.num_pages = num_pages;

@@ -395,6 +395,9 @@ extern "C" mla_status mla_verify_drafts(const void* target_probs, int64_t target
   if ((kept_lens != nullptr) != (seq_lens != nullptr) || (kept_lens && (!aligned_to(kept_lens, 4) || !aligned_to(seq_lens, 4))) ||
       (dev_err && !aligned_to(dev_err, 4)))
     return MLA_ERR_INVALID_ARG;
+  // in place, or apart: sequences read theirs at any time
+  const int64_t per = (int64_t)batch * 4;
+  if (kept_lens != seq_lens && overlap({kept_lens, per}, {seq_lens, per})) return MLA_ERR_INVALID_ARG;
   if (rows > 0 && (INT64_MAX / 4) / rows < (target_row_stride > draft_row_stride || !draft_probs ? target_row_stride : draft_row_stride))
     return MLA_ERR_INVALID_ARG;
   VerifyParams p;
