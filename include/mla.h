@@ -507,9 +507,10 @@ mla_status mla_lse_merge(const float* o_parts, const float* lse_parts, int32_t p
  *               page: what the attention calls take
  *   q_start     [B + 1]: first token row of each request, then the total
  *   seq_lens    [B]: ctx + new
- *   positions, token_req, slot [n_tokens]: each token's position, batch index
- *               and cache slot (mla_cache_append's); 0, -1 and -1 behind the
- *               last token, which the append skips
+ *   positions, token_req, slot [n_tokens]: each token's position (its place
+ *               in the cache; see mla_move_tokens for a cache that was cut),
+ *               batch index and cache slot (mla_cache_append's); 0, -1 and -1
+ *               behind the last token, which the append skips
  *   free_head   [1]: the next step's head (not free_range itself)
  *   A request is refused, and the others go on, when its lengths are
  *   negative or exceed max_pages * 64, or its tokens do not fit n_tokens
@@ -634,8 +635,14 @@ size_t mla_chunk_workspace_bytes(int32_t batch, int32_t n_tokens, int32_t heads,
  * that stay, mla_release_pages (move) gives the sequences fresh pages for
  * them, mla_move_tokens moves them.  Pages are the same for all layers, so
  * the release runs once a step, the others once a layer.  Lengths live on the
- * device, so that a captured step can be replayed with other ones.  No output
- * may overlap an input or another output, but where a call says so.
+ * device, so that a captured step can be replayed with other ones.  The calls
+ * of this section, the plan, the append and mla_chunk_attention take lengths
+ * from the call before them; mla_decode_absorbed, whose lse the attention
+ * weight needs, reads its seq_lens during the launch overlap: between a call
+ * that writes them (the plan, kept_lens, lens_out) and the decode a full
+ * ordering point is needed (see Execution above), for instance a device-to-
+ * device copy of the lengths, which a graph captures as well.  No output may
+ * overlap an input or another output, but where a call says so.
  * ---------------------------------------------------------------------------
  */
 
@@ -693,7 +700,13 @@ mla_status mla_verify_drafts(const void* target_probs, int64_t target_row_stride
  * its seq_lens[b] tokens: query i (of n) sees positions t <= seq_lens[b] - n +
  * i.  They may be fewer than the step's new tokens (an observation window).
  *   q_lat   fp32 [n_tokens][H][512], q_pe bf16 [n_tokens][H][64], lse fp32
- *           [n_tokens][H] (natural log; a row whose lse is not finite adds nothing)
+ *           [n_tokens][H] (natural log; a row whose lse is not finite adds nothing).
+ *           mla_chunk_attention returns neither q_lat nor lse.  For queries of
+ *           a ragged batch they come from mla_q_absorb and a second attention:
+ *           one mla_decode_absorbed whose sequences are the queries (each its
+ *           sequence's block_table row, and as many tokens as it sees: the
+ *           cache is read once a query), or one mla_prefill_absorbed a
+ *           sequence, whose context length lives on the host
  *   block_table int32 [B][max_pages], q_start int32 [B + 1], seq_lens int32 [B]
  *   counted int32 [B]: tokens whose mass is up to date; NULL: seq_lens[b] - n
  *   max_new bound on every n (host; at most n_tokens)
@@ -805,6 +818,11 @@ mla_status mla_release_pages(const int32_t* old_lens, const int32_t* new_lens, c
  *   kept    int32 [B][max_keep] of mla_select_tokens; lens int32 [B]:
  *           mla_release_pages's lens_out
  *   mass    fp32 [num_pages * 64], by cache slot, or NULL
+ *   The kept tokens' k_pe keep the rotation of their old positions, while the
+ *   next mla_plan_chunks counts positions on from the shortened cache: so that
+ *   new tokens keep their distances to those kept, add to its positions,
+ *   before mla_rope, the tokens that the request lost so far (seq_lens - lens,
+ *   summed over its moves).
  *   Slots behind a sequence's last token are left as they were.  A kept
  *   position outside the sequence (MLA_DEVERR_SLOT) or a page id outside the
  *   pool (MLA_DEVERR_PAGE) leaves the new token's slot as it was; a sequence

@@ -556,7 +556,9 @@ def mla_token_mass(cache, q_lat, q_pe, lse, block_table, q_start, seq_lens, work
     [n, H, 64] and lse fp32 [n, H] are the attention's; sequence b's queries
     are rows q_start[b] .. q_start[b + 1] - 1, the last of its seq_lens[b]
     tokens.  Tokens from position counted[b] on (None: those of the queries)
-    start from 0."""
+    start from 0.  The lse comes from mla_decode_absorbed (of several queries
+    a sequence: with every query as a sequence of its own) or from
+    mla_prefill_absorbed; mla_chunk_attention returns none."""
     n, H, _ = q_lat.shape
     B, max_pages = block_table.shape
     f32, i32, dev = torch.float32, torch.int32, _gpu(q_lat, "q_lat")
@@ -612,7 +614,9 @@ def mla_move_tokens(cache, src_table, seq_lens, kept, lens, dst_table, mass=None
     """Moves the tokens that stay into their fresh pages: token j < lens[b] of
     sequence b's pages in dst_table becomes token kept[b][j] of its pages in
     src_table, bit for bit, with its mass.  A sequence with lens[b] ==
-    seq_lens[b] stays where it is."""
+    seq_lens[b] stays where it is.  The kept tokens' k_pe stay rotated to their
+    old positions: add what a request lost so far to mla_plan_chunks's
+    positions before mla_rope."""
     B, max_pages = src_table.shape
     i32, dev = torch.int32, _gpu(src_table, "src_table")
     _step(lib.mla_move_tokens, dev, stream, _pool_on(cache, dev), _flat(src_table, i32, (B, max_pages), "src_table", dev),
