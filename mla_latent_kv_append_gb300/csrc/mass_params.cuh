@@ -15,11 +15,12 @@ constexpr float kKeyGain = 16.f, kQueryGain = 32.f, kMassUngain = 1.f / (kKeyGai
 
 // An accumulation in TMEM cuts the sum off to 24 bits, towards 0: half a last place of
 // it on average, 2^-24 E[1/m] = 4.3e-8 of the sum for its mantissa m spread as in
-// nature.  (Scores of 20 nats were off by 0.75 to 1.0 times that for each accumulation
-// from their channels on, less where products of both signs are added; K-steps of
-// zeros cut nothing off.)  The queries' channels give that mean back, each as often as
-// it is cut off: mass_prep_kernel.
-constexpr float kMassCut = 3.9e-8f;
+// nature; products are cut off one by one before, which takes a fifth of that back where
+// they are of both signs, as a query's and a latent's are.  (Scores of 20 nats were off by
+// 2.9 to 3.4e-8 for each accumulation from their channels on, 2.6 to 5.2e-8 with products
+// of one sign; K-steps of zeros cut nothing off.)  The queries' channels give that mean
+// back, each as often as it is cut off: mass_prep_kernel.
+constexpr float kMassCut = 3.4e-8f;
 
 // TMEM columns of the scores of a pass of R rows.
 __host__ __device__ constexpr int mass_columns(int R) { return R <= 64 ? 64 : kMassMaxRows; }
