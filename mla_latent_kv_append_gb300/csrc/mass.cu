@@ -258,15 +258,18 @@ extern "C" mla_status mla_token_mass(const mla_cache_layer* cache, const float* 
   p.dev_err = dev_err;
   p.wait_ns = wait_limit_ns();
   const int64_t most = (int64_t)max_new * heads;
-  // Rows of a pass: no more than the longest sequence has (32 x 32768 tokens INT4 at 16
-  // rows: 204 us in passes of 16, 251 of 128), and 128 where there are more (24 drafts of
-  // 5 tokens at 64 heads: 77 us, 102 in passes of 64; a window of 32 at 16 heads: 93, 124).
+  // Rows of a pass: no more than the longest sequence has (32 x 32768 tokens INT4 at 32
+  // rows: 206 us in passes of 32, 259 of 128), and 128 where there are more (24 drafts of
+  // 5 tokens at 64 heads: 79 us, 104 in passes of 64; a window of 32 at 16 heads: 94, 124).
   p.R = most <= 16 ? 16 : (most <= 32 ? 32 : (most <= 64 ? 64 : kMassMaxRows));
   const int sms = device_sm_count();
   p.grid = sms < 1 ? 1 : (sms < kMassMaxGrid ? sms : kMassMaxGrid);
   // 16 rows on mma.sync, in the formats that it has: one sequence of 4096 tokens takes 11
-  // us there and 14 to 15 on tcgen05 (bf16, INT8), of 32768 17.7 and 17.9, and 32 of
-  // 32768 INT4 206 and 204.
+  // us there and 14 to 15 on tcgen05 (bf16, INT8), of 32768 16.3 and 18.6 (INT8) or 17.4
+  // and 17.6 (bf16), 32 of 500 17 and 20, 32 of 16384 INT8 108 and 109, 32 of 32768 INT4
+  // 207 and 203.  Only long batches in bf16 lose (32 of 16384: 136 and 107; three products
+  // of bf16 parts where tcgen05 takes two of fp16 ones), and how long they are is known
+  // on the device alone.
   p.few = most <= 16 && (cache->latent_fmt == MLA_FMT_BF16 || cache->latent_fmt == MLA_FMT_INT8_SYM ||
                          cache->latent_fmt == MLA_FMT_INT4_ASYM || cache->latent_fmt == MLA_FMT_INT4_SYM);
   // the unit that the kernels copy at a time (FewShape::kBlocks), or a tile of theirs

@@ -21,9 +21,12 @@
 // What bounds it: the MMAs, 75 to 92 cycles each with A in TMEM, and for 128 rows the
 // queries' way from L2 (295 KB for a pass, 40 bytes a cycle and SM).  Measured
 // (a captured call's share of many): 4 x 16000 tokens INT8, a window of 32 queries at 16 heads
-// 93 us, 400 TFLOP/s of scores or 21% of the bf16 rate, of which three products make
-// 62%; 24 drafts of up to 5 tokens at 64 heads, bf16, 77 us; 32 x 32768 tokens INT4
-// at 32 heads 211 us, at 64 heads 247.
+// 94 us, 390 TFLOP/s of scores or 20% of the bf16 rate, of which three products make
+// 60%; 24 drafts of up to 5 tokens at 64 heads, bf16, 79 us; 32 x 32768 tokens INT4
+// at 32 heads 206 us, at 64 heads 241, at 128 heads 355; 32 x 16384 tokens at 32 heads
+// 109 to 114 us in every format (4.0 TB/s in INT8 blocks of 8), but 288 with protected
+// channels, which are put in their places one by one.  The roles' code together spills
+// 184 bytes a thread at the 64 registers that 1024 threads leave.
 //
 // Work split: all passes (a key tile, up to 128 rows) in a row, cut into runs of equal
 // cost, one to an SM.  A tile that several blocks share is added up by whichever

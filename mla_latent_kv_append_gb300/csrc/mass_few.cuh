@@ -11,16 +11,19 @@
 // halves (22 bits); bf16 latents take bf16 operands, q in three parts.
 //
 // What bounds it: the latency of its instructions (890 a warp and 32-token block,
-// half the issue slots, with the 16 warps that the registers allow) and two thirds of
-// the shared-memory pipe, not the cache's bytes.  The cache comes in bulk copies into a ring; four
+// half the issue slots) and three fifths of the shared-memory pipe, not the cache's
+// bytes.  With the seventeenth warp, which issues the copies, one of the SM's four
+// schedulers has five, which leaves a thread 96 registers: 4-bit latents, and INT8 with
+// a bf16 k_pe, spill 52 to 104 bytes.  The cache comes in bulk copies into a ring; four
 // warps share a 32-token block by channels (eight latent groups and 16 RoPE
 // channels each), three hand their partial scores to the fourth, in turn, which
 // takes the exponentials and adds up the rows.  The queries' fragments lie in
 // shared memory, made anew for every sequence.
 //
-// Measured (a captured call's share of many): 32 x 32768 tokens INT4 206 us, 3.0 TB/s
-// or 45% of a plain copy's rate.  Eight warps to a block, with their queries'
-// fragments in registers: 325 us.
+// Measured (a captured call's share of many): 32 x 32768 tokens INT4 207 us, 3.0 TB/s
+// or 44% of a plain copy's rate; 32 x 16384 tokens INT8 108 us, bf16 136; one sequence of
+// 4096 tokens INT8 11 us.  Eight warps to a block, with their queries' fragments in
+// registers: 325 us for the first.
 #pragma once
 
 #include <math.h>
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) mass_few_kernel(const MassPara
         ++round;
       }
       // a place that is always this quad's needs no look at who had it before (32 x
-      // 32768 tokens INT4: 206 us, with it 212)
+      // 32768 tokens INT4: 207 us, with it 212)
       if (!late && !(NS % SH::kUnits ? ring_wait(raw_full + 8 * at, raw_free + 8 * at, its_round, p.wait_ns, abort)
                                      : warp_wait(raw_full + 8 * at, its_round & 1, p.wait_ns, abort))) {
         late = true;                                   // leaves with the others, at the next sequence

@@ -10,9 +10,9 @@
 // 16-byte chunks, the per-token fields (scales lie side by side for 32 tokens) in
 // 4-byte words, a lane per token, of which a read moves a 32-byte sector.
 //
-// Measured: 2048 tokens of 32768 INT8 3.4 us; 32 sequences cut to a quarter, 104000
-// tokens INT4 (122 MB in and out) 43 us: a quarter of a block's tokens touch nine
-// tenths of its scales' sectors, so that 200 MB move, 4.7 TB/s or 70% of a plain
+// Measured: 2048 tokens of 32768 INT8 3.3 us; 32 sequences cut to a quarter, 104000
+// tokens INT4 (122 MB in and out) 41 us: a quarter of a block's tokens touch nine
+// tenths of its scales' sectors, so that 195 MB move, 4.8 TB/s or 71% of a plain
 // copy's rate.  Four blocks an SM with 64 registers; five (48): 47 us.
 #include "checks.cuh"
 #include "mla_internal.cuh"

@@ -22,9 +22,12 @@
 // border again, in fp64.
 //
 // Measured (a captured call's share of many): 256 sequences of up to 4 drafts over
-// 131072 fp32 values, 268 MB, 67 us, 4.0 TB/s or 60% of a plain copy's rate; one of 4
-// drafts over 32003 values 9.4 us, latency: lengths, drafts, their probabilities,
-// the row, two meetings of the cluster and the last tile follow one another.
+// 131072 fp32 values, up to 268 MB, 68 us, 4.0 TB/s or 59% of a plain copy's rate; half
+// the bytes, in 16 bits or from the target's row alone (drafts that were certain, or
+// none), 60 to 62 us: the additions of a value, and rows that begin and end in step,
+// bound it then.  64 sequences with rows that are not aligned with each other 48 us, 45
+// in 16 bits.  One of 4 drafts over 32003 values 9.6 us, latency: lengths, drafts, their
+// probabilities, the row, two meetings of the cluster and the last tile follow one another.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -348,8 +351,9 @@ template <typename T>
 mla_status launch_verify(const VerifyParams& p, cudaStream_t stream) {
   // Blocks of a sequence: 8 where there are few sequences, so that their rows
   // spread over the SMs; with many, no more blocks than run side by side, four to an
-  // SM (256 sequences of 131072 fp32 values: 94 us with 1, 67 with 2, 82 with 4, 108
-  // with 8, which come in four waves; three blocks to an SM 87, five 84).
+  // SM (256 sequences of 131072 fp32 values: 96 us with 1, 68 with 2, 83 with 4, 112
+  // with 8, which come in four waves; three blocks to an SM 88, five 83.  One sequence: 16,
+  // 12, 9.8 and 9.6 us).
   const int sms = device_sm_count();
   int CL = 8;
   while (CL > 1 && (int64_t)p.B * CL > 4 * (int64_t)sms) CL /= 2;
