@@ -101,7 +101,7 @@ __device__ __forceinline__ int rows_beside(const MassParams& p, int r) {
 
 // The queries times the softmax scale, log2 e and kQueryGain, as two halves:
 // piece kb of 64 channels, all rows of it side by side, in the 128-byte swizzle.
-// A row whose lse is not finite is 0 (it adds nothing).  8 rows a block.
+// A row whose lse is not finite is 0 (it adds nothing).
 //
 // What the MMAs' accumulations cut off on average (kMassCut) is given back here: a
 // channel's part of a score is cut at every accumulation from its own K-step's on, so

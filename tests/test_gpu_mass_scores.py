@@ -131,3 +131,36 @@ def test_mean_error_of_small_scores(mla, lf, kf, H, n):
     for kind in ("all", "gauss"):
         e, _ = zip(*(errors(mla, lf, kf, H, n, kind, seed, size=1.0) for seed in (1, 2, 3)))
         assert abs(float(torch.cat(e).mean())) <= 1e-6
+
+
+@pytest.mark.parametrize("B", [1, 31, 33, 1100], ids=lambda b: "%d sequences" % b)
+def test_mean_error_over_a_ragged_batch(mla, B):
+    """Which accumulations a row's score goes through depends on its row block, and so
+    on where its sequence's rows begin and end: sequences of 16 to 192 rows in passes of
+    128, in batches whose sequences are found in one, two and three steps."""
+    counts = [1, 12, 4, 5, 9, 2, 8, 3]
+    new = [counts[b % 8] for b in range(B)] if B > 1 else [12]
+    ctx = 64 if B > 100 else 300
+    t = Mass(mla, [(ctx, n) for n in new], 16, F_INT8, F_INT8, seed=3, counted=[0] * B, decay=0.0)
+    q = torch.randn(576, generator=torch.Generator().manual_seed(4))
+    x = [torch.cat(h, -1)[:ctx] for h in t.hat]
+    q *= S / float((torch.cat(x) @ q.double() * SCALE).abs().mean())
+    t.q_lat[:], t.q_pe[:] = q[:512], q[512:].bfloat16()
+    y = torch.cat([t.q_lat[0, 0], t.q_pe[0, 0].float()]).double()
+    s = [a @ y * SCALE for a in x]
+    lse = torch.tensor([float(a.mean()) for a in s], dtype=torch.float32)
+    for b in range(B):
+        t.lse[t.start[b]:t.start[b + 1]] = lse[b]
+    got = t.go(mass=torch.zeros(t.num_pages * 64, device="cuda")).double().cpu()
+    assert t.err.item() == 0
+    at = torch.arange(ctx)
+    for n in sorted(set(new)):
+        num = den = 0.0
+        for b in range(B):
+            if new[b] != n:
+                continue
+            want = torch.exp(s[b] - float(lse[b])) * n * 16
+            ok = (want > 1e-25) & (want < 1e25)
+            e = torch.log(got[t.table[b].long()[at // 64] * 64 + at % 64] / want)[ok]
+            num, den = num + float((e * s[b][ok]).sum()), den + float((s[b][ok] ** 2).sum())
+        assert abs(num / den) <= 4.6e-7 + 6e-8, (n, num / den)
