@@ -24,10 +24,11 @@
 // Measured (a captured call's share of many): 256 sequences of up to 4 drafts over
 // 131072 fp32 values 68 us, 3.2 TB/s of the 216 MB read (one row where all drafts
 // passed, else two) or 48% of a plain copy's rate; half the bytes, in 16 bits or from the
-// target's row alone (drafts that were certain, or none), 60 to 62 us: the additions of a value, and rows that begin and end in step,
-// bound it then.  64 sequences with rows that are not aligned with each other 48 us, 45
-// in 16 bits.  One of 4 drafts over 32003 values 9.6 us, latency: lengths, drafts, their
-// probabilities, the row, two meetings of the cluster and the last tile follow one another.
+// target's row alone (drafts that were certain, or none), 60 to 62 us: the additions of
+// a value, and rows that begin and end in step, bound it then.  64 sequences with rows
+// that are not aligned with each other 48 us, 45 in 16 bits.  One of 4 drafts over 32003
+// values 9.6 us, latency: lengths, drafts, their probabilities, the row, two meetings of
+// the cluster and the last tile follow one another.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
